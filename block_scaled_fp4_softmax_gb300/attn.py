@@ -1,0 +1,294 @@
+"""Thin ctypes binding over the C ABI in include/attn.h.
+
+The attention step of a decode over a paged cache.  As in :mod:`.moe`, each
+function carries the C entry point's name, checks types and devices, allocates
+what the caller does not pass, and hands device pointers plus the current CUDA
+stream to the library.  A serving loop makes one :func:`attn_cache` handle per
+layer and keeps its workspaces; the calls then touch no allocator when every
+output is passed.
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import moe as _moe
+from .moe import DEV_TIMEOUT, MoeError, _check, _ptr, _stream  # noqa: F401
+
+BF16 = 0
+FP16 = 1
+
+DEV_BAD_PAGE = 32
+DEV_BAD_LENGTH = 64
+
+EXPORTS = (
+    "attn_qk_norm_rope",
+    "attn_tree_decode_workspace",
+    "attn_tree_decode",
+    "attn_cache_weights",
+    "attn_cache_evict_workspace",
+    "attn_cache_evict",
+)
+
+_DTYPES = {torch.bfloat16: BF16, torch.float16: FP16}
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("page_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong),
+                ("row_stride", ctypes.c_longlong), ("page_table", ctypes.c_void_p),
+                ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+_vp, _i, _ll, _d, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_double, ctypes.c_size_t
+_cp = ctypes.POINTER(_CacheStruct)
+
+_SIGS = {
+    "attn_qk_norm_rope": (_i, [_vp, _vp, _vp, _ll, _ll, _ll, _vp, _vp, _vp, _i, _i, _vp, _vp, _d, _vp, _i, _i, _d,
+                               _vp, _vp, _i, _cp, _vp, _vp]),
+    "attn_tree_decode_workspace": (_sz, [_cp]),
+    "attn_tree_decode": (_i, [_vp, _ll, _vp, _vp, _i, _i, _vp, _i, _d, _cp, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "attn_cache_weights": (_i, [_vp, _ll, _vp, _vp, _vp, _i, _i, _vp, _i, _d, _cp, _vp, _d, _vp, _i, _vp, _vp]),
+    "attn_cache_evict_workspace": (_sz, [_cp, _i]),
+    "attn_cache_evict": (_i, [_cp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
+}
+
+_LIB = None
+
+
+def load():
+    """The library of :func:`.moe.load` with this module's signatures set."""
+    global _LIB
+    if _LIB is None:
+        lib = _moe.load()
+        for name, (res, args) in _SIGS.items():
+            fn = getattr(lib, name)
+            fn.restype = res
+            fn.argtypes = args
+        _LIB = lib
+    return _LIB
+
+
+class AttnCache:
+    """Handle of a paged cache: the C description plus the tensors it points
+    into, which it keeps alive."""
+
+    def __init__(self, k, v, page_table):
+        self.k, self.v, self.page_table = k, v, page_table
+        pages, heads, size, dim = k.shape
+        sp, sh, sr, _ = k.stride()
+        self.batch, self.kv_heads, self.head_dim = page_table.shape[0], heads, dim
+        self.dtype, self.device = k.dtype, k.device
+        self.struct = _CacheStruct(k.data_ptr(), v.data_ptr(), sp, sh, sr, page_table.data_ptr(), page_table.shape[0],
+                                   page_table.shape[1], pages, size, heads, dim, _DTYPES[k.dtype])
+        self.ref = ctypes.byref(self.struct)
+
+
+def attn_cache(k, v, page_table) -> AttnCache:
+    """Describes a cache.  k, v [pages, kv_heads, page_size, D]: any strides
+    with D contiguous, the same for both (a [pages, page_size, kv_heads, D]
+    cache is passed as its transposed view); page_table [batch, max_pages]
+    int32."""
+    for name, t in (("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise MoeError(f"{name} must be a CUDA tensor")
+        if t.dim() != 4 or t.dtype not in _DTYPES or t.stride(3) != 1:
+            raise MoeError(f"{name} must be [pages, kv_heads, page_size, D] of bfloat16 or float16, D contiguous")
+    if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.device != v.device:
+        raise MoeError("k and v must have the same shape, strides, type and device")
+    _moe._cuda(page_table, "page_table", torch.int32)
+    if page_table.dim() != 2 or page_table.device != k.device:
+        raise MoeError("page_table must be [batch, max_pages] on the cache's device")
+    return AttnCache(k, v, page_table)
+
+
+def _rows(t, name, heads, cache):
+    """A [tokens, heads, D] tensor whose heads and elements are contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dtype != cache.dtype or t.device != cache.device:
+        raise MoeError(f"{name} must be {cache.dtype} on {cache.device}, as the cache")
+    D = cache.head_dim
+    if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
+        raise MoeError(f"{name} must be [tokens, {heads or 'heads'}, {D}], got {tuple(t.shape)}")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
+        raise MoeError(f"{name}: heads and elements must be contiguous")
+    # the stride of one token is of no account; a packed one satisfies the checks
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * D
+
+
+def _array(t, name, shape, dtype, cache):
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != cache.device or t.shape != shape
+            or not t.is_contiguous()):
+        raise MoeError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {cache.device}")
+    return t
+
+
+def _sequences(cu, lens, cache):
+    _array(cu, "cu", (cache.batch + 1,), torch.int32, cache)
+    _array(lens, "lens", (cache.batch,), torch.int32, cache)
+
+
+def _tree(tree, tokens, cache):
+    """tree [tokens, words] int64: bit j % 64 of word j // 64 of a row is set
+    if the token sees draft j of its sequence."""
+    if tree is None:
+        return None, 0
+    if tree.dim() != 2:
+        raise MoeError("tree must be [tokens, words]")
+    _array(tree, "tree", (tokens, tree.shape[1]), torch.int64, cache)
+    return tree.data_ptr(), tree.shape[1]
+
+
+def _status(dev_status, cache):
+    if dev_status is None:
+        return None
+    return _array(dev_status, "dev_status", (1,), torch.int32, cache).data_ptr()
+
+
+def _new(stream, make, *args, **kwargs):
+    """Allocates on the stream the call runs on, so that the allocator never
+    hands the memory to another stream while the call uses it."""
+    if stream is None:
+        return make(*args, **kwargs)
+    with torch.cuda.stream(stream):
+        return make(*args, **kwargs)
+
+
+# ---------------------------------------------------------------------------
+# Entry points (same names as the C ABI)
+# ---------------------------------------------------------------------------
+
+def attn_qk_norm_rope(q, k, v, pos, cu, lens, cache: AttnCache, inv_freq, q_weight=None, k_weight=None,
+                      eps: float = 1e-6, interleaved: bool = False, magnitude: float = 1.0, slot_pos=None, q_out=None,
+                      dev_status=None, stream=None):
+    """Head norm and rotation of q and k, append of k and v.  inv_freq [rot /
+    2] FP64: radians per position.  Returns q_out [tokens, q_heads, D]."""
+    sq, sk, sv = _rows(q, "q", None, cache), _rows(k, "k", cache.kv_heads, cache), _rows(v, "v", cache.kv_heads, cache)
+    T, hq = q.shape[0], q.shape[1]
+    if k.shape[0] != T or v.shape[0] != T:
+        raise MoeError("q, k and v must hold the same tokens")
+    _array(pos, "pos", (T,), torch.int32, cache)
+    _sequences(cu, lens, cache)
+    _array(inv_freq, "inv_freq", (inv_freq.numel(),), torch.float64, cache)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _array(w, name, (cache.head_dim,), cache.dtype, cache)
+    if (q_weight is None) != (k_weight is None):
+        raise MoeError("give both of q_weight and k_weight, or neither")
+    cap = 0
+    if slot_pos is not None:
+        cap = slot_pos.shape[-1]
+        _array(slot_pos, "slot_pos", (cache.batch, cache.kv_heads, cap), torch.int32, cache)
+    if q_out is None:
+        q_out = _new(stream, torch.empty, (T, hq, cache.head_dim), dtype=q.dtype, device=q.device)
+    else:
+        _array(q_out, "q_out", (T, hq, cache.head_dim), cache.dtype, cache)
+    _check(load().attn_qk_norm_rope(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), sq, sk, sv, pos.data_ptr(), cu.data_ptr(), lens.data_ptr(), T, hq,
+        _ptr(q_weight), _ptr(k_weight), eps, inv_freq.data_ptr(), 2 * inv_freq.numel(), int(interleaved), magnitude,
+        q_out.data_ptr(), _ptr(slot_pos), cap, cache.ref, _status(dev_status, cache), _stream(stream)),
+        "attn_qk_norm_rope")
+    return q_out
+
+
+def attn_tree_decode_workspace(cache: AttnCache):
+    """A workspace for :func:`attn_tree_decode` on the cache's device."""
+    with torch.cuda.device(cache.device):
+        n = int(load().attn_tree_decode_workspace(cache.ref))
+    if n == 0:
+        raise MoeError("attn_tree_decode does not support this cache")
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def attn_tree_decode(q, cu, lens, cache: AttnCache, tree=None, scale: float | None = None, out=None, lse=None,
+                     workspace=None, dev_status=None, stream=None):
+    """Attention of the tokens in flight over the cache; tree = None: a chain.
+    Returns (out [tokens, q_heads, D], lse [tokens, q_heads])."""
+    sq = _rows(q, "q", None, cache)
+    T, hq = q.shape[0], q.shape[1]
+    _sequences(cu, lens, cache)
+    words, count = _tree(tree, T, cache)
+    if out is None:
+        out = _new(stream, torch.empty, (T, hq, cache.head_dim), dtype=q.dtype, device=q.device)
+    else:
+        _array(out, "out", (T, hq, cache.head_dim), cache.dtype, cache)
+    if lse is None:
+        lse = _new(stream, torch.empty, (T, hq), dtype=torch.float32, device=q.device)
+    else:
+        _array(lse, "lse", (T, hq), torch.float32, cache)
+    if workspace is None:
+        workspace = _new(stream, attn_tree_decode_workspace, cache)
+    else:
+        _moe._cuda(workspace, "workspace", torch.uint8)
+    _check(load().attn_tree_decode(
+        q.data_ptr(), sq, cu.data_ptr(), lens.data_ptr(), T, hq, words, count,
+        cache.head_dim ** -0.5 if scale is None else scale, cache.ref, out.data_ptr(), lse.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _status(dev_status, cache), _stream(stream)), "attn_tree_decode")
+    return out, lse
+
+
+def attn_cache_weights(q, lse, cu, lens, cache: AttnCache, acc, tree=None, scale: float | None = None,
+                       decay: float = 1.0, acc_out=None, dev_status=None, stream=None):
+    """acc_out = decay * acc + the softmax weight each slot received.  acc
+    [batch, kv_heads, slot_cap]; acc_out may be acc; entries past a sequence's
+    end are not written (a new acc_out starts as zeros)."""
+    sq = _rows(q, "q", None, cache)
+    T, hq = q.shape[0], q.shape[1]
+    _sequences(cu, lens, cache)
+    _array(lse, "lse", (T, hq), torch.float32, cache)
+    words, count = _tree(tree, T, cache)
+    shape = (cache.batch, cache.kv_heads, acc.shape[-1])
+    _array(acc, "acc", shape, torch.float32, cache)
+    if acc_out is None:
+        acc_out = _new(stream, torch.zeros, shape, dtype=torch.float32, device=q.device)
+    else:
+        _array(acc_out, "acc_out", shape, torch.float32, cache)
+    _check(load().attn_cache_weights(
+        q.data_ptr(), sq, lse.data_ptr(), cu.data_ptr(), lens.data_ptr(), T, hq, words, count,
+        cache.head_dim ** -0.5 if scale is None else scale, cache.ref, acc.data_ptr(), decay, acc_out.data_ptr(),
+        shape[2], _status(dev_status, cache), _stream(stream)), "attn_cache_weights")
+    return acc_out
+
+
+def attn_cache_evict_workspace(cache: AttnCache, budget: int):
+    """A workspace for :func:`attn_cache_evict` with this budget."""
+    n = int(load().attn_cache_evict_workspace(cache.ref, budget))
+    if n == 0:
+        raise MoeError("attn_cache_evict does not support this cache or budget")
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def attn_cache_evict(cache: AttnCache, acc, slot_pos, lens, next_pos, budget: int, sinks: int = 0, recent: int = 0,
+                     acc_out=None, pos_out=None, lens_out=None, workspace=None, dev_status=None, stream=None):
+    """Keeps the `budget` slots of each sequence and KV head with the most
+    weight and moves their rows below the budget, in place.  Returns
+    (lens_out, acc_out, pos_out)."""
+    shape = (cache.batch, cache.kv_heads, acc.shape[-1])
+    _array(acc, "acc", shape, torch.float32, cache)
+    _array(slot_pos, "slot_pos", shape, torch.int32, cache)
+    _array(lens, "lens", (cache.batch,), torch.int32, cache)
+    _array(next_pos, "next_pos", (cache.batch,), torch.int32, cache)
+    if acc_out is None:
+        acc_out = _new(stream, torch.zeros_like, acc)
+    else:
+        _array(acc_out, "acc_out", shape, torch.float32, cache)
+    if pos_out is None:
+        pos_out = _new(stream, torch.zeros_like, slot_pos)
+    else:
+        _array(pos_out, "pos_out", shape, torch.int32, cache)
+    if lens_out is None:
+        lens_out = _new(stream, torch.empty_like, lens)
+    else:
+        _array(lens_out, "lens_out", (cache.batch,), torch.int32, cache)
+    if workspace is None:
+        workspace = _new(stream, attn_cache_evict_workspace, cache, budget)
+    else:
+        _moe._cuda(workspace, "workspace", torch.uint8)
+    _check(load().attn_cache_evict(
+        cache.ref, acc.data_ptr(), slot_pos.data_ptr(), shape[2], lens.data_ptr(), next_pos.data_ptr(), budget, sinks,
+        recent, acc_out.data_ptr(), pos_out.data_ptr(), lens_out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        _status(dev_status, cache), _stream(stream)), "attn_cache_evict")
+    return lens_out, acc_out, pos_out

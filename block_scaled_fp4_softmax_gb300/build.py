@@ -39,7 +39,9 @@ def _sources():
 
 def _digest(paths) -> str:
     h = hashlib.sha256()
-    for p in paths + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(INCLUDE, "moe.h")]:
+    headers = [glob.glob(os.path.join(CSRC, "*.cuh")), glob.glob(os.path.join(CSRC, "*.h")),
+               glob.glob(os.path.join(INCLUDE, "*.h"))]
+    for p in paths + sorted(sum(headers, [])):
         with open(p, "rb") as f:
             h.update(p.encode() + f.read())
     h.update(" ".join(ARCH + FLAGS).encode())
