@@ -1,0 +1,63 @@
+// How attn_tree_decode divides its work, for host and device.
+//
+// A unit is one (sequence, KV head, group of up to `unit_rows` query rows);
+// a row is one token in flight and query head of the KV head's group.  Its
+// work is the tiles of keys it looks at.  All units' tiles, in the order of
+// sequence, head, row group, form one line that is cut into `parts` nearly
+// equal ranges, one per CTA: every CTA gets the same share however ragged the
+// batch is, and a long sequence is spread over as many CTAs as its share of
+// the work.  A unit that a cut divides is joined from its pieces afterwards.
+#pragma once
+
+#ifdef __CUDACC__
+#define ATTN_HD __host__ __device__ __forceinline__
+#else
+#define ATTN_HD inline
+#endif
+
+namespace attn {
+
+struct PlanDims {
+  int kv_heads, group;      // query heads of a KV head
+  int unit_rows, tile;      // rows of a unit, keys of a tile
+};
+
+ATTN_HD int row_groups(const PlanDims& d, int n) {
+  return (int)(((long long)n * d.group + d.unit_rows - 1) / d.unit_rows);
+}
+ATTN_HD int key_tiles(const PlanDims& d, int len, int n) { return (int)(((long long)len + n + d.tile - 1) / d.tile); }
+// Tiles of all units of a sequence.
+ATTN_HD long long sequence_tiles(const PlanDims& d, int len, int n) {
+  return n <= 0 ? 0 : (long long)d.kv_heads * row_groups(d, n) * key_tiles(d, len, n);
+}
+
+// First tile of part c, and the part that holds tile t.
+ATTN_HD long long part_begin(long long total, int parts, int c) { return (long long)((__int128)total * c / parts); }
+ATTN_HD int part_of(long long total, int parts, long long t) {
+  return (int)((((__int128)t + 1) * parts - 1) / total);
+}
+
+// One piece of a unit: key tiles [kt0, kt1) of its `tiles`.
+struct Piece {
+  int head, rows_group;  // within the sequence
+  int kt0, kt1, tiles;
+  long long unit_begin;  // first tile of the unit on the line
+};
+
+// The piece that starts at tile `t` of the line and ends before `end`, where
+// the sequence's first tile is `base`.
+ATTN_HD Piece piece_at(const PlanDims& d, int len, int n, long long base, long long t, long long end) {
+  Piece p;
+  p.tiles = key_tiles(d, len, n);
+  const long long u = (t - base) / p.tiles;
+  p.unit_begin = base + u * p.tiles;
+  p.kt0 = (int)(t - p.unit_begin);
+  const long long left = end - p.unit_begin;
+  p.kt1 = left < p.tiles ? (int)left : p.tiles;
+  const int groups = row_groups(d, n);
+  p.head = (int)(u / groups);
+  p.rows_group = (int)(u % groups);
+  return p;
+}
+
+}  // namespace attn

@@ -1,10 +1,50 @@
-// Attention of the tokens in flight over a paged cache: one block per token
-// and query head, a running maximum and sum over the keys.
-#include "attn.cuh"
+// Attention of the tokens in flight over a paged cache, on the 5th-generation
+// tensor cores.
+//
+// Rows (token in flight x query head of a KV head) are the M side of both
+// products; a piece of work is up to 256 rows against a run of key tiles:
+//
+//   S = Q . K^T            Q in shared memory, K tile by TMA        -> TMEM
+//   P = exp2(S c - m)      one thread per row: running maximum and sum -> TMEM (16 bits)
+//   O += P . V             P from TMEM, V tile by TMA               -> TMEM
+//
+// What bounds it: K and V are read once per 256 rows (128 for wide heads), so a
+// few rows are HBM bound, whatever part of the 128 MMA rows they fill (a tile of
+// 128 keys is 64 KB at D = 128: about 2800 cycles of an SM's share of HBM, and 1024
+// of MMA); from some 200 rows the MMAs and the exponentials bound it.
+//
+// Two streams of tiles run through one CTA, each with its own S and O in TMEM
+// and its own warpgroup, so that one's softmax runs under the other's MMAs.
+// With more than 128 rows the streams are the two halves of the rows over the
+// same keys; otherwise they are the even and the odd key tiles over the same
+// rows, and their O, m, l are joined at the end of the piece.  Heads wider
+// than 128 leave TMEM for one O: one stream with two S buffers.
+//
+// The MMAs are issued S(i + 1) before O(i), so a softmax always has the other
+// tile's S product running beside it.  The running maximum moves only when a
+// row's scores outgrow it by kLag (in powers of two): O is rescaled rarely.
+// For FP16 the weights carry a factor 2^kLift, which keeps those down to
+// 2^-24 of the largest out of FP16's subnormals; it cancels with the sum.
+//
+// Work division: attn_plan.h.  Pieces of a divided unit go to the workspace
+// (unscaled O, m, l) and join_kernel adds them up in their order, so results
+// repeat bit for bit.
+//
+// What a row must not see: scores are replaced by -inf, and values that could
+// reach the product with weight 0 (slots past the end of the sequence, NaN or
+// infinite elements of drafts) are zeroed in shared memory; the latter are put
+// back, for the rows that do see them, when the piece is written.
+#include "attn_plan.h"
+#include "attn_tma.cuh"
+
+using namespace moe::tc;
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kThreads = 320;  // warps 0-3, 4-7: softmax of streams 0, 1; 8: TMA; 9: MMA
+constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far beyond any legitimate wait
+constexpr float kNaN = __builtin_nanf("");
 
 struct TreeArgs {
   const void* q;
@@ -15,81 +55,691 @@ struct TreeArgs {
   int tree_words;
   float scale;
   attn_cache c;
+  attn::Maps maps;
   void* out;
   float* lse;
   int32_t* st;
+  struct Split* splits;  // [parts]
+  float* ml;             // [parts][2][rows][2]
+  float4* o;             // [parts][2][DP / 4][rows]
 };
 
+// The divided unit whose first piece ends part c, if there is one.
+struct Split {
+  int pieces;  // 0: none
+  int first, n, head, row0, rows;
+};
+
+template <int DP_>
+struct Cfg {
+  static constexpr int DP = DP_;
+  static constexpr int STREAMS = DP <= 128 ? 2 : 1;
+  static constexpr int BN = DP <= 128 ? 128 : 64;      // keys of a tile
+  static constexpr int ROWS = 128 * STREAMS;           // rows of a unit
+  static constexpr int SLOT = BN * DP * 2;             // bytes of a K or V tile
+  static constexpr int SLOTS = DP == 64 ? 10 : 5;
+  static constexpr int QTILE = 128 * DP * 2;
+  static constexpr int PANEL = BN * 128;               // 64 elements of a tile's rows
+  static constexpr int S_COL = 0, O_COL = 2 * BN;      // S buffers, then O of each stream
+  static constexpr int TMEM = 512;
+  static_assert(O_COL + STREAMS * DP <= TMEM, "TMEM");
+  static constexpr size_t OFF_Q = 0;
+  static constexpr size_t OFF_RING = OFF_Q + (size_t)STREAMS * QTILE;
+  static constexpr size_t OFF_CTRL = OFF_RING + (size_t)SLOTS * SLOT;
+};
+
+struct Control {
+  uint64_t full[10], empty[10];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t q_full, qk_done, pv_done, drain;
+  long long scan[kThreads / 32];
+  long long base0, t0, t1, total;
+  int b0;
+  uint32_t tmem;
+  int abort;
+  int bad_page[8];   // piece number, at index piece % 8, that met a bad page
+  int dirty[8];      // ... whose drafts' values hold NaN or infinity
+  float2 ml[128];    // stream 1's m and l for the join
+};
+template <class C>
+constexpr size_t smem_bytes() {
+  return 1024 + C::OFF_CTRL + sizeof(Control);
+}
+static_assert(smem_bytes<Cfg<64>>() <= 232448 && smem_bytes<Cfg<128>>() <= 232448 && smem_bytes<Cfg<256>>() <= 232448,
+              "shared memory");
+
 template <class E>
-__global__ void __launch_bounds__(kWarps * 32) tree_kernel(const __grid_constant__ TreeArgs a) {
-  using T = typename E::T;
-  __shared__ float s_o[kWarps][256];
-  __shared__ float s_m[kWarps], s_l[kWarps];
-  const int t = blockIdx.x, hq = blockIdx.y, D = a.c.head_dim;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int d0 = lane * 8;
-  const int b = attn::sequence_of(a.cu, a.c.batch, t);
-  const attn::Seq s = attn::sequence(a.cu, a.lens, b, a.tokens, (long long)a.c.max_pages * a.c.page_size);
-  const bool ok = s.ok && t >= s.first && t < s.first + s.n;
-  const int h = hq / (a.q_heads / a.c.kv_heads);
-  float q[8] = {}, o[8] = {};
-  float m = -INFINITY, l = 0.f;
-  if (d0 < D) {
-    attn::unpack8<E>(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + t * a.q_stride + (long long)hq * D + d0), q);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] *= a.scale;
+struct Weight {  // P = exp2(s - m + kLift), m lagging the maximum by up to kLag
+  static constexpr float kLift = 0.f, kLag = 8.f;
+};
+template <>
+struct Weight<attn::Half> {
+  static constexpr float kLift = 10.f, kLag = 5.f;
+};
+
+// The pieces of one CTA, in order; every role walks them on its own.
+struct Walk {
+  const TreeArgs& a;
+  attn::PlanDims d;
+  long long base, t, t1;
+  int b, number;
+  attn::Seq s;
+  attn::Piece p;
+  int row0, rows;  // of the unit, counted in rows of the sequence and KV head
+
+  __device__ Walk(const TreeArgs& args, const attn::PlanDims& dims, const Control& c)
+      : a(args), d(dims), base(c.base0), t(c.t0), t1(c.t1), b(c.b0), number(-1) {
+    if (t < t1) s = attn::sequence(a.cu, a.lens, b, a.tokens, attn::kMaxSlots);
   }
-  bool bad = !ok;
-  for (int j = warp; j < (ok ? s.len + s.n : 0); j += kWarps) {
-    if (j >= s.len) {
-      const int d = j - s.len;
-      const uint32_t w = a.tree ? attn::tree_bits(a.tree + (long long)t * a.tree_words, a.tree_words, d) : attn::chain_bits(t - s.first, d);
-      if (!(w & 1u)) continue;
+  __device__ bool next() {
+    if (t >= t1) return false;
+    long long w = attn::sequence_tiles(d, s.len, s.n);
+    while (t >= base + w) {
+      base += w;
+      s = attn::sequence(a.cu, a.lens, ++b, a.tokens, attn::kMaxSlots);
+      w = attn::sequence_tiles(d, s.len, s.n);
     }
-    const long long off = attn::slot_offset(a.c, b, j, h);
-    if (off < 0) {
-      bad = true;
-      moe::status_or(a.st, ATTN_DEV_BAD_PAGE);
-      continue;
-    }
-    float k[8] = {}, v[8] = {};
-    if (d0 < D) {
-      attn::unpack8<E>(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.c.k) + off + d0), k);
-      attn::unpack8<E>(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.c.v) + off + d0), v);
-    }
-    float x = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x = fmaf(q[i], k[i], x);
-    x = moe::warp_sum(x);
-    const float top = fmaxf(m, x);
-    const float f = __expf(m - top), p = __expf(x - top);
-    l = l * f + p;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = o[i] * f + p * v[i];
-    m = top;
+    p = attn::piece_at(d, s.len, s.n, base, t, t1);
+    t += p.kt1 - p.kt0;
+    row0 = p.rows_group * d.unit_rows;
+    rows = min(d.unit_rows, s.n * d.group - row0);
+    ++number;
+    return true;
   }
-  if (!ok && threadIdx.x == 0) moe::status_or(a.st, ATTN_DEV_BAD_LENGTH);
-  if (bad) l = __uint_as_float(0x7FC00000u), m = 0.f;
+  __device__ bool whole() const { return p.kt0 == 0 && p.kt1 == p.tiles; }
+};
+
+template <class C>
+__device__ __forceinline__ attn::PlanDims plan_dims(const TreeArgs& a) {
+  return attn::PlanDims{a.c.kv_heads, a.q_heads / a.c.kv_heads, C::ROWS, C::BN};
+}
+
+// Scans the batch: this CTA's range of tiles, and the sequence it starts in.
+// False if lens or cu are out of range (the same verdict in every CTA).
+template <class C>
+__device__ bool make_plan(const TreeArgs& a, Control& ctl) {
+  const attn::PlanDims d = plan_dims<C>(a);
+  const int B = a.c.batch, per = (B + kThreads - 1) / kThreads;
+  const int b0 = min((int)threadIdx.x * per, B), b1 = min(b0 + per, B);
+  const long long cap = (long long)a.c.max_pages * a.c.page_size;
+  long long mine = 0;
+  bool ok = true;
+  for (int b = b0; b < b1; ++b) {
+    const attn::Seq s = attn::sequence(a.cu, a.lens, b, a.tokens, cap);
+    ok &= s.ok;
+    if (s.ok) mine += attn::sequence_tiles(d, s.len, s.n);
+  }
+  if (threadIdx.x == 0) ok &= __ldg(a.cu) == 0 && __ldg(a.cu + B) == a.tokens;
+  long long upto = mine;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s_o[warp][d0 + i] = o[i];
-  if (lane == 0) s_m[warp] = m, s_l[warp] = l;
+  for (int k = 1; k < 32; k <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, upto, k);
+    if (lane >= k) upto += o;
+  }
+  if (lane == 31) ctl.scan[warp] = upto;
+  if (!__syncthreads_and(ok)) return false;
+  long long total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) upto += ctl.scan[w];
+    total += ctl.scan[w];
+  }
+  const int parts = (int)min((long long)gridDim.x, total), c = blockIdx.x;
+  const long long t0 = c < parts ? attn::part_begin(total, parts, c) : 0;
+  const long long t1 = c < parts ? attn::part_begin(total, parts, c + 1) : 0;
+  if (threadIdx.x == 0) ctl.t0 = t0, ctl.t1 = t1, ctl.total = total;
+  if (t0 < t1 && upto - mine <= t0 && t0 < upto) {
+    long long base = upto - mine;
+    int b = b0;
+    for (;; ++b) {
+      const attn::Seq s = attn::sequence(a.cu, a.lens, b, a.tokens, cap);
+      const long long w = attn::sequence_tiles(d, s.len, s.n);
+      if (t0 < base + w) break;
+      base += w;
+    }
+    ctl.b0 = b;
+    ctl.base0 = base;
+  }
   __syncthreads();
-  if (warp != 0) return;
-  float top = -INFINITY;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
-  float sum = 0.f, y[8] = {};
-  for (int w = 0; w < kWarps; ++w) {
-    const float f = s_m[w] == -INFINITY ? 0.f : __expf(s_m[w] - top);
-    sum += s_l[w] * f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] += s_o[w][d0 + i] * f;
+  return true;
+}
+
+// Which of keys k0 .. k0 + 31 the row's token sees.
+__device__ __forceinline__ uint32_t seen(const TreeArgs& a, const attn::Seq& s, int token, int k0) {
+  const int old = s.len - k0, all = s.len + s.n - k0;
+  const uint32_t below = all >= 32 ? 0xFFFFFFFFu : all <= 0 ? 0u : (1u << all) - 1u;
+  const uint32_t committed = old >= 32 ? 0xFFFFFFFFu : old <= 0 ? 0u : (1u << old) - 1u;
+  if (old >= 32) return 0xFFFFFFFFu;
+  const uint32_t drafts = a.tree ? attn::tree_bits(a.tree + (long long)(s.first + token) * a.tree_words, a.tree_words, -old)
+                                 : attn::chain_bits(token, -old);
+  return (committed | drafts) & below;
+}
+
+template <class E, int DP>
+__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeArgs a) {
+  using C = Cfg<DP>;
+  using T = typename E::T;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* sQ = smem + C::OFF_Q;
+  uint8_t* sRing = smem + C::OFF_RING;
+  Control& ctl = *reinterpret_cast<Control*>(smem + C::OFF_CTRL);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int D = a.c.head_dim, G = a.q_heads / a.c.kv_heads;
+  const int panels = (D + 63) / 64;
+  constexpr int kWorkers = 128 * C::STREAMS;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::SLOTS; ++i) {
+      mbar_init(&ctl.full[i], 1);
+      mbar_init(&ctl.empty[i], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&ctl.s_full[x], 1);
+      mbar_init(&ctl.p_full[x], 128);
+      mbar_init(&ctl.o_full[x], 1);
+    }
+    mbar_init(&ctl.q_full, kWorkers);
+    mbar_init(&ctl.qk_done, 1);
+    mbar_init(&ctl.pv_done, 1);
+    mbar_init(&ctl.drain, 1);
+    ctl.abort = 0;
+    for (int i = 0; i < 8; ++i) ctl.bad_page[i] = ctl.dirty[i] = -1;
+    mbar_fence_init();
+    attn::prefetch_map(&a.maps.k);
+    attn::prefetch_map(&a.maps.v);
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  moe::pdl_wait();
+  moe::pdl_launch_dependents();
+  if (!make_plan<C>(a, ctl)) {  // (its barriers also publish the set-up above)
+    if (threadIdx.x == 0) {
+      if (blockIdx.x == 0) moe::status_or(a.st, ATTN_DEV_BAD_LENGTH);
+      a.splits[blockIdx.x].pieces = 0;
+    }
+    const long long rows = (long long)a.tokens * a.q_heads, step = (long long)gridDim.x * kThreads;
+    const float nan8[8] = {kNaN, kNaN, kNaN, kNaN, kNaN, kNaN, kNaN, kNaN};
+    for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < rows * (D / 8); i += step)
+      reinterpret_cast<uint4*>(a.out)[i] = attn::pack8<E>(nan8);
+    for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; a.lse && i < rows; i += step) a.lse[i] = kNaN;
+    return;
+  }
+  if (ctl.t0 >= ctl.t1) {
+    if (threadIdx.x == 0) a.splits[blockIdx.x].pieces = 0;
+    return;
+  }
+  if (warp == kMmaWarp) tmem_alloc(&ctl.tmem, C::TMEM);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = ctl.tmem;
+  const attn::PlanDims dims = plan_dims<C>(a);
+  volatile int* abort_flag = &ctl.abort;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (mbar_test(bar, parity)) return true;
+    const uint64_t deadline = globaltimer() + kWaitNs;
+    while (!mbar_test(bar, parity)) {
+      if (*abort_flag) return false;
+      if (globaltimer() > deadline) {
+        moe::status_or(a.st, MOE_DEV_TIMEOUT);
+        *abort_flag = 1;
+        return false;
+      }
+    }
+    return true;
+  };
+
+  if (warp == kTmaWarp) {
+    // ------------------------------------------------------------- TMA
+    // Slots are filled K, V, K, V, ... in key order; lane i issues box i of
+    // the tile's at most 32 (8-row boxes of two panels of 128 rows, or four of 64).
+    Walk w(a, dims, ctl);
+    int pos = 0;  // slots filled so far
+    bool alive = true;
+    const int box_rows = a.maps.box_rows, boxes = C::BN / box_rows;
+    const int my_box = lane % boxes, my_panel = lane / boxes;
+    while (alive && w.next()) {
+      const int end = w.s.len + w.s.n;
+      const int32_t* table = a.c.page_table + (size_t)w.b * a.c.max_pages;
+      for (int j = w.p.kt0; j < w.p.kt1 && alive; ++j) {
+        const int slot0 = j * C::BN, start = slot0 + my_box * box_rows;
+        const int issued = min(boxes, (end - slot0 + box_rows - 1) / box_rows);
+        int page = 0, row = 0;
+        if (my_box < issued) {
+          const int pi = start / a.c.page_size;
+          page = __ldg(table + pi);
+          row = start - pi * a.c.page_size;
+          if ((unsigned)page >= (unsigned)a.c.pages) {
+            page = a.c.pages;  // past the last: the copy delivers zeros
+            ctl.bad_page[w.number & 7] = w.number;
+            moe::status_or(a.st, ATTN_DEV_BAD_PAGE);
+          }
+        }
+        __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] *= inv;
-  if (d0 < D)
-    *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + ((long long)t * a.q_heads + hq) * D + d0) = attn::pack8<E>(y);
-  if (lane == 0 && a.lse) a.lse[(long long)t * a.q_heads + hq] = sum == 0.f ? -INFINITY : top + logf(sum);
+        for (int kv = 0; kv < 2; ++kv, ++pos) {
+          const int slot = pos % C::SLOTS;
+          alive = alive && wait(&ctl.empty[slot], ((pos / C::SLOTS) & 1) ^ 1);
+          alive = __all_sync(0xffffffffu, alive);
+          if (!alive) break;
+          if (lane == 0) mbar_arrive_expect_tx(&ctl.full[slot], (uint32_t)(issued * box_rows * 128 * panels));
+          __syncwarp();
+          const uint32_t dst = smem_u32(sRing + (size_t)slot * C::SLOT) + (uint32_t)(my_box * box_rows * 128);
+          if (my_box < issued)
+            for (int p = my_panel; p < panels; p += 32 / boxes)
+              attn::load_box(kv ? &a.maps.v : &a.maps.k, dst + p * C::PANEL, &ctl.full[slot], p * 64, row, w.p.head,
+                             page, a.maps.head_inner);
+        }
+      }
+    }
+    // every copy has landed before the CTA's shared memory goes away
+    if (lane == 0)
+      for (int i = max(0, pos - C::SLOTS); i < pos; ++i) {
+        const uint64_t deadline = globaltimer() + kWaitNs;
+        mbar_wait(&ctl.full[i % C::SLOTS], (i / C::SLOTS) & 1, deadline);
+      }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------- MMA
+    if (lane == 0) {
+      Walk w(a, dims, ctl);
+      int pos = 0, pieces = 0, p_seen[2] = {0, 0};
+      bool alive = true;
+      const int k_steps = (D + 15) / 16;
+      const uint32_t id_s = attn::idesc<E>(128, C::BN, false);
+      const uint32_t id_o = attn::idesc<E>(128, (D + 15) & ~15, true);
+      while (alive && w.next()) {
+        const bool both = C::STREAMS == 2 && w.rows > 128;  // two row tiles over the same keys
+        const int tiles = w.p.kt1 - w.p.kt0, items = both ? 2 * tiles : tiles;
+        alive = wait(&ctl.q_full, pieces & 1);
+        if (!alive) break;
+        fence_after_sync();
+        auto qk = [&](int it) {
+          const int x = it & 1, ps = pos + 2 * (both ? it >> 1 : it), slot = ps % C::SLOTS;
+          if (!both || x == 0) {
+            if (!wait(&ctl.full[slot], (ps / C::SLOTS) & 1)) return false;
+            fence_after_sync();
+          }
+          const uint32_t qa = smem_u32(sQ + (both && x ? C::QTILE : 0));
+          const uint32_t ka = smem_u32(sRing + (size_t)slot * C::SLOT);
+          for (int kk = 0; kk < k_steps; ++kk)
+            mma_bf16(tmem + C::S_COL + x * C::BN, sw128_kmajor_desc(qa + (kk >> 2) * 128 * 128 + (kk & 3) * 32),
+                     sw128_kmajor_desc(ka + (kk >> 2) * C::PANEL + (kk & 3) * 32), id_s, kk != 0);
+          mma_commit(&ctl.s_full[x]);
+          if (!both || x == 1) mma_commit(&ctl.empty[slot]);
+          if (it == items - 1) mma_commit(&ctl.qk_done);
+          return true;
+        };
+        auto pv = [&](int it) {
+          const int x = it & 1, ps = pos + 2 * (both ? it >> 1 : it) + 1, slot = ps % C::SLOTS;
+          const int st = C::STREAMS == 2 ? x : 0;  // whose O
+          if (!wait(&ctl.p_full[x], p_seen[x]++ & 1)) return false;
+          if ((!both || x == 0) && !wait(&ctl.full[slot], (ps / C::SLOTS) & 1)) return false;
+          fence_after_sync();
+          const uint32_t va = smem_u32(sRing + (size_t)slot * C::SLOT);
+          const bool first = C::STREAMS == 2 ? it < 2 : it == 0;
+#pragma unroll
+          for (int kk = 0; kk < C::BN / 16; ++kk)
+            attn::mma_ts(tmem + C::O_COL + st * DP, tmem + C::S_COL + x * C::BN + kk * 8,
+                         attn::sw128_mnmajor_desc(va + kk * 2048, C::PANEL), id_o, !(first && kk == 0));
+          if (!both || x == 1) mma_commit(&ctl.empty[slot]);
+          if (C::STREAMS == 1) mma_commit(&ctl.pv_done);
+          if (it >= items - C::STREAMS) mma_commit(&ctl.o_full[st]);
+          return true;
+        };
+        alive = qk(0);
+        for (int it = 0; it < items && alive; ++it) {
+          if (it + 1 < items) alive = qk(it + 1);
+          alive = alive && pv(it);
+        }
+        pos += 2 * tiles;
+        ++pieces;
+      }
+      // every MMA has completed before TMEM goes back
+      mma_commit(&ctl.drain);
+      mbar_wait(&ctl.drain, 0, globaltimer() + kWaitNs);
+    }
+    __syncwarp();
+  } else if (warp < 4 * C::STREAMS) {
+    // ------------------------------------------------------------- softmax
+    const int st = warp >> 2, wl = warp & 3;
+    const int r_tile = wl * 32 + lane;  // this thread's row of its 128
+    const uint32_t lane_base = (uint32_t)(wl * 32) << 16;
+    const uint32_t o_addr = tmem + lane_base + C::O_COL + st * DP;
+    const float c2 = fabsf(a.scale) * 1.4426950408889634f;
+    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;  // a negative scale turns q's signs instead
+    constexpr float kLift = Weight<E>::kLift, kLag = Weight<E>::kLag;
+    // the TMEM accesses below need whole warps: a warp gives up together
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+    Walk w(a, dims, ctl);
+    int pos = 0, s_seen[2] = {0, 0}, o_seen = 0, pieces = 0, pv_seen = 0;
+    bool alive = true;
+    if (threadIdx.x == 0) a.splits[blockIdx.x].pieces = 0;
+    while (w.next()) {
+      const bool both = C::STREAMS == 2 && w.rows > 128;
+      const int tiles = w.p.kt1 - w.p.kt0, items = both ? 2 * tiles : tiles;
+      // ---- Q into shared memory: rows of 16-byte chunks, zeros past D
+      alive = alive && (pieces == 0 || warp_wait(&ctl.qk_done, (pieces - 1) & 1));
+      {
+        const int t0 = both ? 128 * st : 0, n_rows = min(128, w.rows - t0);
+        uint8_t* dst = sQ + (both ? st * C::QTILE : 0);
+        const int n_thr = both ? 128 : kWorkers, me = both ? threadIdx.x & 127 : threadIdx.x;
+        const int chunks = panels * 8;
+        const T* q = static_cast<const T*>(a.q);
+        for (int i = me; i < n_rows * chunks; i += n_thr) {
+          const int r = i / chunks, ch = i - r * chunks;
+          const int row = w.row0 + t0 + r, tok = row / G, g = row - tok * G;
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (ch * 8 < D)
+            v = *reinterpret_cast<const uint4*>(q + (long long)(w.s.first + tok) * a.q_stride + ((long long)w.p.head * G + g) * D + ch * 8);
+          v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+          *reinterpret_cast<uint4*>(dst + attn::sw128_offset(r, ch, 128)) = v;
+        }
+        fence_proxy_async();
+        mbar_arrive(&ctl.q_full);
+      }
+      const int tile_rows = both ? w.rows - 128 * st : w.rows;    // of this warpgroup's row tile
+      const bool active = wl * 32 < tile_rows;                    // whether the warp has rows at all
+      const int row = w.row0 + (both ? 128 * st : 0) + r_tile;    // of the sequence and head
+      const int token = min(row / G, w.s.n - 1);
+      const bool real = row < w.row0 + w.rows;
+      float m = -INFINITY, l = 0.f;  // m in powers of two
+      int done = 0;
+      for (int it = (C::STREAMS == 2 ? st : 0); it < items && alive; it += C::STREAMS) {
+        const int x = it & 1, tile = both ? it >> 1 : it;
+        const int k0 = (w.p.kt0 + tile) * C::BN;
+        const uint32_t s_addr = tmem + lane_base + C::S_COL + x * C::BN;
+        // ---- clean V where the tile reaches past the committed slots
+        if (k0 + C::BN > w.s.len && (!both || st == 0)) {
+          const int ps = pos + 2 * tile + 1;
+          alive = warp_wait(&ctl.full[ps % C::SLOTS], (ps / C::SLOTS) & 1);
+          if (!alive) break;
+          uint8_t* v = sRing + (size_t)(ps % C::SLOTS) * C::SLOT;
+          const int lo = max(0, w.s.len - k0), hi = w.s.len + w.s.n - k0;
+          const int chunks = panels * 8;
+          for (int i = lo * chunks + (threadIdx.x & 127); i < C::BN * chunks; i += 128) {
+            const int r = i / chunks, ch = i - r * chunks;
+            uint4* at = reinterpret_cast<uint4*>(v + attn::sw128_offset(r, ch, C::BN));
+            if (r >= hi) {
+              *at = make_uint4(0u, 0u, 0u, 0u);
+            } else {
+              uint32_t e[4] = {at->x, at->y, at->z, at->w};
+              bool changed = false;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float2 f = E::up(e[q]);
+                if (!isfinite(f.x)) e[q] &= 0xFFFF0000u, changed = true;
+                if (!isfinite(f.y)) e[q] &= 0x0000FFFFu, changed = true;
+              }
+              if (changed) {
+                *at = make_uint4(e[0], e[1], e[2], e[3]);
+                ctl.dirty[w.number & 7] = w.number;
+              }
+            }
+          }
+          fence_proxy_async();
+        }
+        alive = alive && warp_wait(&ctl.s_full[x], s_seen[x]++ & 1);
+        if (!alive) break;
+        fence_after_sync();
+        if (active) {
+          float s[C::BN];
+#pragma unroll
+          for (int i = 0; i < C::BN; i += 32) attn::tmem_ld32(s_addr + i, s + i);
+          tmem_ld_wait();
+          if (k0 + C::BN > w.s.len) {
+#pragma unroll
+            for (int i = 0; i < C::BN; i += 32) {
+              const uint32_t bits = seen(a, w.s, token, k0 + i);
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (!((bits >> q) & 1u)) s[i + q] = -INFINITY;
+            }
+          }
+          float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < C::BN; i += 8)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) t[q] = attn::max3(t[q], s[i + 2 * q], s[i + 2 * q + 1]);
+          const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * c2;
+          // the first tile takes its maximum; later ones move it only by more than kLag
+          const bool grow = real && top > (done ? m + kLag : m);
+          if (__any_sync(0xffffffffu, grow)) {
+            const float m1 = grow ? top : m;
+            if (done) {
+              if (C::STREAMS == 1) {  // O still takes the tile before: wait for that product
+                alive = warp_wait(&ctl.pv_done, (pv_seen + done - 1) & 1);
+                fence_after_sync();
+              }
+              const float f = m == -INFINITY ? 0.f : attn::exp2_fast(m - m1);
+              l *= f;
+              float o[32];
+              for (int i = 0; i < DP; i += 32) {
+                attn::tmem_ld32(o_addr + i, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int q = 0; q < 32; ++q) o[q] *= f;
+                attn::tmem_st32(o_addr + i, o);
+              }
+            }
+            m = m1;
+          }
+          const float bias = kLift - (m == -INFINITY ? 0.f : m);
+          const float2 c22 = make_float2(c2, c2), b22 = make_float2(bias, bias);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const float2 ones = make_float2(1.f, 1.f);
+#pragma unroll
+          for (int i = 0; i < C::BN; i += 32) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int q = 0; q < 32; q += 2) {
+              float2 e = moe::ffma2(make_float2(s[i + q], s[i + q + 1]), c22, b22);
+              e.x = attn::exp2_fast(e.x);
+              e.y = attn::exp2_fast(e.y);
+              sum[(q >> 1) & 1] = moe::ffma2(e, ones, sum[(q >> 1) & 1]);
+              pk[q >> 1] = E::down(e.x, e.y);
+            }
+            attn::tmem_st16(s_addr + i / 2, pk);
+          }
+          attn::tmem_st_wait();
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        }
+        ++done;
+        fence_before_sync();
+        mbar_arrive(&ctl.p_full[x]);
+      }
+      pv_seen += done;
+      if (l != l && m == -INFINITY) m = 0.f;  // only NaN scores: not to be mistaken for a row that saw nothing
+      // ---- the piece's result
+      const bool has = done > 0;
+      if (has && alive) {
+        alive = warp_wait(&ctl.o_full[st], o_seen & 1);
+        fence_after_sync();
+      }
+      o_seen += has;
+      named_sync(1, kWorkers);  // flags of this piece are final
+      const bool dirty = ctl.dirty[w.number & 7] == w.number;
+      const bool broken = !alive || ctl.bad_page[w.number & 7] == w.number;
+      float f0 = 1.f, f1 = 0.f;
+      const bool join = C::STREAMS == 2 && !both && tiles > 1;
+      float* exch = reinterpret_cast<float*>(sQ + C::QTILE);  // [DP / 2][128]: Q's second tile is unused here
+      if (join && st == 1) ctl.ml[r_tile] = make_float2(m, l);
+      const bool writer = (both || st == 0) && active;
+      const int hq = w.p.head * G + row % G;
+      const long long out_row = (long long)(w.s.first + row / G) * a.q_heads + hq;
+      const int side = w.p.kt0 == 0 ? 1 : 0;
+      const int slot_row = (both ? 128 * st : 0) + r_tile;
+      const size_t slot_id = (size_t)blockIdx.x * 2 + side;
+      float inv = 0.f;
+      constexpr int kHalf = C::STREAMS == 2 ? DP / 2 : DP;
+      for (int c0 = 0; c0 < DP; c0 += kHalf) {
+        if (join) {
+          if (st == 1 && active && alive) {
+            for (int i = 0; i < kHalf; i += 32) {
+              float o[32];
+              attn::tmem_ld32(o_addr + c0 + i, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int q = 0; q < 32; ++q) exch[(i + q) * 128 + r_tile] = o[q];
+            }
+          }
+          named_sync(1, kWorkers);
+        }
+        if (writer) {
+          if (c0 == 0) {
+            if (join) {
+              const float2 other = ctl.ml[r_tile];
+              const float top = fmaxf(m, other.x);
+              f0 = m == -INFINITY ? 0.f : attn::exp2_fast(m - top);
+              f1 = other.x == -INFINITY ? 0.f : attn::exp2_fast(other.x - top);
+              l = l * f0 + other.y * f1;
+              m = top;
+            }
+            if (broken) l = kNaN, m = 0.f;
+            inv = l == 0.f ? 0.f : 1.f / l;
+            if (real) {
+              if (!w.whole()) reinterpret_cast<float2*>(a.ml)[slot_id * C::ROWS + slot_row] = make_float2(m, l);
+              else if (a.lse) a.lse[out_row] = l == 0.f ? -INFINITY : (m - kLift) * 0.6931471805599453f + logf(l);
+            }
+          }
+          for (int i = 0; i < kHalf; i += 32) {
+            if (c0 + i >= D) break;
+            float o[32];
+            attn::tmem_ld32(o_addr + c0 + i, o);
+            tmem_ld_wait();
+            if (join) {
+#pragma unroll
+              for (int q = 0; q < 32; ++q) o[q] = o[q] * f0 + (f1 == 0.f ? 0.f : exch[(i + q) * 128 + r_tile] * f1);
+            }
+            if (dirty && real) {  // NaN and infinities of drafts, for the rows that see them
+              const int d0 = max(w.p.kt0 * C::BN - w.s.len, 0), d1 = min(w.p.kt1 * C::BN - w.s.len, w.s.n);
+              for (int dr = d0; dr < d1; ++dr) {
+                if (!(seen(a, w.s, token, w.s.len + dr) & 1u)) continue;
+                const long long off = attn::slot_offset(a.c, w.b, w.s.len + dr, w.p.head);
+                if (off < 0) continue;
+                const T* v = static_cast<const T*>(a.c.v) + off + c0 + i;
+#pragma unroll
+                for (int q = 0; q < 32; ++q) {
+                  if (c0 + i + q >= D) break;
+                  const float e = (float)v[q];
+                  if (!isfinite(e)) o[q] += e;
+                }
+              }
+            }
+            if (real && w.whole()) {
+#pragma unroll
+              for (int q = 0; q < 32; q += 8) {
+                if (c0 + i + q >= D) break;
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = o[q + e] * inv;
+                *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + out_row * D + c0 + i + q) = attn::pack8<E>(y);
+              }
+            } else if (real) {
+#pragma unroll
+              for (int q = 0; q < 32; q += 4)
+                if (c0 + i + q < D)
+                  a.o[(slot_id * (DP / 4) + (c0 + i + q) / 4) * C::ROWS + slot_row] = make_float4(o[q], o[q + 1], o[q + 2], o[q + 3]);
+            }
+            __syncwarp();
+          }
+        }
+        if (join) named_sync(1, kWorkers);
+      }
+      fence_before_sync();  // O has been read before the next piece's first P is announced
+      if (threadIdx.x == 0 && w.p.kt0 == 0 && !w.whole()) {
+        Split s;
+        const int parts = (int)min((long long)gridDim.x, ctl.total);
+        s.pieces = attn::part_of(ctl.total, parts, w.p.unit_begin + w.p.tiles - 1) - blockIdx.x + 1;
+        s.first = w.s.first, s.n = w.s.n, s.head = w.p.head, s.row0 = w.row0, s.rows = w.rows;
+        a.splits[blockIdx.x] = s;
+      }
+      pos += 2 * tiles;
+      ++pieces;
+    }
+  }
+  fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, C::TMEM);
+}
+
+// Adds up the pieces of divided units.  Block (part, 32 rows): lane = row,
+// warps share the columns.
+constexpr int kJoinThreads = 256;
+
+template <class E, int DP>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ TreeArgs a) {
+  using C = Cfg<DP>;
+  using T = typename E::T;
+  moe::pdl_wait();
+  const int part = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Split s = a.splits[part];
+  const int r = blockIdx.y * 32 + lane;
+  if (blockIdx.y * 32 >= s.rows * (s.pieces > 0)) return;
+  const bool real = r < s.rows;
+  const int rr = real ? r : 0;
+  const int D = a.c.head_dim, G = a.q_heads / a.c.kv_heads;
+  const float2* ml = reinterpret_cast<const float2*>(a.ml);
+  auto id = [&](int i) { return (size_t)(part + i) * 2 + (i == 0); };
+  float top = -INFINITY;
+  for (int i = 0; i < s.pieces; ++i) top = fmaxf(top, ml[id(i) * C::ROWS + rr].x);
+  float l = 0.f;
+  for (int i = 0; i < s.pieces; ++i) {
+    const float2 v = ml[id(i) * C::ROWS + rr];
+    l += v.x == -INFINITY ? 0.f : v.y * attn::exp2_fast(v.x - top);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int row = s.row0 + rr;
+  const long long out_row = (long long)(s.first + row / G) * a.q_heads + s.head * G + row % G;
+  if (warp == 0 && real && a.lse)
+    a.lse[out_row] = l == 0.f ? -INFINITY : (top - Weight<E>::kLift) * 0.6931471805599453f + logf(l);
+  for (int c8 = warp; c8 < D / 8; c8 += kJoinThreads / 32) {
+    float y[8] = {};
+    for (int i = 0; i < s.pieces; ++i) {
+      const float m = ml[id(i) * C::ROWS + rr].x;
+      if (m == -INFINITY) continue;
+      const float f = attn::exp2_fast(m - top);
+      const float4* o = a.o + (id(i) * (DP / 4) + c8 * 2) * C::ROWS + rr;
+      const float4 u = o[0], v = o[C::ROWS];
+      y[0] += u.x * f, y[1] += u.y * f, y[2] += u.z * f, y[3] += u.w * f;
+      y[4] += v.x * f, y[5] += v.y * f, y[6] += v.z * f, y[7] += v.w * f;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] *= inv;
+    if (real) *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + out_row * D + c8 * 8) = attn::pack8<E>(y);
+  }
+}
+
+struct Layout {
+  size_t ml, o, bytes;
+};
+Layout layout(int sms, int DP, int rows) {
+  Layout w;
+  w.ml = ((size_t)sms * sizeof(Split) + 255) & ~(size_t)255;
+  w.o = w.ml + (size_t)sms * 2 * rows * sizeof(float2);
+  w.bytes = w.o + (size_t)sms * 2 * rows * DP * sizeof(float);
+  return w;
+}
+Layout layout(int sms, int head_dim) {
+  return head_dim <= 64    ? layout(sms, 64, Cfg<64>::ROWS)
+         : head_dim <= 128 ? layout(sms, 128, Cfg<128>::ROWS)
+                           : layout(sms, 256, Cfg<256>::ROWS);
+}
+
+template <class E, int DP>
+int launch(TreeArgs& a, int sms, cudaStream_t st) {
+  using C = Cfg<DP>;
+  static moe::SmemGrant grant;
+  if (const int rc = attn::make_maps(a.c, C::BN, a.maps)) return rc;
+  if (!moe::grant_smem(tree_kernel<E, DP>, smem_bytes<C>(), grant)) return MOE_ERR_CUDA;
+  if (const int rc = moe::launch_pdl(tree_kernel<E, DP>, dim3(sms), dim3(kThreads), smem_bytes<C>(), st, a)) return rc;
+  return moe::launch_pdl(join_kernel<E, DP>, dim3(sms, C::ROWS / 32), dim3(kJoinThreads), 0, st, a);
+}
+
+template <class E>
+int launch(TreeArgs& a, int sms, cudaStream_t st) {
+  if (a.c.head_dim <= 64) return launch<E, 64>(a, sms, st);
+  if (a.c.head_dim <= 128) return launch<E, 128>(a, sms, st);
+  return launch<E, 256>(a, sms, st);
 }
 
 }  // namespace
@@ -99,7 +749,8 @@ extern "C" {
 size_t attn_tree_decode_workspace(const attn_cache* cache) {
   attn_cache c;
   if (attn::check_cache(cache, c)) return 0;
-  return 16;
+  const int sms = moe::device_info().sms;
+  return sms > 0 ? layout(sms, c.head_dim).bytes : 0;
 }
 
 int attn_tree_decode(const void* q, long long q_stride, const int32_t* cu, const int32_t* lens, int tokens,
@@ -110,15 +761,20 @@ int attn_tree_decode(const void* q, long long q_stride, const int32_t* cu, const
   if (const int rc = attn::check_queries(a.c, q, q_stride, cu, lens, tokens, q_heads, tree, tree_words)) return rc;
   if ((!out && tokens > 0) || !workspace) return MOE_ERR_INVALID_ARG;
   if (!moe::aligned16(out) || !moe::aligned16(workspace)) return MOE_ERR_ALIGNMENT;
-  if (ws_bytes < attn_tree_decode_workspace(cache)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!(fabs(scale) >= 1e-30 && fabs(scale) <= 1e30)) return MOE_ERR_INVALID_ARG;
   if (tokens == 0) return MOE_OK;
+  if (ws_bytes < 16) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const int sms = moe::device_info().sms;
+  if (sms <= 0) return MOE_ERR_CUDA;
+  const Layout w = layout(sms, a.c.head_dim);
+  if (ws_bytes < w.bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
   a.q = q, a.q_stride = q_stride, a.cu = cu, a.lens = lens, a.tokens = tokens, a.q_heads = q_heads;
   a.tree = tree, a.tree_words = tree_words, a.scale = (float)scale, a.out = out, a.lse = lse, a.st = dev_status;
+  a.splits = static_cast<Split*>(workspace);
+  a.ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.ml);
+  a.o = reinterpret_cast<float4*>(static_cast<char*>(workspace) + w.o);
   const cudaStream_t st = (cudaStream_t)stream;
-  const dim3 grid(tokens, q_heads);
-  if (a.c.dtype == ATTN_BF16) tree_kernel<attn::Brain><<<grid, kWarps * 32, 0, st>>>(a);
-  else tree_kernel<attn::Half><<<grid, kWarps * 32, 0, st>>>(a);
-  return moe::launch_status();
+  return a.c.dtype == ATTN_BF16 ? launch<attn::Brain>(a, sms, st) : launch<attn::Half>(a, sms, st);
 }
 
 }  // extern "C"

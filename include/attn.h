@@ -102,7 +102,7 @@ size_t attn_tree_decode_workspace(const attn_cache* cache);
  * 64] for draft j (bits past the sequence's tokens are ignored, missing words
  * are 0).  tree = NULL: a chain, token i sees drafts 0 .. i.
  *   s_j = scale * <q, k_j>,  out = sum_j softmax(s)_j v_j,  lse = log sum_j exp(s_j)
- * with FP32 accumulation; the weights are rounded once to the cache's type
+ * with FP32 accumulation (1e-30 <= |scale| <= 1e30); the weights are rounded once to the cache's type
  * as operands of the second product (the sum behind lse is of the unrounded
  * ones).  A token that sees nothing gets out = 0 and lse = -inf.  What a token
  * does not see has no influence on it, NaN and infinities included.

@@ -167,3 +167,14 @@ def test_oracle_tree_rows():
     assert A.sees(words, 2, 0, 3).tolist() == [True, True, True, False, False]
     assert A.sees(words, 2, 2, 3).tolist() == [True, True, False, False, False]
     assert A.sees(None, 1, 1, 3).tolist() == [True, True, True, False]
+
+
+def test_work_division_on_host(tmp_path):
+    """csrc/attn_plan.h walked for thousands of batches by tests/attn_plan_check.cu."""
+    exe = tmp_path / "attn_plan_check"
+    cmd = [build._nvcc(), "-std=c++17", "-O2", "-gencode", "arch=compute_103a,code=sm_103a", "-I", build.CSRC, "-o", str(exe),
+           os.path.join(ROOT, "tests", "attn_plan_check.cu")]
+    r = subprocess.run(cmd, capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0, r.stderr[-2000:]
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0 and ", 0 failed" in r.stdout, r.stdout[-3000:]
