@@ -34,8 +34,8 @@
 // reach the product with weight 0 (slots past the end of the sequence, NaN or
 // infinite elements of drafts) are zeroed in shared memory; the latter are put
 // back, for the rows that do see them, when the piece is written.
-#include "attn_plan.h"
 #include "attn_tma.cuh"
+#include "attn_work.cuh"
 
 using namespace moe::tc;
 
@@ -92,9 +92,7 @@ struct Control {
   uint64_t full[10], empty[10];
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t q_full, qk_done, pv_done, drain;
-  long long scan[kThreads / 32];
-  long long base0, t0, t1, total;
-  int b0;
+  attn::Share share;
   uint32_t tmem;
   int abort;
   int bad_page[8];   // piece number, at index piece % 8, that met a bad page
@@ -117,102 +115,9 @@ struct Weight<attn::Half> {
   static constexpr float kLift = 10.f, kLag = 5.f;
 };
 
-// The pieces of one CTA, in order; every role walks them on its own.
-struct Walk {
-  const TreeArgs& a;
-  attn::PlanDims d;
-  long long base, t, t1;
-  int b, number;
-  attn::Seq s;
-  attn::Piece p;
-  int row0, rows;  // of the unit, counted in rows of the sequence and KV head
-
-  __device__ Walk(const TreeArgs& args, const attn::PlanDims& dims, const Control& c)
-      : a(args), d(dims), base(c.base0), t(c.t0), t1(c.t1), b(c.b0), number(-1) {
-    if (t < t1) s = attn::sequence(a.cu, a.lens, b, a.tokens, attn::kMaxSlots);
-  }
-  __device__ bool next() {
-    if (t >= t1) return false;
-    long long w = attn::sequence_tiles(d, s.len, s.n);
-    while (t >= base + w) {
-      base += w;
-      s = attn::sequence(a.cu, a.lens, ++b, a.tokens, attn::kMaxSlots);
-      w = attn::sequence_tiles(d, s.len, s.n);
-    }
-    p = attn::piece_at(d, s.len, s.n, base, t, t1);
-    t += p.kt1 - p.kt0;
-    row0 = p.rows_group * d.unit_rows;
-    rows = min(d.unit_rows, s.n * d.group - row0);
-    ++number;
-    return true;
-  }
-  __device__ bool whole() const { return p.kt0 == 0 && p.kt1 == p.tiles; }
-};
-
 template <class C>
 __device__ __forceinline__ attn::PlanDims plan_dims(const TreeArgs& a) {
   return attn::PlanDims{a.c.kv_heads, a.q_heads / a.c.kv_heads, C::ROWS, C::BN};
-}
-
-// Scans the batch: this CTA's range of tiles, and the sequence it starts in.
-// False if lens or cu are out of range (the same verdict in every CTA).
-template <class C>
-__device__ bool make_plan(const TreeArgs& a, Control& ctl) {
-  const attn::PlanDims d = plan_dims<C>(a);
-  const int B = a.c.batch, per = (B + kThreads - 1) / kThreads;
-  const int b0 = min((int)threadIdx.x * per, B), b1 = min(b0 + per, B);
-  const long long cap = (long long)a.c.max_pages * a.c.page_size;
-  long long mine = 0;
-  bool ok = true;
-  for (int b = b0; b < b1; ++b) {
-    const attn::Seq s = attn::sequence(a.cu, a.lens, b, a.tokens, cap);
-    ok &= s.ok;
-    if (s.ok) mine += attn::sequence_tiles(d, s.len, s.n);
-  }
-  if (threadIdx.x == 0) ok &= __ldg(a.cu) == 0 && __ldg(a.cu + B) == a.tokens;
-  long long upto = mine;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int k = 1; k < 32; k <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, upto, k);
-    if (lane >= k) upto += o;
-  }
-  if (lane == 31) ctl.scan[warp] = upto;
-  if (!__syncthreads_and(ok)) return false;
-  long long total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) upto += ctl.scan[w];
-    total += ctl.scan[w];
-  }
-  const int parts = (int)min((long long)gridDim.x, total), c = blockIdx.x;
-  const long long t0 = c < parts ? attn::part_begin(total, parts, c) : 0;
-  const long long t1 = c < parts ? attn::part_begin(total, parts, c + 1) : 0;
-  if (threadIdx.x == 0) ctl.t0 = t0, ctl.t1 = t1, ctl.total = total;
-  if (t0 < t1 && upto - mine <= t0 && t0 < upto) {
-    long long base = upto - mine;
-    int b = b0;
-    for (;; ++b) {
-      const attn::Seq s = attn::sequence(a.cu, a.lens, b, a.tokens, cap);
-      const long long w = attn::sequence_tiles(d, s.len, s.n);
-      if (t0 < base + w) break;
-      base += w;
-    }
-    ctl.b0 = b;
-    ctl.base0 = base;
-  }
-  __syncthreads();
-  return true;
-}
-
-// Which of keys k0 .. k0 + 31 the row's token sees.
-__device__ __forceinline__ uint32_t seen(const TreeArgs& a, const attn::Seq& s, int token, int k0) {
-  const int old = s.len - k0, all = s.len + s.n - k0;
-  const uint32_t below = all >= 32 ? 0xFFFFFFFFu : all <= 0 ? 0u : (1u << all) - 1u;
-  const uint32_t committed = old >= 32 ? 0xFFFFFFFFu : old <= 0 ? 0u : (1u << old) - 1u;
-  if (old >= 32) return 0xFFFFFFFFu;
-  const uint32_t drafts = a.tree ? attn::tree_bits(a.tree + (long long)(s.first + token) * a.tree_words, a.tree_words, -old)
-                                 : attn::chain_bits(token, -old);
-  return (committed | drafts) & below;
 }
 
 template <class E, int DP>
@@ -251,7 +156,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   }
   moe::pdl_wait();
   moe::pdl_launch_dependents();
-  if (!make_plan<C>(a, ctl)) {  // (its barriers also publish the set-up above)
+  const attn::PlanDims dims = plan_dims<C>(a);
+  if (!attn::take_share<kThreads>(a.cu, a.lens, a.c.batch, a.tokens, (long long)a.c.max_pages * a.c.page_size, dims, ctl.share)) {  // (its barriers also publish the set-up above)
     if (threadIdx.x == 0) {
       if (blockIdx.x == 0) moe::status_or(a.st, ATTN_DEV_BAD_LENGTH);
       a.splits[blockIdx.x].pieces = 0;
@@ -263,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; a.lse && i < rows; i += step) a.lse[i] = kNaN;
     return;
   }
-  if (ctl.t0 >= ctl.t1) {
+  if (ctl.share.t0 >= ctl.share.t1) {
     if (threadIdx.x == 0) a.splits[blockIdx.x].pieces = 0;
     return;
   }
@@ -272,7 +178,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = ctl.tmem;
-  const attn::PlanDims dims = plan_dims<C>(a);
   volatile int* abort_flag = &ctl.abort;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (mbar_test(bar, parity)) return true;
@@ -292,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     // ------------------------------------------------------------- TMA
     // Slots are filled K, V, K, V, ... in key order; lane i issues box i of
     // the tile's at most 32 (8-row boxes of two panels of 128 rows, or four of 64).
-    Walk w(a, dims, ctl);
+    attn::Walk w(a.cu, a.lens, a.tokens, dims, ctl.share);
     int pos = 0;  // slots filled so far
     bool alive = true;
     const int box_rows = a.maps.box_rows, boxes = C::BN / box_rows;
@@ -341,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------- MMA
     if (lane == 0) {
-      Walk w(a, dims, ctl);
+      attn::Walk w(a.cu, a.lens, a.tokens, dims, ctl.share);
       int pos = 0, pieces = 0, p_seen[2] = {0, 0};
       bool alive = true;
       const int k_steps = (D + 15) / 16;
@@ -410,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     constexpr float kLift = Weight<E>::kLift, kLag = Weight<E>::kLag;
     // the TMEM accesses below need whole warps: a warp gives up together
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
-    Walk w(a, dims, ctl);
+    attn::Walk w(a.cu, a.lens, a.tokens, dims, ctl.share);
     int pos = 0, s_seen[2] = {0, 0}, o_seen = 0, pieces = 0, pv_seen = 0;
     bool alive = true;
     if (threadIdx.x == 0) a.splits[blockIdx.x].pieces = 0;
@@ -489,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           if (k0 + C::BN > w.s.len) {
 #pragma unroll
             for (int i = 0; i < C::BN; i += 32) {
-              const uint32_t bits = seen(a, w.s, token, k0 + i);
+              const uint32_t bits = attn::seen(a.tree, a.tree_words, w.s, token, k0 + i);
 #pragma unroll
               for (int q = 0; q < 32; ++q)
                 if (!((bits >> q) & 1u)) s[i + q] = -INFINITY;
@@ -613,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             if (dirty && real) {  // NaN and infinities of drafts, for the rows that see them
               const int d0 = max(w.p.kt0 * C::BN - w.s.len, 0), d1 = min(w.p.kt1 * C::BN - w.s.len, w.s.n);
               for (int dr = d0; dr < d1; ++dr) {
-                if (!(seen(a, w.s, token, w.s.len + dr) & 1u)) continue;
+                if (!(attn::seen(a.tree, a.tree_words, w.s, token, w.s.len + dr) & 1u)) continue;
                 const long long off = attn::slot_offset(a.c, w.b, w.s.len + dr, w.p.head);
                 if (off < 0) continue;
                 const T* v = static_cast<const T*>(a.c.v) + off + c0 + i;
@@ -648,8 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       fence_before_sync();  // O has been read before the next piece's first P is announced
       if (threadIdx.x == 0 && w.p.kt0 == 0 && !w.whole()) {
         Split s;
-        const int parts = (int)min((long long)gridDim.x, ctl.total);
-        s.pieces = attn::part_of(ctl.total, parts, w.p.unit_begin + w.p.tiles - 1) - blockIdx.x + 1;
+        s.pieces = attn::part_of(ctl.share.total, ctl.share.parts, w.p.unit_begin + w.p.tiles - 1) - blockIdx.x + 1;
         s.first = w.s.first, s.n = w.s.n, s.head = w.p.head, s.row0 = w.row0, s.rows = w.rows;
         a.splits[blockIdx.x] = s;
       }

@@ -1,10 +1,42 @@
-// The softmax weight each cached slot received: one warp per slot and KV
-// head, a loop over the rows that see it.
-#include "attn.cuh"
+// The softmax weight each cached slot received, on the tensor cores.
+//
+//   S^T = K . Q^T   (128 slots x up to 128 rows at a time, TMEM)
+//   acc_out[slot] = decay * acc[slot] + sum over rows of exp2(c S - lse)
+//
+// The slots are the M side: a thread owns one slot (a TMEM lane) and adds up
+// its row of S^T itself, so the sum over rows needs no exchange between threads
+// and has a fixed order.  K is read once, by TMA, in panels of 64 elements x 128
+// slots; Q (all rows of a sequence and KV head, up to 128 KB) stays in shared
+// memory for the whole run of tiles.
+//
+// What bounds it: K alone for a few rows (HBM); with R rows a tile of 128 slots
+// costs 128 R exponentials, which passes the time of its 32 KB (D = 128) at some
+// 100 rows, and the MMAs (128 R D products) run beside them.  Two warpgroups take
+// alternate tiles, each with two S buffers, so both the exponentials and the
+// MMAs always have a next chunk to go to.
+//
+// Work division: attn_plan.h, with units of all rows of a sequence and KV
+// head; tiles are independent, so a cut unit needs no joining.  More rows than
+// Q's room holds are taken in passes over the piece's tiles; each pass adds to
+// what the same thread wrote in the one before.
+#include "attn_tma.cuh"
+#include "attn_work.cuh"
+
+using namespace moe::tc;
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kThreads = 320;  // warps 0-3, 4-7: even and odd tiles; 8: TMA; 9: MMA
+constexpr int kWorkers = 256;
+constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kTile = 128;               // slots of a tile
+constexpr int kChunk = 128;              // rows of one MMA and S buffer
+constexpr int kPanel = kTile * 128;      // bytes of 64 elements of a tile
+constexpr int kSlots = 5;                // panels in the ring
+constexpr int kQBytes = 128 * 1024;
+constexpr int kMaxRows = kQBytes / 128;  // rows that Q's room holds at D <= 64
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr float kNaN = __builtin_nanf("");
 
 struct WeightArgs {
   const void* q;
@@ -16,6 +48,7 @@ struct WeightArgs {
   int tree_words;
   float scale;
   attn_cache c;
+  attn::Maps maps;
   const float* acc;
   float decay;
   float* acc_out;
@@ -23,51 +56,305 @@ struct WeightArgs {
   int32_t* st;
 };
 
+struct Control {
+  uint64_t full[kSlots], empty[kSlots];
+  uint64_t s_full[4], s_free[4];  // S buffers 0, 1 of warpgroup 0, then of 1
+  uint64_t q_full, qk_done, drain;
+  attn::Share share;
+  uint32_t tmem;
+  int abort;
+  alignas(16) float bias[kMaxRows];  // -lse in powers of two; -inf for rows that add nothing
+};
+constexpr size_t kOffRing = kQBytes, kOffCtrl = kOffRing + (size_t)kSlots * kPanel;
+constexpr size_t kSmem = 1024 + kOffCtrl + sizeof(Control);
+static_assert(kSmem <= 232448, "shared memory");
+
 template <class E>
-__global__ void __launch_bounds__(kWarps * 32) weights_kernel(const __grid_constant__ WeightArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_constant__ WeightArgs a) {
   using T = typename E::T;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, D = a.c.head_dim, d0 = lane * 8;
-  const int h = blockIdx.y, b = blockIdx.z;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* sQ = smem;
+  uint8_t* sRing = smem + kOffRing;
+  Control& ctl = *reinterpret_cast<Control*>(smem + kOffCtrl);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int D = a.c.head_dim, G = a.q_heads / a.c.kv_heads;
+  const int panels = (D + 63) / 64;
+  const int q_rows = (kMaxRows / panels) & ~31;  // rows of one pass
+  const bool paired = 2 * panels < kSlots;       // two tiles of K at once leave room for a next panel
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&ctl.full[i], 1);
+      mbar_init(&ctl.empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&ctl.s_full[i], 1);
+      mbar_init(&ctl.s_free[i], 128);
+    }
+    mbar_init(&ctl.q_full, kWorkers);
+    mbar_init(&ctl.qk_done, 1);
+    mbar_init(&ctl.drain, 1);
+    ctl.abort = 0;
+    mbar_fence_init();
+    attn::prefetch_map(&a.maps.k);
+  }
+  moe::pdl_wait();
+  moe::pdl_launch_dependents();
+  const attn::PlanDims dims{a.c.kv_heads, G, 0x7FFFFFFF, kTile};
   const long long most = (long long)a.c.max_pages * a.c.page_size;
-  const attn::Seq s = attn::sequence(a.cu, a.lens, b, a.tokens, most < a.slot_cap ? most : a.slot_cap);
-  const int G = a.q_heads / a.c.kv_heads;
-  const long long base = ((long long)b * a.c.kv_heads + h) * a.slot_cap;
-  if (!s.ok) {
-    if (threadIdx.x == 0) moe::status_or(a.st, ATTN_DEV_BAD_LENGTH);
-    for (long long j = blockIdx.x * kWarps * 32 + threadIdx.x; j < a.slot_cap; j += (long long)gridDim.x * kWarps * 32)
-      a.acc_out[base + j] = __uint_as_float(0x7FC00000u);
+  if (!attn::take_share<kThreads>(a.cu, a.lens, a.c.batch, a.tokens, most < a.slot_cap ? most : a.slot_cap, dims,
+                                  ctl.share)) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) moe::status_or(a.st, ATTN_DEV_BAD_LENGTH);
+    const long long n = (long long)a.c.batch * a.c.kv_heads * a.slot_cap;
+    for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kThreads)
+      a.acc_out[i] = kNaN;
     return;
   }
-  for (int j = blockIdx.x * kWarps + warp; j < s.len + s.n; j += gridDim.x * kWarps) {
-    float sum = j < s.len ? a.decay * a.acc[base + j] : 0.f;
-    const long long off = attn::slot_offset(a.c, b, j, h);
-    float k[8] = {};
-    if (off < 0) {
-      sum = __uint_as_float(0x7FC00000u);
-      moe::status_or(a.st, ATTN_DEV_BAD_PAGE);
-    } else if (d0 < D) {
-      attn::unpack8<E>(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.c.k) + off + d0), k);
+  // sequences with nothing in flight only decay
+  for (int b = warp; b < a.c.batch; b += kThreads / 32) {
+    const attn::Seq s = attn::sequence(a.cu, a.lens, b, a.tokens, attn::kMaxSlots);
+    if (s.n > 0) continue;
+    for (int h = 0; h < a.c.kv_heads; ++h) {
+      const long long base = ((long long)b * a.c.kv_heads + h) * a.slot_cap;
+      for (long long j = (long long)blockIdx.x * 32 + lane; j < s.len; j += (long long)gridDim.x * 32)
+        a.acc_out[base + j] = a.decay * a.acc[base + j];
     }
-    for (int i = 0; i < s.n; ++i) {
-      const int t = s.first + i;
-      if (j >= s.len) {
-        const uint32_t w = a.tree ? attn::tree_bits(a.tree + (long long)t * a.tree_words, a.tree_words, j - s.len) : attn::chain_bits(i, j - s.len);
-        if (!(w & 1u)) continue;
-      }
-      for (int g = 0; g < G; ++g) {
-        const int hq = h * G + g;
-        float q[8] = {};
-        if (d0 < D) attn::unpack8<E>(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + t * a.q_stride + (long long)hq * D + d0), q);
-        float x = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x = fmaf(q[e], k[e], x);
-        x = moe::warp_sum(x);
-        const float lse = a.lse[(long long)t * a.q_heads + hq];
-        if (lse != -INFINITY) sum += expf(x * a.scale - lse);
-      }
-    }
-    if (lane == 0) a.acc_out[base + j] = sum;
   }
+  if (ctl.share.t0 >= ctl.share.t1) return;
+  if (warp == kMmaWarp) tmem_alloc(&ctl.tmem, 512);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = ctl.tmem;
+  volatile int* abort_flag = &ctl.abort;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (mbar_test(bar, parity)) return true;
+    const uint64_t deadline = globaltimer() + kWaitNs;
+    while (!mbar_test(bar, parity)) {
+      if (*abort_flag) return false;
+      if (globaltimer() > deadline) {
+        moe::status_or(a.st, MOE_DEV_TIMEOUT);
+        *abort_flag = 1;
+        return false;
+      }
+    }
+    return true;
+  };
+  auto passes = [&](const attn::Walk& w) { return (w.rows + q_rows - 1) / q_rows; };
+
+  if (warp == kTmaWarp) {
+    // ------------------------------------------------------------- TMA
+    attn::Walk w(a.cu, a.lens, a.tokens, dims, ctl.share);
+    int pos = 0;
+    bool alive = true;
+    const int box_rows = a.maps.box_rows, boxes = kTile / box_rows;  // at most 16
+    while (alive && w.next()) {
+      const int end = w.s.len + w.s.n;
+      const int32_t* table = a.c.page_table + (size_t)w.b * a.c.max_pages;
+      const int n_pass = passes(w);
+      for (int pass = 0; pass < n_pass && alive; ++pass) {
+        for (int j = w.p.kt0; j < w.p.kt1 && alive; ++j) {
+          const int slot0 = j * kTile, start = slot0 + lane * box_rows;
+          const int issued = min(boxes, (end - slot0 + box_rows - 1) / box_rows);
+          int page = 0, row = 0;
+          if (lane < issued) {
+            const int pi = start / a.c.page_size;
+            page = __ldg(table + pi);
+            row = start - pi * a.c.page_size;
+            if ((unsigned)page >= (unsigned)a.c.pages) {
+              page = a.c.pages;  // past the last: zeros; the slots' own threads see the page number too
+              moe::status_or(a.st, ATTN_DEV_BAD_PAGE);
+            }
+          }
+          for (int p = 0; p < panels; ++p, ++pos) {
+            const int slot = pos % kSlots;
+            alive = alive && wait(&ctl.empty[slot], ((pos / kSlots) & 1) ^ 1);
+            alive = __all_sync(0xffffffffu, alive);
+            if (!alive) break;
+            if (lane == 0) mbar_arrive_expect_tx(&ctl.full[slot], (uint32_t)(issued * box_rows * 128));
+            __syncwarp();
+            if (lane < issued)
+              attn::load_box(&a.maps.k, smem_u32(sRing + (size_t)slot * kPanel) + (uint32_t)(lane * box_rows * 128),
+                             &ctl.full[slot], p * 64, row, w.p.head, page, a.maps.head_inner);
+          }
+        }
+      }
+    }
+    if (lane == 0)  // every copy has landed before the CTA's shared memory goes away
+      for (int i = max(0, pos - kSlots); i < pos; ++i)
+        mbar_wait(&ctl.full[i % kSlots], (i / kSlots) & 1, globaltimer() + kWaitNs);
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------- MMA
+    if (lane == 0) {
+      attn::Walk w(a.cu, a.lens, a.tokens, dims, ctl.share);
+      int pos = 0, loads = 0, used[2] = {0, 0};
+      bool alive = true;
+      const int k_steps = (D + 15) / 16;
+      while (alive && w.next()) {
+        const int tiles = w.p.kt1 - w.p.kt0, n_pass = passes(w);
+        for (int pass = 0; pass < n_pass && alive; ++pass) {
+          const int rows = min(q_rows, w.rows - pass * q_rows), chunks = (rows + kChunk - 1) / kChunk;
+          alive = wait(&ctl.q_full, loads++ & 1);
+          fence_after_sync();
+          auto product = [&](int tile, int g) {
+            const int x = tile & 1, buf = 2 * x + (used[x] & 1);
+            if (!wait(&ctl.s_free[buf], ((used[x] >> 1) & 1) ^ 1)) return false;
+            ++used[x];
+            const int n = min(kChunk, ((rows - g * kChunk) + 31) & ~31);
+            const uint32_t id = attn::idesc<E>(kTile, n, false);
+            const int ps = pos + tile * panels;
+            fence_after_sync();
+            for (int kk = 0; kk < k_steps; ++kk) {
+              const int p = kk >> 2, slot = (ps + p) % kSlots;
+              if (g == 0 && (kk & 3) == 0) {
+                if (!wait(&ctl.full[slot], ((ps + p) / kSlots) & 1)) return false;
+                fence_after_sync();
+              }
+              mma_bf16(tmem + buf * kChunk,
+                       sw128_kmajor_desc(smem_u32(sRing + (size_t)slot * kPanel) + (kk & 3) * 32),
+                       sw128_kmajor_desc(smem_u32(sQ) + p * q_rows * 128 + g * kChunk * 128 + (kk & 3) * 32), id, kk != 0);
+            }
+            mma_commit(&ctl.s_full[buf]);
+            if (g == chunks - 1) {
+              for (int p = 0; p < panels; ++p) mma_commit(&ctl.empty[(ps + p) % kSlots]);
+              if (tile == tiles - 1) mma_commit(&ctl.qk_done);
+            }
+            return true;
+          };
+          if (paired) {
+            for (int t = 0; t < tiles && alive; t += 2)
+              for (int g = 0; g < chunks && alive; ++g) {
+                alive = product(t, g);
+                if (t + 1 < tiles) alive = alive && product(t + 1, g);
+              }
+          } else {
+            for (int t = 0; t < tiles && alive; ++t)
+              for (int g = 0; g < chunks && alive; ++g) alive = product(t, g);
+          }
+          pos += tiles * panels;
+        }
+      }
+      mma_commit(&ctl.drain);
+      mbar_wait(&ctl.drain, 0, globaltimer() + kWaitNs);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------- sums
+    const int x = warp >> 2, wl = warp & 3;
+    const uint32_t lane_base = (uint32_t)(wl * 32) << 16;
+    const float c2 = fabsf(a.scale) * 1.4426950408889634f;
+    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;  // a negative scale turns q's signs instead
+    const float2 c22 = make_float2(c2, c2), ones = make_float2(1.f, 1.f);
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+    attn::Walk w(a.cu, a.lens, a.tokens, dims, ctl.share);
+    int loads = 0, used = 0;
+    bool alive = true;
+    while (w.next()) {
+      const int n_pass = passes(w);
+      const long long base = ((long long)w.b * a.c.kv_heads + w.p.head) * a.slot_cap;
+      for (int pass = 0; pass < n_pass; ++pass) {
+        const int r0 = pass * q_rows, rows = min(q_rows, w.rows - r0), chunks = (rows + kChunk - 1) / kChunk;
+        alive = alive && (loads == 0 || warp_wait(&ctl.qk_done, (loads - 1) & 1));
+        ++loads;
+        named_sync(1, kWorkers);  // both warpgroups are done with the biases
+        {
+          const int n_chunks = panels * 8, padded = (rows + 31) & ~31;
+          const T* q = static_cast<const T*>(a.q);
+          for (int i = threadIdx.x; i < padded * n_chunks; i += kWorkers) {
+            const int r = i / n_chunks, ch = i - r * n_chunks;
+            const int row = r0 + r, tok = row / G, g = row - tok * G;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (r < rows && ch * 8 < D)
+              v = *reinterpret_cast<const uint4*>(q + (long long)(w.s.first + tok) * a.q_stride + ((long long)w.p.head * G + g) * D + ch * 8);
+            v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+            *reinterpret_cast<uint4*>(sQ + attn::sw128_offset(r, ch, q_rows)) = v;
+          }
+          for (int r = threadIdx.x; r < padded; r += kWorkers) {
+            float bias = -INFINITY;
+            if (r < rows) {
+              const int row = r0 + r, tok = row / G, g = row - tok * G;
+              const float lse = a.lse[(long long)(w.s.first + tok) * a.q_heads + w.p.head * G + g];
+              bias = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
+            }
+            ctl.bias[r] = bias;
+          }
+          fence_proxy_async();
+          named_sync(1, kWorkers);
+          mbar_arrive(&ctl.q_full);
+        }
+        for (int j = w.p.kt0 + x; j < w.p.kt1; j += 2) {
+          const int k0 = j * kTile + wl * 32, slot = k0 + lane;
+          const bool mine = slot < w.s.len + w.s.n;
+          float before = 0.f;
+          bool bad = false;
+          if (mine) {
+            const int page = __ldg(a.c.page_table + (size_t)w.b * a.c.max_pages + slot / a.c.page_size);
+            bad = (unsigned)page >= (unsigned)a.c.pages;
+            if (pass > 0) before = a.acc_out[base + slot];
+            else if (slot < w.s.len) before = a.decay * a.acc[base + slot];
+          }
+          const bool edge = k0 + 32 > w.s.len;  // some of the warp's slots are drafts or past the end
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          for (int g = 0; g < chunks && alive; ++g) {
+            const int buf = 2 * x + (used & 1);
+            alive = warp_wait(&ctl.s_full[buf], (used >> 1) & 1);
+            if (!alive) break;
+            ++used;
+            fence_after_sync();
+            const int n = min(kChunk, ((rows - g * kChunk) + 31) & ~31);
+            for (int i = 0; i < n; i += 32) {
+              float s[32];
+              attn::tmem_ld32(tmem + lane_base + buf * kChunk + i, s);
+              const float4* bias = reinterpret_cast<const float4*>(ctl.bias + g * kChunk + i);
+              tmem_ld_wait();
+              if (!edge) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                  const float4 bb = bias[e >> 2];
+                  float2 u = moe::ffma2(make_float2(s[e], s[e + 1]), c22, make_float2(bb.x, bb.y));
+                  float2 v = moe::ffma2(make_float2(s[e + 2], s[e + 3]), c22, make_float2(bb.z, bb.w));
+                  u.x = attn::exp2_fast(u.x), u.y = attn::exp2_fast(u.y);
+                  v.x = attn::exp2_fast(v.x), v.y = attn::exp2_fast(v.y);
+                  sum[0] = moe::ffma2(u, ones, sum[0]);
+                  sum[1] = moe::ffma2(v, ones, sum[1]);
+                }
+              } else {
+                // lane e looks up what row e sees of the warp's 32 slots
+                const int row = r0 + g * kChunk + i + lane;
+                const uint32_t bits =
+                    row < r0 + rows ? attn::seen(a.tree, a.tree_words, w.s, row / G, k0) : 0u;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  const uint32_t of_row = __shfl_sync(0xffffffffu, bits, e);
+                  const float p = attn::exp2_fast(fmaf(s[e], c2, ctl.bias[g * kChunk + i + e]));
+                  if ((of_row >> lane) & 1u) (e & 1 ? sum[0].y : sum[0].x) += p;
+                }
+              }
+            }
+            fence_before_sync();
+            mbar_arrive(&ctl.s_free[buf]);
+          }
+          if (mine) {
+            const float total = before + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
+            a.acc_out[base + slot] = bad || !alive ? kNaN : total;
+          }
+        }
+      }
+    }
+  }
+  fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+template <class E>
+int launch(WeightArgs& a, int sms, cudaStream_t st) {
+  static moe::SmemGrant grant;
+  if (const int rc = attn::make_maps(a.c, kTile, a.maps)) return rc;
+  if (!moe::grant_smem(weights_kernel<E>, kSmem, grant)) return MOE_ERR_CUDA;
+  return moe::launch_pdl(weights_kernel<E>, dim3(sms), dim3(kThreads), kSmem, st, a);
 }
 
 }  // namespace
@@ -79,14 +366,13 @@ extern "C" int attn_cache_weights(const void* q, long long q_stride, const float
   WeightArgs a;
   if (const int rc = attn::check_cache(cache, a.c)) return rc;
   if (const int rc = attn::check_queries(a.c, q, q_stride, cu, lens, tokens, q_heads, tree, tree_words)) return rc;
-  if ((!lse && tokens > 0) || !acc || !acc_out || slot_cap <= 0) return MOE_ERR_INVALID_ARG;
+  if ((!lse && tokens > 0) || !acc || !acc_out || slot_cap <= 0 || !(fabs(scale) >= 1e-30 && fabs(scale) <= 1e30))
+    return MOE_ERR_INVALID_ARG;
+  const int sms = moe::device_info().sms;
+  if (sms <= 0) return MOE_ERR_CUDA;
   a.q = q, a.q_stride = q_stride, a.lse = lse, a.cu = cu, a.lens = lens, a.tokens = tokens, a.q_heads = q_heads;
   a.tree = tree, a.tree_words = tree_words, a.scale = (float)scale, a.acc = acc, a.decay = (float)decay;
   a.acc_out = acc_out, a.slot_cap = slot_cap, a.st = dev_status;
   const cudaStream_t st = (cudaStream_t)stream;
-  if (a.c.batch > 65535) return MOE_ERR_UNSUPPORTED;
-  const dim3 grid(64, a.c.kv_heads, a.c.batch);
-  if (a.c.dtype == ATTN_BF16) weights_kernel<attn::Brain><<<grid, kWarps * 32, 0, st>>>(a);
-  else weights_kernel<attn::Half><<<grid, kWarps * 32, 0, st>>>(a);
-  return moe::launch_status();
+  return a.c.dtype == ATTN_BF16 ? launch<attn::Brain>(a, sms, st) : launch<attn::Half>(a, sms, st);
 }
