@@ -15,7 +15,7 @@ import ctypes
 import torch
 
 from . import moe as _moe
-from .moe import DEV_TIMEOUT, MoeError, _check, _ptr, _stream  # noqa: F401
+from .moe import DEV_TIMEOUT, MoeError, _check  # noqa: F401
 
 BF16 = 0
 FP16 = 1
@@ -82,7 +82,8 @@ class AttnCache:
         pages, heads, size, dim = k.shape
         sp, sh, sr, _ = k.stride()
         self.batch, self.kv_heads, self.head_dim = page_table.shape[0], heads, dim
-        self.dtype, self.device = k.dtype, k.device
+        self.dtype, self.device, self.index = k.dtype, k.device, k.get_device()
+        self.lens_shape, self.cu_shape = (self.batch,), (self.batch + 1,)
         self.struct = _CacheStruct(k.data_ptr(), v.data_ptr(), sp, sh, sr, page_table.data_ptr(), page_table.shape[0],
                                    page_table.shape[1], pages, size, heads, dim, _DTYPES[k.dtype])
         self.ref = ctypes.byref(self.struct)
@@ -106,29 +107,41 @@ def attn_cache(k, v, page_table) -> AttnCache:
     return AttnCache(k, v, page_table)
 
 
+# The checks below run on every call of a decode step, so each is a handful of
+# attribute reads; the words for a refusal are only put together when there is
+# one.
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _on(stream, cache):
+    return _raw_stream(cache.index) if stream is None else stream.cuda_stream
+
+
 def _rows(t, name, heads, cache):
-    """A [tokens, heads, D] tensor whose heads and elements are contiguous."""
-    if not isinstance(t, torch.Tensor) or t.dtype != cache.dtype or t.device != cache.device:
-        raise MoeError(f"{name} must be {cache.dtype} on {cache.device}, as the cache")
-    D = cache.head_dim
-    if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
-        raise MoeError(f"{name} must be [tokens, {heads or 'heads'}, {D}], got {tuple(t.shape)}")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
-        raise MoeError(f"{name}: heads and elements must be contiguous")
-    # the stride of one token is of no account; a packed one satisfies the checks
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * D
+    """Token stride of a [tokens, heads, D] tensor whose heads and elements are
+    contiguous (heads None: any number)."""
+    try:
+        T, h, D = t.shape
+        st, sh, sd = t.stride()
+        if (t.dtype is cache.dtype and t.get_device() == cache.index and D == cache.head_dim
+                and (heads is None or h == heads) and sd == 1 and (h == 1 or sh == D)):
+            # the stride of one token is of no account; a packed one satisfies the checks
+            return st if T > 1 else h * D
+    except (AttributeError, TypeError, ValueError):
+        pass
+    raise MoeError(f"{name} must be a [tokens, {heads or 'heads'}, {cache.head_dim}] tensor of {cache.dtype} on "
+                   f"{cache.device}, heads and elements contiguous")
 
 
 def _array(t, name, shape, dtype, cache):
-    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != cache.device or t.shape != shape
-            or not t.is_contiguous()):
-        raise MoeError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {cache.device}")
-    return t
-
-
-def _sequences(cu, lens, cache):
-    _array(cu, "cu", (cache.batch + 1,), torch.int32, cache)
-    _array(lens, "lens", (cache.batch,), torch.int32, cache)
+    """Address of a contiguous tensor of just this shape and type."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == cache.index and t.is_contiguous():
+            return t.data_ptr()
+    except (AttributeError, TypeError):
+        pass
+    raise MoeError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {cache.device}")
 
 
 def _tree(tree, tokens, cache):
@@ -138,14 +151,12 @@ def _tree(tree, tokens, cache):
         return None, 0
     if tree.dim() != 2:
         raise MoeError("tree must be [tokens, words]")
-    _array(tree, "tree", (tokens, tree.shape[1]), torch.int64, cache)
-    return tree.data_ptr(), tree.shape[1]
+    words = tree.shape[1]
+    return _array(tree, "tree", (tokens, words), torch.int64, cache), words
 
 
 def _status(dev_status, cache):
-    if dev_status is None:
-        return None
-    return _array(dev_status, "dev_status", (1,), torch.int32, cache).data_ptr()
+    return None if dev_status is None else _array(dev_status, "dev_status", (1,), torch.int32, cache)
 
 
 def _new(stream, make, *args, **kwargs):
@@ -167,30 +178,29 @@ def attn_qk_norm_rope(q, k, v, pos, cu, lens, cache: AttnCache, inv_freq, q_weig
     """Head norm and rotation of q and k, append of k and v.  inv_freq [rot /
     2] FP64: radians per position.  Returns q_out [tokens, q_heads, D]."""
     sq, sk, sv = _rows(q, "q", None, cache), _rows(k, "k", cache.kv_heads, cache), _rows(v, "v", cache.kv_heads, cache)
-    T, hq = q.shape[0], q.shape[1]
+    T, hq, D = q.shape
     if k.shape[0] != T or v.shape[0] != T:
         raise MoeError("q, k and v must hold the same tokens")
-    _array(pos, "pos", (T,), torch.int32, cache)
-    _sequences(cu, lens, cache)
-    _array(inv_freq, "inv_freq", (inv_freq.numel(),), torch.float64, cache)
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _array(w, name, (cache.head_dim,), cache.dtype, cache)
-    if (q_weight is None) != (k_weight is None):
-        raise MoeError("give both of q_weight and k_weight, or neither")
-    cap = 0
+    half = inv_freq.numel()
+    if q_weight is None and k_weight is None:
+        wq = wk = None
+    else:
+        wq = _array(q_weight, "q_weight", (D,), cache.dtype, cache)
+        wk = _array(k_weight, "k_weight", (D,), cache.dtype, cache)
+    at, cap = None, 0
     if slot_pos is not None:
         cap = slot_pos.shape[-1]
-        _array(slot_pos, "slot_pos", (cache.batch, cache.kv_heads, cap), torch.int32, cache)
+        at = _array(slot_pos, "slot_pos", (cache.batch, cache.kv_heads, cap), torch.int32, cache)
     if q_out is None:
-        q_out = _new(stream, torch.empty, (T, hq, cache.head_dim), dtype=q.dtype, device=q.device)
-    else:
-        _array(q_out, "q_out", (T, hq, cache.head_dim), cache.dtype, cache)
-    _check(load().attn_qk_norm_rope(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), sq, sk, sv, pos.data_ptr(), cu.data_ptr(), lens.data_ptr(), T, hq,
-        _ptr(q_weight), _ptr(k_weight), eps, inv_freq.data_ptr(), 2 * inv_freq.numel(), int(interleaved), magnitude,
-        q_out.data_ptr(), _ptr(slot_pos), cap, cache.ref, _status(dev_status, cache), _stream(stream)),
-        "attn_qk_norm_rope")
+        q_out = _new(stream, torch.empty, (T, hq, D), dtype=q.dtype, device=cache.device)
+    rc = load().attn_qk_norm_rope(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), sq, sk, sv, _array(pos, "pos", (T,), torch.int32, cache),
+        _array(cu, "cu", cache.cu_shape, torch.int32, cache), _array(lens, "lens", cache.lens_shape, torch.int32, cache),
+        T, hq, wq, wk, eps, _array(inv_freq, "inv_freq", (half,), torch.float64, cache), 2 * half, interleaved,
+        magnitude, _array(q_out, "q_out", (T, hq, D), cache.dtype, cache), at, cap, cache.ref,
+        _status(dev_status, cache), _on(stream, cache))
+    if rc:
+        _check(rc, "attn_qk_norm_rope")
     return q_out
 
 
@@ -208,25 +218,24 @@ def attn_tree_decode(q, cu, lens, cache: AttnCache, tree=None, scale: float | No
     """Attention of the tokens in flight over the cache; tree = None: a chain.
     Returns (out [tokens, q_heads, D], lse [tokens, q_heads])."""
     sq = _rows(q, "q", None, cache)
-    T, hq = q.shape[0], q.shape[1]
-    _sequences(cu, lens, cache)
+    T, hq, D = q.shape
     words, count = _tree(tree, T, cache)
     if out is None:
-        out = _new(stream, torch.empty, (T, hq, cache.head_dim), dtype=q.dtype, device=q.device)
-    else:
-        _array(out, "out", (T, hq, cache.head_dim), cache.dtype, cache)
+        out = _new(stream, torch.empty, (T, hq, D), dtype=q.dtype, device=cache.device)
     if lse is None:
-        lse = _new(stream, torch.empty, (T, hq), dtype=torch.float32, device=q.device)
-    else:
-        _array(lse, "lse", (T, hq), torch.float32, cache)
+        lse = _new(stream, torch.empty, (T, hq), dtype=torch.float32, device=cache.device)
     if workspace is None:
         workspace = _new(stream, attn_tree_decode_workspace, cache)
-    else:
-        _moe._cuda(workspace, "workspace", torch.uint8)
-    _check(load().attn_tree_decode(
-        q.data_ptr(), sq, cu.data_ptr(), lens.data_ptr(), T, hq, words, count,
-        cache.head_dim ** -0.5 if scale is None else scale, cache.ref, out.data_ptr(), lse.data_ptr(),
-        workspace.data_ptr(), workspace.numel(), _status(dev_status, cache), _stream(stream)), "attn_tree_decode")
+    size = workspace.numel()
+    rc = load().attn_tree_decode(
+        q.data_ptr(), sq, _array(cu, "cu", cache.cu_shape, torch.int32, cache),
+        _array(lens, "lens", cache.lens_shape, torch.int32, cache), T, hq, words, count,
+        D ** -0.5 if scale is None else scale, cache.ref, _array(out, "out", (T, hq, D), cache.dtype, cache),
+        _array(lse, "lse", (T, hq), torch.float32, cache),
+        _array(workspace, "workspace", (size,), torch.uint8, cache), size, _status(dev_status, cache),
+        _on(stream, cache))
+    if rc:
+        _check(rc, "attn_tree_decode")
     return out, lse
 
 
@@ -236,20 +245,19 @@ def attn_cache_weights(q, lse, cu, lens, cache: AttnCache, acc, tree=None, scale
     [batch, kv_heads, slot_cap]; acc_out may be acc; entries past a sequence's
     end are not written (a new acc_out starts as zeros)."""
     sq = _rows(q, "q", None, cache)
-    T, hq = q.shape[0], q.shape[1]
-    _sequences(cu, lens, cache)
-    _array(lse, "lse", (T, hq), torch.float32, cache)
+    T, hq, D = q.shape
     words, count = _tree(tree, T, cache)
     shape = (cache.batch, cache.kv_heads, acc.shape[-1])
-    _array(acc, "acc", shape, torch.float32, cache)
     if acc_out is None:
-        acc_out = _new(stream, torch.zeros, shape, dtype=torch.float32, device=q.device)
-    else:
-        _array(acc_out, "acc_out", shape, torch.float32, cache)
-    _check(load().attn_cache_weights(
-        q.data_ptr(), sq, lse.data_ptr(), cu.data_ptr(), lens.data_ptr(), T, hq, words, count,
-        cache.head_dim ** -0.5 if scale is None else scale, cache.ref, acc.data_ptr(), decay, acc_out.data_ptr(),
-        shape[2], _status(dev_status, cache), _stream(stream)), "attn_cache_weights")
+        acc_out = _new(stream, torch.zeros, shape, dtype=torch.float32, device=cache.device)
+    rc = load().attn_cache_weights(
+        q.data_ptr(), sq, _array(lse, "lse", (T, hq), torch.float32, cache),
+        _array(cu, "cu", cache.cu_shape, torch.int32, cache), _array(lens, "lens", cache.lens_shape, torch.int32, cache),
+        T, hq, words, count, D ** -0.5 if scale is None else scale, cache.ref,
+        _array(acc, "acc", shape, torch.float32, cache), decay, _array(acc_out, "acc_out", shape, torch.float32, cache),
+        shape[2], _status(dev_status, cache), _on(stream, cache))
+    if rc:
+        _check(rc, "attn_cache_weights")
     return acc_out
 
 
@@ -267,28 +275,23 @@ def attn_cache_evict(cache: AttnCache, acc, slot_pos, lens, next_pos, budget: in
     weight and moves their rows below the budget, in place.  Returns
     (lens_out, acc_out, pos_out)."""
     shape = (cache.batch, cache.kv_heads, acc.shape[-1])
-    _array(acc, "acc", shape, torch.float32, cache)
-    _array(slot_pos, "slot_pos", shape, torch.int32, cache)
-    _array(lens, "lens", (cache.batch,), torch.int32, cache)
-    _array(next_pos, "next_pos", (cache.batch,), torch.int32, cache)
     if acc_out is None:
-        acc_out = _new(stream, torch.zeros_like, acc)
-    else:
-        _array(acc_out, "acc_out", shape, torch.float32, cache)
+        acc_out = _new(stream, torch.zeros, shape, dtype=torch.float32, device=cache.device)
     if pos_out is None:
-        pos_out = _new(stream, torch.zeros_like, slot_pos)
-    else:
-        _array(pos_out, "pos_out", shape, torch.int32, cache)
+        pos_out = _new(stream, torch.zeros, shape, dtype=torch.int32, device=cache.device)
     if lens_out is None:
-        lens_out = _new(stream, torch.empty_like, lens)
-    else:
-        _array(lens_out, "lens_out", (cache.batch,), torch.int32, cache)
+        lens_out = _new(stream, torch.empty, cache.lens_shape, dtype=torch.int32, device=cache.device)
     if workspace is None:
         workspace = _new(stream, attn_cache_evict_workspace, cache, budget)
-    else:
-        _moe._cuda(workspace, "workspace", torch.uint8)
-    _check(load().attn_cache_evict(
-        cache.ref, acc.data_ptr(), slot_pos.data_ptr(), shape[2], lens.data_ptr(), next_pos.data_ptr(), budget, sinks,
-        recent, acc_out.data_ptr(), pos_out.data_ptr(), lens_out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-        _status(dev_status, cache), _stream(stream)), "attn_cache_evict")
+    size = workspace.numel()
+    rc = load().attn_cache_evict(
+        cache.ref, _array(acc, "acc", shape, torch.float32, cache), _array(slot_pos, "slot_pos", shape, torch.int32, cache),
+        shape[2], _array(lens, "lens", cache.lens_shape, torch.int32, cache),
+        _array(next_pos, "next_pos", cache.lens_shape, torch.int32, cache), budget, sinks, recent,
+        _array(acc_out, "acc_out", shape, torch.float32, cache), _array(pos_out, "pos_out", shape, torch.int32, cache),
+        _array(lens_out, "lens_out", cache.lens_shape, torch.int32, cache),
+        _array(workspace, "workspace", (size,), torch.uint8, cache), size, _status(dev_status, cache),
+        _on(stream, cache))
+    if rc:
+        _check(rc, "attn_cache_evict")
     return lens_out, acc_out, pos_out

@@ -17,25 +17,33 @@
 
 namespace attn {
 
+// a / b of non-negative numbers; the 32-bit division is several times cheaper
+// and nearly always enough.
+ATTN_HD long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (long long)((unsigned)a / (unsigned)b);
+  return a / b;
+}
+
 struct PlanDims {
   int kv_heads, group;      // query heads of a KV head
   int unit_rows, tile;      // rows of a unit, keys of a tile
 };
 
 ATTN_HD int row_groups(const PlanDims& d, int n) {
-  return (int)(((long long)n * d.group + d.unit_rows - 1) / d.unit_rows);
+  return (int)quotient((long long)n * d.group + d.unit_rows - 1, d.unit_rows);
 }
-ATTN_HD int key_tiles(const PlanDims& d, int len, int n) { return (int)(((long long)len + n + d.tile - 1) / d.tile); }
+ATTN_HD int key_tiles(const PlanDims& d, int len, int n) { return (int)quotient((long long)len + n + d.tile - 1, d.tile); }
 // Tiles of all units of a sequence.
 ATTN_HD long long sequence_tiles(const PlanDims& d, int len, int n) {
   return n <= 0 ? 0 : (long long)d.kv_heads * row_groups(d, n) * key_tiles(d, len, n);
 }
 
-// First tile of part c, and the part that holds tile t.
-ATTN_HD long long part_begin(long long total, int parts, int c) { return (long long)((__int128)total * c / parts); }
-ATTN_HD int part_of(long long total, int parts, long long t) {
-  return (int)((((__int128)t + 1) * parts - 1) / total);
-}
+// A line longer than this is refused (the products below stay within 64 bits).
+constexpr long long kMaxTiles = 1ll << 47;
+
+// First tile of part c, and the part that holds tile t (at most 2^15 parts).
+ATTN_HD long long part_begin(long long total, int parts, int c) { return quotient(total * c, parts); }
+ATTN_HD int part_of(long long total, int parts, long long t) { return (int)quotient((t + 1) * parts - 1, total); }
 
 // One piece of a unit: key tiles [kt0, kt1) of its `tiles`.
 struct Piece {
@@ -49,7 +57,7 @@ struct Piece {
 ATTN_HD Piece piece_at(const PlanDims& d, int len, int n, long long base, long long t, long long end) {
   Piece p;
   p.tiles = key_tiles(d, len, n);
-  const long long u = (t - base) / p.tiles;
+  const long long u = quotient(t - base, p.tiles);
   p.unit_begin = base + u * p.tiles;
   p.kt0 = (int)(t - p.unit_begin);
   const long long left = end - p.unit_begin;

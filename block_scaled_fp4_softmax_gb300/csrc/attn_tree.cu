@@ -90,13 +90,13 @@ struct Cfg {
 
 struct Control {
   uint64_t full[10], empty[10];
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2], p_half[2], p_full[2], o_full[2];
   uint64_t q_full, qk_done, pv_done, drain;
   attn::Share share;
   uint32_t tmem;
   int abort;
   int bad_page[8];   // piece number, at index piece % 8, that met a bad page
-  int dirty[8];      // ... whose drafts' values hold NaN or infinity
+  int dirty[2][8];   // ... whose drafts' values hold NaN or infinity, by cleaning stream
   float2 ml[128];    // stream 1's m and l for the join
 };
 template <class C>
@@ -141,6 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&ctl.s_full[x], 1);
+      mbar_init(&ctl.p_half[x], 128);
       mbar_init(&ctl.p_full[x], 128);
       mbar_init(&ctl.o_full[x], 1);
     }
@@ -149,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     mbar_init(&ctl.pv_done, 1);
     mbar_init(&ctl.drain, 1);
     ctl.abort = 0;
-    for (int i = 0; i < 8; ++i) ctl.bad_page[i] = ctl.dirty[i] = -1;
+    for (int i = 0; i < 8; ++i) ctl.bad_page[i] = ctl.dirty[0][i] = ctl.dirty[1][i] = -1;
     mbar_fence_init();
     attn::prefetch_map(&a.maps.k);
     attn::prefetch_map(&a.maps.v);
@@ -193,102 +194,119 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     return true;
   };
 
-  if (warp == kTmaWarp) {
-    // ------------------------------------------------------------- TMA
-    // Slots are filled K, V, K, V, ... in key order; lane i issues box i of
-    // the tile's at most 32 (8-row boxes of two panels of 128 rows, or four of 64).
-    attn::Walk w(a.cu, a.lens, a.tokens, dims, ctl.share);
-    int pos = 0;  // slots filled so far
-    bool alive = true;
-    const int box_rows = a.maps.box_rows, boxes = C::BN / box_rows;
-    const int my_box = lane % boxes, my_panel = lane / boxes;
-    while (alive && w.next()) {
-      const int end = w.s.len + w.s.n;
-      const int32_t* table = a.c.page_table + (size_t)w.b * a.c.max_pages;
-      for (int j = w.p.kt0; j < w.p.kt1 && alive; ++j) {
-        const int slot0 = j * C::BN, start = slot0 + my_box * box_rows;
-        const int issued = min(boxes, (end - slot0 + box_rows - 1) / box_rows);
-        int page = 0, row = 0;
-        if (my_box < issued) {
-          const int pi = start / a.c.page_size;
-          page = __ldg(table + pi);
-          row = start - pi * a.c.page_size;
-          if ((unsigned)page >= (unsigned)a.c.pages) {
-            page = a.c.pages;  // past the last: the copy delivers zeros
-            ctl.bad_page[w.number & 7] = w.number;
-            moe::status_or(a.st, ATTN_DEV_BAD_PAGE);
+  if (warp >= 8) {
+    if (warp == kTmaWarp) {
+      // ------------------------------------------------------------- TMA
+      // Slots are filled K, V, K, V, ... in key order; lane i issues box i of
+      // the tile's at most 32 (8-row boxes of two panels of 128 rows, or four of 64).
+      attn::Walk w(a.cu, a.lens, a.tokens, dims, ctl.share);
+      int pos = 0;  // slots filled so far
+      bool alive = true;
+      const int box_rows = a.maps.box_rows, boxes = C::BN / box_rows;
+      const int my_box = lane % boxes, my_panel = lane / boxes;
+      while (alive && w.next()) {
+        const int end = w.s.len + w.s.n;
+        const int32_t* table = a.c.page_table + (size_t)w.b * a.c.max_pages;
+        for (int j = w.p.kt0; j < w.p.kt1 && alive; ++j) {
+          const int slot0 = j * C::BN, start = slot0 + my_box * box_rows;
+          const int issued = min(boxes, (end - slot0 + box_rows - 1) / box_rows);
+          int page = 0, row = 0;
+          if (my_box < issued) {
+            const int pi = start / a.c.page_size;
+            page = __ldg(table + pi);
+            row = start - pi * a.c.page_size;
+            if ((unsigned)page >= (unsigned)a.c.pages) {
+              page = a.c.pages;  // past the last: the copy delivers zeros
+              ctl.bad_page[w.number & 7] = w.number;
+              moe::status_or(a.st, ATTN_DEV_BAD_PAGE);
+            }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++pos) {
+            const int slot = pos % C::SLOTS;
+            alive = alive && wait(&ctl.empty[slot], ((pos / C::SLOTS) & 1) ^ 1);
+            alive = __all_sync(0xffffffffu, alive);
+            if (!alive) break;
+            if (lane == 0) mbar_arrive_expect_tx(&ctl.full[slot], (uint32_t)(issued * box_rows * 128 * panels));
+            __syncwarp();
+            const uint32_t dst = smem_u32(sRing + (size_t)slot * C::SLOT) + (uint32_t)(my_box * box_rows * 128);
+            if (my_box < issued)
+              for (int p = my_panel; p < panels; p += 32 / boxes)
+                attn::load_box(kv ? &a.maps.v : &a.maps.k, dst + p * C::PANEL, &ctl.full[slot], p * 64, row, w.p.head,
+                               page, a.maps.head_inner);
           }
         }
-        __syncwarp();
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++pos) {
-          const int slot = pos % C::SLOTS;
-          alive = alive && wait(&ctl.empty[slot], ((pos / C::SLOTS) & 1) ^ 1);
-          alive = __all_sync(0xffffffffu, alive);
-          if (!alive) break;
-          if (lane == 0) mbar_arrive_expect_tx(&ctl.full[slot], (uint32_t)(issued * box_rows * 128 * panels));
-          __syncwarp();
-          const uint32_t dst = smem_u32(sRing + (size_t)slot * C::SLOT) + (uint32_t)(my_box * box_rows * 128);
-          if (my_box < issued)
-            for (int p = my_panel; p < panels; p += 32 / boxes)
-              attn::load_box(kv ? &a.maps.v : &a.maps.k, dst + p * C::PANEL, &ctl.full[slot], p * 64, row, w.p.head,
-                             page, a.maps.head_inner);
+      }
+      // every copy has landed before the CTA's shared memory goes away
+      if (lane == 0)
+        for (int i = max(0, pos - C::SLOTS); i < pos; ++i) {
+          const uint64_t deadline = globaltimer() + kWaitNs;
+          mbar_wait(&ctl.full[i % C::SLOTS], (i / C::SLOTS) & 1, deadline);
         }
-      }
-    }
-    // every copy has landed before the CTA's shared memory goes away
-    if (lane == 0)
-      for (int i = max(0, pos - C::SLOTS); i < pos; ++i) {
-        const uint64_t deadline = globaltimer() + kWaitNs;
-        mbar_wait(&ctl.full[i % C::SLOTS], (i / C::SLOTS) & 1, deadline);
-      }
-    __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------- MMA
-    if (lane == 0) {
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      // ----------------------------------------------------------- MMA
+      // The warp walks and waits as one; its elected lane issues.
+      const bool leader = attn::elect_lane();
+      auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
       attn::Walk w(a.cu, a.lens, a.tokens, dims, ctl.share);
-      int pos = 0, pieces = 0, p_seen[2] = {0, 0};
+      int pos = 0, pieces = 0, p_seen0 = 0, p_seen1 = 0;
       bool alive = true;
       const int k_steps = (D + 15) / 16;
-      const uint32_t id_s = attn::idesc<E>(128, C::BN, false);
+      // a negative scale negates Q, the sums keep |scale|
+      const uint32_t id_s = attn::idesc<E>(128, C::BN, false) | (a.scale < 0.f ? 1u << 13 : 0u);
       const uint32_t id_o = attn::idesc<E>(128, (D + 15) & ~15, true);
+      const uint32_t q_addr = smem_u32(sQ), ring = smem_u32(sRing);
       while (alive && w.next()) {
         const bool both = C::STREAMS == 2 && w.rows > 128;  // two row tiles over the same keys
         const int tiles = w.p.kt1 - w.p.kt0, items = both ? 2 * tiles : tiles;
-        alive = wait(&ctl.q_full, pieces & 1);
+        alive = warp_wait(&ctl.q_full, pieces & 1);
         if (!alive) break;
         fence_after_sync();
         auto qk = [&](int it) {
           const int x = it & 1, ps = pos + 2 * (both ? it >> 1 : it), slot = ps % C::SLOTS;
           if (!both || x == 0) {
-            if (!wait(&ctl.full[slot], (ps / C::SLOTS) & 1)) return false;
+            if (!warp_wait(&ctl.full[slot], (ps / C::SLOTS) & 1)) return false;
             fence_after_sync();
           }
-          const uint32_t qa = smem_u32(sQ + (both && x ? C::QTILE : 0));
-          const uint32_t ka = smem_u32(sRing + (size_t)slot * C::SLOT);
-          for (int kk = 0; kk < k_steps; ++kk)
-            mma_bf16(tmem + C::S_COL + x * C::BN, sw128_kmajor_desc(qa + (kk >> 2) * 128 * 128 + (kk & 3) * 32),
-                     sw128_kmajor_desc(ka + (kk >> 2) * C::PANEL + (kk & 3) * 32), id_s, kk != 0);
-          mma_commit(&ctl.s_full[x]);
-          if (!both || x == 1) mma_commit(&ctl.empty[slot]);
-          if (it == items - 1) mma_commit(&ctl.qk_done);
+          if (leader) {
+            const uint32_t qa = q_addr + (both && x ? C::QTILE : 0), ka = ring + (uint32_t)slot * C::SLOT;
+            const uint32_t d = tmem + C::S_COL + x * C::BN;
+            for (int kk = 0; kk < k_steps; ++kk)
+              mma_bf16(d, sw128_kmajor_desc(qa + (kk >> 2) * 128 * 128 + (kk & 3) * 32),
+                       sw128_kmajor_desc(ka + (kk >> 2) * C::PANEL + (kk & 3) * 32), id_s, kk != 0);
+            mma_commit(&ctl.s_full[x]);
+            if (!both || x == 1) mma_commit(&ctl.empty[slot]);
+            if (it == items - 1) mma_commit(&ctl.qk_done);
+          }
+          __syncwarp();
           return true;
         };
         auto pv = [&](int it) {
           const int x = it & 1, ps = pos + 2 * (both ? it >> 1 : it) + 1, slot = ps % C::SLOTS;
           const int st = C::STREAMS == 2 ? x : 0;  // whose O
-          if (!wait(&ctl.p_full[x], p_seen[x]++ & 1)) return false;
-          if ((!both || x == 0) && !wait(&ctl.full[slot], (ps / C::SLOTS) & 1)) return false;
-          fence_after_sync();
-          const uint32_t va = smem_u32(sRing + (size_t)slot * C::SLOT);
+          const int seen = x ? p_seen1++ : p_seen0++;
+          if (!warp_wait(&ctl.p_half[x], seen & 1)) return false;
+          if ((!both || x == 0) && !warp_wait(&ctl.full[slot], (ps / C::SLOTS) & 1)) return false;
+          const uint32_t va = ring + (uint32_t)slot * C::SLOT;
           const bool first = C::STREAMS == 2 ? it < 2 : it == 0;
-#pragma unroll
-          for (int kk = 0; kk < C::BN / 16; ++kk)
-            attn::mma_ts(tmem + C::O_COL + st * DP, tmem + C::S_COL + x * C::BN + kk * 8,
-                         attn::sw128_mnmajor_desc(va + kk * 2048, C::PANEL), id_o, !(first && kk == 0));
-          if (!both || x == 1) mma_commit(&ctl.empty[slot]);
-          if (C::STREAMS == 1) mma_commit(&ctl.pv_done);
-          if (it >= items - C::STREAMS) mma_commit(&ctl.o_full[st]);
+          const uint32_t d = tmem + C::O_COL + st * DP, p = tmem + C::S_COL + x * C::BN;
+          for (int half = 0; half < 2; ++half) {
+            if (half == 1 && !warp_wait(&ctl.p_full[x], seen & 1)) return false;
+            fence_after_sync();
+            if (leader) {
+              for (int kk = half * (C::BN / 32); kk < (half + 1) * (C::BN / 32); ++kk)
+                attn::mma_ts(d, p + kk * 8, attn::sw128_mnmajor_desc(va + kk * 2048, C::PANEL), id_o, !(first && kk == 0));
+            }
+            __syncwarp();
+          }
+          if (leader) {
+            if (!both || x == 1) mma_commit(&ctl.empty[slot]);
+            if (C::STREAMS == 1) mma_commit(&ctl.pv_done);
+            if (it >= items - C::STREAMS) mma_commit(&ctl.o_full[st]);
+          }
+          __syncwarp();
           return true;
         };
         alive = qk(0);
@@ -300,265 +318,313 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         ++pieces;
       }
       // every MMA has completed before TMEM goes back
-      mma_commit(&ctl.drain);
-      mbar_wait(&ctl.drain, 0, globaltimer() + kWaitNs);
+      if (leader) {
+        mma_commit(&ctl.drain);
+        mbar_wait(&ctl.drain, 0, globaltimer() + kWaitNs);
+      }
+      __syncwarp();
     }
-    __syncwarp();
-  } else if (warp < 4 * C::STREAMS) {
-    // ------------------------------------------------------------- softmax
-    const int st = warp >> 2, wl = warp & 3;
-    const int r_tile = wl * 32 + lane;  // this thread's row of its 128
-    const uint32_t lane_base = (uint32_t)(wl * 32) << 16;
-    const uint32_t o_addr = tmem + lane_base + C::O_COL + st * DP;
-    const float c2 = fabsf(a.scale) * 1.4426950408889634f;
-    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;  // a negative scale turns q's signs instead
-    constexpr float kLift = Weight<E>::kLift, kLag = Weight<E>::kLag;
-    // the TMEM accesses below need whole warps: a warp gives up together
-    auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
-    attn::Walk w(a.cu, a.lens, a.tokens, dims, ctl.share);
-    int pos = 0, s_seen[2] = {0, 0}, o_seen = 0, pieces = 0, pv_seen = 0;
-    bool alive = true;
-    if (threadIdx.x == 0) a.splits[blockIdx.x].pieces = 0;
-    while (w.next()) {
-      const bool both = C::STREAMS == 2 && w.rows > 128;
-      const int tiles = w.p.kt1 - w.p.kt0, items = both ? 2 * tiles : tiles;
-      // ---- Q into shared memory: rows of 16-byte chunks, zeros past D
-      alive = alive && (pieces == 0 || warp_wait(&ctl.qk_done, (pieces - 1) & 1));
-      {
-        const int t0 = both ? 128 * st : 0, n_rows = min(128, w.rows - t0);
-        uint8_t* dst = sQ + (both ? st * C::QTILE : 0);
-        const int n_thr = both ? 128 : kWorkers, me = both ? threadIdx.x & 127 : threadIdx.x;
-        const int chunks = panels * 8;
-        const T* q = static_cast<const T*>(a.q);
-        for (int i = me; i < n_rows * chunks; i += n_thr) {
-          const int r = i / chunks, ch = i - r * chunks;
-          const int row = w.row0 + t0 + r, tok = row / G, g = row - tok * G;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (ch * 8 < D)
-            v = *reinterpret_cast<const uint4*>(q + (long long)(w.s.first + tok) * a.q_stride + ((long long)w.p.head * G + g) * D + ch * 8);
-          v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-          *reinterpret_cast<uint4*>(dst + attn::sw128_offset(r, ch, 128)) = v;
-        }
-        fence_proxy_async();
-        mbar_arrive(&ctl.q_full);
-      }
-      const int tile_rows = both ? w.rows - 128 * st : w.rows;    // of this warpgroup's row tile
-      const bool active = wl * 32 < tile_rows;                    // whether the warp has rows at all
-      const int row = w.row0 + (both ? 128 * st : 0) + r_tile;    // of the sequence and head
-      const int token = min(row / G, w.s.n - 1);
-      const bool real = row < w.row0 + w.rows;
-      float m = -INFINITY, l = 0.f;  // m in powers of two
-      int done = 0;
-      for (int it = (C::STREAMS == 2 ? st : 0); it < items && alive; it += C::STREAMS) {
-        const int x = it & 1, tile = both ? it >> 1 : it;
-        const int k0 = (w.p.kt0 + tile) * C::BN;
-        const uint32_t s_addr = tmem + lane_base + C::S_COL + x * C::BN;
-        // ---- clean V where the tile reaches past the committed slots
-        if (k0 + C::BN > w.s.len && (!both || st == 0)) {
-          const int ps = pos + 2 * tile + 1;
-          alive = warp_wait(&ctl.full[ps % C::SLOTS], (ps / C::SLOTS) & 1);
-          if (!alive) break;
-          uint8_t* v = sRing + (size_t)(ps % C::SLOTS) * C::SLOT;
-          const int lo = max(0, w.s.len - k0), hi = w.s.len + w.s.n - k0;
-          const int chunks = panels * 8;
-          for (int i = lo * chunks + (threadIdx.x & 127); i < C::BN * chunks; i += 128) {
-            const int r = i / chunks, ch = i - r * chunks;
-            uint4* at = reinterpret_cast<uint4*>(v + attn::sw128_offset(r, ch, C::BN));
-            if (r >= hi) {
-              *at = make_uint4(0u, 0u, 0u, 0u);
-            } else {
-              uint32_t e[4] = {at->x, at->y, at->z, at->w};
-              bool changed = false;
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const float2 f = E::up(e[q]);
-                if (!isfinite(f.x)) e[q] &= 0xFFFF0000u, changed = true;
-                if (!isfinite(f.y)) e[q] &= 0x0000FFFFu, changed = true;
-              }
-              if (changed) {
-                *at = make_uint4(e[0], e[1], e[2], e[3]);
-                ctl.dirty[w.number & 7] = w.number;
-              }
+  } else {
+    if (warp < 4 * C::STREAMS) {
+      // ----------------------------------------------------------- softmax
+      const int st = warp >> 2, wl = warp & 3;
+      const int r_tile = wl * 32 + lane;  // this thread's row of its 128
+      const uint32_t lane_base = (uint32_t)(wl * 32) << 16;
+      const uint32_t o_addr = tmem + lane_base + C::O_COL + st * DP;
+      const float c2 = fabsf(a.scale) * 1.4426950408889634f;
+      constexpr float kLift = Weight<E>::kLift, kLag = Weight<E>::kLag;
+      // the TMEM accesses below need whole warps: a warp gives up together
+      auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+      attn::Walk w(a.cu, a.lens, a.tokens, dims, ctl.share);
+      int pos = 0, s_seen[2] = {0, 0}, o_seen = 0, pieces = 0, pv_seen = 0;
+      bool alive = true;
+      if (threadIdx.x == 0) a.splits[blockIdx.x].pieces = 0;
+      while (w.next()) {
+        const bool both = C::STREAMS == 2 && w.rows > 128;
+        const int tiles = w.p.kt1 - w.p.kt0, items = both ? 2 * tiles : tiles;
+        const int tile_row0 = both ? 128 * st : 0;  // first row of this warpgroup's row tile
+        // ---- Q into shared memory, zeros past D
+        alive = alive && (pieces == 0 || warp_wait(&ctl.qk_done, (pieces - 1) & 1));
+        {
+          const int n_rows = min(128, w.rows - tile_row0);
+          const uint32_t dst = smem_u32(sQ) + (both ? st * C::QTILE : 0);
+          const int me = both ? threadIdx.x & 127 : threadIdx.x, step = (both ? 128 : kWorkers) / 8;
+          const int ch = me & 7;  // 8 lanes copy 128 contiguous bytes
+          const T* q = static_cast<const T*>(a.q) + (long long)w.s.first * a.q_stride + (long long)w.p.head * G * D + ch * 8;
+          for (int r = me >> 3; r < n_rows; r += step) {
+            const int row = w.row0 + tile_row0 + r, tok = row / G;
+            const T* src = q + tok * a.q_stride + (row - tok * G) * D;
+            for (int p = 0; p < panels; ++p) {
+              const bool inside = p * 64 + ch * 8 < D;
+              cp_async16(dst + attn::sw128_offset(r, p * 8 + ch, 128), inside ? src + p * 64 : src, inside ? 16u : 0u);
             }
           }
+          cp_async_commit();
+          cp_async_wait<0>();
           fence_proxy_async();
+          mbar_arrive(&ctl.q_full);
         }
-        alive = alive && warp_wait(&ctl.s_full[x], s_seen[x]++ & 1);
-        if (!alive) break;
-        fence_after_sync();
-        if (active) {
-          float s[C::BN];
+        const bool active = wl * 32 < w.rows - tile_row0;  // whether the warp has rows at all
+        const int row = w.row0 + tile_row0 + r_tile;       // of the sequence and head
+        const int token = min(row / G, w.s.n - 1);
+        const bool real = row < w.row0 + w.rows;
+        float m = -INFINITY, l = 0.f;  // m in powers of two
+        int done = 0;
+        for (int it = (C::STREAMS == 2 ? st : 0); it < items && alive; it += C::STREAMS) {
+          const int x = it & 1, tile = both ? it >> 1 : it;
+          const int k0 = (w.p.kt0 + tile) * C::BN;
+          const uint32_t s_addr = tmem + lane_base + C::S_COL + x * C::BN;
+          const bool edge = k0 + C::BN > w.s.len;
+          // ---- clean V where the tile reaches past the committed slots
+          if (edge && (!both || st == 0)) {
+            const int ps = pos + 2 * tile + 1;
+            alive = warp_wait(&ctl.full[ps % C::SLOTS], (ps / C::SLOTS) & 1);
+            if (!alive) break;
+            uint8_t* v = sRing + (size_t)(ps % C::SLOTS) * C::SLOT;
+            const int lo = max(0, w.s.len - k0), hi = w.s.len + w.s.n - k0;
+            const int chunks = panels * 8;
+            for (int i = lo * chunks + (threadIdx.x & 127); i < C::BN * chunks; i += 128) {
+              const int r = i / chunks, ch = i - r * chunks;
+              uint4* at = reinterpret_cast<uint4*>(v + attn::sw128_offset(r, ch, C::BN));
+              if (r >= hi) {
+                *at = make_uint4(0u, 0u, 0u, 0u);
+              } else {
+                uint32_t e[4] = {at->x, at->y, at->z, at->w};
+                bool changed = false;
 #pragma unroll
-          for (int i = 0; i < C::BN; i += 32) attn::tmem_ld32(s_addr + i, s + i);
-          tmem_ld_wait();
-          if (k0 + C::BN > w.s.len) {
-#pragma unroll
-            for (int i = 0; i < C::BN; i += 32) {
-              const uint32_t bits = attn::seen(a.tree, a.tree_words, w.s, token, k0 + i);
-#pragma unroll
-              for (int q = 0; q < 32; ++q)
-                if (!((bits >> q) & 1u)) s[i + q] = -INFINITY;
-            }
-          }
-          float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < C::BN; i += 8)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) t[q] = attn::max3(t[q], s[i + 2 * q], s[i + 2 * q + 1]);
-          const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * c2;
-          // the first tile takes its maximum; later ones move it only by more than kLag
-          const bool grow = real && top > (done ? m + kLag : m);
-          if (__any_sync(0xffffffffu, grow)) {
-            const float m1 = grow ? top : m;
-            if (done) {
-              if (C::STREAMS == 1) {  // O still takes the tile before: wait for that product
-                alive = warp_wait(&ctl.pv_done, (pv_seen + done - 1) & 1);
-                fence_after_sync();
-              }
-              const float f = m == -INFINITY ? 0.f : attn::exp2_fast(m - m1);
-              l *= f;
-              float o[32];
-              for (int i = 0; i < DP; i += 32) {
-                attn::tmem_ld32(o_addr + i, o);
-                tmem_ld_wait();
-#pragma unroll
-                for (int q = 0; q < 32; ++q) o[q] *= f;
-                attn::tmem_st32(o_addr + i, o);
-              }
-            }
-            m = m1;
-          }
-          const float bias = kLift - (m == -INFINITY ? 0.f : m);
-          const float2 c22 = make_float2(c2, c2), b22 = make_float2(bias, bias);
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          const float2 ones = make_float2(1.f, 1.f);
-#pragma unroll
-          for (int i = 0; i < C::BN; i += 32) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int q = 0; q < 32; q += 2) {
-              float2 e = moe::ffma2(make_float2(s[i + q], s[i + q + 1]), c22, b22);
-              e.x = attn::exp2_fast(e.x);
-              e.y = attn::exp2_fast(e.y);
-              sum[(q >> 1) & 1] = moe::ffma2(e, ones, sum[(q >> 1) & 1]);
-              pk[q >> 1] = E::down(e.x, e.y);
-            }
-            attn::tmem_st16(s_addr + i / 2, pk);
-          }
-          attn::tmem_st_wait();
-          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        }
-        ++done;
-        fence_before_sync();
-        mbar_arrive(&ctl.p_full[x]);
-      }
-      pv_seen += done;
-      if (l != l && m == -INFINITY) m = 0.f;  // only NaN scores: not to be mistaken for a row that saw nothing
-      // ---- the piece's result
-      const bool has = done > 0;
-      if (has && alive) {
-        alive = warp_wait(&ctl.o_full[st], o_seen & 1);
-        fence_after_sync();
-      }
-      o_seen += has;
-      named_sync(1, kWorkers);  // flags of this piece are final
-      const bool dirty = ctl.dirty[w.number & 7] == w.number;
-      const bool broken = !alive || ctl.bad_page[w.number & 7] == w.number;
-      float f0 = 1.f, f1 = 0.f;
-      const bool join = C::STREAMS == 2 && !both && tiles > 1;
-      float* exch = reinterpret_cast<float*>(sQ + C::QTILE);  // [DP / 2][128]: Q's second tile is unused here
-      if (join && st == 1) ctl.ml[r_tile] = make_float2(m, l);
-      const bool writer = (both || st == 0) && active;
-      const int hq = w.p.head * G + row % G;
-      const long long out_row = (long long)(w.s.first + row / G) * a.q_heads + hq;
-      const int side = w.p.kt0 == 0 ? 1 : 0;
-      const int slot_row = (both ? 128 * st : 0) + r_tile;
-      const size_t slot_id = (size_t)blockIdx.x * 2 + side;
-      float inv = 0.f;
-      constexpr int kHalf = C::STREAMS == 2 ? DP / 2 : DP;
-      for (int c0 = 0; c0 < DP; c0 += kHalf) {
-        if (join) {
-          if (st == 1 && active && alive) {
-            for (int i = 0; i < kHalf; i += 32) {
-              float o[32];
-              attn::tmem_ld32(o_addr + c0 + i, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int q = 0; q < 32; ++q) exch[(i + q) * 128 + r_tile] = o[q];
-            }
-          }
-          named_sync(1, kWorkers);
-        }
-        if (writer) {
-          if (c0 == 0) {
-            if (join) {
-              const float2 other = ctl.ml[r_tile];
-              const float top = fmaxf(m, other.x);
-              f0 = m == -INFINITY ? 0.f : attn::exp2_fast(m - top);
-              f1 = other.x == -INFINITY ? 0.f : attn::exp2_fast(other.x - top);
-              l = l * f0 + other.y * f1;
-              m = top;
-            }
-            if (broken) l = kNaN, m = 0.f;
-            inv = l == 0.f ? 0.f : 1.f / l;
-            if (real) {
-              if (!w.whole()) reinterpret_cast<float2*>(a.ml)[slot_id * C::ROWS + slot_row] = make_float2(m, l);
-              else if (a.lse) a.lse[out_row] = l == 0.f ? -INFINITY : (m - kLift) * 0.6931471805599453f + logf(l);
-            }
-          }
-          for (int i = 0; i < kHalf; i += 32) {
-            if (c0 + i >= D) break;
-            float o[32];
-            attn::tmem_ld32(o_addr + c0 + i, o);
-            tmem_ld_wait();
-            if (join) {
-#pragma unroll
-              for (int q = 0; q < 32; ++q) o[q] = o[q] * f0 + (f1 == 0.f ? 0.f : exch[(i + q) * 128 + r_tile] * f1);
-            }
-            if (dirty && real) {  // NaN and infinities of drafts, for the rows that see them
-              const int d0 = max(w.p.kt0 * C::BN - w.s.len, 0), d1 = min(w.p.kt1 * C::BN - w.s.len, w.s.n);
-              for (int dr = d0; dr < d1; ++dr) {
-                if (!(attn::seen(a.tree, a.tree_words, w.s, token, w.s.len + dr) & 1u)) continue;
-                const long long off = attn::slot_offset(a.c, w.b, w.s.len + dr, w.p.head);
-                if (off < 0) continue;
-                const T* v = static_cast<const T*>(a.c.v) + off + c0 + i;
-#pragma unroll
-                for (int q = 0; q < 32; ++q) {
-                  if (c0 + i + q >= D) break;
-                  const float e = (float)v[q];
-                  if (!isfinite(e)) o[q] += e;
+                for (int q = 0; q < 4; ++q) {
+                  const float2 f = E::up(e[q]);
+                  if (!isfinite(f.x)) e[q] &= 0xFFFF0000u, changed = true;
+                  if (!isfinite(f.y)) e[q] &= 0x0000FFFFu, changed = true;
+                }
+                if (changed) {
+                  *at = make_uint4(e[0], e[1], e[2], e[3]);
+                  ctl.dirty[st][w.number & 7] = w.number;
                 }
               }
             }
-            if (real && w.whole()) {
+            fence_proxy_async();
+          }
+          alive = alive && warp_wait(&ctl.s_full[x], s_seen[x]++ & 1);
+          if (!alive) break;
+          fence_after_sync();
+          if (active) {
+            // All but the last 32 columns stay in registers from the maximum to the
+            // weights; those are read again (a thread has 168 registers).  P takes
+            // columns of S that have been read.
+            constexpr int kHeld = C::BN - 32;
+            float s[kHeld], last[32];
 #pragma unroll
-              for (int q = 0; q < 32; q += 8) {
-                if (c0 + i + q >= D) break;
-                float y[8];
+            for (int i = 0; i < kHeld; i += 32) attn::tmem_ld32(s_addr + i, s + i);
+            attn::tmem_ld32(s_addr + kHeld, last);
+            uint32_t last_bits = 0xFFFFFFFFu;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = o[q + e] * inv;
-                *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + out_row * D + c0 + i + q) = attn::pack8<E>(y);
+            for (int i = 0; i < kHeld; i += 32) attn::tmem_ld_wait32(s + i);
+            attn::tmem_ld_wait32(last);
+            if (edge) {
+#pragma unroll
+              for (int i = 0; i < kHeld; i += 32) {
+                const uint32_t bits = attn::seen(a.tree, a.tree_words, w.s, token, k0 + i);
+#pragma unroll
+                for (int q = 0; q < 32; ++q) s[i + q] = (bits >> q) & 1u ? s[i + q] : -INFINITY;
               }
-            } else if (real) {
+              last_bits = attn::seen(a.tree, a.tree_words, w.s, token, k0 + kHeld);
 #pragma unroll
-              for (int q = 0; q < 32; q += 4)
-                if (c0 + i + q < D)
-                  a.o[(slot_id * (DP / 4) + (c0 + i + q) / 4) * C::ROWS + slot_row] = make_float4(o[q], o[q + 1], o[q + 2], o[q + 3]);
+              for (int q = 0; q < 32; ++q) last[q] = (last_bits >> q) & 1u ? last[q] : -INFINITY;
             }
-            __syncwarp();
+            float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < kHeld; i += 8)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) t[q] = attn::max3(t[q], s[i + 2 * q], s[i + 2 * q + 1]);
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) t[q] = attn::max3(t[q], last[i + 2 * q], last[i + 2 * q + 1]);
+            const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * c2;
+            // the first tile takes its maximum; later ones move it only by more than kLag
+            const bool grow = real && top > (done ? m + kLag : m);
+            if (__any_sync(0xffffffffu, grow)) {
+              const float m1 = grow ? top : m;
+              if (done) {
+                if (C::STREAMS == 1) {  // O still takes the tile before: wait for that product
+                  alive = warp_wait(&ctl.pv_done, (pv_seen + done - 1) & 1);
+                  fence_after_sync();
+                }
+                const float f = m == -INFINITY ? 0.f : attn::exp2_fast(m - m1);
+                l *= f;
+                float o[32];
+#pragma unroll 1
+                for (int i = 0; i < DP; i += 32) {
+                  attn::tmem_ld32(o_addr + i, o);
+                  attn::tmem_ld_wait32(o);
+#pragma unroll
+                  for (int q = 0; q < 32; ++q) o[q] *= f;
+                  attn::tmem_st32(o_addr + i, o);
+                }
+              }
+              m = m1;
+            }
+            const float bias = kLift - (m == -INFINITY ? 0.f : m);
+            const float2 c22 = make_float2(c2, c2), b22 = make_float2(bias, bias), ones = make_float2(1.f, 1.f);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            auto weights = [&](const float* u, int i) {  // 32 columns from i
+              uint32_t pk[16];
+#pragma unroll
+              for (int q = 0; q < 32; q += 2) {
+                float2 e = moe::ffma2(make_float2(u[q], u[q + 1]), c22, b22);
+                e.x = attn::exp2_fast(e.x);
+                e.y = attn::exp2_fast(e.y);
+                sum[(q >> 1) & 1] = moe::ffma2(e, ones, sum[(q >> 1) & 1]);
+                pk[q >> 1] = E::down(e.x, e.y);
+              }
+              attn::tmem_st16(s_addr + i / 2, pk);
+              if (i + 32 == C::BN / 2) {  // the first half may go into its product
+                attn::tmem_st_wait();
+                fence_before_sync();
+                mbar_arrive(&ctl.p_half[x]);
+              }
+            };
+            weights(s, 0);
+            attn::tmem_ld32(s_addr + kHeld, last);
+#pragma unroll
+            for (int i = 32; i < kHeld; i += 32) weights(s + i, i);
+            attn::tmem_ld_wait32(last);
+            if (edge) {
+#pragma unroll
+              for (int q = 0; q < 32; ++q) last[q] = (last_bits >> q) & 1u ? last[q] : -INFINITY;
+            }
+            weights(last, kHeld);
+            attn::tmem_st_wait();
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          } else {
+            mbar_arrive(&ctl.p_half[x]);
+          }
+          ++done;
+          fence_before_sync();
+          mbar_arrive(&ctl.p_full[x]);
+        }
+        pv_seen += done;
+        if (l != l && m == -INFINITY) m = 0.f;  // only NaN scores: not to be mistaken for a row that saw nothing
+        // ---- the piece's result
+        if (done > 0 && alive) {
+          alive = warp_wait(&ctl.o_full[st], o_seen & 1);
+          fence_after_sync();
+        }
+        o_seen += done > 0;
+        const bool whole = w.whole();
+        // Streams over different keys of a whole unit are joined here: stream 1 hands
+        // its O over in Q's second tile, which is unused then and holds all
+        // columns of 64 rows or half of them of 128.
+        const bool join = C::STREAMS == 2 && !both && tiles > 1 && whole;
+        if (both || join) named_sync(1, kWorkers);  // the other stream's flags are final
+        const bool dirty = ctl.dirty[0][w.number & 7] == w.number || ctl.dirty[1][w.number & 7] == w.number;
+        if (!alive || ctl.bad_page[w.number & 7] == w.number) l = kNaN, m = 0.f;
+        auto read_o = [&](int col, float* o) {
+          attn::tmem_ld32(o_addr + col, o);
+          attn::tmem_ld_wait32(o);
+          if (!dirty) return;
+          // NaN and infinities of drafts, for the rows that see them
+          const int d0 = max(w.p.kt0 * C::BN - w.s.len, 0), d1 = min(w.p.kt1 * C::BN - w.s.len, w.s.n);
+          for (int dr = d0; dr < d1; ++dr) {
+            const long long off = attn::slot_offset(a.c, w.b, w.s.len + dr, w.p.head);
+            if (off < 0 || !(attn::seen(a.tree, a.tree_words, w.s, token, w.s.len + dr) & 1u)) continue;
+            const T* v = static_cast<const T*>(a.c.v) + off + col;
+#pragma unroll
+            for (int q = 0; q < 32; ++q) {
+              const float e = col + q < D ? (float)v[q] : 0.f;
+              if (!isfinite(e)) o[q] += e;
+            }
+          }
+          __syncwarp();
+        };
+        if (!whole) {
+          const size_t slot = (size_t)blockIdx.x * 2 + (w.p.kt0 == 0);
+          const int at = 128 * st + r_tile;
+          if (active) {
+            if (real) reinterpret_cast<float2*>(a.ml)[slot * C::ROWS + at] = make_float2(m, l);
+            float4* dst = a.o + slot * (DP / 4) * C::ROWS + at;
+#pragma unroll 1
+            for (int col = 0; col < D && done > 0; col += 32) {
+              float o[32];
+              read_o(col, o);
+              if (real) {
+#pragma unroll
+                for (int q = 0; q < 32; q += 4)
+                  if (col + q < D) dst[(size_t)((col + q) / 4) * C::ROWS] = make_float4(o[q], o[q + 1], o[q + 2], o[q + 3]);
+              }
+              __syncwarp();
+            }
+          }
+          if (threadIdx.x == 0 && w.p.kt0 == 0) {
+            Split s;
+            s.pieces = attn::part_of(ctl.share.total, ctl.share.parts, w.p.unit_begin + w.p.tiles - 1) - blockIdx.x + 1;
+            s.first = w.s.first, s.n = w.s.n, s.head = w.p.head, s.row0 = w.row0, s.rows = w.rows;
+            a.splits[blockIdx.x] = s;
+          }
+        } else {
+          float* exch = reinterpret_cast<float*>(sQ + C::QTILE);
+          const int exch_rows = w.rows <= 64 ? 64 : 128;
+          const int span = join && exch_rows == 128 ? DP / 2 : DP;
+          const int tok = row / G;
+          const long long out_row = (long long)(w.s.first + tok) * a.q_heads + w.p.head * G + (row - tok * G);
+          float f0 = 1.f, f1 = 0.f, inv = 0.f;
+          if (join && st == 1) ctl.ml[r_tile] = make_float2(m, l);
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += span) {
+            if (join) {
+              if (st == 1 && active) {
+#pragma unroll 1
+                for (int col = 0; col < span; col += 32) {
+                  float o[32];
+                  read_o(c0 + col, o);
+#pragma unroll
+                  for (int q = 0; q < 32; ++q) exch[(col + q) * exch_rows + r_tile] = o[q];
+                }
+              }
+              named_sync(1, kWorkers);
+            }
+            if (active && (both || st == 0)) {
+              if (c0 == 0) {
+                if (join) {
+                  const float2 other = ctl.ml[r_tile];
+                  const float top = fmaxf(m, other.x);
+                  f0 = m == -INFINITY ? 0.f : attn::exp2_fast(m - top);
+                  f1 = other.x == -INFINITY ? 0.f : attn::exp2_fast(other.x - top);
+                  l = l * f0 + other.y * f1;
+                  m = top;
+                }
+                inv = l == 0.f ? 0.f : 1.f / l;
+                if (real && a.lse) a.lse[out_row] = l == 0.f ? -INFINITY : (m - kLift) * 0.6931471805599453f + logf(l);
+              }
+#pragma unroll 1
+              for (int col = 0; col < span && c0 + col < D; col += 32) {
+                float o[32];
+                read_o(c0 + col, o);
+                if (join) {
+#pragma unroll
+                  for (int q = 0; q < 32; ++q) o[q] = o[q] * f0 + (f1 == 0.f ? 0.f : exch[(col + q) * exch_rows + r_tile] * f1);
+                }
+                if (real) {
+#pragma unroll
+                  for (int q = 0; q < 32; q += 8) {
+                    float y[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = o[q + e] * inv;
+                    if (c0 + col + q < D)
+                      *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + out_row * D + c0 + col + q) = attn::pack8<E>(y);
+                  }
+                }
+                __syncwarp();
+              }
+            }
+            if (join) named_sync(1, kWorkers);
           }
         }
-        if (join) named_sync(1, kWorkers);
+        fence_before_sync();  // O has been read before the next piece's first P is announced
+        pos += 2 * tiles;
+        ++pieces;
       }
-      fence_before_sync();  // O has been read before the next piece's first P is announced
-      if (threadIdx.x == 0 && w.p.kt0 == 0 && !w.whole()) {
-        Split s;
-        s.pieces = attn::part_of(ctl.share.total, ctl.share.parts, w.p.unit_begin + w.p.tiles - 1) - blockIdx.x + 1;
-        s.first = w.s.first, s.n = w.s.n, s.head = w.p.head, s.row0 = w.row0, s.rows = w.rows;
-        a.splits[blockIdx.x] = s;
-      }
-      pos += 2 * tiles;
-      ++pieces;
     }
   }
   fence_before_sync();
@@ -582,13 +648,18 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const bool real = r < s.rows;
   const int rr = real ? r : 0;
   const int D = a.c.head_dim, G = a.q_heads / a.c.kv_heads;
+  // streams over different keys of the same rows have a place each
+  const int streams = C::STREAMS == 2 && s.rows <= 128 ? 2 : 1, n = s.pieces * streams;
   const float2* ml = reinterpret_cast<const float2*>(a.ml);
-  auto id = [&](int i) { return (size_t)(part + i) * 2 + (i == 0); };
+  auto id = [&](int i) { return (size_t)(part + i / streams) * 2 + (i < streams); };
+  auto at = [&](int i) { return rr + (i % streams) * 128; };
   float top = -INFINITY;
-  for (int i = 0; i < s.pieces; ++i) top = fmaxf(top, ml[id(i) * C::ROWS + rr].x);
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) top = fmaxf(top, ml[id(i) * C::ROWS + at(i)].x);
   float l = 0.f;
-  for (int i = 0; i < s.pieces; ++i) {
-    const float2 v = ml[id(i) * C::ROWS + rr];
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float2 v = ml[id(i) * C::ROWS + at(i)];
     l += v.x == -INFINITY ? 0.f : v.y * attn::exp2_fast(v.x - top);
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -598,11 +669,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     a.lse[out_row] = l == 0.f ? -INFINITY : (top - Weight<E>::kLift) * 0.6931471805599453f + logf(l);
   for (int c8 = warp; c8 < D / 8; c8 += kJoinThreads / 32) {
     float y[8] = {};
-    for (int i = 0; i < s.pieces; ++i) {
-      const float m = ml[id(i) * C::ROWS + rr].x;
-      if (m == -INFINITY) continue;
-      const float f = attn::exp2_fast(m - top);
-      const float4* o = a.o + (id(i) * (DP / 4) + c8 * 2) * C::ROWS + rr;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float m = ml[id(i) * C::ROWS + at(i)].x;
+      const float f = m == -INFINITY ? 0.f : attn::exp2_fast(m - top);
+      const float4* o = a.o + (id(i) * (DP / 4) + c8 * 2) * C::ROWS + at(i);
+      if (f == 0.f) continue;
       const float4 u = o[0], v = o[C::ROWS];
       y[0] += u.x * f, y[1] += u.y * f, y[2] += u.z * f, y[3] += u.w * f;
       y[4] += v.x * f, y[5] += v.y * f, y[6] += v.z * f, y[7] += v.w * f;

@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
               float s[32];
               attn::tmem_ld32(tmem + lane_base + buf * kChunk + i, s);
               const float4* bias = reinterpret_cast<const float4*>(ctl.bias + g * kChunk + i);
-              tmem_ld_wait();
+              attn::tmem_ld_wait32(s);
               if (!edge) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 4) {

@@ -46,6 +46,7 @@ __device__ bool take_share(const int32_t* __restrict__ cu, const int32_t* __rest
     if (w < warp) upto += sh.scan[w];
     total += sh.scan[w];
   }
+  if (total > kMaxTiles) return false;
   const int parts = (int)min((long long)gridDim.x, total), c = blockIdx.x;
   const long long t0 = c < parts ? part_begin(total, parts, c) : 0;
   const long long t1 = c < parts ? part_begin(total, parts, c + 1) : 0;

@@ -129,6 +129,34 @@ def test_unseen_drafts_do_not_leak(dim, dtype):
     assert torch.equal(out[20:].view(torch.int16), want[20:].view(torch.int16))
 
 
+@pytest.mark.parametrize("dim,scale", [(128, -0.11), (64, -1e-3), (256, 0.5)])
+def test_other_scales(dim, scale):
+    bt = Batch(BF, [300, 5], [3, 40], 2, 4, dim, 16, seed=17, sharp=0.7)
+    bt.scale = scale
+    out, lse = attend(bt, scale=scale)
+    bt.scale = abs(scale)  # the bound of a score is that of its size
+    bound = bt.dot_bound()
+    bt.scale, bt.dot_bound = scale, lambda: bound
+    check_attention(bt, out, lse)
+    acc = torch.zeros(2, 2, bt.cap, device="cuda")
+    got = f64(attn.attn_cache_weights(bt.q, lse, bt.cu, bt.lens, bt.cache, acc, scale=scale))
+    want = bt.expected_weights(f64(lse), f64(acc), 1.0)
+    there = ~np.isnan(want)
+    tol = (4 * (dim * 2.0 ** -23 * bound + 2.0 ** -18) + 160 * 2.0 ** -24) * want + 2.0 ** -40
+    assert np.all(np.abs(got - want)[there] <= tol[there])
+
+
+def test_cache_with_heads_outermost():
+    """[kv_heads, pages, page_size, D]: the pages lie closer together than the heads."""
+    bt = Batch(FP, [130, 33], [2, 5], 3, 2, 64, 16, seed=18)
+    want = attend(bt)
+    k, v = (x.transpose(0, 1).contiguous().transpose(0, 1) for x in (bt.k, bt.v))
+    assert k.stride(0) < k.stride(1)
+    cache = attn.attn_cache(k, v, bt.table)
+    got = attn.attn_tree_decode(bt.q, bt.cu, bt.lens, cache)
+    assert torch.equal(want[0].view(torch.int16), got[0].view(torch.int16)) and torch.equal(want[1], got[1])
+
+
 @pytest.mark.parametrize("dtype", [BF, FP])
 def test_large_scores(dtype):
     """Scores in the hundreds, and rows whose later keys are far above the first ones."""
