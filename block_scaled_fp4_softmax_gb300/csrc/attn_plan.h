@@ -2,11 +2,13 @@
 //
 // A unit is one (sequence, KV head, group of up to `unit_rows` query rows);
 // a row is one token in flight and query head of the KV head's group.  Its
-// work is the tiles of keys it looks at.  All units' tiles, in the order of
-// sequence, head, row group, form one line that is cut into `parts` nearly
-// equal ranges, one per CTA: every CTA gets the same share however ragged the
-// batch is, and a long sequence is spread over as many CTAs as its share of
-// the work.  A unit that a cut divides is joined from its pieces afterwards.
+// work is the tiles of keys it looks at, and `cost` tiles' time for fetching
+// the rows and writing the result, which stand before its first tile.  All
+// units, in the order of sequence, head, row group, form one line that is cut
+// into `parts` nearly equal ranges, one per CTA: every CTA gets the same share
+// however ragged the batch is, and a long sequence is spread over as many CTAs
+// as its share of the work.  A unit that a cut divides is joined from its
+// pieces afterwards.
 #pragma once
 
 #ifdef __CUDACC__
@@ -27,41 +29,45 @@ ATTN_HD long long quotient(long long a, long long b) {
 struct PlanDims {
   int kv_heads, group;      // query heads of a KV head
   int unit_rows, tile;      // rows of a unit, keys of a tile
+  int cost;                 // places of the line before a unit's first tile
 };
 
 ATTN_HD int row_groups(const PlanDims& d, int n) {
   return (int)quotient((long long)n * d.group + d.unit_rows - 1, d.unit_rows);
 }
 ATTN_HD int key_tiles(const PlanDims& d, int len, int n) { return (int)quotient((long long)len + n + d.tile - 1, d.tile); }
-// Tiles of all units of a sequence.
-ATTN_HD long long sequence_tiles(const PlanDims& d, int len, int n) {
-  return n <= 0 ? 0 : (long long)d.kv_heads * row_groups(d, n) * key_tiles(d, len, n);
+// Places of all units of a sequence.
+ATTN_HD long long sequence_length(const PlanDims& d, int len, int n) {
+  return n <= 0 ? 0 : (long long)d.kv_heads * row_groups(d, n) * (d.cost + key_tiles(d, len, n));
 }
 
 // A line longer than this is refused (the products below stay within 64 bits).
-constexpr long long kMaxTiles = 1ll << 47;
+constexpr long long kMaxLine = 1ll << 47;
 
-// First tile of part c, and the part that holds tile t (at most 2^15 parts).
+// First place of part c, and the part that holds place t (at most 2^15 parts).
 ATTN_HD long long part_begin(long long total, int parts, int c) { return quotient(total * c, parts); }
 ATTN_HD int part_of(long long total, int parts, long long t) { return (int)quotient((t + 1) * parts - 1, total); }
 
-// One piece of a unit: key tiles [kt0, kt1) of its `tiles`.
+// One piece of a unit: key tiles [kt0, kt1) of its `tiles` (none, if the part
+// holds only places before the first tile).
 struct Piece {
   int head, rows_group;  // within the sequence
   int kt0, kt1, tiles;
-  long long unit_begin;  // first tile of the unit on the line
+  long long first_tile;  // the place of the unit's tile 0
+  long long next;        // where the part goes on
 };
 
-// The piece that starts at tile `t` of the line and ends before `end`, where
-// the sequence's first tile is `base`.
+// The piece that starts at place `t` of the line and ends before `end`, where
+// the sequence's first place is `base`.
 ATTN_HD Piece piece_at(const PlanDims& d, int len, int n, long long base, long long t, long long end) {
   Piece p;
   p.tiles = key_tiles(d, len, n);
-  const long long u = quotient(t - base, p.tiles);
-  p.unit_begin = base + u * p.tiles;
-  p.kt0 = (int)(t - p.unit_begin);
-  const long long left = end - p.unit_begin;
-  p.kt1 = left < p.tiles ? (int)left : p.tiles;
+  const long long u = quotient(t - base, p.tiles + d.cost);
+  p.first_tile = base + u * (p.tiles + d.cost) + d.cost;
+  const long long from = t - p.first_tile, to = end - p.first_tile;
+  p.kt0 = from < 0 ? 0 : (int)from;
+  p.kt1 = to < 0 ? 0 : to < p.tiles ? (int)to : p.tiles;
+  p.next = to < p.tiles ? end : p.first_tile + p.tiles;
   const int groups = row_groups(d, n);
   p.head = (int)(u / groups);
   p.rows_group = (int)(u % groups);

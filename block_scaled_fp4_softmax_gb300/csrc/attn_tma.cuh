@@ -59,6 +59,24 @@ inline int make_maps(const attn_cache& c, int tile, Maps& m) {
 // Device
 // ---------------------------------------------------------------------------
 
+// Waits for the barrier's phase.  The first tries run without a clock, whose
+// reads are slow; after some 2 s (4e9 cycles), or once another role of the CTA has
+// given up (*abort), the wait gives up too: MOE_DEV_TIMEOUT, *abort set, false.
+__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* st) {
+  for (int i = 0; i < 64; ++i)
+    if (moe::tc::mbar_test(bar, parity)) return true;
+  const long long from = clock64();
+  while (!moe::tc::mbar_test(bar, parity)) {
+    if (abort && *abort) return false;
+    if (clock64() - from > 4000000000ll) {
+      moe::status_or(st, MOE_DEV_TIMEOUT);
+      if (abort) *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
 // One box: 64 elements from x (a multiple of 64), `box_rows` rows from `row`
 // of one head and page.  A page number past the last reads as zeros.
 __device__ __forceinline__ void load_box(const CUtensorMap* m, uint32_t dst, uint64_t* bar, int x, int row, int head,
@@ -83,6 +101,14 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t 
   d |= (uint64_t)(1024 >> 4) << 32;
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// The words of a descriptor: the high one is the same wherever the tile lies,
+// the low one holds the address and advances by (bytes >> 4).
+__device__ __forceinline__ uint64_t make_desc(uint32_t high, uint32_t low) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(low), "r"(high));
   return d;
 }
 
@@ -139,6 +165,19 @@ __device__ __forceinline__ void tmem_ld_wait32(float* r) {
         "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]),
         "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]),
         "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])
+      :
+      : "memory");
+}
+// The same; what has been added up into `done` before it in the source stays
+// before it, so that the arithmetic on one group of columns covers the loads of
+// the next.
+__device__ __forceinline__ void tmem_ld_wait32(float* r, float2 (&done)[2]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+      : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+        "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]),
+        "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]),
+        "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])
+        , "+f"(done[0].x), "+f"(done[0].y), "+f"(done[1].x), "+f"(done[1].y)
       :
       : "memory");
 }

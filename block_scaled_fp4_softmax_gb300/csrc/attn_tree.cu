@@ -43,7 +43,6 @@ namespace {
 
 constexpr int kThreads = 320;  // warps 0-3, 4-7: softmax of streams 0, 1; 8: TMA; 9: MMA
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
-constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far beyond any legitimate wait
 constexpr float kNaN = __builtin_nanf("");
 
 struct TreeArgs {
@@ -82,6 +81,9 @@ struct Cfg {
   static constexpr int PANEL = BN * 128;               // 64 elements of a tile's rows
   static constexpr int S_COL = 0, O_COL = 2 * BN;      // S buffers, then O of each stream
   static constexpr int TMEM = 512;
+  // fetching the rows and writing the result: some 8000 cycles, of which a tile
+  // takes 2700 (1400 at half the width)
+  static constexpr int UNIT_COST = DP == 64 ? 5 : 3;
   static_assert(O_COL + STREAMS * DP <= TMEM, "TMEM");
   static constexpr size_t OFF_Q = 0;
   static constexpr size_t OFF_RING = OFF_Q + (size_t)STREAMS * QTILE;
@@ -117,7 +119,24 @@ struct Weight<attn::Half> {
 
 template <class C>
 __device__ __forceinline__ attn::PlanDims plan_dims(const TreeArgs& a) {
-  return attn::PlanDims{a.c.kv_heads, a.q_heads / a.c.kv_heads, C::ROWS, C::BN};
+  return attn::PlanDims{a.c.kv_heads, a.q_heads / a.c.kv_heads, C::ROWS, C::BN, C::UNIT_COST};
+}
+
+// Adds the NaN and infinite elements of a piece's drafts, which the products
+// took as zeros, to the result of a row that sees them.
+// Element d of the row is out[(d / 4) * step + d % 4].
+template <class T, class O>
+__device__ __noinline__ void put_back(const TreeArgs& a, attn::Seq s, int b, int head, int token, int d0, int d1,
+                                      O* out, int step) {
+  for (int dr = d0; dr < d1; ++dr) {
+    const long long off = attn::slot_offset(a.c, b, s.len + dr, head);
+    if (off < 0 || !(attn::seen(a.tree, a.tree_words, s, token, s.len + dr) & 1u)) continue;
+    const T* v = static_cast<const T*>(a.c.v) + off;
+    for (int d = 0; d < a.c.head_dim; ++d) {
+      const float e = (float)v[d];
+      if (!isfinite(e)) out[d / 4 * step + d % 4] = (O)((float)out[d / 4 * step + d % 4] + e);
+    }
+  }
 }
 
 template <class E, int DP>
@@ -180,19 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   fence_after_sync();
   const uint32_t tmem = ctl.tmem;
   volatile int* abort_flag = &ctl.abort;
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (mbar_test(bar, parity)) return true;
-    const uint64_t deadline = globaltimer() + kWaitNs;
-    while (!mbar_test(bar, parity)) {
-      if (*abort_flag) return false;
-      if (globaltimer() > deadline) {
-        moe::status_or(a.st, MOE_DEV_TIMEOUT);
-        *abort_flag = 1;
-        return false;
-      }
-    }
-    return true;
-  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return attn::bounded_wait(bar, parity, abort_flag, a.st); };
 
   if (warp >= 8) {
     if (warp == kTmaWarp) {
@@ -241,8 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       // every copy has landed before the CTA's shared memory goes away
       if (lane == 0)
         for (int i = max(0, pos - C::SLOTS); i < pos; ++i) {
-          const uint64_t deadline = globaltimer() + kWaitNs;
-          mbar_wait(&ctl.full[i % C::SLOTS], (i / C::SLOTS) & 1, deadline);
+          attn::bounded_wait(&ctl.full[i % C::SLOTS], (i / C::SLOTS) & 1, nullptr, a.st);
         }
       __syncwarp();
     } else if (warp == kMmaWarp) {
@@ -257,7 +263,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       // a negative scale negates Q, the sums keep |scale|
       const uint32_t id_s = attn::idesc<E>(128, C::BN, false) | (a.scale < 0.f ? 1u << 13 : 0u);
       const uint32_t id_o = attn::idesc<E>(128, (D + 15) & ~15, true);
-      const uint32_t q_addr = smem_u32(sQ), ring = smem_u32(sRing);
+      const uint64_t q_desc = sw128_kmajor_desc(smem_u32(sQ)), k_desc = sw128_kmajor_desc(smem_u32(sRing));
+      const uint64_t v_desc = attn::sw128_mnmajor_desc(smem_u32(sRing), C::PANEL);
+      const uint32_t q_low = (uint32_t)q_desc, k_low = (uint32_t)k_desc, k_high = (uint32_t)(k_desc >> 32);
+      const uint32_t v_low = (uint32_t)v_desc, v_high = (uint32_t)(v_desc >> 32);
       while (alive && w.next()) {
         const bool both = C::STREAMS == 2 && w.rows > 128;  // two row tiles over the same keys
         const int tiles = w.p.kt1 - w.p.kt0, items = both ? 2 * tiles : tiles;
@@ -271,11 +280,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             fence_after_sync();
           }
           if (leader) {
-            const uint32_t qa = q_addr + (both && x ? C::QTILE : 0), ka = ring + (uint32_t)slot * C::SLOT;
+            uint32_t ql = q_low + (both && x ? C::QTILE >> 4 : 0), kl = k_low + (uint32_t)slot * (C::SLOT >> 4);
             const uint32_t d = tmem + C::S_COL + x * C::BN;
-            for (int kk = 0; kk < k_steps; ++kk)
-              mma_bf16(d, sw128_kmajor_desc(qa + (kk >> 2) * 128 * 128 + (kk & 3) * 32),
-                       sw128_kmajor_desc(ka + (kk >> 2) * C::PANEL + (kk & 3) * 32), id_s, kk != 0);
+            for (int p = 0; p < panels; ++p, ql += (128 * 128) >> 4, kl += C::PANEL >> 4) {
+              if (4 * p + 4 <= k_steps) {  // unrolled, the MMAs leave at the tensor core's pace
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  mma_bf16(d, attn::make_desc(k_high, ql + 2 * kk), attn::make_desc(k_high, kl + 2 * kk), id_s, (p | kk) != 0);
+              } else {
+                for (int kk = 0; kk < k_steps - 4 * p; ++kk)
+                  mma_bf16(d, attn::make_desc(k_high, ql + 2 * kk), attn::make_desc(k_high, kl + 2 * kk), id_s, (p | kk) != 0);
+              }
+            }
             mma_commit(&ctl.s_full[x]);
             if (!both || x == 1) mma_commit(&ctl.empty[slot]);
             if (it == items - 1) mma_commit(&ctl.qk_done);
@@ -289,15 +305,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           const int seen = x ? p_seen1++ : p_seen0++;
           if (!warp_wait(&ctl.p_half[x], seen & 1)) return false;
           if ((!both || x == 0) && !warp_wait(&ctl.full[slot], (ps / C::SLOTS) & 1)) return false;
-          const uint32_t va = ring + (uint32_t)slot * C::SLOT;
+          const uint32_t vl = v_low + (uint32_t)slot * (C::SLOT >> 4);
           const bool first = C::STREAMS == 2 ? it < 2 : it == 0;
           const uint32_t d = tmem + C::O_COL + st * DP, p = tmem + C::S_COL + x * C::BN;
           for (int half = 0; half < 2; ++half) {
             if (half == 1 && !warp_wait(&ctl.p_full[x], seen & 1)) return false;
             fence_after_sync();
             if (leader) {
-              for (int kk = half * (C::BN / 32); kk < (half + 1) * (C::BN / 32); ++kk)
-                attn::mma_ts(d, p + kk * 8, attn::sw128_mnmajor_desc(va + kk * 2048, C::PANEL), id_o, !(first && kk == 0));
+              const uint32_t ph = p + half * (C::BN / 4), vh = vl + half * (C::PANEL / 2 >> 4);
+#pragma unroll
+              for (int kk = 0; kk < C::BN / 32; ++kk)
+                attn::mma_ts(d, ph + kk * 8, attn::make_desc(v_high, vh + kk * (2048 >> 4)), id_o, !(first && half == 0 && kk == 0));
             }
             __syncwarp();
           }
@@ -320,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       // every MMA has completed before TMEM goes back
       if (leader) {
         mma_commit(&ctl.drain);
-        mbar_wait(&ctl.drain, 0, globaltimer() + kWaitNs);
+        attn::bounded_wait(&ctl.drain, 0, nullptr, a.st);
       }
       __syncwarp();
     }
@@ -351,13 +369,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           const int me = both ? threadIdx.x & 127 : threadIdx.x, step = (both ? 128 : kWorkers) / 8;
           const int ch = me & 7;  // 8 lanes copy 128 contiguous bytes
           const T* q = static_cast<const T*>(a.q) + (long long)w.s.first * a.q_stride + (long long)w.p.head * G * D + ch * 8;
+          const int first = w.row0 + tile_row0 + (me >> 3), step_tok = step / G, step_g = step - step_tok * G;
+          int tok = first / G, g = first - tok * G;
           for (int r = me >> 3; r < n_rows; r += step) {
-            const int row = w.row0 + tile_row0 + r, tok = row / G;
-            const T* src = q + tok * a.q_stride + (row - tok * G) * D;
+            const T* src = q + tok * a.q_stride + g * D;
             for (int p = 0; p < panels; ++p) {
               const bool inside = p * 64 + ch * 8 < D;
               cp_async16(dst + attn::sw128_offset(r, p * 8 + ch, 128), inside ? src + p * 64 : src, inside ? 16u : 0u);
             }
+            tok += step_tok, g += step_g;
+            if (g >= G) g -= G, ++tok;
           }
           cp_async_commit();
           cp_async_wait<0>();
@@ -520,23 +541,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         if (both || join) named_sync(1, kWorkers);  // the other stream's flags are final
         const bool dirty = ctl.dirty[0][w.number & 7] == w.number || ctl.dirty[1][w.number & 7] == w.number;
         if (!alive || ctl.bad_page[w.number & 7] == w.number) l = kNaN, m = 0.f;
+        const int d0 = max(w.p.kt0 * C::BN - w.s.len, 0), d1 = min(w.p.kt1 * C::BN - w.s.len, w.s.n);  // its drafts
         auto read_o = [&](int col, float* o) {
           attn::tmem_ld32(o_addr + col, o);
           attn::tmem_ld_wait32(o);
-          if (!dirty) return;
-          // NaN and infinities of drafts, for the rows that see them
-          const int d0 = max(w.p.kt0 * C::BN - w.s.len, 0), d1 = min(w.p.kt1 * C::BN - w.s.len, w.s.n);
-          for (int dr = d0; dr < d1; ++dr) {
-            const long long off = attn::slot_offset(a.c, w.b, w.s.len + dr, w.p.head);
-            if (off < 0 || !(attn::seen(a.tree, a.tree_words, w.s, token, w.s.len + dr) & 1u)) continue;
-            const T* v = static_cast<const T*>(a.c.v) + off + col;
-#pragma unroll
-            for (int q = 0; q < 32; ++q) {
-              const float e = col + q < D ? (float)v[q] : 0.f;
-              if (!isfinite(e)) o[q] += e;
-            }
-          }
-          __syncwarp();
         };
         if (!whole) {
           const size_t slot = (size_t)blockIdx.x * 2 + (w.p.kt0 == 0);
@@ -551,14 +559,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
               if (real) {
 #pragma unroll
                 for (int q = 0; q < 32; q += 4)
-                  if (col + q < D) dst[(size_t)((col + q) / 4) * C::ROWS] = make_float4(o[q], o[q + 1], o[q + 2], o[q + 3]);
+                  if (col + q < D) dst[(col + q) / 4 * C::ROWS] = make_float4(o[q], o[q + 1], o[q + 2], o[q + 3]);
               }
               __syncwarp();
             }
+            if (dirty && real && done > 0) {
+              put_back<T>(a, w.s, w.b, w.p.head, token, d0, d1, reinterpret_cast<float*>(dst), 4 * C::ROWS);
+            }
+            __syncwarp();
           }
           if (threadIdx.x == 0 && w.p.kt0 == 0) {
             Split s;
-            s.pieces = attn::part_of(ctl.share.total, ctl.share.parts, w.p.unit_begin + w.p.tiles - 1) - blockIdx.x + 1;
+            s.pieces = attn::part_of(ctl.share.total, ctl.share.parts, w.p.first_tile + w.p.tiles - 1) - blockIdx.x + 1;
             s.first = w.s.first, s.n = w.s.n, s.head = w.p.head, s.row0 = w.row0, s.rows = w.rows;
             a.splits[blockIdx.x] = s;
           }
@@ -620,6 +632,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             }
             if (join) named_sync(1, kWorkers);
           }
+          if (dirty && real && active && (both || st == 0)) {
+            put_back<T>(a, w.s, w.b, w.p.head, token, d0, d1, static_cast<T*>(a.out) + out_row * D, 4);
+          }
+          __syncwarp();
         }
         fence_before_sync();  // O has been read before the next piece's first P is announced
         pos += 2 * tiles;
@@ -632,56 +648,78 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   if (warp == kMmaWarp) tmem_dealloc(tmem, C::TMEM);
 }
 
-// Adds up the pieces of divided units.  Block (part, 32 rows): lane = row,
-// warps share the columns.
-constexpr int kJoinThreads = 256;
+// Adds up the pieces of divided units.  Block (part, y) takes rows 32 y .. 32 y +
+// 31 of the unit, a lane to a row.  The warps first share the pieces (m and l,
+// turned into factors in shared memory), then the columns.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 
 template <class E, int DP>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ TreeArgs a) {
   using C = Cfg<DP>;
   using T = typename E::T;
+  constexpr int kChunk = 32;  // pieces whose factors are held at a time
+  __shared__ float s_top[kJoinWarps][32], s_l[kJoinWarps][32], s_factor[kChunk][32];
   moe::pdl_wait();
   const int part = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Split s = a.splits[part];
-  const int r = blockIdx.y * 32 + lane;
-  if (blockIdx.y * 32 >= s.rows * (s.pieces > 0)) return;
-  const bool real = r < s.rows;
-  const int rr = real ? r : 0;
+  if (s.pieces == 0) return;
   const int D = a.c.head_dim, G = a.q_heads / a.c.kv_heads;
   // streams over different keys of the same rows have a place each
   const int streams = C::STREAMS == 2 && s.rows <= 128 ? 2 : 1, n = s.pieces * streams;
   const float2* ml = reinterpret_cast<const float2*>(a.ml);
-  auto id = [&](int i) { return (size_t)(part + i / streams) * 2 + (i < streams); };
-  auto at = [&](int i) { return rr + (i % streams) * 128; };
-  float top = -INFINITY;
+  for (int r0 = blockIdx.y * 32; r0 < s.rows; r0 += gridDim.y * 32) {
+    const bool real = r0 + lane < s.rows;
+    const int r = real ? r0 + lane : r0;
+    auto slot = [&](int i) { return (size_t)(part + i / streams) * 2 + (i < streams); };
+    auto at = [&](int i) { return r + (i % streams) * 128; };
+    float top = -INFINITY;
 #pragma unroll 4
-  for (int i = 0; i < n; ++i) top = fmaxf(top, ml[id(i) * C::ROWS + at(i)].x);
-  float l = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float2 v = ml[id(i) * C::ROWS + at(i)];
-    l += v.x == -INFINITY ? 0.f : v.y * attn::exp2_fast(v.x - top);
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int row = s.row0 + rr;
-  const long long out_row = (long long)(s.first + row / G) * a.q_heads + s.head * G + row % G;
-  if (warp == 0 && real && a.lse)
-    a.lse[out_row] = l == 0.f ? -INFINITY : (top - Weight<E>::kLift) * 0.6931471805599453f + logf(l);
-  for (int c8 = warp; c8 < D / 8; c8 += kJoinThreads / 32) {
-    float y[8] = {};
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float m = ml[id(i) * C::ROWS + at(i)].x;
-      const float f = m == -INFINITY ? 0.f : attn::exp2_fast(m - top);
-      const float4* o = a.o + (id(i) * (DP / 4) + c8 * 2) * C::ROWS + at(i);
-      if (f == 0.f) continue;
-      const float4 u = o[0], v = o[C::ROWS];
-      y[0] += u.x * f, y[1] += u.y * f, y[2] += u.z * f, y[3] += u.w * f;
-      y[4] += v.x * f, y[5] += v.y * f, y[6] += v.z * f, y[7] += v.w * f;
-    }
+    for (int i = warp; i < n; i += kJoinWarps) top = fmaxf(top, ml[slot(i) * C::ROWS + at(i)].x);
+    s_top[warp][lane] = top;
+    __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] *= inv;
-    if (real) *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + out_row * D + c8 * 8) = attn::pack8<E>(y);
+    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, s_top[w][lane]);
+    float l = 0.f, y[DP / kJoinWarps] = {};  // columns 4 (warp + 8 k) ..
+    for (int i0 = 0; i0 < n; i0 += kChunk) {
+      const int count = min(kChunk, n - i0);
+      for (int i = warp; i < count; i += kJoinWarps) {
+        const float2 v = ml[slot(i0 + i) * C::ROWS + at(i0 + i)];
+        const float f = v.x == -INFINITY ? 0.f : attn::exp2_fast(v.x - top);
+        if (v.x != -INFINITY) l += v.y * f;
+        s_factor[i][lane] = f;
+      }
+      __syncthreads();
+#pragma unroll 4
+      for (int i = 0; i < count; ++i) {
+        const float f = s_factor[i][lane];
+        const float4* o = a.o + (slot(i0 + i) * (DP / 4) + warp) * C::ROWS + at(i0 + i);
+#pragma unroll
+        for (int k = 0; k < DP / 4 / kJoinWarps; ++k)
+          if (f != 0.f && (warp + k * kJoinWarps) * 4 < D) {  // 0: a piece that saw nothing, and wrote nothing
+            const float4 v = o[(size_t)k * kJoinWarps * C::ROWS];
+            y[4 * k] += v.x * f, y[4 * k + 1] += v.y * f, y[4 * k + 2] += v.z * f, y[4 * k + 3] += v.w * f;
+          }
+      }
+      __syncthreads();
+    }
+    s_l[warp][lane] = l;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) l += s_l[w][lane];
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int row = s.row0 + r, tok = row / G;
+    const long long out_row = (long long)(s.first + tok) * a.q_heads + s.head * G + (row - tok * G);
+    if (warp == 0 && real && a.lse)
+      a.lse[out_row] = l == 0.f ? -INFINITY : (top - Weight<E>::kLift) * 0.6931471805599453f + logf(l);
+#pragma unroll
+    for (int k = 0; k < DP / 4 / kJoinWarps; ++k) {
+      const int d = (warp + k * kJoinWarps) * 4;
+      if (real && d < D)
+        *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + out_row * D + d) =
+            make_uint2(E::down(y[4 * k] * inv, y[4 * k + 1] * inv), E::down(y[4 * k + 2] * inv, y[4 * k + 3] * inv));
+    }
+    __syncthreads();
   }
 }
 
@@ -707,8 +745,11 @@ int launch(TreeArgs& a, int sms, cudaStream_t st) {
   static moe::SmemGrant grant;
   if (const int rc = attn::make_maps(a.c, C::BN, a.maps)) return rc;
   if (!moe::grant_smem(tree_kernel<E, DP>, smem_bytes<C>(), grant)) return MOE_ERR_CUDA;
+  // rows of an average sequence; a block goes on with the rows 32 join_blocks on
+  const long long rows = ((long long)a.tokens + a.c.batch - 1) / a.c.batch * (a.q_heads / a.c.kv_heads);
+  const int join_blocks = rows >= C::ROWS ? C::ROWS / 32 : (int)(rows + 31) / 32;
   if (const int rc = moe::launch_pdl(tree_kernel<E, DP>, dim3(sms), dim3(kThreads), smem_bytes<C>(), st, a)) return rc;
-  return moe::launch_pdl(join_kernel<E, DP>, dim3(sms, C::ROWS / 32), dim3(kJoinThreads), 0, st, a);
+  return moe::launch_pdl(join_kernel<E, DP>, dim3(sms, join_blocks), dim3(kJoinThreads), 0, st, a);
 }
 
 template <class E>

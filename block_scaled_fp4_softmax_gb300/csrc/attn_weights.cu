@@ -11,9 +11,9 @@
 //
 // What bounds it: K alone for a few rows (HBM); with R rows a tile of 128 slots
 // costs 128 R exponentials, which passes the time of its 32 KB (D = 128) at some
-// 100 rows, and the MMAs (128 R D products) run beside them.  Two warpgroups take
-// alternate tiles, each with two S buffers, so both the exponentials and the
-// MMAs always have a next chunk to go to.
+// 100 rows, and the MMAs (128 R D products) run beside them.  Four warpgroups
+// share the chunks of two tiles, each with an S buffer of its own: while one
+// waits for its next product, three keep the exponential units busy.
 //
 // Work division: attn_plan.h, with units of all rows of a sequence and KV
 // head; tiles are independent, so a cut unit needs no joining.  More rows than
@@ -26,16 +26,17 @@ using namespace moe::tc;
 
 namespace {
 
-constexpr int kThreads = 320;  // warps 0-3, 4-7: even and odd tiles; 8: TMA; 9: MMA
-constexpr int kWorkers = 256;
-constexpr int kTmaWarp = 8, kMmaWarp = 9;
+// Warpgroups 0, 1: even and odd chunks of the even tiles; 2, 3: of the odd
+// tiles; then a warp each for TMA and MMA.
+constexpr int kThreads = 576;
+constexpr int kWorkers = 512;
+constexpr int kTmaWarp = 16, kMmaWarp = 17;
 constexpr int kTile = 128;               // slots of a tile
 constexpr int kChunk = 128;              // rows of one MMA and S buffer
 constexpr int kPanel = kTile * 128;      // bytes of 64 elements of a tile
 constexpr int kSlots = 5;                // panels in the ring
 constexpr int kQBytes = 128 * 1024;
 constexpr int kMaxRows = kQBytes / 128;  // rows that Q's room holds at D <= 64
-constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kNaN = __builtin_nanf("");
 
 struct WeightArgs {
@@ -58,11 +59,12 @@ struct WeightArgs {
 
 struct Control {
   uint64_t full[kSlots], empty[kSlots];
-  uint64_t s_full[4], s_free[4];  // S buffers 0, 1 of warpgroup 0, then of 1
+  uint64_t s_full[4], s_free[4];  // one S buffer for each warpgroup
   uint64_t q_full, qk_done, drain;
   attn::Share share;
   uint32_t tmem;
   int abort;
+  float odd[2][2][kTile];  // [tile parity][even, odd of its tiles]: sums of the odd chunks
   alignas(16) float bias[kMaxRows];  // -lse in powers of two; -inf for rows that add nothing
 };
 constexpr size_t kOffRing = kQBytes, kOffCtrl = kOffRing + (size_t)kSlots * kPanel;
@@ -101,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
   }
   moe::pdl_wait();
   moe::pdl_launch_dependents();
-  const attn::PlanDims dims{a.c.kv_heads, G, 0x7FFFFFFF, kTile};
+  const attn::PlanDims dims{a.c.kv_heads, G, 0x7FFFFFFF, kTile, 2};
   const long long most = (long long)a.c.max_pages * a.c.page_size;
   if (!attn::take_share<kThreads>(a.cu, a.lens, a.c.batch, a.tokens, most < a.slot_cap ? most : a.slot_cap, dims,
                                   ctl.share)) {
@@ -128,19 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
   fence_after_sync();
   const uint32_t tmem = ctl.tmem;
   volatile int* abort_flag = &ctl.abort;
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (mbar_test(bar, parity)) return true;
-    const uint64_t deadline = globaltimer() + kWaitNs;
-    while (!mbar_test(bar, parity)) {
-      if (*abort_flag) return false;
-      if (globaltimer() > deadline) {
-        moe::status_or(a.st, MOE_DEV_TIMEOUT);
-        *abort_flag = 1;
-        return false;
-      }
-    }
-    return true;
-  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return attn::bounded_wait(bar, parity, abort_flag, a.st); };
   auto passes = [&](const attn::Walk& w) { return (w.rows + q_rows - 1) / q_rows; };
 
   if (warp == kTmaWarp) {
@@ -183,69 +173,94 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
     }
     if (lane == 0)  // every copy has landed before the CTA's shared memory goes away
       for (int i = max(0, pos - kSlots); i < pos; ++i)
-        mbar_wait(&ctl.full[i % kSlots], (i / kSlots) & 1, globaltimer() + kWaitNs);
+        attn::bounded_wait(&ctl.full[i % kSlots], (i / kSlots) & 1, nullptr, a.st);
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------- MMA
-    if (lane == 0) {
-      attn::Walk w(a.cu, a.lens, a.tokens, dims, ctl.share);
-      int pos = 0, loads = 0, used[2] = {0, 0};
-      bool alive = true;
-      const int k_steps = (D + 15) / 16;
-      while (alive && w.next()) {
-        const int tiles = w.p.kt1 - w.p.kt0, n_pass = passes(w);
-        for (int pass = 0; pass < n_pass && alive; ++pass) {
-          const int rows = min(q_rows, w.rows - pass * q_rows), chunks = (rows + kChunk - 1) / kChunk;
-          alive = wait(&ctl.q_full, loads++ & 1);
-          fence_after_sync();
-          auto product = [&](int tile, int g) {
-            const int x = tile & 1, buf = 2 * x + (used[x] & 1);
-            if (!wait(&ctl.s_free[buf], ((used[x] >> 1) & 1) ^ 1)) return false;
-            ++used[x];
-            const int n = min(kChunk, ((rows - g * kChunk) + 31) & ~31);
-            const uint32_t id = attn::idesc<E>(kTile, n, false);
-            const int ps = pos + tile * panels;
+    // The warp walks and waits as one; its elected lane issues.
+    const bool leader = attn::elect_lane();
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+    attn::Walk w(a.cu, a.lens, a.tokens, dims, ctl.share);
+    int slot0 = 0, round0 = 0;          // ring slot of the pass's first panel, and how often the ring had turned
+    int loads = 0;
+    uint32_t used = 0;                  // bit b: buffer b has been used an odd number of times
+    bool alive = true;
+    const int k_steps = (D + 15) / 16;
+    const uint64_t q_desc = sw128_kmajor_desc(smem_u32(sQ)), k_desc = sw128_kmajor_desc(smem_u32(sRing));
+    const uint32_t high = (uint32_t)(q_desc >> 32), q_low = (uint32_t)q_desc, k_low = (uint32_t)k_desc;
+    const uint32_t negate = a.scale < 0.f ? 1u << 13 : 0u;  // a negative scale negates K, the sums keep |scale|
+    while (alive && w.next()) {
+      const int tiles = w.p.kt1 - w.p.kt0, n_pass = passes(w);
+      for (int pass = 0; pass < n_pass && alive; ++pass) {
+        const int rows = min(q_rows, w.rows - pass * q_rows), chunks = (rows + kChunk - 1) / kChunk;
+        alive = warp_wait(&ctl.q_full, loads++ & 1);
+        fence_after_sync();
+        // chunks g and g + 1 in one product: a slot's elements are read once for both
+        auto product = [&](int tile, int first_slot, int first_round, int g) {
+          const int buf = 2 * (tile & 1);
+          const bool second = g + 1 < chunks, last = g + 2 >= chunks;
+          if (!warp_wait(&ctl.s_free[buf], ((used >> buf) & 1) ^ 1)) return false;
+          if (second && !warp_wait(&ctl.s_free[buf + 1], ((used >> (buf + 1)) & 1) ^ 1)) return false;
+          used ^= (second ? 3u : 1u) << buf;
+          const int n = min(2 * kChunk, ((rows - g * kChunk) + 31) & ~31);
+          const uint32_t id = attn::idesc<E>(kTile, n, false) | negate;
+          const uint32_t d = tmem + buf * kChunk;
+          int slot = first_slot, round = first_round;
+          for (int p = 0; p < panels; ++p) {
+            if (g == 0 && !warp_wait(&ctl.full[slot], round & 1)) return false;
             fence_after_sync();
-            for (int kk = 0; kk < k_steps; ++kk) {
-              const int p = kk >> 2, slot = (ps + p) % kSlots;
-              if (g == 0 && (kk & 3) == 0) {
-                if (!wait(&ctl.full[slot], ((ps + p) / kSlots) & 1)) return false;
-                fence_after_sync();
+            if (leader) {
+              uint32_t kl = k_low + (uint32_t)slot * (kPanel >> 4);
+              uint32_t ql = q_low + (uint32_t)(p * q_rows + g * kChunk) * (128 >> 4);
+              const int steps = min(4, k_steps - 4 * p);
+              if (steps == 4) {  // unrolled, the MMAs leave at the tensor core's pace
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  mma_bf16(d, attn::make_desc(high, kl + 2 * kk), attn::make_desc(high, ql + 2 * kk), id, (p | kk) != 0);
+              } else {
+                for (int kk = 0; kk < steps; ++kk)
+                  mma_bf16(d, attn::make_desc(high, kl + 2 * kk), attn::make_desc(high, ql + 2 * kk), id, (p | kk) != 0);
               }
-              mma_bf16(tmem + buf * kChunk,
-                       sw128_kmajor_desc(smem_u32(sRing + (size_t)slot * kPanel) + (kk & 3) * 32),
-                       sw128_kmajor_desc(smem_u32(sQ) + p * q_rows * 128 + g * kChunk * 128 + (kk & 3) * 32), id, kk != 0);
+              if (last) mma_commit(&ctl.empty[slot]);
             }
-            mma_commit(&ctl.s_full[buf]);
-            if (g == chunks - 1) {
-              for (int p = 0; p < panels; ++p) mma_commit(&ctl.empty[(ps + p) % kSlots]);
-              if (tile == tiles - 1) mma_commit(&ctl.qk_done);
-            }
-            return true;
-          };
-          if (paired) {
-            for (int t = 0; t < tiles && alive; t += 2)
-              for (int g = 0; g < chunks && alive; ++g) {
-                alive = product(t, g);
-                if (t + 1 < tiles) alive = alive && product(t + 1, g);
-              }
-          } else {
-            for (int t = 0; t < tiles && alive; ++t)
-              for (int g = 0; g < chunks && alive; ++g) alive = product(t, g);
+            __syncwarp();
+            if (++slot == kSlots) slot = 0, ++round;
           }
-          pos += tiles * panels;
+          if (leader) {
+            mma_commit(&ctl.s_full[buf]);
+            if (second) mma_commit(&ctl.s_full[buf + 1]);
+            if (last && tile == tiles - 1) mma_commit(&ctl.qk_done);
+          }
+          __syncwarp();
+          return true;
+        };
+        auto advance = [&](int& slot, int& round) {
+          slot += panels;
+          if (slot >= kSlots) slot -= kSlots, ++round;
+        };
+        for (int t = 0; t < tiles && alive; t += paired ? 2 : 1) {
+          int slot1 = slot0, round1 = round0;
+          advance(slot1, round1);
+          const bool two = paired && t + 1 < tiles;
+          for (int g = 0; g < chunks && alive; g += 2) {
+            alive = product(t, slot0, round0, g);
+            if (two) alive = alive && product(t + 1, slot1, round1, g);
+          }
+          slot0 = slot1, round0 = round1;
+          if (two) advance(slot0, round0);
         }
       }
+    }
+    if (leader) {
       mma_commit(&ctl.drain);
-      mbar_wait(&ctl.drain, 0, globaltimer() + kWaitNs);
+      attn::bounded_wait(&ctl.drain, 0, nullptr, a.st);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------- sums
-    const int x = warp >> 2, wl = warp & 3;
+    const int buf = warp >> 2, x = buf >> 1, odd = buf & 1, wl = warp & 3;
     const uint32_t lane_base = (uint32_t)(wl * 32) << 16;
     const float c2 = fabsf(a.scale) * 1.4426950408889634f;
-    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;  // a negative scale turns q's signs instead
     const float2 c22 = make_float2(c2, c2), ones = make_float2(1.f, 1.f);
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
     attn::Walk w(a.cu, a.lens, a.tokens, dims, ctl.share);
@@ -260,17 +275,21 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
         ++loads;
         named_sync(1, kWorkers);  // both warpgroups are done with the biases
         {
-          const int n_chunks = panels * 8, padded = (rows + 31) & ~31;
-          const T* q = static_cast<const T*>(a.q);
-          for (int i = threadIdx.x; i < padded * n_chunks; i += kWorkers) {
-            const int r = i / n_chunks, ch = i - r * n_chunks;
-            const int row = r0 + r, tok = row / G, g = row - tok * G;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (r < rows && ch * 8 < D)
-              v = *reinterpret_cast<const uint4*>(q + (long long)(w.s.first + tok) * a.q_stride + ((long long)w.p.head * G + g) * D + ch * 8);
-            v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-            *reinterpret_cast<uint4*>(sQ + attn::sw128_offset(r, ch, q_rows)) = v;
+          const int padded = (rows + 31) & ~31, ch = threadIdx.x & 7;  // 8 lanes copy 128 contiguous bytes
+          const uint32_t dst = smem_u32(sQ);
+          const T* q = static_cast<const T*>(a.q) + (long long)w.s.first * a.q_stride + (long long)w.p.head * G * D + ch * 8;
+          const int first = r0 + (threadIdx.x >> 3), step = kWorkers / 8, step_tok = step / G, step_g = step - step_tok * G;
+          int tok = first / G, g = first - tok * G;
+          for (int r = threadIdx.x >> 3; r < padded; r += step) {
+            const T* src = r < rows ? q + tok * a.q_stride + g * D : q;
+            for (int p = 0; p < panels; ++p) {
+              const bool inside = r < rows && p * 64 + ch * 8 < D;
+              cp_async16(dst + attn::sw128_offset(r, p * 8 + ch, q_rows), inside ? src + p * 64 : src, inside ? 16u : 0u);
+            }
+            tok += step_tok, g += step_g;
+            if (g >= G) g -= G, ++tok;
           }
+          cp_async_commit();
           for (int r = threadIdx.x; r < padded; r += kWorkers) {
             float bias = -INFINITY;
             if (r < rows) {
@@ -280,36 +299,36 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
             }
             ctl.bias[r] = bias;
           }
+          cp_async_wait<0>();
           fence_proxy_async();
           named_sync(1, kWorkers);
           mbar_arrive(&ctl.q_full);
         }
         for (int j = w.p.kt0 + x; j < w.p.kt1; j += 2) {
           const int k0 = j * kTile + wl * 32, slot = k0 + lane;
-          const bool mine = slot < w.s.len + w.s.n;
+          const bool mine = !odd && slot < w.s.len + w.s.n;
+          // loaded here, used behind the sums: a use any earlier would stall the warp
           float before = 0.f;
-          bool bad = false;
+          int page = 0;
           if (mine) {
-            const int page = __ldg(a.c.page_table + (size_t)w.b * a.c.max_pages + slot / a.c.page_size);
-            bad = (unsigned)page >= (unsigned)a.c.pages;
+            page = __ldg(a.c.page_table + (size_t)w.b * a.c.max_pages + slot / a.c.page_size);
             if (pass > 0) before = a.acc_out[base + slot];
-            else if (slot < w.s.len) before = a.decay * a.acc[base + slot];
+            else if (slot < w.s.len) before = a.acc[base + slot];
           }
           const bool edge = k0 + 32 > w.s.len;  // some of the warp's slots are drafts or past the end
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          for (int g = 0; g < chunks && alive; ++g) {
-            const int buf = 2 * x + (used & 1);
-            alive = warp_wait(&ctl.s_full[buf], (used >> 1) & 1);
+          for (int g = odd; g < chunks && alive; g += 2) {
+            alive = warp_wait(&ctl.s_full[buf], used++ & 1);
             if (!alive) break;
-            ++used;
             fence_after_sync();
             const int n = min(kChunk, ((rows - g * kChunk) + 31) & ~31);
+#pragma unroll 1
             for (int i = 0; i < n; i += 32) {
               float s[32];
               attn::tmem_ld32(tmem + lane_base + buf * kChunk + i, s);
-              const float4* bias = reinterpret_cast<const float4*>(ctl.bias + g * kChunk + i);
               attn::tmem_ld_wait32(s);
               if (!edge) {
+                const float4* bias = reinterpret_cast<const float4*>(ctl.bias + g * kChunk + i);
 #pragma unroll
                 for (int e = 0; e < 32; e += 4) {
                   const float4 bb = bias[e >> 2];
@@ -323,8 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
               } else {
                 // lane e looks up what row e sees of the warp's 32 slots
                 const int row = r0 + g * kChunk + i + lane;
-                const uint32_t bits =
-                    row < r0 + rows ? attn::seen(a.tree, a.tree_words, w.s, row / G, k0) : 0u;
+                const uint32_t bits = row < r0 + rows ? attn::seen(a.tree, a.tree_words, w.s, row / G, k0) : 0u;
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
                   const uint32_t of_row = __shfl_sync(0xffffffffu, bits, e);
@@ -336,9 +354,16 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
             fence_before_sync();
             mbar_arrive(&ctl.s_free[buf]);
           }
+          float total = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          if (chunks > 1) {  // the odd chunks' sums; the next tile's take the other place
+            float* from = ctl.odd[x][(j >> 1) & 1];
+            if (odd) from[wl * 32 + lane] = alive ? total : kNaN;
+            named_sync(2 + x, 256);
+            if (!odd) total += from[wl * 32 + lane];
+          }
           if (mine) {
-            const float total = before + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
-            a.acc_out[base + slot] = bad || !alive ? kNaN : total;
+            const bool bad = (unsigned)page >= (unsigned)a.c.pages;
+            a.acc_out[base + slot] = bad || !alive ? kNaN : (pass > 0 ? before : a.decay * before) + total;
           }
         }
       }

@@ -1,4 +1,4 @@
-// The line of key tiles that attn_plan.h describes, as the kernels walk it.
+// The line of work that attn_plan.h describes, as the kernels walk it.
 #pragma once
 
 #include "attn.cuh"
@@ -9,44 +9,46 @@ namespace attn {
 // What a kernel's CTA knows of the batch, in shared memory.
 struct Share {
   long long scan[32];
-  long long base0;      // first tile of sequence b0
-  long long t0, t1;     // this CTA's tiles
-  long long total;      // tiles of the line
+  long long base0;      // first place of sequence b0
+  long long t0, t1;     // this CTA's places
+  long long total;      // places of the line
   int b0;               // the sequence that t0 lies in
-  int parts;            // CTAs that have tiles
+  int parts;            // CTAs that have places
 };
 
 // Scans the batch with the whole block of THREADS threads: the CTA's range of
-// tiles and the sequence it starts in.  False if lens or cu are out of range
+// the line and the sequence it starts in.  False if lens or cu are out of range
 // (the same verdict in every CTA).  Ends with a block barrier.
 template <int THREADS>
 __device__ bool take_share(const int32_t* __restrict__ cu, const int32_t* __restrict__ lens, int batch, int tokens,
                            long long cap, const PlanDims& d, Share& sh) {
   const int per = (batch + THREADS - 1) / THREADS;
   const int b0 = min((int)threadIdx.x * per, batch), b1 = min(b0 + per, batch);
+  bool ok = __ldg(cu) == 0 && __ldg(cu + batch) == tokens;
   long long mine = 0;
-  bool ok = true;
   for (int b = b0; b < b1; ++b) {
     const Seq s = sequence(cu, lens, b, tokens, cap);
     ok &= s.ok;
-    if (s.ok) mine += sequence_tiles(d, s.len, s.n);
+    if (s.ok) mine += sequence_length(d, s.len, s.n);
   }
-  if (threadIdx.x == 0) ok &= __ldg(cu) == 0 && __ldg(cu + batch) == tokens;
   long long upto = mine;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warps = min(THREADS, (batch + per - 1) / per + 31) / 32;  // those that hold sequences
+  if (warp < warps) {
 #pragma unroll
-  for (int k = 1; k < 32; k <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, upto, k);
-    if (lane >= k) upto += o;
+    for (int k = 1; k < 32; k <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, upto, k);
+      if (lane >= k) upto += o;
+    }
+    if (lane == 31) sh.scan[warp] = upto;
   }
-  if (lane == 31) sh.scan[warp] = upto;
   if (!__syncthreads_and(ok)) return false;
   long long total = 0;
-  for (int w = 0; w < THREADS / 32; ++w) {
+  for (int w = 0; w < warps; ++w) {
     if (w < warp) upto += sh.scan[w];
     total += sh.scan[w];
   }
-  if (total > kMaxTiles) return false;
+  if (total > kMaxLine) return false;
   const int parts = (int)min((long long)gridDim.x, total), c = blockIdx.x;
   const long long t0 = c < parts ? part_begin(total, parts, c) : 0;
   const long long t1 = c < parts ? part_begin(total, parts, c + 1) : 0;
@@ -56,7 +58,7 @@ __device__ bool take_share(const int32_t* __restrict__ cu, const int32_t* __rest
     int b = b0;
     for (;; ++b) {
       const Seq s = sequence(cu, lens, b, tokens, cap);
-      const long long w = sequence_tiles(d, s.len, s.n);
+      const long long w = sequence_length(d, s.len, s.n);
       if (t0 < base + w) break;
       base += w;
     }
@@ -83,15 +85,17 @@ struct Walk {
     if (t < t1) s = sequence(cu, lens, b, tokens, kMaxSlots);
   }
   __device__ bool next() {
-    if (t >= t1) return false;
-    long long w = sequence_tiles(d, s.len, s.n);
-    while (t >= base + w) {
-      base += w;
-      s = sequence(cu, lens, ++b, tokens, kMaxSlots);
-      w = sequence_tiles(d, s.len, s.n);
-    }
-    p = piece_at(d, s.len, s.n, base, t, t1);
-    t += p.kt1 - p.kt0;
+    do {
+      if (t >= t1) return false;
+      long long w = sequence_length(d, s.len, s.n);
+      while (t >= base + w) {
+        base += w;
+        s = sequence(cu, lens, ++b, tokens, kMaxSlots);
+        w = sequence_length(d, s.len, s.n);
+      }
+      p = piece_at(d, s.len, s.n, base, t, t1);
+      t = p.next;
+    } while (p.kt0 >= p.kt1);
     row0 = p.rows_group * d.unit_rows;
     const long long left = (long long)s.n * d.group - row0;
     rows = left < d.unit_rows ? (int)left : d.unit_rows;

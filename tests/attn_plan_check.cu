@@ -22,7 +22,7 @@ static void check(bool ok, const char* what) {
 
 static void run(const PlanDims& d, const std::vector<int>& len, const std::vector<int>& n, int grid) {
   long long total = 0;
-  for (size_t b = 0; b < len.size(); ++b) total += sequence_tiles(d, len[b], n[b]);
+  for (size_t b = 0; b < len.size(); ++b) total += sequence_length(d, len[b], n[b]);
   const int parts = (int)(total < grid ? total : grid);
   std::map<std::tuple<int, int, int>, int> reached;  // unit -> tiles covered so far
   std::map<std::tuple<int, int, int>, std::pair<int, int>> split;  // divided unit -> first part, pieces announced
@@ -38,9 +38,12 @@ static void run(const PlanDims& d, const std::vector<int>& len, const std::vecto
     size_t b = 0;
     int going_on = 0, starting = 0;
     while (t < t1) {
-      while (t >= base + sequence_tiles(d, len[b], n[b])) base += sequence_tiles(d, len[b], n[b]), ++b;
+      while (t >= base + sequence_length(d, len[b], n[b])) base += sequence_length(d, len[b], n[b]), ++b;
       check(b < len.size(), "sequence in range");
       const Piece p = piece_at(d, len[b], n[b], base, t, t1);
+      check(p.next > t && p.next <= t1, "goes on");
+      t = p.next;
+      if (p.kt0 >= p.kt1) continue;
       check(p.head >= 0 && p.head < d.kv_heads && p.rows_group >= 0 && p.rows_group < row_groups(d, n[b]), "unit in range");
       check(p.kt0 >= 0 && p.kt0 < p.kt1 && p.kt1 <= p.tiles && p.tiles == key_tiles(d, len[b], n[b]), "tiles in range");
       const auto unit = std::make_tuple((int)b, p.head, p.rows_group);
@@ -52,11 +55,10 @@ static void run(const PlanDims& d, const std::vector<int>& len, const std::vecto
         ++pieces[unit];
       } else if (p.kt1 < p.tiles) {
         ++starting;
-        const int last = part_of(total, parts, p.unit_begin + p.tiles - 1);
+        const int last = part_of(total, parts, p.first_tile + p.tiles - 1);
         split[unit] = {c, last - c + 1};
         pieces[unit] = 1;
       }
-      t += p.kt1 - p.kt0;
     }
     check(t == t1 && going_on <= 1 && starting <= 1, "two places a part");
   }
@@ -71,7 +73,7 @@ int main() {
   std::mt19937 g(1);
   auto in = [&](int a, int b) { return (int)(a + g() % (unsigned)(b - a + 1)); };
   for (int trial = 0; trial < 3000; ++trial) {
-    PlanDims d{in(1, 8), in(1, 16), trial % 3 ? 256 : 128, trial % 2 ? 128 : 64};
+    PlanDims d{in(1, 8), in(1, 16), trial % 3 ? 256 : 128, trial % 2 ? 128 : 64, (int)(g() % 6)};
     const int B = in(1, trial % 7 ? 6 : 60);
     std::vector<int> len(B), n(B);
     for (int b = 0; b < B; ++b) {
@@ -81,7 +83,7 @@ int main() {
     run(d, len, n, in(0, 1) ? 152 : in(1, 300));
   }
   // lengths near the limit
-  run(PlanDims{8, 8, 256, 128}, {2147481600 - 300, 2147480000, 5}, {100, 64, 0}, 152);
+  run(PlanDims{8, 8, 256, 128, 3}, {2147481600 - 300, 2147480000, 5}, {100, 64, 0}, 152);
   std::printf("%lld checks, %lld failed\n", checks, failed);
   return failed != 0;
 }
