@@ -27,7 +27,7 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;  // beyond 8 the kernel has to allow it, and the device to have room
 constexpr int kMaxKeys = 48 * 1024;  // keys of one CTA's slice held in shared memory
 
 struct EvictArgs {
@@ -63,8 +63,9 @@ struct alignas(16) Shared {
 };
 
 // KEYS: the slice's keys fit in shared memory; otherwise each pass reads acc
-// and slot_pos again.
-template <bool KEYS>
+// and slot_pos again.  A warp owns `sub` consecutive slots and takes 128 at a
+// time, four to a lane.  VEC: rows of acc and slot_pos are 16-byte aligned.
+template <bool KEYS, bool VEC>
 __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ EvictArgs a) {
   extern __shared__ uint4 s_all[];
   Shared& sh = *reinterpret_cast<Shared*>(s_all);
@@ -73,7 +74,11 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
   const int C = (int)cluster.num_blocks(), r = (int)cluster.block_rank();
   const int problem = blockIdx.x / C, b = problem / a.c.kv_heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) (&sh.hist[0][0])[i] = 0;
+  moe::pdl_wait();
+  moe::pdl_launch_dependents();
   const int n = __ldg(a.lens + b), K = a.budget;
+  const long long recent_from = (long long)__ldg(a.next_pos + b) - a.recent;
   const long long base = (long long)problem * a.slot_cap;
   const float* __restrict__ acc = a.acc + base;
   const int32_t* __restrict__ pos = a.slot_pos + base;
@@ -92,16 +97,57 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     if (r == 0 && threadIdx.x == 0) a.counts[problem] = 0;
     return;
   }
-  const long long recent_from = (long long)__ldg(a.next_pos + b) - a.recent;
-  const int sub = ((n + C * kWarps - 1) / (C * kWarps) + 31) & ~31;  // slots of a warp
+  const int sub = ((n + C * kWarps - 1) / (C * kWarps) + 127) & ~127;
   const int j0 = min((r * kWarps + warp) * sub, n), j1 = min(j0 + sub, n);
   uint32_t* keys = s_keys + warp * sub;
-  for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) (&sh.hist[0][0])[i] = 0;
-  if (KEYS) {
-#pragma unroll 8
-    for (int j = j0 + lane; j < j1; j += 32) keys[j - j0] = rank_key(acc[j], pos[j], a.sinks, recent_from);
+  auto fetch = [&](int j, float4& w, int4& p) {  // slots j .. j + 3; nothing past the end
+    w = make_float4(0.f, 0.f, 0.f, 0.f);
+    p = make_int4(0, 0, 0, 0);
+    if (VEC && j + 4 <= n) {
+      w = *reinterpret_cast<const float4*>(acc + j);
+      p = *reinterpret_cast<const int4*>(pos + j);
+      return;
+    }
+    if (j < n) w.x = acc[j], p.x = pos[j];
+    if (j + 1 < n) w.y = acc[j + 1], p.y = pos[j + 1];
+    if (j + 2 < n) w.z = acc[j + 2], p.z = pos[j + 2];
+    if (j + 3 < n) w.w = acc[j + 3], p.w = pos[j + 3];
+  };
+  auto keys_of = [&](const float4& w, const int4& p) {
+    return make_uint4(rank_key(w.x, p.x, a.sinks, recent_from), rank_key(w.y, p.y, a.sinks, recent_from),
+                      rank_key(w.z, p.z, a.sinks, recent_from), rank_key(w.w, p.w, a.sinks, recent_from));
+  };
+  auto keys_at = [&](int j) {
+    if (KEYS) return *reinterpret_cast<const uint4*>(keys + (j - j0));
+    float4 w;
+    int4 p;
+    fetch(j, w, p);
+    return keys_of(w, p);
+  };
+  // keys into shared memory; what lies below the budget goes to the outputs as it
+  // is (a mover overwrites what is dropped there)
+  constexpr int kAhead = 4;
+  for (int c0 = j0; c0 < j1; c0 += 128 * kAhead) {
+    float4 w[kAhead];
+    int4 p[kAhead];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) fetch(c0 + 128 * q + 4 * lane < j1 ? c0 + 128 * q + 4 * lane : n, w[q], p[q]);
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      const int j = c0 + 128 * q + 4 * lane;
+      if (j >= j1) continue;
+      if (KEYS) *reinterpret_cast<uint4*>(keys + (j - j0)) = keys_of(w[q], p[q]);
+      if (VEC && j + 4 <= K) {
+        *reinterpret_cast<float4*>(a.acc_out + base + j) = w[q];
+        *reinterpret_cast<int4*>(a.pos_out + base + j) = p[q];
+      } else {
+        if (j < K) a.acc_out[base + j] = w[q].x, a.pos_out[base + j] = p[q].x;
+        if (j + 1 < K) a.acc_out[base + j + 1] = w[q].y, a.pos_out[base + j + 1] = p[q].y;
+        if (j + 2 < K) a.acc_out[base + j + 2] = w[q].z, a.pos_out[base + j + 2] = p[q].z;
+        if (j + 3 < K) a.acc_out[base + j + 3] = w[q].w, a.pos_out[base + j + 3] = p[q].w;
+      }
+    }
   }
-  auto key_of = [&](int j) { return KEYS ? keys[j - j0] : rank_key(acc[j], pos[j], a.sinks, recent_from); };
   __syncthreads();
 
   uint32_t prefix = 0, rest = (uint32_t)K;  // slots still to be placed among those with this prefix
@@ -109,26 +155,19 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     const int shift = round == 0 ? 21 : round == 1 ? 10 : 0;
     const int bits = round == 2 ? 10 : 11;
     const uint32_t above = round == 0 ? 0u : 0xFFFFFFFFu << (shift + bits);
-    for (int c0 = j0; c0 < j1; c0 += 32) {
-      const uint32_t k = c0 + lane < j1 ? key_of(c0 + lane) : 0u;
-      const bool in = c0 + lane < j1 && (k & above) == prefix;
-      const uint32_t digit = (k >> shift) & ((1u << bits) - 1u);
-      // many slots share a digit (weights that are 0, protected slots): one
-      // add for a warp that holds a single one
-      const unsigned act = __ballot_sync(0xffffffffu, in);
-      if (act == 0) continue;
-      const int leader = __ffs(act) - 1;
-      const uint32_t first = __shfl_sync(0xffffffffu, digit, leader);
-      if (__all_sync(0xffffffffu, !in || digit == first)) {
-        if (lane == leader) atomicAdd(&sh.hist[round][digit], (unsigned)__popc(act));
-      } else if (in) {
-        atomicAdd(&sh.hist[round][digit], 1u);
-      }
+    for (int j = j0 + 4 * lane; j < j1; j += 128) {
+      const uint4 v = keys_at(j);
+      const uint32_t k[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (j + q < j1 && (k[q] & above) == prefix)
+          atomicAdd(&sh.hist[round][(k[q] >> shift) & ((1u << bits) - 1u)], 1u);
     }
     cluster.sync();
     // thread i: bins kBins - 1 - 2i and the one below, over the cluster
     const int hi = kBins - 1 - 2 * threadIdx.x;
     uint32_t n_hi = 0, n_lo = 0;
+#pragma unroll 4
     for (int q = 0; q < C; ++q) {
       const uint32_t* other = cluster.map_shared_rank(&sh.hist[round][0], q);
       const uint2 v = *reinterpret_cast<const uint2*>(other + hi - 1);
@@ -143,8 +182,9 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     }
     if (lane == 31) sh.warp_sum[warp] = scan;
     __syncthreads();
-    uint32_t lower = 0;
-    for (int w = 0; w < warp; ++w) lower += sh.warp_sum[w];
+    uint32_t lower = lane < warp ? sh.warp_sum[lane] : 0u;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) lower += __shfl_xor_sync(0xffffffffu, lower, d);
     const uint32_t upto = lower + scan, before_hi = upto - n_hi - n_lo, before_lo = upto - n_lo;
     if (before_hi < rest && rest <= before_lo) sh.digit = hi, sh.rest = rest - before_hi;
     else if (before_lo < rest && rest <= upto) sh.digit = hi - 1, sh.rest = rest - before_lo;
@@ -154,12 +194,16 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
   }
   // slots with a key above `prefix` stay, and the first `rest` of those equal to it
   int4 cnt = make_int4(0, 0, 0, 0);
-  for (int j = j0 + lane; j < j1; j += 32) {
-    const uint32_t k = key_of(j);
-    cnt.x += k > prefix;
-    cnt.y += k == prefix;
-    cnt.z += k > prefix && j < K;
-    cnt.w += k == prefix && j < K;
+  for (int j = j0 + 4 * lane; j < j1; j += 128) {
+    const uint4 v = keys_at(j);
+    const uint32_t k[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int gt = j + q < j1 && k[q] > prefix, eq = j + q < j1 && k[q] == prefix;
+      cnt.x += gt;
+      cnt.y += eq;
+      if (j + q < K) cnt.z += gt, cnt.w += eq;
+    }
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) {
@@ -200,90 +244,173 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
   int above = sh.before[warp].x, equal = sh.before[warp].y;
   int32_t* src = a.src + (long long)problem * K;
   int32_t* dst = a.dst + (long long)problem * K;
-  const unsigned below_me = (1u << lane) - 1u;
-  for (int c0 = j0; c0 < j1; c0 += 32) {
-    const int j = c0 + lane;
-    const uint32_t k = j < j1 ? key_of(j) : 0u;
-    const bool gt = j < j1 && k > prefix, eq = j < j1 && k == prefix;
-    const unsigned m_gt = __ballot_sync(0xffffffffu, gt), m_eq = __ballot_sync(0xffffffffu, eq);
-    const int eq_rank = equal + __popc(m_eq & below_me);
-    const bool kept = gt || (eq && eq_rank < ties);
-    const int kept_before = above + __popc(m_gt & below_me) + min(eq_rank, ties);
-    if (j < j1) {
-      if (j < K) {
-        if (kept) {
-          a.acc_out[base + j] = acc[j];
-          a.pos_out[base + j] = pos[j];
-        } else {
-          dst[j - kept_before] = j;
-        }
-      } else if (kept) {
-        src[kept_before - kept_low] = j;
-      }
+  for (int c0 = j0; c0 < j1; c0 += 128) {
+    const int j = c0 + 4 * lane;
+    const uint4 v = j < j1 ? keys_at(j) : make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t k[4] = {v.x, v.y, v.z, v.w};
+    int mine = 0;  // above in the low half, equal in the high
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (j + q < j1) mine += (k[q] > prefix ? 1 : 0) + (k[q] == prefix ? 1 << 16 : 0);
+    int scan = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, scan, d);
+      if (lane >= d) scan += up;
     }
-    above += __popc(m_gt);
-    equal += __popc(m_eq);
+    int gt_before = above + ((scan - mine) & 0xFFFF), eq_before = equal + ((scan - mine) >> 16);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (j + q >= j1) break;
+      const bool gt = k[q] > prefix, eq = k[q] == prefix;
+      const bool kept = gt || (eq && eq_before < ties);
+      const int kept_before = gt_before + min(eq_before, ties);
+      if (j + q < K) {
+        if (!kept) dst[j + q - kept_before] = j + q;
+      } else if (kept) {
+        src[kept_before - kept_low] = j + q;
+      }
+      gt_before += gt;
+      eq_before += eq;
+    }
+    const int all = __shfl_sync(0xffffffffu, scan, 31);
+    above += all & 0xFFFF;
+    equal += all >> 16;
   }
   cluster.sync();  // no CTA leaves while another may still read its shared memory
 }
 
 constexpr int kMoveThreads = 256;
 
-// One group of LANES lanes copies one moved row of k and of v.
+constexpr int kBatch = 128;  // moves a block takes at a time
+constexpr int kMoves = 4;    // moves of a group whose loads are in flight together
+
+// A thread looks up where each move of a batch leads from and to, and moves the
+// weight and position; then a group of LANES lanes copies a row of k and of v.
 template <int LANES>
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const __grid_constant__ EvictArgs a) {
   constexpr int kGroups = kMoveThreads / LANES;
-  const int problem = blockIdx.y, b = problem / a.c.kv_heads, h = problem % a.c.kv_heads;
+  static_assert(kBatch % (kGroups * kMoves) == 0 || kBatch < kGroups * kMoves, "whole rounds");
+  __shared__ long long s_from[kBatch], s_to[kBatch];  // -1: no move
+  moe::pdl_wait();
+  const int problem = blockIdx.y, b = problem / a.c.kv_heads, h = problem - b * a.c.kv_heads;
   const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
   const int n = __ldg(a.counts + problem);
   const long long base = (long long)problem * a.slot_cap;
   const int32_t* src = a.src + (long long)problem * a.budget;
   const int32_t* dst = a.dst + (long long)problem * a.budget;
   const bool mine = lane * 8 < a.c.head_dim;
-  for (int i = blockIdx.x * kGroups + group; i < n; i += gridDim.x * kGroups) {
-    const int s = __ldg(src + i), d = __ldg(dst + i);
-    const long long from = attn::slot_offset(a.c, b, s, h), to = attn::slot_offset(a.c, b, d, h);
-    const bool bad = from < 0 || to < 0;
-    if (!bad && mine) {
-      const uint16_t* k = static_cast<const uint16_t*>(a.c.k) + lane * 8;
-      const uint16_t* v = static_cast<const uint16_t*>(a.c.v) + lane * 8;
-      const uint4 x = *reinterpret_cast<const uint4*>(k + from), y = *reinterpret_cast<const uint4*>(v + from);
-      *reinterpret_cast<uint4*>(const_cast<uint16_t*>(k) + to) = x;
-      *reinterpret_cast<uint4*>(const_cast<uint16_t*>(v) + to) = y;
+  uint16_t* const k = static_cast<uint16_t*>(a.c.k) + lane * 8;
+  uint16_t* const v = static_cast<uint16_t*>(a.c.v) + lane * 8;
+  for (int i0 = blockIdx.x * kBatch; i0 < n; i0 += gridDim.x * kBatch) {
+    __syncthreads();
+    if (threadIdx.x < kBatch) {
+      long long from = -1, to = -1;
+      if (i0 + (int)threadIdx.x < n) {
+        const int s = __ldg(src + i0 + threadIdx.x), d = __ldg(dst + i0 + threadIdx.x);
+        const float w = a.acc[base + s];
+        const int p = a.slot_pos[base + s];
+        from = attn::slot_offset(a.c, b, s, h), to = attn::slot_offset(a.c, b, d, h);
+        const bool good = from >= 0 && to >= 0;
+        if (!good) moe::status_or(a.st, ATTN_DEV_BAD_PAGE), from = -1;
+        a.acc_out[base + d] = good ? w : __uint_as_float(0x7FC00000u);
+        a.pos_out[base + d] = p;
+      }
+      s_from[threadIdx.x] = from;
+      s_to[threadIdx.x] = to;
     }
-    if (lane == 0) {
-      if (bad) moe::status_or(a.st, ATTN_DEV_BAD_PAGE);
-      a.acc_out[base + d] = bad ? __uint_as_float(0x7FC00000u) : a.acc[base + s];
-      a.pos_out[base + d] = a.slot_pos[base + s];
+    __syncthreads();
+#pragma unroll 1
+    for (int m0 = group; m0 < kBatch; m0 += kGroups * kMoves) {
+      long long from[kMoves];
+      uint4 x[kMoves], y[kMoves];
+#pragma unroll
+      for (int m = 0; m < kMoves; ++m) {
+        from[m] = m0 + m * kGroups < kBatch ? s_from[m0 + m * kGroups] : -1;
+        if (mine && from[m] >= 0) {
+          x[m] = *reinterpret_cast<const uint4*>(k + from[m]);
+          y[m] = *reinterpret_cast<const uint4*>(v + from[m]);
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < kMoves; ++m)
+        if (mine && from[m] >= 0) {
+          const long long to = s_to[m0 + m * kGroups];
+          *reinterpret_cast<uint4*>(k + to) = x[m];
+          *reinterpret_cast<uint4*>(v + to) = y[m];
+        }
     }
   }
 }
 
 template <int LANES>
 int launch_move(const EvictArgs& a, int problems, int sms, cudaStream_t st) {
-  constexpr int kGroups = kMoveThreads / LANES;
   // no more blocks than the budget's rows need, nor than a few waves
-  long long per = (a.budget + kGroups - 1) / kGroups, most = (16ll * sms + problems - 1) / problems;
-  move_kernel<LANES><<<dim3((unsigned)(per < most ? per : most), problems), kMoveThreads, 0, st>>>(a);
-  return moe::launch_status();
+  const long long per = ((long long)a.budget + kBatch - 1) / kBatch, most = (16ll * sms + problems - 1) / problems;
+  return moe::launch_pdl(move_kernel<LANES>, dim3((unsigned)(per < most ? per : most), problems), dim3(kMoveThreads), 0, st, a);
 }
 
-template <bool KEYS>
+// Whether clusters of 16 CTAs with `smem` bytes each can run on the current
+// device; asked once per device (for the largest slice).
+template <bool KEYS, bool VEC>
+bool sixteen_fit() {
+  static std::atomic<int> known[moe::kMaxDevices];  // 0: not asked, 1: no, 2: yes
+  const int d = moe::current_device();
+  if (d < 0) return false;
+  int k = known[d].load(std::memory_order_acquire);
+  if (k == 0) {
+    const size_t smem = sizeof(Shared) + (KEYS ? (size_t)kMaxKeys * 4 : 0);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(16);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 16;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    const bool yes =
+        cudaFuncSetAttribute(select_kernel<KEYS, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess &&
+        cudaFuncSetAttribute(select_kernel<KEYS, VEC>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&n, select_kernel<KEYS, VEC>, &cfg) == cudaSuccess && n > 0;
+    if (!yes) (void)cudaGetLastError();
+    known[d].store(k = yes ? 2 : 1, std::memory_order_release);
+  }
+  return k == 2;
+}
+
+template <bool KEYS, bool VEC>
 int launch_select(const EvictArgs& a, int problems, int C, size_t smem, cudaStream_t st) {
   static moe::SmemGrant grant;
-  if (!moe::grant_smem(select_kernel<KEYS>, smem, grant)) return MOE_ERR_CUDA;
+  if (!moe::grant_smem(select_kernel<KEYS, VEC>, smem, grant)) return MOE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(problems * C));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = C;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, select_kernel<KEYS>, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, select_kernel<KEYS, VEC>, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+template <bool VEC>
+int select(const EvictArgs& a, int problems, int sms, cudaStream_t st) {
+  // one CTA a problem, more while SMs are idle and a CTA has more than two rounds of slots
+  int C = 1;
+  while (C < kMaxCluster && problems * C < sms && a.slot_cap > 2 * kThreads * C) C *= 2;
+  auto slots = [&](int c) { return (((a.slot_cap + c * kWarps - 1) / (c * kWarps) + 127) & ~127) * kWarps; };  // of a CTA
+  const bool keys = slots(C) <= kMaxKeys;
+  if (C == 16 && !(keys ? sixteen_fit<true, VEC>() : sixteen_fit<false, VEC>())) C = 8;
+  return slots(C) <= kMaxKeys ? launch_select<true, VEC>(a, problems, C, sizeof(Shared) + (size_t)slots(C) * 4, st)
+                              : launch_select<false, VEC>(a, problems, C, sizeof(Shared), st);
 }
 
 size_t counts_bytes(const attn_cache& c) { return ((size_t)c.batch * c.kv_heads * 4 + 15) & ~(size_t)15; }
@@ -321,12 +448,9 @@ int attn_cache_evict(const attn_cache* cache, const float* acc, const int32_t* s
   const int sms = moe::device_info().sms;
   if (sms <= 0) return MOE_ERR_CUDA;
   const cudaStream_t st = (cudaStream_t)stream;
-  int C = 1;
-  while (C < kMaxCluster && problems * C < sms && slot_cap > 1024 * C) C *= 2;
-  const int sub = ((slot_cap + C * kWarps - 1) / (C * kWarps) + 31) & ~31;
-  const bool keys = sub * kWarps <= kMaxKeys;
-  const int rc = keys ? launch_select<true>(a, (int)problems, C, sizeof(Shared) + (size_t)sub * kWarps * 4, st)
-                      : launch_select<false>(a, (int)problems, C, sizeof(Shared), st);
+  const bool vec = slot_cap % 4 == 0 && moe::aligned16(acc) && moe::aligned16(slot_pos) && moe::aligned16(acc_out) &&
+                   moe::aligned16(slot_pos_out);
+  const int rc = vec ? select<true>(a, (int)problems, sms, st) : select<false>(a, (int)problems, sms, st);
   if (rc) return rc;
   if (a.c.head_dim <= 32) return launch_move<4>(a, (int)problems, sms, st);
   if (a.c.head_dim <= 64) return launch_move<8>(a, (int)problems, sms, st);

@@ -1,11 +1,15 @@
 // Head norm, position rotation and cache append in one pass over q, k and v.
 //
-// Every head row is read once and written once; the arithmetic is about ten
-// flops an element, so the pass is HBM bound.  A row of D elements belongs to
-// a group of 4, 8, 16 or 32 lanes, 8 elements (16 bytes) a lane: loads and
-// stores are whole rows, the mean square is a shuffle sum inside the group.
-// A block takes a few tokens at a time; its threads compute their sines and
-// cosines once into shared memory for all of their heads.
+// Every head row is read once and written once.  HBM bounds the pass for many
+// tokens, but only if a row costs few instructions: at 48 rows of 256 bytes a
+// token, some 200 instructions a row and warp already take as long as the bytes.
+// A row of D elements belongs to a group of 4, 8, 16 or 32 lanes, 8 elements a
+// lane in two blocks of 4: for the half-split rotation the blocks are a block
+// of the first half and the one it is paired with, so no lane needs another's
+// channels; otherwise they lie side by side.  The mean square is a shuffle sum
+// inside the group.  A block takes a few tokens at a time: its threads compute
+// their sines, cosines and cache slots once into shared memory for all of their
+// heads (the sines laid out so that a group's reads meet no bank twice).
 //
 // Angles.  pos * inv_freq loses whole turns' worth of bits in FP32 at far
 // positions.  inv_freq / 2 pi is turned into a 64-bit fixed-point fraction F
@@ -36,170 +40,179 @@ struct RopeArgs {
   int tokens_per_block;
 };
 
-// LANES per row, so that LANES * 8 >= D.  PAIRED: the half-split partner of a
-// lane's 8 channels is another lane's 8 channels (rot / 2 a multiple of 8), a
-// shuffle; otherwise it goes through shared memory.  Interleaved pairs never
-// leave the lane.  A block takes kRound rows of each group at a time with all
-// of their loads in flight; the rows of up to kTokens tokens make up the list.
-constexpr int kRound = 4;
-constexpr int kTokens = 4;
+constexpr int kRound = 4;   // rows of a group whose loads are in flight together
+constexpr int kTokens = 4;  // tokens whose sines and slots are held
 
-template <class E, int LANES, bool PAIRED>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
+// How a row's channels pair up, and where a lane's two blocks of 4 lie.
+enum Pairing {
+  kBlocks,    // half-split, rot % 8 == 0: blocks 4 l and rot / 2 + 4 l; behind rot side by side
+  kInside,    // interleaved: side by side, pairs inside a block
+  kScattered  // half-split, any other rot: side by side, partners by shared memory
+};
+
+template <class E>
+__device__ __forceinline__ float4 up4(const uint2& v) {
+  const float2 a = E::up(v.x), b = E::up(v.y);
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// LANES per row, so that LANES * 8 >= D.
+template <class E, int LANES, Pairing P>
+__global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int kGroups = kThreads / LANES;
   using T = typename E::T;
-  __shared__ float2 s_cs[kTokens][128];  // magnitude * (cos, sin) of the tokens' pairs
+  // pair j of a token at [j % 4][j / 4]: magnitude * (cos, sin)
+  __shared__ float2 s_cs[kTokens][4][33];
   __shared__ int s_pos[kTokens], s_seq[kTokens], s_slot[kTokens];  // slot -1: out of range
-  __shared__ float s_row[PAIRED ? 1 : kGroups][PAIRED ? 1 : LANES * 8 + 4];
+  __shared__ long long s_off[kTokens];                             // of the slot in head 0, -1: bad page
+  __shared__ float s_row[P == kScattered ? kGroups : 1][P == kScattered ? LANES * 8 + 4 : 1];
   const int D = a.c.head_dim, half = a.rot / 2;
   const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
-  const int d0 = lane * 8;
-  const bool mine = d0 < D;
+  // the lane's blocks start at channels c0 and c1
+  int c0 = lane * 8, c1 = c0 + 4;
+  bool turns = false;  // kBlocks: the two blocks are each other's partners
+  if (P == kBlocks) {
+    turns = lane * 4 < half;
+    if (turns) c0 = lane * 4, c1 = half + c0;
+  }
+  const bool mine = lane * 8 < D;
   const int heads = a.q_heads + 2 * a.c.kv_heads;
   const bool norm = a.q_weight != nullptr;
-  // the weights and frequencies are parameters of the model: read before the wait
-  // on the kernel that makes q, k and v
+  const float inv_d = 1.f / (float)D;
+  moe::pdl_wait();
+  moe::pdl_launch_dependents();
   unsigned long long turn = 0;  // inv_freq / 2 pi as a fraction of 2^64
   if (threadIdx.x % 128 < half) {
     const double t = a.inv_freq[threadIdx.x % 128] * 0.15915494309189533577;
     const double f = t - floor(t);
     turn = f < 1.0 ? (unsigned long long)(f * 18446744073709551616.0) : 0ull;
   }
-  uint4 wq = make_uint4(0u, 0u, 0u, 0u), wk = wq;
+  uint2 wt[2][2] = {};  // [q, k][block]
   if (norm && mine) {
-    wq = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q_weight) + d0));
-    wk = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.k_weight) + d0));
+    const T* w[2] = {static_cast<const T*>(a.q_weight), static_cast<const T*>(a.k_weight)};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      wt[i][0] = __ldg(reinterpret_cast<const uint2*>(w[i] + c0));
+      wt[i][1] = __ldg(reinterpret_cast<const uint2*>(w[i] + c1));
+    }
   }
-  moe::pdl_wait();
-  moe::pdl_launch_dependents();
 
   for (int t0 = blockIdx.x * a.tokens_per_block; t0 < a.tokens; t0 += gridDim.x * a.tokens_per_block) {
     const int n_tok = min(a.tokens_per_block, a.tokens - t0);
-    __syncthreads();  // the tokens before are done with the shared arrays
-    if (threadIdx.x < n_tok) {
-      const int t = t0 + threadIdx.x;
-      const int b = attn::sequence_of(a.cu, a.c.batch, t);
-      const attn::Seq s = attn::sequence(a.cu, a.lens, b, a.tokens, (long long)a.c.max_pages * a.c.page_size);
-      const bool ok = s.ok && t >= s.first && t < s.first + s.n;
-      const int slot = s.len + (t - s.first);
-      s_pos[threadIdx.x] = __ldg(a.pos + t);
-      s_seq[threadIdx.x] = b;
-      s_slot[threadIdx.x] = ok ? slot : -1;
-      if (!ok || (a.slot_pos && slot >= a.slot_cap)) moe::status_or(a.st, ATTN_DEV_BAD_LENGTH);
-    }
-    for (int i = threadIdx.x / 128; i < n_tok; i += kThreads / 128) {
-      if (threadIdx.x % 128 < half) {
-        const unsigned long long u = turn * (unsigned long long)(long long)__ldg(a.pos + t0 + i);
-        float sn, cs;
-        sincospif((float)(int32_t)(u >> 32) * 0x1p-31f, &sn, &cs);
-        s_cs[i][threadIdx.x % 128] = make_float2(cs * a.magnitude, sn * a.magnitude);
-      }
-    }
-    __syncthreads();
-    const int rows = n_tok * heads;
-    for (int r0 = 0; r0 < rows; r0 += kRound * kGroups) {  // uniform over the block: the shuffles need whole warps
-      uint4 raw[kRound];
-      int tok[kRound], head[kRound];  // head counted over q, k, v
+    for (int i = 0; i < n_tok; ++i) {
+      const long long t = t0 + i;
+      for (int h0 = 0; h0 < heads; h0 += kRound * kGroups) {  // uniform over the block
+        uint2 raw[kRound][2];
 #pragma unroll
-      for (int i = 0; i < kRound; ++i) {
-        const int r = r0 + i * kGroups + group;
-        tok[i] = r / heads;
-        head[i] = r - tok[i] * heads;
-        raw[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (mine && r < rows) {
-          const long long t = t0 + tok[i];
-          const T* src = head[i] < a.q_heads
-                             ? static_cast<const T*>(a.q) + t * a.q_stride + (long long)head[i] * D
-                         : head[i] < a.q_heads + a.c.kv_heads
-                             ? static_cast<const T*>(a.k) + t * a.k_stride + (long long)(head[i] - a.q_heads) * D
-                             : static_cast<const T*>(a.v) + t * a.v_stride +
-                                   (long long)(head[i] - a.q_heads - a.c.kv_heads) * D;
-          raw[i] = *reinterpret_cast<const uint4*>(src + d0);
+        for (int k = 0; k < kRound; ++k) {
+          const int h = h0 + k * kGroups + group;
+          raw[k][0] = raw[k][1] = make_uint2(0u, 0u);
+          if (mine && h < heads) {
+            const T* src = h < a.q_heads ? static_cast<const T*>(a.q) + t * a.q_stride + h * D
+                           : h < a.q_heads + a.c.kv_heads
+                               ? static_cast<const T*>(a.k) + t * a.k_stride + (h - a.q_heads) * D
+                               : static_cast<const T*>(a.v) + t * a.v_stride + (h - a.q_heads - a.c.kv_heads) * D;
+            raw[k][0] = *reinterpret_cast<const uint2*>(src + c0);
+            raw[k][1] = *reinterpret_cast<const uint2*>(src + c1);
+          }
         }
-      }
-#pragma unroll
-      for (int i = 0; i < kRound; ++i) {
-        const bool live = mine && r0 + i * kGroups + group < rows;
-        const int kind = head[i] < a.q_heads ? 0 : head[i] < a.q_heads + a.c.kv_heads ? 1 : 2;  // q, k, v
-        const float2* cs_of = s_cs[live ? tok[i] : 0];
-        float x[8];
-        attn::unpack8<E>(raw[i], x);
-        if (norm) {
-          float ss = 0.f, wt[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-          for (int m = LANES / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-          const float r = rsqrtf(ss / (float)D + a.eps);
-          attn::unpack8<E>(kind == 0 ? wq : wk, wt);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= r * wt[e];
-        }
-        float y[8];
-        if (a.interleaved) {
-#pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const int j = (d0 + e) / 2;
+        if (i == 0 && h0 == 0) {  // the tokens' set-up, under the first rows' loads
+          __syncthreads();        // the tokens before are done with the shared arrays
+          if (threadIdx.x < n_tok) {
+            const int tt = t0 + threadIdx.x;
+            const int b = attn::sequence_of(a.cu, a.c.batch, tt);
+            const attn::Seq s = attn::sequence(a.cu, a.lens, b, a.tokens, (long long)a.c.max_pages * a.c.page_size);
+            const bool ok = s.ok && tt >= s.first && tt < s.first + s.n;
+            const int slot = s.len + (tt - s.first);
+            s_pos[threadIdx.x] = __ldg(a.pos + tt);
+            s_seq[threadIdx.x] = b;
+            s_slot[threadIdx.x] = ok ? slot : -1;
+            s_off[threadIdx.x] = ok ? attn::slot_offset(a.c, b, slot, 0) : -1;
+            if (!ok || (a.slot_pos && slot >= a.slot_cap)) moe::status_or(a.st, ATTN_DEV_BAD_LENGTH);
+            if (ok && s_off[threadIdx.x] < 0) moe::status_or(a.st, ATTN_DEV_BAD_PAGE);
+          }
+          for (int m = threadIdx.x / 128; m < n_tok; m += kThreads / 128) {
+            const int j = threadIdx.x % 128;
             if (j < half) {
-              const float2 cs = cs_of[j];
-              y[e] = x[e] * cs.x - x[e + 1] * cs.y;
-              y[e + 1] = x[e] * cs.y + x[e + 1] * cs.x;
-            } else {
-              y[e] = x[e];
-              y[e + 1] = x[e + 1];
+              const unsigned long long u = turn * (unsigned long long)(long long)__ldg(a.pos + t0 + m);
+              float sn, cs;
+              sincospif((float)(int32_t)(u >> 32) * 0x1p-31f, &sn, &cs);
+              s_cs[m][j & 3][j >> 2] = make_float2(cs * a.magnitude, sn * a.magnitude);
             }
           }
-        } else {
-          float p[8];  // the other channel of each pair
-          if (PAIRED) {
-            const int other = d0 < half ? lane + half / 8 : lane - half / 8;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) p[e] = __shfl_sync(0xffffffffu, x[e], other, LANES);
-          } else {
-            __syncwarp();
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s_row[group][d0 + e] = x[e];
-            __syncwarp();
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int d = d0 + e;
-              p[e] = d < a.rot ? s_row[group][d < half ? d + half : d - half] : 0.f;
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int d = d0 + e;
-            if (d < half) {
-              const float2 cs = cs_of[d];
-              y[e] = x[e] * cs.x - p[e] * cs.y;
-            } else if (d < a.rot) {
-              const float2 cs = cs_of[d - half];
-              y[e] = p[e] * cs.y + x[e] * cs.x;
-            } else {
-              y[e] = x[e];
-            }
-          }
+          __syncthreads();
         }
-        if (!live) continue;
-        const int slot = s_slot[tok[i]], b = s_seq[tok[i]];
-        if (kind == 0) {
-          if (slot < 0) {
+        const int slot = s_slot[i];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(0x7FC00000u);
+        for (int k = 0; k < kRound; ++k) {
+          const int h = h0 + k * kGroups + group;
+          if (h0 + k * kGroups >= heads) break;  // uniform
+          const bool live = mine && h < heads;
+          const int kind = h < a.q_heads ? 0 : h < a.q_heads + a.c.kv_heads ? 1 : 2;  // q, k, v
+          float4 x = up4<E>(raw[k][0]), z = up4<E>(raw[k][1]);
+          if (norm) {
+            float ss = x.x * x.x + x.y * x.y + x.z * x.z + x.w * x.w + z.x * z.x + z.y * z.y + z.z * z.z + z.w * z.w;
+#pragma unroll
+            for (int m = LANES / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+            const float r = rsqrtf(ss * inv_d + a.eps);
+            const float4 w0 = up4<E>(kind == 0 ? wt[0][0] : wt[1][0]), w1 = up4<E>(kind == 0 ? wt[0][1] : wt[1][1]);
+            x.x *= r * w0.x, x.y *= r * w0.y, x.z *= r * w0.z, x.w *= r * w0.w;
+            z.x *= r * w1.x, z.y *= r * w1.y, z.z *= r * w1.z, z.w *= r * w1.w;
           }
-          *reinterpret_cast<uint4*>(static_cast<T*>(a.q_out) + ((long long)(t0 + tok[i]) * a.q_heads + head[i]) * D + d0) =
-              attn::pack8<E>(y);
-        } else if (slot >= 0) {
-          const int hk = head[i] - a.q_heads - (kind == 2 ? a.c.kv_heads : 0);
-          const long long off = attn::slot_offset(a.c, b, slot, hk);
-          if (off < 0) {
-            moe::status_or(a.st, ATTN_DEV_BAD_PAGE);
+          if (P == kBlocks) {
+            if (turns) {
+              const float2 e0 = s_cs[i][0][lane], e1 = s_cs[i][1][lane], e2 = s_cs[i][2][lane], e3 = s_cs[i][3][lane];
+              const float4 p = x;
+              x.x = p.x * e0.x - z.x * e0.y, z.x = p.x * e0.y + z.x * e0.x;
+              x.y = p.y * e1.x - z.y * e1.y, z.y = p.y * e1.y + z.y * e1.x;
+              x.z = p.z * e2.x - z.z * e2.y, z.z = p.z * e2.y + z.z * e2.x;
+              x.w = p.w * e3.x - z.w * e3.y, z.w = p.w * e3.y + z.w * e3.x;
+            }
+          } else if (P == kInside) {
+            auto turn2 = [&](float& u, float& v, int j) {
+              if (j >= half) return;
+              const float2 e = s_cs[i][j & 3][j >> 2];
+              const float p = u;
+              u = p * e.x - v * e.y, v = p * e.y + v * e.x;
+            };
+            turn2(x.x, x.y, lane * 4), turn2(x.z, x.w, lane * 4 + 1);
+            turn2(z.x, z.y, lane * 4 + 2), turn2(z.z, z.w, lane * 4 + 3);
           } else {
-            T* dst = static_cast<T*>(kind == 1 ? a.c.k : a.c.v) + off + d0;
-            *reinterpret_cast<uint4*>(dst) = kind == 1 ? attn::pack8<E>(y) : raw[i];
-            if (kind == 1 && lane == 0 && a.slot_pos && slot < a.slot_cap)
-              a.slot_pos[((long long)b * a.c.kv_heads + hk) * a.slot_cap + slot] = s_pos[tok[i]];
+            float* row = s_row[group];
+            __syncwarp();
+            *reinterpret_cast<float4*>(row + c0) = x;
+            *reinterpret_cast<float4*>(row + c1) = z;
+            __syncwarp();
+            auto turn1 = [&](float u, int d) {
+              if (d >= a.rot) return u;
+              const bool low = d < half;
+              const int j = low ? d : d - half;
+              const float2 e = s_cs[i][j & 3][j >> 2];
+              const float p = row[low ? d + half : j];
+              return low ? u * e.x - p * e.y : p * e.y + u * e.x;
+            };
+            x = make_float4(turn1(x.x, c0), turn1(x.y, c0 + 1), turn1(x.z, c0 + 2), turn1(x.w, c0 + 3));
+            z = make_float4(turn1(z.x, c1), turn1(z.y, c1 + 1), turn1(z.z, c1 + 2), turn1(z.w, c1 + 3));
           }
+          if (!live) continue;
+          if (slot < 0) {
+            const float nan = __uint_as_float(0x7FC00000u);
+            x = z = make_float4(nan, nan, nan, nan);
+          }
+          uint2 o0 = make_uint2(E::down(x.x, x.y), E::down(x.z, x.w)), o1 = make_uint2(E::down(z.x, z.y), E::down(z.z, z.w));
+          T* dst;
+          if (kind == 0) {
+            dst = static_cast<T*>(a.q_out) + (t * a.q_heads + h) * D;
+          } else {
+            if (s_off[i] < 0) continue;
+            const int hk = h - a.q_heads - (kind == 2 ? a.c.kv_heads : 0);
+            dst = static_cast<T*>(kind == 1 ? a.c.k : a.c.v) + s_off[i] + hk * a.c.head_stride;
+            if (kind == 2) o0 = raw[k][0], o1 = raw[k][1];
+            else if (lane == 0 && a.slot_pos && slot < a.slot_cap)
+              a.slot_pos[((long long)s_seq[i] * a.c.kv_heads + hk) * a.slot_cap + slot] = s_pos[i];
+          }
+          *reinterpret_cast<uint2*>(dst + c0) = o0;
+          *reinterpret_cast<uint2*>(dst + c1) = o1;
         }
       }
     }
@@ -208,15 +221,16 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
 
 template <class E, int LANES>
 int launch(RopeArgs& a, cudaStream_t st) {
-  const bool paired = a.interleaved || (a.rot / 2) % 8 == 0;
   const int sms = moe::device_info().sms;
   if (sms <= 0) return MOE_ERR_CUDA;
   // several tokens a block share its set-up, once there are enough to fill the GPU
   a.tokens_per_block = a.tokens >= 16 * sms ? kTokens : 1;
   const int blocks = (a.tokens + a.tokens_per_block - 1) / a.tokens_per_block;
   const int grid = blocks < 8 * sms ? blocks : 8 * sms;
-  return paired ? moe::launch_pdl(qk_norm_rope_kernel<E, LANES, true>, dim3(grid), dim3(kThreads), 0, st, a)
-                : moe::launch_pdl(qk_norm_rope_kernel<E, LANES, false>, dim3(grid), dim3(kThreads), 0, st, a);
+  const auto kernel = a.interleaved      ? qk_norm_rope_kernel<E, LANES, kInside>
+                      : a.rot % 8 == 0 ? qk_norm_rope_kernel<E, LANES, kBlocks>
+                                       : qk_norm_rope_kernel<E, LANES, kScattered>;
+  return moe::launch_pdl(kernel, dim3(grid), dim3(kThreads), 0, st, a);
 }
 
 template <class E>
