@@ -40,8 +40,8 @@ struct RopeArgs {
   int tokens_per_block;
 };
 
-constexpr int kRound = 4;   // rows of a group whose loads are in flight together
-constexpr int kTokens = 4;  // tokens whose sines and slots are held
+constexpr int kRound = 2;   // rows of q of a group whose loads are in flight together, beside one of k or v
+constexpr int kTokens = 8;  // tokens whose sines and slots are held
 
 // How a row's channels pair up, and where a lane's two blocks of 4 lie.
 enum Pairing {
@@ -76,7 +76,6 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const __grid_
     if (turns) c0 = lane * 4, c1 = half + c0;
   }
   const bool mine = lane * 8 < D;
-  const int heads = a.q_heads + 2 * a.c.kv_heads;
   const bool norm = a.q_weight != nullptr;
   const float inv_d = 1.f / (float)D;
   moe::pdl_wait();
@@ -99,121 +98,144 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const __grid_
 
   for (int t0 = blockIdx.x * a.tokens_per_block; t0 < a.tokens; t0 += gridDim.x * a.tokens_per_block) {
     const int n_tok = min(a.tokens_per_block, a.tokens - t0);
+    // The first rows' loads leave before the tokens' set-up.
+    auto load = [&](const T* src, bool there, uint2 (&raw)[2]) {
+      raw[0] = raw[1] = make_uint2(0u, 0u);
+      if (there) {
+        raw[0] = *reinterpret_cast<const uint2*>(src + c0);
+        raw[1] = *reinterpret_cast<const uint2*>(src + c1);
+      }
+    };
+    // row `h` of the 2 kv_heads rows of k and v
+    auto load_kv = [&](long long t, int h, uint2 (&raw)[2]) {
+      const bool is_k = h < a.c.kv_heads;
+      load(is_k ? static_cast<const T*>(a.k) + t * a.k_stride + h * D
+                : static_cast<const T*>(a.v) + t * a.v_stride + (h - a.c.kv_heads) * D,
+           mine && h < 2 * a.c.kv_heads, raw);
+    };
+    auto load_q = [&](long long t, int h, uint2 (&raw)[kRound][2]) {
+#pragma unroll
+      for (int k = 0; k < kRound; ++k)
+        load(static_cast<const T*>(a.q) + t * a.q_stride + (h + k * kGroups) * D, mine && h + k * kGroups < a.q_heads, raw[k]);
+    };
+    uint2 raw_q[kRound][2], raw_kv[2];
+    load_q(t0, group, raw_q);
+    load_kv(t0, group, raw_kv);
+    __syncthreads();  // the tokens before are done with the shared arrays
+    if (threadIdx.x < n_tok) {
+      const int tt = t0 + threadIdx.x;
+      const int b = attn::sequence_of(a.cu, a.c.batch, tt);
+      const attn::Seq s = attn::sequence(a.cu, a.lens, b, a.tokens, (long long)a.c.max_pages * a.c.page_size);
+      const bool ok = s.ok && tt >= s.first && tt < s.first + s.n;
+      const int slot = s.len + (tt - s.first);
+      s_pos[threadIdx.x] = __ldg(a.pos + tt);
+      s_seq[threadIdx.x] = b;
+      s_slot[threadIdx.x] = ok ? slot : -1;
+      s_off[threadIdx.x] = ok ? attn::slot_offset(a.c, b, slot, 0) : -1;
+      if (!ok || (a.slot_pos && slot >= a.slot_cap)) moe::status_or(a.st, ATTN_DEV_BAD_LENGTH);
+      if (ok && s_off[threadIdx.x] < 0) moe::status_or(a.st, ATTN_DEV_BAD_PAGE);
+    }
+    for (int m = threadIdx.x / 128; m < n_tok; m += kThreads / 128) {
+      const int j = threadIdx.x % 128;
+      if (j < half) {
+        const unsigned long long u = turn * (unsigned long long)(long long)__ldg(a.pos + t0 + m);
+        float sn, cs;
+        sincospif((float)(int32_t)(u >> 32) * 0x1p-31f, &sn, &cs);
+        s_cs[m][j & 3][j >> 2] = make_float2(cs * a.magnitude, sn * a.magnitude);
+      }
+    }
+    __syncthreads();
     for (int i = 0; i < n_tok; ++i) {
       const long long t = t0 + i;
-      for (int h0 = 0; h0 < heads; h0 += kRound * kGroups) {  // uniform over the block
-        uint2 raw[kRound][2];
+      const int slot = s_slot[i];
+      // a lane's four pairs are the same in every head
+      float2 e[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int j = lane * 4 + q;
+        e[q] = P != kScattered && j < half ? s_cs[i][q][lane] : make_float2(1.f, 0.f);
+      }
+      // norm and rotation of one row; w: its weights.  Whole warps come here.
+      auto turned = [&](const uint2 (&raw)[2], const uint2 (&w)[2], uint2 (&out)[2]) {
+        float4 x = up4<E>(raw[0]), z = up4<E>(raw[1]);
+        if (norm) {
+          float ss = x.x * x.x + x.y * x.y + x.z * x.z + x.w * x.w + z.x * z.x + z.y * z.y + z.z * z.z + z.w * z.w;
+#pragma unroll
+          for (int m = LANES / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+          const float r = rsqrtf(ss * inv_d + a.eps);
+          const float4 w0 = up4<E>(w[0]), w1 = up4<E>(w[1]);
+          x.x *= r * w0.x, x.y *= r * w0.y, x.z *= r * w0.z, x.w *= r * w0.w;
+          z.x *= r * w1.x, z.y *= r * w1.y, z.z *= r * w1.z, z.w *= r * w1.w;
+        }
+        auto turn2 = [](float& u, float& v, const float2& c) {
+          const float p = u;
+          u = p * c.x - v * c.y, v = p * c.y + v * c.x;
+        };
+        if (P == kBlocks) {
+          if (turns) turn2(x.x, z.x, e[0]), turn2(x.y, z.y, e[1]), turn2(x.z, z.z, e[2]), turn2(x.w, z.w, e[3]);
+        } else if (P == kInside) {
+          const int j = lane * 4;
+          if (j < half) turn2(x.x, x.y, e[0]);
+          if (j + 1 < half) turn2(x.z, x.w, e[1]);
+          if (j + 2 < half) turn2(z.x, z.y, e[2]);
+          if (j + 3 < half) turn2(z.z, z.w, e[3]);
+        } else {
+          float* row = s_row[group];
+          __syncwarp();
+          *reinterpret_cast<float4*>(row + c0) = x;
+          *reinterpret_cast<float4*>(row + c1) = z;
+          __syncwarp();
+          auto turn1 = [&](float u, int d) {
+            if (d >= a.rot) return u;
+            const bool low = d < half;
+            const int j = low ? d : d - half;
+            const float2 c = s_cs[i][j & 3][j >> 2];
+            const float p = row[low ? d + half : j];
+            return low ? u * c.x - p * c.y : p * c.y + u * c.x;
+          };
+          x = make_float4(turn1(x.x, c0), turn1(x.y, c0 + 1), turn1(x.z, c0 + 2), turn1(x.w, c0 + 3));
+          z = make_float4(turn1(z.x, c1), turn1(z.y, c1 + 1), turn1(z.z, c1 + 2), turn1(z.w, c1 + 3));
+        }
+        out[0] = make_uint2(E::down(x.x, x.y), E::down(x.z, x.w));
+        out[1] = make_uint2(E::down(z.x, z.y), E::down(z.z, z.w));
+      };
+      if (i > 0) {
+        load_q(t, group, raw_q);
+        load_kv(t, group, raw_kv);
+      }
+      for (int h0 = 0; h0 < a.q_heads; h0 += kRound * kGroups) {  // uniform over the block
+        if (h0 > 0) load_q(t, h0 + group, raw_q);
 #pragma unroll
         for (int k = 0; k < kRound; ++k) {
+          if (h0 + k * kGroups >= a.q_heads) break;  // uniform
           const int h = h0 + k * kGroups + group;
-          raw[k][0] = raw[k][1] = make_uint2(0u, 0u);
-          if (mine && h < heads) {
-            const T* src = h < a.q_heads ? static_cast<const T*>(a.q) + t * a.q_stride + h * D
-                           : h < a.q_heads + a.c.kv_heads
-                               ? static_cast<const T*>(a.k) + t * a.k_stride + (h - a.q_heads) * D
-                               : static_cast<const T*>(a.v) + t * a.v_stride + (h - a.q_heads - a.c.kv_heads) * D;
-            raw[k][0] = *reinterpret_cast<const uint2*>(src + c0);
-            raw[k][1] = *reinterpret_cast<const uint2*>(src + c1);
-          }
+          uint2 out[2];
+          turned(raw_q[k], wt[0], out);
+          if (!mine || h >= a.q_heads) continue;
+          if (slot < 0) out[0].x = out[0].y = out[1].x = out[1].y = E::down(__uint_as_float(0x7FC00000u), __uint_as_float(0x7FC00000u));
+          T* dst = static_cast<T*>(a.q_out) + (t * a.q_heads + h) * D;
+          *reinterpret_cast<uint2*>(dst + c0) = out[0];
+          *reinterpret_cast<uint2*>(dst + c1) = out[1];
         }
-        if (i == 0 && h0 == 0) {  // the tokens' set-up, under the first rows' loads
-          __syncthreads();        // the tokens before are done with the shared arrays
-          if (threadIdx.x < n_tok) {
-            const int tt = t0 + threadIdx.x;
-            const int b = attn::sequence_of(a.cu, a.c.batch, tt);
-            const attn::Seq s = attn::sequence(a.cu, a.lens, b, a.tokens, (long long)a.c.max_pages * a.c.page_size);
-            const bool ok = s.ok && tt >= s.first && tt < s.first + s.n;
-            const int slot = s.len + (tt - s.first);
-            s_pos[threadIdx.x] = __ldg(a.pos + tt);
-            s_seq[threadIdx.x] = b;
-            s_slot[threadIdx.x] = ok ? slot : -1;
-            s_off[threadIdx.x] = ok ? attn::slot_offset(a.c, b, slot, 0) : -1;
-            if (!ok || (a.slot_pos && slot >= a.slot_cap)) moe::status_or(a.st, ATTN_DEV_BAD_LENGTH);
-            if (ok && s_off[threadIdx.x] < 0) moe::status_or(a.st, ATTN_DEV_BAD_PAGE);
-          }
-          for (int m = threadIdx.x / 128; m < n_tok; m += kThreads / 128) {
-            const int j = threadIdx.x % 128;
-            if (j < half) {
-              const unsigned long long u = turn * (unsigned long long)(long long)__ldg(a.pos + t0 + m);
-              float sn, cs;
-              sincospif((float)(int32_t)(u >> 32) * 0x1p-31f, &sn, &cs);
-              s_cs[m][j & 3][j >> 2] = make_float2(cs * a.magnitude, sn * a.magnitude);
-            }
-          }
-          __syncthreads();
+      }
+      const long long off = s_off[i];
+      for (int h0 = 0; h0 < 2 * a.c.kv_heads; h0 += kGroups) {
+        const int h = h0 + group;
+        if (h0 > 0) load_kv(t, h, raw_kv);
+        const bool is_k = h < a.c.kv_heads;
+        uint2 out[2] = {raw_kv[0], raw_kv[1]};
+        if (h0 < a.c.kv_heads) {  // uniform: rows of k among them
+          uint2 of_k[2];
+          turned(raw_kv, wt[1], of_k);
+          if (is_k) out[0] = of_k[0], out[1] = of_k[1];
         }
-        const int slot = s_slot[i];
-#pragma unroll
-        for (int k = 0; k < kRound; ++k) {
-          const int h = h0 + k * kGroups + group;
-          if (h0 + k * kGroups >= heads) break;  // uniform
-          const bool live = mine && h < heads;
-          const int kind = h < a.q_heads ? 0 : h < a.q_heads + a.c.kv_heads ? 1 : 2;  // q, k, v
-          float4 x = up4<E>(raw[k][0]), z = up4<E>(raw[k][1]);
-          if (norm) {
-            float ss = x.x * x.x + x.y * x.y + x.z * x.z + x.w * x.w + z.x * z.x + z.y * z.y + z.z * z.z + z.w * z.w;
-#pragma unroll
-            for (int m = LANES / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-            const float r = rsqrtf(ss * inv_d + a.eps);
-            const float4 w0 = up4<E>(kind == 0 ? wt[0][0] : wt[1][0]), w1 = up4<E>(kind == 0 ? wt[0][1] : wt[1][1]);
-            x.x *= r * w0.x, x.y *= r * w0.y, x.z *= r * w0.z, x.w *= r * w0.w;
-            z.x *= r * w1.x, z.y *= r * w1.y, z.z *= r * w1.z, z.w *= r * w1.w;
-          }
-          if (P == kBlocks) {
-            if (turns) {
-              const float2 e0 = s_cs[i][0][lane], e1 = s_cs[i][1][lane], e2 = s_cs[i][2][lane], e3 = s_cs[i][3][lane];
-              const float4 p = x;
-              x.x = p.x * e0.x - z.x * e0.y, z.x = p.x * e0.y + z.x * e0.x;
-              x.y = p.y * e1.x - z.y * e1.y, z.y = p.y * e1.y + z.y * e1.x;
-              x.z = p.z * e2.x - z.z * e2.y, z.z = p.z * e2.y + z.z * e2.x;
-              x.w = p.w * e3.x - z.w * e3.y, z.w = p.w * e3.y + z.w * e3.x;
-            }
-          } else if (P == kInside) {
-            auto turn2 = [&](float& u, float& v, int j) {
-              if (j >= half) return;
-              const float2 e = s_cs[i][j & 3][j >> 2];
-              const float p = u;
-              u = p * e.x - v * e.y, v = p * e.y + v * e.x;
-            };
-            turn2(x.x, x.y, lane * 4), turn2(x.z, x.w, lane * 4 + 1);
-            turn2(z.x, z.y, lane * 4 + 2), turn2(z.z, z.w, lane * 4 + 3);
-          } else {
-            float* row = s_row[group];
-            __syncwarp();
-            *reinterpret_cast<float4*>(row + c0) = x;
-            *reinterpret_cast<float4*>(row + c1) = z;
-            __syncwarp();
-            auto turn1 = [&](float u, int d) {
-              if (d >= a.rot) return u;
-              const bool low = d < half;
-              const int j = low ? d : d - half;
-              const float2 e = s_cs[i][j & 3][j >> 2];
-              const float p = row[low ? d + half : j];
-              return low ? u * e.x - p * e.y : p * e.y + u * e.x;
-            };
-            x = make_float4(turn1(x.x, c0), turn1(x.y, c0 + 1), turn1(x.z, c0 + 2), turn1(x.w, c0 + 3));
-            z = make_float4(turn1(z.x, c1), turn1(z.y, c1 + 1), turn1(z.z, c1 + 2), turn1(z.w, c1 + 3));
-          }
-          if (!live) continue;
-          if (slot < 0) {
-            const float nan = __uint_as_float(0x7FC00000u);
-            x = z = make_float4(nan, nan, nan, nan);
-          }
-          uint2 o0 = make_uint2(E::down(x.x, x.y), E::down(x.z, x.w)), o1 = make_uint2(E::down(z.x, z.y), E::down(z.z, z.w));
-          T* dst;
-          if (kind == 0) {
-            dst = static_cast<T*>(a.q_out) + (t * a.q_heads + h) * D;
-          } else {
-            if (s_off[i] < 0) continue;
-            const int hk = h - a.q_heads - (kind == 2 ? a.c.kv_heads : 0);
-            dst = static_cast<T*>(kind == 1 ? a.c.k : a.c.v) + s_off[i] + hk * a.c.head_stride;
-            if (kind == 2) o0 = raw[k][0], o1 = raw[k][1];
-            else if (lane == 0 && a.slot_pos && slot < a.slot_cap)
-              a.slot_pos[((long long)s_seq[i] * a.c.kv_heads + hk) * a.slot_cap + slot] = s_pos[i];
-          }
-          *reinterpret_cast<uint2*>(dst + c0) = o0;
-          *reinterpret_cast<uint2*>(dst + c1) = o1;
-        }
+        if (!mine || h >= 2 * a.c.kv_heads || off < 0) continue;
+        const int hk = is_k ? h : h - a.c.kv_heads;
+        T* dst = static_cast<T*>(is_k ? a.c.k : a.c.v) + off + hk * a.c.head_stride;
+        *reinterpret_cast<uint2*>(dst + c0) = out[0];
+        *reinterpret_cast<uint2*>(dst + c1) = out[1];
+        if (is_k && lane == 0 && a.slot_pos && slot < a.slot_cap)
+          a.slot_pos[((long long)s_seq[i] * a.c.kv_heads + hk) * a.slot_cap + slot] = s_pos[i];
       }
     }
   }
@@ -223,10 +245,10 @@ template <class E, int LANES>
 int launch(RopeArgs& a, cudaStream_t st) {
   const int sms = moe::device_info().sms;
   if (sms <= 0) return MOE_ERR_CUDA;
-  // several tokens a block share its set-up, once there are enough to fill the GPU
-  a.tokens_per_block = a.tokens >= 16 * sms ? kTokens : 1;
-  const int blocks = (a.tokens + a.tokens_per_block - 1) / a.tokens_per_block;
-  const int grid = blocks < 8 * sms ? blocks : 8 * sms;
+  // tokens share a block's set-up as far as every SM still gets its four blocks twice
+  const int share = a.tokens / (8 * sms);
+  a.tokens_per_block = share < 1 ? 1 : share < kTokens ? share : kTokens;
+  const int grid = (a.tokens + a.tokens_per_block - 1) / a.tokens_per_block;
   const auto kernel = a.interleaved      ? qk_norm_rope_kernel<E, LANES, kInside>
                       : a.rot % 8 == 0 ? qk_norm_rope_kernel<E, LANES, kBlocks>
                                        : qk_norm_rope_kernel<E, LANES, kScattered>;
