@@ -4,11 +4,16 @@
 // a row is one token in flight and query head of the KV head's group.  Its
 // work is the tiles of keys it looks at, and `cost` tiles' time for fetching
 // the rows and writing the result, which stand before its first tile.  All
-// units, in the order of sequence, head, row group, form one line that is cut
-// into `parts` nearly equal ranges, one per CTA: every CTA gets the same share
-// however ragged the batch is, and a long sequence is spread over as many CTAs
-// as its share of the work.  A unit that a cut divides is joined from its
-// pieces afterwards.
+// units form one line that is cut into `parts` nearly equal ranges, one per
+// CTA: every CTA gets the same share however ragged the batch is, and a long
+// sequence is spread over as many CTAs as its share of the work.  A unit that a
+// cut divides is joined from its pieces afterwards.
+//
+// The order on the line is row group (level), sequence, head.  The levels of a
+// batch of like sequences are equally long, so the CTAs that take the second row
+// group of some keys run beside those that take the first, and find the keys in
+// L2: with the row groups of a head side by side instead, 8 sequences of 16384
+// slots and 504 rows read K and V from HBM twice (134 us against 108).
 #pragma once
 
 #ifdef __CUDACC__
@@ -36,9 +41,9 @@ ATTN_HD int row_groups(const PlanDims& d, int n) {
   return (int)quotient((long long)n * d.group + d.unit_rows - 1, d.unit_rows);
 }
 ATTN_HD int key_tiles(const PlanDims& d, int len, int n) { return (int)quotient((long long)len + n + d.tile - 1, d.tile); }
-// Places of all units of a sequence.
-ATTN_HD long long sequence_length(const PlanDims& d, int len, int n) {
-  return n <= 0 ? 0 : (long long)d.kv_heads * row_groups(d, n) * (d.cost + key_tiles(d, len, n));
+// Places of the units of a sequence on a level.
+ATTN_HD long long sequence_length(const PlanDims& d, int len, int n, int level) {
+  return n <= 0 || row_groups(d, n) <= level ? 0 : (long long)d.kv_heads * (d.cost + key_tiles(d, len, n));
 }
 
 // A line longer than this is refused (the products below stay within 64 bits).
@@ -51,14 +56,14 @@ ATTN_HD int part_of(long long total, int parts, long long t) { return (int)quoti
 // One piece of a unit: key tiles [kt0, kt1) of its `tiles` (none, if the part
 // holds only places before the first tile).
 struct Piece {
-  int head, rows_group;  // within the sequence
+  int head;
   int kt0, kt1, tiles;
   long long first_tile;  // the place of the unit's tile 0
   long long next;        // where the part goes on
 };
 
 // The piece that starts at place `t` of the line and ends before `end`, where
-// the sequence's first place is `base`.
+// the sequence's first place on the level is `base`.
 ATTN_HD Piece piece_at(const PlanDims& d, int len, int n, long long base, long long t, long long end) {
   Piece p;
   p.tiles = key_tiles(d, len, n);
@@ -68,9 +73,7 @@ ATTN_HD Piece piece_at(const PlanDims& d, int len, int n, long long base, long l
   p.kt0 = from < 0 ? 0 : (int)from;
   p.kt1 = to < 0 ? 0 : to < p.tiles ? (int)to : p.tiles;
   p.next = to < p.tiles ? end : p.first_tile + p.tiles;
-  const int groups = row_groups(d, n);
-  p.head = (int)(u / groups);
-  p.rows_group = (int)(u % groups);
+  p.head = (int)u;
   return p;
 }
 

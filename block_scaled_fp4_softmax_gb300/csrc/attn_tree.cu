@@ -41,7 +41,11 @@ using namespace moe::tc;
 
 namespace {
 
-constexpr int kThreads = 320;  // warps 0-3, 4-7: softmax of streams 0, 1; 8: TMA; 9: MMA
+// Warps 0-3, 4-7: softmax of streams 0, 1; 8: TMA; 9: MMA (10, 11 fill up the
+// warpgroup, whose registers go to the other two: they hold a row of S each, and
+// spilling a few of them cost 10% of the whole kernel's time).
+constexpr int kThreads = 384;
+constexpr int kRegsSoftmax = 208;
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
 constexpr float kNaN = __builtin_nanf("");
 
@@ -84,6 +88,8 @@ struct Cfg {
   // fetching the rows and writing the result: some 8000 cycles, of which a tile
   // takes 2700 (1400 at half the width)
   static constexpr int UNIT_COST = DP == 64 ? 5 : 3;
+  static constexpr int REGS_OTHER = STREAMS == 2 ? 88 : 144;  // of a warpgroup that runs no softmax
+  static_assert(STREAMS * kRegsSoftmax + (3 - STREAMS) * REGS_OTHER <= 3 * 168, "168 registers a thread at launch");
   static_assert(O_COL + STREAMS * DP <= TMEM, "TMEM");
   static constexpr size_t OFF_Q = 0;
   static constexpr size_t OFF_RING = OFF_Q + (size_t)STREAMS * QTILE;
@@ -160,8 +166,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&ctl.s_full[x], 1);
-      mbar_init(&ctl.p_half[x], 128);
-      mbar_init(&ctl.p_full[x], 128);
+      mbar_init(&ctl.p_half[x], 4);
+      mbar_init(&ctl.p_full[x], 4);
       mbar_init(&ctl.o_full[x], 1);
     }
     mbar_init(&ctl.q_full, kWorkers);
@@ -201,12 +207,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   volatile int* abort_flag = &ctl.abort;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return attn::bounded_wait(bar, parity, abort_flag, a.st); };
 
-  if (warp >= 8) {
+  // A role ends inside its branch: code behind the branches would run with either
+  // number of registers.
+  auto finish = [&]() {
+    fence_before_sync();
+    named_sync(0, kThreads);
+  };
+  if (warp >= 4 * C::STREAMS) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
     if (warp == kTmaWarp) {
       // ------------------------------------------------------------- TMA
       // Slots are filled K, V, K, V, ... in key order; lane i issues box i of
       // the tile's at most 32 (8-row boxes of two panels of 128 rows, or four of 64).
-      attn::Walk w(a.cu, a.lens, a.tokens, dims, ctl.share);
+      attn::Walk w(a.cu, a.lens, a.c.batch, a.tokens, dims, ctl.share);
       int pos = 0;  // slots filled so far
       bool alive = true;
       const int box_rows = a.maps.box_rows, boxes = C::BN / box_rows;
@@ -256,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       // The warp walks and waits as one; its elected lane issues.
       const bool leader = attn::elect_lane();
       auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
-      attn::Walk w(a.cu, a.lens, a.tokens, dims, ctl.share);
+      attn::Walk w(a.cu, a.lens, a.c.batch, a.tokens, dims, ctl.share);
       int pos = 0, pieces = 0, p_seen0 = 0, p_seen1 = 0;
       bool alive = true;
       const int k_steps = (D + 15) / 16;
@@ -342,8 +355,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       }
       __syncwarp();
     }
+    finish();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, C::TMEM);
+    return;
   } else {
-    if (warp < 4 * C::STREAMS) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    {
       // ----------------------------------------------------------- softmax
       const int st = warp >> 2, wl = warp & 3;
       const int r_tile = wl * 32 + lane;  // this thread's row of its 128
@@ -353,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       constexpr float kLift = Weight<E>::kLift, kLag = Weight<E>::kLag;
       // the TMEM accesses below need whole warps: a warp gives up together
       auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
-      attn::Walk w(a.cu, a.lens, a.tokens, dims, ctl.share);
+      attn::Walk w(a.cu, a.lens, a.c.batch, a.tokens, dims, ctl.share);
       int pos = 0, s_seen[2] = {0, 0}, o_seen = 0, pieces = 0, pv_seen = 0;
       bool alive = true;
       if (threadIdx.x == 0) a.splits[blockIdx.x].pieces = 0;
@@ -430,38 +447,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           if (!alive) break;
           fence_after_sync();
           if (active) {
-            // All but the last 32 columns stay in registers from the maximum to the
-            // weights; those are read again (a thread has 168 registers).  P takes
-            // columns of S that have been read.
-            constexpr int kHeld = C::BN - 32;
-            float s[kHeld], last[32];
+            float s[C::BN];
 #pragma unroll
-            for (int i = 0; i < kHeld; i += 32) attn::tmem_ld32(s_addr + i, s + i);
-            attn::tmem_ld32(s_addr + kHeld, last);
-            uint32_t last_bits = 0xFFFFFFFFu;
+            for (int i = 0; i < C::BN; i += 32) attn::tmem_ld32(s_addr + i, s + i);
 #pragma unroll
-            for (int i = 0; i < kHeld; i += 32) attn::tmem_ld_wait32(s + i);
-            attn::tmem_ld_wait32(last);
+            for (int i = 0; i < C::BN; i += 32) attn::tmem_ld_wait32(s + i);
             if (edge) {
 #pragma unroll
-              for (int i = 0; i < kHeld; i += 32) {
+              for (int i = 0; i < C::BN; i += 32) {
                 const uint32_t bits = attn::seen(a.tree, a.tree_words, w.s, token, k0 + i);
 #pragma unroll
                 for (int q = 0; q < 32; ++q) s[i + q] = (bits >> q) & 1u ? s[i + q] : -INFINITY;
               }
-              last_bits = attn::seen(a.tree, a.tree_words, w.s, token, k0 + kHeld);
-#pragma unroll
-              for (int q = 0; q < 32; ++q) last[q] = (last_bits >> q) & 1u ? last[q] : -INFINITY;
             }
             float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < kHeld; i += 8)
+            for (int i = 0; i < C::BN; i += 8)
 #pragma unroll
               for (int q = 0; q < 4; ++q) t[q] = attn::max3(t[q], s[i + 2 * q], s[i + 2 * q + 1]);
-#pragma unroll
-            for (int i = 0; i < 32; i += 8)
-#pragma unroll
-              for (int q = 0; q < 4; ++q) t[q] = attn::max3(t[q], last[i + 2 * q], last[i + 2 * q + 1]);
             const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * c2;
             // the first tile takes its maximum; later ones move it only by more than kLag
             const bool grow = real && top > (done ? m + kLag : m);
@@ -503,27 +506,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
               if (i + 32 == C::BN / 2) {  // the first half may go into its product
                 attn::tmem_st_wait();
                 fence_before_sync();
-                mbar_arrive(&ctl.p_half[x]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.p_half[x]);
               }
             };
-            weights(s, 0);
-            attn::tmem_ld32(s_addr + kHeld, last);
 #pragma unroll
-            for (int i = 32; i < kHeld; i += 32) weights(s + i, i);
-            attn::tmem_ld_wait32(last);
-            if (edge) {
-#pragma unroll
-              for (int q = 0; q < 32; ++q) last[q] = (last_bits >> q) & 1u ? last[q] : -INFINITY;
-            }
-            weights(last, kHeld);
+            for (int i = 0; i < C::BN; i += 32) weights(s + i, i);
             attn::tmem_st_wait();
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-          } else {
+          } else if (lane == 0) {
             mbar_arrive(&ctl.p_half[x]);
           }
           ++done;
           fence_before_sync();
-          mbar_arrive(&ctl.p_full[x]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl.p_full[x]);
         }
         pv_seen += done;
         if (l != l && m == -INFINITY) m = 0.f;  // only NaN scores: not to be mistaken for a row that saw nothing
@@ -642,10 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         ++pieces;
       }
     }
+    finish();
   }
-  fence_before_sync();
-  __syncthreads();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, C::TMEM);
 }
 
 // Adds up the pieces of divided units.  Block (part, y) takes rows 32 y .. 32 y +

@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
 
   if (warp == kTmaWarp) {
     // ------------------------------------------------------------- TMA
-    attn::Walk w(a.cu, a.lens, a.tokens, dims, ctl.share);
+    attn::Walk w(a.cu, a.lens, a.c.batch, a.tokens, dims, ctl.share);
     int pos = 0;
     bool alive = true;
     const int box_rows = a.maps.box_rows, boxes = kTile / box_rows;  // at most 16
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
     // The warp walks and waits as one; its elected lane issues.
     const bool leader = attn::elect_lane();
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
-    attn::Walk w(a.cu, a.lens, a.tokens, dims, ctl.share);
+    attn::Walk w(a.cu, a.lens, a.c.batch, a.tokens, dims, ctl.share);
     int slot0 = 0, round0 = 0;          // ring slot of the pass's first panel, and how often the ring had turned
     int loads = 0;
     uint32_t used = 0;                  // bit b: buffer b has been used an odd number of times
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
     const float c2 = fabsf(a.scale) * 1.4426950408889634f;
     const float2 c22 = make_float2(c2, c2), ones = make_float2(1.f, 1.f);
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
-    attn::Walk w(a.cu, a.lens, a.tokens, dims, ctl.share);
+    attn::Walk w(a.cu, a.lens, a.c.batch, a.tokens, dims, ctl.share);
     int loads = 0, used = 0;
     bool alive = true;
     while (w.next()) {

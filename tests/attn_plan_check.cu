@@ -22,7 +22,12 @@ static void check(bool ok, const char* what) {
 
 static void run(const PlanDims& d, const std::vector<int>& len, const std::vector<int>& n, int grid) {
   long long total = 0;
-  for (size_t b = 0; b < len.size(); ++b) total += sequence_length(d, len[b], n[b]);
+  int levels = 0;
+  for (size_t b = 0; b < len.size(); ++b)
+    for (int level = 0; n[b] > 0 && level < row_groups(d, n[b]); ++level) {
+      total += sequence_length(d, len[b], n[b], level);
+      levels = level + 1 > levels ? level + 1 : levels;
+    }
   const int parts = (int)(total < grid ? total : grid);
   std::map<std::tuple<int, int, int>, int> reached;  // unit -> tiles covered so far
   std::map<std::tuple<int, int, int>, std::pair<int, int>> split;  // divided unit -> first part, pieces announced
@@ -36,17 +41,20 @@ static void run(const PlanDims& d, const std::vector<int>& len, const std::vecto
     check(part_of(total, parts, t0) == c && part_of(total, parts, t1 - 1) == c, "part_of");
     long long t = t0, base = 0;
     size_t b = 0;
-    int going_on = 0, starting = 0;
+    int level = 0, going_on = 0, starting = 0;
     while (t < t1) {
-      while (t >= base + sequence_length(d, len[b], n[b])) base += sequence_length(d, len[b], n[b]), ++b;
-      check(b < len.size(), "sequence in range");
+      while (t >= base + sequence_length(d, len[b], n[b], level)) {
+        base += sequence_length(d, len[b], n[b], level);
+        if (++b == len.size()) b = 0, ++level;
+      }
+      check(level < levels, "level in range");
       const Piece p = piece_at(d, len[b], n[b], base, t, t1);
       check(p.next > t && p.next <= t1, "goes on");
       t = p.next;
       if (p.kt0 >= p.kt1) continue;
-      check(p.head >= 0 && p.head < d.kv_heads && p.rows_group >= 0 && p.rows_group < row_groups(d, n[b]), "unit in range");
+      check(p.head >= 0 && p.head < d.kv_heads && level < row_groups(d, n[b]), "unit in range");
       check(p.kt0 >= 0 && p.kt0 < p.kt1 && p.kt1 <= p.tiles && p.tiles == key_tiles(d, len[b], n[b]), "tiles in range");
-      const auto unit = std::make_tuple((int)b, p.head, p.rows_group);
+      const auto unit = std::make_tuple((int)b, p.head, level);
       check(reached[unit] == p.kt0, "tiles in order, once");
       reached[unit] = p.kt1;
       if (p.kt0 > 0) {
