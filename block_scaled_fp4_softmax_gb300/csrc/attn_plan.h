@@ -35,6 +35,7 @@ struct PlanDims {
   int kv_heads, group;      // query heads of a KV head
   int unit_rows, tile;      // rows of a unit, keys of a tile
   int cost;                 // places of the line before a unit's first tile
+  int least;                // places that a part has at least, if the line has them
 };
 
 ATTN_HD int row_groups(const PlanDims& d, int n) {
@@ -49,6 +50,11 @@ ATTN_HD long long sequence_length(const PlanDims& d, int len, int n, int level) 
 // A line longer than this is refused (the products below stay within 64 bits).
 constexpr long long kMaxLine = 1ll << 47;
 
+// Into how many parts a line is cut for a grid.
+ATTN_HD int part_count(const PlanDims& d, long long total, int grid) {
+  const long long most = quotient(total + d.least - 1, d.least);
+  return most < grid ? (int)most : grid;
+}
 // First place of part c, and the part that holds place t (at most 2^15 parts).
 ATTN_HD long long part_begin(long long total, int parts, int c) { return quotient(total * c, parts); }
 ATTN_HD int part_of(long long total, int parts, long long t) { return (int)quotient((t + 1) * parts - 1, total); }

@@ -125,7 +125,12 @@ struct Weight<attn::Half> {
 
 template <class C>
 __device__ __forceinline__ attn::PlanDims plan_dims(const TreeArgs& a) {
-  return attn::PlanDims{a.c.kv_heads, a.q_heads / a.c.kv_heads, C::ROWS, C::BN, C::UNIT_COST};
+  // A piece of R rows writes and reads back R * D * 8 bytes, as much as R / 64 tiles
+  // at D = 128: pieces of many rows are not cut as short as those of few.
+  const int G = a.q_heads / a.c.kv_heads;
+  const long long rows = (long long)a.tokens * G / a.c.batch;  // of an average sequence
+  const int least = 1 + (int)(rows < C::ROWS ? rows : C::ROWS) / 64;
+  return attn::PlanDims{a.c.kv_heads, G, C::ROWS, C::BN, C::UNIT_COST, least};
 }
 
 // Adds the NaN and infinite elements of a piece's drafts, which the products

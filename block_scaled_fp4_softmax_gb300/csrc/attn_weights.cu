@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
   }
   moe::pdl_wait();
   moe::pdl_launch_dependents();
-  const attn::PlanDims dims{a.c.kv_heads, G, 0x7FFFFFFF, kTile, 2};
+  const attn::PlanDims dims{a.c.kv_heads, G, 0x7FFFFFFF, kTile, 2, 1};
   const long long most = (long long)a.c.max_pages * a.c.page_size;
   if (!attn::take_share<kThreads>(a.cu, a.lens, a.c.batch, a.tokens, most < a.slot_cap ? most : a.slot_cap, dims,
                                   ctl.share)) {

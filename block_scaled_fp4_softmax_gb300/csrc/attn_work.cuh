@@ -59,7 +59,7 @@ __device__ bool take_share(const int32_t* __restrict__ cu, const int32_t* __rest
     total += sh.all[w];
   }
   if (total > kMaxLine) return false;
-  const int parts = (int)min((long long)gridDim.x, total), c = blockIdx.x;
+  const int parts = part_count(d, total, gridDim.x), c = blockIdx.x;
   const long long t0 = c < parts ? part_begin(total, parts, c) : 0;
   const long long t1 = c < parts ? part_begin(total, parts, c + 1) : 0;
   if (threadIdx.x == 0) sh.t0 = t0, sh.t1 = t1, sh.total = total, sh.parts = parts;

@@ -28,7 +28,8 @@ static void run(const PlanDims& d, const std::vector<int>& len, const std::vecto
       total += sequence_length(d, len[b], n[b], level);
       levels = level + 1 > levels ? level + 1 : levels;
     }
-  const int parts = (int)(total < grid ? total : grid);
+  const int parts = part_count(d, total, grid);
+  check(parts <= grid && (parts < grid || total >= grid) && (total == 0) == (parts == 0), "parts");
   std::map<std::tuple<int, int, int>, int> reached;  // unit -> tiles covered so far
   std::map<std::tuple<int, int, int>, std::pair<int, int>> split;  // divided unit -> first part, pieces announced
   std::map<std::tuple<int, int, int>, int> pieces;
@@ -81,7 +82,7 @@ int main() {
   std::mt19937 g(1);
   auto in = [&](int a, int b) { return (int)(a + g() % (unsigned)(b - a + 1)); };
   for (int trial = 0; trial < 3000; ++trial) {
-    PlanDims d{in(1, 8), in(1, 16), trial % 3 ? 256 : 128, trial % 2 ? 128 : 64, (int)(g() % 6)};
+    PlanDims d{in(1, 8), in(1, 16), trial % 3 ? 256 : 128, trial % 2 ? 128 : 64, (int)(g() % 6), in(1, 5)};
     const int B = in(1, trial % 7 ? 6 : 60);
     std::vector<int> len(B), n(B);
     for (int b = 0; b < B; ++b) {
@@ -91,7 +92,7 @@ int main() {
     run(d, len, n, in(0, 1) ? 152 : in(1, 300));
   }
   // lengths near the limit
-  run(PlanDims{8, 8, 256, 128, 3}, {2147481600 - 300, 2147480000, 5}, {100, 64, 0}, 152);
+  run(PlanDims{8, 8, 256, 128, 3, 5}, {2147481600 - 300, 2147480000, 5}, {100, 64, 0}, 152);
   std::printf("%lld checks, %lld failed\n", checks, failed);
   return failed != 0;
 }
