@@ -271,13 +271,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       __syncwarp();
     } else if (warp == kMmaWarp) {
       // ----------------------------------------------------------- MMA
-      // The warp walks and waits as one; its elected lane issues.
+      // The warp walks and waits as one, its elected lane issues.  What it does between
+      // the MMAs is kept short: at 128 keys and 128 elements a product takes 512 cycles,
+      // and the tensor core idles while the next one's operands are worked out.
       const bool leader = attn::elect_lane();
-      auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
       attn::Walk w(a.cu, a.lens, a.c.batch, a.tokens, dims, ctl.share);
-      int pos = 0, pieces = 0, p_seen0 = 0, p_seen1 = 0;
+      int k_slot = 0, k_round = 0, v_slot = 1, v_round = 0, pieces = 0;
+      uint32_t p_odd = 0;  // bit x: an odd number of tiles' weights has been taken from S buffer x
       bool alive = true;
-      const int k_steps = (D + 15) / 16;
+      const int k_steps = (D + 15) / 16, full_panels = k_steps / 4, rest = k_steps - 4 * full_panels;
       // a negative scale negates Q, the sums keep |scale|
       const uint32_t id_s = attn::idesc<E>(128, C::BN, false) | (a.scale < 0.f ? 1u << 13 : 0u);
       const uint32_t id_o = attn::idesc<E>(128, (D + 15) & ~15, true);
@@ -285,64 +287,68 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       const uint64_t v_desc = attn::sw128_mnmajor_desc(smem_u32(sRing), C::PANEL);
       const uint32_t q_low = (uint32_t)q_desc, k_low = (uint32_t)k_desc, k_high = (uint32_t)(k_desc >> 32);
       const uint32_t v_low = (uint32_t)v_desc, v_high = (uint32_t)(v_desc >> 32);
+      auto on = [](int& slot, int& round) {  // K and V alternate in the ring
+        slot += 2;
+        if (slot >= C::SLOTS) slot -= C::SLOTS, ++round;
+      };
       while (alive && w.next()) {
         const bool both = C::STREAMS == 2 && w.rows > 128;  // two row tiles over the same keys
         const int tiles = w.p.kt1 - w.p.kt0, items = both ? 2 * tiles : tiles;
-        alive = warp_wait(&ctl.q_full, pieces & 1);
+        alive = wait(&ctl.q_full, pieces & 1);
         if (!alive) break;
         fence_after_sync();
         auto qk = [&](int it) {
-          const int x = it & 1, ps = pos + 2 * (both ? it >> 1 : it), slot = ps % C::SLOTS;
+          const int x = it & 1;
           if (!both || x == 0) {
-            if (!warp_wait(&ctl.full[slot], (ps / C::SLOTS) & 1)) return false;
+            if (!wait(&ctl.full[k_slot], k_round & 1)) return false;
             fence_after_sync();
           }
           if (leader) {
-            uint32_t ql = q_low + (both && x ? C::QTILE >> 4 : 0), kl = k_low + (uint32_t)slot * (C::SLOT >> 4);
+            uint32_t ql = q_low + (both && x ? C::QTILE >> 4 : 0), kl = k_low + (uint32_t)k_slot * (C::SLOT >> 4);
             const uint32_t d = tmem + C::S_COL + x * C::BN;
-            for (int p = 0; p < panels; ++p, ql += (128 * 128) >> 4, kl += C::PANEL >> 4) {
-              if (4 * p + 4 <= k_steps) {  // unrolled, the MMAs leave at the tensor core's pace
+            uint32_t more = 0;
+            for (int p = 0; p < full_panels; ++p, ql += (128 * 128) >> 4, kl += C::PANEL >> 4) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  mma_bf16(d, attn::make_desc(k_high, ql + 2 * kk), attn::make_desc(k_high, kl + 2 * kk), id_s, (p | kk) != 0);
-              } else {
-                for (int kk = 0; kk < k_steps - 4 * p; ++kk)
-                  mma_bf16(d, attn::make_desc(k_high, ql + 2 * kk), attn::make_desc(k_high, kl + 2 * kk), id_s, (p | kk) != 0);
-              }
+              for (int kk = 0; kk < 4; ++kk, more = 1)
+                mma_bf16(d, attn::make_desc(k_high, ql + 2 * kk), attn::make_desc(k_high, kl + 2 * kk), id_s, more);
             }
+            for (int kk = 0; kk < rest; ++kk, more = 1)
+              mma_bf16(d, attn::make_desc(k_high, ql + 2 * kk), attn::make_desc(k_high, kl + 2 * kk), id_s, more);
             mma_commit(&ctl.s_full[x]);
-            if (!both || x == 1) mma_commit(&ctl.empty[slot]);
+            if (!both || x == 1) mma_commit(&ctl.empty[k_slot]);
             if (it == items - 1) mma_commit(&ctl.qk_done);
           }
           __syncwarp();
+          if (!both || x == 1) on(k_slot, k_round);
           return true;
         };
         auto pv = [&](int it) {
-          const int x = it & 1, ps = pos + 2 * (both ? it >> 1 : it) + 1, slot = ps % C::SLOTS;
-          const int st = C::STREAMS == 2 ? x : 0;  // whose O
-          const int seen = x ? p_seen1++ : p_seen0++;
-          if (!warp_wait(&ctl.p_half[x], seen & 1)) return false;
-          if ((!both || x == 0) && !warp_wait(&ctl.full[slot], (ps / C::SLOTS) & 1)) return false;
-          const uint32_t vl = v_low + (uint32_t)slot * (C::SLOT >> 4);
-          const bool first = C::STREAMS == 2 ? it < 2 : it == 0;
-          const uint32_t d = tmem + C::O_COL + st * DP, p = tmem + C::S_COL + x * C::BN;
-          for (int half = 0; half < 2; ++half) {
-            if (half == 1 && !warp_wait(&ctl.p_full[x], seen & 1)) return false;
-            fence_after_sync();
-            if (leader) {
-              const uint32_t ph = p + half * (C::BN / 4), vh = vl + half * (C::PANEL / 2 >> 4);
-#pragma unroll
-              for (int kk = 0; kk < C::BN / 32; ++kk)
-                attn::mma_ts(d, ph + kk * 8, attn::make_desc(v_high, vh + kk * (2048 >> 4)), id_o, !(first && half == 0 && kk == 0));
-            }
-            __syncwarp();
-          }
+          const int x = it & 1, st = C::STREAMS == 2 ? x : 0;  // whose O
+          const uint32_t o = tmem + C::O_COL + st * DP, p = tmem + C::S_COL + x * C::BN;
+          const uint32_t vl = v_low + (uint32_t)v_slot * (C::SLOT >> 4), seen = (p_odd >> x) & 1;
+          const uint32_t more = it >= C::STREAMS;
+          p_odd ^= 1u << x;
+          if ((!both || x == 0) && !wait(&ctl.full[v_slot], v_round & 1)) return false;
+          if (!wait(&ctl.p_half[x], seen)) return false;
+          fence_after_sync();
           if (leader) {
-            if (!both || x == 1) mma_commit(&ctl.empty[slot]);
+#pragma unroll
+            for (int kk = 0; kk < C::BN / 32; ++kk)
+              attn::mma_ts(o, p + kk * 8, attn::make_desc(v_high, vl + kk * (2048 >> 4)), id_o, kk ? 1 : more);
+          }
+          __syncwarp();
+          if (!wait(&ctl.p_full[x], seen)) return false;
+          fence_after_sync();
+          if (leader) {
+#pragma unroll
+            for (int kk = C::BN / 32; kk < C::BN / 16; ++kk)
+              attn::mma_ts(o, p + kk * 8, attn::make_desc(v_high, vl + kk * (2048 >> 4)), id_o, 1);
+            if (!both || x == 1) mma_commit(&ctl.empty[v_slot]);
             if (C::STREAMS == 1) mma_commit(&ctl.pv_done);
             if (it >= items - C::STREAMS) mma_commit(&ctl.o_full[st]);
           }
           __syncwarp();
+          if (!both || x == 1) on(v_slot, v_round);
           return true;
         };
         alive = qk(0);
@@ -350,10 +356,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           if (it + 1 < items) alive = qk(it + 1);
           alive = alive && pv(it);
         }
-        pos += 2 * tiles;
         ++pieces;
       }
       // every MMA has completed before TMEM goes back
+      __syncwarp();
       if (leader) {
         mma_commit(&ctl.drain);
         attn::bounded_wait(&ctl.drain, 0, nullptr, a.st);
@@ -413,7 +419,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         const bool real = row < w.row0 + w.rows;
         float m = -INFINITY, l = 0.f;  // m in powers of two
         int done = 0;
-        for (int it = (C::STREAMS == 2 ? st : 0); it < items && alive; it += C::STREAMS) {
+        // Where a wait has given up, the loop still runs to its end without waiting, so
+        // that the warpgroups meet at every barrier.
+        for (int it = (C::STREAMS == 2 ? st : 0); it < items; it += C::STREAMS) {
           const int x = it & 1, tile = both ? it >> 1 : it;
           const int k0 = (w.p.kt0 + tile) * C::BN;
           const uint32_t s_addr = tmem + lane_base + C::S_COL + x * C::BN;
@@ -421,12 +429,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           // ---- clean V where the tile reaches past the committed slots
           if (edge && (!both || st == 0)) {
             const int ps = pos + 2 * tile + 1;
-            alive = warp_wait(&ctl.full[ps % C::SLOTS], (ps / C::SLOTS) & 1);
-            if (!alive) break;
+            alive = alive && warp_wait(&ctl.full[ps % C::SLOTS], (ps / C::SLOTS) & 1);
             uint8_t* v = sRing + (size_t)(ps % C::SLOTS) * C::SLOT;
             const int lo = max(0, w.s.len - k0), hi = w.s.len + w.s.n - k0;
             const int chunks = panels * 8;
-            for (int i = lo * chunks + (threadIdx.x & 127); i < C::BN * chunks; i += 128) {
+            for (int i = lo * chunks + (threadIdx.x & 127); alive && i < C::BN * chunks; i += 128) {
               const int r = i / chunks, ch = i - r * chunks;
               uint4* at = reinterpret_cast<uint4*>(v + attn::sw128_offset(r, ch, C::BN));
               if (r >= hi) {
@@ -449,7 +456,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             fence_proxy_async();
           }
           alive = alive && warp_wait(&ctl.s_full[x], s_seen[x]++ & 1);
-          if (!alive) break;
           fence_after_sync();
           if (active) {
             float s[C::BN];
@@ -477,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
               const float m1 = grow ? top : m;
               if (done) {
                 if (C::STREAMS == 1) {  // O still takes the tile before: wait for that product
-                  alive = warp_wait(&ctl.pv_done, (pv_seen + done - 1) & 1);
+                  alive = alive && warp_wait(&ctl.pv_done, (pv_seen + done - 1) & 1);
                   fence_after_sync();
                 }
                 const float f = m == -INFINITY ? 0.f : attn::exp2_fast(m - m1);
