@@ -10,6 +10,7 @@ output is passed.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -112,6 +113,7 @@ def attn_cache(k, v, page_table) -> AttnCache:
 # one.
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_i32, _i64, _f32, _f64, _u8 = torch.int32, torch.int64, torch.float32, torch.float64, torch.uint8
 
 
 def _on(stream, cache):
@@ -137,7 +139,7 @@ def _rows(t, name, heads, cache):
 def _array(t, name, shape, dtype, cache):
     """Address of a contiguous tensor of just this shape and type."""
     try:
-        if t.dtype is dtype and t.shape == shape and t.get_device() == cache.index and t.is_contiguous():
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == cache.index:
             return t.data_ptr()
     except (AttributeError, TypeError):
         pass
@@ -152,20 +154,21 @@ def _tree(tree, tokens, cache):
     if tree.dim() != 2:
         raise MoeError("tree must be [tokens, words]")
     words = tree.shape[1]
-    return _array(tree, "tree", (tokens, words), torch.int64, cache), words
+    return _array(tree, "tree", (tokens, words), _i64, cache), words
 
 
 def _status(dev_status, cache):
-    return None if dev_status is None else _array(dev_status, "dev_status", (1,), torch.int32, cache)
+    return None if dev_status is None else _array(dev_status, "dev_status", (1,), _i32, cache)
 
 
-def _new(stream, make, *args, **kwargs):
-    """Allocates on the stream the call runs on, so that the allocator never
-    hands the memory to another stream while the call uses it."""
-    if stream is None:
-        return make(*args, **kwargs)
-    with torch.cuda.stream(stream):
-        return make(*args, **kwargs)
+def _elsewhere(stream):
+    """Context for allocating on the stream the call runs on, so that the
+    allocator never hands the memory to another stream while the call uses it."""
+    return _HERE if stream is None else torch.cuda.stream(stream)
+
+
+_HERE = contextlib.nullcontext()
+_empty = torch.empty
 
 
 # ---------------------------------------------------------------------------
@@ -190,14 +193,18 @@ def attn_qk_norm_rope(q, k, v, pos, cu, lens, cache: AttnCache, inv_freq, q_weig
     at, cap = None, 0
     if slot_pos is not None:
         cap = slot_pos.shape[-1]
-        at = _array(slot_pos, "slot_pos", (cache.batch, cache.kv_heads, cap), torch.int32, cache)
+        at = _array(slot_pos, "slot_pos", (cache.batch, cache.kv_heads, cap), _i32, cache)
     if q_out is None:
-        q_out = _new(stream, torch.empty, (T, hq, D), dtype=q.dtype, device=cache.device)
-    rc = load().attn_qk_norm_rope(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), sq, sk, sv, _array(pos, "pos", (T,), torch.int32, cache),
-        _array(cu, "cu", cache.cu_shape, torch.int32, cache), _array(lens, "lens", cache.lens_shape, torch.int32, cache),
-        T, hq, wq, wk, eps, _array(inv_freq, "inv_freq", (half,), torch.float64, cache), 2 * half, interleaved,
-        magnitude, _array(q_out, "q_out", (T, hq, D), cache.dtype, cache), at, cap, cache.ref,
+        with _elsewhere(stream):
+            q_out = _empty((T, hq, D), dtype=cache.dtype, device=cache.device)
+        to = q_out.data_ptr()
+    else:
+        to = _array(q_out, "q_out", (T, hq, D), cache.dtype, cache)
+    rc = (_LIB or load()).attn_qk_norm_rope(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), sq, sk, sv, _array(pos, "pos", (T,), _i32, cache),
+        _array(cu, "cu", cache.cu_shape, _i32, cache), _array(lens, "lens", cache.lens_shape, _i32, cache),
+        T, hq, wq, wk, eps, _array(inv_freq, "inv_freq", (half,), _f64, cache), 2 * half, interleaved,
+        magnitude, to, at, cap, cache.ref,
         _status(dev_status, cache), _on(stream, cache))
     if rc:
         _check(rc, "attn_qk_norm_rope")
@@ -210,7 +217,7 @@ def attn_tree_decode_workspace(cache: AttnCache):
         n = int(load().attn_tree_decode_workspace(cache.ref))
     if n == 0:
         raise MoeError("attn_tree_decode does not support this cache")
-    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+    return torch.empty(n, dtype=_u8, device=cache.device)
 
 
 def attn_tree_decode(q, cu, lens, cache: AttnCache, tree=None, scale: float | None = None, out=None, lse=None,
@@ -220,19 +227,21 @@ def attn_tree_decode(q, cu, lens, cache: AttnCache, tree=None, scale: float | No
     sq = _rows(q, "q", None, cache)
     T, hq, D = q.shape
     words, count = _tree(tree, T, cache)
-    if out is None:
-        out = _new(stream, torch.empty, (T, hq, D), dtype=q.dtype, device=cache.device)
-    if lse is None:
-        lse = _new(stream, torch.empty, (T, hq), dtype=torch.float32, device=cache.device)
-    if workspace is None:
-        workspace = _new(stream, attn_tree_decode_workspace, cache)
+    if out is None or lse is None or workspace is None:
+        with _elsewhere(stream):
+            if out is None:
+                out = _empty((T, hq, D), dtype=cache.dtype, device=cache.device)
+            if lse is None:
+                lse = _empty((T, hq), dtype=_f32, device=cache.device)
+            if workspace is None:
+                workspace = attn_tree_decode_workspace(cache)
     size = workspace.numel()
-    rc = load().attn_tree_decode(
-        q.data_ptr(), sq, _array(cu, "cu", cache.cu_shape, torch.int32, cache),
-        _array(lens, "lens", cache.lens_shape, torch.int32, cache), T, hq, words, count,
+    rc = (_LIB or load()).attn_tree_decode(
+        q.data_ptr(), sq, _array(cu, "cu", cache.cu_shape, _i32, cache),
+        _array(lens, "lens", cache.lens_shape, _i32, cache), T, hq, words, count,
         D ** -0.5 if scale is None else scale, cache.ref, _array(out, "out", (T, hq, D), cache.dtype, cache),
-        _array(lse, "lse", (T, hq), torch.float32, cache),
-        _array(workspace, "workspace", (size,), torch.uint8, cache), size, _status(dev_status, cache),
+        _array(lse, "lse", (T, hq), _f32, cache),
+        _array(workspace, "workspace", (size,), _u8, cache), size, _status(dev_status, cache),
         _on(stream, cache))
     if rc:
         _check(rc, "attn_tree_decode")
@@ -249,12 +258,13 @@ def attn_cache_weights(q, lse, cu, lens, cache: AttnCache, acc, tree=None, scale
     words, count = _tree(tree, T, cache)
     shape = (cache.batch, cache.kv_heads, acc.shape[-1])
     if acc_out is None:
-        acc_out = _new(stream, torch.zeros, shape, dtype=torch.float32, device=cache.device)
-    rc = load().attn_cache_weights(
-        q.data_ptr(), sq, _array(lse, "lse", (T, hq), torch.float32, cache),
-        _array(cu, "cu", cache.cu_shape, torch.int32, cache), _array(lens, "lens", cache.lens_shape, torch.int32, cache),
+        with _elsewhere(stream):
+            acc_out = torch.zeros(shape, dtype=_f32, device=cache.device)
+    rc = (_LIB or load()).attn_cache_weights(
+        q.data_ptr(), sq, _array(lse, "lse", (T, hq), _f32, cache),
+        _array(cu, "cu", cache.cu_shape, _i32, cache), _array(lens, "lens", cache.lens_shape, _i32, cache),
         T, hq, words, count, D ** -0.5 if scale is None else scale, cache.ref,
-        _array(acc, "acc", shape, torch.float32, cache), decay, _array(acc_out, "acc_out", shape, torch.float32, cache),
+        _array(acc, "acc", shape, _f32, cache), decay, _array(acc_out, "acc_out", shape, _f32, cache),
         shape[2], _status(dev_status, cache), _on(stream, cache))
     if rc:
         _check(rc, "attn_cache_weights")
@@ -266,7 +276,7 @@ def attn_cache_evict_workspace(cache: AttnCache, budget: int):
     n = int(load().attn_cache_evict_workspace(cache.ref, budget))
     if n == 0:
         raise MoeError("attn_cache_evict does not support this cache or budget")
-    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+    return torch.empty(n, dtype=_u8, device=cache.device)
 
 
 def attn_cache_evict(cache: AttnCache, acc, slot_pos, lens, next_pos, budget: int, sinks: int = 0, recent: int = 0,
@@ -275,22 +285,24 @@ def attn_cache_evict(cache: AttnCache, acc, slot_pos, lens, next_pos, budget: in
     weight and moves their rows below the budget, in place.  Returns
     (lens_out, acc_out, pos_out)."""
     shape = (cache.batch, cache.kv_heads, acc.shape[-1])
-    if acc_out is None:
-        acc_out = _new(stream, torch.zeros, shape, dtype=torch.float32, device=cache.device)
-    if pos_out is None:
-        pos_out = _new(stream, torch.zeros, shape, dtype=torch.int32, device=cache.device)
-    if lens_out is None:
-        lens_out = _new(stream, torch.empty, cache.lens_shape, dtype=torch.int32, device=cache.device)
-    if workspace is None:
-        workspace = _new(stream, attn_cache_evict_workspace, cache, budget)
+    if acc_out is None or pos_out is None or lens_out is None or workspace is None:
+        with _elsewhere(stream):
+            if acc_out is None:
+                acc_out = torch.zeros(shape, dtype=_f32, device=cache.device)
+            if pos_out is None:
+                pos_out = torch.zeros(shape, dtype=_i32, device=cache.device)
+            if lens_out is None:
+                lens_out = _empty(cache.lens_shape, dtype=_i32, device=cache.device)
+            if workspace is None:
+                workspace = attn_cache_evict_workspace(cache, budget)
     size = workspace.numel()
-    rc = load().attn_cache_evict(
-        cache.ref, _array(acc, "acc", shape, torch.float32, cache), _array(slot_pos, "slot_pos", shape, torch.int32, cache),
-        shape[2], _array(lens, "lens", cache.lens_shape, torch.int32, cache),
-        _array(next_pos, "next_pos", cache.lens_shape, torch.int32, cache), budget, sinks, recent,
-        _array(acc_out, "acc_out", shape, torch.float32, cache), _array(pos_out, "pos_out", shape, torch.int32, cache),
-        _array(lens_out, "lens_out", cache.lens_shape, torch.int32, cache),
-        _array(workspace, "workspace", (size,), torch.uint8, cache), size, _status(dev_status, cache),
+    rc = (_LIB or load()).attn_cache_evict(
+        cache.ref, _array(acc, "acc", shape, _f32, cache), _array(slot_pos, "slot_pos", shape, _i32, cache),
+        shape[2], _array(lens, "lens", cache.lens_shape, _i32, cache),
+        _array(next_pos, "next_pos", cache.lens_shape, _i32, cache), budget, sinks, recent,
+        _array(acc_out, "acc_out", shape, _f32, cache), _array(pos_out, "pos_out", shape, _i32, cache),
+        _array(lens_out, "lens_out", cache.lens_shape, _i32, cache),
+        _array(workspace, "workspace", (size,), _u8, cache), size, _status(dev_status, cache),
         _on(stream, cache))
     if rc:
         _check(rc, "attn_cache_evict")

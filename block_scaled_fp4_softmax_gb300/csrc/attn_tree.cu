@@ -676,29 +676,41 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   for (int r0 = blockIdx.y * 32; r0 < s.rows; r0 += gridDim.y * 32) {
     const bool real = r0 + lane < s.rows;
     const int r = real ? r0 + lane : r0;
-    auto slot = [&](int i) { return (size_t)(part + i / streams) * 2 + (i < streams); };
-    auto at = [&](int i) { return r + (i % streams) * 128; };
-    float top = -INFINITY;
+    auto place = [&](int i) {  // of piece i's row among all rows of the workspace
+      return ((size_t)(part + i / streams) * 2 + (i < streams)) * C::ROWS + r + (i % streams) * 128;
+    };
+    // one look at every piece's m and l: a running maximum, and the sum under it
+    float top = -INFINITY, l = 0.f;
 #pragma unroll 4
-    for (int i = warp; i < n; i += kJoinWarps) top = fmaxf(top, ml[slot(i) * C::ROWS + at(i)].x);
+    for (int i = warp; i < n; i += kJoinWarps) {
+      const float2 v = ml[place(i)];
+      const float m = fmaxf(top, v.x);
+      if (m != -INFINITY) l = l * attn::exp2_fast(top - m) + (v.x == -INFINITY ? 0.f : v.y * attn::exp2_fast(v.x - m));
+      top = m;
+    }
     s_top[warp][lane] = top;
+    s_l[warp][lane] = l;
     __syncthreads();
+    top = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, s_top[w][lane]);
-    float l = 0.f, y[DP / kJoinWarps] = {};  // columns 4 (warp + 8 k) ..
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w)
+      if (s_top[w][lane] != -INFINITY) l += s_l[w][lane] * attn::exp2_fast(s_top[w][lane] - top);
+    float y[DP / kJoinWarps] = {};  // columns 4 (warp + 8 k) ..
     for (int i0 = 0; i0 < n; i0 += kChunk) {
       const int count = min(kChunk, n - i0);
       for (int i = warp; i < count; i += kJoinWarps) {
-        const float2 v = ml[slot(i0 + i) * C::ROWS + at(i0 + i)];
-        const float f = v.x == -INFINITY ? 0.f : attn::exp2_fast(v.x - top);
-        if (v.x != -INFINITY) l += v.y * f;
-        s_factor[i][lane] = f;
+        const float m = ml[place(i0 + i)].x;
+        s_factor[i][lane] = m == -INFINITY ? 0.f : attn::exp2_fast(m - top);
       }
       __syncthreads();
-#pragma unroll 4
+#pragma unroll 8
       for (int i = 0; i < count; ++i) {
         const float f = s_factor[i][lane];
-        const float4* o = a.o + (slot(i0 + i) * (DP / 4) + warp) * C::ROWS + at(i0 + i);
+        const size_t at = place(i0 + i), slot = at / C::ROWS;
+        const float4* o = a.o + (slot * (DP / 4) + warp) * C::ROWS + (at - slot * C::ROWS);
 #pragma unroll
         for (int k = 0; k < DP / 4 / kJoinWarps; ++k)
           if (f != 0.f && (warp + k * kJoinWarps) * 4 < D) {  // 0: a piece that saw nothing, and wrote nothing
@@ -708,11 +720,6 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       }
       __syncthreads();
     }
-    s_l[warp][lane] = l;
-    __syncthreads();
-    l = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) l += s_l[w][lane];
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int row = s.row0 + r, tok = row / G;
     const long long out_row = (long long)(s.first + tok) * a.q_heads + s.head * G + (row - tok * G);
@@ -725,7 +732,6 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + out_row * D + d) =
             make_uint2(E::down(y[4 * k] * inv, y[4 * k + 1] * inv), E::down(y[4 * k + 2] * inv, y[4 * k + 3] * inv));
     }
-    __syncthreads();
   }
 }
 
