@@ -28,7 +28,7 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 16;  // beyond 8 the kernel has to allow it, and the device to have room
-constexpr int kMaxKeys = 48 * 1024;  // keys of one CTA's slice held in shared memory
+constexpr int kMaxKeys = 44 * 1024;  // keys of one CTA's slice held in shared memory
 
 struct EvictArgs {
   attn_cache c;
@@ -56,10 +56,11 @@ __device__ __forceinline__ uint32_t rank_key(float w, int pos, int sinks, long l
 struct alignas(16) Shared {
   uint32_t hist[3][kBins];
   uint32_t total[kBins];  // the cluster's histogram, where it is added up in slices
+  uint32_t part[kThreads];  // of this CTA's slice: sums over two CTAs each
   uint32_t warp_sum[kWarps];
   int4 counts[kWarps];  // above, equal, above below the budget, equal below the budget
-  int2 before[kWarps];
-  int2 at_budget;
+  int2 before[kWarps];       // above and equal in the CTA's warps before
+  int4 of_cta[kMaxCluster];  // the same four counts of each CTA
   uint32_t digit, rest;
 };
 
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     cluster.sync();
     // thread i: bins kBins - 1 - 2i and the one below, over the cluster.  Up to four
     // CTAs each read all histograms; more share the bins out and hand the sums
-    // round (16 CTAs reading 16 histograms took 12000 cycles a round, 2500 so).
+    // round (16 CTAs reading 16 histograms took 12000 cycles a round).
     const int hi = kBins - 1 - 2 * threadIdx.x;
     uint32_t n_hi = 0, n_lo = 0;
     if (C <= 4) {
@@ -178,12 +179,15 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
         n_hi += v.y;
       }
     } else {
-      const int slice = kBins / C;  // threads: bin of the slice x CTA to tell
-      const int bin = r * slice + (int)threadIdx.x % slice;
+      const int slice = kBins / C, half = C / 2;  // threads: bin of the slice x pair of CTAs
+      const int bin = r * slice + (int)threadIdx.x % slice, pair = threadIdx.x / slice;
+      sh.part[threadIdx.x] = cluster.map_shared_rank(&sh.hist[round][0], pair)[bin] +
+                             cluster.map_shared_rank(&sh.hist[round][0], pair + half)[bin];
+      __syncthreads();
       uint32_t sum = 0;
-#pragma unroll 4
-      for (int q = 0; q < C; ++q) sum += cluster.map_shared_rank(&sh.hist[round][0], q)[bin];
-      for (int q = threadIdx.x / slice; q < C; q += kThreads / slice) cluster.map_shared_rank(&sh.total[0], q)[bin] = sum;
+      for (int q = 0; q < half; ++q) sum += sh.part[q * slice + (int)threadIdx.x % slice];
+      cluster.map_shared_rank(&sh.total[0], pair)[bin] = sum;
+      cluster.map_shared_rank(&sh.total[0], pair + half)[bin] = sum;
       cluster.sync();
       n_lo = sh.total[hi - 1];
       n_hi = sh.total[hi];
@@ -219,43 +223,35 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
       if (j + q < K) cnt.z += gt, cnt.w += eq;
     }
   }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    cnt.x += __shfl_xor_sync(0xffffffffu, cnt.x, d);
-    cnt.y += __shfl_xor_sync(0xffffffffu, cnt.y, d);
-    cnt.z += __shfl_xor_sync(0xffffffffu, cnt.z, d);
-    cnt.w += __shfl_xor_sync(0xffffffffu, cnt.w, d);
-  }
+  cnt.x = __reduce_add_sync(0xffffffffu, cnt.x);
+  cnt.y = __reduce_add_sync(0xffffffffu, cnt.y);
+  cnt.z = __reduce_add_sync(0xffffffffu, cnt.z);
+  cnt.w = __reduce_add_sync(0xffffffffu, cnt.w);
   if (lane == 0) sh.counts[warp] = cnt;
   cluster.sync();
-  if (warp == 0) {  // lane = warp of a CTA; prefix over the cluster in slot order
-    int2 run = make_int2(0, 0), at = make_int2(0, 0);
-    for (int q = 0; q < C; ++q) {
-      const int4 v = *cluster.map_shared_rank(&sh.counts[lane], q);
-      int2 in = make_int2(v.x, v.y);
-      at.x += v.z;
-      at.y += v.w;
+  if (warp < C) {  // a warp to a CTA, a lane to a warp of it
+    const int4 v = *cluster.map_shared_rank(&sh.counts[lane], warp);
+    int2 in = make_int2(v.x, v.y);
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int ux = __shfl_up_sync(0xffffffffu, in.x, d), uy = __shfl_up_sync(0xffffffffu, in.y, d);
-        if (lane >= d) in.x += ux, in.y += uy;
-      }
-      if (q == r) sh.before[lane] = make_int2(run.x + in.x - v.x, run.y + in.y - v.y);
-      run.x += __shfl_sync(0xffffffffu, in.x, 31);
-      run.y += __shfl_sync(0xffffffffu, in.y, 31);
+    for (int d = 1; d < 32; d <<= 1) {
+      const int ux = __shfl_up_sync(0xffffffffu, in.x, d), uy = __shfl_up_sync(0xffffffffu, in.y, d);
+      if (lane >= d) in.x += ux, in.y += uy;
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      at.x += __shfl_xor_sync(0xffffffffu, at.x, d);
-      at.y += __shfl_xor_sync(0xffffffffu, at.y, d);
-    }
-    if (lane == 0) sh.at_budget = at;
+    if (warp == r) sh.before[lane] = make_int2(in.x - v.x, in.y - v.y);
+    const int low = __reduce_add_sync(0xffffffffu, v.z), low_equal = __reduce_add_sync(0xffffffffu, v.w);
+    if (lane == 31) sh.of_cta[warp] = make_int4(in.x, in.y, low, low_equal);
   }
   __syncthreads();
+  int above = sh.before[warp].x, equal = sh.before[warp].y, low = 0, low_equal = 0;
+  for (int q = 0; q < C; ++q) {
+    const int4 v = sh.of_cta[q];
+    if (q < r) above += v.x, equal += v.y;
+    low += v.z;
+    low_equal += v.w;
+  }
   const int ties = (int)rest;
-  const int kept_low = sh.at_budget.x + min(sh.at_budget.y, ties);  // kept slots below the budget
+  const int kept_low = low + min(low_equal, ties);  // kept slots below the budget
   if (r == 0 && threadIdx.x == 0) a.counts[problem] = K - kept_low;
-  int above = sh.before[warp].x, equal = sh.before[warp].y;
   int32_t* src = a.src + (long long)problem * K;
   int32_t* dst = a.dst + (long long)problem * K;
   for (int c0 = j0; c0 < j1; c0 += 128) {
