@@ -175,6 +175,16 @@ __device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
       :
       : "memory");
 }
+// The same; what has been added up into `done` before it in the source stays before
+// it, so that the arithmetic on one group of columns covers the loads of the next.
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16], float2 (&done)[2]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+        "+f"(done[0].x), "+f"(done[0].y), "+f"(done[1].x), "+f"(done[1].y)
+      :
+      : "memory");
+}
 // The same as tmem_ld_wait32; what has been added up into `done` before it in the source stays
 // before it, so that the arithmetic on one group of columns covers the loads of
 // the next.
