@@ -323,16 +323,18 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
             fence_after_sync();
             const int n = min(kChunk, ((rows - g * kChunk) + 31) & ~31);
             const uint32_t from = tmem + lane_base + buf * kChunk;
+            uint32_t sa[16];
             if (!edge) {
               // 16 columns are on their way from TMEM while the 16 before are added up
-              uint32_t sa[16], sb[16];
-              auto add = [&](const uint32_t (&s)[16], int i) {
-                const float4* bias = reinterpret_cast<const float4*>(ctl.bias + g * kChunk + i);
+              uint32_t sb[16];
+              auto add = [&](const uint32_t (&s)[16], int half, int i) {
+                const float4* bias = reinterpret_cast<const float4*>(ctl.bias + g * kChunk + i + half);
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) {
+                for (int e = 0; e < 8; e += 4) {
                   const float4 bb = bias[e >> 2];
-                  float2 u = moe::ffma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c22, make_float2(bb.x, bb.y));
-                  float2 v = moe::ffma2(make_float2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), c22, make_float2(bb.z, bb.w));
+                  const uint32_t* x = s + half + e;
+                  float2 u = moe::ffma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), c22, make_float2(bb.x, bb.y));
+                  float2 v = moe::ffma2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), c22, make_float2(bb.z, bb.w));
                   u.x = attn::exp2_fast(u.x), u.y = attn::exp2_fast(u.y);
                   v.x = attn::exp2_fast(v.x), v.y = attn::exp2_fast(v.y);
                   sum[0] = moe::ffma2(u, ones, sum[0]);
@@ -344,25 +346,26 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
 #pragma unroll 1
               for (int i = 0; i < n; i += 32) {
                 tmem_ld16(from + i + 16, sb);
-                add(sa, i);
+                add(sa, 0, i);
                 attn::tmem_ld_wait16(sb, sum);
-                if (i + 32 < n) tmem_ld16(from + i + 32, sa);
-                add(sb, i + 16);
-                if (i + 32 < n) attn::tmem_ld_wait16(sa, sum);
+                add(sa, 8, i);
+                tmem_ld16(from + min(i + 32, n - 16), sa);
+                add(sb, 0, i + 16);
+                attn::tmem_ld_wait16(sa, sum);
+                add(sb, 8, i + 16);
               }
             } else {
 #pragma unroll 1
-              for (int i = 0; i < n; i += 32) {
-                float s[32];
-                attn::tmem_ld32(from + i, s);
-                attn::tmem_ld_wait32(s);
+              for (int i = 0; i < n; i += 16) {
+                tmem_ld16(from + i, sa);
+                attn::tmem_ld_wait16(sa, sum);
                 // lane e looks up what row e sees of the warp's 32 slots
-                const int row = r0 + g * kChunk + i + lane;
+                const int row = r0 + g * kChunk + i + (lane & 15);
                 const uint32_t bits = row < r0 + rows ? attn::seen(a.tree, a.tree_words, w.s, row / G, k0) : 0u;
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
+                for (int e = 0; e < 16; ++e) {
                   const uint32_t of_row = __shfl_sync(0xffffffffu, bits, e);
-                  const float p = attn::exp2_fast(fmaf(s[e], c2, ctl.bias[g * kChunk + i + e]));
+                  const float p = attn::exp2_fast(fmaf(__uint_as_float(sa[e]), c2, ctl.bias[g * kChunk + i + e]));
                   if ((of_row >> lane) & 1u) (e & 1 ? sum[0].y : sum[0].x) += p;
                 }
               }
