@@ -654,15 +654,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   }
 }
 
-// Adds up the pieces of divided units.  Block (part, y) takes rows 32 y .. 32 y +
-// 31 of the unit, a lane to a row.  The warps first share the pieces (m and l,
-// turned into factors in shared memory), then the columns.
+// Adds up the pieces of divided units.  Block (part, y, z) takes rows 32 y .. 32 y +
+// 31 of the unit, a lane to a row, and the z-th of SLICES parts of the columns.
+// The warps first share the pieces (m and l, turned into factors in shared
+// memory), then the columns.
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 
-template <class E, int DP>
+template <class E, int DP, int SLICES>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ TreeArgs a) {
   using C = Cfg<DP>;
   using T = typename E::T;
+  constexpr int kMine = DP / 4 / kJoinWarps / SLICES;  // columns of a lane, by fours
+  const int first = 4 * (threadIdx.x >> 5) + 32 * kMine * blockIdx.z;
   constexpr int kChunk = 32;  // pieces whose factors are held at a time
   __shared__ float s_top[kJoinWarps][32], s_l[kJoinWarps][32], s_factor[kChunk][32];
   moe::pdl_wait();
@@ -698,7 +701,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w)
       if (s_top[w][lane] != -INFINITY) l += s_l[w][lane] * attn::exp2_fast(s_top[w][lane] - top);
-    float y[DP / kJoinWarps] = {};  // columns 4 (warp + 8 k) ..
+    float y[4 * kMine] = {};  // columns first + 32 k ..
     for (int i0 = 0; i0 < n; i0 += kChunk) {
       const int count = min(kChunk, n - i0);
       for (int i = warp; i < count; i += kJoinWarps) {
@@ -710,10 +713,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       for (int i = 0; i < count; ++i) {
         const float f = s_factor[i][lane];
         const size_t at = place(i0 + i), slot = at / C::ROWS;
-        const float4* o = a.o + (slot * (DP / 4) + warp) * C::ROWS + (at - slot * C::ROWS);
+        const float4* o = a.o + (slot * (DP / 4) + first / 4) * C::ROWS + (at - slot * C::ROWS);
 #pragma unroll
-        for (int k = 0; k < DP / 4 / kJoinWarps; ++k)
-          if (f != 0.f && (warp + k * kJoinWarps) * 4 < D) {  // 0: a piece that saw nothing, and wrote nothing
+        for (int k = 0; k < kMine; ++k)
+          if (f != 0.f && first + 32 * k < D) {  // 0: a piece that saw nothing, and wrote nothing
             const float4 v = o[(size_t)k * kJoinWarps * C::ROWS];
             y[4 * k] += v.x * f, y[4 * k + 1] += v.y * f, y[4 * k + 2] += v.z * f, y[4 * k + 3] += v.w * f;
           }
@@ -723,11 +726,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int row = s.row0 + r, tok = row / G;
     const long long out_row = (long long)(s.first + tok) * a.q_heads + s.head * G + (row - tok * G);
-    if (warp == 0 && real && a.lse)
+    if (first == 0 && real && a.lse)
       a.lse[out_row] = l == 0.f ? -INFINITY : (top - Weight<E>::kLift) * 0.6931471805599453f + logf(l);
 #pragma unroll
-    for (int k = 0; k < DP / 4 / kJoinWarps; ++k) {
-      const int d = (warp + k * kJoinWarps) * 4;
+    for (int k = 0; k < kMine; ++k) {
+      const int d = first + 32 * k;
       if (real && d < D)
         *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + out_row * D + d) =
             make_uint2(E::down(y[4 * k] * inv, y[4 * k + 1] * inv), E::down(y[4 * k + 2] * inv, y[4 * k + 3] * inv));
@@ -761,7 +764,14 @@ int launch(TreeArgs& a, int sms, cudaStream_t st) {
   const long long rows = ((long long)a.tokens + a.c.batch - 1) / a.c.batch * (a.q_heads / a.c.kv_heads);
   const int join_blocks = rows >= C::ROWS ? C::ROWS / 32 : (int)(rows + 31) / 32;
   if (const int rc = moe::launch_pdl(tree_kernel<E, DP>, dim3(sms), dim3(kThreads), smem_bytes<C>(), st, a)) return rc;
-  return moe::launch_pdl(join_kernel<E, DP>, dim3(sms, join_blocks), dim3(kJoinThreads), 0, st, a);
+  const long long units = (long long)a.c.batch * a.c.kv_heads * ((rows + C::ROWS - 1) / C::ROWS);
+  // 32 columns a block where the blocks with work are all resident at once, four to an
+  // SM: few units have many pieces each (1 sequence of 300001 slots, 136 rows, D = 256:
+  // 174 us without slices, 163 with; 8 sequences of 504 rows: 123 without, 126 with)
+  constexpr int kSlices = DP / 32;
+  if (units * join_blocks * kSlices <= 4 * sms)
+    return moe::launch_pdl(join_kernel<E, DP, kSlices>, dim3(sms, join_blocks, kSlices), dim3(kJoinThreads), 0, st, a);
+  return moe::launch_pdl(join_kernel<E, DP, 1>, dim3(sms, join_blocks), dim3(kJoinThreads), 0, st, a);
 }
 
 template <class E>
