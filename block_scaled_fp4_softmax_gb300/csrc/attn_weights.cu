@@ -15,6 +15,14 @@
 // share the chunks of two tiles, each with an S buffer of its own: while one
 // waits for its next product, three keep the exponential units busy.
 //
+// Measured: 8 sequences of 16384 slots and 504 rows, D = 128, BF16: 78 us, 0.88
+// PFLOP/s, 3.4 exponentials a ns (the units could do 9); a single-token step of two
+// short caches: 7 us.  Of a CTA's 137000 cycles there, 62000 go to issuing MMAs, 36000
+// to waiting for an S buffer, 16000 for K, 11000 to the start and Q.  Reading the
+// biases (a shared-memory word for every row and warp, beside the operands of the
+// MMAs) costs 11 us, the exponentials 12, half of the MMAs 7; none of them alone
+// is the bound.
+//
 // Work division: attn_plan.h, with units of all rows of a sequence and KV
 // head; tiles are independent, so a cut unit needs no joining.  More rows than
 // Q's room holds are taken in passes over the piece's tiles; each pass adds to
