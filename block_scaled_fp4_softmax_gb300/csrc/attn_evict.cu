@@ -166,9 +166,10 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     for (int j = j0 + 4 * lane; j < j1; j += 128) {
       const uint4 v = keys_at(j);
       const uint32_t k[4] = {v.x, v.y, v.z, v.w};
+      const int live = j1 - j;
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        if (j + q < j1 && (k[q] & above) == prefix)
+        if (q < live && (k[q] & above) == prefix)
           atomicAdd(&sh.hist[round][(k[q] >> shift) & ((1u << bits) - 1u)], 1u);
     }
     cluster.sync();
@@ -218,15 +219,26 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
   }
   // slots with a key above `prefix` stay, and the first `rest` of those equal to it
   int4 cnt = make_int4(0, 0, 0, 0);
-  for (int j = j0 + 4 * lane; j < j1; j += 128) {
-    const uint4 v = keys_at(j);
+  for (int c0 = j0; c0 < j1; c0 += 128) {
+    const int j = c0 + 4 * lane, live = j1 - j;
+    const uint4 v = live > 0 ? keys_at(j) : make_uint4(0u, 0u, 0u, 0u);
     const uint32_t k[4] = {v.x, v.y, v.z, v.w};
+    int gt = 0, eq = 0;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int gt = j + q < j1 && k[q] > prefix, eq = j + q < j1 && k[q] == prefix;
-      cnt.x += gt;
-      cnt.y += eq;
-      if (j + q < K) cnt.z += gt, cnt.w += eq;
+      gt += q < live && k[q] > prefix;
+      eq += q < live && k[q] == prefix;
+    }
+    cnt.x += gt;
+    cnt.y += eq;
+    if (c0 + 128 <= K) {
+      cnt.z += gt, cnt.w += eq;
+    } else if (c0 < K) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        cnt.z += q < live && j + q < K && k[q] > prefix;
+        cnt.w += q < live && j + q < K && k[q] == prefix;
+      }
     }
   }
   cnt.x = __reduce_add_sync(0xffffffffu, cnt.x);
@@ -260,38 +272,30 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
   if (r == 0 && threadIdx.x == 0) a.counts[problem] = K - kept_low;
   int32_t* src = a.src + (long long)problem * K;
   int32_t* dst = a.dst + (long long)problem * K;
+  // here a lane takes every 32nd slot: what the warp writes lies side by side
+  const uint32_t lower_lanes = (1u << lane) - 1u;
   for (int c0 = j0; c0 < j1; c0 += 128) {
-    const int j = c0 + 4 * lane;
-    const uint4 v = j < j1 ? keys_at(j) : make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t k[4] = {v.x, v.y, v.z, v.w};
-    int mine = 0;  // above in the low half, equal in the high
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (j + q < j1) mine += (k[q] > prefix ? 1 : 0) + (k[q] == prefix ? 1 << 16 : 0);
-    int scan = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, scan, d);
-      if (lane >= d) scan += up;
-    }
-    int gt_before = above + ((scan - mine) & 0xFFFF), eq_before = equal + ((scan - mine) >> 16);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      if (j + q >= j1) break;
-      const bool gt = k[q] > prefix, eq = k[q] == prefix;
+      const int j = c0 + 32 * q + lane;
+      const bool live = j < j1;
+      uint32_t key = 0u;
+      if (live) key = KEYS ? keys[j - j0] : rank_key(acc[j], pos[j], a.sinks, recent_from);
+      const bool gt = live && key > prefix, eq = live && key == prefix;
+      const uint32_t all_gt = __ballot_sync(0xffffffffu, gt), all_eq = __ballot_sync(0xffffffffu, eq);
+      const int eq_before = equal + __popc(all_eq & lower_lanes);
       const bool kept = gt || (eq && eq_before < ties);
-      const int kept_before = gt_before + min(eq_before, ties);
-      if (j + q < K) {
-        if (!kept) dst[j + q - kept_before] = j + q;
-      } else if (kept) {
-        src[kept_before - kept_low] = j + q;
+      const int kept_before = above + __popc(all_gt & lower_lanes) + min(eq_before, ties);
+      if (live) {
+        if (j >= K) {
+          if (kept) src[kept_before - kept_low] = j;
+        } else if (!kept) {
+          dst[j - kept_before] = j;
+        }
       }
-      gt_before += gt;
-      eq_before += eq;
+      above += __popc(all_gt);
+      equal += __popc(all_eq);
     }
-    const int all = __shfl_sync(0xffffffffu, scan, 31);
-    above += all & 0xFFFF;
-    equal += all >> 16;
   }
   cluster.sync();  // no CTA leaves while another may still read its shared memory
 }
