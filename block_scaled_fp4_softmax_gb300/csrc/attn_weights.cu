@@ -55,7 +55,9 @@ struct WeightArgs {
   int tokens, q_heads;
   const uint64_t* tree;
   int tree_words;
-  float scale;
+  float c2;         // |scale| in powers of two, rounded
+  double lse_to_2;  // c2 / |scale|: what lse has to be multiplied with to go with c2
+  bool negative;    // the scale
   attn_cache c;
   attn::Maps maps;
   const float* acc;
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
     const int k_steps = (D + 15) / 16;
     const uint64_t q_desc = sw128_kmajor_desc(smem_u32(sQ)), k_desc = sw128_kmajor_desc(smem_u32(sRing));
     const uint32_t high = (uint32_t)(q_desc >> 32), q_low = (uint32_t)q_desc, k_low = (uint32_t)k_desc;
-    const uint32_t negate = a.scale < 0.f ? 1u << 13 : 0u;  // a negative scale negates K, the sums keep |scale|
+    const uint32_t negate = a.negative ? 1u << 13 : 0u;  // a negative scale negates K, the sums keep |scale|
     while (alive && w.next()) {
       const int tiles = w.p.kt1 - w.p.kt0, n_pass = passes(w);
       for (int pass = 0; pass < n_pass && alive; ++pass) {
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
     // ------------------------------------------------------------- sums
     const int buf = warp >> 2, x = buf >> 1, odd = buf & 1, wl = warp & 3;
     const uint32_t lane_base = (uint32_t)(wl * 32) << 16;
-    const float c2 = fabsf(a.scale) * 1.4426950408889634f;
+    const float c2 = a.c2;
     const float2 c22 = make_float2(c2, c2), ones = make_float2(1.f, 1.f);
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
     attn::Walk w(a.cu, a.lens, a.c.batch, a.tokens, dims, ctl.share);
@@ -303,7 +305,9 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
             if (r < rows) {
               const int row = r0 + r, tok = row / G, g = row - tok * G;
               const float lse = a.lse[(long long)(w.s.first + tok) * a.q_heads + w.p.head * G + g];
-              bias = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
+              // in FP64: the rounding of c2 cancels where weights are large, instead of adding up
+              // over all rows
+              bias = lse == -INFINITY ? -INFINITY : (float)(-(double)lse * a.lse_to_2);
             }
             ctl.bias[r] = bias;
           }
@@ -423,8 +427,9 @@ extern "C" int attn_cache_weights(const void* q, long long q_stride, const float
   const int sms = moe::device_info().sms;
   if (sms <= 0) return MOE_ERR_CUDA;
   a.q = q, a.q_stride = q_stride, a.lse = lse, a.cu = cu, a.lens = lens, a.tokens = tokens, a.q_heads = q_heads;
-  a.tree = tree, a.tree_words = tree_words, a.scale = (float)scale, a.acc = acc, a.decay = (float)decay;
+  a.tree = tree, a.tree_words = tree_words, a.acc = acc, a.decay = (float)decay;
   a.acc_out = acc_out, a.slot_cap = slot_cap, a.st = dev_status;
+  a.c2 = (float)(fabs(scale) * 1.4426950408889634), a.lse_to_2 = (double)a.c2 / fabs(scale), a.negative = scale < 0.0;
   const cudaStream_t st = (cudaStream_t)stream;
   return a.c.dtype == ATTN_BF16 ? launch<attn::Brain>(a, sms, st) : launch<attn::Half>(a, sms, st);
 }
