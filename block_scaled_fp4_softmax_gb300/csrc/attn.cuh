@@ -30,17 +30,7 @@ struct Brain {  // BF16
   }
 };
 
-// 8 elements of 16 bits <-> FP32
-template <class E>
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 t = E::up(w[i]);
-    f[2 * i] = t.x;
-    f[2 * i + 1] = t.y;
-  }
-}
+// 8 elements of FP32 -> 16 bits
 template <class E>
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(E::down(f[0], f[1]), E::down(f[2], f[3]), E::down(f[4], f[5]), E::down(f[6], f[7]));

@@ -168,33 +168,14 @@ __device__ __forceinline__ void tmem_ld_wait32(float* r) {
       :
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-      :
-      : "memory");
-}
-// The same; what has been added up into `done` before it in the source stays before
-// it, so that the arithmetic on one group of columns covers the loads of the next.
+// The same for 16 columns; what has been added up into `done` before it in the
+// source stays before it, so that the arithmetic on one group of columns covers
+// the loads of the next.
 __device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16], float2 (&done)[2]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
       : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
         "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
         "+f"(done[0].x), "+f"(done[0].y), "+f"(done[1].x), "+f"(done[1].y)
-      :
-      : "memory");
-}
-// The same as tmem_ld_wait32; what has been added up into `done` before it in the source stays
-// before it, so that the arithmetic on one group of columns covers the loads of
-// the next.
-__device__ __forceinline__ void tmem_ld_wait32(float* r, float2 (&done)[2]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-      : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
-        "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]),
-        "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]),
-        "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])
-        , "+f"(done[0].x), "+f"(done[0].y), "+f"(done[1].x), "+f"(done[1].y)
       :
       : "memory");
 }
