@@ -21,9 +21,11 @@
 //   1 of 1000, 4 rows, D = 128                       15 us
 // Some 20 us of a call do not grow with it: launch, plan and first loads 6 to 8, a
 // change of piece 2 to 5, the join 8 to 11.  With 504 rows the tensor pipe is active
-// for half of the time: an MMA of Q and K takes 87 cycles where its operations need
-// 64, as both operands come from shared memory, one of P and V 70; taking out the
-// exponentials changes nothing, halving the products of Q and K 10 us.
+// for half of the time: an MMA of Q and K takes 85 cycles (65 alone, with no copies
+// into the shared memory that both operands come from), one of P and V 70; taking out
+// the exponentials and maxima gains 2 us, halving either product 10.  With wide heads
+// and a second row group K and V come from L2 twice, 8.2 TB/s in all, and neither the
+// products nor the softmax show in the time.
 //
 // Two streams of tiles run through one CTA, each with its own S and O in TMEM
 // and its own warpgroup, so that one's softmax runs under the other's MMAs.
