@@ -39,7 +39,7 @@ class Config:
     slack: int = 32      # ... once it has so many more
     sinks: int = 4
     recent: int = 16
-    most: int = 64       # tokens in flight of a sequence
+    most: int = 64       # tokens in flight of a sequence; a tree's ancestors are one 64-bit word
     decay: float = 0.95
     eps: float = 1e-6
     base: float = 10000.0
@@ -171,6 +171,8 @@ class Decoder:
         """Tokens that are given: parts[b], maybe none, go behind sequence b as a chain."""
         tokens, pos, cu = [], [], [0]
         for b, t in enumerate(parts):
+            if len(t) > self.cfg.most:
+                raise ValueError(f"sequence {b}: {len(t)} tokens; {self.cfg.most} fit")
             tokens += t
             pos += range(self.next_pos[b], self.next_pos[b] + len(t))
             cu.append(len(tokens))
@@ -183,10 +185,12 @@ class Decoder:
         the logits that chose it."""
         cu, tokens, pos, rows = [0], [], [], []
         for b, (t, parents) in enumerate(drafts):
+            if not 1 <= len(t) <= min(self.cfg.most, 64) or len(t) != len(parents):
+                raise ValueError(f"sequence {b}: {len(t)} tokens and {len(parents)} parents; 1 to {min(self.cfg.most, 64)} fit")
             bits, depth = ancestors(parents)
             tokens += t
             pos += [self.next_pos[b] + d for d in depth]
-            rows += [x - (1 << 64) if x >> 63 else x for x in bits]  # 64 nodes at most: one word each
+            rows += [x - (1 << 64) if x >> 63 else x for x in bits]
             cu.append(len(tokens))
         h, kept, pos, lens = self._forward(tokens, pos, cu, self._ints(rows, torch.int64).view(-1, 1))
         logits = (moe.moe_rmsnorm_bf16(h, self.cfg.eps) @ self.embed.T).float()

@@ -127,6 +127,20 @@ def test_example_keeps_its_budget():
 
 
 @pytest.mark.gpu
+def test_steps_that_do_not_fit_are_refused():
+    decoder = S.Decoder(S.Config(layers=1, **WHOLE), 1)
+    for tree in (([], []), ([1] * 65, [-1] + [0] * 64), ([1, 2], [-1])):
+        with pytest.raises(ValueError):
+            decoder.step([tree])
+    with pytest.raises(ValueError):
+        decoder.prefill([[1] * 65])
+    # a full tree whose last node is bit 63
+    took, logits = decoder.step([([1] * 64, [-1] + list(range(63)))])
+    assert len(took[0]) == len(logits[0]) and decoder.lens == [len(took[0])]
+    decoder.check()
+
+
+@pytest.mark.gpu
 def test_weights_are_what_was_looked_at():
     """Every accepted token hands out one unit of weight per query head."""
     cfg = S.Config(layers=1, budget=256, slack=64, decay=1.0, **WHOLE)
