@@ -56,7 +56,7 @@ __device__ __forceinline__ Seq sequence(const int32_t* __restrict__ cu, const in
 }
 
 // The sequence that token t belongs to: the last b with cu[b] <= t (for
-// ascending cu; any cu gives an index in range, which `sequence` then judges
+// ascending cu; any cu gives an index in range, which `sequence` then checks
 // together with first <= t < first + n).
 __device__ __forceinline__ int sequence_of(const int32_t* __restrict__ cu, int batch, int t) {
   int lo = 0, hi = batch - 1;

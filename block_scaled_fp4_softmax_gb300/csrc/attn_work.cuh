@@ -18,7 +18,7 @@ struct Share {
 
 // Scans the batch with the whole block of THREADS threads: the CTA's range of
 // the line and the sequence it starts in.  False if lens or cu are out of range
-// (the same verdict in every CTA).  Ends with a block barrier.
+// (the same answer in every CTA).  Ends with a block barrier.
 template <int THREADS>
 __device__ bool take_share(const int32_t* __restrict__ cu, const int32_t* __restrict__ lens, int batch, int tokens,
                            long long cap, const PlanDims& d, Share& sh) {
