@@ -23,10 +23,18 @@
 // MMAs) costs 11 us, the exponentials 12, half of the MMAs 7; none of them alone
 // is the bound.
 //
+// Rows are padded to 32 with copies of the pass's first row under a bias of
+// -FLT_MAX: whatever the score, infinities and NaN included, a copy adds nothing
+// that its original does not add too (zeros under -inf would make NaN of an
+// infinite key).  Rows with lse = -inf, whose score may be anything, are picked out
+// one by one; the passes that hold some are flagged.
+//
 // Work division: attn_plan.h, with units of all rows of a sequence and KV
 // head; tiles are independent, so a cut unit needs no joining.  More rows than
 // Q's room holds are taken in passes over the piece's tiles; each pass adds to
 // what the same thread wrote in the one before.
+#include <float.h>
+
 #include "attn_tma.cuh"
 #include "attn_work.cuh"
 
@@ -74,8 +82,9 @@ struct Control {
   attn::Share share;
   uint32_t tmem;
   int abort;
+  int left_out[2];  // whether rows of a pass add nothing, by turns
   float odd[2][2][kTile];  // [tile parity][even, odd of its tiles]: sums of the odd chunks
-  alignas(16) float bias[kMaxRows];  // -lse in powers of two; -inf for rows that add nothing
+  alignas(16) float bias[kMaxRows];  // -lse in powers of two; +inf: the row adds nothing
 };
 constexpr size_t kOffRing = kQBytes, kOffCtrl = kOffRing + (size_t)kSlots * kPanel;
 constexpr size_t kSmem = 1024 + kOffCtrl + sizeof(Control);
@@ -107,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
     mbar_init(&ctl.q_full, kWorkers);
     mbar_init(&ctl.qk_done, 1);
     mbar_init(&ctl.drain, 1);
-    ctl.abort = 0;
+    ctl.abort = ctl.left_out[0] = ctl.left_out[1] = 0;
     mbar_fence_init();
     attn::prefetch_map(&a.maps.k);
   }
@@ -291,9 +300,9 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
           const int first = r0 + (threadIdx.x >> 3), step = kWorkers / 8, step_tok = step / G, step_g = step - step_tok * G;
           int tok = first / G, g = first - tok * G;
           for (int r = threadIdx.x >> 3; r < padded; r += step) {
-            const T* src = r < rows ? q + tok * a.q_stride + g * D : q;
+            const T* src = r < rows ? q + tok * a.q_stride + g * D : q + r0 / G * a.q_stride + r0 % G * D;
             for (int p = 0; p < panels; ++p) {
-              const bool inside = r < rows && p * 64 + ch * 8 < D;
+              const bool inside = p * 64 + ch * 8 < D;
               cp_async16(dst + attn::sw128_offset(r, p * 8 + ch, q_rows), inside ? src + p * 64 : src, inside ? 16u : 0u);
             }
             tok += step_tok, g += step_g;
@@ -301,13 +310,14 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
           }
           cp_async_commit();
           for (int r = threadIdx.x; r < padded; r += kWorkers) {
-            float bias = -INFINITY;
+            float bias = -FLT_MAX;
             if (r < rows) {
               const int row = r0 + r, tok = row / G, g = row - tok * G;
               const float lse = a.lse[(long long)(w.s.first + tok) * a.q_heads + w.p.head * G + g];
               // in FP64: the rounding of c2 cancels where weights are large, instead of adding up
               // over all rows
-              bias = lse == -INFINITY ? -INFINITY : (float)(-(double)lse * a.lse_to_2);
+              bias = (float)(-(double)lse * a.lse_to_2);
+              if (lse == -INFINITY) ctl.left_out[loads & 1] = 1;
             }
             ctl.bias[r] = bias;
           }
@@ -316,6 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
           named_sync(1, kWorkers);
           mbar_arrive(&ctl.q_full);
         }
+        const bool left_out = ctl.left_out[loads & 1] != 0;
+        if (threadIdx.x == 0) ctl.left_out[(loads + 1) & 1] = 0;  // read by all before this pass began
         for (int j = w.p.kt0 + x; j < w.p.kt1; j += 2) {
           const int k0 = j * kTile + wl * 32, slot = k0 + lane;
           const bool mine = !odd && slot < w.s.len + w.s.n;
@@ -336,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
             const int n = min(kChunk, ((rows - g * kChunk) + 31) & ~31);
             const uint32_t from = tmem + lane_base + buf * kChunk;
             uint32_t sa[16];
-            if (!edge) {
+            if (!edge && !left_out) {
               // 16 columns are on their way from TMEM while the 16 before are added up
               uint32_t sb[16];
               auto add = [&](const uint32_t (&s)[16], int half, int i) {
@@ -377,8 +389,9 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                   const uint32_t of_row = __shfl_sync(0xffffffffu, bits, e);
-                  const float p = attn::exp2_fast(fmaf(__uint_as_float(sa[e]), c2, ctl.bias[g * kChunk + i + e]));
-                  if ((of_row >> lane) & 1u) (e & 1 ? sum[0].y : sum[0].x) += p;
+                  const float b = ctl.bias[g * kChunk + i + e];
+                  const float p = attn::exp2_fast(fmaf(__uint_as_float(sa[e]), c2, b));
+                  if (((of_row >> lane) & 1u) && b != INFINITY) (e & 1 ? sum[0].y : sum[0].x) += p;
                 }
               }
             }

@@ -119,7 +119,8 @@ int attn_tree_decode(const void* q, long long q_stride, const int32_t* cu, const
  *                      + sum over tokens i that see j and query heads of h of exp(s_ij - lse_i)
  * for j < lens[b] + tokens in flight; later entries of acc_out are not
  * written.  q, tree and scale as for attn_tree_decode, lse as it wrote it
- * (a row with lse = -inf adds nothing).  acc, acc_out [batch x kv_heads x
+ * (a row with lse = -inf adds nothing, whatever its q holds; a score of -inf adds
+ * 0 as any other weight of 0).  acc, acc_out [batch x kv_heads x
  * slot_cap] FP32, may be the same array.  The sum runs over rows in
  * a fixed order: results are bit-identical between repeated calls.
  * Slots on a bad page become NaN with ATTN_DEV_BAD_PAGE. */
