@@ -25,6 +25,7 @@
 #include <cooperative_groups.h>
 
 #include "attn.cuh"
+#include "attn_slice.h"
 
 namespace cg = cooperative_groups;
 
@@ -98,7 +99,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
   }
   if (bad || n <= K) {  // the whole cluster takes this branch together
     const int m = n < 0 ? 0 : bad ? min(min(n, K), a.slot_cap) : n;
-    for (int j = r * kThreads + threadIdx.x; j < m; j += C * kThreads) {
+    const int share = attn::slice_slots(m, C * kWarps), w = r * kWarps + warp, end = attn::slice_begin(m, share, w + 1);
+    for (int j = attn::slice_begin(m, share, w) + lane; j < end; j += 32) {
       a.acc_out[base + j] = bad ? __uint_as_float(0x7FC00000u) : acc[j];
       a.pos_out[base + j] = bad ? -1 : pos[j];
     }
