@@ -100,9 +100,20 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
   if (bad || n <= K) {  // the whole cluster takes this branch together
     const int m = n < 0 ? 0 : bad ? min(min(n, K), a.slot_cap) : n;
     const int share = attn::slice_slots(m, C * kWarps), w = r * kWarps + warp, end = attn::slice_begin(m, share, w + 1);
-    for (int j = attn::slice_begin(m, share, w) + lane; j < end; j += 32) {
-      a.acc_out[base + j] = bad ? __uint_as_float(0x7FC00000u) : acc[j];
-      a.pos_out[base + j] = bad ? -1 : pos[j];
+    for (int c0 = attn::slice_begin(m, share, w); c0 < end; c0 += 128) {
+      float old[4];
+      int at[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int j = c0 + 32 * q + lane;
+        old[q] = __uint_as_float(0x7FC00000u), at[q] = -1;
+        if (!bad && j < end) old[q] = acc[j], at[q] = pos[j];
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int j = c0 + 32 * q + lane;
+        if (j < end) a.acc_out[base + j] = old[q], a.pos_out[base + j] = at[q];
+      }
     }
     if (r == 0 && threadIdx.x == 0) a.counts[problem] = 0;
     return;
