@@ -118,8 +118,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     if (r == 0 && threadIdx.x == 0) a.counts[problem] = 0;
     return;
   }
-  const int sub = ((n + C * kWarps - 1) / (C * kWarps) + 127) & ~127;
-  const int j0 = min((r * kWarps + warp) * sub, n), j1 = min(j0 + sub, n);
+  const int sub = attn::slice_slots(n, C * kWarps);
+  const int j0 = attn::slice_begin(n, sub, r * kWarps + warp), j1 = attn::slice_begin(n, sub, r * kWarps + warp + 1);
   uint32_t* keys = s_keys + warp * sub;
   auto fetch = [&](int j, float4& w, int4& p) {  // slots j .. j + 3; nothing past the end
     w = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -439,7 +439,7 @@ int select(const EvictArgs& a, int problems, int sms, cudaStream_t st) {
   // one CTA a problem, more while SMs are idle and a CTA has more than two rounds of slots
   int C = 1;
   while (C < kMaxCluster && problems * C < sms && a.slot_cap > 2 * kThreads * C) C *= 2;
-  auto slots = [&](int c) { return (((a.slot_cap + c * kWarps - 1) / (c * kWarps) + 127) & ~127) * kWarps; };  // of a CTA
+  auto slots = [&](int c) { return (long long)attn::slice_slots(a.slot_cap, c * kWarps) * kWarps; };  // of a CTA
   const bool keys = slots(C) <= kMaxKeys;
   if (C == 16 && !(keys ? sixteen_fit<true, VEC>() : sixteen_fit<false, VEC>())) C = 8;
   return slots(C) <= kMaxKeys ? launch_select<true, VEC>(a, problems, C, sizeof(Shared) + (size_t)slots(C) * 4, st)

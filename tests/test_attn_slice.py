@@ -25,3 +25,5 @@ def test_the_kernel_takes_its_slots_from_there():
     select = text[text.index("select_kernel("):text.index("constexpr int kMoveThreads")]
     assert "C * kThreads" not in select
     assert "slice_begin" in select
+    # nor is a slice's size or end formed anywhere else
+    assert "j0 + sub" not in text and "* sub" not in select.replace("warp * sub;", "") and "+ 127" not in text
