@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const __grid_
   // pairs 2 j and 2 j + 1 of a token at [j % 2][j / 2]: magnitude * (cos, cos', sin, sin')
   __shared__ float4 s_cs[kTokens][2][33];
   __shared__ int s_pos[kTokens], s_seq[kTokens], s_slot[kTokens];  // slot -1: out of range
-  __shared__ long long s_off[kTokens];                             // of the slot in head 0, -1: bad page
+  __shared__ long long s_off[kTokens];                             // of the slot in head 0, -1: nothing is appended
   __shared__ float s_row[P == kScattered ? kGroups : 1][P == kScattered ? LANES * 8 + 4 : 1];
   const int D = a.c.head_dim, half = a.rot / 2;
   const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
@@ -146,9 +146,11 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const __grid_
       s_pos[threadIdx.x] = __ldg(a.pos + tt);
       s_seq[threadIdx.x] = b;
       s_slot[threadIdx.x] = ok ? slot : -1;
-      s_off[threadIdx.x] = ok ? attn::slot_offset(a.c, b, slot, 0) : -1;
-      if (!ok || (a.slot_pos && slot >= a.slot_cap)) moe::status_or(a.st, ATTN_DEV_BAD_LENGTH);
-      if (ok && s_off[threadIdx.x] < 0) moe::status_or(a.st, ATTN_DEV_BAD_PAGE);
+      // a slot without a position would be lost on attn_cache_evict: it is not filled either
+      const bool fits = ok && (!a.slot_pos || slot < a.slot_cap);
+      s_off[threadIdx.x] = fits ? attn::slot_offset(a.c, b, slot, 0) : -1;
+      if (!fits) moe::status_or(a.st, ATTN_DEV_BAD_LENGTH);
+      else if (s_off[threadIdx.x] < 0) moe::status_or(a.st, ATTN_DEV_BAD_PAGE);
     }
     for (int m = threadIdx.x / 128; m < n_tok; m += kThreads / 128) {
       const int j = threadIdx.x % 128;
@@ -267,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const __grid_
         T* dst = static_cast<T*>(is_k ? a.c.k : a.c.v) + off + hk * a.c.head_stride;
         *reinterpret_cast<uint2*>(dst + c0) = out[0];
         *reinterpret_cast<uint2*>(dst + c1) = out[1];
-        if (is_k && lane == 0 && a.slot_pos && slot < a.slot_cap)
+        if (is_k && lane == 0 && a.slot_pos)
           a.slot_pos[((long long)s_seq[i] * a.c.kv_heads + hk) * a.slot_cap + slot] = s_pos[i];
       }
     }

@@ -1,5 +1,5 @@
 """The attention operators where include/attn.h promises something that random
-inputs do not show: infinite keys, rows that add nothing."""
+inputs do not show: infinite keys, rows that add nothing, slots without a position."""
 import numpy as np
 import pytest
 import torch
@@ -69,3 +69,32 @@ def test_rows_without_weight_add_nothing(dtype, dim, group, new):
     acc = torch.rand(2, 2, bt.cap, device="cuda")
     got = attn.attn_cache_weights(bt.q, lse, bt.cu, bt.lens, bt.cache, acc, tree=bt.tree, decay=0.875)
     weights_near(bt, lse, acc, got, bound)
+
+
+# ---------------------------------------------------------------------------
+# Norm, rotation, append
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("cap,fits", [(42, 2), (40, 0), (44, 4)])
+def test_a_slot_that_has_no_position_is_not_appended(cap, fits):
+    """Tokens whose slots `slot_pos` does not hold: no row, no position, but the rotated q."""
+    bt = Batch(BF, [40, 5], [4, 2], 2, 3, 64, 16, seed=3)
+    pos = torch.tensor([40, 41, 42, 43, 5, 6], dtype=torch.int32, device="cuda")
+    freq = (10000.0 ** (-torch.arange(0, 64, 2, dtype=torch.float64) / 64)).cuda()
+    k0, v0 = bt.k.clone(), bt.v.clone()
+    want_q = attn.attn_qk_norm_rope(bt.q, bt.k_new, bt.v_new, pos, bt.cu, bt.lens, bt.cache, freq)
+    k1, v1 = bt.k.clone(), bt.v.clone()
+    bt.k.copy_(k0), bt.v.copy_(v0)
+    slot_pos = torch.full((2, 2, cap), -9, dtype=torch.int32, device="cuda")
+    q = attn.attn_qk_norm_rope(bt.q, bt.k_new, bt.v_new, pos, bt.cu, bt.lens, bt.cache, freq, slot_pos=slot_pos,
+                               dev_status=bt.status)
+    assert int(bt.status) == (0 if fits == 4 else attn.DEV_BAD_LENGTH)
+    assert torch.equal(q, want_q)
+    page, row = bt.rows(0)
+    for s in range(40 + fits, 44):
+        k1[page[s], :, row[s]], v1[page[s], :, row[s]] = k0[page[s], :, row[s]], v0[page[s], :, row[s]]
+    assert torch.equal(bt.k.view(torch.int16), k1.view(torch.int16)) and torch.equal(bt.v.view(torch.int16), v1.view(torch.int16))
+    want = torch.full_like(slot_pos, -9)
+    want[0, :, 40:40 + fits] = pos[:fits]
+    want[1, :, 5:7] = pos[4:]
+    assert torch.equal(slot_pos, want)
