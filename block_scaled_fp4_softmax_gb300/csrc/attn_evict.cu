@@ -6,7 +6,10 @@
 //
 // Selection is a radix select on 32-bit keys whose unsigned order is the
 // ranking (protected slots all ones, FP32 weights order-preserving, NaN 0),
-// 11 + 11 + 10 bits a round, by one cluster of CTAs per (sequence, head).  Each
+// 11 + 11 + 10 bits a round, by one cluster of CTAs per (sequence, head).  All
+// protected slots stay as a rule, whatever their order; where the first round finds
+// that they alone fill the budget, the keys are formed anew, of the protected slots'
+// weights and 0 for the others, and the rounds begin again.  Each
 // CTA keeps its slice's keys in shared memory, so acc and slot_pos are read
 // once; a round counts digits into a shared histogram, and every CTA adds up
 // the cluster's histograms through distributed shared memory.  The result is
@@ -53,9 +56,11 @@ struct EvictArgs {
   int32_t* st;
 };
 
-__device__ __forceinline__ uint32_t rank_key(float w, int pos, int sinks, long long recent_from) {
-  if (pos < sinks || pos >= recent_from) return 0xFFFFFFFFu;
-  if (w != w) return 0u;
+// `of_held`: of the protected slots' weights (NaN 1), 0 for the others.
+__device__ __forceinline__ uint32_t rank_key(float w, int pos, int sinks, long long recent_from, bool of_held) {
+  const bool held = pos < sinks || pos >= recent_from;
+  if (held != of_held) return held ? 0xFFFFFFFFu : 0u;
+  if (w != w) return of_held ? 1u : 0u;
   const uint32_t u = __float_as_uint(w == 0.f ? 0.f : w);
   return (u >> 31) ? ~u : u | 0x80000000u;
 }
@@ -134,9 +139,10 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     if (j + 2 < n) w.z = acc[j + 2], p.z = pos[j + 2];
     if (j + 3 < n) w.w = acc[j + 3], p.w = pos[j + 3];
   };
+  bool of_held = false;
+  auto key_of = [&](float w, int p) { return rank_key(w, p, a.sinks, recent_from, of_held); };
   auto keys_of = [&](const float4& w, const int4& p) {
-    return make_uint4(rank_key(w.x, p.x, a.sinks, recent_from), rank_key(w.y, p.y, a.sinks, recent_from),
-                      rank_key(w.z, p.z, a.sinks, recent_from), rank_key(w.w, p.w, a.sinks, recent_from));
+    return make_uint4(key_of(w.x, p.x), key_of(w.y, p.y), key_of(w.z, p.z), key_of(w.w, p.w));
   };
   auto keys_at = [&](int j) {
     if (KEYS) return *reinterpret_cast<const uint4*>(keys + (j - j0));
@@ -176,6 +182,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     const int shift = round == 0 ? 21 : round == 1 ? 10 : 0;
     const int bits = round == 2 ? 10 : 11;
     const uint32_t above = round == 0 ? 0u : 0xFFFFFFFFu << (shift + bits);
+    uint32_t* const hist = sh.hist[of_held ? (round + 1) % 3 : round];  // one that is all zeros
     for (int j = j0 + 4 * lane; j < j1; j += 128) {
       const uint4 v = keys_at(j);
       const uint32_t k[4] = {v.x, v.y, v.z, v.w};
@@ -183,9 +190,11 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         if (q < live && (k[q] & above) == prefix)
-          atomicAdd(&sh.hist[round][(k[q] >> shift) & ((1u << bits) - 1u)], 1u);
+          atomicAdd(&hist[(k[q] >> shift) & ((1u << bits) - 1u)], 1u);
     }
     cluster.sync();
+    if (of_held && round == 0)  // no CTA looks at the first histogram any more
+      for (int i = threadIdx.x; i < kBins; i += kThreads) sh.hist[0][i] = 0;
     // thread i: bins kBins - 1 - 2i and the one below, over the cluster.  Up to four
     // CTAs each read all histograms; more share the bins out and hand the sums
     // round (16 CTAs reading 16 histograms took 12000 cycles a round).
@@ -193,7 +202,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     uint32_t n_hi = 0, n_lo = 0;
     if (C <= 4) {
       for (int q = 0; q < C; ++q) {
-        const uint32_t* other = cluster.map_shared_rank(&sh.hist[round][0], q);
+        const uint32_t* other = cluster.map_shared_rank(hist, q);
         const uint2 v = *reinterpret_cast<const uint2*>(other + hi - 1);
         n_lo += v.x;
         n_hi += v.y;
@@ -201,8 +210,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     } else {
       const int slice = kBins / C, half = C / 2;  // threads: bin of the slice x pair of CTAs
       const int bin = r * slice + (int)threadIdx.x % slice, pair = threadIdx.x / slice;
-      sh.part[threadIdx.x] = cluster.map_shared_rank(&sh.hist[round][0], pair)[bin] +
-                             cluster.map_shared_rank(&sh.hist[round][0], pair + half)[bin];
+      sh.part[threadIdx.x] = cluster.map_shared_rank(hist, pair)[bin] +
+                             cluster.map_shared_rank(hist, pair + half)[bin];
       __syncthreads();
       uint32_t sum = 0;
       for (int q = 0; q < half; ++q) sum += sh.part[q * slice + (int)threadIdx.x % slice];
@@ -229,6 +238,17 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     __syncthreads();
     prefix |= sh.digit << shift;
     rest = sh.rest;
+    if (round == 0 && !of_held && prefix >> shift == kBins - 1) {  // (no weight has this digit)
+      of_held = true;
+      if (KEYS)
+        for (int j = j0 + 4 * lane; j < j1; j += 128) {
+          float4 w;
+          int4 p;
+          fetch(j, w, p);
+          *reinterpret_cast<uint4*>(keys + (j - j0)) = keys_of(w, p);
+        }
+      prefix = 0, rest = (uint32_t)K, round = -1;
+    }
   }
   // slots with a key above `prefix` stay, and the first `rest` of those equal to it
   int4 cnt = make_int4(0, 0, 0, 0);
@@ -293,7 +313,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
       const int j = c0 + 32 * q + lane;
       const bool live = j < j1;
       uint32_t key = 0u;
-      if (live) key = KEYS ? keys[j - j0] : rank_key(acc[j], pos[j], a.sinks, recent_from);
+      if (live) key = KEYS ? keys[j - j0] : key_of(acc[j], pos[j]);
       const bool gt = live && key > prefix, eq = live && key == prefix;
       const uint32_t all_gt = __ballot_sync(0xffffffffu, gt), all_eq = __ballot_sync(0xffffffffu, eq);
       const int eq_before = equal + __popc(all_eq & lower_lanes);

@@ -136,7 +136,8 @@ size_t attn_cache_evict_workspace(const attn_cache* cache, int budget);
 /* Shrinks every sequence with more than `budget` slots to `budget`, for each
  * KV head on its own.  Slots are ranked: protected ones first (slot_pos <
  * sinks or slot_pos >= next_pos[b] - recent), then the larger acc (NaN counts as the
- * least), then the lower slot; the first `budget` stay.  Attention over keys
+ * least), then the lower slot; the first `budget` stay (of more protected
+ * slots than that, those with the larger acc).  Attention over keys
  * that are rotated already does not depend on their order, so nothing is
  * shifted: the kept slots from `budget` on move, in order, into the dropped
  * slots below `budget`, in order.  Only those rows of k and v are copied.

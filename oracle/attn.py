@@ -76,9 +76,8 @@ def evict(acc, pos, budget, sinks, recent, next_pos):
 
     def key(j):  # protected, then larger weight, NaN below every number, then lower slot
         w = float(acc[j])
-        if pos[j] < sinks or pos[j] >= next_pos - recent:
-            return (0, 0.0, j)
-        return (2, 0.0, j) if w != w else (1, -w, j)
+        free = not (pos[j] < sinks or pos[j] >= next_pos - recent)
+        return (free, True, 0.0, j) if w != w else (free, False, -w, j)
 
     stays = set(sorted(range(n), key=key)[:budget])
     holes = [j for j in range(budget) if j not in stays]

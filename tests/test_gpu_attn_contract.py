@@ -1,12 +1,13 @@
 """The attention operators where include/attn.h promises something that random
-inputs do not show: infinite keys, rows that add nothing, slots without a position."""
+inputs do not show: infinite keys, rows that add nothing, slots without a position, more
+protected slots than stay."""
 import numpy as np
 import pytest
 import torch
 
 from attn_helpers import Batch, f64, trees
 from block_scaled_fp4_softmax_gb300 import attn
-from test_gpu_attn import BF, FP, attend
+from test_gpu_attn import BF, FP, attend, run_evict
 
 pytestmark = pytest.mark.gpu
 
@@ -98,3 +99,41 @@ def test_a_slot_that_has_no_position_is_not_appended(cap, fits):
     want[0, :, 40:40 + fits] = pos[:fits]
     want[1, :, 5:7] = pos[4:]
     assert torch.equal(slot_pos, want)
+
+
+# ---------------------------------------------------------------------------
+# Eviction
+# ---------------------------------------------------------------------------
+
+def test_protected_slots_are_ranked_by_weight():
+    bt = Batch(BF, [5], [0], 1, 1, 64, 16, seed=1)
+    acc, pos = torch.zeros(1, 1, 8, device="cuda"), torch.arange(8, dtype=torch.int32, device="cuda").view(1, 1, 8)
+    acc[0, 0, :5] = torch.tensor([9.0, 1.0, 5.0, 7.0, 3.0])
+    _, acc_out, pos_out = attn.attn_cache_evict(bt.cache, acc, pos, bt.lens, bt.lens, 3, recent=5)
+    assert pos_out[0, 0, :3].tolist() == [0, 3, 2] and acc_out[0, 0, :3].tolist() == [9.0, 7.0, 5.0]
+
+
+@pytest.mark.parametrize("lens,hk,page,budget,over", [
+    ([900, 40, 700], 2, 16, 500, 37),           # one CTA, beside sequences that have room
+    ([5000, 4001], 2, 64, 1000, 1),             # clusters of two and four
+    ([900, 2000], 1, 16, 800, 0),               # exactly as many as stay
+    ([70001], 1, 1024, 30001, 20011),           # 16 CTAs, rows not on 16 bytes
+    ([420000], 1, 4096, 200001, 777),           # the same, aligned
+    ([46001, 50, 45999] + [7] * 17, 8, 1024, 20011, 5000),  # keys that shared memory does not hold
+])
+@pytest.mark.parametrize("kind", ["ties", "special"])
+def test_more_protected_slots_than_the_budget(lens, hk, page, budget, over, kind):
+    """`over` protected slots too many: by weight, then by slot, NaN last."""
+    bt = Batch(BF, lens, [0] * len(lens), hk, 1, 16, page, seed=budget + over)
+    g = torch.Generator(device="cuda").manual_seed(over)
+    if kind == "ties":
+        acc = torch.rand(bt.B, hk, bt.cap, generator=g, device="cuda").mul_(300).round_()
+    else:
+        vals = torch.tensor([0.0, -0.0, float("nan"), float("inf"), -float("inf"), 1e-42, -1.0, 3.0, -float("nan")], device="cuda")
+        acc = vals[torch.randint(0, len(vals), (bt.B, hk, bt.cap), generator=g, device="cuda")]
+    # each sequence's positions are a permutation of 0 .. n - 1, in random order
+    pos = torch.full((bt.B, hk, bt.cap), -1, dtype=torch.int32, device="cuda")
+    for b, n in enumerate(lens):
+        pos[b, :, :n] = torch.rand(hk, n, generator=g, device="cuda").argsort(dim=-1).to(torch.int32)
+    sinks = 4
+    run_evict(bt, acc, pos, lens, torch.tensor(lens, dtype=torch.int32, device="cuda"), budget, sinks, budget + over - sinks)
