@@ -5,7 +5,7 @@ function carries the C entry point's name, checks types and devices, allocates
 what the caller does not pass, and hands device pointers plus the current CUDA
 stream to the library.  A serving loop makes one :func:`attn_cache` handle per
 layer and keeps its workspaces; the calls then touch no allocator when every
-output is passed.
+output is passed.  The cache's device has to be the current one.
 """
 
 from __future__ import annotations
@@ -113,11 +113,20 @@ def attn_cache(k, v, page_table) -> AttnCache:
 # one.
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current = torch._C._cuda_getDevice
 _i32, _i64, _f32, _f64, _u8 = torch.int32, torch.int64, torch.float32, torch.float64, torch.uint8
 
 
 def _on(stream, cache):
-    return _raw_stream(cache.index) if stream is None else stream.cuda_stream
+    """Handle of the stream to launch on.  A launch goes to the device that is
+    current: any other than the cache's is refused, before anything else is done."""
+    if _current() != cache.index:
+        raise MoeError(f"the cache is on {cache.device}, cuda:{_current()} is current")
+    if stream is None:
+        return _raw_stream(cache.index)
+    if stream.device_index != cache.index:
+        raise MoeError(f"the cache is on {cache.device}, the stream on cuda:{stream.device_index}")
+    return stream.cuda_stream
 
 
 def _rows(t, name, heads, cache):
@@ -180,6 +189,7 @@ def attn_qk_norm_rope(q, k, v, pos, cu, lens, cache: AttnCache, inv_freq, q_weig
                       dev_status=None, stream=None):
     """Head norm and rotation of q and k, append of k and v.  inv_freq [rot /
     2] FP64: radians per position.  Returns q_out [tokens, q_heads, D]."""
+    on = _on(stream, cache)
     sq, sk, sv = _rows(q, "q", None, cache), _rows(k, "k", cache.kv_heads, cache), _rows(v, "v", cache.kv_heads, cache)
     T, hq, D = q.shape
     if k.shape[0] != T or v.shape[0] != T:
@@ -205,7 +215,7 @@ def attn_qk_norm_rope(q, k, v, pos, cu, lens, cache: AttnCache, inv_freq, q_weig
         _array(cu, "cu", cache.cu_shape, _i32, cache), _array(lens, "lens", cache.lens_shape, _i32, cache),
         T, hq, wq, wk, eps, _array(inv_freq, "inv_freq", (half,), _f64, cache), 2 * half, interleaved,
         magnitude, to, at, cap, cache.ref,
-        _status(dev_status, cache), _on(stream, cache))
+        _status(dev_status, cache), on)
     if rc:
         _check(rc, "attn_qk_norm_rope")
     return q_out
@@ -224,6 +234,7 @@ def attn_tree_decode(q, cu, lens, cache: AttnCache, tree=None, scale: float | No
                      workspace=None, dev_status=None, stream=None):
     """Attention of the tokens in flight over the cache; tree = None: a chain.
     Returns (out [tokens, q_heads, D], lse [tokens, q_heads])."""
+    on = _on(stream, cache)
     sq = _rows(q, "q", None, cache)
     T, hq, D = q.shape
     words, count = _tree(tree, T, cache)
@@ -241,8 +252,7 @@ def attn_tree_decode(q, cu, lens, cache: AttnCache, tree=None, scale: float | No
         _array(lens, "lens", cache.lens_shape, _i32, cache), T, hq, words, count,
         D ** -0.5 if scale is None else scale, cache.ref, _array(out, "out", (T, hq, D), cache.dtype, cache),
         _array(lse, "lse", (T, hq), _f32, cache),
-        _array(workspace, "workspace", (size,), _u8, cache), size, _status(dev_status, cache),
-        _on(stream, cache))
+        _array(workspace, "workspace", (size,), _u8, cache), size, _status(dev_status, cache), on)
     if rc:
         _check(rc, "attn_tree_decode")
     return out, lse
@@ -253,6 +263,7 @@ def attn_cache_weights(q, lse, cu, lens, cache: AttnCache, acc, tree=None, scale
     """acc_out = decay * acc + the softmax weight each slot received.  acc
     [batch, kv_heads, slot_cap]; acc_out may be acc; entries past a sequence's
     end are not written (a new acc_out starts as zeros)."""
+    on = _on(stream, cache)
     sq = _rows(q, "q", None, cache)
     T, hq, D = q.shape
     words, count = _tree(tree, T, cache)
@@ -265,7 +276,7 @@ def attn_cache_weights(q, lse, cu, lens, cache: AttnCache, acc, tree=None, scale
         _array(cu, "cu", cache.cu_shape, _i32, cache), _array(lens, "lens", cache.lens_shape, _i32, cache),
         T, hq, words, count, D ** -0.5 if scale is None else scale, cache.ref,
         _array(acc, "acc", shape, _f32, cache), decay, _array(acc_out, "acc_out", shape, _f32, cache),
-        shape[2], _status(dev_status, cache), _on(stream, cache))
+        shape[2], _status(dev_status, cache), on)
     if rc:
         _check(rc, "attn_cache_weights")
     return acc_out
@@ -284,6 +295,7 @@ def attn_cache_evict(cache: AttnCache, acc, slot_pos, lens, next_pos, budget: in
     """Keeps the `budget` slots of each sequence and KV head with the most
     weight and moves their rows below the budget, in place.  Returns
     (lens_out, acc_out, pos_out)."""
+    on = _on(stream, cache)
     shape = (cache.batch, cache.kv_heads, acc.shape[-1])
     if acc_out is None or pos_out is None or lens_out is None or workspace is None:
         with _elsewhere(stream):
@@ -302,8 +314,7 @@ def attn_cache_evict(cache: AttnCache, acc, slot_pos, lens, next_pos, budget: in
         _array(next_pos, "next_pos", cache.lens_shape, _i32, cache), budget, sinks, recent,
         _array(acc_out, "acc_out", shape, _f32, cache), _array(pos_out, "pos_out", shape, _i32, cache),
         _array(lens_out, "lens_out", cache.lens_shape, _i32, cache),
-        _array(workspace, "workspace", (size,), _u8, cache), size, _status(dev_status, cache),
-        _on(stream, cache))
+        _array(workspace, "workspace", (size,), _u8, cache), size, _status(dev_status, cache), on)
     if rc:
         _check(rc, "attn_cache_evict")
     return lens_out, acc_out, pos_out

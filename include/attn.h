@@ -3,7 +3,8 @@
  * GB300 (sm_103a).  Same library, same conventions as moe.h: device pointers
  * owned by the caller, no state and no allocation, `stream` a cudaStream_t as
  * void*, a moe_status as the return value, device-side errors OR-ed into the
- * optional word `dev_status`.
+ * optional word `dev_status`.  Calls launch on the current device, which has to
+ * be the one that the pointers and the stream belong to.
  *
  * The step sits between a layer's q/k/v projections and its routed-MoE part,
  * for sequences that each have some tokens in flight: one (plain decode), a
