@@ -20,6 +20,11 @@ struct Maps {
   int head_inner;  // heads lie closer together than rows
 };
 
+// Cycles of a wait in the kernels: at most 2.07 of them are a ns.
+inline long long wait_cycles() { return 2 * (long long)moe::wait_limit_ns(); }
+// ... of one behind which shared memory or TMEM is given up: some 2 s, whatever the others' limit.
+constexpr long long kDrainCycles = 4000000000ll;
+
 inline int make_map(const attn_cache& c, void* base, int box_rows, bool head_inner, CUtensorMap* m) {
   typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -60,15 +65,17 @@ inline int make_maps(const attn_cache& c, int tile, Maps& m) {
 // ---------------------------------------------------------------------------
 
 // Waits for the barrier's phase.  The first tries run without a clock, whose
-// reads are slow; after some 2 s (4e9 cycles), or once another role of the CTA has
-// given up (*abort), the wait gives up too: MOE_DEV_TIMEOUT, *abort set, false.
-__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* st) {
+// reads are slow; after `limit` cycles, or once another role of the CTA has given
+// up (*abort), the wait gives up too: MOE_DEV_TIMEOUT, *abort set, false.  Lanes of
+// a warp may part here, one by one: what a warp does together takes a vote.
+__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, long long limit, volatile int* abort,
+                                             int32_t* st) {
   for (int i = 0; i < 64; ++i)
     if (moe::tc::mbar_test(bar, parity)) return true;
   const long long from = clock64();
   while (!moe::tc::mbar_test(bar, parity)) {
     if (abort && *abort) return false;
-    if (clock64() - from > 4000000000ll) {
+    if (clock64() - from > limit) {
       moe::status_or(st, MOE_DEV_TIMEOUT);
       if (abort) *abort = 1;
       return false;

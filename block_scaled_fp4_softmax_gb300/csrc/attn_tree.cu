@@ -73,6 +73,8 @@ struct TreeArgs {
   float scale;
   attn_cache c;
   attn::Maps maps;
+  long long wait_cycles;
+  int extra;  // arrivals that never come, on p_full
   void* out;
   float* lse;
   int32_t* st;
@@ -186,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     for (int x = 0; x < 2; ++x) {
       mbar_init(&ctl.s_full[x], 1);
       mbar_init(&ctl.p_half[x], 4);
-      mbar_init(&ctl.p_full[x], 4);
+      mbar_init(&ctl.p_full[x], 4 + a.extra);
       mbar_init(&ctl.o_full[x], 1);
     }
     mbar_init(&ctl.q_full, kWorkers);
@@ -224,7 +226,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   fence_after_sync();
   const uint32_t tmem = ctl.tmem;
   volatile int* abort_flag = &ctl.abort;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return attn::bounded_wait(bar, parity, abort_flag, a.st); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return attn::bounded_wait(bar, parity, a.wait_cycles, abort_flag, a.st);
+  };
+  // for what a warp does together: it goes on, or gives up, as one
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
 
   // A role ends inside its branch: code behind the branches would run with either
   // number of registers.
@@ -264,8 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv, ++pos) {
             const int slot = pos % C::SLOTS;
-            alive = alive && wait(&ctl.empty[slot], ((pos / C::SLOTS) & 1) ^ 1);
-            alive = __all_sync(0xffffffffu, alive);
+            alive = warp_wait(&ctl.empty[slot], ((pos / C::SLOTS) & 1) ^ 1);
             if (!alive) break;
             if (lane == 0) mbar_arrive_expect_tx(&ctl.full[slot], (uint32_t)(issued * box_rows * 128 * panels));
             __syncwarp();
@@ -280,12 +285,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       // every copy has landed before the CTA's shared memory goes away
       if (lane == 0)
         for (int i = max(0, pos - C::SLOTS); i < pos; ++i) {
-          attn::bounded_wait(&ctl.full[i % C::SLOTS], (i / C::SLOTS) & 1, nullptr, a.st);
+          attn::bounded_wait(&ctl.full[i % C::SLOTS], (i / C::SLOTS) & 1, attn::kDrainCycles, nullptr, a.st);
         }
       __syncwarp();
     } else if (warp == kMmaWarp) {
       // ----------------------------------------------------------- MMA
-      // The warp walks and waits as one, its elected lane issues.  What it does between
+      // The warp walks as one, its elected lane issues.  Every lane waits for itself and
+      // they vote once a product, behind its MMAs, whether to go on (a vote after
+      // every wait cost 8% of the whole kernel's time).  What it does between
       // the MMAs is kept short: at 128 keys and 128 elements a product takes 512 cycles,
       // and the tensor core idles while the next one's operands are worked out.
       const bool leader = attn::elect_lane();
@@ -308,16 +315,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       while (alive && w.next()) {
         const bool both = C::STREAMS == 2 && w.rows > 128;  // two row tiles over the same keys
         const int tiles = w.p.kt1 - w.p.kt0, items = both ? 2 * tiles : tiles;
-        alive = wait(&ctl.q_full, pieces & 1);
+        alive = warp_wait(&ctl.q_full, pieces & 1);
         if (!alive) break;
         fence_after_sync();
         auto qk = [&](int it) {
           const int x = it & 1;
+          bool ok = true;  // of this lane's waits; the vote behind the MMAs makes it the warp's
           if (!both || x == 0) {
-            if (!wait(&ctl.full[k_slot], k_round & 1)) return false;
+            ok = wait(&ctl.full[k_slot], k_round & 1);
             fence_after_sync();
           }
-          if (leader) {
+          if (leader && ok) {
             uint32_t ql = q_low + (both && x ? C::QTILE >> 4 : 0), kl = k_low + (uint32_t)k_slot * (C::SLOT >> 4);
             const uint32_t d = tmem + C::S_COL + x * C::BN;
             uint32_t more = 0;
@@ -332,9 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             if (!both || x == 1) mma_commit(&ctl.empty[k_slot]);
             if (it == items - 1) mma_commit(&ctl.qk_done);
           }
-          __syncwarp();
           if (!both || x == 1) on(k_slot, k_round);
-          return true;
+          return __all_sync(0xffffffffu, ok) != 0;
         };
         auto pv = [&](int it) {
           const int x = it & 1, st = C::STREAMS == 2 ? x : 0;  // whose O
@@ -342,18 +349,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           const uint32_t vl = v_low + (uint32_t)v_slot * (C::SLOT >> 4), seen = (p_odd >> x) & 1;
           const uint32_t more = it >= C::STREAMS;
           p_odd ^= 1u << x;
-          if ((!both || x == 0) && !wait(&ctl.full[v_slot], v_round & 1)) return false;
-          if (!wait(&ctl.p_half[x], seen)) return false;
+          bool ok = (both && x != 0) || wait(&ctl.full[v_slot], v_round & 1);
+          ok = ok && wait(&ctl.p_half[x], seen);
           fence_after_sync();
-          if (leader) {
+          if (leader && ok) {
 #pragma unroll
             for (int kk = 0; kk < C::BN / 32; ++kk)
               attn::mma_ts(o, p + kk * 8, attn::make_desc(v_high, vl + kk * (2048 >> 4)), id_o, kk ? 1 : more);
           }
           __syncwarp();
-          if (!wait(&ctl.p_full[x], seen)) return false;
+          ok = ok && wait(&ctl.p_full[x], seen);
           fence_after_sync();
-          if (leader) {
+          if (leader && ok) {
 #pragma unroll
             for (int kk = C::BN / 32; kk < C::BN / 16; ++kk)
               attn::mma_ts(o, p + kk * 8, attn::make_desc(v_high, vl + kk * (2048 >> 4)), id_o, 1);
@@ -361,9 +368,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             if (C::STREAMS == 1) mma_commit(&ctl.pv_done);
             if (it >= items - C::STREAMS) mma_commit(&ctl.o_full[st]);
           }
-          __syncwarp();
           if (!both || x == 1) on(v_slot, v_round);
-          return true;
+          return __all_sync(0xffffffffu, ok) != 0;
         };
         alive = qk(0);
         for (int it = 0; it < items && alive; ++it) {
@@ -376,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       __syncwarp();
       if (leader) {
         mma_commit(&ctl.drain);
-        attn::bounded_wait(&ctl.drain, 0, nullptr, a.st);
+        attn::bounded_wait(&ctl.drain, 0, attn::kDrainCycles, nullptr, a.st);
       }
       __syncwarp();
     }
@@ -393,8 +399,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
       const uint32_t o_addr = tmem + lane_base + C::O_COL + st * DP;
       const float c2 = fabsf(a.scale) * 1.4426950408889634f;
       constexpr float kLift = Weight<E>::kLift, kLag = Weight<E>::kLag;
-      // the TMEM accesses below need whole warps: a warp gives up together
-      auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
       attn::Walk w(a.cu, a.lens, a.c.batch, a.tokens, dims, ctl.share);
       int pos = 0, s_seen[2] = {0, 0}, o_seen = 0, pieces = 0, pv_seen = 0;
       bool alive = true;
@@ -822,6 +826,7 @@ int attn_tree_decode(const void* q, long long q_stride, const int32_t* cu, const
   const Layout w = layout(sms, a.c.head_dim);
   if (ws_bytes < w.bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
   a.q = q, a.q_stride = q_stride, a.cu = cu, a.lens = lens, a.tokens = tokens, a.q_heads = q_heads;
+  a.wait_cycles = attn::wait_cycles(), a.extra = (int)moe::barrier_extra();
   a.tree = tree, a.tree_words = tree_words, a.scale = (float)scale, a.out = out, a.lse = lse, a.st = dev_status;
   a.splits = static_cast<Split*>(workspace);
   a.ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.ml);

@@ -68,6 +68,8 @@ struct WeightArgs {
   bool negative;    // the scale
   attn_cache c;
   attn::Maps maps;
+  long long wait_cycles;
+  int extra;  // arrivals that never come, on s_free
   const float* acc;
   float decay;
   float* acc_out;
@@ -111,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&ctl.s_full[i], 1);
-      mbar_init(&ctl.s_free[i], 128);
+      mbar_init(&ctl.s_free[i], 128 + a.extra);
     }
     mbar_init(&ctl.q_full, kWorkers);
     mbar_init(&ctl.qk_done, 1);
@@ -149,7 +151,11 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
   fence_after_sync();
   const uint32_t tmem = ctl.tmem;
   volatile int* abort_flag = &ctl.abort;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return attn::bounded_wait(bar, parity, abort_flag, a.st); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return attn::bounded_wait(bar, parity, a.wait_cycles, abort_flag, a.st);
+  };
+  // for what a warp does together: it goes on, or gives up, as one
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
   auto passes = [&](const attn::Walk& w) { return (w.rows + q_rows - 1) / q_rows; };
 
   if (warp == kTmaWarp) {
@@ -178,8 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
           }
           for (int p = 0; p < panels; ++p, ++pos) {
             const int slot = pos % kSlots;
-            alive = alive && wait(&ctl.empty[slot], ((pos / kSlots) & 1) ^ 1);
-            alive = __all_sync(0xffffffffu, alive);
+            alive = warp_wait(&ctl.empty[slot], ((pos / kSlots) & 1) ^ 1);
             if (!alive) break;
             if (lane == 0) mbar_arrive_expect_tx(&ctl.full[slot], (uint32_t)(issued * box_rows * 128));
             __syncwarp();
@@ -192,13 +197,12 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
     }
     if (lane == 0)  // every copy has landed before the CTA's shared memory goes away
       for (int i = max(0, pos - kSlots); i < pos; ++i)
-        attn::bounded_wait(&ctl.full[i % kSlots], (i / kSlots) & 1, nullptr, a.st);
+        attn::bounded_wait(&ctl.full[i % kSlots], (i / kSlots) & 1, attn::kDrainCycles, nullptr, a.st);
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------- MMA
     // The warp walks and waits as one; its elected lane issues.
     const bool leader = attn::elect_lane();
-    auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
     attn::Walk w(a.cu, a.lens, a.c.batch, a.tokens, dims, ctl.share);
     int slot0 = 0, round0 = 0;          // ring slot of the pass's first panel, and how often the ring had turned
     int loads = 0;
@@ -272,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
     }
     if (leader) {
       mma_commit(&ctl.drain);
-      attn::bounded_wait(&ctl.drain, 0, nullptr, a.st);
+      attn::bounded_wait(&ctl.drain, 0, attn::kDrainCycles, nullptr, a.st);
     }
     __syncwarp();
   } else {
@@ -281,7 +285,6 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
     const uint32_t lane_base = (uint32_t)(wl * 32) << 16;
     const float c2 = a.c2;
     const float2 c22 = make_float2(c2, c2), ones = make_float2(1.f, 1.f);
-    auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
     attn::Walk w(a.cu, a.lens, a.c.batch, a.tokens, dims, ctl.share);
     int loads = 0, used = 0;
     bool alive = true;
@@ -440,6 +443,7 @@ extern "C" int attn_cache_weights(const void* q, long long q_stride, const float
   const int sms = moe::device_info().sms;
   if (sms <= 0) return MOE_ERR_CUDA;
   a.q = q, a.q_stride = q_stride, a.lse = lse, a.cu = cu, a.lens = lens, a.tokens = tokens, a.q_heads = q_heads;
+  a.wait_cycles = attn::wait_cycles(), a.extra = (int)moe::barrier_extra();
   a.tree = tree, a.tree_words = tree_words, a.acc = acc, a.decay = (float)decay;
   a.acc_out = acc_out, a.slot_cap = slot_cap, a.st = dev_status;
   a.c2 = (float)(fabs(scale) * 1.4426950408889634), a.lse_to_2 = (double)a.c2 / fabs(scale), a.negative = scale < 0.0;

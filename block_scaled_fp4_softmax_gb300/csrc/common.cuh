@@ -237,6 +237,11 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// The limit of the kernels' waits and what moe_test_set_wait_limit adds to a
+// barrier's arrivals (decode_oneshot.cu).
+unsigned long long wait_limit_ns();
+unsigned barrier_extra();
+
 __device__ __forceinline__ void status_or(int32_t* st, int bits) {
   if (st) atomicOr(st, bits);
 }

@@ -798,12 +798,17 @@ std::atomic<unsigned> g_barrier_extra{0};
 constexpr unsigned long long kDefaultWaitNs = 2000000000ull;  // 2 s: far beyond any legitimate wait
 }  // namespace
 
+unsigned long long moe::wait_limit_ns() {
+  const unsigned long long w = g_wait_ns.load(std::memory_order_relaxed);
+  return w ? w : kDefaultWaitNs;
+}
+unsigned moe::barrier_extra() { return g_barrier_extra.load(std::memory_order_relaxed); }
+
 int launch_decode_oneshot(const DecodeOneshotArgs& a0, int fmt, int grid, void* stream) {
   cudaStream_t st = (cudaStream_t)stream;
   DecodeOneshotArgs a = a0;
-  const unsigned long long w = g_wait_ns.load(std::memory_order_relaxed);
-  a.wait_ns = w ? w : kDefaultWaitNs;
-  a.barrier_extra = g_barrier_extra.load(std::memory_order_relaxed);
+  a.wait_ns = moe::wait_limit_ns();
+  a.barrier_extra = moe::barrier_extra();
   return fmt == MOE_FMT_NVFP4 ? moe::os::launch_fmt<MOE_FMT_NVFP4>(a, grid, st)
                               : moe::os::launch_fmt<MOE_FMT_MXFP4>(a, grid, st);
 }

@@ -325,15 +325,17 @@ int fp8_rowscale_gemv(const uint8_t* w_e4m3, const float* row_scale, const uint1
 /* Static text for a moe_status value. */
 const char* moe_status_string(int status);
 
-/* Test hook for the bounded waits of moe_decode_layer and of
- * moe_experts_decode's one-shot kernel, so that a test can make a wait run
- * out without faulting or hanging the GPU.  The pages have no counterpart.
+/* Test hook for the bounded waits of moe_decode_layer, of
+ * moe_experts_decode's one-shot kernel and of the attention kernels (attn.h),
+ * so that a test can make a wait run out without faulting or hanging the GPU.  The pages have no counterpart.
  * wait_ns: the limit of every bounded wait in those kernels (0 restores the
  *   default of 2 s; otherwise 1 us .. 10 s).
  * barrier_extra_arrivals: 0, or 1 to make every grid barrier wait for one
  *   arrival more than the grid makes -- it then runs out after wait_ns, the
  *   launch sets MOE_DEV_TIMEOUT and writes NaN outputs.  Zero the workspace
- *   again before the next call.
+ *   again before the next call.  In attn_tree_decode it is the barrier that
+ *   announces a tile's weights, in attn_cache_weights the one that frees a
+ *   buffer of scores.
  * The setting is process-wide and applies to launches made after the call.
  * Returns MOE_ERR_INVALID_ARG for values outside those ranges. */
 int moe_test_set_wait_limit(unsigned long long wait_ns, int barrier_extra_arrivals);
