@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           const T* q = static_cast<const T*>(a.q) + (long long)w.s.first * a.q_stride + (long long)w.p.head * G * D + ch * 8;
           const int first = w.row0 + tile_row0 + (me >> 3), step_tok = step / G, step_g = step - step_tok * G;
           int tok = first / G, g = first - tok * G;
-          for (int r = me >> 3; r < n_rows; r += step) {
+          for (int r = me >> 3; r < n_rows && alive; r += step) {
             const T* src = q + tok * a.q_stride + g * D;
             for (int p = 0; p < panels; ++p) {
               const bool inside = p * 64 + ch * 8 < D;
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           cp_async_commit();
           cp_async_wait<0>();
           fence_proxy_async();
-          mbar_arrive(&ctl.q_full);
+          if (alive) mbar_arrive(&ctl.q_full);
         }
         const bool active = wl * 32 < w.rows - tile_row0;  // whether the warp has rows at all
         const int row = w.row0 + tile_row0 + r_tile;       // of the sequence and head
@@ -438,7 +438,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         float m = -INFINITY, l = 0.f;  // m in powers of two
         int done = 0;
         // Where a wait has given up, the loop still runs to its end without waiting, so
-        // that the warpgroups meet at every barrier.
+        // that the warpgroups meet at every barrier; but it announces nothing any more, and
+        // no product is made of rows, weights or values that are not what they should be.
         for (int it = (C::STREAMS == 2 ? st : 0); it < items; it += C::STREAMS) {
           const int x = it & 1, tile = both ? it >> 1 : it;
           const int k0 = (w.p.kt0 + tile) * C::BN;
@@ -536,20 +537,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 attn::tmem_st_wait();
                 fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.p_half[x]);
+                if (lane == 0 && alive) mbar_arrive(&ctl.p_half[x]);
               }
             };
 #pragma unroll
             for (int i = 0; i < C::BN; i += 32) weights(s + i, i);
             attn::tmem_st_wait();
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-          } else if (lane == 0) {
+          } else if (lane == 0 && alive) {
             mbar_arrive(&ctl.p_half[x]);
           }
           ++done;
           fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl.p_full[x]);
+          if (lane == 0 && alive) mbar_arrive(&ctl.p_full[x]);
         }
         pv_seen += done;
         if (l != l && m == -INFINITY) m = 0.f;  // only NaN scores: not to be mistaken for a row that saw nothing

@@ -302,7 +302,9 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
           const T* q = static_cast<const T*>(a.q) + (long long)w.s.first * a.q_stride + (long long)w.p.head * G * D + ch * 8;
           const int first = r0 + (threadIdx.x >> 3), step = kWorkers / 8, step_tok = step / G, step_g = step - step_tok * G;
           int tok = first / G, g = first - tok * G;
-          for (int r = threadIdx.x >> 3; r < padded; r += step) {
+          // who has given up leaves Q alone and does not announce it: no product is made of
+          // rows that are not what they should be
+          for (int r = threadIdx.x >> 3; r < padded && alive; r += step) {
             const T* src = r < rows ? q + tok * a.q_stride + g * D : q + r0 / G * a.q_stride + r0 % G * D;
             for (int p = 0; p < panels; ++p) {
               const bool inside = p * 64 + ch * 8 < D;
@@ -327,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
           cp_async_wait<0>();
           fence_proxy_async();
           named_sync(1, kWorkers);
-          mbar_arrive(&ctl.q_full);
+          if (alive) mbar_arrive(&ctl.q_full);
         }
         const bool left_out = ctl.left_out[loads & 1] != 0;
         if (threadIdx.x == 0) ctl.left_out[(loads + 1) & 1] = 0;  // read by all before this pass began
