@@ -160,10 +160,11 @@ def _tree(tree, tokens, cache):
     if the token sees draft j of its sequence."""
     if tree is None:
         return None, 0
-    if tree.dim() != 2:
-        raise MoeError("tree must be [tokens, words]")
+    if tree.dim() != 2 or tree.shape[1] == 0:
+        raise MoeError("tree must be [tokens, words], of one word or more")
     words = tree.shape[1]
-    return _array(tree, "tree", (tokens, words), _i64, cache), words
+    at = _array(tree, "tree", (tokens, words), _i64, cache)
+    return (at, words) if tokens else (None, 0)
 
 
 def _status(dev_status, cache):

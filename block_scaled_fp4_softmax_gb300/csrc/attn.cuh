@@ -129,7 +129,8 @@ inline int check_cache(const attn_cache* in, attn_cache& c) {
 inline int check_queries(const attn_cache& c, const void* q, long long q_stride, const int32_t* cu,
                          const int32_t* lens, int tokens, int q_heads, const uint64_t* tree, int tree_words) {
   if ((!q && tokens > 0) || !cu || !lens || tokens < 0 || q_heads <= 0) return MOE_ERR_INVALID_ARG;
-  if (tree && tree_words <= 0) return MOE_ERR_INVALID_ARG;
+  // (words of no array would be taken for a chain)
+  if (tree ? tree_words <= 0 : tree_words != 0) return MOE_ERR_INVALID_ARG;
   if (q_heads % c.kv_heads != 0 || q_heads > 65535) return MOE_ERR_UNSUPPORTED;
   if (tree && tree_words > (1 << 20)) return MOE_ERR_UNSUPPORTED;
   if (tokens > (1 << 24)) return MOE_ERR_UNSUPPORTED;

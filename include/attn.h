@@ -101,7 +101,8 @@ size_t attn_tree_decode_workspace(const attn_cache* cache);
  * its lens[b] committed slots and, of the tokens in flight, those whose bit
  * is set in its row of `tree`: bit j % 64 of word tree[t * tree_words + j /
  * 64] for draft j (bits past the sequence's tokens are ignored, missing words
- * are 0).  tree = NULL: a chain, token i sees drafts 0 .. i.
+ * are 0; there is at least one).  tree = NULL, tree_words = 0: a chain, token i
+ * sees drafts 0 .. i.
  *   s_j = scale * <q, k_j>,  out = sum_j softmax(s)_j v_j,  lse = log sum_j exp(s_j)
  * with FP32 accumulation (1e-30 <= |scale| <= 1e30); the weights are rounded once to the cache's type
  * as operands of the second product (the sum behind lse is of the unrounded

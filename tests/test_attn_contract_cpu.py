@@ -1,10 +1,12 @@
 """What include/attn.h promises and the host can show: the oracle's readings of it, and refusals."""
+import ctypes
 import types
 
 import numpy as np
 import pytest
+import torch
 
-from block_scaled_fp4_softmax_gb300 import attn
+from block_scaled_fp4_softmax_gb300 import attn, build
 from oracle import attn as A
 
 
@@ -34,3 +36,39 @@ def test_a_cache_of_another_device_is_refused(call, monkeypatch):
     monkeypatch.setattr(attn, "_current", lambda: 1)
     with pytest.raises(attn.MoeError, match="the stream on cuda:0"):
         CALLS[call](cache, stream=types.SimpleNamespace(device_index=0, cuda_stream=7))
+
+
+ONE = 4096  # an aligned address that no call below reaches
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return attn.load()
+
+
+def cache(**kw):
+    c = dict(k=ONE, v=ONE, page_stride=4 * 16 * 128, head_stride=16 * 128, row_stride=128, page_table=ONE, batch=2,
+             max_pages=8, pages=16, page_size=16, kv_heads=4, head_dim=128, dtype=attn.BF16)
+    c.update(kw)
+    return ctypes.byref(attn._CacheStruct(**c))
+
+
+def test_trees_without_words_are_refused(lib):
+    """They would be taken for a chain, whose tokens see what came before them."""
+    def calls(words, count):
+        return (lib.attn_tree_decode(ONE, 1024, ONE, ONE, 3, 8, words, count, 0.1, cache(), ONE, ONE, ONE, 1 << 40, None, None),
+                lib.attn_cache_weights(ONE, 1024, ONE, ONE, ONE, 3, 8, words, count, 0.1, cache(), ONE, 1.0, ONE, 128, None, None))
+
+    for words, count in ((None, 1), (None, -1), (ONE, 0)):
+        assert calls(words, count) == (1, 1)
+    here = types.SimpleNamespace(index=-1, device="cpu")  # get_device() of a CPU tensor
+    with pytest.raises(attn.MoeError, match="one word or more"):
+        attn._tree(torch.zeros(3, 0, dtype=torch.int64), 3, here)
+    with pytest.raises(attn.MoeError, match="one word or more"):
+        attn._tree(torch.zeros(3, dtype=torch.int64), 3, here)
+    rows = torch.zeros(3, 2, dtype=torch.int64)
+    assert attn._tree(rows, 3, here) == (rows.data_ptr(), 2)
+    # no tokens, no address: not to be taken for an array
+    assert attn._tree(torch.zeros(0, 2, dtype=torch.int64), 0, here) == (None, 0)
+    assert attn._tree(None, 3, here) == (None, 0)
