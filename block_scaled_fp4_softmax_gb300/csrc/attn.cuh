@@ -139,4 +139,9 @@ inline int check_queries(const attn_cache& c, const void* q, long long q_stride,
   return MOE_OK;
 }
 
+// The rows (token x query head) of a sequence and KV head are counted in an int.
+inline bool rows_fit(const attn_cache& c, int tokens, int q_heads) {
+  return (long long)tokens * (q_heads / c.kv_heads) <= kMaxSlots;
+}
+
 }  // namespace attn

@@ -817,6 +817,7 @@ int attn_tree_decode(const void* q, long long q_stride, const int32_t* cu, const
   TreeArgs a;
   if (const int rc = attn::check_cache(cache, a.c)) return rc;
   if (const int rc = attn::check_queries(a.c, q, q_stride, cu, lens, tokens, q_heads, tree, tree_words)) return rc;
+  if (!attn::rows_fit(a.c, tokens, q_heads)) return MOE_ERR_UNSUPPORTED;
   if ((!out && tokens > 0) || !workspace) return MOE_ERR_INVALID_ARG;
   if (!moe::aligned16(out) || !moe::aligned16(workspace)) return MOE_ERR_ALIGNMENT;
   if (!(fabs(scale) >= 1e-30 && fabs(scale) <= 1e30)) return MOE_ERR_INVALID_ARG;

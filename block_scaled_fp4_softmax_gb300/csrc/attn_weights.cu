@@ -440,6 +440,7 @@ extern "C" int attn_cache_weights(const void* q, long long q_stride, const float
   WeightArgs a;
   if (const int rc = attn::check_cache(cache, a.c)) return rc;
   if (const int rc = attn::check_queries(a.c, q, q_stride, cu, lens, tokens, q_heads, tree, tree_words)) return rc;
+  if (!attn::rows_fit(a.c, tokens, q_heads)) return MOE_ERR_UNSUPPORTED;
   if ((!lse && tokens > 0) || !acc || !acc_out || slot_cap <= 0 || !(fabs(scale) >= 1e-30 && fabs(scale) <= 1e30))
     return MOE_ERR_INVALID_ARG;
   const int sms = moe::device_info().sms;

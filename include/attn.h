@@ -23,7 +23,8 @@
  * writes NaN to its floating outputs (at least to those of the tokens or
  * sequences concerned) and neither reads nor writes their part of the cache.
  *
- * Heads.  q_heads = G * kv_heads; query head h reads KV head h / G.
+ * Heads.  q_heads = G * kv_heads; query head h reads KV head h / G.  Attention
+ * and weights take up to 2^31 - 2049 rows (tokens x G) in a call.
  */
 #ifndef ATTN_GB300_H
 #define ATTN_GB300_H

@@ -72,3 +72,17 @@ def test_trees_without_words_are_refused(lib):
     # no tokens, no address: not to be taken for an array
     assert attn._tree(torch.zeros(0, 2, dtype=torch.int64), 0, here) == (None, 0)
     assert attn._tree(None, 3, here) == (None, 0)
+
+
+def test_rows_beyond_an_int_are_refused(lib):
+    """2^24 tokens of 128 query heads a KV head: 2^31 rows."""
+    c = dict(kv_heads=1, head_dim=16, row_stride=16, head_stride=256, page_stride=256)
+
+    def calls(tokens, heads):
+        return (lib.attn_tree_decode(ONE, heads * 16, ONE, ONE, tokens, heads, None, 0, 0.1, cache(**c), None, ONE, ONE, 1 << 40, None, None),
+                lib.attn_cache_weights(ONE, heads * 16, None, ONE, ONE, tokens, heads, None, 0, 0.1, cache(**c), ONE, 1.0, ONE, 128, None, None))
+
+    assert calls(1 << 24, 128) == (3, 3)
+    assert calls((1 << 24) - 16, 128) == (3, 3)       # 2^31 - 2048
+    assert calls((1 << 24) - 17, 128) == (1, 1)       # fits: what is missing is found next
+    assert calls(1 << 24, 127) == (1, 1)
