@@ -105,6 +105,8 @@ def attn_cache(k, v, page_table) -> AttnCache:
     _moe._cuda(page_table, "page_table", torch.int32)
     if page_table.dim() != 2 or page_table.device != k.device:
         raise MoeError("page_table must be [batch, max_pages] on the cache's device")
+    _fit(batch=page_table.shape[0], max_pages=page_table.shape[1], pages=k.shape[0], kv_heads=k.shape[1],
+         page_size=k.shape[2], head_dim=k.shape[3])
     return AttnCache(k, v, page_table)
 
 
@@ -167,6 +169,13 @@ def _tree(tree, tokens, cache):
     return (at, words) if tokens else (None, 0)
 
 
+def _fit(**sizes):
+    """ctypes drops what passes 32 bits without a word."""
+    for name, x in sizes.items():
+        if not 0 <= x < 1 << 31:
+            raise MoeError(f"{name} must be 0 to 2^31 - 1, got {x}")
+
+
 def _status(dev_status, cache):
     return None if dev_status is None else _array(dev_status, "dev_status", (1,), _i32, cache)
 
@@ -204,6 +213,7 @@ def attn_qk_norm_rope(q, k, v, pos, cu, lens, cache: AttnCache, inv_freq, q_weig
     at, cap = None, 0
     if slot_pos is not None:
         cap = slot_pos.shape[-1]
+        _fit(slot_cap=cap)
         at = _array(slot_pos, "slot_pos", (cache.batch, cache.kv_heads, cap), _i32, cache)
     if q_out is None:
         with _elsewhere(stream):
@@ -269,6 +279,7 @@ def attn_cache_weights(q, lse, cu, lens, cache: AttnCache, acc, tree=None, scale
     T, hq, D = q.shape
     words, count = _tree(tree, T, cache)
     shape = (cache.batch, cache.kv_heads, acc.shape[-1])
+    _fit(slot_cap=shape[2])
     if acc_out is None:
         with _elsewhere(stream):
             acc_out = torch.zeros(shape, dtype=_f32, device=cache.device)
@@ -285,6 +296,7 @@ def attn_cache_weights(q, lse, cu, lens, cache: AttnCache, acc, tree=None, scale
 
 def attn_cache_evict_workspace(cache: AttnCache, budget: int):
     """A workspace for :func:`attn_cache_evict` with this budget."""
+    _fit(budget=budget)
     n = int(load().attn_cache_evict_workspace(cache.ref, budget))
     if n == 0:
         raise MoeError("attn_cache_evict does not support this cache or budget")
@@ -298,6 +310,7 @@ def attn_cache_evict(cache: AttnCache, acc, slot_pos, lens, next_pos, budget: in
     (lens_out, acc_out, pos_out)."""
     on = _on(stream, cache)
     shape = (cache.batch, cache.kv_heads, acc.shape[-1])
+    _fit(slot_cap=shape[2], budget=budget, sinks=sinks, recent=recent)
     if acc_out is None or pos_out is None or lens_out is None or workspace is None:
         with _elsewhere(stream):
             if acc_out is None:

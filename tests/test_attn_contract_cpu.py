@@ -86,3 +86,27 @@ def test_rows_beyond_an_int_are_refused(lib):
     assert calls((1 << 24) - 16, 128) == (3, 3)       # 2^31 - 2048
     assert calls((1 << 24) - 17, 128) == (1, 1)       # fits: what is missing is found next
     assert calls(1 << 24, 127) == (1, 1)
+
+
+@pytest.mark.parametrize("name", ["budget", "sinks", "recent"])
+@pytest.mark.parametrize("value", [1 << 31, 1 << 32, (1 << 32) + 5, -1, -(1 << 32)])
+def test_numbers_beyond_32_bits_are_refused(name, value, monkeypatch):
+    """2^32 protected positions are not none."""
+    def library():
+        raise AssertionError("called")
+
+    monkeypatch.setattr(attn, "_current", lambda: 0)
+    monkeypatch.setattr(attn, "_raw_stream", lambda i: 0)
+    monkeypatch.setattr(attn, "load", library)
+    monkeypatch.setattr(attn, "_LIB", None)
+    here = types.SimpleNamespace(index=0, device="cuda:0", batch=1, kv_heads=1, lens_shape=(1,), ref=None)
+    acc = torch.zeros(1, 1, 8)
+    args = dict(budget=4, sinks=0, recent=0) | {name: value}
+    with pytest.raises(attn.MoeError, match=f"{name} must be"):
+        attn.attn_cache_evict(here, acc, acc, acc, acc, workspace=acc, acc_out=acc, pos_out=acc, lens_out=acc, **args)
+    if name == "budget":
+        with pytest.raises(attn.MoeError, match="budget must be"):
+            attn.attn_cache_evict_workspace(here, value)
+    far = torch.empty(0, 1, 1 << 31)
+    with pytest.raises(attn.MoeError, match="slot_cap must be"):
+        attn.attn_cache_evict(here, far, acc, acc, acc, 4)
