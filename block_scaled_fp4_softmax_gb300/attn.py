@@ -157,14 +157,23 @@ def _array(t, name, shape, dtype, cache):
     raise MoeError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {cache.device}")
 
 
+def _size(t, name):
+    """Elements of the last axis of a tensor whose shape is checked later."""
+    try:
+        return t.shape[-1]
+    except (AttributeError, IndexError):
+        pass
+    raise MoeError(f"{name} must be a tensor with a shape")
+
+
 def _tree(tree, tokens, cache):
     """tree [tokens, words] int64: bit j % 64 of word j // 64 of a row is set
     if the token sees draft j of its sequence."""
     if tree is None:
         return None, 0
-    if tree.dim() != 2 or tree.shape[1] == 0:
+    words = _size(tree, "tree")
+    if len(tree.shape) != 2 or words == 0:
         raise MoeError("tree must be [tokens, words], of one word or more")
-    words = tree.shape[1]
     at = _array(tree, "tree", (tokens, words), _i64, cache)
     return (at, words) if tokens else (None, 0)
 
@@ -204,7 +213,7 @@ def attn_qk_norm_rope(q, k, v, pos, cu, lens, cache: AttnCache, inv_freq, q_weig
     T, hq, D = q.shape
     if k.shape[0] != T or v.shape[0] != T:
         raise MoeError("q, k and v must hold the same tokens")
-    half = inv_freq.numel()
+    half = _size(inv_freq, "inv_freq")
     if q_weight is None and k_weight is None:
         wq = wk = None
     else:
@@ -212,7 +221,7 @@ def attn_qk_norm_rope(q, k, v, pos, cu, lens, cache: AttnCache, inv_freq, q_weig
         wk = _array(k_weight, "k_weight", (D,), cache.dtype, cache)
     at, cap = None, 0
     if slot_pos is not None:
-        cap = slot_pos.shape[-1]
+        cap = _size(slot_pos, "slot_pos")
         _fit(slot_cap=cap)
         at = _array(slot_pos, "slot_pos", (cache.batch, cache.kv_heads, cap), _i32, cache)
     if q_out is None:
@@ -257,7 +266,7 @@ def attn_tree_decode(q, cu, lens, cache: AttnCache, tree=None, scale: float | No
                 lse = _empty((T, hq), dtype=_f32, device=cache.device)
             if workspace is None:
                 workspace = attn_tree_decode_workspace(cache)
-    size = workspace.numel()
+    size = _size(workspace, "workspace")
     rc = (_LIB or load()).attn_tree_decode(
         q.data_ptr(), sq, _array(cu, "cu", cache.cu_shape, _i32, cache),
         _array(lens, "lens", cache.lens_shape, _i32, cache), T, hq, words, count,
@@ -278,7 +287,7 @@ def attn_cache_weights(q, lse, cu, lens, cache: AttnCache, acc, tree=None, scale
     sq = _rows(q, "q", None, cache)
     T, hq, D = q.shape
     words, count = _tree(tree, T, cache)
-    shape = (cache.batch, cache.kv_heads, acc.shape[-1])
+    shape = (cache.batch, cache.kv_heads, _size(acc, "acc"))
     _fit(slot_cap=shape[2])
     if acc_out is None:
         with _elsewhere(stream):
@@ -309,7 +318,7 @@ def attn_cache_evict(cache: AttnCache, acc, slot_pos, lens, next_pos, budget: in
     weight and moves their rows below the budget, in place.  Returns
     (lens_out, acc_out, pos_out)."""
     on = _on(stream, cache)
-    shape = (cache.batch, cache.kv_heads, acc.shape[-1])
+    shape = (cache.batch, cache.kv_heads, _size(acc, "acc"))
     _fit(slot_cap=shape[2], budget=budget, sinks=sinks, recent=recent)
     if acc_out is None or pos_out is None or lens_out is None or workspace is None:
         with _elsewhere(stream):
@@ -321,7 +330,7 @@ def attn_cache_evict(cache: AttnCache, acc, slot_pos, lens, next_pos, budget: in
                 lens_out = _empty(cache.lens_shape, dtype=_i32, device=cache.device)
             if workspace is None:
                 workspace = attn_cache_evict_workspace(cache, budget)
-    size = workspace.numel()
+    size = _size(workspace, "workspace")
     rc = (_LIB or load()).attn_cache_evict(
         cache.ref, _array(acc, "acc", shape, _f32, cache), _array(slot_pos, "slot_pos", shape, _i32, cache),
         shape[2], _array(lens, "lens", cache.lens_shape, _i32, cache),

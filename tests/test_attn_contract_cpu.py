@@ -110,3 +110,29 @@ def test_numbers_beyond_32_bits_are_refused(name, value, monkeypatch):
     far = torch.empty(0, 1, 1 << 31)
     with pytest.raises(attn.MoeError, match="slot_cap must be"):
         attn.attn_cache_evict(here, far, acc, acc, acc, 4)
+
+
+@pytest.mark.parametrize("what", [None, [1.0], 3, torch.zeros(())], ids=["none", "list", "number", "scalar"])
+def test_what_has_no_shape_is_refused(what, monkeypatch):
+    monkeypatch.setattr(attn, "_current", lambda: -1)
+    monkeypatch.setattr(attn, "_raw_stream", lambda i: 0)
+    here = types.SimpleNamespace(index=-1, device="cpu", dtype=torch.bfloat16, batch=1, kv_heads=2, head_dim=16,
+                                 cu_shape=(2,), lens_shape=(1,), ref=None)  # index: get_device() of a CPU tensor
+    x = torch.zeros(3, 2, 16, dtype=torch.bfloat16)
+    ints, acc = torch.zeros(2, dtype=torch.int32), torch.zeros(1, 2, 8)
+    lse, freq = torch.zeros(3, 2), torch.zeros(8, dtype=torch.float64)
+    with pytest.raises(attn.MoeError, match="inv_freq"):
+        attn.attn_qk_norm_rope(x, x, x, ints, ints, ints, here, what)
+    if what is not None:
+        with pytest.raises(attn.MoeError, match="slot_pos"):
+            attn.attn_qk_norm_rope(x, x, x, ints, ints, ints, here, freq, slot_pos=what)
+        with pytest.raises(attn.MoeError, match="tree"):
+            attn.attn_tree_decode(x, ints, ints, here, tree=what)
+        with pytest.raises(attn.MoeError, match="workspace"):
+            attn.attn_tree_decode(x, ints, ints, here, out=x, lse=lse, workspace=what)
+        with pytest.raises(attn.MoeError, match="workspace"):
+            attn.attn_cache_evict(here, acc, acc, ints, ints, 4, acc_out=acc, pos_out=acc, lens_out=ints, workspace=what)
+    with pytest.raises(attn.MoeError, match="acc"):
+        attn.attn_cache_weights(x, lse, ints, ints, here, what)
+    with pytest.raises(attn.MoeError, match="acc"):
+        attn.attn_cache_evict(here, what, acc, ints, ints, 4)
