@@ -466,6 +466,11 @@ int select(const EvictArgs& a, int problems, int sms, cudaStream_t st) {
                               : launch_select<false, VEC>(a, problems, C, sizeof(Shared), st);
 }
 
+bool overlap(const void* a, size_t n, const void* b, size_t m) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x < y + m && y < x + n;
+}
+
 size_t counts_bytes(const attn_cache& c) { return ((size_t)c.batch * c.kv_heads * 4 + 15) & ~(size_t)15; }
 
 }  // namespace
@@ -485,11 +490,15 @@ int attn_cache_evict(const attn_cache* cache, const float* acc, const int32_t* s
   EvictArgs a;
   if (const int rc = attn::check_cache(cache, a.c)) return rc;
   if (!acc || !slot_pos || !lens || !next_pos || !acc_out || !slot_pos_out || !lens_out || !workspace ||
-      slot_cap <= 0 || budget <= 0 || sinks < 0 || recent < 0 || acc == acc_out || slot_pos == slot_pos_out ||
-      lens == lens_out)
+      slot_cap <= 0 || budget <= 0 || sinks < 0 || recent < 0)
     return MOE_ERR_INVALID_ARG;
   const long long problems = (long long)a.c.batch * a.c.kv_heads;
   if (slot_cap > attn::kMaxSlots || problems > 65535) return MOE_ERR_UNSUPPORTED;
+  // the CTAs of a sequence read its inputs while others write
+  const size_t all = (size_t)problems * slot_cap * 4, each = (size_t)a.c.batch * 4;
+  if (overlap(acc_out, all, acc, all) || overlap(slot_pos_out, all, slot_pos, all) ||
+      overlap(lens_out, each, lens, each) || overlap(lens_out, each, next_pos, each))
+    return MOE_ERR_INVALID_ARG;
   if (!moe::aligned16(workspace)) return MOE_ERR_ALIGNMENT;
   if (ws_bytes < attn_cache_evict_workspace(cache, budget)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   a.acc = acc, a.slot_pos = slot_pos, a.slot_cap = slot_cap, a.lens = lens, a.next_pos = next_pos;

@@ -136,3 +136,21 @@ def test_what_has_no_shape_is_refused(what, monkeypatch):
         attn.attn_cache_weights(x, lse, ints, ints, here, what)
     with pytest.raises(attn.MoeError, match="acc"):
         attn.attn_cache_evict(here, what, acc, ints, ints, 4)
+
+
+def test_eviction_outputs_that_lie_in_inputs_are_refused(lib):
+    """lens_out is written while other CTAs of the batch still read next_pos."""
+    rows = 2 * 4 * 128 * 4
+
+    def evict(acc=ONE, pos=ONE, lens=ONE, nxt=ONE, acc_out=16 * ONE, pos_out=16 * ONE, lens_out=16 * ONE):
+        # the workspace is too small: the next thing to be found
+        return lib.attn_cache_evict(cache(), acc, pos, 128, lens, nxt, 10, 0, 0, acc_out, pos_out, lens_out, ONE, 0, None, None)
+
+    assert evict() == 4
+    assert evict(lens_out=ONE) == 1 and evict(nxt=16 * ONE) == 1 and evict(lens=16 * ONE) == 1
+    assert evict(lens_out=ONE + 4) == 1 and evict(lens_out=ONE + 8) == 4 and evict(lens_out=ONE - 8) == 4
+    for name in ("acc", "pos"):
+        for at in (4 * ONE, 4 * ONE + rows - 4, 4 * ONE - rows + 4):
+            assert evict(**{name: 4 * ONE, name + "_out": at}) == 1
+        for at in (4 * ONE + rows, 4 * ONE - rows):
+            assert evict(**{name: 4 * ONE, name + "_out": at}) == 4
