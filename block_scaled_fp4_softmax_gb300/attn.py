@@ -122,11 +122,12 @@ _i32, _i64, _f32, _f64, _u8 = torch.int32, torch.int64, torch.float32, torch.flo
 def _on(stream, cache):
     """Handle of the stream to launch on.  A launch goes to the device that is
     current: any other than the cache's is refused, before anything else is done."""
-    if _current() != cache.index:
+    index = cache.index
+    if _current() != index:
         raise MoeError(f"the cache is on {cache.device}, cuda:{_current()} is current")
     if stream is None:
-        return _raw_stream(cache.index)
-    if stream.device_index != cache.index:
+        return _raw_stream(index)
+    if stream.device_index != index:
         raise MoeError(f"the cache is on {cache.device}, the stream on cuda:{stream.device_index}")
     return stream.cuda_stream
 
@@ -178,10 +179,13 @@ def _tree(tree, tokens, cache):
     return (at, words) if tokens else (None, 0)
 
 
+_MOST = (1 << 31) - 1
+
+
 def _fit(**sizes):
     """ctypes drops what passes 32 bits without a word."""
     for name, x in sizes.items():
-        if not 0 <= x < 1 << 31:
+        if not 0 <= x <= _MOST:
             raise MoeError(f"{name} must be 0 to 2^31 - 1, got {x}")
 
 
@@ -222,7 +226,8 @@ def attn_qk_norm_rope(q, k, v, pos, cu, lens, cache: AttnCache, inv_freq, q_weig
     at, cap = None, 0
     if slot_pos is not None:
         cap = _size(slot_pos, "slot_pos")
-        _fit(slot_cap=cap)
+        if cap > _MOST:
+            _fit(slot_cap=cap)
         at = _array(slot_pos, "slot_pos", (cache.batch, cache.kv_heads, cap), _i32, cache)
     if q_out is None:
         with _elsewhere(stream):
@@ -288,7 +293,8 @@ def attn_cache_weights(q, lse, cu, lens, cache: AttnCache, acc, tree=None, scale
     T, hq, D = q.shape
     words, count = _tree(tree, T, cache)
     shape = (cache.batch, cache.kv_heads, _size(acc, "acc"))
-    _fit(slot_cap=shape[2])
+    if shape[2] > _MOST:
+        _fit(slot_cap=shape[2])
     if acc_out is None:
         with _elsewhere(stream):
             acc_out = torch.zeros(shape, dtype=_f32, device=cache.device)
@@ -319,7 +325,8 @@ def attn_cache_evict(cache: AttnCache, acc, slot_pos, lens, next_pos, budget: in
     (lens_out, acc_out, pos_out)."""
     on = _on(stream, cache)
     shape = (cache.batch, cache.kv_heads, _size(acc, "acc"))
-    _fit(slot_cap=shape[2], budget=budget, sinks=sinks, recent=recent)
+    if not (shape[2] <= _MOST and 0 <= budget <= _MOST and 0 <= sinks <= _MOST and 0 <= recent <= _MOST):
+        _fit(slot_cap=shape[2], budget=budget, sinks=sinks, recent=recent)
     if acc_out is None or pos_out is None or lens_out is None or workspace is None:
         with _elsewhere(stream):
             if acc_out is None:
