@@ -1,6 +1,6 @@
 """The attention operators where include/attn.h promises something that random
 inputs do not show: infinite keys, rows that add nothing, slots without a position, more
-protected slots than stay."""
+protected slots than stay, infinite values, chains of a prompt's length."""
 import numpy as np
 import pytest
 import torch
@@ -8,8 +8,47 @@ import torch
 from attn_helpers import Batch, f64, trees
 from block_scaled_fp4_softmax_gb300 import attn
 from test_gpu_attn import BF, FP, attend, run_evict
+from test_gpu_attn_long import CASES, test_long_caches as check_long
 
 pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# Attention
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,dim,lens,new", [
+    (BF, 128, [300, 77], [2, 1]), (FP, 64, [300, 5000], [40, 3]), (BF, 256, [200, 7000], [20, 33]),
+    (FP, 72, [30000], [1]),
+])
+def test_infinite_committed_values(dtype, dim, lens, new):
+    """Every token sees them with a weight above 0: what they make of their own column, and
+    nothing of the others."""
+    bt = Batch(dtype, lens, new, 2, 4, dim, 16, True, trees(new, 5), seed=dim, sharp=0.3)
+    want, want_lse = attend(bt)
+    inf = float("inf")
+    for b, n in enumerate(lens):
+        page, row = bt.rows(b)
+        for slot, d, x in ((0, 1, inf), (n - 1, 1, inf), (n // 2, 9, -inf), (3, dim - 1, inf), (n - 2, dim - 1, -inf),
+                           (7, dim - 2, float("nan"))):
+            bt.v[page[slot], 1, row[slot], d] = x
+    out, lse = attend(bt)
+    assert int(bt.status) == 0 and torch.equal(lse, want_lse)
+    assert torch.equal(out[:, :4].view(torch.int16), want[:, :4].view(torch.int16))
+    assert (out[:, 4:, 1] == inf).all() and (out[:, 4:, 9] == -inf).all() and torch.isnan(out[:, 4:, dim - 2:]).all()
+    rest = [d for d in range(dim) if d not in (1, 9, dim - 2, dim - 1)]
+    assert torch.equal(out[:, 4:, rest].view(torch.int16), want[:, 4:, rest].view(torch.int16))
+
+
+@pytest.mark.parametrize("case", [
+    (BF, [0], [2451], 2, 4, 128, 64, False),           # a prompt into an empty cache
+    (FP, [4096, 0], [256, 1031], 1, 8, 64, 16, False),  # a later part of one, beside another
+    (BF, [130], [1300], 1, 3, 256, 24, False),
+])
+def test_chains_of_a_prompts_length(case, monkeypatch):
+    """Attention and weights of thousands of tokens in flight, as for long caches."""
+    monkeypatch.setitem(CASES, "chain", case)
+    check_long("chain")
 
 
 # ---------------------------------------------------------------------------
