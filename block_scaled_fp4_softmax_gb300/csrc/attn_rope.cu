@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const __grid_
   __shared__ float4 s_cs[kTokens][2][33];
   __shared__ int s_pos[kTokens], s_seq[kTokens], s_slot[kTokens];  // slot -1: out of range
   __shared__ long long s_off[kTokens];                             // of the slot in head 0, -1: nothing is appended
-  __shared__ float s_row[P == kScattered ? kGroups : 1][P == kScattered ? LANES * 8 + 4 : 1];
+  alignas(16) __shared__ float s_row[P == kScattered ? kGroups : 1][P == kScattered ? LANES * 8 + 4 : 4];
   const int D = a.c.head_dim, half = a.rot / 2;
   const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
   // the lane's blocks start at channels c0 and c1
