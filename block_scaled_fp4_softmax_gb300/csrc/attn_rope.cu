@@ -16,9 +16,10 @@
 //
 // Angles.  pos * inv_freq loses whole turns' worth of bits in FP32 at far
 // positions.  inv_freq / 2 pi is turned into a 64-bit fixed-point fraction F
-// of a turn once per block; pos * F modulo 2^64 is then the angle modulo one
-// turn, exactly: an integer multiply does the reduction.  Its top 32 bits as a
-// signed fraction go to sincospif.
+// of a turn once per block (FP64: off by up to inv_freq * 2^-54 turns, and 2^-64);
+// pos * F modulo 2^64 is then the angle modulo one turn without any further
+// error: an integer multiply does the reduction.  Its top 32 bits as a signed
+// fraction, rounded to FP32, go to sincospif.
 #include "attn.cuh"
 
 namespace {

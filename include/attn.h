@@ -76,8 +76,10 @@ typedef struct {
  *   magnitude * (a cos - c sin, a sin + c cos); the pair is channels
  *   (j, j + rot/2), or (2j, 2j + 1) if `interleaved`.
  * then one rounding.  inv_freq [rot / 2] is FP64 on the device and theta is
- * reduced in 64-bit fixed point, so positions far out lose nothing: the angle
- * is off by less than pos * 2^-65 turns before its sine is taken.  Scaled
+ * reduced to one turn in 64-bit fixed point: the angle is off by less than
+ * (|pos| * inv_freq * 2^-54 + 2^-26) turns before its sine is taken (inv_freq
+ * below 2^-9: |pos| * 2^-63 + 2^-26).  The first term is what FP64 makes of
+ * inv_freq / 2 pi, the second is FP32's of the reduced angle.  Scaled
  * rotations (interpolated, stretched per frequency) are a choice of inv_freq
  * and magnitude.
  * q_out [tokens x q_heads x D] contiguous; may be q itself if q is contiguous.

@@ -1,6 +1,7 @@
 """What include/attn.h promises and the host can show: the oracle's readings of it, and refusals."""
 import ctypes
 import types
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -154,3 +155,28 @@ def test_eviction_outputs_that_lie_in_inputs_are_refused(lib):
             assert evict(**{name: 4 * ONE, name + "_out": at}) == 1
         for at in (4 * ONE + rows, 4 * ONE - rows):
             assert evict(**{name: 4 * ONE, name + "_out": at}) == 4
+
+
+def test_angles_are_as_near_as_the_header_says():
+    """The rotation's reduction, operation by operation, against pi to 60 digits."""
+    pi = Fraction(3141592653589793238462643383279502884197169399375105820974944, 10 ** 60)
+
+    def turns(inv_freq, pos):
+        t = np.float64(inv_freq) * np.float64(0.15915494309189533577)
+        f = t - np.floor(t)
+        u = int(f * np.float64(2.0 ** 64)) * pos % 2 ** 64
+        top = u >> 32
+        return Fraction(float(np.float32(top - 2 ** 32 if top >> 31 else top))) / 2 ** 32  # half turns / 2
+
+    rng = np.random.default_rng(0)
+    worst = 0
+    for inv_freq in [1.0, 5.75, *rng.uniform(2.0 ** -9, 1.0, 200), *(10000.0 ** -rng.uniform(0.7, 1.0, 100) / 64)]:
+        for pos in [0, 1, 2 ** 31 - 1, -2 ** 31, *map(int, rng.integers(-2 ** 31, 2 ** 31, 20))]:
+            want = Fraction(float(inv_freq)) * pos / (2 * pi)
+            off = turns(inv_freq, pos) - want
+            off -= round(off)
+            first = abs(pos) * (Fraction(float(inv_freq)) / 2 ** 54 if inv_freq >= 2.0 ** -9 else Fraction(1, 2 ** 63))
+            bound = first + Fraction(1, 2 ** 26)
+            assert abs(off) <= bound, (inv_freq, pos, float(off), float(bound))
+            worst = max(worst, abs(off) / bound)
+    assert worst > Fraction(1, 4)  # nor is the bound out of all proportion
