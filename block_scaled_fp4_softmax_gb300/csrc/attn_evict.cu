@@ -23,8 +23,8 @@
 // What bounds it: three dependent rounds, each two barriers of the cluster and a
 // scan (3000 cycles; 7000 in clusters of 16), and for many rows the copies, which
 // are scattered rows of D elements.  Measured, with the copies: 16 ragged sequences of
-// up to 16384 slots x 8 heads of 128 to 6144: 46 us (select 21, move 25 for 0.11 GB);
-// 2 of 200003 x 2 heads of 64 to 131072: 40 us (26, 16); 1 of 2500 x 4 heads: 12 us.
+// up to 16384 slots x 8 heads of 128 to 6144: 44 us (select 19, move 25 for 0.11 GB);
+// 2 of 200003 x 2 heads of 64 to 131072: 40 us (25, 16); 1 of 2500 x 4 heads: 13 us.
 #include <cooperative_groups.h>
 
 #include "attn.cuh"

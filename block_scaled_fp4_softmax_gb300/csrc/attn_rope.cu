@@ -4,8 +4,9 @@
 // tokens, but only if a row costs few instructions: at 48 rows of 256 bytes a
 // token, some 200 instructions a row and warp already take as long as the bytes.
 // Measured: 12255 tokens of 32 + 2 x 8 heads of 128, BF16: 65 us, 4.6 TB/s (69% of
-// the copy bandwidth; it is short of issue slots: loads that leave earlier cost 4 us,
-// arithmetic by twos gained 4); one token: 3 us.
+// the copy bandwidth); one token: 3 us.  No unit is full: 166 instructions a pair of
+// rows use 65% of the issue slots, with 44% of the warps that an SM can hold (64
+// registers); loads that leave earlier cost 4 us, arithmetic by twos gained 4.
 // A row of D elements belongs to a group of 4, 8, 16 or 32 lanes, 8 elements a
 // lane in two blocks of 4: for the half-split rotation the blocks are a block
 // of the first half and the one it is paired with, so no lane needs another's

@@ -14,13 +14,13 @@
 // of MMA); from some 200 rows the MMAs and the exponentials bound it.
 //
 // Measured, BF16 (copy bandwidth 6.69 TB/s, library GEMM 1.90 PFLOP/s):
-//   32 sequences of 16384 slots, 8 rows, D = 128    176 us, 6.1 TB/s
-//   32 ragged ones of 1024 .. 8192, the same         71 us, 4.5 TB/s
-//   8 of 16384, 504 rows, D = 128                   123 us, 1.10 PFLOP/s
-//   1 of 300001, 136 rows, D = 256 (FP16)           163 us, 3.8 TB/s
-//   1 of 1000, 4 rows, D = 128                       15 us
-// Some 20 us of a call do not grow with it: launch, plan and first loads 6 to 8, a
-// change of piece 2 to 5, the join 8 to 11.  With 504 rows the tensor pipe is active
+//   32 sequences of 16384 slots, 4 x 8 heads of 128  177 us, 6.1 TB/s
+//   32 ragged ones of 1024 .. 8192, the same         72 us, 4.4 TB/s
+//   8 of 16384, 504 rows, D = 128                   125 us, 1.08 PFLOP/s
+//   1 of 300001, 136 rows, D = 256 (FP16)           166 us, 3.7 TB/s
+//   1 of 1000, 4 rows, D = 128                       16 us
+// Of the ragged batch's time some 20 us do not grow with the bytes: launch, plan and
+// first loads 6 to 8, changes of piece 2 to 5, the join 8 to 11.  With 504 rows the tensor pipe is active
 // for half of the time: an MMA of Q and K takes 85 cycles (65 alone, with no copies
 // into the shared memory that both operands come from), one of P and V 70; taking out
 // the exponentials and maxima gains 2 us, halving either product 10.  With wide heads

@@ -15,7 +15,7 @@
 // share the chunks of two tiles, each with an S buffer of its own: while one
 // waits for its next product, three keep the exponential units busy.
 //
-// Measured: 8 sequences of 16384 slots and 504 rows, D = 128, BF16: 78 us, 0.88
+// Measured: 8 sequences of 16384 slots and 504 rows, D = 128, BF16: 78 us, 0.87
 // PFLOP/s, 3.4 exponentials a ns (the units could do 9); a single-token step of two
 // short caches: 7 us.  Of a CTA's 137000 cycles there, 62000 go to issuing MMAs, 36000
 // to waiting for an S buffer, 16000 for K, 11000 to the start and Q.  Reading the

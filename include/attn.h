@@ -50,7 +50,10 @@ enum {
  * any way (strides in elements, the same for k and v), for instance
  * [pages, kv_heads, page_size, D] or [pages, page_size, kv_heads, D].  A
  * cache without paging is one page per sequence.  Page numbers of slots past
- * a sequence's end are not read.
+ * a sequence's end are not read.  A page that is written belongs to one
+ * sequence: attn_qk_norm_rope writes the tokens' slots, and attn_cache_evict any
+ * slot below the budget, in place.  Pages that sequences share (a common prefix)
+ * are for calls that only read, attn_tree_decode and attn_cache_weights.
  * Supported: head_dim a multiple of 8 from 16 to 256; page_size a multiple of
  * 8 up to 2^20; strides multiples of 8 and at least head_dim; k and v 16-B
  * aligned; max_pages * page_size < 2^31 - 2048. */
@@ -109,7 +112,8 @@ size_t attn_tree_decode_workspace(const attn_cache* cache);
  *   s_j = scale * <q, k_j>,  out = sum_j softmax(s)_j v_j,  lse = log sum_j exp(s_j)
  * with FP32 accumulation (1e-30 <= |scale| <= 1e30); the weights are rounded once to the cache's type
  * as operands of the second product (the sum behind lse is of the unrounded
- * ones).  A token that sees nothing gets out = 0 and lse = -inf.  What a token
+ * ones; a weight below 2^-35 of the row's largest, or 2^-126 in BF16, may
+ * become 0, and an infinite value that it meets NaN).  A token that sees nothing gets out = 0 and lse = -inf.  What a token
  * does not see has no influence on it, NaN and infinities included.
  * q [tokens x q_heads x D]: q_stride elements from token to token; out and
  * lse [tokens x q_heads] contiguous.  lse may be NULL.
@@ -126,7 +130,9 @@ int attn_tree_decode(const void* q, long long q_stride, const int32_t* cu, const
  * written.  q, tree and scale as for attn_tree_decode, lse as it wrote it
  * (a row with lse = -inf adds nothing, whatever its q holds; a score of -inf adds
  * 0 as any other weight of 0).  acc, acc_out [batch x kv_heads x
- * slot_cap] FP32, may be the same array.  The sum runs over rows in
+ * slot_cap] FP32, may be the same array.  A score's FP32 sum is cut off, not
+ * rounded, by the tensor core: a weight is off by some 2^-24 times the
+ * score's size, 2e-6 of the weight for scores of 40.  The sum runs over rows in
  * a fixed order: results are bit-identical between repeated calls.
  * Slots on a bad page become NaN with ATTN_DEV_BAD_PAGE. */
 int attn_cache_weights(const void* q, long long q_stride, const float* lse, const int32_t* cu, const int32_t* lens,
