@@ -16,7 +16,7 @@
 // Measured, BF16 (copy bandwidth 6.69 TB/s, library GEMM 1.90 PFLOP/s):
 //   32 sequences of 16384 slots, 4 x 8 heads of 128  177 us, 6.1 TB/s
 //   32 ragged ones of 1024 .. 8192, the same         72 us, 4.4 TB/s
-//   8 of 16384, 504 rows, D = 128                   125 us, 1.08 PFLOP/s
+//   8 of 16384, 504 rows, D = 128                   127 us, 1.07 PFLOP/s
 //   1 of 300001, 136 rows, D = 256 (FP16)           166 us, 3.7 TB/s
 //   1 of 1000, 4 rows, D = 128                       16 us
 // Of the ragged batch's time some 20 us do not grow with the bytes: launch, plan and
@@ -150,12 +150,14 @@ __device__ __forceinline__ attn::PlanDims plan_dims(const TreeArgs& a) {
 }
 
 // Adds the NaN and infinite elements of a piece's drafts, which the products
-// took as zeros, to the result of a row that sees them.
+// took as zeros, to the result of a row that sees them.  `skip`: slots of the tiles
+// that another stream took, of every two tiles from slot k0 on (-1: none).
 // Element d of the row is out[(d / 4) * step + d % 4].
-template <class T, class O>
+template <int BN, class T, class O>
 __device__ __noinline__ void put_back(const TreeArgs& a, attn::Seq s, int b, int head, int token, int d0, int d1,
-                                      O* out, int step) {
+                                      int k0, int skip, O* out, int step) {
   for (int dr = d0; dr < d1; ++dr) {
+    if ((((s.len + dr - k0) / BN) & 1) == skip) continue;
     const long long off = attn::slot_offset(a.c, b, s.len + dr, head);
     if (off < 0 || !(attn::seen(a.tree, a.tree_words, s, token, s.len + dr) & 1u)) continue;
     const T* v = static_cast<const T*>(a.c.v) + off;
@@ -577,7 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
           const size_t slot = (size_t)blockIdx.x * 2 + (w.p.kt0 == 0);
           const int at = 128 * st + r_tile;
           if (active) {
-            if (real) reinterpret_cast<float2*>(a.ml)[slot * C::ROWS + at] = make_float2(m, l);
+            // l < 0: the stream had no tile of the piece, its place in the workspace holds nothing
+            if (real) reinterpret_cast<float2*>(a.ml)[slot * C::ROWS + at] = make_float2(m, done > 0 || l != l ? l : -1.f);
             float4* dst = a.o + slot * (DP / 4) * C::ROWS + at;
 #pragma unroll 1
             for (int col = 0; col < D && done > 0; col += 32) {
@@ -591,7 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
               __syncwarp();
             }
             if (dirty && real && done > 0) {
-              put_back<T>(a, w.s, w.b, w.p.head, token, d0, d1, reinterpret_cast<float*>(dst), 4 * C::ROWS);
+              put_back<C::BN, T>(a, w.s, w.b, w.p.head, token, d0, d1, w.p.kt0 * C::BN, C::STREAMS == 1 || both ? -1 : 1 - st,
+                                 reinterpret_cast<float*>(dst), 4 * C::ROWS);
             }
             __syncwarp();
           }
@@ -642,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 read_o(c0 + col, o);
                 if (join) {
 #pragma unroll
-                  for (int q = 0; q < 32; ++q) o[q] = o[q] * f0 + (f1 == 0.f ? 0.f : exch[(col + q) * exch_rows + r_tile] * f1);
+                  for (int q = 0; q < 32; ++q) o[q] = o[q] * f0 + exch[(col + q) * exch_rows + r_tile] * f1;
                 }
                 if (real) {
 #pragma unroll
@@ -660,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             if (join) named_sync(1, kWorkers);
           }
           if (dirty && real && active && (both || st == 0)) {
-            put_back<T>(a, w.s, w.b, w.p.head, token, d0, d1, static_cast<T*>(a.out) + out_row * D, 4);
+            put_back<C::BN, T>(a, w.s, w.b, w.p.head, token, d0, d1, 0, -1, static_cast<T*>(a.out) + out_row * D, 4);
           }
           __syncwarp();
         }
@@ -724,8 +728,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     for (int i0 = 0; i0 < n; i0 += kChunk) {
       const int count = min(kChunk, n - i0);
       for (int i = warp; i < count; i += kJoinWarps) {
-        const float m = ml[place(i0 + i)].x;
-        s_factor[i][lane] = m == -INFINITY ? 0.f : attn::exp2_fast(m - top);
+        const float2 v = ml[place(i0 + i)];
+        s_factor[i][lane] = v.x != -INFINITY ? attn::exp2_fast(v.x - top) : v.y < 0.f ? -1.f : 0.f;
       }
       __syncthreads();
 #pragma unroll 8
@@ -735,7 +739,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         const float4* o = a.o + (slot * (DP / 4) + first / 4) * C::ROWS + (at - slot * C::ROWS);
 #pragma unroll
         for (int k = 0; k < kMine; ++k)
-          if (f != 0.f && first + 32 * k < D) {  // 0: a piece that saw nothing, and wrote nothing
+          // 0 counts: of a seen key with an infinite value 0 * inf is NaN
+          if (!(f < 0.f) && first + 32 * k < D) {
             const float4 v = o[(size_t)k * kJoinWarps * C::ROWS];
             y[4 * k] += v.x * f, y[4 * k + 1] += v.y * f, y[4 * k + 2] += v.z * f, y[4 * k + 3] += v.w * f;
           }

@@ -40,6 +40,28 @@ def test_infinite_committed_values(dtype, dim, lens, new):
     assert torch.equal(out[:, 4:, rest].view(torch.int16), want[:, 4:, rest].view(torch.int16))
 
 
+@pytest.mark.parametrize("batch", [2, 64], ids=["divided", "whole"])
+@pytest.mark.parametrize("dtype,dim", [(BF, 128), (FP, 64), (BF, 256)])
+def test_weights_of_zero_meet_infinite_values(dtype, dim, batch):
+    """A seen key of score -inf has weight 0, and 0 * inf is NaN, however the work is divided: also
+    where a piece, or one of its two streams, holds no other key that the row sees."""
+    new = [3] * batch
+    bt = Batch(dtype, [129] * batch, new, 8, 2, dim, 16, True, trees(new, 4, blind=(0, 1, 2)), seed=dim)
+    bt.q[:, :, 5] = -1.0
+    for b in range(batch):
+        page, row = bt.rows(b)
+        bt.k[page[128], :, row[128], 5] = float("inf")
+    want, want_lse = attend(bt)
+    assert torch.isfinite(want).all() and torch.isfinite(want_lse).all()
+    for b in range(batch):
+        page, row = bt.rows(b)
+        bt.v[page[128], :, row[128], 3] = float("inf")
+    out, lse = attend(bt)
+    assert torch.isnan(out[:, :, 3]).all() and torch.equal(lse, want_lse)
+    rest = [d for d in range(dim) if d != 3]
+    assert torch.equal(out[:, :, rest].view(torch.int16), want[:, :, rest].view(torch.int16))
+
+
 @pytest.mark.parametrize("case", [
     (BF, [0], [2451], 2, 4, 128, 64, False),           # a prompt into an empty cache
     (FP, [4096, 0], [256, 1031], 1, 8, 64, 16, False),  # a later part of one, beside another
