@@ -38,7 +38,9 @@ extern "C" {
 /* Element types of q, k, v and the cache (all of one type in a call). */
 enum { ATTN_BF16 = 0, ATTN_FP16 = 1 };
 
-/* Bits of the device status word, beside MOE_DEV_TIMEOUT. */
+/* Bits of the device status word, beside MOE_DEV_TIMEOUT (a wait of
+ * attn_tree_decode or attn_cache_weights has run out: their outputs are NaN
+ * where that wait was for them). */
 enum {
   ATTN_DEV_BAD_PAGE = 32,  /* a page number outside [0, pages) */
   ATTN_DEV_BAD_LENGTH = 64 /* lens or cu out of range */

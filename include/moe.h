@@ -329,7 +329,8 @@ const char* moe_status_string(int status);
  * moe_experts_decode's one-shot kernel and of the attention kernels (attn.h),
  * so that a test can make a wait run out without faulting or hanging the GPU.  The pages have no counterpart.
  * wait_ns: the limit of every bounded wait in those kernels (0 restores the
- *   default of 2 s; otherwise 1 us .. 10 s).
+ *   default of 2 s; otherwise 1 us .. 10 s).  Not of the attention kernels' last
+ *   waits, for copies and products in flight: these keep 2 s.
  * barrier_extra_arrivals: 0, or 1 to make every grid barrier wait for one
  *   arrival more than the grid makes -- it then runs out after wait_ns, the
  *   launch sets MOE_DEV_TIMEOUT and writes NaN outputs.  Zero the workspace
