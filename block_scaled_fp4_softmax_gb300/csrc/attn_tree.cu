@@ -16,7 +16,7 @@
 // Measured, BF16 (copy bandwidth 6.69 TB/s, library GEMM 1.90 PFLOP/s):
 //   32 sequences of 16384 slots, 4 x 8 heads of 128  177 us, 6.1 TB/s
 //   32 ragged ones of 1024 .. 8192, the same         72 us, 4.4 TB/s
-//   8 of 16384, 504 rows, D = 128                   127 us, 1.07 PFLOP/s
+//   8 of 16384, 504 rows, D = 128                   125 us, 1.08 PFLOP/s
 //   1 of 300001, 136 rows, D = 256 (FP16)           166 us, 3.7 TB/s
 //   1 of 1000, 4 rows, D = 128                       16 us
 // Of the ragged batch's time some 20 us do not grow with the bytes: launch, plan and
