@@ -9,4 +9,4 @@ loads nothing; the library is loaded on first use and must have been built
 (:func:`.build.build`).
 """
 
-__all__ = ["attn", "build", "moe", "speculate", "synth"]
+__all__ = ["attn", "build", "fp4", "moe", "speculate", "synth"]

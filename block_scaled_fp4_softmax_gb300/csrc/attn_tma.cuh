@@ -25,19 +25,26 @@ inline long long wait_cycles() { return 2 * (long long)moe::wait_limit_ns(); }
 // ... of one behind which shared memory or TMEM is given up: some 2 s, whatever the others' limit.
 constexpr long long kDrainCycles = 4000000000ll;
 
-inline int make_map(const attn_cache& c, void* base, int box_rows, bool head_inner, CUtensorMap* m) {
-  typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+typedef CUresult (*MapEncoder)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+// The driver's cuTensorMapEncodeTiled, looked up once; NULL where there is none.
+inline MapEncoder map_encoder() {
   static std::atomic<void*> entry{nullptr};
   void* f = entry.load(std::memory_order_acquire);
   if (!f) {
     cudaDriverEntryPointQueryResult found;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
             cudaSuccess || found != cudaDriverEntryPointSuccess || !f)
-      return MOE_ERR_CUDA;
+      return nullptr;
     entry.store(f, std::memory_order_release);
   }
+  return reinterpret_cast<MapEncoder>(f);
+}
+
+inline int make_map(const attn_cache& c, void* base, int box_rows, bool head_inner, CUtensorMap* m) {
+  const MapEncoder encode = map_encoder();
+  if (!encode) return MOE_ERR_CUDA;
   const cuuint64_t rows = c.page_size, heads = c.kv_heads;
   const cuuint64_t sr = (cuuint64_t)c.row_stride * 2, sh = (cuuint64_t)c.head_stride * 2;
   const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, head_inner ? heads : rows, head_inner ? rows : heads,
@@ -45,7 +52,7 @@ inline int make_map(const attn_cache& c, void* base, int box_rows, bool head_inn
   const cuuint64_t strides[3] = {head_inner ? sh : sr, head_inner ? sr : sh, (cuuint64_t)c.page_stride * 2};
   const cuuint32_t br = (cuuint32_t)box_rows;
   const cuuint32_t box[4] = {64, head_inner ? 1 : br, head_inner ? br : 1, 1}, one[4] = {1, 1, 1, 1};
-  const CUresult rc = reinterpret_cast<Encode>(f)(
+  const CUresult rc = encode(
       m, c.dtype == ATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base, dims,
       strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

@@ -169,6 +169,22 @@ __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t byte_in_low8) {
   return h2;
 }
 
+// Nearest E4M3 (ties to even, saturating) as its byte.
+__device__ __forceinline__ uint32_t f32_to_e4m3_rn_sat(float v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(v));
+  return r & 0xFFu;  // second source lands in the low byte
+}
+
+// Two floats -> one byte of e2m1 codes: `lo` to the low nibble.
+__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
+      : "=r"(r)
+      : "f"(hi), "f"(lo));
+  return r;
+}
+
 // Packed FP32 FMA: (d.x, d.y) = (a.x * b.x + c.x, a.y * b.y + c.y).
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
   unsigned long long ra, rb, rc, rd;

@@ -1,0 +1,421 @@
+// Products of two FP4 matrices on the 5th-generation tensor cores, whose MMA takes
+// e2m1 operands and their block scales (kind::mxf4nvf4, 64 columns a step).
+//
+//   D[n, t] = sum_k w[n, k] x[t, k]      weights on the M side, 128 rows a tile
+//
+// Chunks of 256 columns go through a ring in shared memory: codes by TMA (128 bytes a
+// row, 128-byte swizzle), block scales by bulk copies (they lie in memory as
+// the tensor core wants them, 512 bytes for 128 rows x 4 blocks), from where
+// tcgen05.cp takes them to TMEM beside the sums.
+//
+// Few rows of x are bound by the weights' bytes: a tile's columns are split over a
+// cluster of CTAs, whose sums meet in distributed shared memory in a fixed order.
+#include <math.h>
+
+#include "attn_tma.cuh"
+#include "fp4.cuh"
+
+using namespace moe::tc;
+
+namespace {
+
+constexpr int kThreads = 192;  // warps 0-3: epilogue; 4: copies; 5: MMA
+constexpr int kTmaWarp = 4, kMmaWarp = 5;
+constexpr int kChunk = 256;    // columns of a ring slot
+constexpr float kNaN = __builtin_nanf("");
+
+struct LinearArgs {
+  CUtensorMap w_map, x_map;
+  const uint8_t *w_scales, *x_scales;
+  const float *w_row, *x_row, *bias;
+  int n, t, cols;  // columns of y, rows of y, summed columns
+  void* y;
+  long long y_stride;
+  int y_type;
+  int split;  // CTAs of a cluster: parts of the summed columns
+  long long wait_cycles;
+  int extra;  // arrivals that never come, on the barrier of the sums
+  int32_t* st;
+};
+
+template <int FMT, int BN_>
+struct Cfg {
+  static constexpr int BN = BN_;                               // rows of x of a tile
+  static constexpr bool NV = FMT == MOE_FMT_NVFP4;
+  static constexpr int COPIES = NV ? 4 : 2;                    // tiles of scales of a chunk
+  static constexpr int W_BYTES = 128 * 128, X_BYTES = BN * 128, S_BYTES = COPIES * 512;
+  static constexpr int SLOT = W_BYTES + X_BYTES + 2 * S_BYTES;
+  // two CTAs to an SM: one's loads run while the other starts or ends
+  static constexpr int SLOTS = (113 * 1024 - 3072) / SLOT;
+  static constexpr int S_COLS = COPIES * 4;                    // TMEM columns of a chunk's scales, of either side
+  static constexpr int SETS = 4;                               // chunks whose scales TMEM holds
+  static constexpr int S_COL = BN <= 32 ? 32 : BN;             // first of them, behind the sums
+  static constexpr int TMEM = S_COL + SETS * 2 * S_COLS <= 128 ? 128 : 256;
+  static_assert(S_COL + SETS * 2 * S_COLS <= TMEM, "TMEM");
+  static_assert(SLOTS >= 3 && SLOTS * SLOT >= BN * 128 * 4, "ring");
+};
+
+struct Control {
+  uint64_t full[8], empty[8], done, drain;
+  uint32_t tmem;
+  int abort;
+};
+
+template <class C>
+constexpr size_t smem_bytes(int slots) {
+  return 1024 + (size_t)slots * C::SLOT + sizeof(Control);
+}
+
+// Instruction descriptor of kind::mxf4nvf4: e2m1 operands, both K-major, M = 128.
+// `id`: which bytes of the scales' words a step of two scales a row takes.
+template <int FMT>
+__device__ constexpr uint32_t idesc_fp4(int N, int id) {
+  return ((uint32_t)id << 4)                         // bytes of B's scales
+         | (1u << 7) | (1u << 10)                    // A and B: e2m1
+         | ((uint32_t)(N >> 3) << 17)                // N / 8
+         | (FMT == MOE_FMT_MXFP4 ? 1u << 23 : 0u)    // scales: UE8M0, or E4M3
+         | (8u << 24)                                // M / 16
+         | ((uint32_t)id << 29);                     // bytes of A's scales
+}
+
+// Descriptor of 512 bytes of scales: 32 rows of 16 bytes, no swizzle.
+__device__ __forceinline__ uint64_t scales_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(128 >> 4) << 32;  // next 8 rows
+  d |= (uint64_t)1 << 46;           // descriptor version
+  return d;
+}
+// ... to 32 lanes x 4 columns of TMEM, the same for each of the four warps' lanes.
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+template <int FMT>
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                        uint32_t accumulate) {
+  if constexpr (FMT == MOE_FMT_NVFP4) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+  }
+}
+
+// 128 bytes from x of `box` rows from row y on; what lies outside reads as zeros.
+__device__ __forceinline__ void load_codes(const CUtensorMap* m, uint32_t dst, uint64_t* bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(m), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A float of another CTA's shared memory, at the address that it has in this one's.
+__device__ __forceinline__ float peer_float(uint32_t saddr, int rank) {
+  uint32_t at;
+  float v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(saddr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void store_one(void* y, long long at, int type, float v) {
+  if (type == FP4_FP32) static_cast<float*>(y)[at] = v;
+  else if (type == FP4_BF16) static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16(v);
+  else static_cast<__half*>(y)[at] = __float2half(v);
+}
+
+// Grid: split * ceil(n / 128) * ceil(t / BN), in clusters of `split`.
+template <int FMT, int BN>
+__global__ void __launch_bounds__(kThreads, 2) linear_kernel(const __grid_constant__ LinearArgs a, int slots) {
+  using C = Cfg<FMT, BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  Control& ctl = *reinterpret_cast<Control*>(ring + (size_t)slots * C::SLOT);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = a.split > 1 ? (int)cluster_rank() : 0;
+  const int t_tiles = (a.t + BN - 1) / BN, tile = blockIdx.x / a.split;
+  const int n0 = tile / t_tiles * 128, t0 = tile % t_tiles * BN;
+  const int chunks = (a.cols + kChunk - 1) / kChunk;
+  const int c0 = chunks * rank / a.split, c1 = chunks * (rank + 1) / a.split;
+  const int tiles = fp4::scale_tiles(a.cols, FMT);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < slots; ++i) {
+      mbar_init(&ctl.full[i], 1);
+      mbar_init(&ctl.empty[i], 1);
+    }
+    mbar_init(&ctl.done, 1 + a.extra);
+    mbar_init(&ctl.drain, 1);
+    ctl.abort = 0;
+    mbar_fence_init();
+    attn::prefetch_map(&a.w_map);
+    attn::prefetch_map(&a.x_map);
+  }
+  // TMEM is taken only when the kernel before has ended, and before the next one may
+  // start: CTAs that wait for one another's kernels never hold what the others need.
+  moe::pdl_wait();
+  if (warp == kMmaWarp) tmem_alloc(&ctl.tmem, C::TMEM);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  moe::pdl_launch_dependents();
+  const uint32_t tmem = ctl.tmem;
+  volatile int* abort_flag = &ctl.abort;
+
+  if (warp == kTmaWarp) {
+    if (lane == 0) {
+      bool alive = true;
+      int filled = 0;
+      for (int c = c0; c < c1; ++c, ++filled) {
+        const int slot = filled % slots;
+        alive = attn::bounded_wait(&ctl.empty[slot], ((filled / slots) & 1) ^ 1, a.wait_cycles, abort_flag, a.st);
+        if (!alive) break;
+        const uint32_t at = smem_u32(ring + (size_t)slot * C::SLOT);
+        const int kt = c * C::COPIES, count = min(C::COPIES, tiles - kt);  // tiles of scales
+        mbar_arrive_expect_tx(&ctl.full[slot], C::W_BYTES + C::X_BYTES + 2 * count * 512);
+        load_codes(&a.w_map, at, &ctl.full[slot], c * (kChunk / 2), n0);
+        load_codes(&a.x_map, at + C::W_BYTES, &ctl.full[slot], c * (kChunk / 2), t0);
+        bulk_g2s(at + C::W_BYTES + C::X_BYTES, a.w_scales + ((size_t)(n0 >> 7) * tiles + kt) * 512, count * 512,
+                 &ctl.full[slot]);
+        bulk_g2s(at + C::W_BYTES + C::X_BYTES + C::S_BYTES, a.x_scales + ((size_t)(t0 >> 7) * tiles + kt) * 512,
+                 count * 512, &ctl.full[slot]);
+      }
+      // every copy has landed before the CTA's shared memory goes away
+      for (int i = max(0, filled - slots); i < filled; ++i)
+        attn::bounded_wait(&ctl.full[i % slots], (i / slots) & 1, attn::kDrainCycles, nullptr, a.st);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      bool alive = true;
+      const uint64_t w_desc = sw128_kmajor_desc(smem_u32(ring)), x_desc = sw128_kmajor_desc(smem_u32(ring) + C::W_BYTES);
+      for (int c = c0, i = 0; c < c1; ++c, ++i) {
+        const int slot = i % slots;
+        alive = attn::bounded_wait(&ctl.full[slot], (i / slots) & 1, a.wait_cycles, abort_flag, a.st);
+        // The products that took the scales whose place these get have been made (with
+        // as many slots or fewer, the copy that has landed waited for them already).
+        if (alive && C::SETS < slots && i >= C::SETS)
+          alive = attn::bounded_wait(&ctl.empty[(i - C::SETS) % slots], ((i - C::SETS) / slots) & 1, a.wait_cycles,
+                                     abort_flag, a.st);
+        if (!alive) break;
+        fence_after_sync();
+        const uint32_t off = (uint32_t)slot * (C::SLOT >> 4);
+        const uint32_t scales = smem_u32(ring + (size_t)slot * C::SLOT) + C::W_BYTES + C::X_BYTES;
+        const uint32_t set = tmem + C::S_COL + (i % C::SETS) * 2 * C::S_COLS;
+        const int steps = min(kChunk, a.cols - c * kChunk + 63) / 64;
+#pragma unroll
+        for (int k = 0; k < kChunk / 64; ++k) {
+          if (k >= steps) break;
+          const int copy = C::NV ? k : k / 2, id = C::NV ? 0 : 2 * (k & 1);
+          const uint32_t sw = set + 4 * copy, sx = sw + C::S_COLS;
+          if (id == 0) {
+            copy_scales(sw, scales_desc(scales + copy * 512));
+            copy_scales(sx, scales_desc(scales + C::S_BYTES + copy * 512));
+          }
+          mma_fp4<FMT>(tmem, w_desc + off + 2 * k, x_desc + off + 2 * k, idesc_fp4<FMT>(BN, id), sw, sx, i > 0 || k > 0);
+        }
+        mma_commit(&ctl.empty[slot]);
+      }
+      mma_commit(&ctl.done);
+      // TMEM goes back only when every MMA has completed
+      mma_commit(&ctl.drain);
+      attn::bounded_wait(&ctl.drain, 0, attn::kDrainCycles, nullptr, a.st);
+    }
+    __syncwarp();
+  } else {
+    attn::bounded_wait(&ctl.done, 0, a.wait_cycles, abort_flag, a.st);
+    __syncwarp();
+  }
+  __syncthreads();  // no copy is under way any more, and nobody gives up from here on
+  const bool ok = !*abort_flag;
+  if (warp < 4) {
+    fence_after_sync();
+    const uint32_t sums = tmem + ((uint32_t)(warp * 32) << 16);
+    const int n = n0 + threadIdx.x;
+    const float scale = a.w_row && n < a.n ? __ldg(a.w_row + n) : 1.f;
+    const float add = a.bias && n < a.n ? __ldg(a.bias + n) : 0.f;
+    auto put = [&](int j, float v) {
+      const int t = t0 + j;
+      if (n >= a.n || t >= a.t) return;
+      if (a.x_row) v *= __ldg(a.x_row + t);
+      store_one(a.y, t * a.y_stride + n, a.y_type, ok ? fmaf(v, scale, add) : kNaN);
+    };
+    float* part = reinterpret_cast<float*>(ring);  // [BN][128], where the chunks were
+#pragma unroll 1
+    for (int j = 0; j < BN; j += 16) {
+      uint32_t r[16];
+      tmem_ld16(sums + j, r);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float v = __uint_as_float(r[i]);
+        if (a.split == 1) put(j + i, v);
+        else part[(j + i) * 128 + threadIdx.x] = ok ? v : kNaN;
+      }
+    }
+    fence_before_sync();
+  }
+  if (a.split > 1) {
+    cluster_sync();
+    if (threadIdx.x < 128) {
+      const int n = n0 + threadIdx.x;
+      const float scale = a.w_row && n < a.n ? __ldg(a.w_row + n) : 1.f;
+      const float add = a.bias && n < a.n ? __ldg(a.bias + n) : 0.f;
+      const int j1 = min(BN * (rank + 1) / a.split, a.t - t0);
+      for (int j = BN * rank / a.split; j < j1; ++j) {
+        const uint32_t at = smem_u32(ring) + (uint32_t)(j * 128 + threadIdx.x) * 4;
+        float v = 0.f;
+        for (int k = 0; k < a.split; ++k) v += peer_float(at, k);
+        if (n >= a.n) continue;
+        if (a.x_row) v *= __ldg(a.x_row + t0 + j);
+        store_one(a.y, (t0 + j) * a.y_stride + n, a.y_type, fmaf(v, scale, add));
+      }
+    }
+    cluster_sync();  // the others have read this CTA's part
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, C::TMEM);
+}
+
+int make_map(const void* codes, int rows, int cols, int box, CUtensorMap* m) {
+  const attn::MapEncoder encode = attn::map_encoder();
+  if (!encode) return MOE_ERR_CUDA;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols / 2, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)cols / 2};
+  const cuuint32_t boxes[2] = {128, (cuuint32_t)box}, one[2] = {1, 1};
+  const CUresult rc = encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, boxes, one,
+                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return rc == CUDA_SUCCESS ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+
+template <int FMT, int BN>
+int launch(LinearArgs& a, const fp4_matrix& x, const fp4_matrix& w, int sms, cudaStream_t st) {
+  using C = Cfg<FMT, BN>;
+  static moe::SmemGrant grant;
+  if (const int rc = make_map(w.codes, w.rows, w.cols, 128, &a.w_map)) return rc;
+  if (const int rc = make_map(x.codes, x.rows, x.cols, BN, &a.x_map)) return rc;
+  if (!moe::grant_smem(linear_kernel<FMT, BN>, smem_bytes<C>(C::SLOTS), grant)) return MOE_ERR_CUDA;
+  const int n_tiles = (a.n + 127) / 128, t_tiles = (a.t + BN - 1) / BN, chunks = (a.cols + kChunk - 1) / kChunk;
+  // the split that leaves the busiest SM the fewest chunks
+  a.split = 1;
+  long long best = 1ll << 62;
+  for (int s = 1; s <= 8 && s <= chunks; s *= 2) {
+    const long long waves = ((long long)n_tiles * t_tiles * s + sms - 1) / sms, cost = waves * ((chunks + s - 1) / s + 1);
+    if (cost < best) best = cost, a.split = s;
+  }
+  const int slots = C::SLOTS;
+  const long long blocks = (long long)n_tiles * t_tiles * a.split;
+  if (blocks > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<C>(slots);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.split, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, linear_kernel<FMT, BN>, a, slots) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+template <int FMT>
+int launch(LinearArgs& a, const fp4_matrix& x, const fp4_matrix& w, int sms, cudaStream_t st) {
+  if (a.t <= 16) return launch<FMT, 16>(a, x, w, sms, st);
+  if (a.t <= 32) return launch<FMT, 32>(a, x, w, sms, st);
+  if (a.t <= 64) return launch<FMT, 64>(a, x, w, sms, st);
+  return launch<FMT, 128>(a, x, w, sms, st);
+}
+
+// Where fp4_linear_rows keeps its quantised rows.
+struct Layout {
+  size_t scales, row_scale, bytes;
+};
+Layout layout(int rows, int cols, int format) {
+  Layout l;
+  l.scales = ((size_t)rows * cols / 2 + 255) & ~(size_t)255;
+  l.row_scale = l.scales + fp4_scale_bytes(rows, cols, format);
+  l.bytes = l.row_scale + (size_t)rows * sizeof(float);
+  return l;
+}
+
+int check_output(const fp4_rows* y, int rows, int cols) {
+  if (!y || (!y->data && rows > 0 && cols > 0)) return MOE_ERR_INVALID_ARG;
+  if (y->type != FP4_BF16 && y->type != FP4_FP16 && y->type != FP4_FP32) return MOE_ERR_UNSUPPORTED;
+  if ((uintptr_t)y->data % fp4::element_bytes(y->type)) return MOE_ERR_ALIGNMENT;
+  if (rows > 1 && (y->stride < cols || y->stride >= (1ll << 38))) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fp4_linear(const fp4_matrix* x, const fp4_matrix* w, const float* bias, const fp4_rows* y,
+               int32_t* dev_status, void* stream) {
+  if (const int rc = fp4::check_matrix(x)) return rc;
+  if (const int rc = fp4::check_matrix(w)) return rc;
+  if (x->cols != w->cols || x->format != w->format) return MOE_ERR_INVALID_ARG;
+  if (const int rc = check_output(y, x->rows, w->rows)) return rc;
+  if ((uintptr_t)bias & 3u) return MOE_ERR_ALIGNMENT;
+  if (x->rows == 0 || w->rows == 0) return MOE_OK;
+  const int sms = moe::device_info().sms;
+  if (sms <= 0) return MOE_ERR_CUDA;
+  LinearArgs a;
+  a.w_scales = static_cast<const uint8_t*>(w->scales), a.x_scales = static_cast<const uint8_t*>(x->scales);
+  a.w_row = w->row_scale, a.x_row = x->row_scale, a.bias = bias;
+  a.n = w->rows, a.t = x->rows, a.cols = x->cols;
+  a.y = y->data, a.y_stride = x->rows > 1 ? y->stride : 0, a.y_type = y->type;
+  a.wait_cycles = attn::wait_cycles(), a.extra = (int)moe::barrier_extra(), a.st = dev_status;
+  return w->format == MOE_FMT_NVFP4 ? launch<MOE_FMT_NVFP4>(a, *x, *w, sms, (cudaStream_t)stream)
+                                    : launch<MOE_FMT_MXFP4>(a, *x, *w, sms, (cudaStream_t)stream);
+}
+
+size_t fp4_linear_rows_workspace(const fp4_matrix* w, int rows) {
+  if (!w || rows < 0 || !fp4::shape_ok(rows, w->cols, w->format)) return 0;
+  return layout(rows, w->cols, w->format).bytes + 16;
+}
+
+int fp4_linear_rows(const fp4_rows* x, int rows, const fp4_matrix* w, const float* bias, const fp4_rows* y,
+                    void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream) {
+  if (rows < 0) return MOE_ERR_INVALID_ARG;
+  if (const int rc = fp4::check_matrix(w)) return rc;
+  if (!fp4::shape_ok(rows, w->cols, w->format)) return MOE_ERR_UNSUPPORTED;
+  if (const int rc = fp4::check_rows(x, rows, w->cols, true)) return rc;
+  if (const int rc = check_output(y, rows, w->rows)) return rc;
+  if ((uintptr_t)bias & 3u) return MOE_ERR_ALIGNMENT;
+  if (rows == 0 || w->rows == 0) return MOE_OK;
+  if (!workspace) return MOE_ERR_INVALID_ARG;
+  if (!moe::aligned16(workspace)) return MOE_ERR_ALIGNMENT;
+  const Layout l = layout(rows, w->cols, w->format);
+  if (ws_bytes < l.bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  uint8_t* at = static_cast<uint8_t*>(workspace);
+  const fp4_matrix m = {at, at + l.scales,
+                        w->format == MOE_FMT_NVFP4 ? reinterpret_cast<float*>(at + l.row_scale) : nullptr, rows,
+                        w->cols, w->format};
+  if (const int rc = fp4_quantize(x, &m, stream)) return rc;
+  return fp4_linear(&m, w, bias, y, dev_status, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,568 @@
+// What stands between FP4 products: quantisation, SwiGLU and the norms around a
+// residual sum, row by row, and the way back to 16 or 32 bits.
+//
+// A row belongs to `threads` consecutive threads; a thread holds NB units of 8
+// columns, unit u = j * threads + t, so every load and store of a warp is
+// contiguous.  A block of 16 or 32 columns is 2 or 4 neighbouring lanes, four scales
+// (one 32-bit word of the tiled layout) are 8 or 16.  The row stays in registers between its
+// reductions: each element is read once and written once.
+//
+// What bounds these: HBM (they move 3 to 14 bytes for some 20 instructions an
+// element), and for few rows the launch and the row's two or three reductions.
+#include <math.h>
+
+#include <type_traits>
+
+#include "fp4.cuh"
+
+namespace {
+
+constexpr float kNaN = __builtin_nanf("");
+
+// 2^(bits of the exponent field), field from 1 to 254.
+__device__ __forceinline__ float power_field(int field) { return __uint_as_float((uint32_t)field << 23); }
+
+// 8 elements as they lie in memory (plain loads: a residual may be overwritten in place).
+template <bool WIDE>
+struct Raw;
+template <>
+struct Raw<false> {
+  uint4 q;
+  __device__ __forceinline__ void load(const void* base, long long at) {
+    q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
+  }
+  __device__ __forceinline__ void zero() { q = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void floats(int type, float (&f)[8]) const {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 v;
+      if (type == FP4_BF16) {
+        v = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+      } else {
+        v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      }
+      f[2 * i] = v.x, f[2 * i + 1] = v.y;
+    }
+  }
+};
+template <>
+struct Raw<true> {
+  float4 q[2];
+  __device__ __forceinline__ void load(const void* base, long long at) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+    q[0] = p[0], q[1] = p[1];
+  }
+  __device__ __forceinline__ void zero() { q[0] = q[1] = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void floats(int, float (&f)[8]) const {
+    f[0] = q[0].x, f[1] = q[0].y, f[2] = q[0].z, f[3] = q[0].w;
+    f[4] = q[1].x, f[5] = q[1].y, f[6] = q[1].z, f[7] = q[1].w;
+  }
+};
+
+// 8 elements rounded to `type` and written.
+__device__ __forceinline__ void store8(void* base, long long at, int type, const float (&f)[8]) {
+  if (type == FP4_FP32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
+    p[0] = make_float4(f[0], f[1], f[2], f[3]);
+    p[1] = make_float4(f[4], f[5], f[6], f[7]);
+    return;
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (type == FP4_BF16) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&v);
+    } else {
+      const __half2 v = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+  }
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Where a thread stands: blockDim.x threads (a multiple of 32) to a row, blockDim.y
+// rows to a block.
+struct Place {
+  int t, threads, row, cols;
+  bool live;
+  __device__ Place(int rows, int cols_) : t(threadIdx.x), threads(blockDim.x), cols(cols_) {
+    row = blockIdx.x * blockDim.y + threadIdx.y;
+    live = row < rows;
+  }
+  __device__ __forceinline__ int col(int j) const { return (j * threads + t) * 8; }
+  __device__ __forceinline__ bool in(int j) const { return live && col(j) < cols; }
+};
+
+// Reduction over a row's threads, in a fixed order; every thread gets the result.
+// `slots` is used once in a kernel.  All threads of the block call it.
+typedef uint32_t Slots[8][32];
+
+__device__ __forceinline__ uint32_t row_max(uint32_t v, Slots& slots) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  if (blockDim.x == 32) return v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) slots[threadIdx.y][threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = lane < (int)blockDim.x / 32 ? slots[threadIdx.y][lane] : 0u;
+  return __reduce_max_sync(0xffffffffu, v);
+}
+__device__ __forceinline__ float row_sum(float v, Slots& slots) {
+  v = moe::warp_sum(v);
+  if (blockDim.x == 32) return v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) slots[threadIdx.y][threadIdx.x >> 5] = __float_as_uint(v);
+  __syncthreads();
+  v = lane < (int)blockDim.x / 32 ? __uint_as_float(slots[threadIdx.y][lane]) : 0.f;
+  return moe::warp_sum(v);
+}
+
+// ---------------------------------------------------------------------------
+// Quantisation of a row in registers; every thread of the block takes part, with
+// zeros past the row's end.
+// ---------------------------------------------------------------------------
+
+template <int NB>
+__device__ __forceinline__ void to_fp4(const fp4_matrix& m, const Place& p, float (&v)[NB][8], Slots& slots) {
+  const bool nv = m.format == MOE_FMT_NVFP4;
+  // The largest magnitudes as bit patterns: in that order infinities and NaN are
+  // above all numbers.
+  uint32_t top[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
+    a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    if (!nv) a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+    top[j] = a;
+  }
+  float down = 1.f;  // 2^-E
+  bool bad = false;
+  if (nv) {
+    uint32_t a = top[0];
+#pragma unroll
+    for (int j = 1; j < NB; ++j) a = max(a, top[j]);
+    a = row_max(a, slots);
+    bad = a >= 0x7F800000u;
+    // a = f * 2^e: 2688 = 1.3125 * 2^11
+    const int e = max(-126, (int)(a >> 23) - 127 - 11 + ((a & 0x7FFFFFu) > 0x280000u));
+    down = bad ? 0.f : power_field(127 - e);
+    if (p.t == 0 && p.live) m.row_scale[p.row] = bad ? kNaN : power_field(127 + e);
+  } else if (m.row_scale && p.t == 0 && p.live) {
+    m.row_scale[p.row] = 1.f;
+  }
+  const int tiles = fp4::scale_tiles(m.cols, m.format);
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    uint32_t scale, word = 0;
+    float q[8];
+    if (nv) {
+      scale = moe::f32_to_e4m3_rn_sat(__fdiv_rn(__uint_as_float(top[j]) * down, 6.f));
+      if (bad) scale = 0;
+      const float s = moe::e4m3x2_to_f32x2(scale).x;
+      if (scale) {
+        // x / s by Markstein's theorem: from a correctly rounded reciprocal and a
+        // quotient within an ulp, one residual gives the correctly rounded quotient
+        // (ties of e2m1 included), at half the cost of eight divisions.  With the
+        // signs as they are, a zero keeps its own.
+        const float inv = __frcp_rn(s);
+        const float2 inv2 = make_float2(-inv, -inv), s2 = make_float2(s, s), none = make_float2(-0.f, -0.f);
+        const float2 d2 = make_float2(-down, -down);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const float2 x = moe::ffma2(make_float2(v[j][i], v[j][i + 1]), d2, none);  // -x 2^-E
+          const float2 q0 = moe::ffma2(x, inv2, none);
+          const float2 y = moe::ffma2(moe::ffma2(q0, s2, x), inv2, q0);
+          q[i] = y.x, q[i + 1] = y.y;
+        }
+      }
+    } else {
+      const uint32_t a = top[j];
+      // 6 = 1.5 * 2^2
+      scale = a >= 0x7F800000u ? 255u : (uint32_t)max(0, (int)(a >> 23) - 2 + ((a & 0x7FFFFFu) > 0x400000u));
+      if (scale != 255u) {
+        const float mult = power_field(254 - (int)scale);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = v[j][i] * mult;
+      }
+    }
+    if (nv ? scale != 0u : scale != 255u) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) word |= moe::f32x2_to_e2m1x2(q[2 * i], q[2 * i + 1]) << (8 * i);
+    }
+    const int lane = p.t & 31;
+    const bool in = p.in(j);
+    if (!in) scale = 0;
+    // four scales into one word: of lanes 0, 2, 4, 6 (mod 8), or 0, 4, 8, 12 (mod 16)
+    uint32_t four = scale << (8 * ((nv ? lane >> 1 : lane >> 2) & 3));
+    const int step = nv ? 2 : 4;
+    four |= __shfl_xor_sync(0xffffffffu, four, step);
+    four |= __shfl_xor_sync(0xffffffffu, four, 2 * step);
+    if (in) {
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(m.codes) + ((size_t)p.row * m.cols + p.col(j)) / 2) = word;
+      if ((lane & (4 * step - 1)) == 0)
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(m.scales) +
+                                     fp4::scale_word(p.row, p.col(j) / (8 * 4 * step), tiles)) = four;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Kernels
+// ---------------------------------------------------------------------------
+
+struct QuantizeArgs {
+  fp4_rows x;
+  fp4_matrix m;
+};
+
+template <int NB, bool WIDE>
+__global__ void __launch_bounds__(256 * NB) quantize_kernel(const __grid_constant__ QuantizeArgs a) {
+  __shared__ Slots slots;
+  const Place p(a.m.rows, a.m.cols);
+  moe::pdl_wait();
+  moe::pdl_launch_dependents();
+  Raw<WIDE> raw[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    if (p.in(j)) raw[j].load(a.x.data, p.row * a.x.stride + p.col(j));
+    else raw[j].zero();
+  }
+  float v[NB][8];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) raw[j].floats(a.x.type, v[j]);
+  to_fp4<NB>(a.m, p, v, slots);
+}
+
+struct SwigluArgs {
+  fp4_rows gate, up, out;  // out.data, m.codes: NULL where not wanted
+  fp4_matrix m;
+  int rows, cols;
+};
+
+template <int NB, bool WIDE>
+__global__ void __launch_bounds__(256 * NB) swiglu_kernel(const __grid_constant__ SwigluArgs a) {
+  __shared__ Slots slots;
+  const Place p(a.rows, a.cols);
+  moe::pdl_wait();
+  moe::pdl_launch_dependents();
+  Raw<WIDE> g[NB], u[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    if (p.in(j)) {
+      g[j].load(a.gate.data, p.row * a.gate.stride + p.col(j));
+      u[j].load(a.up.data, p.row * a.up.stride + p.col(j));
+    } else {
+      g[j].zero(), u[j].zero();
+    }
+  }
+  float v[NB][8];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    float up[8];
+    g[j].floats(a.gate.type, v[j]);
+    u[j].floats(a.gate.type, up);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[j][i] = v[j][i] / (1.f + __expf(-v[j][i])) * up[i];
+    if (a.out.data && p.in(j)) store8(a.out.data, p.row * a.out.stride + p.col(j), a.out.type, v[j]);
+  }
+  if (a.m.codes) to_fp4<NB>(a.m, p, v, slots);
+}
+
+struct NormArgs {
+  fp4_rows r, y, gate, r_out, h;  // .data NULL: not there
+  int gate_cols;
+  const float *post_weight, *weight;
+  float scale, eps;
+  int rows, cols;
+  fp4_matrix m;  // .codes NULL: not wanted
+};
+
+__device__ __forceinline__ void load_weights(const float* w, int col, float (&f)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(w + col)), b = __ldg(reinterpret_cast<const float4*>(w + col) + 1);
+  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+
+__device__ __forceinline__ float one_element(const fp4_rows& x, long long at) {
+  if (x.type == FP4_FP32) return __ldg(static_cast<const float*>(x.data) + at);
+  const uint16_t b = __ldg(static_cast<const uint16_t*>(x.data) + at);
+  return x.type == FP4_BF16 ? __uint_as_float((uint32_t)b << 16) : __half2float(__ushort_as_half(b));
+}
+
+template <int NB, bool R_WIDE, bool Y_WIDE>
+__global__ void __launch_bounds__(256 * NB) norm_kernel(const __grid_constant__ NormArgs a) {
+  __shared__ Slots slots[3];
+  const Place p(a.rows, a.cols);
+  const float per = 1.f / (float)a.cols;
+  moe::pdl_wait();
+  moe::pdl_launch_dependents();
+  Raw<R_WIDE> r[NB];
+  Raw<Y_WIDE> y[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    if (p.in(j)) r[j].load(a.r.data, p.row * a.r.stride + p.col(j));
+    else r[j].zero();
+    if (a.y.data && p.in(j)) y[j].load(a.y.data, p.row * a.y.stride + p.col(j));
+    else y[j].zero();
+  }
+  float v[NB][8];
+  float factor = a.scale;
+  if (a.y.data) {
+    if (a.gate.data && a.gate_cols == 1 && p.live) factor *= one_element(a.gate, p.row * a.gate.stride);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) y[j].floats(a.y.type, v[j]);
+    if (a.post_weight) {
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fmaf(v[j][i], v[j][i], sum);
+      const float f = 1.f / sqrtf(row_sum(sum, slots[0]) * per + a.eps);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        if (!p.in(j)) continue;
+        float w[8];
+        load_weights(a.post_weight, p.col(j), w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j][i] = v[j][i] * f * w[i];
+      }
+    }
+  }
+  float sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    float x[8];
+    r[j].floats(a.r.type, x);
+    if (a.y.data) {
+      float g[8];
+      if (a.gate.data && a.gate_cols != 1 && p.in(j)) {
+        Raw<Y_WIDE> raw;
+        raw.load(a.gate.data, p.row * a.gate.stride + p.col(j));
+        raw.floats(a.gate.type, g);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = 1.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = fmaf(factor * g[i], v[j][i], x[i]);
+    }
+    if (a.r_out.data && p.in(j)) store8(a.r_out.data, p.row * a.r_out.stride + p.col(j), a.r_out.type, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[j][i] = x[i];
+      sum = fmaf(x[i], x[i], sum);
+    }
+  }
+  const float f = 1.f / sqrtf(row_sum(sum, slots[1]) * per + a.eps);
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    if (!p.in(j)) continue;
+    if (a.weight) {
+      float w[8];
+      load_weights(a.weight, p.col(j), w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j][i] = v[j][i] * f * w[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j][i] *= f;
+    }
+    if (a.h.data) store8(a.h.data, p.row * a.h.stride + p.col(j), a.h.type, v[j]);
+  }
+  if (a.m.codes) to_fp4<NB>(a.m, p, v, slots[2]);
+}
+
+// A thread to 8 columns of a row.
+struct DequantizeArgs {
+  fp4_matrix m;
+  fp4_rows out;
+};
+
+__global__ void __launch_bounds__(256) dequantize_kernel(const __grid_constant__ DequantizeArgs a) {
+  const Place p(a.m.rows, a.m.cols);
+  moe::pdl_wait();
+  moe::pdl_launch_dependents();
+  const int tiles = fp4::scale_tiles(a.m.cols, a.m.format), block = fp4::block_of(a.m.format);
+  const float row = p.live && a.m.row_scale ? __ldg(a.m.row_scale + p.row) : 1.f;
+  for (int col = p.col(0); p.live && col < p.cols; col += 8 * p.threads) {
+    const uint32_t codes = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m.codes) +
+                                                                   ((size_t)p.row * p.cols + col) / 2));
+    const int b = col / block;
+    const uint32_t s = __ldg(static_cast<const uint8_t*>(a.m.scales) + fp4::scale_word(p.row, b >> 2, tiles) + (b & 3));
+    const float scale = a.m.format == MOE_FMT_NVFP4 ? moe::e4m3x2_to_f32x2(s).x : moe::ue8m0_to_f32(s);
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t h2 = moe::e2m1x2_to_f16x2((codes >> (8 * i)) & 0xFFu);
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+      // code * block scale is exact: at most 2 + 4 significant bits
+      f[2 * i] = v.x * scale * row, f[2 * i + 1] = v.y * scale * row;
+    }
+    store8(a.out.data, p.row * a.out.stride + col, a.out.type, f);
+  }
+}
+
+// A thread to the four scales of a row's tile.
+__global__ void __launch_bounds__(256) tile_scales_kernel(const uint8_t* __restrict__ in, int rows, int blocks,
+                                                          int tiles, uint8_t* __restrict__ out) {
+  moe::pdl_wait();
+  moe::pdl_launch_dependents();
+  const long long words = (long long)rows * tiles, step = (long long)gridDim.x * blockDim.x;
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < words; i += step) {
+    const int r = (int)(i / tiles), kt = (int)(i - (long long)r * tiles);
+    uint32_t four = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int b = kt * 4 + k;
+      if (b < blocks) four |= (uint32_t)__ldg(in + (long long)r * blocks + b) << (8 * k);
+    }
+    *reinterpret_cast<uint32_t*>(out + fp4::scale_word(r, kt, tiles)) = four;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------
+
+// Units of a thread by the row's length, and the block's shape: one row, or
+// several short ones.
+struct Shape {
+  int nb;
+  dim3 grid, block;
+  Shape(int rows, int cols) {
+    nb = cols <= 2048 ? 1 : cols <= 8192 ? 2 : 4;
+    const int threads = (cols + 8 * nb * 32 - 1) / (8 * nb * 32) * 32;
+    const int per = threads >= 256 ? 1 : threads == 32 ? 8 : 256 / threads;
+    block = dim3(threads, per);
+    grid = dim3((rows + per - 1) / per);
+  }
+};
+
+template <class F>
+int by_units(int nb, F f) {
+  return nb == 1 ? f(std::integral_constant<int, 1>()) : nb == 2 ? f(std::integral_constant<int, 2>())
+                                                                 : f(std::integral_constant<int, 4>());
+}
+template <class F>
+int by_width(int type, F f) {
+  return type == FP4_FP32 ? f(std::true_type()) : f(std::false_type());
+}
+
+// The stride of a single row is of no account.
+void one_row(fp4_rows& x, int rows) {
+  if (rows == 1) x.stride = 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fp4_scale_bytes(int rows, int cols, int format) {
+  if (!fp4::shape_ok(rows, cols, format)) return 0;
+  return (size_t)((rows + 127) / 128) * fp4::scale_tiles(cols, format) * 512;
+}
+
+int fp4_tile_scales(const uint8_t* scales, int rows, int cols, int format, uint8_t* tiled, void* stream) {
+  if (rows < 0) return MOE_ERR_INVALID_ARG;
+  if (!fp4::shape_ok(rows, cols, format)) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!scales || !tiled) return MOE_ERR_INVALID_ARG;
+  if (!moe::aligned16(tiled)) return MOE_ERR_ALIGNMENT;
+  const int tiles = fp4::scale_tiles(cols, format);
+  const long long blocks = ((long long)rows * tiles + 255) / 256;
+  return moe::launch_pdl(tile_scales_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0,
+                         (cudaStream_t)stream, scales, rows, cols / fp4::block_of(format), tiles, tiled);
+}
+
+int fp4_quantize(const fp4_rows* x, const fp4_matrix* out, void* stream) {
+  if (!out) return MOE_ERR_INVALID_ARG;
+  if (const int rc = fp4::check_target(out, out->rows, out->cols)) return rc;
+  if (const int rc = fp4::check_rows(x, out->rows, out->cols, true)) return rc;
+  if (out->rows == 0) return MOE_OK;
+  QuantizeArgs a{*x, *out};
+  one_row(a.x, out->rows);
+  const Shape s(out->rows, out->cols);
+  return by_units(s.nb, [&](auto nb) {
+    return by_width(x->type, [&](auto wide) {
+      return moe::launch_pdl(quantize_kernel<nb, wide>, s.grid, s.block, 0, (cudaStream_t)stream, a);
+    });
+  });
+}
+
+int fp4_dequantize(const fp4_matrix* m, const fp4_rows* out, void* stream) {
+  if (const int rc = fp4::check_matrix(m)) return rc;
+  if (const int rc = fp4::check_rows(out, m->rows, m->cols, true)) return rc;
+  if (m->rows == 0) return MOE_OK;
+  DequantizeArgs a{*m, *out};
+  one_row(a.out, m->rows);
+  const int threads = m->cols >= 2048 ? 256 : (m->cols + 255) / 256 * 32, per = 256 / threads;
+  return moe::launch_pdl(dequantize_kernel, dim3((m->rows + per - 1) / per), dim3(threads, per), 0,
+                         (cudaStream_t)stream, a);
+}
+
+int fp4_swiglu(const fp4_rows* gate, const fp4_rows* up, int rows, int cols, const fp4_rows* out,
+               const fp4_matrix* m, void* stream) {
+  if (rows < 0 || (!out && !m)) return MOE_ERR_INVALID_ARG;
+  if (!fp4::shape_ok(rows, cols, MOE_FMT_NVFP4)) return MOE_ERR_UNSUPPORTED;
+  if (const int rc = fp4::check_rows(gate, rows, cols, true)) return rc;
+  if (const int rc = fp4::check_rows(up, rows, cols, true)) return rc;
+  if (gate->type != up->type) return MOE_ERR_INVALID_ARG;
+  if (out)
+    if (const int rc = fp4::check_rows(out, rows, cols, false)) return rc;
+  if (m)
+    if (const int rc = fp4::check_target(m, rows, cols)) return rc;
+  if (rows == 0) return MOE_OK;
+  SwigluArgs a{*gate, *up, out ? *out : fp4_rows{}, m ? *m : fp4_matrix{}, rows, cols};
+  one_row(a.gate, rows), one_row(a.up, rows), one_row(a.out, rows);
+  const Shape s(rows, cols);
+  return by_units(s.nb, [&](auto nb) {
+    return by_width(gate->type, [&](auto wide) {
+      return moe::launch_pdl(swiglu_kernel<nb, wide>, s.grid, s.block, 0, (cudaStream_t)stream, a);
+    });
+  });
+}
+
+int fp4_block_norm(const fp4_rows* r, const fp4_rows* y, const float* post_weight, const fp4_rows* gate,
+                   int gate_cols, double scale, const float* weight, double eps, int rows, int cols,
+                   const fp4_rows* r_out, const fp4_rows* h, const fp4_matrix* m, void* stream) {
+  if (rows < 0 || (!h && !m) || !(eps >= 0.) || !(eps <= 1e30) || !(fabs(scale) <= 1e30)) return MOE_ERR_INVALID_ARG;
+  if (!y && (post_weight || gate)) return MOE_ERR_INVALID_ARG;
+  if (!fp4::shape_ok(rows, cols, MOE_FMT_NVFP4)) return MOE_ERR_UNSUPPORTED;
+  if (const int rc = fp4::check_rows(r, rows, cols, true)) return rc;
+  if (y)
+    if (const int rc = fp4::check_rows(y, rows, cols, true)) return rc;
+  if (!moe::aligned16(post_weight) || !moe::aligned16(weight)) return MOE_ERR_ALIGNMENT;
+  NormArgs a{*r, y ? *y : fp4_rows{}, gate ? *gate : fp4_rows{}, r_out ? *r_out : fp4_rows{}, h ? *h : fp4_rows{},
+             gate_cols, post_weight, weight, (float)scale, (float)eps, rows, cols, m ? *m : fp4_matrix{}};
+  if (gate) {
+    if (gate->type != y->type || (gate_cols != 1 && gate_cols != cols)) return MOE_ERR_INVALID_ARG;
+    if (!gate->data && rows > 0) return MOE_ERR_INVALID_ARG;
+    if (gate_cols == 1) {  // a number for each row, at any stride
+      if ((uintptr_t)gate->data % fp4::element_bytes(gate->type)) return MOE_ERR_ALIGNMENT;
+      if (gate->stride < 0 || gate->stride >= (1ll << 38)) return MOE_ERR_INVALID_ARG;
+    } else if (const int rc = fp4::check_rows(gate, gate->stride == 0 ? (rows > 0) : rows, cols, true)) {
+      return rc;
+    }
+  }
+  if (r_out) {
+    if (const int rc = fp4::check_rows(r_out, rows, cols, true)) return rc;
+    if (r_out->type != r->type) return MOE_ERR_INVALID_ARG;
+  }
+  if (h)
+    if (const int rc = fp4::check_rows(h, rows, cols, false)) return rc;
+  if (m)
+    if (const int rc = fp4::check_target(m, rows, cols)) return rc;
+  if (rows == 0) return MOE_OK;
+  for (fp4_rows* x : {&a.r, &a.y, &a.gate, &a.r_out, &a.h}) one_row(*x, rows);
+  const Shape s(rows, cols);
+  return by_units(s.nb, [&](auto nb) {
+    return by_width(r->type, [&](auto rw) {
+      return by_width(y ? y->type : FP4_BF16, [&](auto yw) {
+        return moe::launch_pdl(norm_kernel<nb, rw, yw>, s.grid, s.block, 0, (cudaStream_t)stream, a);
+      });
+    });
+  });
+}
+
+}  // extern "C"

@@ -10,20 +10,8 @@
 
 namespace {
 
-__device__ __forceinline__ uint32_t f32_to_e4m3_rn_sat(float v) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(v));
-  return r & 0xFFu;  // second source lands in the low byte
-}
-
-// Two floats -> one byte of e2m1 codes: `lo` to the low nibble.
-__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
-      : "=r"(r)
-      : "f"(hi), "f"(lo));
-  return r;
-}
+using moe::f32_to_e4m3_rn_sat;
+using moe::f32x2_to_e2m1x2;
 
 template <int G>
 __device__ __forceinline__ void quantize_block(const float* __restrict__ src, uint8_t* codes,

@@ -1,0 +1,226 @@
+"""fp4_linear and fp4_linear_rows against the oracle, and the operators together."""
+import numpy as np
+import pytest
+import torch
+
+from block_scaled_fp4_softmax_gb300 import fp4, moe
+from fp4_helpers import BF, F32, FP, f64, held, random_matrix, rounded
+from oracle import fp4 as O
+
+pytestmark = pytest.mark.gpu
+NV, MX = fp4.NVFP4, fp4.MXFP4
+
+
+def slack(x, w, xr, wr, bias, want):
+    """FP32 sums of K terms, each cut off or rounded once per addition (2^-23 of what
+    has been summed up, at most the sum of magnitudes), the two row scales and the bias."""
+    K = x.shape[1]
+    size = np.abs(x) @ np.abs(w).T
+    size = size * (1 if xr is None else xr[:, None]) * (1 if wr is None else wr)
+    return size * (K + 3) * 2.0 ** -23 + (0 if bias is None else np.abs(bias) * 2.0 ** -23)
+
+
+def check(T, N, K, format, dtype=BF, bias=False, seed=0, row_scale=True, out=None, dev_status=None):
+    x, xc, xs, xr = random_matrix(T, K, format, seed + 1, 0.5, row_scale)
+    w, wc, ws, wr = random_matrix(N, K, format, seed + 2, 0.5, row_scale)
+    b = torch.randn(N, device="cuda") if bias else None
+    y = fp4.fp4_linear(x, w, bias=b, dtype=dtype, out=out, dev_status=dev_status)
+    torch.cuda.synchronize()
+    xv, wv = O.values(xc, xs, None, format), O.values(wc, ws, None, format)
+    want = xv @ wv.T
+    if row_scale:
+        want = want * xr[:, None].astype(np.float64) * wr.astype(np.float64)
+    bv = None if b is None else f64(b)
+    if bias:
+        want = want + bv
+    off = np.abs(f64(y) - want)
+    most = rounded(want, y.dtype, slack(xv, wv, xr, wr, bv, want))
+    ok = (off <= most) | (np.abs(want) > (65504 if y.dtype == FP else np.inf))
+    assert ok.all(), (off.max(), np.argwhere(~ok)[:5], int((~ok).sum()))
+    return x, w, b, y
+
+
+@pytest.mark.parametrize("format", [NV, MX])
+@pytest.mark.parametrize("T,N,K", [
+    (1, 128, 256), (1, 1, 32), (1, 5, 64), (2, 130, 96), (7, 257, 288), (16, 128, 512), (17, 300, 2560), (32, 64, 160),
+    (33, 129, 1056), (64, 1000, 320), (65, 128, 256), (127, 77, 544), (128, 256, 1024), (129, 131, 4128), (300, 640, 2880),
+])
+def test_linear(T, N, K, format):
+    check(T, N, K, format, F32, seed=T + N + K)
+
+
+@pytest.mark.parametrize("format", [NV, MX])
+@pytest.mark.parametrize("dtype", [BF, FP, F32])
+def test_types_and_bias(dtype, format):
+    check(5, 200, 640, format, dtype, bias=True)
+    check(150, 333, 640, format, dtype, bias=True, row_scale=False)
+
+
+@pytest.mark.parametrize("format", [NV, MX])
+def test_long_rows(format):
+    check(3, 140, 32768, format, F32)
+    check(200, 40, 16416, format, F32)
+
+
+@pytest.mark.parametrize("format", [NV, MX])
+@pytest.mark.parametrize("T,N,K", [(700, 1500, 512), (513, 2049, 96), (2000, 515, 288), (1025, 1030, 2080)])
+def test_many_tiles(T, N, K, format):
+    check(T, N, K, format, BF, bias=True)
+    check(T, N, K, format, F32)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,N", [(3, 130), (40, 257), (260, 511), (600, 700)])
+def test_output_is_a_strided_view(T, N, dtype):
+    """Nothing between the rows is written, at any alignment."""
+    for pad, off in ((3, 0), (13, 1), (16, 8)):
+        big = torch.full((T + 1, N + pad), 7.0, device="cuda", dtype=dtype)
+        check(T, N, 320, NV, out=big[:T, off:off + N])
+        assert (big[T] == 7).all() and (big[:, :off] == 7).all() and (big[:, off + N:] == 7).all()
+
+
+def test_every_scale_reaches_its_block():
+    """One element of each row and one block scale at a time stand out."""
+    for format, block in ((NV, 16), (MX, 32)):
+        K, T, N = 512, 140, 300
+        xc = np.full((T, K), 2, np.uint8)
+        wc = np.full((N, K), 2, np.uint8)
+        one = 0x38 if format == NV else 127
+        xs, ws = np.full((T, K // block), one, np.uint8), np.full((N, K // block), one, np.uint8)
+        up = 8 if format == NV else 1  # twice
+        for t in range(T):
+            xs[t, t % (K // block)] += up * (1 + t % 3)
+        for n in range(N):
+            ws[n, (n * 7) % (K // block)] += up * (1 + n % 2)
+        x, w = (fp4.fp4_matrix(torch.from_numpy(O.pack(c)).cuda(), torch.from_numpy(s).cuda(), format=format)
+                for c, s in ((xc, xs), (wc, ws)))
+        want = O.values(xc, xs, None, format) @ O.values(wc, ws, None, format).T
+        assert np.array_equal(f64(fp4.fp4_linear(x, w, dtype=F32)), want)
+        assert np.array_equal(f64(fp4.fp4_linear(w, x, dtype=F32)), want.T)
+        few = fp4.fp4_matrix(torch.from_numpy(O.pack(xc[:9])).cuda(), torch.from_numpy(xs[:9]).cuda(), format=format)
+        assert np.array_equal(f64(fp4.fp4_linear(few, w, dtype=F32)), want[:9])
+
+
+@pytest.mark.parametrize("format", [NV, MX])
+@pytest.mark.parametrize("T", [4, 150, 600])
+def test_nan_stays_in_its_row_and_column(format, T):
+    N, K = 260, 1056
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn(T, K, generator=g, device="cuda").to(BF)
+    wx = torch.randn(N, K, generator=g, device="cuda")
+    clean = fp4.fp4_linear(fp4.fp4_quantize(x, format), fp4.fp4_quantize(wx, format))
+    x[T - 2, 40], wx[131, K - 1] = float("nan"), float("inf")
+    y = fp4.fp4_linear(fp4.fp4_quantize(x, format), fp4.fp4_quantize(wx, format))
+    bad = torch.zeros(T, N, dtype=torch.bool, device="cuda")
+    bad[T - 2], bad[:, 131] = True, True
+    assert torch.isnan(y[bad]).all()
+    assert torch.equal(y[~bad], clean[~bad])
+
+
+@pytest.mark.parametrize("format", [NV, MX])
+@pytest.mark.parametrize("T", [1, 3, 16, 17, 90, 200, 700])
+def test_rows_are_quantised(T, format):
+    """fp4_linear_rows is fp4_linear of fp4_quantize, bit by bit, from any type and stride."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    w = fp4.fp4_quantize(torch.randn(500, 1120, generator=g, device="cuda"), format)
+    bias = torch.randn(500, device="cuda")
+    ws = fp4.fp4_linear_rows_workspace(w, 1000)
+    for dtype in (BF, FP, F32):
+        x = (torch.randn(T, 1200, generator=g, device="cuda") * 3).to(dtype)[:, :1120]
+        want = fp4.fp4_linear(fp4.fp4_quantize(x, format), w, bias=bias)
+        ws.random_()
+        assert torch.equal(fp4.fp4_linear_rows(x, w, bias=bias, workspace=ws), want)
+        assert torch.equal(fp4.fp4_linear_rows(x, w, bias=bias), want)
+
+
+def test_no_rows_and_no_features():
+    w = fp4.fp4_quantize(torch.randn(40, 64, device="cuda"))
+    none = fp4.fp4_empty(0, 64)
+    assert fp4.fp4_linear(none, w).shape == (0, 40)
+    assert fp4.fp4_linear(w, none).shape == (40, 0)
+    assert fp4.fp4_linear_rows(torch.empty(0, 64, device="cuda"), w).shape == (0, 40)
+
+
+@pytest.mark.parametrize("T", [1, 20, 300, 1500])
+def test_repeats_bit_for_bit(T):
+    x, _, _, _ = random_matrix(T, 2560, NV, 1)
+    w, _, _, _ = random_matrix(1100, 2560, NV, 2)
+    want = fp4.fp4_linear(x, w, dtype=F32)
+    for _ in range(5):
+        assert torch.equal(fp4.fp4_linear(x, w, dtype=F32).view(torch.int32), want.view(torch.int32))
+
+
+@pytest.mark.parametrize("T", [1, 40, 100, 700])
+def test_streams_side_by_side_and_a_graph(T):
+    """Calls that overlap share nothing but their inputs."""
+    x = torch.randn(T, 1024, device="cuda").to(BF)
+    w = fp4.fp4_quantize(torch.randn(3000, 1024, device="cuda"))
+    want = fp4.fp4_linear_rows(x, w)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = []
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for s in streams:
+            outs.append(fp4.fp4_linear_rows(x, w, stream=s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a = fp4.fp4_linear_rows(x, w)
+        b = fp4.fp4_linear_rows(a[:, :1024], w)
+    want_b = fp4.fp4_linear_rows(want[:, :1024], w)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(a, want) and torch.equal(b, want_b)
+
+
+@pytest.mark.parametrize("T,K", [(1, 2560), (8, 256), (40, 4096), (200, 1024), (900, 1024)])
+def test_a_wait_that_runs_out(T, K):
+    """The barrier of the sums expects an arrival that never comes: NaN, the flag, and
+    the next call is right."""
+    x, _, _, _ = random_matrix(T, K, NV, 1)
+    w, _, _, _ = random_matrix(700, K, NV, 2)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want = fp4.fp4_linear(x, w, dev_status=status)
+    assert int(status) == 0
+    moe.moe_test_set_wait_limit(200_000, 1)
+    try:
+        y = fp4.fp4_linear(x, w, dev_status=status)
+        torch.cuda.synchronize()
+    finally:
+        moe.moe_test_set_wait_limit(0, 0)
+    assert int(status) == fp4.DEV_TIMEOUT and torch.isnan(y).all()
+    status.zero_()
+    assert torch.equal(fp4.fp4_linear(x, w, dev_status=status), want) and int(status) == 0
+
+
+@pytest.mark.parametrize("format", [NV, MX])
+@pytest.mark.parametrize("T,H,I", [(1, 256, 128), (35, 2560, 640), (300, 512, 288)])
+def test_shared_expert_between_two_sums(T, H, I, format):
+    """The operators as a layer runs them, each step against the oracle on what the step before handed over."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    r = torch.randn(T, H, generator=g, device="cuda")
+    y = torch.randn(T, H, generator=g, device="cuda").to(BF)
+    w_in = fp4.fp4_quantize(torch.randn(2 * I, H, generator=g, device="cuda") * H ** -0.5, format)
+    w_out = fp4.fp4_quantize(torch.randn(H, I, generator=g, device="cuda") * I ** -0.5, format)
+    ones = torch.ones(H, device="cuda")
+    r1, _, h = fp4.fp4_block_norm(r, y, weight=ones, dtype=None, format=format)
+    both = fp4.fp4_linear(h, w_in)
+    _, a = fp4.fp4_swiglu(both[:, :I], both[:, I:], dtype=None, format=format)
+    down = fp4.fp4_linear(a, w_out)
+    r2, h2, _ = fp4.fp4_block_norm(r1, down, weight=ones, r_out=r1)
+    assert r2 is r1
+    want = held(h) @ held(w_in).T
+    size = np.abs(held(h)) @ np.abs(held(w_in)).T
+    assert (np.abs(f64(both) - want) <= rounded(want, BF, size * (H + 3) * 2.0 ** -23)).all()
+    want = held(a) @ held(w_out).T
+    size = np.abs(held(a)) @ np.abs(held(w_out)).T
+    assert (np.abs(f64(down) - want) <= rounded(want, BF, size * (I + 3) * 2.0 ** -23)).all()
+    # the whole in 64 bits without FP4: what the quantisation costs, no more than its steps.
+    # An element in FP4 is off by at most a sixth of its block's largest (NVFP4), or a third.
+    full, norm = O.block_norm(f64(r), f64(y), None, None, 1.0, None, 1e-6)
+    assert np.abs(held(h) - norm).max() <= np.abs(norm).max() * (1 / 5.6 if format == NV else 1 / 2.9)
+    want_r, want_h = O.block_norm(full, f64(down), None, None, 1.0, None, 1e-6)
+    assert (np.abs(f64(r2) - want_r) <= rounded(want_r, F32, np.abs(full) * 2.0 ** -22 + np.abs(want_r) * 2.0 ** -22)).all()
+    assert (np.abs(f64(h2) - want_h) <= rounded(want_h, BF, (np.abs(want_h) + 1) * 40 * 2.0 ** -24)).all()
