@@ -12,31 +12,15 @@
 // cluster of CTAs, whose sums meet in distributed shared memory in a fixed order.
 #include <math.h>
 
-#include "attn_tma.cuh"
-#include "fp4.cuh"
+#include "fp4_mma.cuh"
 
 using namespace moe::tc;
+using namespace fp4;
 
 namespace {
 
 constexpr int kThreads = 192;  // warps 0-3: epilogue; 4: copies; 5: MMA
 constexpr int kTmaWarp = 4, kMmaWarp = 5;
-constexpr int kChunk = 256;    // columns of a ring slot
-constexpr float kNaN = __builtin_nanf("");
-
-struct LinearArgs {
-  CUtensorMap w_map, x_map;
-  const uint8_t *w_scales, *x_scales;
-  const float *w_row, *x_row, *bias;
-  int n, t, cols;  // columns of y, rows of y, summed columns
-  void* y;
-  long long y_stride;
-  int y_type;
-  int split;  // CTAs of a cluster: parts of the summed columns
-  long long wait_cycles;
-  int extra;  // arrivals that never come, on the barrier of the sums
-  int32_t* st;
-};
 
 template <int FMT, int BN_>
 struct Cfg {
@@ -66,96 +50,20 @@ constexpr size_t smem_bytes(int slots) {
   return 1024 + (size_t)slots * C::SLOT + sizeof(Control);
 }
 
-// Instruction descriptor of kind::mxf4nvf4: e2m1 operands, both K-major, M = 128.
-// `id`: which bytes of the scales' words a step of two scales a row takes.
-template <int FMT>
-__device__ constexpr uint32_t idesc_fp4(int N, int id) {
-  return ((uint32_t)id << 4)                         // bytes of B's scales
-         | (1u << 7) | (1u << 10)                    // A and B: e2m1
-         | ((uint32_t)(N >> 3) << 17)                // N / 8
-         | (FMT == MOE_FMT_MXFP4 ? 1u << 23 : 0u)    // scales: UE8M0, or E4M3
-         | (8u << 24)                                // M / 16
-         | ((uint32_t)id << 29);                     // bytes of A's scales
-}
-
-// Descriptor of 512 bytes of scales: 32 rows of 16 bytes, no swizzle.
-__device__ __forceinline__ uint64_t scales_desc(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(128 >> 4) << 32;  // next 8 rows
-  d |= (uint64_t)1 << 46;           // descriptor version
-  return d;
-}
-// ... to 32 lanes x 4 columns of TMEM, the same for each of the four warps' lanes.
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-}
-
-template <int FMT>
-__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
-                                        uint32_t accumulate) {
-  if constexpr (FMT == MOE_FMT_NVFP4) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
-        : "memory");
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
-        : "memory");
-  }
-}
-
-// 128 bytes from x of `box` rows from row y on; what lies outside reads as zeros.
-__device__ __forceinline__ void load_codes(const CUtensorMap* m, uint32_t dst, uint64_t* bar, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          dst),
-      "l"(m), "r"(x), "r"(y), "r"(smem_u32(bar))
-      : "memory");
-}
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// A float of another CTA's shared memory, at the address that it has in this one's.
-__device__ __forceinline__ float peer_float(uint32_t saddr, int rank) {
-  uint32_t at;
-  float v;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(saddr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-  return v;
-}
-
-__device__ __forceinline__ void store_one(void* y, long long at, int type, float v) {
-  if (type == FP4_FP32) static_cast<float*>(y)[at] = v;
-  else if (type == FP4_BF16) static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16(v);
-  else static_cast<__half*>(y)[at] = __float2half(v);
-}
-
 // Grid: split * ceil(n / 128) * ceil(t / BN), in clusters of `split`.
 template <int FMT, int BN>
-__global__ void __launch_bounds__(kThreads, 2) linear_kernel(const __grid_constant__ LinearArgs a, int slots) {
+__global__ void __launch_bounds__(kThreads, 2) linear_kernel(const __grid_constant__ LinearArgs a, int split,
+                                                            int slots) {
   using C = Cfg<FMT, BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   Control& ctl = *reinterpret_cast<Control*>(ring + (size_t)slots * C::SLOT);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = a.split > 1 ? (int)cluster_rank() : 0;
-  const int t_tiles = (a.t + BN - 1) / BN, tile = blockIdx.x / a.split;
+  const int rank = split > 1 ? (int)cluster_rank() : 0;
+  const int t_tiles = (a.t + BN - 1) / BN, tile = blockIdx.x / split;
   const int n0 = tile / t_tiles * 128, t0 = tile % t_tiles * BN;
   const int chunks = (a.cols + kChunk - 1) / kChunk;
-  const int c0 = chunks * rank / a.split, c1 = chunks * (rank + 1) / a.split;
+  const int c0 = chunks * rank / split, c1 = chunks * (rank + 1) / split;
   const int tiles = fp4::scale_tiles(a.cols, FMT);
 
   if (threadIdx.x == 0) {
@@ -228,10 +136,10 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(const __grid_consta
           const int copy = C::NV ? k : k / 2, id = C::NV ? 0 : 2 * (k & 1);
           const uint32_t sw = set + 4 * copy, sx = sw + C::S_COLS;
           if (id == 0) {
-            copy_scales(sw, scales_desc(scales + copy * 512));
-            copy_scales(sx, scales_desc(scales + C::S_BYTES + copy * 512));
+            copy_scales<1>(sw, scales_desc(scales + copy * 512));
+            copy_scales<1>(sx, scales_desc(scales + C::S_BYTES + copy * 512));
           }
-          mma_fp4<FMT>(tmem, w_desc + off + 2 * k, x_desc + off + 2 * k, idesc_fp4<FMT>(BN, id), sw, sx, i > 0 || k > 0);
+          mma_fp4<FMT, 1>(tmem, w_desc + off + 2 * k, x_desc + off + 2 * k, idesc_fp4<FMT>(128, BN, id), sw, sx, i > 0 || k > 0);
         }
         mma_commit(&ctl.empty[slot]);
       }
@@ -268,23 +176,23 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(const __grid_consta
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float v = __uint_as_float(r[i]);
-        if (a.split == 1) put(j + i, v);
+        if (split == 1) put(j + i, v);
         else part[(j + i) * 128 + threadIdx.x] = ok ? v : kNaN;
       }
     }
     fence_before_sync();
   }
-  if (a.split > 1) {
+  if (split > 1) {
     cluster_sync();
     if (threadIdx.x < 128) {
       const int n = n0 + threadIdx.x;
       const float scale = a.w_row && n < a.n ? __ldg(a.w_row + n) : 1.f;
       const float add = a.bias && n < a.n ? __ldg(a.bias + n) : 0.f;
-      const int j1 = min(BN * (rank + 1) / a.split, a.t - t0);
-      for (int j = BN * rank / a.split; j < j1; ++j) {
+      const int j1 = min(BN * (rank + 1) / split, a.t - t0);
+      for (int j = BN * rank / split; j < j1; ++j) {
         const uint32_t at = smem_u32(ring) + (uint32_t)(j * 128 + threadIdx.x) * 4;
         float v = 0.f;
-        for (int k = 0; k < a.split; ++k) v += peer_float(at, k);
+        for (int k = 0; k < split; ++k) v += peer_float(at, k);
         if (n >= a.n) continue;
         if (a.x_row) v *= __ldg(a.x_row + t0 + j);
         store_one(a.y, (t0 + j) * a.y_stride + n, a.y_type, fmaf(v, scale, add));
@@ -296,17 +204,6 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(const __grid_consta
   if (warp == kMmaWarp) tmem_dealloc(tmem, C::TMEM);
 }
 
-int make_map(const void* codes, int rows, int cols, int box, CUtensorMap* m) {
-  const attn::MapEncoder encode = attn::map_encoder();
-  if (!encode) return MOE_ERR_CUDA;
-  const cuuint64_t dims[2] = {(cuuint64_t)cols / 2, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)cols / 2};
-  const cuuint32_t boxes[2] = {128, (cuuint32_t)box}, one[2] = {1, 1};
-  const CUresult rc = encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, boxes, one,
-                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return rc == CUDA_SUCCESS ? MOE_OK : MOE_ERR_UNSUPPORTED;
-}
-
 template <int FMT, int BN>
 int launch(LinearArgs& a, const fp4_matrix& x, const fp4_matrix& w, int sms, cudaStream_t st) {
   using C = Cfg<FMT, BN>;
@@ -316,14 +213,14 @@ int launch(LinearArgs& a, const fp4_matrix& x, const fp4_matrix& w, int sms, cud
   if (!moe::grant_smem(linear_kernel<FMT, BN>, smem_bytes<C>(C::SLOTS), grant)) return MOE_ERR_CUDA;
   const int n_tiles = (a.n + 127) / 128, t_tiles = (a.t + BN - 1) / BN, chunks = (a.cols + kChunk - 1) / kChunk;
   // the split that leaves the busiest SM the fewest chunks
-  a.split = 1;
+  int split = 1;
   long long best = 1ll << 62;
   for (int s = 1; s <= 8 && s <= chunks; s *= 2) {
     const long long waves = ((long long)n_tiles * t_tiles * s + sms - 1) / sms, cost = waves * ((chunks + s - 1) / s + 1);
-    if (cost < best) best = cost, a.split = s;
+    if (cost < best) best = cost, split = s;
   }
   const int slots = C::SLOTS;
-  const long long blocks = (long long)n_tiles * t_tiles * a.split;
+  const long long blocks = (long long)n_tiles * t_tiles * split;
   if (blocks > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
@@ -334,10 +231,10 @@ int launch(LinearArgs& a, const fp4_matrix& x, const fp4_matrix& w, int sms, cud
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = a.split, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+  attr[1].val.clusterDim.x = split, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = a.split > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, linear_kernel<FMT, BN>, a, slots) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  cfg.numAttrs = split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, linear_kernel<FMT, BN>, a, split, slots) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 template <int FMT>
@@ -345,6 +242,7 @@ int launch(LinearArgs& a, const fp4_matrix& x, const fp4_matrix& w, int sms, cud
   if (a.t <= 16) return launch<FMT, 16>(a, x, w, sms, st);
   if (a.t <= 32) return launch<FMT, 32>(a, x, w, sms, st);
   if (a.t <= 64) return launch<FMT, 64>(a, x, w, sms, st);
+  if (a.t > 256) return launch_wide(a, x, w, sms, st);
   return launch<FMT, 128>(a, x, w, sms, st);
 }
 

@@ -1,0 +1,311 @@
+// Products of FP4 matrices with many rows of x: pairs of CTAs that make one tile of
+// 256 rows of x by BN columns of y between them (cta_group::2).
+//
+// Each CTA of a pair holds its 128 rows of x and half of the tile's rows of w, so
+// that w's codes come to an SM once for 256 rows; the first of the two issues the MMAs of
+// both.  A persistent pair walks over tiles; its ring of chunks (fp4_linear.cu) runs
+// on from tile to tile, and the 8 epilogue warps take the sums from TMEM into
+// registers at once, so that the next tile's products start while they write.
+//
+// Barriers: full (a CTA's own copies), peer_full (the second CTA tells the first that its
+// copies have landed), empty and sums_full (commits, to both CTAs), sums_empty (the
+// epilogue warps of both CTAs, at the first).
+#include "fp4_mma.cuh"
+
+using namespace moe::tc;
+using namespace fp4;
+
+namespace {
+
+constexpr int kEpilogueWarps = 8, kTmaWarp = 8, kMmaWarp = 9, kThreads = 320;
+
+template <int FMT, int BN_>
+struct Cfg {
+  static constexpr int BN = BN_;                                // columns of y of a tile
+  static constexpr bool NV = FMT == MOE_FMT_NVFP4;
+  static constexpr int COPIES = NV ? 4 : 2;                     // tiles of scales of a chunk and 128 rows
+  static constexpr int W_TILES = (BN + 127) / 128;              // 128 rows of w's scales; both CTAs take all
+  static constexpr int X_BYTES = 128 * 128, W_BYTES = BN / 2 * 128, S_BYTES = COPIES * 512;
+  static constexpr int SLOT = X_BYTES + W_BYTES + (1 + W_TILES) * S_BYTES;
+  static constexpr int SLOTS = (227 * 1024 - 8192) / SLOT < 8 ? (227 * 1024 - 8192) / SLOT : 8;
+  static constexpr int SX_COLS = COPIES * 4, SW_COLS = SX_COLS * W_TILES;
+  static constexpr int SETS = 4;                                // chunks whose scales TMEM holds
+  static constexpr int S_COL = BN;
+  static constexpr int TMEM = 512;
+  static_assert(S_COL + SETS * (SX_COLS + SW_COLS) <= TMEM, "TMEM");
+  static_assert(SLOT % 1024 == 0, "the swizzle's alignment");
+};
+
+struct Control {
+  uint64_t full[8], empty[8], peer_full[8];
+  uint64_t sums_full, sums_empty, drain;
+  uint32_t tmem;
+  int abort;
+  float2 column[2][256];  // w's row scale and the bias, of a tile's columns
+};
+template <class C>
+constexpr size_t smem_bytes() {
+  return 1024 + (size_t)C::SLOTS * C::SLOT + sizeof(Control);
+}
+
+// Which tile of the grid of tiles comes i-th: blocks of 8 tiles of rows, so that the
+// tiles that run at a time share both operands in L2.
+struct Tile {
+  int t0, n0;
+  __device__ __forceinline__ Tile(int i, int t_tiles, int n_tiles, int BN) {
+    const int group = i / (8 * n_tiles), first = group * 8, rows = min(8, t_tiles - first);
+    const int k = i - group * 8 * n_tiles;
+    t0 = (first + k % rows) * 256;
+    n0 = k / rows * BN;
+  }
+};
+
+__device__ __forceinline__ void commit_both(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+template <int TYPE>
+__device__ __forceinline__ void store8(void* y, const float* f) {
+  if constexpr (TYPE == FP4_FP32) {
+    reinterpret_cast<float4*>(y)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(y)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  } else {
+    const float(&v)[8] = *reinterpret_cast<const float(*)[8]>(f);
+    *reinterpret_cast<uint4*>(y) = TYPE == FP4_BF16 ? attn::pack8<attn::Brain>(v) : attn::pack8<attn::Half>(v);
+  }
+}
+
+template <int FMT, int BN>
+__global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant__ LinearArgs a, int t_tiles,
+                                                          int n_tiles, int vector) {
+  using C = Cfg<FMT, BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  Control& ctl = *reinterpret_cast<Control*>(ring + (size_t)C::SLOTS * C::SLOT);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int all = t_tiles * n_tiles;
+  const int chunks = (a.cols + kChunk - 1) / kChunk;
+  const int tiles = fp4::scale_tiles(a.cols, FMT);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::SLOTS; ++i) {
+      mbar_init(&ctl.full[i], 1);
+      mbar_init(&ctl.empty[i], 1);
+      mbar_init(&ctl.peer_full[i], 1);
+    }
+    mbar_init(&ctl.sums_full, 1 + a.extra);
+    mbar_init(&ctl.sums_empty, 2 * kEpilogueWarps);
+    mbar_init(&ctl.drain, 1);
+    ctl.abort = 0;
+    mbar_fence_init();
+    attn::prefetch_map(&a.w_map);
+    attn::prefetch_map(&a.x_map);
+  }
+  // (as in fp4_linear.cu: TMEM is taken between the kernel before and the one behind)
+  moe::pdl_wait();
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)),
+                 "r"(C::TMEM)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // the barriers of both CTAs are set up
+  fence_after_sync();
+  moe::pdl_launch_dependents();
+  const uint32_t tmem = ctl.tmem;
+  volatile int* abort_flag = &ctl.abort;
+
+  if (warp == kTmaWarp) {
+    if (lane == 0) {
+      bool alive = true;
+      int i = 0;  // chunks so far
+      for (int at = pair; at < all && alive; at += pairs) {
+        const Tile tile(at, t_tiles, n_tiles, BN);
+        const int t0 = tile.t0 + 128 * rank, n0 = tile.n0;
+        for (int c = 0; c < chunks; ++c, ++i) {
+          const int slot = i % C::SLOTS;
+          alive = cluster_wait(&ctl.empty[slot], ((i / C::SLOTS) & 1) ^ 1, a.wait_cycles, abort_flag, a.st);
+          if (!alive) break;
+          uint64_t* bar = &ctl.full[slot];
+          const uint32_t x = smem_u32(ring + (size_t)slot * C::SLOT), w = x + C::X_BYTES, s = w + C::W_BYTES;
+          const int kt = c * C::COPIES, bytes = min(C::COPIES, tiles - kt) * 512;
+          const int sx = t0 < a.t, sw = min(C::W_TILES, (a.n - n0 + 127) / 128);  // tiles of scales that there are
+          mbar_arrive_expect_tx(bar, C::X_BYTES + C::W_BYTES + (sx + sw) * bytes);
+          load_codes(&a.x_map, x, bar, c * (kChunk / 2), t0);
+          load_codes(&a.w_map, w, bar, c * (kChunk / 2), n0 + BN / 2 * rank);
+          if (sx) bulk_g2s(s, a.x_scales + ((size_t)(t0 >> 7) * tiles + kt) * 512, bytes, bar);
+          for (int k = 0; k < sw; ++k)
+            bulk_g2s(s + (1 + k) * C::S_BYTES, a.w_scales + ((size_t)((n0 >> 7) + k) * tiles + kt) * 512, bytes, bar);
+        }
+      }
+      // every copy has landed before the CTA's shared memory goes away
+      for (int k = max(0, i - C::SLOTS); k < i; ++k)
+        attn::bounded_wait(&ctl.full[k % C::SLOTS], (k / C::SLOTS) & 1, attn::kDrainCycles, nullptr, a.st);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp && rank == 1) {
+    if (lane == 0) {
+      bool alive = true;
+      int i = 0;
+      for (int at = pair; at < all && alive; at += pairs)
+        for (int c = 0; c < chunks && alive; ++c, ++i) {
+          const int slot = i % C::SLOTS;
+          alive = attn::bounded_wait(&ctl.full[slot], (i / C::SLOTS) & 1, a.wait_cycles, abort_flag, a.st);
+          if (alive) arrive_at(&ctl.peer_full[slot], 0);
+        }
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      bool alive = true;
+      int i = 0, done = 0;  // chunks, tiles so far
+      const uint64_t x_desc = sw128_kmajor_desc(smem_u32(ring)), w_desc = sw128_kmajor_desc(smem_u32(ring) + C::X_BYTES);
+      for (int at = pair; at < all && alive; at += pairs, ++done) {
+        if (done > 0)
+          alive = cluster_wait(&ctl.sums_empty, (done - 1) & 1, a.wait_cycles, abort_flag, a.st);
+        for (int c = 0; c < chunks && alive; ++c, ++i) {
+          const int slot = i % C::SLOTS;
+          alive = attn::bounded_wait(&ctl.full[slot], (i / C::SLOTS) & 1, a.wait_cycles, abort_flag, a.st) &&
+                  cluster_wait(&ctl.peer_full[slot], (i / C::SLOTS) & 1, a.wait_cycles, abort_flag, a.st);
+          // the products that took the scales whose place these get have been made
+          if (alive && C::SETS < C::SLOTS && i >= C::SETS)
+            alive = attn::bounded_wait(&ctl.empty[(i - C::SETS) % C::SLOTS], ((i - C::SETS) / C::SLOTS) & 1,
+                                       a.wait_cycles, abort_flag, a.st);
+          if (!alive) break;
+          fence_after_sync();
+          const uint32_t off = (uint32_t)slot * (C::SLOT >> 4);
+          const uint32_t scales = smem_u32(ring + (size_t)slot * C::SLOT) + C::X_BYTES + C::W_BYTES;
+          const uint32_t set = tmem + C::S_COL + (i % C::SETS) * (C::SX_COLS + C::SW_COLS);
+          const int steps = min(kChunk, a.cols - c * kChunk + 63) / 64;
+#pragma unroll
+          for (int k = 0; k < kChunk / 64; ++k) {
+            if (k >= steps) break;
+            const int copy = C::NV ? k : k / 2, id = C::NV ? 0 : 2 * (k & 1);
+            const uint32_t sx = set + 4 * copy, sw = set + C::SX_COLS + 4 * C::W_TILES * copy;
+            if (id == 0) {
+              copy_scales<2>(sx, scales_desc(scales + copy * 512));
+#pragma unroll
+              for (int q = 0; q < C::W_TILES; ++q)
+                copy_scales<2>(sw + 4 * q, scales_desc(scales + (1 + q) * C::S_BYTES + copy * 512));
+            }
+            mma_fp4<FMT, 2>(tmem, x_desc + off + 2 * k, w_desc + off + 2 * k, idesc_fp4<FMT>(256, BN, id), sx, sw,
+                            c > 0 || k > 0);
+          }
+          commit_both(&ctl.empty[slot]);
+        }
+        if (alive) commit_both(&ctl.sums_full);
+      }
+      // TMEM and the ring go back only when every MMA has completed
+      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&ctl.drain))
+                   : "memory");
+      attn::bounded_wait(&ctl.drain, 0, attn::kDrainCycles, nullptr, a.st);
+    }
+    __syncwarp();
+  } else {
+    constexpr int HALF = BN / 2;
+    const int half = warp >> 2;  // of the tile's columns
+    const uint32_t sums = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * HALF;
+    const int item = a.y_type == FP4_FP32 ? 4 : 2;
+    bool alive = true;
+    int done = 0;
+    for (int at = pair; at < all; at += pairs, ++done) {
+      const Tile tile(at, t_tiles, n_tiles, BN);
+      const int t = tile.t0 + 128 * rank + (warp & 3) * 32 + lane;
+      float2* column = ctl.column[done & 1];
+      if (threadIdx.x < BN) {
+        const int n = tile.n0 + threadIdx.x;
+        column[threadIdx.x] = make_float2(a.w_row && n < a.n ? __ldg(a.w_row + n) : 1.f,
+                                          a.bias && n < a.n ? __ldg(a.bias + n) : 0.f);
+      }
+      const float row = a.x_row && t < a.t ? __ldg(a.x_row + t) : 1.f;
+      named_sync(1, 32 * kEpilogueWarps);
+      alive = alive && __all_sync(0xffffffffu, cluster_wait(&ctl.sums_full, done & 1, a.wait_cycles, abort_flag, a.st));
+      fence_after_sync();
+      float v[HALF];
+#pragma unroll
+      for (int i = 0; i < HALF; i += 32) attn::tmem_ld32(sums + i, v + i);
+#pragma unroll
+      for (int i = 0; i < HALF; i += 32) attn::tmem_ld_wait32(v + i);
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0 && alive) arrive_at(&ctl.sums_empty, 0);
+      if (t < a.t) {
+        const int n0 = tile.n0 + half * HALF, left = a.n - n0;
+#pragma unroll
+        for (int i = 0; i < HALF; ++i) {
+          const float2 c = column[half * HALF + i];
+          v[i] = alive ? fmaf(v[i] * row, c.x, c.y) : kNaN;
+        }
+        uint8_t* y = static_cast<uint8_t*>(a.y) + (t * a.y_stride + n0) * item;
+        if (vector && left >= HALF) {
+          if (a.y_type == FP4_BF16) {
+#pragma unroll
+            for (int i = 0; i < HALF; i += 8) store8<FP4_BF16>(y + 2 * i, v + i);
+          } else if (a.y_type == FP4_FP16) {
+#pragma unroll
+            for (int i = 0; i < HALF; i += 8) store8<FP4_FP16>(y + 2 * i, v + i);
+          } else {
+#pragma unroll
+            for (int i = 0; i < HALF; i += 8) store8<FP4_FP32>(y + 4 * i, v + i);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < HALF; ++i)
+            if (i < left) store_one(y, i, a.y_type, v[i]);
+        }
+      }
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  cluster_sync();  // no CTA's shared memory or TMEM is in use by the other any more
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM) : "memory");
+}
+
+template <int FMT, int BN>
+int launch(LinearArgs& a, const fp4_matrix& x, const fp4_matrix& w, int sms, cudaStream_t st) {
+  using C = Cfg<FMT, BN>;
+  static moe::SmemGrant grant;
+  if (const int rc = make_map(x.codes, x.rows, x.cols, 128, &a.x_map)) return rc;
+  if (const int rc = make_map(w.codes, w.rows, w.cols, BN / 2, &a.w_map)) return rc;
+  if (!moe::grant_smem(wide_kernel<FMT, BN>, smem_bytes<C>(), grant)) return MOE_ERR_CUDA;
+  const long long t_tiles = (a.t + 255) / 256, n_tiles = (a.n + BN - 1) / BN;
+  if (t_tiles * n_tiles > 0x3FFFFFFF || 8 * n_tiles > 0x3FFFFFFF) return MOE_ERR_UNSUPPORTED;
+  const int pairs = (int)(t_tiles * n_tiles < sms / 2 ? t_tiles * n_tiles : sms / 2);
+  const int item = fp4::element_bytes(a.y_type);
+  const int vector = moe::aligned16(a.y) && a.y_stride * item % 16 == 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<C>();
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, wide_kernel<FMT, BN>, a, (int)t_tiles, (int)n_tiles, vector) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
+}
+
+}  // namespace
+
+namespace fp4 {
+
+int launch_wide(LinearArgs& a, const fp4_matrix& x, const fp4_matrix& w, int sms, cudaStream_t st) {
+  return w.format == MOE_FMT_NVFP4 ? launch<MOE_FMT_NVFP4, 256>(a, x, w, sms, st)
+                                   : launch<MOE_FMT_MXFP4, 256>(a, x, w, sms, st);
+}
+
+}  // namespace fp4
