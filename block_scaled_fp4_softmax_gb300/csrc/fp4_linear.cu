@@ -113,36 +113,41 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(const __grid_consta
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      bool alive = true;
-      const uint64_t w_desc = sw128_kmajor_desc(smem_u32(ring)), x_desc = sw128_kmajor_desc(smem_u32(ring) + C::W_BYTES);
-      for (int c = c0, i = 0; c < c1; ++c, ++i) {
-        const int slot = i % slots;
-        alive = attn::bounded_wait(&ctl.full[slot], (i / slots) & 1, a.wait_cycles, abort_flag, a.st);
-        // The products that took the scales whose place these get have been made (with
-        // as many slots or fewer, the copy that has landed waited for them already).
-        if (alive && C::SETS < slots && i >= C::SETS)
-          alive = attn::bounded_wait(&ctl.empty[(i - C::SETS) % slots], ((i - C::SETS) / slots) & 1, a.wait_cycles,
-                                     abort_flag, a.st);
-        if (!alive) break;
-        fence_after_sync();
-        const uint32_t off = (uint32_t)slot * (C::SLOT >> 4);
-        const uint32_t scales = smem_u32(ring + (size_t)slot * C::SLOT) + C::W_BYTES + C::X_BYTES;
-        const uint32_t set = tmem + C::S_COL + (i % C::SETS) * 2 * C::S_COLS;
-        const int steps = min(kChunk, a.cols - c * kChunk + 63) / 64;
+    // (the warp walks and waits as one, its elected lane issues; see fp4_linear_wide.cu)
+    const bool leader = attn::elect_lane();
+    const uint64_t w_desc = sw128_kmajor_desc(smem_u32(ring)), x_desc = sw128_kmajor_desc(smem_u32(ring) + C::W_BYTES);
+    const uint64_t s_desc = scales_desc(smem_u32(ring) + C::W_BYTES + C::X_BYTES);
+    for (int c = c0, i = 0; c < c1; ++c, ++i) {
+      const int slot = i % slots;
+      bool ok = attn::bounded_wait(&ctl.full[slot], (i / slots) & 1, a.wait_cycles, abort_flag, a.st);
+      // The products that took the scales whose place these get have been made (with
+      // as many slots or fewer, the copy that has landed waited for them already).
+      if (ok && C::SETS < slots && i >= C::SETS)
+        ok = attn::bounded_wait(&ctl.empty[(i - C::SETS) % slots], ((i - C::SETS) / slots) & 1, a.wait_cycles,
+                                abort_flag, a.st);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      fence_after_sync();
+      const uint32_t off = (uint32_t)slot * (C::SLOT >> 4);
+      const uint32_t set = tmem + C::S_COL + (i % C::SETS) * 2 * C::S_COLS;
+      const int steps = min(kChunk, a.cols - c * kChunk + 63) / 64;
+      if (leader) {
 #pragma unroll
         for (int k = 0; k < kChunk / 64; ++k) {
           if (k >= steps) break;
           const int copy = C::NV ? k : k / 2, id = C::NV ? 0 : 2 * (k & 1);
           const uint32_t sw = set + 4 * copy, sx = sw + C::S_COLS;
           if (id == 0) {
-            copy_scales<1>(sw, scales_desc(scales + copy * 512));
-            copy_scales<1>(sx, scales_desc(scales + C::S_BYTES + copy * 512));
+            copy_scales<1>(sw, s_desc + off + copy * 32);
+            copy_scales<1>(sx, s_desc + off + (C::S_BYTES >> 4) + copy * 32);
           }
-          mma_fp4<FMT, 1>(tmem, w_desc + off + 2 * k, x_desc + off + 2 * k, idesc_fp4<FMT>(128, BN, id), sw, sx, i > 0 || k > 0);
+          mma_fp4<FMT, 1>(tmem, w_desc + off + 2 * k, x_desc + off + 2 * k, idesc_fp4<FMT>(128, BN, id), sw, sx,
+                          i > 0 || k > 0);
         }
         mma_commit(&ctl.empty[slot]);
       }
+      __syncwarp();
+    }
+    if (leader) {
       mma_commit(&ctl.done);
       // TMEM goes back only when every MMA has completed
       mma_commit(&ctl.drain);
@@ -192,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(const __grid_consta
       for (int j = BN * rank / split; j < j1; ++j) {
         const uint32_t at = smem_u32(ring) + (uint32_t)(j * 128 + threadIdx.x) * 4;
         float v = 0.f;
-        for (int k = 0; k < split; ++k) v += peer_float(at, k);
+        for (int k = 0; k < split; ++k) v += __uint_as_float(peer_word(at, k));
         if (n >= a.n) continue;
         if (a.x_row) v *= __ldg(a.x_row + t0 + j);
         store_one(a.y, (t0 + j) * a.y_stride + n, a.y_type, fmaf(v, scale, add));
@@ -208,8 +213,8 @@ template <int FMT, int BN>
 int launch(LinearArgs& a, const fp4_matrix& x, const fp4_matrix& w, int sms, cudaStream_t st) {
   using C = Cfg<FMT, BN>;
   static moe::SmemGrant grant;
-  if (const int rc = make_map(w.codes, w.rows, w.cols, 128, &a.w_map)) return rc;
-  if (const int rc = make_map(x.codes, x.rows, x.cols, BN, &a.x_map)) return rc;
+  if (const int rc = codes_map(w, 128, &a.w_map)) return rc;
+  if (const int rc = codes_map(x, BN, &a.x_map)) return rc;
   if (!moe::grant_smem(linear_kernel<FMT, BN>, smem_bytes<C>(C::SLOTS), grant)) return MOE_ERR_CUDA;
   const int n_tiles = (a.n + 127) / 128, t_tiles = (a.t + BN - 1) / BN, chunks = (a.cols + kChunk - 1) / kChunk;
   // the split that leaves the busiest SM the fewest chunks

@@ -7,9 +7,8 @@
 // on from tile to tile, and the 8 epilogue warps take the sums from TMEM into
 // registers at once, so that the next tile's products start while they write.
 //
-// Barriers: full (a CTA's own copies), peer_full (the second CTA tells the first that its
-// copies have landed), empty and sums_full (commits, to both CTAs), sums_empty (the
-// epilogue warps of both CTAs, at the first).
+// Barriers: full (the copies of both CTAs, at the first), empty and sums_full (commits, to
+// both CTAs), sums_empty (the epilogue warps of both CTAs, at the first).
 #include "fp4_mma.cuh"
 
 using namespace moe::tc;
@@ -37,10 +36,11 @@ struct Cfg {
 };
 
 struct Control {
-  uint64_t full[8], empty[8], peer_full[8];
+  uint64_t full[8], empty[8];
   uint64_t sums_full, sums_empty, drain;
   uint32_t tmem;
   int abort;
+  int loaded;  // chunks whose copies the CTA has issued, at its end
   float2 column[2][256];  // w's row scale and the bias, of a tile's columns
 };
 template <class C>
@@ -79,9 +79,17 @@ __device__ __forceinline__ void store8(void* y, const float* f) {
   }
 }
 
+struct WideArgs {
+  LinearArgs l;
+  CUtensorMap w_scales_map, x_scales_map;
+  int t_tiles, n_tiles;
+  int vector;  // y may be written 16 bytes at a time
+};
+
 template <int FMT, int BN>
-__global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant__ LinearArgs a, int t_tiles,
-                                                          int n_tiles, int vector) {
+__global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant__ WideArgs args) {
+  const LinearArgs& a = args.l;
+  const int t_tiles = args.t_tiles, n_tiles = args.n_tiles;
   using C = Cfg<FMT, BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -90,13 +98,12 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
   const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int all = t_tiles * n_tiles;
   const int chunks = (a.cols + kChunk - 1) / kChunk;
-  const int tiles = fp4::scale_tiles(a.cols, FMT);
+  const int tiles = scale_tiles(a.cols, FMT);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(&ctl.full[i], 1);
       mbar_init(&ctl.empty[i], 1);
-      mbar_init(&ctl.peer_full[i], 1);
     }
     mbar_init(&ctl.sums_full, 1 + a.extra);
     mbar_init(&ctl.sums_empty, 2 * kEpilogueWarps);
@@ -105,6 +112,8 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
     mbar_fence_init();
     attn::prefetch_map(&a.w_map);
     attn::prefetch_map(&a.x_map);
+    attn::prefetch_map(&args.w_scales_map);
+    attn::prefetch_map(&args.x_scales_map);
   }
   // (as in fp4_linear.cu: TMEM is taken between the kernel before and the one behind)
   moe::pdl_wait();
@@ -133,76 +142,73 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
           const int slot = i % C::SLOTS;
           alive = cluster_wait(&ctl.empty[slot], ((i / C::SLOTS) & 1) ^ 1, a.wait_cycles, abort_flag, a.st);
           if (!alive) break;
-          uint64_t* bar = &ctl.full[slot];
+          // Both CTAs' copies are counted at the first one's barrier.  A box of scales may
+          // reach into the next rows' tiles or past the last: nothing takes those.
+          if (rank == 0) mbar_arrive_expect_tx(&ctl.full[slot], 2 * C::SLOT);
+          const uint32_t bar = peer_address(smem_u32(&ctl.full[slot]), 0);
           const uint32_t x = smem_u32(ring + (size_t)slot * C::SLOT), w = x + C::X_BYTES, s = w + C::W_BYTES;
-          const int kt = c * C::COPIES, bytes = min(C::COPIES, tiles - kt) * 512;
-          const int sx = t0 < a.t, sw = min(C::W_TILES, (a.n - n0 + 127) / 128);  // tiles of scales that there are
-          mbar_arrive_expect_tx(bar, C::X_BYTES + C::W_BYTES + (sx + sw) * bytes);
-          load_codes(&a.x_map, x, bar, c * (kChunk / 2), t0);
-          load_codes(&a.w_map, w, bar, c * (kChunk / 2), n0 + BN / 2 * rank);
-          if (sx) bulk_g2s(s, a.x_scales + ((size_t)(t0 >> 7) * tiles + kt) * 512, bytes, bar);
-          for (int k = 0; k < sw; ++k)
-            bulk_g2s(s + (1 + k) * C::S_BYTES, a.w_scales + ((size_t)((n0 >> 7) + k) * tiles + kt) * 512, bytes, bar);
+          const int kt = c * C::COPIES;
+          load_pair(&a.x_map, x, bar, c * (kChunk / 2), t0);
+          load_pair(&a.w_map, w, bar, c * (kChunk / 2), n0 + BN / 2 * rank);
+          load_pair(&args.x_scales_map, s, bar, 0, (t0 >> 7) * tiles + kt);
+#pragma unroll
+          for (int k = 0; k < C::W_TILES; ++k)
+            load_pair(&args.w_scales_map, s + (1 + k) * C::S_BYTES, bar, 0, ((n0 >> 7) + k) * tiles + kt);
         }
       }
-      // every copy has landed before the CTA's shared memory goes away
-      for (int k = max(0, i - C::SLOTS); k < i; ++k)
-        attn::bounded_wait(&ctl.full[k % C::SLOTS], (k / C::SLOTS) & 1, attn::kDrainCycles, nullptr, a.st);
+      ctl.loaded = i;
     }
     __syncwarp();
   } else if (warp == kMmaWarp && rank == 1) {
-    if (lane == 0) {
-      bool alive = true;
-      int i = 0;
-      for (int at = pair; at < all && alive; at += pairs)
-        for (int c = 0; c < chunks && alive; ++c, ++i) {
-          const int slot = i % C::SLOTS;
-          alive = attn::bounded_wait(&ctl.full[slot], (i / C::SLOTS) & 1, a.wait_cycles, abort_flag, a.st);
-          if (alive) arrive_at(&ctl.peer_full[slot], 0);
-        }
-    }
-    __syncwarp();
+    // (the first CTA's issues for both)
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      bool alive = true;
-      int i = 0, done = 0;  // chunks, tiles so far
-      const uint64_t x_desc = sw128_kmajor_desc(smem_u32(ring)), w_desc = sw128_kmajor_desc(smem_u32(ring) + C::X_BYTES);
-      for (int at = pair; at < all && alive; at += pairs, ++done) {
-        if (done > 0)
-          alive = cluster_wait(&ctl.sums_empty, (done - 1) & 1, a.wait_cycles, abort_flag, a.st);
-        for (int c = 0; c < chunks && alive; ++c, ++i) {
-          const int slot = i % C::SLOTS;
-          alive = attn::bounded_wait(&ctl.full[slot], (i / C::SLOTS) & 1, a.wait_cycles, abort_flag, a.st) &&
-                  cluster_wait(&ctl.peer_full[slot], (i / C::SLOTS) & 1, a.wait_cycles, abort_flag, a.st);
-          // the products that took the scales whose place these get have been made
-          if (alive && C::SETS < C::SLOTS && i >= C::SETS)
-            alive = attn::bounded_wait(&ctl.empty[(i - C::SETS) % C::SLOTS], ((i - C::SETS) / C::SLOTS) & 1,
-                                       a.wait_cycles, abort_flag, a.st);
-          if (!alive) break;
-          fence_after_sync();
-          const uint32_t off = (uint32_t)slot * (C::SLOT >> 4);
-          const uint32_t scales = smem_u32(ring + (size_t)slot * C::SLOT) + C::X_BYTES + C::W_BYTES;
-          const uint32_t set = tmem + C::S_COL + (i % C::SETS) * (C::SX_COLS + C::SW_COLS);
-          const int steps = min(kChunk, a.cols - c * kChunk + 63) / 64;
+    // The warp walks and waits as one and its elected lane issues: with what it issues
+    // in a branch of one lane's own, each of these instructions took 67 cycles, 1075 a
+    // chunk, twice the time of its products.
+    const bool leader = attn::elect_lane();
+    bool alive = true;
+    int i = 0, done = 0;  // chunks, tiles so far
+    const uint64_t x_desc = sw128_kmajor_desc(smem_u32(ring)), w_desc = sw128_kmajor_desc(smem_u32(ring) + C::X_BYTES);
+    const uint64_t s_desc = scales_desc(smem_u32(ring) + C::X_BYTES + C::W_BYTES);
+    for (int at = pair; at < all && alive; at += pairs, ++done) {
+      if (done > 0)
+        alive = __all_sync(0xffffffffu, cluster_wait(&ctl.sums_empty, (done - 1) & 1, a.wait_cycles, abort_flag, a.st));
+      for (int c = 0; c < chunks && alive; ++c, ++i) {
+        const int slot = i % C::SLOTS;
+        bool ok = cluster_wait(&ctl.full[slot], (i / C::SLOTS) & 1, a.wait_cycles, abort_flag, a.st);
+        // the products that took the scales whose place these get have been made
+        if (ok && C::SETS < C::SLOTS && i >= C::SETS)
+          ok = attn::bounded_wait(&ctl.empty[(i - C::SETS) % C::SLOTS], ((i - C::SETS) / C::SLOTS) & 1, a.wait_cycles,
+                                  abort_flag, a.st);
+        alive = __all_sync(0xffffffffu, ok);
+        if (!alive) break;
+        fence_after_sync();
+        const uint32_t off = (uint32_t)slot * (C::SLOT >> 4);
+        const uint32_t set = tmem + C::S_COL + (i % C::SETS) * (C::SX_COLS + C::SW_COLS);
+        const int steps = min(kChunk, a.cols - c * kChunk + 63) / 64;
+        if (leader) {
 #pragma unroll
           for (int k = 0; k < kChunk / 64; ++k) {
             if (k >= steps) break;
             const int copy = C::NV ? k : k / 2, id = C::NV ? 0 : 2 * (k & 1);
             const uint32_t sx = set + 4 * copy, sw = set + C::SX_COLS + 4 * C::W_TILES * copy;
             if (id == 0) {
-              copy_scales<2>(sx, scales_desc(scales + copy * 512));
+              copy_scales<2>(sx, s_desc + off + copy * 32);
 #pragma unroll
               for (int q = 0; q < C::W_TILES; ++q)
-                copy_scales<2>(sw + 4 * q, scales_desc(scales + (1 + q) * C::S_BYTES + copy * 512));
+                copy_scales<2>(sw + 4 * q, s_desc + off + ((1 + q) * C::S_BYTES >> 4) + copy * 32);
             }
             mma_fp4<FMT, 2>(tmem, x_desc + off + 2 * k, w_desc + off + 2 * k, idesc_fp4<FMT>(256, BN, id), sx, sw,
                             c > 0 || k > 0);
           }
           commit_both(&ctl.empty[slot]);
+          if (c == chunks - 1) commit_both(&ctl.sums_full);
         }
-        if (alive) commit_both(&ctl.sums_full);
+        __syncwarp();
       }
-      // TMEM and the ring go back only when every MMA has completed
+    }
+    // TMEM and the ring go back only when every MMA has completed
+    if (leader) {
       asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&ctl.drain))
                    : "memory");
       attn::bounded_wait(&ctl.drain, 0, attn::kDrainCycles, nullptr, a.st);
@@ -244,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
           v[i] = alive ? fmaf(v[i] * row, c.x, c.y) : kNaN;
         }
         uint8_t* y = static_cast<uint8_t*>(a.y) + (t * a.y_stride + n0) * item;
-        if (vector && left >= HALF) {
+        if (args.vector && left >= HALF) {
           if (a.y_type == FP4_BF16) {
 #pragma unroll
             for (int i = 0; i < HALF; i += 8) store8<FP4_BF16>(y + 2 * i, v + i);
@@ -265,6 +271,20 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
     }
   }
   __syncthreads();
+  cluster_sync();  // every MMA has completed; the copies have, unless a wait has run out
+  if (rank == 0 && threadIdx.x == 0) {
+    // Then one CTA may have stopped a few copies before the other: what the barriers still
+    // expect of it is struck off, what they do not expect is added.
+    const int mine = ctl.loaded, other = (int)peer_word(smem_u32(&ctl.loaded), 1);
+    for (int k = max(0, max(mine, other) - C::SLOTS); k < max(mine, other); ++k) {
+      uint64_t* bar = &ctl.full[k % C::SLOTS];
+      if (k >= other)
+        asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(C::SLOT)
+                     : "memory");
+      if (k >= mine) mbar_arrive_expect_tx(bar, C::SLOT);
+      attn::bounded_wait(bar, (k / C::SLOTS) & 1, attn::kDrainCycles, nullptr, a.st);
+    }
+  }
   cluster_sync();  // no CTA's shared memory or TMEM is in use by the other any more
   if (warp == kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM) : "memory");
@@ -274,14 +294,16 @@ template <int FMT, int BN>
 int launch(LinearArgs& a, const fp4_matrix& x, const fp4_matrix& w, int sms, cudaStream_t st) {
   using C = Cfg<FMT, BN>;
   static moe::SmemGrant grant;
-  if (const int rc = make_map(x.codes, x.rows, x.cols, 128, &a.x_map)) return rc;
-  if (const int rc = make_map(w.codes, w.rows, w.cols, BN / 2, &a.w_map)) return rc;
-  if (!moe::grant_smem(wide_kernel<FMT, BN>, smem_bytes<C>(), grant)) return MOE_ERR_CUDA;
   const long long t_tiles = (a.t + 255) / 256, n_tiles = (a.n + BN - 1) / BN;
   if (t_tiles * n_tiles > 0x3FFFFFFF || 8 * n_tiles > 0x3FFFFFFF) return MOE_ERR_UNSUPPORTED;
+  WideArgs args = {a, {}, {}, (int)t_tiles, (int)n_tiles, 0};
+  args.vector = moe::aligned16(a.y) && a.y_stride * element_bytes(a.y_type) % 16 == 0;
+  if (const int rc = codes_map(x, 128, &args.l.x_map)) return rc;
+  if (const int rc = codes_map(w, BN / 2, &args.l.w_map)) return rc;
+  if (const int rc = scales_map(x, &args.x_scales_map)) return rc;
+  if (const int rc = scales_map(w, &args.w_scales_map)) return rc;
+  if (!moe::grant_smem(wide_kernel<FMT, BN>, smem_bytes<C>(), grant)) return MOE_ERR_CUDA;
   const int pairs = (int)(t_tiles * n_tiles < sms / 2 ? t_tiles * n_tiles : sms / 2);
-  const int item = fp4::element_bytes(a.y_type);
-  const int vector = moe::aligned16(a.y) && a.y_stride * item % 16 == 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs);
   cfg.blockDim = dim3(kThreads);
@@ -294,9 +316,7 @@ int launch(LinearArgs& a, const fp4_matrix& x, const fp4_matrix& w, int sms, cud
   attr[1].val.clusterDim.x = 2, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, wide_kernel<FMT, BN>, a, (int)t_tiles, (int)n_tiles, vector) == cudaSuccess
-             ? MOE_OK
-             : MOE_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, wide_kernel<FMT, BN>, args) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace

@@ -80,6 +80,16 @@ __device__ __forceinline__ void load_codes(const CUtensorMap* m, uint32_t dst, u
       : "memory");
 }
 
+// The same for a CTA of a pair, whose copies are counted at the first CTA's barrier
+// (`bar`: its address in the cluster).
+__device__ __forceinline__ void load_pair(const CUtensorMap* m, uint32_t dst, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(dst),
+      "l"(m), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -88,20 +98,23 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// A float of another CTA's shared memory, at the address that it has in this one's.
-__device__ __forceinline__ float peer_float(uint32_t saddr, int rank) {
+// What CTA `rank` of the cluster has at an address of this one's shared memory.
+__device__ __forceinline__ uint32_t peer_address(uint32_t saddr, int rank) {
   uint32_t at;
-  float v;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(saddr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return at;
+}
+__device__ __forceinline__ uint32_t peer_word(uint32_t saddr, int rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(peer_address(saddr, rank)) : "memory");
   return v;
 }
 
-// Arrives at the barrier that CTA `rank` of the cluster has at this one's address.
+// Arrives at CTA `rank`'s barrier.  (Its release takes some 1500 cycles.)
 __device__ __forceinline__ void arrive_at(uint64_t* bar, int rank) {
-  uint32_t at;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(moe::tc::smem_u32(bar)), "r"(rank));
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(at) : "memory");
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                   peer_address(moe::tc::smem_u32(bar), rank))
+               : "memory");
 }
 // attn::bounded_wait for a barrier at which other CTAs of the cluster arrive.
 __device__ __forceinline__ bool cluster_wait(uint64_t* bar, uint32_t parity, long long limit, volatile int* abort,
@@ -137,15 +150,26 @@ __device__ __forceinline__ void store_one(void* y, long long at, int type, float
   else static_cast<__half*>(y)[at] = __float2half(v);
 }
 
-inline int make_map(const void* codes, int rows, int cols, int box, CUtensorMap* m) {
+inline int make_map(CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* base, cuuint64_t width,
+                    cuuint64_t bytes, cuuint64_t rows, int box_width, int box_rows, CUtensorMap* m) {
   const attn::MapEncoder encode = attn::map_encoder();
   if (!encode) return MOE_ERR_CUDA;
-  const cuuint64_t dims[2] = {(cuuint64_t)cols / 2, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)cols / 2};
-  const cuuint32_t boxes[2] = {128, (cuuint32_t)box}, one[2] = {1, 1};
-  const CUresult rc = encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, boxes, one,
-                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const cuuint64_t dims[2] = {width, rows}, strides[1] = {bytes};
+  const cuuint32_t boxes[2] = {(cuuint32_t)box_width, (cuuint32_t)box_rows}, one[2] = {1, 1};
+  const CUresult rc = encode(m, type, 2, const_cast<void*>(base), dims, strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return rc == CUDA_SUCCESS ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+// `box` rows of a chunk's codes.
+inline int codes_map(const fp4_matrix& m, int box, CUtensorMap* map) {
+  return make_map(CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, m.codes, m.cols / 2, m.cols / 2, m.rows,
+                  kChunk / 2, box, map);
+}
+// A chunk's scales of 128 rows: consecutive tiles of 512 bytes.
+inline int scales_map(const fp4_matrix& m, CUtensorMap* map) {
+  const long long tiles = (long long)((m.rows + 127) / 128) * scale_tiles(m.cols, m.format);
+  return make_map(CU_TENSOR_MAP_DATA_TYPE_UINT32, CU_TENSOR_MAP_SWIZZLE_NONE, m.scales, 128, 512, tiles, 128,
+                  m.format == MOE_FMT_NVFP4 ? 4 : 2, map);
 }
 
 // fp4_linear with many rows of x (fp4_linear_wide.cu).
