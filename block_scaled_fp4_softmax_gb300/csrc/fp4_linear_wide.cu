@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
       for (int i = 0; i < HALF; i += 32) attn::tmem_ld_wait32(v + i);
       fence_before_sync();
       __syncwarp();
-      if (lane == 0 && alive) arrive_at(&ctl.sums_empty, 0);
+      if (lane == 0 && alive) arrive_relaxed_at(&ctl.sums_empty, 0);
       if (t < a.t) {
         const int n0 = tile.n0 + half * HALF, left = a.n - n0;
 #pragma unroll

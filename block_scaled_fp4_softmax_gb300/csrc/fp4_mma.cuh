@@ -110,9 +110,10 @@ __device__ __forceinline__ uint32_t peer_word(uint32_t saddr, int rank) {
   return v;
 }
 
-// Arrives at CTA `rank`'s barrier.  (Its release takes some 1500 cycles.)
-__device__ __forceinline__ void arrive_at(uint64_t* bar, int rank) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+// Arrives at CTA `rank`'s barrier, when nothing in memory has to be seen behind it
+// (TMEM that has been read): a release of what the thread wrote before takes some 1500 cycles.
+__device__ __forceinline__ void arrive_relaxed_at(uint64_t* bar, int rank) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
                    peer_address(moe::tc::smem_u32(bar), rank))
                : "memory");
 }
