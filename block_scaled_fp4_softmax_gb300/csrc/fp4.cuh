@@ -45,7 +45,7 @@ inline int check_target(const fp4_matrix* m, int rows, int cols) {
   return MOE_OK;
 }
 
-inline int element_bytes(int type) { return type == FP4_FP32 ? 4 : 2; }
+__host__ __device__ __forceinline__ int element_bytes(int type) { return type == FP4_FP32 ? 4 : 2; }
 
 // Rows that are read or written 16 bytes at a time.  `wide`: 32-bit rows are allowed.
 inline int check_rows(const fp4_rows* x, int rows, int cols, bool wide) {

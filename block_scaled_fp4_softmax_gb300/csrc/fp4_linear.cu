@@ -32,10 +32,11 @@ struct Cfg {
   // two CTAs to an SM: one's loads run while the other starts or ends
   static constexpr int SLOTS = (113 * 1024 - 3072) / SLOT;
   static constexpr int S_COLS = COPIES * 4;                    // TMEM columns of a chunk's scales, of either side
-  static constexpr int SETS = 4;                               // chunks whose scales TMEM holds
+  // TMEM holds the scales of as many chunks as the ring: where a slot's copies have
+  // landed, the products that took the scales before it have been made.
   static constexpr int S_COL = BN <= 32 ? 32 : BN;             // first of them, behind the sums
-  static constexpr int TMEM = S_COL + SETS * 2 * S_COLS <= 128 ? 128 : 256;
-  static_assert(S_COL + SETS * 2 * S_COLS <= TMEM, "TMEM");
+  static constexpr int TMEM = S_COL + SLOTS * 2 * S_COLS <= 128 ? 128 : 256;
+  static_assert(S_COL + SLOTS * 2 * S_COLS <= TMEM, "TMEM");
   static_assert(SLOTS >= 3 && SLOTS * SLOT >= BN * 128 * 4, "ring");
 };
 
@@ -119,16 +120,11 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(const __grid_consta
     const uint64_t s_desc = scales_desc(smem_u32(ring) + C::W_BYTES + C::X_BYTES);
     for (int c = c0, i = 0; c < c1; ++c, ++i) {
       const int slot = i % slots;
-      bool ok = attn::bounded_wait(&ctl.full[slot], (i / slots) & 1, a.wait_cycles, abort_flag, a.st);
-      // The products that took the scales whose place these get have been made (with
-      // as many slots or fewer, the copy that has landed waited for them already).
-      if (ok && C::SETS < slots && i >= C::SETS)
-        ok = attn::bounded_wait(&ctl.empty[(i - C::SETS) % slots], ((i - C::SETS) / slots) & 1, a.wait_cycles,
-                                abort_flag, a.st);
+      const bool ok = attn::bounded_wait(&ctl.full[slot], (i / slots) & 1, a.wait_cycles, abort_flag, a.st);
       if (!__all_sync(0xffffffffu, ok)) break;
       fence_after_sync();
       const uint32_t off = (uint32_t)slot * (C::SLOT >> 4);
-      const uint32_t set = tmem + C::S_COL + (i % C::SETS) * 2 * C::S_COLS;
+      const uint32_t set = tmem + C::S_COL + slot * 2 * C::S_COLS;
       const int steps = min(kChunk, a.cols - c * kChunk + 63) / 64;
       if (leader) {
 #pragma unroll

@@ -26,13 +26,18 @@ struct Cfg {
   static constexpr int W_TILES = (BN + 127) / 128;              // 128 rows of w's scales; both CTAs take all
   static constexpr int X_BYTES = 128 * 128, W_BYTES = BN / 2 * 128, S_BYTES = COPIES * 512;
   static constexpr int SLOT = X_BYTES + W_BYTES + (1 + W_TILES) * S_BYTES;
-  static constexpr int SLOTS = (227 * 1024 - 8192) / SLOT < 8 ? (227 * 1024 - 8192) / SLOT : 8;
+  static constexpr int STAGE = kEpilogueWarps * 32 * 128;       // 128 bytes of 32 rows for each epilogue warp
+  static constexpr int ROOM = (227 * 1024 - 1024 - STAGE - 2560) / SLOT;
+  static constexpr int SLOTS = ROOM < 8 ? ROOM : 8;
   static constexpr int SX_COLS = COPIES * 4, SW_COLS = SX_COLS * W_TILES;
-  static constexpr int SETS = 4;                                // chunks whose scales TMEM holds
+  // TMEM holds the scales of as many chunks as the ring: where a slot's copies have
+  // landed, the products that took the scales before it have been made.
   static constexpr int S_COL = BN;
   static constexpr int TMEM = 512;
-  static_assert(S_COL + SETS * (SX_COLS + SW_COLS) <= TMEM, "TMEM");
+  static constexpr int FIRST = BN > 128 ? 128 : 64;             // columns of an epilogue warp: the first four's
+  static_assert(S_COL + SLOTS * (SX_COLS + SW_COLS) <= TMEM, "TMEM");
   static_assert(SLOT % 1024 == 0, "the swizzle's alignment");
+  static_assert(BN % 64 == 0 && BN - FIRST <= FIRST, "tiles of scales may start in the middle of 128 rows");
 };
 
 struct Control {
@@ -41,12 +46,13 @@ struct Control {
   uint32_t tmem;
   int abort;
   int loaded;  // chunks whose copies the CTA has issued, at its end
-  float2 column[2][256];  // w's row scale and the bias, of a tile's columns
+  float2 column[256];  // w's row scale and the bias, of a tile's columns
 };
 template <class C>
 constexpr size_t smem_bytes() {
-  return 1024 + (size_t)C::SLOTS * C::SLOT + sizeof(Control);
+  return 1024 + (size_t)C::SLOTS * C::SLOT + C::STAGE + sizeof(Control);
 }
+static_assert(sizeof(Control) <= 2560, "Cfg::ROOM");
 
 // Which tile of the grid of tiles comes i-th: blocks of 8 tiles of rows, so that the
 // tiles that run at a time share both operands in L2.
@@ -68,15 +74,32 @@ __device__ __forceinline__ void commit_both(uint64_t* bar) {
       : "memory");
 }
 
-template <int TYPE>
-__device__ __forceinline__ void store8(void* y, const float* f) {
-  if constexpr (TYPE == FP4_FP32) {
-    reinterpret_cast<float4*>(y)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(y)[1] = make_float4(f[4], f[5], f[6], f[7]);
-  } else {
-    const float(&v)[8] = *reinterpret_cast<const float(*)[8]>(f);
-    *reinterpret_cast<uint4*>(y) = TYPE == FP4_BF16 ? attn::pack8<attn::Brain>(v) : attn::pack8<attn::Half>(v);
+// `stage`: 128 bytes of each of 32 rows, in pieces of 16 bytes that are swizzled.
+__device__ __forceinline__ uint4* staged(uint8_t* stage, int row, int piece) {
+  return reinterpret_cast<uint4*>(stage + row * 128 + ((piece ^ (row & 7)) << 4));
+}
+
+// Writes what the warp has staged, the first `rows` rows and `left` columns of it, so that its
+// stores are whole lines: with rows written by their own threads the epilogue held up the
+// next tile's copies for some 4000 cycles.
+__device__ __forceinline__ void write_staged(uint8_t* stage, int lane, bool vector, uint8_t* to, long long step, int item,
+                                             int rows, int left) {
+  __syncwarp();
+  if (vector && left * item >= 128) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int r = 4 * k + (lane >> 3), c = lane & 7;
+      if (r < rows) *reinterpret_cast<uint4*>(to + r * step + 16 * c) = *staged(stage, r, c);
+    }
+  } else {  // the edge of y, or rows that do not lie on 16 bytes
+    for (int r = 0; r < rows; ++r, to += step)
+      for (int c = lane; c < min(left, 128 / item); c += 32) {
+        const uint8_t* from = reinterpret_cast<const uint8_t*>(staged(stage, r, (c * item) >> 4)) + ((c * item) & 15);
+        if (item == 4) *reinterpret_cast<uint32_t*>(to + 4 * c) = *reinterpret_cast<const uint32_t*>(from);
+        else *reinterpret_cast<uint16_t*>(to + 2 * c) = *reinterpret_cast<const uint16_t*>(from);
+      }
   }
+  __syncwarp();
 }
 
 struct WideArgs {
@@ -93,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
   using C = Cfg<FMT, BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  Control& ctl = *reinterpret_cast<Control*>(ring + (size_t)C::SLOTS * C::SLOT);
+  Control& ctl = *reinterpret_cast<Control*>(ring + (size_t)C::SLOTS * C::SLOT + C::STAGE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int all = t_tiles * n_tiles;
@@ -167,29 +190,23 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
     // chunk, twice the time of its products.
     const bool leader = attn::elect_lane();
     bool alive = true;
-    int i = 0, done = 0;  // chunks, tiles so far
+    int slot = 0, done = 0;  // of the ring; tiles so far
+    uint32_t round = 0;      // parity of the ring's rounds
     const uint64_t x_desc = sw128_kmajor_desc(smem_u32(ring)), w_desc = sw128_kmajor_desc(smem_u32(ring) + C::X_BYTES);
     const uint64_t s_desc = scales_desc(smem_u32(ring) + C::X_BYTES + C::W_BYTES);
     for (int at = pair; at < all && alive; at += pairs, ++done) {
       if (done > 0)
         alive = __all_sync(0xffffffffu, cluster_wait(&ctl.sums_empty, (done - 1) & 1, a.wait_cycles, abort_flag, a.st));
-      for (int c = 0; c < chunks && alive; ++c, ++i) {
-        const int slot = i % C::SLOTS;
-        bool ok = cluster_wait(&ctl.full[slot], (i / C::SLOTS) & 1, a.wait_cycles, abort_flag, a.st);
-        // the products that took the scales whose place these get have been made
-        if (ok && C::SETS < C::SLOTS && i >= C::SETS)
-          ok = attn::bounded_wait(&ctl.empty[(i - C::SETS) % C::SLOTS], ((i - C::SETS) / C::SLOTS) & 1, a.wait_cycles,
-                                  abort_flag, a.st);
-        alive = __all_sync(0xffffffffu, ok);
+      // a tile that starts in the middle of 128 rows of w takes their scales from there
+      const uint32_t skip = Tile(at, t_tiles, n_tiles, BN).n0 % 128 / 32;
+      for (int c = 0; c < chunks && alive; ++c) {
+        alive = __all_sync(0xffffffffu, cluster_wait(&ctl.full[slot], round, a.wait_cycles, abort_flag, a.st));
         if (!alive) break;
         fence_after_sync();
-        const uint32_t off = (uint32_t)slot * (C::SLOT >> 4);
-        const uint32_t set = tmem + C::S_COL + (i % C::SETS) * (C::SX_COLS + C::SW_COLS);
-        const int steps = min(kChunk, a.cols - c * kChunk + 63) / 64;
         if (leader) {
-#pragma unroll
-          for (int k = 0; k < kChunk / 64; ++k) {
-            if (k >= steps) break;
+          const uint32_t off = (uint32_t)slot * (C::SLOT >> 4);
+          const uint32_t set = tmem + C::S_COL + slot * (C::SX_COLS + C::SW_COLS);
+          auto step = [&](int k) {
             const int copy = C::NV ? k : k / 2, id = C::NV ? 0 : 2 * (k & 1);
             const uint32_t sx = set + 4 * copy, sw = set + C::SX_COLS + 4 * C::W_TILES * copy;
             if (id == 0) {
@@ -198,13 +215,24 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
               for (int q = 0; q < C::W_TILES; ++q)
                 copy_scales<2>(sw + 4 * q, s_desc + off + ((1 + q) * C::S_BYTES >> 4) + copy * 32);
             }
-            mma_fp4<FMT, 2>(tmem, x_desc + off + 2 * k, w_desc + off + 2 * k, idesc_fp4<FMT>(256, BN, id), sx, sw,
+            mma_fp4<FMT, 2>(tmem, x_desc + off + 2 * k, w_desc + off + 2 * k, idesc_fp4<FMT>(256, BN, id), sx, sw + skip,
                             c > 0 || k > 0);
+          };
+          if (a.cols - c * kChunk >= kChunk) {
+#pragma unroll
+            for (int k = 0; k < kChunk / 64; ++k) step(k);
+          } else {
+            const int steps = (a.cols - c * kChunk + 63) / 64;
+#pragma unroll
+            for (int k = 0; k < kChunk / 64 - 1; ++k)
+              if (k < steps) step(k);
+            if (steps == kChunk / 64) step(kChunk / 64 - 1);
           }
           commit_both(&ctl.empty[slot]);
           if (c == chunks - 1) commit_both(&ctl.sums_full);
         }
         __syncwarp();
+        if (++slot == C::SLOTS) slot = 0, round ^= 1;
       }
     }
     // TMEM and the ring go back only when every MMA has completed
@@ -215,59 +243,84 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
     }
     __syncwarp();
   } else {
-    constexpr int HALF = BN / 2;
-    const int half = warp >> 2;  // of the tile's columns
-    const uint32_t sums = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * HALF;
-    const int item = a.y_type == FP4_FP32 ? 4 : 2;
+    // The first four warps take the tile's first columns, the other four the rest.
+    const int half = warp >> 2, mine = half ? BN - C::FIRST : C::FIRST;
+    const uint32_t sums = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * C::FIRST;
+    uint8_t* stage = ring + (size_t)C::SLOTS * C::SLOT + warp * (32 * 128);
+    const int item = element_bytes(a.y_type);
     bool alive = true;
     int done = 0;
     for (int at = pair; at < all; at += pairs, ++done) {
       const Tile tile(at, t_tiles, n_tiles, BN);
-      const int t = tile.t0 + 128 * rank + (warp & 3) * 32 + lane;
-      float2* column = ctl.column[done & 1];
+      const int t0 = tile.t0 + 128 * rank + (warp & 3) * 32, n0 = tile.n0 + half * C::FIRST;
+      named_sync(1, 32 * kEpilogueWarps);  // the tile before has been written
       if (threadIdx.x < BN) {
         const int n = tile.n0 + threadIdx.x;
-        column[threadIdx.x] = make_float2(a.w_row && n < a.n ? __ldg(a.w_row + n) : 1.f,
-                                          a.bias && n < a.n ? __ldg(a.bias + n) : 0.f);
+        ctl.column[threadIdx.x] = make_float2(a.w_row && n < a.n ? __ldg(a.w_row + n) : 1.f,
+                                              a.bias && n < a.n ? __ldg(a.bias + n) : 0.f);
       }
-      const float row = a.x_row && t < a.t ? __ldg(a.x_row + t) : 1.f;
+      const float row = a.x_row && t0 + lane < a.t ? __ldg(a.x_row + t0 + lane) : 1.f;
       named_sync(1, 32 * kEpilogueWarps);
       alive = alive && __all_sync(0xffffffffu, cluster_wait(&ctl.sums_full, done & 1, a.wait_cycles, abort_flag, a.st));
       fence_after_sync();
-      float v[HALF];
+      const float factor = alive ? row : kNaN;
+      const float2* column = ctl.column + half * C::FIRST;
+      uint8_t* y = static_cast<uint8_t*>(a.y) + (t0 * a.y_stride + n0) * item;
+      const long long step = a.y_stride * item;
+      const int rows = min(32, a.t - t0), left = a.n - n0;
+      auto read = [&](int i, float(&v)[64]) {  // 64 columns from i on
+        attn::tmem_ld32(sums + i, v);
+        attn::tmem_ld32(sums + i + 32, v + 32);
+        attn::tmem_ld_wait32(v);
+        attn::tmem_ld_wait32(v + 32);
 #pragma unroll
-      for (int i = 0; i < HALF; i += 32) attn::tmem_ld32(sums + i, v + i);
-#pragma unroll
-      for (int i = 0; i < HALF; i += 32) attn::tmem_ld_wait32(v + i);
-      fence_before_sync();
-      __syncwarp();
-      if (lane == 0 && alive) arrive_relaxed_at(&ctl.sums_empty, 0);
-      if (t < a.t) {
-        const int n0 = tile.n0 + half * HALF, left = a.n - n0;
-#pragma unroll
-        for (int i = 0; i < HALF; ++i) {
-          const float2 c = column[half * HALF + i];
-          v[i] = alive ? fmaf(v[i] * row, c.x, c.y) : kNaN;
+        for (int k = 0; k < 64; ++k) {
+          const float2 c = column[i + k];
+          v[k] = fmaf(v[k] * factor, c.x, c.y);
         }
-        uint8_t* y = static_cast<uint8_t*>(a.y) + (t * a.y_stride + n0) * item;
-        if (args.vector && left >= HALF) {
-          if (a.y_type == FP4_BF16) {
+      };
+      auto release = [&]() {  // the next tile's products may have the sums' place
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0 && alive) arrive_relaxed_at(&ctl.sums_empty, 0);
+      };
+      if (a.y_type != FP4_FP32) {
+        uint4 q[C::FIRST / 8];
 #pragma unroll
-            for (int i = 0; i < HALF; i += 8) store8<FP4_BF16>(y + 2 * i, v + i);
-          } else if (a.y_type == FP4_FP16) {
+        for (int i = 0; i < C::FIRST; i += 64) {
+          if (i >= mine) break;
+          float v[64];
+          read(i, v);
 #pragma unroll
-            for (int i = 0; i < HALF; i += 8) store8<FP4_FP16>(y + 2 * i, v + i);
-          } else {
-#pragma unroll
-            for (int i = 0; i < HALF; i += 8) store8<FP4_FP32>(y + 4 * i, v + i);
+          for (int k = 0; k < 8; ++k) {
+            const float(&f)[8] = *reinterpret_cast<const float(*)[8]>(v + 8 * k);
+            q[i / 8 + k] = a.y_type == FP4_BF16 ? attn::pack8<attn::Brain>(f) : attn::pack8<attn::Half>(f);
           }
-        } else {
+        }
+        release();
 #pragma unroll
-          for (int i = 0; i < HALF; ++i)
-            if (i < left) store_one(y, i, a.y_type, v[i]);
+        for (int i = 0; i < C::FIRST; i += 64) {
+          if (i >= mine || i >= left || rows <= 0) break;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) *staged(stage, lane, k) = q[i / 8 + k];
+          write_staged(stage, lane, args.vector, y + 2 * i, step, 2, rows, left - i);
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < mine; i += 64) {
+          float v[64];
+          read(i, v);
+          if (i + 64 >= mine) release();
+#pragma unroll
+          for (int p = 0; p < 64; p += 32) {
+            if (i + p >= left || rows <= 0) break;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *staged(stage, lane, k) = *reinterpret_cast<const uint4*>(v + p + 4 * k);
+            write_staged(stage, lane, args.vector, y + 4 * (i + p), step, 4, rows, left - i - p);
+          }
         }
       }
-      __syncwarp();
     }
   }
   __syncthreads();
@@ -319,13 +372,29 @@ int launch(LinearArgs& a, const fp4_matrix& x, const fp4_matrix& w, int sms, cud
   return cudaLaunchKernelEx(&cfg, wide_kernel<FMT, BN>, args) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// The width of a tile that gives the least time: rounds of tiles over the pairs, each of
+// its chunks (2 cycles a column of y, or the 400 that issuing takes) and some 2500 cycles
+// between tiles.
+template <int FMT>
+int by_width(LinearArgs& a, const fp4_matrix& x, const fp4_matrix& w, int sms, cudaStream_t st) {
+  const int widths[3] = {256, 192, 128};
+  long long best = 1ll << 62;
+  int width = 0;
+  for (int b : widths) {
+    const long long tiles = (long long)((a.t + 255) / 256) * ((a.n + b - 1) / b), rounds = (tiles + sms / 2 - 1) / (sms / 2);
+    const long long cost = rounds * ((a.cols + kChunk - 1) / kChunk * (2 * b > 400 ? 2 * b : 400) + 2500);
+    if (cost < best) best = cost, width = b;
+  }
+  return width == 256 ? launch<FMT, 256>(a, x, w, sms, st) : width == 192 ? launch<FMT, 192>(a, x, w, sms, st)
+                                                                           : launch<FMT, 128>(a, x, w, sms, st);
+}
+
 }  // namespace
 
 namespace fp4 {
 
 int launch_wide(LinearArgs& a, const fp4_matrix& x, const fp4_matrix& w, int sms, cudaStream_t st) {
-  return w.format == MOE_FMT_NVFP4 ? launch<MOE_FMT_NVFP4, 256>(a, x, w, sms, st)
-                                   : launch<MOE_FMT_MXFP4, 256>(a, x, w, sms, st);
+  return w.format == MOE_FMT_NVFP4 ? by_width<MOE_FMT_NVFP4>(a, x, w, sms, st) : by_width<MOE_FMT_MXFP4>(a, x, w, sms, st);
 }
 
 }  // namespace fp4

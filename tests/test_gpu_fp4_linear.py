@@ -224,3 +224,12 @@ def test_shared_expert_between_two_sums(T, H, I, format):
     want_r, want_h = O.block_norm(full, f64(down), None, None, 1.0, None, 1e-6)
     assert (np.abs(f64(r2) - want_r) <= rounded(want_r, F32, np.abs(full) * 2.0 ** -22 + np.abs(want_r) * 2.0 ** -22)).all()
     assert (np.abs(f64(h2) - want_h) <= rounded(want_h, BF, (np.abs(want_h) + 1) * 40 * 2.0 ** -24)).all()
+
+
+@pytest.mark.parametrize("format", [NV, MX])
+@pytest.mark.parametrize("T,N,K", [(300, 192, 256), (257, 577, 1056), (2451, 5760, 320), (2451, 4096, 288), (260, 19000, 96),
+                                   (5000, 1000, 64)])
+def test_tiles_of_every_width(T, N, K, format):
+    """Rounds of tiles that come out best at 256, 192 and 128 columns."""
+    check(T, N, K, format, BF, bias=True)
+    check(T, N, K, format, F32)
