@@ -16,7 +16,7 @@ using namespace fp4;
 
 namespace {
 
-constexpr int kEpilogueWarps = 8, kTmaWarp = 8, kMmaWarp = 9, kThreads = 320;
+constexpr int kEpilogueWarps = 16, kTmaWarp = 16, kMmaWarp = 17, kThreads = 576;
 
 template <int FMT, int BN_>
 struct Cfg {
@@ -26,7 +26,7 @@ struct Cfg {
   static constexpr int W_TILES = (BN + 127) / 128;              // 128 rows of w's scales; both CTAs take all
   static constexpr int X_BYTES = 128 * 128, W_BYTES = BN / 2 * 128, S_BYTES = COPIES * 512;
   static constexpr int SLOT = X_BYTES + W_BYTES + (1 + W_TILES) * S_BYTES;
-  static constexpr int STAGE = kEpilogueWarps * 32 * 128;       // 128 bytes of 32 rows for each epilogue warp
+  static constexpr int STAGE = kEpilogueWarps * 32 * 64;        // 64 bytes of 32 rows for each epilogue warp
   static constexpr int ROOM = (227 * 1024 - 1024 - STAGE - 2560) / SLOT;
   static constexpr int SLOTS = ROOM < 8 ? ROOM : 8;
   static constexpr int SX_COLS = COPIES * 4, SW_COLS = SX_COLS * W_TILES;
@@ -34,10 +34,10 @@ struct Cfg {
   // landed, the products that took the scales before it have been made.
   static constexpr int S_COL = BN;
   static constexpr int TMEM = 512;
-  static constexpr int FIRST = BN > 128 ? 128 : 64;             // columns of an epilogue warp: the first four's
+  static constexpr int SHARE = 64;                              // columns of an epilogue warp
   static_assert(S_COL + SLOTS * (SX_COLS + SW_COLS) <= TMEM, "TMEM");
   static_assert(SLOT % 1024 == 0, "the swizzle's alignment");
-  static_assert(BN % 64 == 0 && BN - FIRST <= FIRST, "tiles of scales may start in the middle of 128 rows");
+  static_assert(BN % 64 == 0, "tiles of scales may start in the middle of 128 rows");
 };
 
 struct Control {
@@ -74,30 +74,31 @@ __device__ __forceinline__ void commit_both(uint64_t* bar) {
       : "memory");
 }
 
-// `stage`: 128 bytes of each of 32 rows, in pieces of 16 bytes that are swizzled.
+// `stage`: 64 bytes of each of 32 rows, in pieces of 16 bytes that are swizzled.
 __device__ __forceinline__ uint4* staged(uint8_t* stage, int row, int piece) {
-  return reinterpret_cast<uint4*>(stage + row * 128 + ((piece ^ (row & 7)) << 4));
+  return reinterpret_cast<uint4*>(stage + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
 }
 
 // Writes what the warp has staged, the first `rows` rows and `left` columns of it, so that its
-// stores are whole lines: with rows written by their own threads the epilogue held up the
-// next tile's copies for some 4000 cycles.
+// stores are whole sectors, four lanes to a row: with rows written by their own threads the
+// epilogue held up the next tile's copies for some 4000 cycles.
 __device__ __forceinline__ void write_staged(uint8_t* stage, int lane, bool vector, uint8_t* to, long long step, int item,
                                              int rows, int left) {
   __syncwarp();
-  if (vector && left * item >= 128) {
+  if (vector && left * item >= 64) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int r = 4 * k + (lane >> 3), c = lane & 7;
+    for (int k = 0; k < 4; ++k) {
+      const int r = 8 * k + (lane >> 2), c = lane & 3;
       if (r < rows) *reinterpret_cast<uint4*>(to + r * step + 16 * c) = *staged(stage, r, c);
     }
-  } else {  // the edge of y, or rows that do not lie on 16 bytes
-    for (int r = 0; r < rows; ++r, to += step)
-      for (int c = lane; c < min(left, 128 / item); c += 32) {
-        const uint8_t* from = reinterpret_cast<const uint8_t*>(staged(stage, r, (c * item) >> 4)) + ((c * item) & 15);
-        if (item == 4) *reinterpret_cast<uint32_t*>(to + 4 * c) = *reinterpret_cast<const uint32_t*>(from);
-        else *reinterpret_cast<uint16_t*>(to + 2 * c) = *reinterpret_cast<const uint16_t*>(from);
-      }
+  } else {  // the edge of y, or rows that do not lie on 16 bytes: 32 or 16 elements a row
+    const int per = 64 / item, first = lane / per, c = lane % per;
+    for (int r = first; r < rows; r += 32 / per) {
+      const uint8_t* from = reinterpret_cast<const uint8_t*>(staged(stage, r, (c * item) >> 4)) + ((c * item) & 15);
+      if (c >= left) continue;
+      if (item == 4) *reinterpret_cast<uint32_t*>(to + r * step + 4 * c) = *reinterpret_cast<const uint32_t*>(from);
+      else *reinterpret_cast<uint16_t*>(to + r * step + 2 * c) = *reinterpret_cast<const uint16_t*>(from);
+    }
   }
   __syncwarp();
 }
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
       mbar_init(&ctl.empty[i], 1);
     }
     mbar_init(&ctl.sums_full, 1 + a.extra);
-    mbar_init(&ctl.sums_empty, 2 * kEpilogueWarps);
+    mbar_init(&ctl.sums_empty, 2 * 4 * (BN / C::SHARE));
     mbar_init(&ctl.drain, 1);
     ctl.abort = 0;
     mbar_fence_init();
@@ -243,82 +244,74 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
     }
     __syncwarp();
   } else {
-    // The first four warps take the tile's first columns, the other four the rest.
-    const int half = warp >> 2, mine = half ? BN - C::FIRST : C::FIRST;
-    const uint32_t sums = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * C::FIRST;
-    uint8_t* stage = ring + (size_t)C::SLOTS * C::SLOT + warp * (32 * 128);
+    // Four warps to the 128 rows of 64 columns each.  They take the sums as they are into
+    // registers and free their place, before any arithmetic: the next tile's products
+    // wait for that (some 3000 cycles when they scaled and rounded first).
+    const int first = (warp >> 2) * C::SHARE;
+    const uint32_t sums = tmem + ((uint32_t)((warp & 3) * 32) << 16) + first;
+    uint8_t* stage = ring + (size_t)C::SLOTS * C::SLOT + warp * (32 * 64);
     const int item = element_bytes(a.y_type);
+    const long long step = a.y_stride * item;
+    const float2* column = ctl.column + first;
     bool alive = true;
     int done = 0;
     for (int at = pair; at < all; at += pairs, ++done) {
       const Tile tile(at, t_tiles, n_tiles, BN);
-      const int t0 = tile.t0 + 128 * rank + (warp & 3) * 32, n0 = tile.n0 + half * C::FIRST;
+      const int t0 = tile.t0 + 128 * rank + (warp & 3) * 32, n0 = tile.n0 + first;
       named_sync(1, 32 * kEpilogueWarps);  // the tile before has been written
       if (threadIdx.x < BN) {
         const int n = tile.n0 + threadIdx.x;
         ctl.column[threadIdx.x] = make_float2(a.w_row && n < a.n ? __ldg(a.w_row + n) : 1.f,
                                               a.bias && n < a.n ? __ldg(a.bias + n) : 0.f);
       }
-      const float row = a.x_row && t0 + lane < a.t ? __ldg(a.x_row + t0 + lane) : 1.f;
+      float row = a.x_row && t0 + lane < a.t ? __ldg(a.x_row + t0 + lane) : 1.f;
       named_sync(1, 32 * kEpilogueWarps);
+      if (first >= BN) continue;
       alive = alive && __all_sync(0xffffffffu, cluster_wait(&ctl.sums_full, done & 1, a.wait_cycles, abort_flag, a.st));
       fence_after_sync();
-      const float factor = alive ? row : kNaN;
-      const float2* column = ctl.column + half * C::FIRST;
-      uint8_t* y = static_cast<uint8_t*>(a.y) + (t0 * a.y_stride + n0) * item;
-      const long long step = a.y_stride * item;
+      float v[C::SHARE];
+      attn::tmem_ld32(sums, v);
+      attn::tmem_ld32(sums + 32, v + 32);
+      attn::tmem_ld_wait32(v);
+      attn::tmem_ld_wait32(v + 32);
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0 && alive) arrive_relaxed_at(&ctl.sums_empty, 0);
+      if (!alive) row = kNaN;
       const int rows = min(32, a.t - t0), left = a.n - n0;
-      auto read = [&](int i, float(&v)[64]) {  // 64 columns from i on
-        attn::tmem_ld32(sums + i, v);
-        attn::tmem_ld32(sums + i + 32, v + 32);
-        attn::tmem_ld_wait32(v);
-        attn::tmem_ld_wait32(v + 32);
-#pragma unroll
-        for (int k = 0; k < 64; ++k) {
-          const float2 c = column[i + k];
-          v[k] = fmaf(v[k] * factor, c.x, c.y);
-        }
-      };
-      auto release = [&]() {  // the next tile's products may have the sums' place
-        fence_before_sync();
-        __syncwarp();
-        if (lane == 0 && alive) arrive_relaxed_at(&ctl.sums_empty, 0);
-      };
+      uint8_t* y = static_cast<uint8_t*>(a.y) + (t0 * a.y_stride + n0) * item;
+      if (rows <= 0) continue;
       if (a.y_type != FP4_FP32) {
-        uint4 q[C::FIRST / 8];
 #pragma unroll
-        for (int i = 0; i < C::FIRST; i += 64) {
-          if (i >= mine) break;
-          float v[64];
-          read(i, v);
+        for (int i = 0; i < C::SHARE; i += 32) {
+          if (i >= left) break;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float(&f)[8] = *reinterpret_cast<const float(*)[8]>(v + 8 * k);
-            q[i / 8 + k] = a.y_type == FP4_BF16 ? attn::pack8<attn::Brain>(f) : attn::pack8<attn::Half>(f);
+          for (int k = 0; k < 4; ++k) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 c = column[i + 8 * k + e];
+              f[e] = fmaf(v[i + 8 * k + e] * row, c.x, c.y);
+            }
+            *staged(stage, lane, k) = a.y_type == FP4_BF16 ? attn::pack8<attn::Brain>(f) : attn::pack8<attn::Half>(f);
           }
-        }
-        release();
-#pragma unroll
-        for (int i = 0; i < C::FIRST; i += 64) {
-          if (i >= mine || i >= left || rows <= 0) break;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) *staged(stage, lane, k) = q[i / 8 + k];
           write_staged(stage, lane, args.vector, y + 2 * i, step, 2, rows, left - i);
         }
       } else {
-#pragma unroll 1
-        for (int i = 0; i < mine; i += 64) {
-          float v[64];
-          read(i, v);
-          if (i + 64 >= mine) release();
 #pragma unroll
-          for (int p = 0; p < 64; p += 32) {
-            if (i + p >= left || rows <= 0) break;
+        for (int i = 0; i < C::SHARE; i += 16) {
+          if (i >= left) break;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              *staged(stage, lane, k) = *reinterpret_cast<const uint4*>(v + p + 4 * k);
-            write_staged(stage, lane, args.vector, y + 4 * (i + p), step, 4, rows, left - i - p);
+          for (int k = 0; k < 4; ++k) {
+            float f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 c = column[i + 4 * k + e];
+              f[e] = fmaf(v[i + 4 * k + e] * row, c.x, c.y);
+            }
+            *staged(stage, lane, k) = *reinterpret_cast<const uint4*>(f);
           }
+          write_staged(stage, lane, args.vector, y + 4 * i, step, 4, rows, left - i);
         }
       }
     }
