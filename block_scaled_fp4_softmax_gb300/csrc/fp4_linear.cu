@@ -67,7 +67,22 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(const __grid_consta
   const int c0 = chunks * rank / split, c1 = chunks * (rank + 1) / split;
   const int tiles = fp4::scale_tiles(a.cols, FMT);
 
-  if (threadIdx.x == 0) {
+  auto load_w = [&](int slot, int c) {  // ... and announces all of the chunk's copies
+    const uint32_t at = smem_u32(ring + (size_t)slot * C::SLOT);
+    const int kt = c * C::COPIES, bytes = min(C::COPIES, tiles - kt) * 512;
+    mbar_arrive_expect_tx(&ctl.full[slot], C::W_BYTES + C::X_BYTES + 2 * bytes);
+    load_codes(&a.w_map, at, &ctl.full[slot], c * (kChunk / 2), n0);
+    bulk_g2s(at + C::W_BYTES + C::X_BYTES, a.w_scales + ((size_t)(n0 >> 7) * tiles + kt) * 512, bytes, &ctl.full[slot]);
+  };
+  auto load_x = [&](int slot, int c) {
+    const uint32_t at = smem_u32(ring + (size_t)slot * C::SLOT);
+    const int kt = c * C::COPIES, bytes = min(C::COPIES, tiles - kt) * 512;
+    load_codes(&a.x_map, at + C::W_BYTES, &ctl.full[slot], c * (kChunk / 2), t0);
+    bulk_g2s(at + C::W_BYTES + C::X_BYTES + C::S_BYTES, a.x_scales + ((size_t)(t0 >> 7) * tiles + kt) * 512, bytes,
+             &ctl.full[slot]);
+  };
+  const int ahead = a.early ? min(slots, c1 - c0) : 0;  // chunks whose part of w does not wait
+  if (threadIdx.x == 32 * kTmaWarp) {
     for (int i = 0; i < slots; ++i) {
       mbar_init(&ctl.full[i], 1);
       mbar_init(&ctl.empty[i], 1);
@@ -78,6 +93,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(const __grid_consta
     mbar_fence_init();
     attn::prefetch_map(&a.w_map);
     attn::prefetch_map(&a.x_map);
+    for (int i = 0; i < ahead; ++i) load_w(i, c0 + i);
   }
   // TMEM is taken only when the kernel before has ended, and before the next one may
   // start: CTAs that wait for one another's kernels never hold what the others need.
@@ -98,15 +114,8 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(const __grid_consta
         const int slot = filled % slots;
         alive = attn::bounded_wait(&ctl.empty[slot], ((filled / slots) & 1) ^ 1, a.wait_cycles, abort_flag, a.st);
         if (!alive) break;
-        const uint32_t at = smem_u32(ring + (size_t)slot * C::SLOT);
-        const int kt = c * C::COPIES, count = min(C::COPIES, tiles - kt);  // tiles of scales
-        mbar_arrive_expect_tx(&ctl.full[slot], C::W_BYTES + C::X_BYTES + 2 * count * 512);
-        load_codes(&a.w_map, at, &ctl.full[slot], c * (kChunk / 2), n0);
-        load_codes(&a.x_map, at + C::W_BYTES, &ctl.full[slot], c * (kChunk / 2), t0);
-        bulk_g2s(at + C::W_BYTES + C::X_BYTES, a.w_scales + ((size_t)(n0 >> 7) * tiles + kt) * 512, count * 512,
-                 &ctl.full[slot]);
-        bulk_g2s(at + C::W_BYTES + C::X_BYTES + C::S_BYTES, a.x_scales + ((size_t)(t0 >> 7) * tiles + kt) * 512,
-                 count * 512, &ctl.full[slot]);
+        if (filled >= ahead) load_w(slot, c);
+        load_x(slot, c);
       }
       // every copy has landed before the CTA's shared memory goes away
       for (int i = max(0, filled - slots); i < filled; ++i)
@@ -185,18 +194,49 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(const __grid_consta
   }
   if (split > 1) {
     cluster_sync();
-    if (threadIdx.x < 128) {
-      const int n = n0 + threadIdx.x;
-      const float scale = a.w_row && n < a.n ? __ldg(a.w_row + n) : 1.f;
-      const float add = a.bias && n < a.n ? __ldg(a.bias + n) : 0.f;
-      const int j1 = min(BN * (rank + 1) / split, a.t - t0);
-      for (int j = BN * rank / split; j < j1; ++j) {
-        const uint32_t at = smem_u32(ring) + (uint32_t)(j * 128 + threadIdx.x) * 4;
-        float v = 0.f;
-        for (int k = 0; k < split; ++k) v += __uint_as_float(peer_word(at, k));
-        if (n >= a.n) continue;
-        if (a.x_row) v *= __ldg(a.x_row + t0 + j);
-        store_one(a.y, (t0 + j) * a.y_stride + n, a.y_type, fmaf(v, scale, add));
+    // A thread adds up 4 columns of y of a row of x; 4 of those at a time, as a word of
+    // another CTA is some 500 cycles away (128 rows of x, 2 CTAs: one at a time took 20 us).
+    const int q0 = BN * rank / split * 32, q1 = min(BN * (rank + 1) / split, a.t - t0) * 32;
+    const int item = element_bytes(a.y_type);
+    constexpr int U = 4;
+    for (int q = q0 + threadIdx.x; q < q1; q += U * kThreads) {
+      float4 v[U] = {};
+      for (int k = 0; k < split; ++k) {
+        float4 w[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) w[u] = peer_float4(smem_u32(ring) + (uint32_t)min(q + u * kThreads, q1 - 1) * 16, k);
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u].x += w[u].x, v[u].y += w[u].y, v[u].z += w[u].z, v[u].w += w[u].w;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int at = q + u * kThreads, t = t0 + (at >> 5), n = n0 + (at & 31) * 4;
+        if (at >= q1) break;
+        const float row = a.x_row ? __ldg(a.x_row + t) : 1.f;
+        const float f[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        uint32_t out[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float scale = a.w_row && n + e < a.n ? __ldg(a.w_row + n + e) : 1.f;
+          const float add = a.bias && n + e < a.n ? __ldg(a.bias + n + e) : 0.f;
+          out[e] = __float_as_uint(fmaf(f[e] * row, scale, add));
+        }
+        uint8_t* y = static_cast<uint8_t*>(a.y) + (t * a.y_stride + n) * item;
+        if (((uintptr_t)y & (4 * item - 1)) == 0 && n + 4 <= a.n) {
+          if (item == 4) {
+            *reinterpret_cast<uint4*>(y) = make_uint4(out[0], out[1], out[2], out[3]);
+          } else {
+            auto two = [&](int e) {
+              const float lo = __uint_as_float(out[e]), hi = __uint_as_float(out[e + 1]);
+              return a.y_type == FP4_BF16 ? attn::Brain::down(lo, hi) : attn::Half::down(lo, hi);
+            };
+            *reinterpret_cast<uint2*>(y) = make_uint2(two(0), two(2));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < a.n) store_one(y, e, a.y_type, __uint_as_float(out[e]));
+        }
       }
     }
     cluster_sync();  // the others have read this CTA's part
@@ -267,12 +307,9 @@ int check_output(const fp4_rows* y, int rows, int cols) {
   return MOE_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-int fp4_linear(const fp4_matrix* x, const fp4_matrix* w, const float* bias, const fp4_rows* y,
-               int32_t* dev_status, void* stream) {
+// `early`: the kernel before on the stream writes x alone, and waited for those before it.
+int product(const fp4_matrix* x, const fp4_matrix* w, const float* bias, const fp4_rows* y, int32_t* dev_status,
+            void* stream, bool early) {
   if (const int rc = fp4::check_matrix(x)) return rc;
   if (const int rc = fp4::check_matrix(w)) return rc;
   if (x->cols != w->cols || x->format != w->format) return MOE_ERR_INVALID_ARG;
@@ -287,8 +324,18 @@ int fp4_linear(const fp4_matrix* x, const fp4_matrix* w, const float* bias, cons
   a.n = w->rows, a.t = x->rows, a.cols = x->cols;
   a.y = y->data, a.y_stride = x->rows > 1 ? y->stride : 0, a.y_type = y->type;
   a.wait_cycles = attn::wait_cycles(), a.extra = (int)moe::barrier_extra(), a.st = dev_status;
+  a.early = early;
   return w->format == MOE_FMT_NVFP4 ? launch<MOE_FMT_NVFP4>(a, *x, *w, sms, (cudaStream_t)stream)
                                     : launch<MOE_FMT_MXFP4>(a, *x, *w, sms, (cudaStream_t)stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int fp4_linear(const fp4_matrix* x, const fp4_matrix* w, const float* bias, const fp4_rows* y,
+               int32_t* dev_status, void* stream) {
+  return product(x, w, bias, y, dev_status, stream, false);
 }
 
 size_t fp4_linear_rows_workspace(const fp4_matrix* w, int rows) {
@@ -314,7 +361,7 @@ int fp4_linear_rows(const fp4_rows* x, int rows, const fp4_matrix* w, const floa
                         w->format == MOE_FMT_NVFP4 ? reinterpret_cast<float*>(at + l.row_scale) : nullptr, rows,
                         w->cols, w->format};
   if (const int rc = fp4_quantize(x, &m, stream)) return rc;
-  return fp4_linear(&m, w, bias, y, dev_status, stream);
+  return product(&m, w, bias, y, dev_status, stream, true);
 }
 
 }  // extern "C"

@@ -20,6 +20,7 @@ struct LinearArgs {
   int y_type;
   long long wait_cycles;
   int extra;  // arrivals that never come, on the barrier of the sums
+  int early;  // w may be read before the kernel before this one has ended
   int32_t* st;
 };
 
@@ -143,6 +144,15 @@ __device__ __forceinline__ bool cluster_wait(uint64_t* bar, uint32_t parity, lon
     }
   }
   return true;
+}
+
+// (volatile alone: behind the barriers of the cluster, but several at a time)
+__device__ __forceinline__ float4 peer_float4(uint32_t saddr, int rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(peer_address(saddr, rank)));
+  return v;
 }
 
 __device__ __forceinline__ void store_one(void* y, long long at, int type, float v) {
