@@ -20,6 +20,14 @@ __device__ __forceinline__ size_t scale_word(int r, int kt, int tiles) {
   return ((size_t)(r >> 7) * tiles + kt) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4;
 }
 
+// Rows of 16 or 32 bits, as the entry points' arguments describe them.
+struct Rows {
+  void* data;
+  long long stride;
+  int type;
+};
+inline Rows rows_of(const void* data, long long stride, int type) { return Rows{const_cast<void*>(data), stride, type}; }
+
 // ---------------------------------------------------------------------------
 // Host checks
 // ---------------------------------------------------------------------------
@@ -48,12 +56,12 @@ inline int check_target(const fp4_matrix* m, int rows, int cols) {
 __host__ __device__ __forceinline__ int element_bytes(int type) { return type == FP4_FP32 ? 4 : 2; }
 
 // Rows that are read or written 16 bytes at a time.  `wide`: 32-bit rows are allowed.
-inline int check_rows(const fp4_rows* x, int rows, int cols, bool wide) {
-  if (!x || (!x->data && rows > 0)) return MOE_ERR_INVALID_ARG;
-  if (x->type != FP4_BF16 && x->type != FP4_FP16 && !(wide && x->type == FP4_FP32)) return MOE_ERR_UNSUPPORTED;
-  if (!moe::aligned16(x->data)) return MOE_ERR_ALIGNMENT;
-  if (rows > 1 && (x->stride < cols || x->stride >= (1ll << 38))) return MOE_ERR_INVALID_ARG;
-  if (rows > 1 && x->stride % (16 / element_bytes(x->type)) != 0) return MOE_ERR_ALIGNMENT;
+inline int check_rows(const Rows& x, int rows, int cols, bool wide) {
+  if (!x.data && rows > 0) return MOE_ERR_INVALID_ARG;
+  if (x.type != FP4_BF16 && x.type != FP4_FP16 && !(wide && x.type == FP4_FP32)) return MOE_ERR_UNSUPPORTED;
+  if (!moe::aligned16(x.data)) return MOE_ERR_ALIGNMENT;
+  if (rows > 1 && (x.stride < cols || x.stride >= (1ll << 38))) return MOE_ERR_INVALID_ARG;
+  if (rows > 1 && x.stride % (16 / element_bytes(x.type)) != 0) return MOE_ERR_ALIGNMENT;
   return MOE_OK;
 }
 

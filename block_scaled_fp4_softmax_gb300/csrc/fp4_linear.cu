@@ -299,17 +299,17 @@ Layout layout(int rows, int cols, int format) {
   return l;
 }
 
-int check_output(const fp4_rows* y, int rows, int cols) {
-  if (!y || (!y->data && rows > 0 && cols > 0)) return MOE_ERR_INVALID_ARG;
-  if (y->type != FP4_BF16 && y->type != FP4_FP16 && y->type != FP4_FP32) return MOE_ERR_UNSUPPORTED;
-  if ((uintptr_t)y->data % fp4::element_bytes(y->type)) return MOE_ERR_ALIGNMENT;
-  if (rows > 1 && (y->stride < cols || y->stride >= (1ll << 38))) return MOE_ERR_INVALID_ARG;
+int check_output(const Rows& y, int rows, int cols) {
+  if (!y.data && rows > 0 && cols > 0) return MOE_ERR_INVALID_ARG;
+  if (y.type != FP4_BF16 && y.type != FP4_FP16 && y.type != FP4_FP32) return MOE_ERR_UNSUPPORTED;
+  if ((uintptr_t)y.data % element_bytes(y.type)) return MOE_ERR_ALIGNMENT;
+  if (rows > 1 && (y.stride < cols || y.stride >= (1ll << 38))) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
 
 // `early`: the kernel before on the stream writes x alone, and waited for those before it.
-int product(const fp4_matrix* x, const fp4_matrix* w, const float* bias, const fp4_rows* y, int32_t* dev_status,
-            void* stream, bool early) {
+int product(const fp4_matrix* x, const fp4_matrix* w, const float* bias, const Rows& y, int32_t* dev_status, void* stream,
+            bool early) {
   if (const int rc = fp4::check_matrix(x)) return rc;
   if (const int rc = fp4::check_matrix(w)) return rc;
   if (x->cols != w->cols || x->format != w->format) return MOE_ERR_INVALID_ARG;
@@ -322,7 +322,7 @@ int product(const fp4_matrix* x, const fp4_matrix* w, const float* bias, const f
   a.w_scales = static_cast<const uint8_t*>(w->scales), a.x_scales = static_cast<const uint8_t*>(x->scales);
   a.w_row = w->row_scale, a.x_row = x->row_scale, a.bias = bias;
   a.n = w->rows, a.t = x->rows, a.cols = x->cols;
-  a.y = y->data, a.y_stride = x->rows > 1 ? y->stride : 0, a.y_type = y->type;
+  a.y = y.data, a.y_stride = x->rows > 1 ? y.stride : 0, a.y_type = y.type;
   a.wait_cycles = attn::wait_cycles(), a.extra = (int)moe::barrier_extra(), a.st = dev_status;
   a.early = early;
   return w->format == MOE_FMT_NVFP4 ? launch<MOE_FMT_NVFP4>(a, *x, *w, sms, (cudaStream_t)stream)
@@ -333,9 +333,9 @@ int product(const fp4_matrix* x, const fp4_matrix* w, const float* bias, const f
 
 extern "C" {
 
-int fp4_linear(const fp4_matrix* x, const fp4_matrix* w, const float* bias, const fp4_rows* y,
+int fp4_linear(const fp4_matrix* x, const fp4_matrix* w, const float* bias, void* y, long long y_stride, int y_type,
                int32_t* dev_status, void* stream) {
-  return product(x, w, bias, y, dev_status, stream, false);
+  return product(x, w, bias, rows_of(y, y_stride, y_type), dev_status, stream, false);
 }
 
 size_t fp4_linear_rows_workspace(const fp4_matrix* w, int rows) {
@@ -343,13 +343,15 @@ size_t fp4_linear_rows_workspace(const fp4_matrix* w, int rows) {
   return layout(rows, w->cols, w->format).bytes + 16;
 }
 
-int fp4_linear_rows(const fp4_rows* x, int rows, const fp4_matrix* w, const float* bias, const fp4_rows* y,
-                    void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream) {
+int fp4_linear_rows(const void* x, long long x_stride, int x_type, int rows, const fp4_matrix* w, const float* bias,
+                    void* y, long long y_stride, int y_type, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                    void* stream) {
   if (rows < 0) return MOE_ERR_INVALID_ARG;
   if (const int rc = fp4::check_matrix(w)) return rc;
   if (!fp4::shape_ok(rows, w->cols, w->format)) return MOE_ERR_UNSUPPORTED;
-  if (const int rc = fp4::check_rows(x, rows, w->cols, true)) return rc;
-  if (const int rc = check_output(y, rows, w->rows)) return rc;
+  const Rows out = rows_of(y, y_stride, y_type);
+  if (const int rc = check_rows(rows_of(x, x_stride, x_type), rows, w->cols, true)) return rc;
+  if (const int rc = check_output(out, rows, w->rows)) return rc;
   if ((uintptr_t)bias & 3u) return MOE_ERR_ALIGNMENT;
   if (rows == 0 || w->rows == 0) return MOE_OK;
   if (!workspace) return MOE_ERR_INVALID_ARG;
@@ -360,8 +362,8 @@ int fp4_linear_rows(const fp4_rows* x, int rows, const fp4_matrix* w, const floa
   const fp4_matrix m = {at, at + l.scales,
                         w->format == MOE_FMT_NVFP4 ? reinterpret_cast<float*>(at + l.row_scale) : nullptr, rows,
                         w->cols, w->format};
-  if (const int rc = fp4_quantize(x, &m, stream)) return rc;
-  return product(&m, w, bias, y, dev_status, stream, true);
+  if (const int rc = fp4_quantize(x, x_stride, x_type, &m, stream)) return rc;
+  return product(&m, w, bias, out, dev_status, stream, true);
 }
 
 }  // extern "C"

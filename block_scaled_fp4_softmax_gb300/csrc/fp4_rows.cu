@@ -214,7 +214,7 @@ __device__ __forceinline__ void to_fp4(const fp4_matrix& m, const Place& p, floa
 // ---------------------------------------------------------------------------
 
 struct QuantizeArgs {
-  fp4_rows x;
+  fp4::Rows x;
   fp4_matrix m;
 };
 
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(256 * NB) quantize_kernel(const __grid_constan
 }
 
 struct SwigluArgs {
-  fp4_rows gate, up, out;  // out.data, m.codes: NULL where not wanted
+  fp4::Rows gate, up, out;  // out.data, m.codes: NULL where not wanted
   fp4_matrix m;
   int rows, cols;
 };
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(256 * NB) swiglu_kernel(const __grid_constant_
 }
 
 struct NormArgs {
-  fp4_rows r, y, gate, r_out, h;  // .data NULL: not there
+  fp4::Rows r, y, gate, r_out, h;  // .data NULL: not there
   int gate_cols;
   const float *post_weight, *weight;
   float scale, eps;
@@ -285,7 +285,7 @@ __device__ __forceinline__ void load_weights(const float* w, int col, float (&f)
   f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
 }
 
-__device__ __forceinline__ float one_element(const fp4_rows& x, long long at) {
+__device__ __forceinline__ float one_element(const fp4::Rows& x, long long at) {
   if (x.type == FP4_FP32) return __ldg(static_cast<const float*>(x.data) + at);
   const uint16_t b = __ldg(static_cast<const uint16_t*>(x.data) + at);
   return x.type == FP4_BF16 ? __uint_as_float((uint32_t)b << 16) : __half2float(__ushort_as_half(b));
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(256 * NB) norm_kernel(const __grid_constant__ 
 // A thread to 8 columns of a row.
 struct DequantizeArgs {
   fp4_matrix m;
-  fp4_rows out;
+  fp4::Rows out;
 };
 
 __global__ void __launch_bounds__(256) dequantize_kernel(const __grid_constant__ DequantizeArgs a) {
@@ -450,7 +450,7 @@ int by_width(int type, F f) {
 }
 
 // The stride of a single row is of no account.
-void one_row(fp4_rows& x, int rows) {
+void one_row(fp4::Rows& x, int rows) {
   if (rows == 1) x.stride = 0;
 }
 
@@ -475,90 +475,91 @@ int fp4_tile_scales(const uint8_t* scales, int rows, int cols, int format, uint8
                          (cudaStream_t)stream, scales, rows, cols / fp4::block_of(format), tiles, tiled);
 }
 
-int fp4_quantize(const fp4_rows* x, const fp4_matrix* out, void* stream) {
+int fp4_quantize(const void* x, long long x_stride, int x_type, const fp4_matrix* out, void* stream) {
   if (!out) return MOE_ERR_INVALID_ARG;
+  QuantizeArgs a{fp4::rows_of(x, x_stride, x_type), *out};
   if (const int rc = fp4::check_target(out, out->rows, out->cols)) return rc;
-  if (const int rc = fp4::check_rows(x, out->rows, out->cols, true)) return rc;
+  if (const int rc = fp4::check_rows(a.x, out->rows, out->cols, true)) return rc;
   if (out->rows == 0) return MOE_OK;
-  QuantizeArgs a{*x, *out};
   one_row(a.x, out->rows);
   const Shape s(out->rows, out->cols);
   return by_units(s.nb, [&](auto nb) {
-    return by_width(x->type, [&](auto wide) {
+    return by_width(x_type, [&](auto wide) {
       return moe::launch_pdl(quantize_kernel<nb, wide>, s.grid, s.block, 0, (cudaStream_t)stream, a);
     });
   });
 }
 
-int fp4_dequantize(const fp4_matrix* m, const fp4_rows* out, void* stream) {
+int fp4_dequantize(const fp4_matrix* m, void* out, long long out_stride, int out_type, void* stream) {
   if (const int rc = fp4::check_matrix(m)) return rc;
-  if (const int rc = fp4::check_rows(out, m->rows, m->cols, true)) return rc;
+  DequantizeArgs a{*m, fp4::rows_of(out, out_stride, out_type)};
+  if (const int rc = fp4::check_rows(a.out, m->rows, m->cols, true)) return rc;
   if (m->rows == 0) return MOE_OK;
-  DequantizeArgs a{*m, *out};
   one_row(a.out, m->rows);
   const int threads = m->cols >= 2048 ? 256 : (m->cols + 255) / 256 * 32, per = 256 / threads;
   return moe::launch_pdl(dequantize_kernel, dim3((m->rows + per - 1) / per), dim3(threads, per), 0,
                          (cudaStream_t)stream, a);
 }
 
-int fp4_swiglu(const fp4_rows* gate, const fp4_rows* up, int rows, int cols, const fp4_rows* out,
-               const fp4_matrix* m, void* stream) {
-  if (rows < 0 || (!out && !m)) return MOE_ERR_INVALID_ARG;
+int fp4_swiglu(const void* gate, long long gate_stride, const void* up, long long up_stride, int type, int rows,
+               int cols, void* out, long long out_stride, int out_type, const fp4_matrix* m, void* stream) {
+  if (rows < 0 || (!out && !m && rows > 0)) return MOE_ERR_INVALID_ARG;
   if (!fp4::shape_ok(rows, cols, MOE_FMT_NVFP4)) return MOE_ERR_UNSUPPORTED;
-  if (const int rc = fp4::check_rows(gate, rows, cols, true)) return rc;
-  if (const int rc = fp4::check_rows(up, rows, cols, true)) return rc;
-  if (gate->type != up->type) return MOE_ERR_INVALID_ARG;
+  SwigluArgs a{fp4::rows_of(gate, gate_stride, type), fp4::rows_of(up, up_stride, type),
+               fp4::rows_of(out, out_stride, out_type), m ? *m : fp4_matrix{}, rows, cols};
+  if (const int rc = fp4::check_rows(a.gate, rows, cols, true)) return rc;
+  if (const int rc = fp4::check_rows(a.up, rows, cols, true)) return rc;
   if (out)
-    if (const int rc = fp4::check_rows(out, rows, cols, false)) return rc;
+    if (const int rc = fp4::check_rows(a.out, rows, cols, false)) return rc;
   if (m)
     if (const int rc = fp4::check_target(m, rows, cols)) return rc;
   if (rows == 0) return MOE_OK;
-  SwigluArgs a{*gate, *up, out ? *out : fp4_rows{}, m ? *m : fp4_matrix{}, rows, cols};
   one_row(a.gate, rows), one_row(a.up, rows), one_row(a.out, rows);
   const Shape s(rows, cols);
   return by_units(s.nb, [&](auto nb) {
-    return by_width(gate->type, [&](auto wide) {
+    return by_width(type, [&](auto wide) {
       return moe::launch_pdl(swiglu_kernel<nb, wide>, s.grid, s.block, 0, (cudaStream_t)stream, a);
     });
   });
 }
 
-int fp4_block_norm(const fp4_rows* r, const fp4_rows* y, const float* post_weight, const fp4_rows* gate,
-                   int gate_cols, double scale, const float* weight, double eps, int rows, int cols,
-                   const fp4_rows* r_out, const fp4_rows* h, const fp4_matrix* m, void* stream) {
-  if (rows < 0 || (!h && !m) || !(eps >= 0.) || !(eps <= 1e30) || !(fabs(scale) <= 1e30)) return MOE_ERR_INVALID_ARG;
-  if (!y && (post_weight || gate)) return MOE_ERR_INVALID_ARG;
+int fp4_block_norm(const void* r, long long r_stride, int r_type, const void* y, long long y_stride, int y_type,
+                   const float* post_weight, const void* gate, long long gate_stride, int gate_cols, double scale,
+                   const float* weight, double eps, int rows, int cols, void* r_out, long long r_out_stride, void* h,
+                   long long h_stride, int h_type, const fp4_matrix* m, void* stream) {
+  if (rows < 0 || (!h && !m && rows > 0) || !(eps >= 0.) || !(eps <= 1e30) || !(fabs(scale) <= 1e30))
+    return MOE_ERR_INVALID_ARG;
+  if (!y && rows > 0 && (post_weight || gate)) return MOE_ERR_INVALID_ARG;
   if (!fp4::shape_ok(rows, cols, MOE_FMT_NVFP4)) return MOE_ERR_UNSUPPORTED;
-  if (const int rc = fp4::check_rows(r, rows, cols, true)) return rc;
+  NormArgs a{fp4::rows_of(r, r_stride, r_type), fp4::rows_of(y, y_stride, y_type),
+             fp4::rows_of(gate, gate_stride, y_type), fp4::rows_of(r_out, r_out_stride, r_type),
+             fp4::rows_of(h, h_stride, h_type), gate_cols, post_weight, weight, (float)scale, (float)eps, rows, cols,
+             m ? *m : fp4_matrix{}};
+  if (const int rc = fp4::check_rows(a.r, rows, cols, true)) return rc;
   if (y)
-    if (const int rc = fp4::check_rows(y, rows, cols, true)) return rc;
+    if (const int rc = fp4::check_rows(a.y, rows, cols, true)) return rc;
   if (!moe::aligned16(post_weight) || !moe::aligned16(weight)) return MOE_ERR_ALIGNMENT;
-  NormArgs a{*r, y ? *y : fp4_rows{}, gate ? *gate : fp4_rows{}, r_out ? *r_out : fp4_rows{}, h ? *h : fp4_rows{},
-             gate_cols, post_weight, weight, (float)scale, (float)eps, rows, cols, m ? *m : fp4_matrix{}};
   if (gate) {
-    if (gate->type != y->type || (gate_cols != 1 && gate_cols != cols)) return MOE_ERR_INVALID_ARG;
-    if (!gate->data && rows > 0) return MOE_ERR_INVALID_ARG;
-    if (gate_cols == 1) {  // a number for each row, at any stride
-      if ((uintptr_t)gate->data % fp4::element_bytes(gate->type)) return MOE_ERR_ALIGNMENT;
-      if (gate->stride < 0 || gate->stride >= (1ll << 38)) return MOE_ERR_INVALID_ARG;
-    } else if (const int rc = fp4::check_rows(gate, gate->stride == 0 ? (rows > 0) : rows, cols, true)) {
+    if (gate_cols != 1 && gate_cols != cols) return MOE_ERR_INVALID_ARG;
+    if (gate_cols == 1) {
+      if ((uintptr_t)gate % fp4::element_bytes(y_type)) return MOE_ERR_ALIGNMENT;
+      if (gate_stride < 0 || gate_stride >= (1ll << 38)) return MOE_ERR_INVALID_ARG;
+    } else if (const int rc = fp4::check_rows(a.gate, gate_stride == 0 ? 1 : rows, cols, true)) {
       return rc;
     }
   }
-  if (r_out) {
-    if (const int rc = fp4::check_rows(r_out, rows, cols, true)) return rc;
-    if (r_out->type != r->type) return MOE_ERR_INVALID_ARG;
-  }
+  if (r_out)
+    if (const int rc = fp4::check_rows(a.r_out, rows, cols, true)) return rc;
   if (h)
-    if (const int rc = fp4::check_rows(h, rows, cols, false)) return rc;
+    if (const int rc = fp4::check_rows(a.h, rows, cols, false)) return rc;
   if (m)
     if (const int rc = fp4::check_target(m, rows, cols)) return rc;
   if (rows == 0) return MOE_OK;
-  for (fp4_rows* x : {&a.r, &a.y, &a.gate, &a.r_out, &a.h}) one_row(*x, rows);
+  for (fp4::Rows* x : {&a.r, &a.y, &a.gate, &a.r_out, &a.h}) one_row(*x, rows);
   const Shape s(rows, cols);
   return by_units(s.nb, [&](auto nb) {
-    return by_width(r->type, [&](auto rw) {
-      return by_width(y ? y->type : FP4_BF16, [&](auto yw) {
+    return by_width(r_type, [&](auto rw) {
+      return by_width(y ? y_type : FP4_BF16, [&](auto yw) {
         return moe::launch_pdl(norm_kernel<nb, rw, yw>, s.grid, s.block, 0, (cudaStream_t)stream, a);
       });
     });

@@ -46,23 +46,20 @@ class _MatrixStruct(ctypes.Structure):
                 ("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("format", ctypes.c_int32)]
 
 
-class _RowsStruct(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_longlong), ("type", ctypes.c_int32)]
+_vp, _i, _ll, _d, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_double, ctypes.c_size_t
 
-
-_vp, _i, _d, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_double, ctypes.c_size_t
-_mp, _rp = ctypes.POINTER(_MatrixStruct), ctypes.POINTER(_RowsStruct)
-
+# matrices go by their address, a plain number
 _SIGS = {
     "fp4_scale_bytes": (_sz, [_i, _i, _i]),
     "fp4_tile_scales": (_i, [_vp, _i, _i, _i, _vp, _vp]),
-    "fp4_quantize": (_i, [_rp, _mp, _vp]),
-    "fp4_dequantize": (_i, [_mp, _rp, _vp]),
-    "fp4_swiglu": (_i, [_rp, _rp, _i, _i, _rp, _mp, _vp]),
-    "fp4_block_norm": (_i, [_rp, _rp, _vp, _rp, _i, _d, _vp, _d, _i, _i, _rp, _rp, _mp, _vp]),
-    "fp4_linear": (_i, [_mp, _mp, _vp, _rp, _vp, _vp]),
-    "fp4_linear_rows_workspace": (_sz, [_mp, _i]),
-    "fp4_linear_rows": (_i, [_rp, _i, _mp, _vp, _rp, _vp, _sz, _vp, _vp]),
+    "fp4_quantize": (_i, [_vp, _ll, _i, _vp, _vp]),
+    "fp4_dequantize": (_i, [_vp, _vp, _ll, _i, _vp]),
+    "fp4_swiglu": (_i, [_vp, _ll, _vp, _ll, _i, _i, _i, _vp, _ll, _i, _vp, _vp]),
+    "fp4_block_norm": (_i, [_vp, _ll, _i, _vp, _ll, _i, _vp, _vp, _ll, _i, _d, _vp, _d, _i, _i, _vp, _ll, _vp, _ll, _i,
+                            _vp, _vp]),
+    "fp4_linear": (_i, [_vp, _vp, _vp, _vp, _ll, _i, _vp, _vp]),
+    "fp4_linear_rows_workspace": (_sz, [_vp, _i]),
+    "fp4_linear_rows": (_i, [_vp, _ll, _i, _i, _vp, _vp, _vp, _ll, _i, _vp, _sz, _vp, _vp]),
 }
 
 _LIB = None
@@ -92,21 +89,35 @@ _HERE = contextlib.nullcontext()
 _empty = torch.empty
 
 
+def _wrong_device(index):
+    raise MoeError(f"the operands are on cuda:{index}, cuda:{_current()} is current")
+
+
 def _index(t, name):
-    """CUDA device of an operand."""
+    """CUDA device of an operand, which has to be the current one: a launch goes there.
+    Any other is refused before anything else is done."""
     try:
-        if t.is_cuda:
-            return t.get_device()
+        index = t.get_device()
     except AttributeError:
-        pass
-    raise MoeError(f"{name} must be a CUDA tensor")
+        index = -1
+    if index < 0:
+        raise MoeError(f"{name} must be a CUDA tensor")
+    if _current() != index:
+        _wrong_device(index)
+    return index
+
+
+def _of(m, name):
+    """Device of a matrix, which has to be the current one."""
+    if m.__class__ is not Fp4Matrix:
+        raise MoeError(f"{name} must be an FP4 matrix (fp4_matrix, fp4_empty), got {type(m).__name__}")
+    if _current() != m.index:
+        _wrong_device(m.index)
+    return m.index
 
 
 def _on(stream, index):
-    """Handle of the stream to launch on.  A launch goes to the device that is
-    current: any other than the operands' is refused, before anything else is done."""
-    if _current() != index:
-        raise MoeError(f"the operands are on cuda:{index}, cuda:{_current()} is current")
+    """Handle of the stream to launch on."""
     if stream is None:
         return _raw_stream(index)
     if stream.device_index != index:
@@ -121,36 +132,34 @@ def _elsewhere(stream):
 
 
 def _rows(t, name, index, shape=None, types=_TYPES):
-    """The C description of a [rows, cols] tensor with contiguous columns."""
+    """Address, stride and type of a [rows, cols] tensor with contiguous columns."""
     try:
-        if (t.dim() == 2 and (shape is None or tuple(t.shape) == shape) and t.dtype in types and t.get_device() == index
-                and (t.stride(1) == 1 or t.shape[1] == 1)):
-            return _RowsStruct(t.data_ptr(), t.stride(0), types[t.dtype])
-    except (AttributeError, TypeError):
+        rows, one = t.stride()
+        if t.get_device() == index and (one == 1 or t.shape[1] == 1) and (shape is None or t.shape == shape):
+            return t.data_ptr(), rows, types[t.dtype]
+    except (AttributeError, TypeError, ValueError, KeyError):
         pass
     raise MoeError(f"{name} must be a {list(shape) if shape else '[rows, cols]'} tensor of "
                    f"{', '.join(map(str, types))} on cuda:{index}, columns contiguous")
 
 
 def _array(t, name, shape, dtype, index):
-    """Address of a contiguous tensor of just this shape and type; None stays None."""
-    if t is None:
-        return None
+    """Address of a contiguous tensor of just this shape and type."""
     try:
-        if t.dtype is dtype and tuple(t.shape) == shape and t.is_contiguous() and t.get_device() == index:
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index:
             return t.data_ptr()
     except (AttributeError, TypeError):
         pass
-    raise MoeError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on cuda:{index}")
+    raise MoeError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}")
 
 
-def _matrix(m, name, index, shape=None, format=None):
-    if not isinstance(m, Fp4Matrix):
-        raise MoeError(f"{name} must be an FP4 matrix (fp4_matrix, fp4_empty)")
-    if m.index != index or (shape is not None and m.shape != shape) or (format is not None and m.format != format):
-        raise MoeError(f"{name} must be a {shape or ''} FP4 matrix"
-                       f"{'' if format is None else f' of format {format}'} on cuda:{index}, got {m}")
-    return m
+def _matrix(m, name, index, shape, format=None):
+    """Address of a matrix's C description."""
+    if (m.__class__ is Fp4Matrix and m.shape == shape and m.index == index
+            and (format is None or m.format == format)):
+        return m.at
+    raise MoeError(f"{name} must be a {list(shape)} FP4 matrix{'' if format is None else f' of format {format}'} "
+                   f"on cuda:{index}, got {m!r}")
 
 
 def _short(dtype):
@@ -174,7 +183,7 @@ class Fp4Matrix:
         self.device, self.index = codes.device, codes.get_device()
         self.struct = _MatrixStruct(codes.data_ptr(), scales.data_ptr(),
                                     None if row_scale is None else row_scale.data_ptr(), rows, cols, format)
-        self.ref = ctypes.byref(self.struct)
+        self.at = ctypes.addressof(self.struct)
 
     def __repr__(self):
         return f"Fp4Matrix({self.rows} x {self.cols}, {'NVFP4' if self.format == NVFP4 else 'MXFP4'}, {self.device})"
@@ -231,7 +240,8 @@ def fp4_matrix(codes, scales, row_scale=None, format: int = NVFP4, stream=None) 
     rows, cols = codes.shape[0], 2 * codes.shape[1]
     _check_shape(rows, cols, format)
     _array(codes, "codes", (rows, cols // 2), _u8, index)
-    _array(row_scale, "row_scale", (rows,), _f32, index)
+    if row_scale is not None:
+        _array(row_scale, "row_scale", (rows,), _f32, index)
     return Fp4Matrix(codes, fp4_tile_scales(scales, cols, format, stream=stream), row_scale, rows, cols, format)
 
 
@@ -243,10 +253,10 @@ def fp4_quantize(x, format: int = NVFP4, out: Fp4Matrix | None = None, stream=No
     """x [rows, cols] of bfloat16, float16 or float32 as an FP4 matrix."""
     index = _index(x, "x")
     on = _on(stream, index)
-    rows = _rows(x, "x", index)
+    at, stride, kind = _rows(x, "x", index)
     if out is None:
         out = fp4_empty(*x.shape, format, x.device, stream)
-    rc = (_LIB or load()).fp4_quantize(rows, _matrix(out, "out", index, tuple(x.shape), format).ref, on)
+    rc = (_LIB or load()).fp4_quantize(at, stride, kind, _matrix(out, "out", index, x.shape, format), on)
     if rc:
         _check(rc, "fp4_quantize")
     return out
@@ -254,29 +264,40 @@ def fp4_quantize(x, format: int = NVFP4, out: Fp4Matrix | None = None, stream=No
 
 def fp4_dequantize(m: Fp4Matrix, dtype=torch.bfloat16, out=None, stream=None):
     """The values of m's elements, [rows, cols] of dtype (or out's type)."""
-    index = _index(getattr(m, "codes", None), "m's codes")
+    index = _of(m, "m")
     on = _on(stream, index)
     if out is None:
-        if dtype not in _TYPES:
-            raise MoeError(f"dtype must be one of {', '.join(map(str, _TYPES))}, got {dtype}")
-        with _elsewhere(stream):
-            out = _empty(m.shape, dtype=dtype, device=m.device)
-    rc = (_LIB or load()).fp4_dequantize(_matrix(m, "m", index).ref, _rows(out, "out", index, m.shape), on)
+        out = _result(m.shape, dtype, m.device, stream)
+    rc = (_LIB or load()).fp4_dequantize(m.at, *_rows(out, "out", index, m.shape), on)
     if rc:
         _check(rc, "fp4_dequantize")
     return out
 
 
-def _targets(shape, device, dtype, format, out, matrix, stream, names):
-    """The 16-bit and the FP4 output that a call writes, made where they are wanted and not given."""
-    if out is None and dtype is not None:
-        with _elsewhere(stream):
-            out = _empty(shape, dtype=_short(dtype), device=device)
+_NOTHING = (None, 0, 0)
+
+
+def _targets(shape, t, dtype, format, out, matrix, index, stream, names):
+    """What a call writes, made where it is wanted and not given: the 16-bit output, its
+    description, the FP4 output and its address."""
+    to, at = _NOTHING, None
+    if out is None:
+        if dtype is not None:
+            if stream is None:
+                out = _empty(shape, dtype=_short(dtype), device=t.device)
+            else:
+                with _elsewhere(stream):
+                    out = _empty(shape, dtype=_short(dtype), device=t.device)
+            to = out.data_ptr(), shape[1], _SHORT[dtype]
+    else:
+        to = _rows(out, names[0], index, shape, _SHORT)
     if matrix is None and format is not None:
-        matrix = fp4_empty(*shape, format, device, stream)
-    if out is None and matrix is None:
+        matrix = fp4_empty(*shape, format, t.device, stream)
+    if matrix is not None:
+        at = _matrix(matrix, names[1], index, shape, format)
+    elif out is None:
         raise MoeError(f"neither {names[0]} nor {names[1]} is wanted")
-    return out, matrix
+    return out, to, matrix, at
 
 
 def fp4_swiglu(gate, up, dtype=torch.bfloat16, format: int | None = None, out=None, matrix: Fp4Matrix | None = None,
@@ -285,13 +306,14 @@ def fp4_swiglu(gate, up, dtype=torch.bfloat16, format: int | None = None, out=No
     matrix of format or None): dtype = None and format = None leave theirs away."""
     index = _index(gate, "gate")
     on = _on(stream, index)
-    g = _rows(gate, "gate", index)
-    shape = tuple(gate.shape)
-    u = _rows(up, "up", index, shape)
-    out, matrix = _targets(shape, gate.device, dtype, format, out, matrix, stream, ("out", "matrix"))
-    rc = (_LIB or load()).fp4_swiglu(
-        g, u, shape[0], shape[1], None if out is None else _rows(out, "out", index, shape, _SHORT),
-        None if matrix is None else _matrix(matrix, "matrix", index, shape, format).ref, on)
+    g, g_stride, kind = _rows(gate, "gate", index)
+    shape = gate.shape
+    u, u_stride, other = _rows(up, "up", index, shape)
+    if other != kind:
+        raise MoeError(f"gate and up must be of one type, got {gate.dtype} and {up.dtype}")
+    out, to, matrix, at = _targets(shape, gate, dtype, format, out, matrix, index, stream, ("out", "matrix"))
+    rows, cols = shape
+    rc = (_LIB or load()).fp4_swiglu(g, g_stride, u, u_stride, kind, rows, cols, *to, at, on)
     if rc:
         _check(rc, "fp4_swiglu")
     return out, matrix
@@ -308,8 +330,9 @@ def fp4_block_norm(r, y=None, post_weight=None, gate=None, scale: float = 1.0, w
     index = _index(r, "r")
     on = _on(stream, index)
     a = _rows(r, "r", index)
-    shape = tuple(r.shape)
-    g, gate_cols, b, to = None, 0, None, None
+    shape = r.shape
+    rows, cols = shape
+    b, g, gate_stride, gate_cols, to, to_stride = _NOTHING, None, 0, 0, None, 0
     if y is None:
         if post_weight is not None or gate is not None or r_out is not None:
             raise MoeError("post_weight, gate and r_out go with y")
@@ -317,62 +340,68 @@ def fp4_block_norm(r, y=None, post_weight=None, gate=None, scale: float = 1.0, w
     else:
         b = _rows(y, "y", index, shape)
         if gate is not None:
-            g, gate_cols = _gate(gate, y, index, shape)
-        if r_out is None:
+            g, gate_stride, gate_cols = _gate(gate, y, index, shape)
+        if r_out is r:
+            to, to_stride = a[:2]
+        elif r_out is None:
             with _elsewhere(stream):
                 r_out = _empty(shape, dtype=r.dtype, device=r.device)
-        to = _rows(r_out, "r_out", index, shape)
-    out, matrix = _targets(shape, r.device, dtype, format, out, matrix, stream, ("out", "matrix"))
-    rc = (_LIB or load()).fp4_block_norm(
-        a, b, _array(post_weight, "post_weight", shape[1:], _f32, index), g, gate_cols, scale,
-        _array(weight, "weight", shape[1:], _f32, index), eps, shape[0], shape[1], to,
-        None if out is None else _rows(out, "out", index, shape, _SHORT),
-        None if matrix is None else _matrix(matrix, "matrix", index, shape, format).ref, on)
+            to, to_stride = r_out.data_ptr(), cols
+        else:
+            to, to_stride, kind = _rows(r_out, "r_out", index, shape)
+            if kind != a[2]:
+                raise MoeError(f"r_out must be of r's type, got {r_out.dtype} and {r.dtype}")
+    post = None if post_weight is None else _array(post_weight, "post_weight", (cols,), _f32, index)
+    w = None if weight is None else _array(weight, "weight", (cols,), _f32, index)
+    out, h, matrix, at = _targets(shape, r, dtype, format, out, matrix, index, stream, ("out", "matrix"))
+    rc = (_LIB or load()).fp4_block_norm(*a, *b, post, g, gate_stride, gate_cols, scale, w, eps, rows, cols, to,
+                                         to_stride, *h, at, on)
     if rc:
         _check(rc, "fp4_block_norm")
     return r_out, out, matrix
 
 
 def _gate(gate, y, index, shape):
-    """The C description of a gate, and how many columns it has."""
+    """Address, row stride and columns of a gate."""
     try:
-        form = tuple(gate.shape)
+        form = gate.shape
         if gate.dtype is y.dtype and gate.get_device() == index:
             if form == shape[1:] and gate.is_contiguous():
-                return _RowsStruct(gate.data_ptr(), 0, _TYPES[gate.dtype]), shape[1]
+                return gate.data_ptr(), 0, shape[1]
             if form == shape and gate.stride(1) == 1:
-                return _RowsStruct(gate.data_ptr(), gate.stride(0), _TYPES[gate.dtype]), shape[1]
+                return gate.data_ptr(), gate.stride(0), shape[1]
             if form == (shape[0], 1):
-                return _RowsStruct(gate.data_ptr(), gate.stride(0), _TYPES[gate.dtype]), 1
+                return gate.data_ptr(), gate.stride(0), 1
     except (AttributeError, TypeError):
         pass
     raise MoeError(f"gate must be a {list(shape[1:])}, {list(shape)} or {[shape[0], 1]} tensor of {y.dtype} on "
                    f"cuda:{index}, columns contiguous")
 
 
-def _result(rows, w, dtype, out, stream):
-    if out is None:
-        if dtype not in _TYPES:
-            raise MoeError(f"dtype must be one of {', '.join(map(str, _TYPES))}, got {dtype}")
-        with _elsewhere(stream):
-            out = _empty((rows, w.rows), dtype=dtype, device=w.device)
-    return out
-
-
-def _status(dev_status, index):
-    return None if dev_status is None else _array(dev_status, "dev_status", (1,), _i32, index)
+def _result(shape, dtype, device, stream):
+    if dtype not in _TYPES:
+        raise MoeError(f"dtype must be one of {', '.join(map(str, _TYPES))}, got {dtype}")
+    if stream is None:
+        return _empty(shape, dtype=dtype, device=device)
+    with _elsewhere(stream):
+        return _empty(shape, dtype=dtype, device=device)
 
 
 def fp4_linear(x: Fp4Matrix, w: Fp4Matrix, bias=None, dtype=torch.bfloat16, out=None, dev_status=None, stream=None):
     """x [tokens, cols] times w [features, cols], both in FP4 of one format, plus
     bias [features] float32: [tokens, features] of dtype (or out's type)."""
-    index = _index(getattr(w, "codes", None), "w's codes")
+    index = _of(w, "w")
     on = _on(stream, index)
-    _matrix(w, "w", index)
-    _matrix(x, "x", index, (getattr(x, "rows", None), w.cols), w.format)
-    out = _result(x.rows, w, dtype, out, stream)
-    rc = (_LIB or load()).fp4_linear(x.ref, w.ref, _array(bias, "bias", (w.rows,), _f32, index),
-                                     _rows(out, "out", index, (x.rows, w.rows)), _status(dev_status, index), on)
+    _of(x, "x")
+    if x.cols != w.cols or x.format != w.format:
+        raise MoeError(f"x and w must have the same columns and format, got {x!r} and {w!r}")
+    shape = (x.rows, w.rows)
+    if out is None:
+        out = _result(shape, dtype, w.device, stream)
+    rc = (_LIB or load()).fp4_linear(
+        x.at, w.at, None if bias is None else _array(bias, "bias", (w.rows,), _f32, index),
+        *_rows(out, "out", index, shape),
+        None if dev_status is None else _array(dev_status, "dev_status", (1,), _i32, index), on)
     if rc:
         _check(rc, "fp4_linear")
     return out
@@ -380,10 +409,10 @@ def fp4_linear(x: Fp4Matrix, w: Fp4Matrix, bias=None, dtype=torch.bfloat16, out=
 
 def fp4_linear_rows_workspace(w: Fp4Matrix, rows: int):
     """A workspace for :func:`fp4_linear_rows` with up to `rows` rows."""
-    index = _index(getattr(w, "codes", None), "w's codes")
+    _of(w, "w")
     if not 0 <= rows <= 1 << 24:
         raise MoeError(f"rows must be 0 to 2^24, got {rows}")
-    n = int(load().fp4_linear_rows_workspace(_matrix(w, "w", index).ref, rows))
+    n = int(load().fp4_linear_rows_workspace(w.at, rows))
     if n == 0:
         raise MoeError("fp4_linear_rows does not support this matrix")
     return torch.empty(n, dtype=_u8, device=w.device)
@@ -393,14 +422,15 @@ def fp4_linear_rows(x, w: Fp4Matrix, bias=None, dtype=torch.bfloat16, out=None, 
                     stream=None):
     """:func:`fp4_linear` of x [tokens, cols] of bfloat16, float16 or float32,
     quantised in w's format."""
-    index = _index(x, "x")
+    index = _of(w, "w")
     on = _on(stream, index)
-    _matrix(w, "w", index)
-    rows = _rows(x, "x", index)
-    T = x.shape[0]
-    if x.shape[1] != w.cols:
+    at, stride, kind = _rows(x, "x", index)
+    T, cols = x.shape
+    if cols != w.cols:
         raise MoeError(f"x must be [tokens, {w.cols}], got {list(x.shape)}")
-    out = _result(T, w, dtype, out, stream)
+    shape = (T, w.rows)
+    if out is None:
+        out = _result(shape, dtype, w.device, stream)
     if workspace is None:
         with _elsewhere(stream):
             workspace = fp4_linear_rows_workspace(w, T)
@@ -408,10 +438,10 @@ def fp4_linear_rows(x, w: Fp4Matrix, bias=None, dtype=torch.bfloat16, out=None, 
         size = workspace.shape[-1]
     except (AttributeError, IndexError):
         raise MoeError("workspace must be a tensor with a shape") from None
-    rc = (_LIB or load()).fp4_linear_rows(rows, T, w.ref, _array(bias, "bias", (w.rows,), _f32, index),
-                                          _rows(out, "out", index, (T, w.rows)),
-                                          _array(workspace, "workspace", (size,), _u8, index), size,
-                                          _status(dev_status, index), on)
+    rc = (_LIB or load()).fp4_linear_rows(
+        at, stride, kind, T, w.at, None if bias is None else _array(bias, "bias", (w.rows,), _f32, index),
+        *_rows(out, "out", index, shape), _array(workspace, "workspace", (size,), _u8, index), size,
+        None if dev_status is None else _array(dev_status, "dev_status", (1,), _i32, index), on)
     if rc:
         _check(rc, "fp4_linear_rows")
     return out

@@ -27,17 +27,10 @@
 extern "C" {
 #endif
 
-/* Element types of rows. */
+/* Element types of rows.  Element c of row r of an argument x is x[r * x_stride
+ * + c]; rows are 16-B aligned, and a stride (which plays no part for a single row) is a
+ * multiple of 16 bytes and at least a row's length, unless it is said otherwise. */
 enum { FP4_BF16 = 0, FP4_FP16 = 1, FP4_FP32 = 2 };
-
-/* Rows of elements: element c of row r is data[r * stride + c].  Data is 16-B
- * aligned, and a stride (which plays no part for a single row) a multiple of 16 bytes
- * and at least a row's length. */
-typedef struct {
-  void* data;
-  long long stride;
-  int32_t type;
-} fp4_rows;
 
 /* A matrix in FP4.
  * codes [rows x cols / 2]: e2m1, two to a byte, the even column in the low
@@ -76,30 +69,31 @@ int fp4_tile_scales(const uint8_t* scales, int rows, int cols, int format, uint8
  *   gets s = NaN (byte 255) and codes of 0.
  * Round to nearest, ties to even; nothing saturates.  The rules of
  * fp4_pack_expert, but for the row's power of two. */
-int fp4_quantize(const fp4_rows* x, const fp4_matrix* out, void* stream);
+int fp4_quantize(const void* x, long long x_stride, int x_type, const fp4_matrix* out, void* stream);
 
 /* The values of m's elements, rounded once to out's type (in BF16 that changes
  * nothing in what fp4_quantize made, but for magnitudes below 2^-126). */
-int fp4_dequantize(const fp4_matrix* m, const fp4_rows* out, void* stream);
+int fp4_dequantize(const fp4_matrix* m, void* out, long long out_stride, int out_type, void* stream);
 
 /* a = gate / (1 + exp(-gate)) * up, in FP32, for rows x cols elements.
  * out (BF16 or FP16) gets a rounded, m gets a quantised as by fp4_quantize;
  * either may be NULL, not both.  gate and up are of one type. */
-int fp4_swiglu(const fp4_rows* gate, const fp4_rows* up, int rows, int cols, const fp4_rows* out,
-               const fp4_matrix* m, void* stream);
+int fp4_swiglu(const void* gate, long long gate_stride, const void* up, long long up_stride, int type, int rows,
+               int cols, void* out, long long out_stride, int out_type, const fp4_matrix* m, void* stream);
 
 /* r' = r + scale * gate * N(y; post_weight),  h = N(r'; weight), with
  * N(x; w) = x / sqrt(mean(x^2) + eps) * w over a row, in FP32.
  * y NULL: r' = r.  post_weight NULL: y without a norm.  gate NULL: 1; gate_cols
- * = cols: an element for each element (stride 0: one row for all rows); gate_cols =
- * 1: an element for each row.  gate is of y's type.  weight NULL: 1.  Weights
+ * = cols: an element for each element (gate_stride 0: one row for all rows); gate_cols =
+ * 1: an element for each row, at any stride.  gate is of y's type.  weight NULL: 1.  Weights
  * are FP32 [cols], 16-B aligned.
  * r_out, of r's type, gets r' rounded (NULL: it is not kept; it may be r itself,
  * with r's stride).  h (BF16 or FP16) and m (FP4) get h, either may be NULL, not
  * both; they are made from r' before it is rounded. */
-int fp4_block_norm(const fp4_rows* r, const fp4_rows* y, const float* post_weight, const fp4_rows* gate,
-                   int gate_cols, double scale, const float* weight, double eps, int rows, int cols,
-                   const fp4_rows* r_out, const fp4_rows* h, const fp4_matrix* m, void* stream);
+int fp4_block_norm(const void* r, long long r_stride, int r_type, const void* y, long long y_stride, int y_type,
+                   const float* post_weight, const void* gate, long long gate_stride, int gate_cols, double scale,
+                   const float* weight, double eps, int rows, int cols, void* r_out, long long r_out_stride, void* h,
+                   long long h_stride, int h_type, const fp4_matrix* m, void* stream);
 
 /* y[t, n] = x.row_scale[t] * w.row_scale[n] * sum_k x[t, k] w[n, k] + bias[n],
  * for the x.rows rows of y and w.rows columns, rounded once to y's type (BF16,
@@ -111,7 +105,7 @@ int fp4_block_norm(const fp4_rows* r, const fp4_rows* y, const float* post_weigh
  * Results are bit-identical between repeated calls.
  * A wait that runs out sets MOE_DEV_TIMEOUT in dev_status (device int32 or NULL)
  * and makes the outputs that it was for NaN. */
-int fp4_linear(const fp4_matrix* x, const fp4_matrix* w, const float* bias, const fp4_rows* y,
+int fp4_linear(const fp4_matrix* x, const fp4_matrix* w, const float* bias, void* y, long long y_stride, int y_type,
                int32_t* dev_status, void* stream);
 
 /* Workspace bytes of fp4_linear_rows for up to `rows` rows of x; 0 where it is
@@ -120,8 +114,9 @@ int fp4_linear(const fp4_matrix* x, const fp4_matrix* w, const float* bias, cons
 size_t fp4_linear_rows_workspace(const fp4_matrix* w, int rows);
 
 /* fp4_linear of fp4_quantize(x) in w's format. */
-int fp4_linear_rows(const fp4_rows* x, int rows, const fp4_matrix* w, const float* bias, const fp4_rows* y,
-                    void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream);
+int fp4_linear_rows(const void* x, long long x_stride, int x_type, int rows, const fp4_matrix* w, const float* bias,
+                    void* y, long long y_stride, int y_type, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                    void* stream);
 
 #ifdef __cplusplus
 }
