@@ -22,39 +22,34 @@ constexpr float kNaN = __builtin_nanf("");
 // 2^(bits of the exponent field), field from 1 to 254.
 __device__ __forceinline__ float power_field(int field) { return __uint_as_float((uint32_t)field << 23); }
 
-// 8 elements as they lie in memory (plain loads: a residual may be overwritten in place).
-template <bool WIDE>
-struct Raw;
-template <>
-struct Raw<false> {
+// 8 elements of a type as they lie in memory (plain loads: a residual may be overwritten
+// in place).
+template <int TYPE>
+struct Raw {
   uint4 q;
   __device__ __forceinline__ void load(const void* base, long long at) {
     q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
   }
   __device__ __forceinline__ void zero() { q = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ void floats(int type, float (&f)[8]) const {
+  __device__ __forceinline__ void floats(float (&f)[8]) const {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float2 v;
-      if (type == FP4_BF16) {
-        v = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
-      } else {
-        v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      }
+      const float2 v = TYPE == FP4_BF16 ? make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u))
+                                        : __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
       f[2 * i] = v.x, f[2 * i + 1] = v.y;
     }
   }
 };
 template <>
-struct Raw<true> {
+struct Raw<FP4_FP32> {
   float4 q[2];
   __device__ __forceinline__ void load(const void* base, long long at) {
     const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
     q[0] = p[0], q[1] = p[1];
   }
   __device__ __forceinline__ void zero() { q[0] = q[1] = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void floats(int, float (&f)[8]) const {
+  __device__ __forceinline__ void floats(float (&f)[8]) const {
     f[0] = q[0].x, f[1] = q[0].y, f[2] = q[0].z, f[3] = q[0].w;
     f[4] = q[1].x, f[5] = q[1].y, f[6] = q[1].z, f[7] = q[1].w;
   }
@@ -123,24 +118,35 @@ __device__ __forceinline__ float row_sum(float v, Slots& slots) {
 // zeros past the row's end.
 // ---------------------------------------------------------------------------
 
-template <int NB>
+// 1 / x within an ulp.
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The larger of |a|, |b|, |c|; NaN if there is one.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+template <int NB, bool NV>
 __device__ __forceinline__ void to_fp4(const fp4_matrix& m, const Place& p, float (&v)[NB][8], Slots& slots) {
-  const bool nv = m.format == MOE_FMT_NVFP4;
   // The largest magnitudes as bit patterns: in that order infinities and NaN are
   // above all numbers.
   uint32_t top[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
-    uint32_t a = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
-    a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-    if (!nv) a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-    top[j] = a;
+    const float a = max_abs(v[j][0], v[j][1], v[j][2]), b = max_abs(v[j][3], v[j][4], v[j][5]);
+    uint32_t t = __float_as_uint(max_abs(max_abs(v[j][6], v[j][7], a), b, 0.f));
+    t = max(t, __shfl_xor_sync(0xffffffffu, t, 1));
+    if (!NV) t = max(t, __shfl_xor_sync(0xffffffffu, t, 2));
+    top[j] = t;
   }
-  float down = 1.f;  // 2^-E
+  float up = 1.f, down = 1.f;  // 2^E, 2^-E
   bool bad = false;
-  if (nv) {
+  if (NV) {
     uint32_t a = top[0];
 #pragma unroll
     for (int j = 1; j < NB; ++j) a = max(a, top[j]);
@@ -148,63 +154,69 @@ __device__ __forceinline__ void to_fp4(const fp4_matrix& m, const Place& p, floa
     bad = a >= 0x7F800000u;
     // a = f * 2^e: 2688 = 1.3125 * 2^11
     const int e = max(-126, (int)(a >> 23) - 127 - 11 + ((a & 0x7FFFFFu) > 0x280000u));
-    down = bad ? 0.f : power_field(127 - e);
-    if (p.t == 0 && p.live) m.row_scale[p.row] = bad ? kNaN : power_field(127 + e);
+    up = power_field(127 + e), down = power_field(127 - e);
+    if (p.t == 0 && p.live) m.row_scale[p.row] = bad ? kNaN : up;
+    if (e < -110) {  // 2^-E / s below would not be finite: such a row is scaled first
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        top[j] = __float_as_uint(__uint_as_float(top[j]) * down);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j][i] *= down;
+      }
+      up = down = 1.f;
+    }
   } else if (m.row_scale && p.t == 0 && p.live) {
     m.row_scale[p.row] = 1.f;
   }
-  const int tiles = fp4::scale_tiles(m.cols, m.format);
+  const int tiles = fp4::scale_tiles(m.cols, NV ? MOE_FMT_NVFP4 : MOE_FMT_MXFP4);
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
     uint32_t scale, word = 0;
     float q[8];
-    if (nv) {
-      scale = moe::f32_to_e4m3_rn_sat(__fdiv_rn(__uint_as_float(top[j]) * down, 6.f));
-      if (bad) scale = 0;
+    if (NV) {
+      // Quotients by Markstein's theorem: from a correctly rounded reciprocal and a
+      // quotient within an ulp, one residual gives the correctly rounded quotient (ties
+      // of e2m1 included), at a third of the cost of divisions.
+      const float a = __uint_as_float(top[j]) * down, sixth = 1.f / 6.f, b = a * sixth;
+      scale = bad ? 0u : moe::f32_to_e4m3_rn_sat(fmaf(fmaf(-6.f, b, a), sixth, b));
       const float s = moe::e4m3x2_to_f32x2(scale).x;
-      if (scale) {
-        // x / s by Markstein's theorem: from a correctly rounded reciprocal and a
-        // quotient within an ulp, one residual gives the correctly rounded quotient
-        // (ties of e2m1 included), at half the cost of eight divisions.  With the
-        // signs as they are, a zero keeps its own.
-        const float inv = __frcp_rn(s);
-        const float2 inv2 = make_float2(-inv, -inv), s2 = make_float2(s, s), none = make_float2(-0.f, -0.f);
-        const float2 d2 = make_float2(-down, -down);
+      // 1 / s of a number of four bits: one step of Newton's method rounds it correctly
+      const float y0 = reciprocal(s), y = fmaf(fmaf(-s, y0, 1.f), y0, y0);
+      // with the signs as they are (r = s q + (-x), q - r / s), a zero keeps its own
+      const float2 inv = make_float2(y * down, y * down), minus = make_float2(-inv.x, -inv.x);
+      const float2 s2 = make_float2(s * up, s * up), none = make_float2(-0.f, -0.f);
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const float2 x = moe::ffma2(make_float2(v[j][i], v[j][i + 1]), d2, none);  // -x 2^-E
-          const float2 q0 = moe::ffma2(x, inv2, none);
-          const float2 y = moe::ffma2(moe::ffma2(q0, s2, x), inv2, q0);
-          q[i] = y.x, q[i + 1] = y.y;
-        }
+      for (int i = 0; i < 8; i += 2) {
+        const float2 x = make_float2(v[j][i], v[j][i + 1]), q0 = moe::ffma2(x, inv, none);
+        const float2 r = moe::ffma2(q0, s2, make_float2(-x.x, -x.y));
+        const float2 z = moe::ffma2(r, minus, q0);
+        q[i] = z.x, q[i + 1] = z.y;
       }
     } else {
       const uint32_t a = top[j];
       // 6 = 1.5 * 2^2
-      scale = a >= 0x7F800000u ? 255u : (uint32_t)max(0, (int)(a >> 23) - 2 + ((a & 0x7FFFFFu) > 0x400000u));
-      if (scale != 255u) {
-        const float mult = power_field(254 - (int)scale);
+      bad = a >= 0x7F800000u;
+      scale = bad ? 255u : (uint32_t)max(0, (int)(a >> 23) - 2 + ((a & 0x7FFFFFu) > 0x400000u));
+      const float mult = power_field(254 - (int)min(scale, 253u));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = v[j][i] * mult;
-      }
+      for (int i = 0; i < 8; ++i) q[i] = v[j][i] * mult;
     }
-    if (nv ? scale != 0u : scale != 255u) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) word |= moe::f32x2_to_e2m1x2(q[2 * i], q[2 * i + 1]) << (8 * i);
-    }
+    for (int i = 0; i < 4; ++i) word |= moe::f32x2_to_e2m1x2(q[2 * i], q[2 * i + 1]) << (8 * i);
+    if (NV ? scale == 0u : bad) word = 0;
     const int lane = p.t & 31;
     const bool in = p.in(j);
     if (!in) scale = 0;
     // four scales into one word: of lanes 0, 2, 4, 6 (mod 8), or 0, 4, 8, 12 (mod 16)
-    uint32_t four = scale << (8 * ((nv ? lane >> 1 : lane >> 2) & 3));
-    const int step = nv ? 2 : 4;
-    four |= __shfl_xor_sync(0xffffffffu, four, step);
-    four |= __shfl_xor_sync(0xffffffffu, four, 2 * step);
+    uint32_t four = scale << (8 * ((NV ? lane >> 1 : lane >> 2) & 3));
+    constexpr int kStep = NV ? 2 : 4;
+    four |= __shfl_xor_sync(0xffffffffu, four, kStep);
+    four |= __shfl_xor_sync(0xffffffffu, four, 2 * kStep);
     if (in) {
       *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(m.codes) + ((size_t)p.row * m.cols + p.col(j)) / 2) = word;
-      if ((lane & (4 * step - 1)) == 0)
+      if ((lane & (4 * kStep - 1)) == 0)
         *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(m.scales) +
-                                     fp4::scale_word(p.row, p.col(j) / (8 * 4 * step), tiles)) = four;
+                                     fp4::scale_word(p.row, p.col(j) / (8 * 4 * kStep), tiles)) = four;
     }
   }
 }
@@ -218,13 +230,13 @@ struct QuantizeArgs {
   fp4_matrix m;
 };
 
-template <int NB, bool WIDE>
-__global__ void __launch_bounds__(256 * NB) quantize_kernel(const __grid_constant__ QuantizeArgs a) {
+template <int NB, int TYPE, bool NV>
+__global__ void __launch_bounds__(NB == 1 ? 256 : 1024) quantize_kernel(const __grid_constant__ QuantizeArgs a) {
   __shared__ Slots slots;
   const Place p(a.m.rows, a.m.cols);
   moe::pdl_wait();
   moe::pdl_launch_dependents();
-  Raw<WIDE> raw[NB];
+  Raw<TYPE> raw[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
     if (p.in(j)) raw[j].load(a.x.data, p.row * a.x.stride + p.col(j));
@@ -232,8 +244,8 @@ __global__ void __launch_bounds__(256 * NB) quantize_kernel(const __grid_constan
   }
   float v[NB][8];
 #pragma unroll
-  for (int j = 0; j < NB; ++j) raw[j].floats(a.x.type, v[j]);
-  to_fp4<NB>(a.m, p, v, slots);
+  for (int j = 0; j < NB; ++j) raw[j].floats(v[j]);
+  to_fp4<NB, NV>(a.m, p, v, slots);
 }
 
 struct SwigluArgs {
@@ -242,13 +254,13 @@ struct SwigluArgs {
   int rows, cols;
 };
 
-template <int NB, bool WIDE>
-__global__ void __launch_bounds__(256 * NB) swiglu_kernel(const __grid_constant__ SwigluArgs a) {
+template <int NB, int TYPE>
+__global__ void __launch_bounds__(NB == 1 ? 256 : 1024) swiglu_kernel(const __grid_constant__ SwigluArgs a) {
   __shared__ Slots slots;
   const Place p(a.rows, a.cols);
   moe::pdl_wait();
   moe::pdl_launch_dependents();
-  Raw<WIDE> g[NB], u[NB];
+  Raw<TYPE> g[NB], u[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
     if (p.in(j)) {
@@ -262,13 +274,15 @@ __global__ void __launch_bounds__(256 * NB) swiglu_kernel(const __grid_constant_
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
     float up[8];
-    g[j].floats(a.gate.type, v[j]);
-    u[j].floats(a.gate.type, up);
+    g[j].floats(v[j]);
+    u[j].floats(up);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[j][i] = v[j][i] / (1.f + __expf(-v[j][i])) * up[i];
+    for (int i = 0; i < 8; ++i) v[j][i] = v[j][i] * reciprocal(1.f + __expf(-v[j][i])) * up[i];
     if (a.out.data && p.in(j)) store8(a.out.data, p.row * a.out.stride + p.col(j), a.out.type, v[j]);
   }
-  if (a.m.codes) to_fp4<NB>(a.m, p, v, slots);
+  if (!a.m.codes) return;
+  if (a.m.format == MOE_FMT_NVFP4) to_fp4<NB, true>(a.m, p, v, slots);
+  else to_fp4<NB, false>(a.m, p, v, slots);
 }
 
 struct NormArgs {
@@ -291,15 +305,15 @@ __device__ __forceinline__ float one_element(const fp4::Rows& x, long long at) {
   return x.type == FP4_BF16 ? __uint_as_float((uint32_t)b << 16) : __half2float(__ushort_as_half(b));
 }
 
-template <int NB, bool R_WIDE, bool Y_WIDE>
-__global__ void __launch_bounds__(256 * NB) norm_kernel(const __grid_constant__ NormArgs a) {
+template <int NB, int R_TYPE, int Y_TYPE>
+__global__ void __launch_bounds__(NB == 1 ? 256 : 1024) norm_kernel(const __grid_constant__ NormArgs a) {
   __shared__ Slots slots[3];
   const Place p(a.rows, a.cols);
   const float per = 1.f / (float)a.cols;
   moe::pdl_wait();
   moe::pdl_launch_dependents();
-  Raw<R_WIDE> r[NB];
-  Raw<Y_WIDE> y[NB];
+  Raw<R_TYPE> r[NB];
+  Raw<Y_TYPE> y[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
     if (p.in(j)) r[j].load(a.r.data, p.row * a.r.stride + p.col(j));
@@ -312,7 +326,7 @@ __global__ void __launch_bounds__(256 * NB) norm_kernel(const __grid_constant__ 
   if (a.y.data) {
     if (a.gate.data && a.gate_cols == 1 && p.live) factor *= one_element(a.gate, p.row * a.gate.stride);
 #pragma unroll
-    for (int j = 0; j < NB; ++j) y[j].floats(a.y.type, v[j]);
+    for (int j = 0; j < NB; ++j) y[j].floats(v[j]);
     if (a.post_weight) {
       float sum = 0.f;
 #pragma unroll
@@ -334,13 +348,13 @@ __global__ void __launch_bounds__(256 * NB) norm_kernel(const __grid_constant__ 
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
     float x[8];
-    r[j].floats(a.r.type, x);
+    r[j].floats(x);
     if (a.y.data) {
       float g[8];
       if (a.gate.data && a.gate_cols != 1 && p.in(j)) {
-        Raw<Y_WIDE> raw;
+        Raw<Y_TYPE> raw;
         raw.load(a.gate.data, p.row * a.gate.stride + p.col(j));
-        raw.floats(a.gate.type, g);
+        raw.floats(g);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[i] = 1.f;
@@ -348,7 +362,7 @@ __global__ void __launch_bounds__(256 * NB) norm_kernel(const __grid_constant__ 
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = fmaf(factor * g[i], v[j][i], x[i]);
     }
-    if (a.r_out.data && p.in(j)) store8(a.r_out.data, p.row * a.r_out.stride + p.col(j), a.r_out.type, x);
+    if (a.r_out.data && p.in(j)) store8(a.r_out.data, p.row * a.r_out.stride + p.col(j), R_TYPE, x);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       v[j][i] = x[i];
@@ -370,7 +384,9 @@ __global__ void __launch_bounds__(256 * NB) norm_kernel(const __grid_constant__ 
     }
     if (a.h.data) store8(a.h.data, p.row * a.h.stride + p.col(j), a.h.type, v[j]);
   }
-  if (a.m.codes) to_fp4<NB>(a.m, p, v, slots[2]);
+  if (!a.m.codes) return;
+  if (a.m.format == MOE_FMT_NVFP4) to_fp4<NB, true>(a.m, p, v, slots[2]);
+  else to_fp4<NB, false>(a.m, p, v, slots[2]);
 }
 
 // A thread to 8 columns of a row.
@@ -431,7 +447,7 @@ struct Shape {
   int nb;
   dim3 grid, block;
   Shape(int rows, int cols) {
-    nb = cols <= 2048 ? 1 : cols <= 8192 ? 2 : 4;
+    nb = cols <= 2048 ? 1 : cols <= 16384 ? 2 : 4;
     const int threads = (cols + 8 * nb * 32 - 1) / (8 * nb * 32) * 32;
     const int per = threads >= 256 ? 1 : threads == 32 ? 8 : 256 / threads;
     block = dim3(threads, per);
@@ -445,8 +461,10 @@ int by_units(int nb, F f) {
                                                                  : f(std::integral_constant<int, 4>());
 }
 template <class F>
-int by_width(int type, F f) {
-  return type == FP4_FP32 ? f(std::true_type()) : f(std::false_type());
+int by_type(int type, F f) {
+  return type == FP4_BF16   ? f(std::integral_constant<int, FP4_BF16>())
+         : type == FP4_FP16 ? f(std::integral_constant<int, FP4_FP16>())
+                            : f(std::integral_constant<int, FP4_FP32>());
 }
 
 // The stride of a single row is of no account.
@@ -484,8 +502,9 @@ int fp4_quantize(const void* x, long long x_stride, int x_type, const fp4_matrix
   one_row(a.x, out->rows);
   const Shape s(out->rows, out->cols);
   return by_units(s.nb, [&](auto nb) {
-    return by_width(x_type, [&](auto wide) {
-      return moe::launch_pdl(quantize_kernel<nb, wide>, s.grid, s.block, 0, (cudaStream_t)stream, a);
+    return by_type(x_type, [&](auto type) {
+      return moe::launch_pdl(out->format == MOE_FMT_NVFP4 ? quantize_kernel<nb, type, true> : quantize_kernel<nb, type, false>,
+                             s.grid, s.block, 0, (cudaStream_t)stream, a);
     });
   });
 }
@@ -517,8 +536,8 @@ int fp4_swiglu(const void* gate, long long gate_stride, const void* up, long lon
   one_row(a.gate, rows), one_row(a.up, rows), one_row(a.out, rows);
   const Shape s(rows, cols);
   return by_units(s.nb, [&](auto nb) {
-    return by_width(type, [&](auto wide) {
-      return moe::launch_pdl(swiglu_kernel<nb, wide>, s.grid, s.block, 0, (cudaStream_t)stream, a);
+    return by_type(type, [&](auto t) {
+      return moe::launch_pdl(swiglu_kernel<nb, t>, s.grid, s.block, 0, (cudaStream_t)stream, a);
     });
   });
 }
@@ -558,9 +577,9 @@ int fp4_block_norm(const void* r, long long r_stride, int r_type, const void* y,
   for (fp4::Rows* x : {&a.r, &a.y, &a.gate, &a.r_out, &a.h}) one_row(*x, rows);
   const Shape s(rows, cols);
   return by_units(s.nb, [&](auto nb) {
-    return by_width(r_type, [&](auto rw) {
-      return by_width(y ? y_type : FP4_BF16, [&](auto yw) {
-        return moe::launch_pdl(norm_kernel<nb, rw, yw>, s.grid, s.block, 0, (cudaStream_t)stream, a);
+    return by_type(r_type, [&](auto rt) {
+      return by_type(y ? y_type : FP4_BF16, [&](auto yt) {
+        return moe::launch_pdl(norm_kernel<nb, rt, yt>, s.grid, s.block, 0, (cudaStream_t)stream, a);
       });
     });
   });

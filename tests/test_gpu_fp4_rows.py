@@ -69,6 +69,23 @@ def test_quantize_ties_and_extremes(format):
     same(fp4.fp4_quantize(x.to(BF), format), x.to(BF))
 
 
+@pytest.mark.parametrize("power", [0, 40, -100, -119, -126])
+def test_quantize_every_scale_and_tie(power):
+    """Blocks of each E4M3 scale, with every tie of e2m1 and its neighbours in FP32: what the
+    products that stand for quotients have to get right.  `power`: of the row."""
+    ties = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], dtype=np.float32)
+    around = [np.nextafter(ties, np.float32(0)), ties, np.nextafter(ties, np.float32(9))]
+    for near in around:
+        x = np.zeros((1, 127, 16), dtype=np.float32)
+        for code in range(1, 127):
+            s = np.float32(O.E4M3[code])
+            x[0, code, 0], x[0, code, 1:8], x[0, code, 8:15] = 6 * s, near * s, -near * s
+        x[0, 0, 0] = 2688
+        x = np.ldexp(np.concatenate([x.reshape(1, -1), np.zeros((1, 16), np.float32)], 1), power).astype(np.float32)
+        rows = torch.from_numpy(x).cuda()
+        same(fp4.fp4_quantize(rows, NV), rows)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("format", [NV, MX])
 def test_quantize_not_finite(dtype, format):
