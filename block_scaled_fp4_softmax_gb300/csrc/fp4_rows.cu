@@ -118,11 +118,24 @@ __device__ __forceinline__ float row_sum(float v, Slots& slots) {
 // zeros past the row's end.
 // ---------------------------------------------------------------------------
 
-// 1 / x within an ulp.
+// 1 / x within an ulp, 0 where that is below 2^-126.
 __device__ __forceinline__ float reciprocal(float x) {
   float y;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// 8 floats -> a word of e2m1 codes, the first in the lowest nibble.
+__device__ __forceinline__ uint32_t to_e2m1x8(const float (&f)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+  return r;
 }
 // The larger of |a|, |b|, |c|; NaN if there is one.
 __device__ __forceinline__ float max_abs(float a, float b, float c) {
@@ -201,9 +214,7 @@ __device__ __forceinline__ void to_fp4(const fp4_matrix& m, const Place& p, floa
 #pragma unroll
       for (int i = 0; i < 8; ++i) q[i] = v[j][i] * mult;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) word |= moe::f32x2_to_e2m1x2(q[2 * i], q[2 * i + 1]) << (8 * i);
-    if (NV ? scale == 0u : bad) word = 0;
+    if (NV ? scale != 0u : !bad) word = to_e2m1x8(q);
     const int lane = p.t & 31;
     const bool in = p.in(j);
     if (!in) scale = 0;
@@ -231,7 +242,7 @@ struct QuantizeArgs {
 };
 
 template <int NB, int TYPE, bool NV>
-__global__ void __launch_bounds__(NB == 1 ? 256 : 1024) quantize_kernel(const __grid_constant__ QuantizeArgs a) {
+__global__ void __launch_bounds__(NB <= 2 ? 256 : 512) quantize_kernel(const __grid_constant__ QuantizeArgs a) {
   __shared__ Slots slots;
   const Place p(a.m.rows, a.m.cols);
   moe::pdl_wait();
@@ -255,7 +266,7 @@ struct SwigluArgs {
 };
 
 template <int NB, int TYPE>
-__global__ void __launch_bounds__(NB == 1 ? 256 : 1024) swiglu_kernel(const __grid_constant__ SwigluArgs a) {
+__global__ void __launch_bounds__(NB <= 2 ? 256 : 512) swiglu_kernel(const __grid_constant__ SwigluArgs a) {
   __shared__ Slots slots;
   const Place p(a.rows, a.cols);
   moe::pdl_wait();
@@ -306,7 +317,7 @@ __device__ __forceinline__ float one_element(const fp4::Rows& x, long long at) {
 }
 
 template <int NB, int R_TYPE, int Y_TYPE>
-__global__ void __launch_bounds__(NB == 1 ? 256 : 1024) norm_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(256 * NB) norm_kernel(const __grid_constant__ NormArgs a) {
   __shared__ Slots slots[3];
   const Place p(a.rows, a.cols);
   const float per = 1.f / (float)a.cols;
@@ -389,33 +400,48 @@ __global__ void __launch_bounds__(NB == 1 ? 256 : 1024) norm_kernel(const __grid
   else to_fp4<NB, false>(a.m, p, v, slots[2]);
 }
 
-// A thread to 8 columns of a row.
 struct DequantizeArgs {
   fp4_matrix m;
   fp4::Rows out;
 };
 
-__global__ void __launch_bounds__(256) dequantize_kernel(const __grid_constant__ DequantizeArgs a) {
+template <int NB, int TYPE, bool NV>
+__global__ void __launch_bounds__(NB <= 2 ? 256 : 512) dequantize_kernel(const __grid_constant__ DequantizeArgs a) {
   const Place p(a.m.rows, a.m.cols);
   moe::pdl_wait();
   moe::pdl_launch_dependents();
-  const int tiles = fp4::scale_tiles(a.m.cols, a.m.format), block = fp4::block_of(a.m.format);
+  const int tiles = fp4::scale_tiles(p.cols, NV ? MOE_FMT_NVFP4 : MOE_FMT_MXFP4);
+  const uint32_t* codes = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m.codes) + (size_t)p.row * p.cols / 2);
+  const uint8_t* scales = static_cast<const uint8_t*>(a.m.scales) + fp4::scale_word(p.row, 0, tiles);
   const float row = p.live && a.m.row_scale ? __ldg(a.m.row_scale + p.row) : 1.f;
-  for (int col = p.col(0); p.live && col < p.cols; col += 8 * p.threads) {
-    const uint32_t codes = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m.codes) +
-                                                                   ((size_t)p.row * p.cols + col) / 2));
-    const int b = col / block;
-    const uint32_t s = __ldg(static_cast<const uint8_t*>(a.m.scales) + fp4::scale_word(p.row, b >> 2, tiles) + (b & 3));
-    const float scale = a.m.format == MOE_FMT_NVFP4 ? moe::e4m3x2_to_f32x2(s).x : moe::ue8m0_to_f32(s);
+  uint32_t c[NB], b[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    if (!p.in(j)) continue;
+    const int block = p.col(j) / (NV ? 16 : 32);
+    c[j] = __ldg(codes + p.col(j) / 8);
+    b[j] = __ldg(scales + (size_t)(block >> 2) * 512 + (block & 3));
+  }
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    if (!p.in(j)) continue;
+    // code * block scale is exact: at most 2 + 4 significant bits, of NVFP4 within FP16
+    // too; a power of two times the row's scale is
+    uint32_t s2 = 0;
+    if (NV) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"((uint16_t)(b[j] | b[j] << 8)));
+    const float factor = NV ? row : moe::ue8m0_to_f32(b[j]) * row;
     float f[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t h2 = moe::e2m1x2_to_f16x2((codes >> (8 * i)) & 0xFFu);
-      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-      // code * block scale is exact: at most 2 + 4 significant bits
-      f[2 * i] = v.x * scale * row, f[2 * i + 1] = v.y * scale * row;
+      uint32_t h = moe::e2m1x2_to_f16x2(c[j] >> (8 * i));
+      if (NV) {
+        const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&s2));
+        h = *reinterpret_cast<const uint32_t*>(&v);
+      }
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      f[2 * i] = v.x * factor, f[2 * i + 1] = v.y * factor;
     }
-    store8(a.out.data, p.row * a.out.stride + col, a.out.type, f);
+    store8(a.out.data, p.row * a.out.stride + p.col(j), TYPE, f);
   }
 }
 
@@ -441,25 +467,41 @@ __global__ void __launch_bounds__(256) tile_scales_kernel(const uint8_t* __restr
 // Launches
 // ---------------------------------------------------------------------------
 
-// Units of a thread by the row's length, and the block's shape: one row, or
-// several short ones.
+// Units of a thread, and the block's shape: one row, or several short ones.
 struct Shape {
   int nb;
   dim3 grid, block;
-  Shape(int rows, int cols) {
-    nb = cols <= 2048 ? 1 : cols <= 16384 ? 2 : 4;
+  void set(int rows, int cols, int units) {
+    nb = units;
     const int threads = (cols + 8 * nb * 32 - 1) / (8 * nb * 32) * 32;
     const int per = threads >= 256 ? 1 : threads == 32 ? 8 : 256 / threads;
     block = dim3(threads, per);
     grid = dim3((rows + per - 1) / per);
   }
 };
-
+// Of kernels that hold a row or two in registers: with many rows 4 units of a thread,
+// as what is done once for a row (its reduction, its exponent) is some 50 instructions of
+// every thread; with few of them as many threads as there may be.
+struct LightShape : Shape {
+  LightShape(int rows, int cols) { set(rows, cols, cols > 16384 ? 8 : cols > 4096 || (rows >= 1024 && cols >= 1024) ? 4 : cols > 2048 ? 2 : 1); }
+};
 template <class F>
-int by_units(int nb, F f) {
-  return nb == 1 ? f(std::integral_constant<int, 1>()) : nb == 2 ? f(std::integral_constant<int, 2>())
-                                                                 : f(std::integral_constant<int, 4>());
+int by_units(const LightShape& s, F f) {
+  return s.nb == 1   ? f(std::integral_constant<int, 1>())
+         : s.nb == 2 ? f(std::integral_constant<int, 2>())
+         : s.nb == 4 ? f(std::integral_constant<int, 4>())
+                     : f(std::integral_constant<int, 8>());
 }
+// Of the norm's, whose threads hold four operands of each unit.
+struct HeavyShape : Shape {
+  HeavyShape(int rows, int cols) { set(rows, cols, cols <= 2048 ? 1 : cols <= 8192 ? 2 : 4); }
+};
+template <class F>
+int by_units(const HeavyShape& s, F f) {
+  return s.nb == 1 ? f(std::integral_constant<int, 1>()) : s.nb == 2 ? f(std::integral_constant<int, 2>())
+                                                                   : f(std::integral_constant<int, 4>());
+}
+
 template <class F>
 int by_type(int type, F f) {
   return type == FP4_BF16   ? f(std::integral_constant<int, FP4_BF16>())
@@ -500,8 +542,8 @@ int fp4_quantize(const void* x, long long x_stride, int x_type, const fp4_matrix
   if (const int rc = fp4::check_rows(a.x, out->rows, out->cols, true)) return rc;
   if (out->rows == 0) return MOE_OK;
   one_row(a.x, out->rows);
-  const Shape s(out->rows, out->cols);
-  return by_units(s.nb, [&](auto nb) {
+  const LightShape s(out->rows, out->cols);
+  return by_units(s, [&](auto nb) {
     return by_type(x_type, [&](auto type) {
       return moe::launch_pdl(out->format == MOE_FMT_NVFP4 ? quantize_kernel<nb, type, true> : quantize_kernel<nb, type, false>,
                              s.grid, s.block, 0, (cudaStream_t)stream, a);
@@ -515,9 +557,14 @@ int fp4_dequantize(const fp4_matrix* m, void* out, long long out_stride, int out
   if (const int rc = fp4::check_rows(a.out, m->rows, m->cols, true)) return rc;
   if (m->rows == 0) return MOE_OK;
   one_row(a.out, m->rows);
-  const int threads = m->cols >= 2048 ? 256 : (m->cols + 255) / 256 * 32, per = 256 / threads;
-  return moe::launch_pdl(dequantize_kernel, dim3((m->rows + per - 1) / per), dim3(threads, per), 0,
-                         (cudaStream_t)stream, a);
+  const LightShape s(m->rows, m->cols);
+  return by_units(s, [&](auto nb) {
+    return by_type(out_type, [&](auto type) {
+      return moe::launch_pdl(
+          m->format == MOE_FMT_NVFP4 ? dequantize_kernel<nb, type, true> : dequantize_kernel<nb, type, false>, s.grid,
+          s.block, 0, (cudaStream_t)stream, a);
+    });
+  });
 }
 
 int fp4_swiglu(const void* gate, long long gate_stride, const void* up, long long up_stride, int type, int rows,
@@ -534,8 +581,8 @@ int fp4_swiglu(const void* gate, long long gate_stride, const void* up, long lon
     if (const int rc = fp4::check_target(m, rows, cols)) return rc;
   if (rows == 0) return MOE_OK;
   one_row(a.gate, rows), one_row(a.up, rows), one_row(a.out, rows);
-  const Shape s(rows, cols);
-  return by_units(s.nb, [&](auto nb) {
+  const LightShape s(rows, cols);
+  return by_units(s, [&](auto nb) {
     return by_type(type, [&](auto t) {
       return moe::launch_pdl(swiglu_kernel<nb, t>, s.grid, s.block, 0, (cudaStream_t)stream, a);
     });
@@ -575,8 +622,8 @@ int fp4_block_norm(const void* r, long long r_stride, int r_type, const void* y,
     if (const int rc = fp4::check_target(m, rows, cols)) return rc;
   if (rows == 0) return MOE_OK;
   for (fp4::Rows* x : {&a.r, &a.y, &a.gate, &a.r_out, &a.h}) one_row(*x, rows);
-  const Shape s(rows, cols);
-  return by_units(s.nb, [&](auto nb) {
+  const HeavyShape s(rows, cols);
+  return by_units(s, [&](auto nb) {
     return by_type(r_type, [&](auto rt) {
       return by_type(y ? y_type : FP4_BF16, [&](auto yt) {
         return moe::launch_pdl(norm_kernel<nb, rt, yt>, s.grid, s.block, 0, (cudaStream_t)stream, a);
