@@ -8,11 +8,17 @@
 // the tensor core wants them, 512 bytes for 128 rows x 4 blocks), from where
 // tcgen05.cp takes them to TMEM beside the sums.
 //
-// Few rows of x are bound by the weights' bytes: a tile's columns are split over a
-// cluster of CTAs, whose sums meet in distributed shared memory in a fixed order.
+// Few rows of x are bound by the weights' bytes.  A persistent CTA walks over tiles; its
+// ring runs on from tile to tile, and a tile's sums are written while the next one's are
+// made (two places in TMEM).  Where there are fewer tiles than SMs, a tile's columns are split
+// over a cluster of CTAs, whose sums meet in distributed shared memory in a fixed order.
+//
+// Up to 16 rows of x stay in shared memory for all tiles (HELD), if they fit.  Of a few
+// elements in all, each CTA quantises them itself, which saves a launch.
 #include <math.h>
 
 #include "fp4_mma.cuh"
+#include "fp4_quantize.cuh"
 
 using namespace moe::tc;
 using namespace fp4;
@@ -21,65 +27,121 @@ namespace {
 
 constexpr int kThreads = 192;  // warps 0-3: epilogue; 4: copies; 5: MMA
 constexpr int kTmaWarp = 4, kMmaWarp = 5;
+constexpr int kMaxRaw = 32768;  // elements of x that every CTA quantises for itself
 
-template <int FMT, int BN_>
+template <int FMT, int BN_, bool HELD>
 struct Cfg {
   static constexpr int BN = BN_;                               // rows of x of a tile
   static constexpr bool NV = FMT == MOE_FMT_NVFP4;
   static constexpr int COPIES = NV ? 4 : 2;                    // tiles of scales of a chunk
   static constexpr int W_BYTES = 128 * 128, X_BYTES = BN * 128, S_BYTES = COPIES * 512;
-  static constexpr int SLOT = W_BYTES + X_BYTES + 2 * S_BYTES;
-  // two CTAs to an SM: one's loads run while the other starts or ends
-  static constexpr int SLOTS = (113 * 1024 - 3072) / SLOT;
+  static constexpr int X_PART = X_BYTES + S_BYTES;             // a chunk of x with its scales
+  static constexpr int SLOT = W_BYTES + S_BYTES + (HELD ? 0 : X_PART);
+  static constexpr int MOST = 10;                              // slots
   static constexpr int S_COLS = COPIES * 4;                    // TMEM columns of a chunk's scales, of either side
-  // TMEM holds the scales of as many chunks as the ring: where a slot's copies have
-  // landed, the products that took the scales before it have been made.
-  static constexpr int S_COL = BN <= 32 ? 32 : BN;             // first of them, behind the sums
-  static constexpr int TMEM = S_COL + SLOTS * 2 * S_COLS <= 128 ? 128 : 256;
-  static_assert(S_COL + SLOTS * 2 * S_COLS <= TMEM, "TMEM");
-  static_assert(SLOTS >= 3 && SLOTS * SLOT >= BN * 128 * 4, "ring");
+  // TMEM holds two tiles' sums, and the scales of as many chunks as the ring: where a
+  // slot's copies have landed, the products that took the scales before it have been made.
+  static constexpr int SUMS = BN <= 32 ? 32 : BN, S_COL = 2 * SUMS;
+  static_assert(SLOT % 1024 == 0 && X_PART % 1024 == 0, "the swizzle's alignment");
+  static constexpr int slots_of(int bytes) {
+    const int n = bytes / SLOT, m = (512 - S_COL) / (2 * S_COLS);
+    return n < m ? (n < MOST ? n : MOST) : (m < MOST ? m : MOST);
+  }
 };
 
 struct Control {
-  uint64_t full[8], empty[8], done, drain;
+  uint64_t full[10], empty[10], sums_full[2], sums_empty[2], x_full, drain;
   uint32_t tmem;
   int abort;
+  uint32_t row_top[4][16];
+  float row_scale[16];
 };
+constexpr int kRoom = 227 * 1024 - 1024 - (int)sizeof(Control);  // for the ring and the held rows
 
-template <class C>
-constexpr size_t smem_bytes(int slots) {
-  return 1024 + (size_t)slots * C::SLOT + sizeof(Control);
+// Quantises all of x for the CTA's chunks c0 .. c1 - 1, as fp4_quantize does, with the four
+// epilogue warps.
+template <int FMT, int TYPE>
+__device__ void hold_raw(const LinearArgs& a, Control& ctl, uint8_t* held, int part, int x_bytes, int c0, int c1) {
+  constexpr bool NV = FMT == MOE_FMT_NVFP4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto load = [&](int t, int col, float(&v)[8]) {
+    Raw<TYPE> raw;
+    if (col < a.cols) raw.load(a.raw.data, t * a.raw.stride + col);
+    else raw.zero();
+    raw.floats(v);
+  };
+  if (NV) {
+    for (int t = 0; t < a.t; ++t) {
+      uint32_t top = 0;
+#pragma unroll 4
+      for (int col = threadIdx.x * 8; col < a.cols; col += 128 * 8) {
+        float v[8];
+        load(t, col, v);
+        const float b = max_abs(max_abs(v[0], v[1], v[2]), max_abs(v[3], v[4], v[5]), max_abs(v[6], v[7], 0.f));
+        top = max(top, __float_as_uint(b));
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (lane == 0) ctl.row_top[warp][t] = top;
+    }
+    named_sync(1, 128);
+  }
+  for (int t = 0; t < a.t; ++t) {
+    RowScale scale;
+    if (NV) scale = row_scale(max(max(ctl.row_top[0][t], ctl.row_top[1][t]), max(ctl.row_top[2][t], ctl.row_top[3][t])));
+    if (threadIdx.x == 0) ctl.row_scale[t] = scale.value();
+    const int end = min(c1 * kChunk, (a.cols + 63) / 64 * 64);  // whole words of NVFP4's scales
+#pragma unroll 2
+    for (int first = c0 * kChunk; first < end; first += 128 * 8) {
+      const int col = first + threadIdx.x * 8;
+      float v[8];
+      load(t, col, v);
+      uint32_t top = block_top<NV>(v), word;
+      if (NV && scale.tiny) scale_first(scale, v, top);
+      const uint32_t four = quantize8<NV>(v, top, scale, lane, col < a.cols, word);
+      if (col >= c1 * kChunk) continue;
+      uint8_t* at = held + (size_t)(col / kChunk - c0) * part;
+      const int b = col % kChunk / 2;  // byte of the row's 128
+      *reinterpret_cast<uint32_t*>(at + t * 128 + (((b >> 4) ^ (t & 7)) << 4) + (b & 15)) = word;
+      if ((lane & (kScaleLanes<NV> - 1)) == 0)
+        *reinterpret_cast<uint32_t*>(at + x_bytes + col % kChunk / (8 * kScaleLanes<NV>) * 512 + t * 16) = four;
+    }
+  }
+  fence_proxy_async();
+  named_sync(1, 128);
 }
 
-// Grid: split * ceil(n / 128) * ceil(t / BN), in clusters of `split`.
-template <int FMT, int BN>
-__global__ void __launch_bounds__(kThreads, 2) linear_kernel(const __grid_constant__ LinearArgs a, int split,
-                                                            int slots) {
-  using C = Cfg<FMT, BN>;
+// Grid: min(SMs, tiles) CTAs, or split * tiles in clusters of `split`; tiles = ceil(n / 128)
+// * ceil(t / BN).
+template <int FMT, int BN, bool HELD>
+__global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ LinearArgs a, int split,
+                                                            int slots, int tmem_columns) {
+  using C = Cfg<FMT, BN, HELD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  Control& ctl = *reinterpret_cast<Control*>(ring + (size_t)slots * C::SLOT);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = split > 1 ? (int)cluster_rank() : 0;
-  const int t_tiles = (a.t + BN - 1) / BN, tile = blockIdx.x / split;
-  const int n0 = tile / t_tiles * 128, t0 = tile % t_tiles * BN;
+  const int t_tiles = (a.t + BN - 1) / BN, all = (a.n + 127) / 128 * t_tiles;
+  const int first = blockIdx.x / split, step = gridDim.x / split;
   const int chunks = (a.cols + kChunk - 1) / kChunk;
   const int c0 = chunks * rank / split, c1 = chunks * (rank + 1) / split;
-  const int tiles = fp4::scale_tiles(a.cols, FMT);
+  const int tiles = scale_tiles(a.cols, FMT);
+  uint8_t* held = ring + (size_t)slots * C::SLOT;
+  Control& ctl = *reinterpret_cast<Control*>(held + (HELD ? (size_t)(c1 - c0) * C::X_PART : 0));
+  auto n_of = [&](int tile) { return tile / t_tiles * 128; };
+  auto t_of = [&](int tile) { return tile % t_tiles * BN; };
 
-  auto load_w = [&](int slot, int c) {  // ... and announces all of the chunk's copies
+  // copies of a chunk of w; all of the slot's are announced
+  auto load_w = [&](int slot, int tile, int c) {
     const uint32_t at = smem_u32(ring + (size_t)slot * C::SLOT);
     const int kt = c * C::COPIES, bytes = min(C::COPIES, tiles - kt) * 512;
-    mbar_arrive_expect_tx(&ctl.full[slot], C::W_BYTES + C::X_BYTES + 2 * bytes);
-    load_codes(&a.w_map, at, &ctl.full[slot], c * (kChunk / 2), n0);
-    bulk_g2s(at + C::W_BYTES + C::X_BYTES, a.w_scales + ((size_t)(n0 >> 7) * tiles + kt) * 512, bytes, &ctl.full[slot]);
+    mbar_arrive_expect_tx(&ctl.full[slot], C::W_BYTES + bytes + (HELD ? 0 : C::X_BYTES + bytes));
+    load_codes(&a.w_map, at, &ctl.full[slot], c * (kChunk / 2), n_of(tile));
+    bulk_g2s(at + C::W_BYTES, a.w_scales + ((size_t)(n_of(tile) >> 7) * tiles + kt) * 512, bytes, &ctl.full[slot]);
   };
-  auto load_x = [&](int slot, int c) {
-    const uint32_t at = smem_u32(ring + (size_t)slot * C::SLOT);
+  auto load_x = [&](uint32_t at, uint64_t* bar, int tile, int c) {
     const int kt = c * C::COPIES, bytes = min(C::COPIES, tiles - kt) * 512;
-    load_codes(&a.x_map, at + C::W_BYTES, &ctl.full[slot], c * (kChunk / 2), t0);
-    bulk_g2s(at + C::W_BYTES + C::X_BYTES + C::S_BYTES, a.x_scales + ((size_t)(t0 >> 7) * tiles + kt) * 512, bytes,
-             &ctl.full[slot]);
+    load_codes(&a.x_map, at, bar, c * (kChunk / 2), t_of(tile));
+    bulk_g2s(at + C::X_BYTES, a.x_scales + ((size_t)(t_of(tile) >> 7) * tiles + kt) * 512, bytes, bar);
   };
   const int ahead = a.early ? min(slots, c1 - c0) : 0;  // chunks whose part of w does not wait
   if (threadIdx.x == 32 * kTmaWarp) {
@@ -87,18 +149,22 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(const __grid_consta
       mbar_init(&ctl.full[i], 1);
       mbar_init(&ctl.empty[i], 1);
     }
-    mbar_init(&ctl.done, 1 + a.extra);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.sums_full[i], 1 + a.extra);
+      mbar_init(&ctl.sums_empty[i], 4);
+    }
+    mbar_init(&ctl.x_full, 1);
     mbar_init(&ctl.drain, 1);
     ctl.abort = 0;
     mbar_fence_init();
     attn::prefetch_map(&a.w_map);
-    attn::prefetch_map(&a.x_map);
-    for (int i = 0; i < ahead; ++i) load_w(i, c0 + i);
+    if (!a.raw.data) attn::prefetch_map(&a.x_map);
+    for (int i = 0; i < ahead; ++i) load_w(i, first, c0 + i);
   }
   // TMEM is taken only when the kernel before has ended, and before the next one may
   // start: CTAs that wait for one another's kernels never hold what the others need.
   moe::pdl_wait();
-  if (warp == kMmaWarp) tmem_alloc(&ctl.tmem, C::TMEM);
+  if (warp == kMmaWarp) tmem_alloc(&ctl.tmem, tmem_columns);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
@@ -109,93 +175,137 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(const __grid_consta
   if (warp == kTmaWarp) {
     if (lane == 0) {
       bool alive = true;
-      int filled = 0;
-      for (int c = c0; c < c1; ++c, ++filled) {
-        const int slot = filled % slots;
-        alive = attn::bounded_wait(&ctl.empty[slot], ((filled / slots) & 1) ^ 1, a.wait_cycles, abort_flag, a.st);
-        if (!alive) break;
-        if (filled >= ahead) load_w(slot, c);
-        load_x(slot, c);
+      if (HELD && !a.raw.data) {
+        uint32_t bytes = 0;
+        for (int c = c0; c < c1; ++c) bytes += C::X_BYTES + min(C::COPIES, tiles - c * C::COPIES) * 512;
+        mbar_arrive_expect_tx(&ctl.x_full, bytes);
+        for (int c = c0; c < c1; ++c) load_x(smem_u32(held + (size_t)(c - c0) * C::X_PART), &ctl.x_full, first, c);
       }
+      int filled = 0, slot = 0;
+      uint32_t round = 1;
+      for (int tile = first; tile < all && alive; tile += step)
+        for (int c = c0; c < c1; ++c, ++filled) {
+          alive = attn::bounded_wait(&ctl.empty[slot], round, a.wait_cycles, abort_flag, a.st);
+          if (!alive) break;
+          if (filled >= ahead) load_w(slot, tile, c);
+          if (!HELD) load_x(smem_u32(ring + (size_t)slot * C::SLOT) + C::W_BYTES + C::S_BYTES, &ctl.full[slot], tile, c);
+          if (++slot == slots) slot = 0, round ^= 1;
+        }
       // every copy has landed before the CTA's shared memory goes away
       for (int i = max(0, filled - slots); i < filled; ++i)
         attn::bounded_wait(&ctl.full[i % slots], (i / slots) & 1, attn::kDrainCycles, nullptr, a.st);
+      if (HELD && !a.raw.data) attn::bounded_wait(&ctl.x_full, 0, attn::kDrainCycles, nullptr, a.st);
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // (the warp walks and waits as one, its elected lane issues; see fp4_linear_wide.cu)
     const bool leader = attn::elect_lane();
-    const uint64_t w_desc = sw128_kmajor_desc(smem_u32(ring)), x_desc = sw128_kmajor_desc(smem_u32(ring) + C::W_BYTES);
-    const uint64_t s_desc = scales_desc(smem_u32(ring) + C::W_BYTES + C::X_BYTES);
-    for (int c = c0, i = 0; c < c1; ++c, ++i) {
-      const int slot = i % slots;
-      const bool ok = attn::bounded_wait(&ctl.full[slot], (i / slots) & 1, a.wait_cycles, abort_flag, a.st);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      fence_after_sync();
-      const uint32_t off = (uint32_t)slot * (C::SLOT >> 4);
-      const uint32_t set = tmem + C::S_COL + slot * 2 * C::S_COLS;
-      const int steps = min(kChunk, a.cols - c * kChunk + 63) / 64;
-      if (leader) {
+    const uint64_t w_desc = sw128_kmajor_desc(smem_u32(ring)), ws_desc = scales_desc(smem_u32(ring) + C::W_BYTES);
+    const uint32_t x_at = HELD ? smem_u32(held) : smem_u32(ring) + C::W_BYTES + C::S_BYTES;
+    const uint64_t x_desc = sw128_kmajor_desc(x_at), xs_desc = scales_desc(x_at + C::X_BYTES);
+    bool alive = !HELD || __all_sync(0xffffffffu, attn::bounded_wait(&ctl.x_full, 0, a.wait_cycles, abort_flag, a.st));
+    int slot = 0, done = 0;
+    uint32_t round = 0;
+    for (int tile = first; tile < all && alive; tile += step, ++done) {
+      const int place = done & 1;
+      if (done >= 2)
+        alive = __all_sync(0xffffffffu, attn::bounded_wait(&ctl.sums_empty[place], ((done >> 1) - 1) & 1, a.wait_cycles,
+                                                           abort_flag, a.st));
+      for (int c = c0; c < c1 && alive; ++c) {
+        alive = __all_sync(0xffffffffu, attn::bounded_wait(&ctl.full[slot], round, a.wait_cycles, abort_flag, a.st));
+        if (!alive) break;
+        fence_after_sync();
+        if (leader) {
+          const uint32_t off = (uint32_t)slot * (C::SLOT >> 4);
+          const uint32_t x_off = HELD ? (uint32_t)(c - c0) * (C::X_PART >> 4) : off;
+          const uint32_t set = tmem + C::S_COL + slot * 2 * C::S_COLS, sums = tmem + place * C::SUMS;
+          const int steps = min(kChunk, a.cols - c * kChunk + 63) / 64;
 #pragma unroll
-        for (int k = 0; k < kChunk / 64; ++k) {
-          if (k >= steps) break;
-          const int copy = C::NV ? k : k / 2, id = C::NV ? 0 : 2 * (k & 1);
-          const uint32_t sw = set + 4 * copy, sx = sw + C::S_COLS;
-          if (id == 0) {
-            copy_scales<1>(sw, s_desc + off + copy * 32);
-            copy_scales<1>(sx, s_desc + off + (C::S_BYTES >> 4) + copy * 32);
+          for (int k = 0; k < kChunk / 64; ++k) {
+            if (k >= steps) break;
+            const int copy = C::NV ? k : k / 2, id = C::NV ? 0 : 2 * (k & 1);
+            const uint32_t sw = set + 4 * copy, sx = sw + C::S_COLS;
+            if (id == 0) {
+              copy_scales<1>(sw, ws_desc + off + copy * 32);
+              copy_scales<1>(sx, xs_desc + x_off + copy * 32);
+            }
+            mma_fp4<FMT, 1>(sums, w_desc + off + 2 * k, x_desc + x_off + 2 * k, idesc_fp4<FMT>(128, BN, id), sw, sx,
+                            c > c0 || k > 0);
           }
-          mma_fp4<FMT, 1>(tmem, w_desc + off + 2 * k, x_desc + off + 2 * k, idesc_fp4<FMT>(128, BN, id), sw, sx,
-                          i > 0 || k > 0);
+          mma_commit(&ctl.empty[slot]);
+          if (c == c1 - 1) mma_commit(&ctl.sums_full[place]);
         }
-        mma_commit(&ctl.empty[slot]);
+        __syncwarp();
+        if (++slot == slots) slot = 0, round ^= 1;
       }
-      __syncwarp();
     }
+    // TMEM and the ring go back only when every MMA has completed
     if (leader) {
-      mma_commit(&ctl.done);
-      // TMEM goes back only when every MMA has completed
       mma_commit(&ctl.drain);
       attn::bounded_wait(&ctl.drain, 0, attn::kDrainCycles, nullptr, a.st);
     }
     __syncwarp();
   } else {
-    attn::bounded_wait(&ctl.done, 0, a.wait_cycles, abort_flag, a.st);
-    __syncwarp();
-  }
-  __syncthreads();  // no copy is under way any more, and nobody gives up from here on
-  const bool ok = !*abort_flag;
-  if (warp < 4) {
-    fence_after_sync();
-    const uint32_t sums = tmem + ((uint32_t)(warp * 32) << 16);
-    const int n = n0 + threadIdx.x;
-    const float scale = a.w_row && n < a.n ? __ldg(a.w_row + n) : 1.f;
-    const float add = a.bias && n < a.n ? __ldg(a.bias + n) : 0.f;
-    auto put = [&](int j, float v) {
-      const int t = t0 + j;
-      if (n >= a.n || t >= a.t) return;
-      if (a.x_row) v *= __ldg(a.x_row + t);
-      store_one(a.y, t * a.y_stride + n, a.y_type, ok ? fmaf(v, scale, add) : kNaN);
-    };
-    float* part = reinterpret_cast<float*>(ring);  // [BN][128], where the chunks were
+    if (HELD && a.raw.data) {
+      if (a.raw.type == FP4_BF16) hold_raw<FMT, FP4_BF16>(a, ctl, held, C::X_PART, C::X_BYTES, c0, c1);
+      else if (a.raw.type == FP4_FP16) hold_raw<FMT, FP4_FP16>(a, ctl, held, C::X_PART, C::X_BYTES, c0, c1);
+      else hold_raw<FMT, FP4_FP32>(a, ctl, held, C::X_PART, C::X_BYTES, c0, c1);
+      if (threadIdx.x == 0) mbar_arrive(&ctl.x_full);
+    }
+    bool alive = true;
+    int done = 0;
+    for (int tile = first; tile < all; tile += step, ++done) {
+      const int place = done & 1, n = n_of(tile) + threadIdx.x, t0 = t_of(tile);
+      float scale = a.w_row && n < a.n ? __ldg(a.w_row + n) : 1.f;
+      const float add = a.bias && n < a.n ? __ldg(a.bias + n) : 0.f;
+      alive = alive && __all_sync(0xffffffffu, attn::bounded_wait(&ctl.sums_full[place], (done >> 1) & 1, a.wait_cycles,
+                                                                  abort_flag, a.st));
+      fence_after_sync();
+      if (split > 1) break;  // (of one tile; below)
+      if (!alive) scale = kNaN;
+      const uint32_t sums = tmem + place * C::SUMS + ((uint32_t)(warp * 32) << 16);
+      const int rows = min(BN, a.t - t0);
+      uint8_t* y = static_cast<uint8_t*>(a.y) + (t0 * a.y_stride + n) * element_bytes(a.y_type);
+      const long long next = a.y_stride * element_bytes(a.y_type);
 #pragma unroll 1
-    for (int j = 0; j < BN; j += 16) {
-      uint32_t r[16];
-      tmem_ld16(sums + j, r);
-      tmem_ld_wait();
+      for (int j = 0; j < rows; j += 16) {
+        uint32_t r[16];
+        tmem_ld16(sums + j, r);
+        tmem_ld_wait();
+        if (j + 16 >= rows) {  // the tile's sums have been read
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0 && alive) mbar_arrive(&ctl.sums_empty[place]);
+        }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float v = __uint_as_float(r[i]);
-        if (split == 1) put(j + i, v);
-        else part[(j + i) * 128 + threadIdx.x] = ok ? v : kNaN;
+        for (int i = 0; i < 16; ++i) {
+          if (j + i >= rows || n >= a.n) break;
+          const float row = HELD && a.raw.data ? ctl.row_scale[j + i] : a.x_row ? __ldg(a.x_row + t0 + j + i) : 1.f;
+          store_one(y + (j + i) * next, 0, a.y_type, fmaf(__uint_as_float(r[i]) * row, scale, add));
+        }
       }
     }
-    fence_before_sync();
   }
   if (split > 1) {
+    __syncthreads();  // no copy is under way any more, and nobody gives up from here on
+    const bool ok = !*abort_flag;
+    if (warp < 4) {
+      const uint32_t sums = tmem + ((uint32_t)(warp * 32) << 16);
+      float* part = reinterpret_cast<float*>(ring);  // [BN][128], where the chunks were
+#pragma unroll 1
+      for (int j = 0; j < BN; j += 16) {
+        uint32_t r[16];
+        tmem_ld16(sums + j, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) part[(j + i) * 128 + threadIdx.x] = ok ? __uint_as_float(r[i]) : kNaN;
+      }
+      fence_before_sync();
+    }
     cluster_sync();
     // A thread adds up 4 columns of y of a row of x; 4 of those at a time, as a word of
     // another CTA is some 500 cycles away (128 rows of x, 2 CTAs: one at a time took 20 us).
+    const int n0 = n_of(first), t0 = t_of(first);
     const int q0 = BN * rank / split * 32, q1 = min(BN * (rank + 1) / split, a.t - t0) * 32;
     const int item = element_bytes(a.y_type);
     constexpr int U = 4;
@@ -210,9 +320,9 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(const __grid_consta
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int at = q + u * kThreads, t = t0 + (at >> 5), n = n0 + (at & 31) * 4;
+        const int at = q + u * kThreads, j = at >> 5, n = n0 + (at & 31) * 4;
         if (at >= q1) break;
-        const float row = a.x_row ? __ldg(a.x_row + t) : 1.f;
+        const float row = HELD && a.raw.data ? ctl.row_scale[j] : a.x_row ? __ldg(a.x_row + t0 + j) : 1.f;
         const float f[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
         uint32_t out[4];
 #pragma unroll
@@ -221,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(const __grid_consta
           const float add = a.bias && n + e < a.n ? __ldg(a.bias + n + e) : 0.f;
           out[e] = __float_as_uint(fmaf(f[e] * row, scale, add));
         }
-        uint8_t* y = static_cast<uint8_t*>(a.y) + (t * a.y_stride + n) * item;
+        uint8_t* y = static_cast<uint8_t*>(a.y) + ((t0 + j) * a.y_stride + n) * item;
         if (((uintptr_t)y & (4 * item - 1)) == 0 && n + 4 <= a.n) {
           if (item == 4) {
             *reinterpret_cast<uint4*>(y) = make_uint4(out[0], out[1], out[2], out[3]);
@@ -241,32 +351,47 @@ __global__ void __launch_bounds__(kThreads, 2) linear_kernel(const __grid_consta
     }
     cluster_sync();  // the others have read this CTA's part
   }
+  fence_before_sync();
   __syncthreads();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, C::TMEM);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, tmem_columns);
 }
 
-template <int FMT, int BN>
-int launch(LinearArgs& a, const fp4_matrix& x, const fp4_matrix& w, int sms, cudaStream_t st) {
-  using C = Cfg<FMT, BN>;
+// Bytes of held rows that still leave a ring of six slots or more.
+template <int FMT>
+bool can_hold(int chunks) {
+  using C = Cfg<FMT, 16, true>;
+  return C::slots_of(kRoom - chunks * C::X_PART) >= 6;
+}
+
+template <int FMT, int BN, bool HELD>
+int launch(LinearArgs& a, const fp4_matrix* x, const fp4_matrix& w, int split, int sms, cudaStream_t st) {
+  using C = Cfg<FMT, BN, HELD>;
   static moe::SmemGrant grant;
   if (const int rc = codes_map(w, 128, &a.w_map)) return rc;
-  if (const int rc = codes_map(x, BN, &a.x_map)) return rc;
-  if (!moe::grant_smem(linear_kernel<FMT, BN>, smem_bytes<C>(C::SLOTS), grant)) return MOE_ERR_CUDA;
-  const int n_tiles = (a.n + 127) / 128, t_tiles = (a.t + BN - 1) / BN, chunks = (a.cols + kChunk - 1) / kChunk;
-  // the split that leaves the busiest SM the fewest chunks
-  int split = 1;
-  long long best = 1ll << 62;
-  for (int s = 1; s <= 8 && s <= chunks; s *= 2) {
-    const long long waves = ((long long)n_tiles * t_tiles * s + sms - 1) / sms, cost = waves * ((chunks + s - 1) / s + 1);
-    if (cost < best) best = cost, split = s;
-  }
-  const int slots = C::SLOTS;
-  const long long blocks = (long long)n_tiles * t_tiles * split;
-  if (blocks > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
+  if (x)
+    if (const int rc = codes_map(*x, BN, &a.x_map)) return rc;
+  const int chunks = (a.cols + kChunk - 1) / kChunk, most = (chunks + split - 1) / split;  // of a CTA
+  const long long tiles = (long long)((a.n + 127) / 128) * ((a.t + BN - 1) / BN);
+  if (tiles > 0x3FFFFFFF) return MOE_ERR_UNSUPPORTED;
+  const int clusters = (int)(tiles < sms / split ? tiles : sms / split);
+  const size_t held = HELD ? (size_t)most * C::X_PART : 0;
+  int slots = C::slots_of(kRoom - (int)held);
+  // no more than a CTA's tiles have chunks, but room for the sums that a cluster exchanges
+  const long long work = (tiles + clusters - 1) / clusters * most;
+  const int least = split > 1 ? (BN * 512 + C::SLOT - 1) / C::SLOT : 1;
+  if (slots > work) slots = (int)(work < least ? least : work);
+  // Two CTAs on an SM, of clusters in two streams, must not wait for each other's TMEM: as
+  // many as shared memory lets in have to find theirs.  So half of TMEM goes with half of
+  // the shared memory or more, and all of it with more than half.
+  size_t smem = 1024 + (size_t)slots * C::SLOT + held + sizeof(Control);
+  const size_t half = 113 * 1024;
+  const int columns = smem <= half && C::S_COL + slots * 2 * C::S_COLS <= 256 ? 256 : 512;
+  if (smem <= half) smem = columns == 256 ? half : half + 1024;
+  if (!moe::grant_smem(linear_kernel<FMT, BN, HELD>, smem, grant)) return MOE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.gridDim = dim3((unsigned)(clusters * split));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes<C>(slots);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -275,16 +400,30 @@ int launch(LinearArgs& a, const fp4_matrix& x, const fp4_matrix& w, int sms, cud
   attr[1].val.clusterDim.x = split, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = split > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, linear_kernel<FMT, BN>, a, split, slots) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, linear_kernel<FMT, BN, HELD>, a, split, slots, columns) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// Over how many CTAs a tile's columns are split: as many as still give each tile a
+// cluster of its own at the same time.
+int split_of(int tiles, int chunks, int sms) {
+  int split = 1;
+  while (split < 8 && 2 * split <= chunks && (long long)tiles * 2 * split <= sms) split *= 2;
+  return split;
+}
+
+// x NULL: a.raw, which is held.
 template <int FMT>
-int launch(LinearArgs& a, const fp4_matrix& x, const fp4_matrix& w, int sms, cudaStream_t st) {
-  if (a.t <= 16) return launch<FMT, 16>(a, x, w, sms, st);
-  if (a.t <= 32) return launch<FMT, 32>(a, x, w, sms, st);
-  if (a.t <= 64) return launch<FMT, 64>(a, x, w, sms, st);
-  if (a.t > 256) return launch_wide(a, x, w, sms, st);
-  return launch<FMT, 128>(a, x, w, sms, st);
+int launch(LinearArgs& a, const fp4_matrix* x, const fp4_matrix& w, int sms, cudaStream_t st) {
+  const int n_tiles = (a.n + 127) / 128, chunks = (a.cols + kChunk - 1) / kChunk;
+  if (a.t <= 16) {
+    const int split = split_of(n_tiles, chunks, sms);
+    return can_hold<FMT>((chunks + split - 1) / split) ? launch<FMT, 16, true>(a, x, w, split, sms, st)
+                                                       : launch<FMT, 16, false>(a, x, w, split, sms, st);
+  }
+  if (a.t <= 32) return launch<FMT, 32, false>(a, x, w, split_of(n_tiles, chunks, sms), sms, st);
+  if (a.t <= 64) return launch<FMT, 64, false>(a, x, w, split_of(n_tiles, chunks, sms), sms, st);
+  if (a.t > 256) return launch_wide(a, *x, w, sms, st);
+  return launch<FMT, 128, false>(a, x, w, split_of(n_tiles * ((a.t + 127) / 128), chunks, sms), sms, st);
 }
 
 // Where fp4_linear_rows keeps its quantised rows.
@@ -307,26 +446,18 @@ int check_output(const Rows& y, int rows, int cols) {
   return MOE_OK;
 }
 
-// `early`: the kernel before on the stream writes x alone, and waited for those before it.
-int product(const fp4_matrix* x, const fp4_matrix* w, const float* bias, const Rows& y, int32_t* dev_status, void* stream,
-            bool early) {
-  if (const int rc = fp4::check_matrix(x)) return rc;
-  if (const int rc = fp4::check_matrix(w)) return rc;
-  if (x->cols != w->cols || x->format != w->format) return MOE_ERR_INVALID_ARG;
-  if (const int rc = check_output(y, x->rows, w->rows)) return rc;
-  if ((uintptr_t)bias & 3u) return MOE_ERR_ALIGNMENT;
-  if (x->rows == 0 || w->rows == 0) return MOE_OK;
-  const int sms = moe::device_info().sms;
-  if (sms <= 0) return MOE_ERR_CUDA;
-  LinearArgs a;
-  a.w_scales = static_cast<const uint8_t*>(w->scales), a.x_scales = static_cast<const uint8_t*>(x->scales);
-  a.w_row = w->row_scale, a.x_row = x->row_scale, a.bias = bias;
-  a.n = w->rows, a.t = x->rows, a.cols = x->cols;
-  a.y = y.data, a.y_stride = x->rows > 1 ? y.stride : 0, a.y_type = y.type;
+// What the kernels are told, but for x.
+LinearArgs arguments(const fp4_matrix& w, const float* bias, const Rows& y, int rows, int32_t* dev_status) {
+  LinearArgs a = {};
+  a.w_scales = static_cast<const uint8_t*>(w.scales), a.w_row = w.row_scale, a.bias = bias;
+  a.n = w.rows, a.t = rows, a.cols = w.cols;
+  a.y = y.data, a.y_stride = rows > 1 ? y.stride : 0, a.y_type = y.type;
   a.wait_cycles = attn::wait_cycles(), a.extra = (int)moe::barrier_extra(), a.st = dev_status;
-  a.early = early;
-  return w->format == MOE_FMT_NVFP4 ? launch<MOE_FMT_NVFP4>(a, *x, *w, sms, (cudaStream_t)stream)
-                                    : launch<MOE_FMT_MXFP4>(a, *x, *w, sms, (cudaStream_t)stream);
+  return a;
+}
+int launch(LinearArgs& a, const fp4_matrix* x, const fp4_matrix& w, int sms, cudaStream_t st) {
+  if (x) a.x_scales = static_cast<const uint8_t*>(x->scales), a.x_row = x->row_scale;
+  return w.format == MOE_FMT_NVFP4 ? launch<MOE_FMT_NVFP4>(a, x, w, sms, st) : launch<MOE_FMT_MXFP4>(a, x, w, sms, st);
 }
 
 }  // namespace
@@ -335,11 +466,21 @@ extern "C" {
 
 int fp4_linear(const fp4_matrix* x, const fp4_matrix* w, const float* bias, void* y, long long y_stride, int y_type,
                int32_t* dev_status, void* stream) {
-  return product(x, w, bias, rows_of(y, y_stride, y_type), dev_status, stream, false);
+  if (const int rc = check_matrix(x)) return rc;
+  if (const int rc = check_matrix(w)) return rc;
+  if (x->cols != w->cols || x->format != w->format) return MOE_ERR_INVALID_ARG;
+  const Rows out = rows_of(y, y_stride, y_type);
+  if (const int rc = check_output(out, x->rows, w->rows)) return rc;
+  if ((uintptr_t)bias & 3u) return MOE_ERR_ALIGNMENT;
+  if (x->rows == 0 || w->rows == 0) return MOE_OK;
+  const int sms = moe::device_info().sms;
+  if (sms <= 0) return MOE_ERR_CUDA;
+  LinearArgs a = arguments(*w, bias, out, x->rows, dev_status);
+  return launch(a, x, *w, sms, (cudaStream_t)stream);
 }
 
 size_t fp4_linear_rows_workspace(const fp4_matrix* w, int rows) {
-  if (!w || rows < 0 || !fp4::shape_ok(rows, w->cols, w->format)) return 0;
+  if (!w || rows < 0 || !shape_ok(rows, w->cols, w->format)) return 0;
   return layout(rows, w->cols, w->format).bytes + 16;
 }
 
@@ -347,10 +488,10 @@ int fp4_linear_rows(const void* x, long long x_stride, int x_type, int rows, con
                     void* y, long long y_stride, int y_type, void* workspace, size_t ws_bytes, int32_t* dev_status,
                     void* stream) {
   if (rows < 0) return MOE_ERR_INVALID_ARG;
-  if (const int rc = fp4::check_matrix(w)) return rc;
-  if (!fp4::shape_ok(rows, w->cols, w->format)) return MOE_ERR_UNSUPPORTED;
-  const Rows out = rows_of(y, y_stride, y_type);
-  if (const int rc = check_rows(rows_of(x, x_stride, x_type), rows, w->cols, true)) return rc;
+  if (const int rc = check_matrix(w)) return rc;
+  if (!shape_ok(rows, w->cols, w->format)) return MOE_ERR_UNSUPPORTED;
+  const Rows in = rows_of(x, x_stride, x_type), out = rows_of(y, y_stride, y_type);
+  if (const int rc = check_rows(in, rows, w->cols, true)) return rc;
   if (const int rc = check_output(out, rows, w->rows)) return rc;
   if ((uintptr_t)bias & 3u) return MOE_ERR_ALIGNMENT;
   if (rows == 0 || w->rows == 0) return MOE_OK;
@@ -358,12 +499,21 @@ int fp4_linear_rows(const void* x, long long x_stride, int x_type, int rows, con
   if (!moe::aligned16(workspace)) return MOE_ERR_ALIGNMENT;
   const Layout l = layout(rows, w->cols, w->format);
   if (ws_bytes < l.bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const int sms = moe::device_info().sms;
+  if (sms <= 0) return MOE_ERR_CUDA;
+  LinearArgs a = arguments(*w, bias, out, rows, dev_status);
+  if (rows <= 16 && rows * w->cols <= kMaxRaw) {
+    a.raw = in;
+    if (rows == 1) a.raw.stride = 0;
+    return launch(a, nullptr, *w, sms, (cudaStream_t)stream);
+  }
   uint8_t* at = static_cast<uint8_t*>(workspace);
   const fp4_matrix m = {at, at + l.scales,
                         w->format == MOE_FMT_NVFP4 ? reinterpret_cast<float*>(at + l.row_scale) : nullptr, rows,
                         w->cols, w->format};
   if (const int rc = fp4_quantize(x, x_stride, x_type, &m, stream)) return rc;
-  return product(&m, w, bias, out, dev_status, stream, true);
+  a.early = 1;  // the kernel before writes x alone, and has waited for those before it
+  return launch(a, &m, *w, sms, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -21,6 +21,7 @@ struct LinearArgs {
   long long wait_cycles;
   int extra;  // arrivals that never come, on the barrier of the sums
   int early;  // w may be read before the kernel before this one has ended
+  Rows raw;   // .data, where there is no matrix of x: its rows, to be quantised
   int32_t* st;
 };
 

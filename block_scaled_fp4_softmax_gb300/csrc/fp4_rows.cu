@@ -13,47 +13,11 @@
 
 #include <type_traits>
 
-#include "fp4.cuh"
+#include "fp4_quantize.cuh"
+
+using namespace fp4;
 
 namespace {
-
-constexpr float kNaN = __builtin_nanf("");
-
-// 2^(bits of the exponent field), field from 1 to 254.
-__device__ __forceinline__ float power_field(int field) { return __uint_as_float((uint32_t)field << 23); }
-
-// 8 elements of a type as they lie in memory (plain loads: a residual may be overwritten
-// in place).
-template <int TYPE>
-struct Raw {
-  uint4 q;
-  __device__ __forceinline__ void load(const void* base, long long at) {
-    q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
-  }
-  __device__ __forceinline__ void zero() { q = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ void floats(float (&f)[8]) const {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 v = TYPE == FP4_BF16 ? make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u))
-                                        : __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      f[2 * i] = v.x, f[2 * i + 1] = v.y;
-    }
-  }
-};
-template <>
-struct Raw<FP4_FP32> {
-  float4 q[2];
-  __device__ __forceinline__ void load(const void* base, long long at) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-    q[0] = p[0], q[1] = p[1];
-  }
-  __device__ __forceinline__ void zero() { q[0] = q[1] = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void floats(float (&f)[8]) const {
-    f[0] = q[0].x, f[1] = q[0].y, f[2] = q[0].z, f[3] = q[0].w;
-    f[4] = q[1].x, f[5] = q[1].y, f[6] = q[1].z, f[7] = q[1].w;
-  }
-};
 
 // 8 elements rounded to `type` and written.
 __device__ __forceinline__ void store8(void* base, long long at, int type, const float (&f)[8]) {
@@ -118,116 +82,36 @@ __device__ __forceinline__ float row_sum(float v, Slots& slots) {
 // zeros past the row's end.
 // ---------------------------------------------------------------------------
 
-// 1 / x within an ulp, 0 where that is below 2^-126.
-__device__ __forceinline__ float reciprocal(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// 8 floats -> a word of e2m1 codes, the first in the lowest nibble.
-__device__ __forceinline__ uint32_t to_e2m1x8(const float (&f)[8]) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
-      "mov.b32 %0, {a, b, c, d};\n\t}"
-      : "=r"(r)
-      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
-  return r;
-}
-// The larger of |a|, |b|, |c|; NaN if there is one.
-__device__ __forceinline__ float max_abs(float a, float b, float c) {
-  float d;
-  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
 template <int NB, bool NV>
 __device__ __forceinline__ void to_fp4(const fp4_matrix& m, const Place& p, float (&v)[NB][8], Slots& slots) {
-  // The largest magnitudes as bit patterns: in that order infinities and NaN are
-  // above all numbers.
   uint32_t top[NB];
 #pragma unroll
-  for (int j = 0; j < NB; ++j) {
-    const float a = max_abs(v[j][0], v[j][1], v[j][2]), b = max_abs(v[j][3], v[j][4], v[j][5]);
-    uint32_t t = __float_as_uint(max_abs(max_abs(v[j][6], v[j][7], a), b, 0.f));
-    t = max(t, __shfl_xor_sync(0xffffffffu, t, 1));
-    if (!NV) t = max(t, __shfl_xor_sync(0xffffffffu, t, 2));
-    top[j] = t;
-  }
-  float up = 1.f, down = 1.f;  // 2^E, 2^-E
-  bool bad = false;
+  for (int j = 0; j < NB; ++j) top[j] = block_top<NV>(v[j]);
+  RowScale scale;
   if (NV) {
     uint32_t a = top[0];
 #pragma unroll
     for (int j = 1; j < NB; ++j) a = max(a, top[j]);
-    a = row_max(a, slots);
-    bad = a >= 0x7F800000u;
-    // a = f * 2^e: 2688 = 1.3125 * 2^11
-    const int e = max(-126, (int)(a >> 23) - 127 - 11 + ((a & 0x7FFFFFu) > 0x280000u));
-    up = power_field(127 + e), down = power_field(127 - e);
-    if (p.t == 0 && p.live) m.row_scale[p.row] = bad ? kNaN : up;
-    if (e < -110) {  // 2^-E / s below would not be finite: such a row is scaled first
+    scale = row_scale(row_max(a, slots));
+    if (p.t == 0 && p.live) m.row_scale[p.row] = scale.value();
+    if (scale.tiny) {
 #pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        top[j] = __float_as_uint(__uint_as_float(top[j]) * down);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] *= down;
-      }
-      up = down = 1.f;
+      for (int j = 0; j < NB; ++j) scale_first(scale, v[j], top[j]);
     }
   } else if (m.row_scale && p.t == 0 && p.live) {
     m.row_scale[p.row] = 1.f;
   }
-  const int tiles = fp4::scale_tiles(m.cols, NV ? MOE_FMT_NVFP4 : MOE_FMT_MXFP4);
+  const int tiles = scale_tiles(m.cols, NV ? MOE_FMT_NVFP4 : MOE_FMT_MXFP4);
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
-    uint32_t scale, word = 0;
-    float q[8];
-    if (NV) {
-      // Quotients by Markstein's theorem: from a correctly rounded reciprocal and a
-      // quotient within an ulp, one residual gives the correctly rounded quotient (ties
-      // of e2m1 included), at a third of the cost of divisions.
-      const float a = __uint_as_float(top[j]) * down, sixth = 1.f / 6.f, b = a * sixth;
-      scale = bad ? 0u : moe::f32_to_e4m3_rn_sat(fmaf(fmaf(-6.f, b, a), sixth, b));
-      const float s = moe::e4m3x2_to_f32x2(scale).x;
-      // 1 / s of a number of four bits: one step of Newton's method rounds it correctly
-      const float y0 = reciprocal(s), y = fmaf(fmaf(-s, y0, 1.f), y0, y0);
-      // with the signs as they are (r = s q + (-x), q - r / s), a zero keeps its own
-      const float2 inv = make_float2(y * down, y * down), minus = make_float2(-inv.x, -inv.x);
-      const float2 s2 = make_float2(s * up, s * up), none = make_float2(-0.f, -0.f);
-#pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const float2 x = make_float2(v[j][i], v[j][i + 1]), q0 = moe::ffma2(x, inv, none);
-        const float2 r = moe::ffma2(q0, s2, make_float2(-x.x, -x.y));
-        const float2 z = moe::ffma2(r, minus, q0);
-        q[i] = z.x, q[i + 1] = z.y;
-      }
-    } else {
-      const uint32_t a = top[j];
-      // 6 = 1.5 * 2^2
-      bad = a >= 0x7F800000u;
-      scale = bad ? 255u : (uint32_t)max(0, (int)(a >> 23) - 2 + ((a & 0x7FFFFFu) > 0x400000u));
-      const float mult = power_field(254 - (int)min(scale, 253u));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = v[j][i] * mult;
-    }
-    if (NV ? scale != 0u : !bad) word = to_e2m1x8(q);
-    const int lane = p.t & 31;
+    uint32_t word;
     const bool in = p.in(j);
-    if (!in) scale = 0;
-    // four scales into one word: of lanes 0, 2, 4, 6 (mod 8), or 0, 4, 8, 12 (mod 16)
-    uint32_t four = scale << (8 * ((NV ? lane >> 1 : lane >> 2) & 3));
-    constexpr int kStep = NV ? 2 : 4;
-    four |= __shfl_xor_sync(0xffffffffu, four, kStep);
-    four |= __shfl_xor_sync(0xffffffffu, four, 2 * kStep);
+    const uint32_t four = quantize8<NV>(v[j], top[j], scale, p.t & 31, in, word);
     if (in) {
       *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(m.codes) + ((size_t)p.row * m.cols + p.col(j)) / 2) = word;
-      if ((lane & (4 * kStep - 1)) == 0)
+      if ((p.t & (kScaleLanes<NV> - 1)) == 0)
         *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(m.scales) +
-                                     fp4::scale_word(p.row, p.col(j) / (8 * 4 * kStep), tiles)) = four;
+                                     scale_word(p.row, p.col(j) / (8 * kScaleLanes<NV>), tiles)) = four;
     }
   }
 }

@@ -233,3 +233,30 @@ def test_tiles_of_every_width(T, N, K, format):
     """Rounds of tiles that come out best at 256, 192 and 128 columns."""
     check(T, N, K, format, BF, bias=True)
     check(T, N, K, format, F32)
+
+
+@pytest.mark.parametrize("format", [NV, MX])
+@pytest.mark.parametrize("T,K", [(1, 32), (1, 2560), (1, 32768), (2, 16384), (3, 96), (5, 1056), (7, 2880), (16, 2048), (16, 2080)])
+def test_few_elements_are_quantised_by_the_product(T, K, format):
+    """Below and above 32768 elements the same bits as from a matrix: rows of zeros, of
+    tiny numbers, with an infinity."""
+    g = torch.Generator(device="cuda").manual_seed(K)
+    w = fp4.fp4_quantize(torch.randn(700, K, generator=g, device="cuda"), format)
+    for dtype in (BF, FP, F32):
+        x = torch.randn(T, K + 32, generator=g, device="cuda")
+        x[0] *= 1e-3
+        if T > 2:
+            x[1], x[2, 40 % K] = 0, float("inf")
+        if T > 4 and dtype != FP:
+            x[3] *= 1e-37
+        x = x.to(dtype)[:, :K]
+        want = fp4.fp4_linear(fp4.fp4_quantize(x, format), w, dtype=F32)
+        got = fp4.fp4_linear_rows(x, w, dtype=F32)
+        assert torch.equal(got.view(torch.int32), want.view(torch.int32))
+
+
+@pytest.mark.parametrize("format", [NV, MX])
+def test_many_tiles_of_few_rows(format):
+    """More tiles than SMs: each CTA makes several, from one ring and two places of sums."""
+    for T, N, K in ((1, 30000, 288), (16, 50257, 64), (17, 40000, 96), (64, 25000, 1056), (100, 20500, 320), (9, 20000, 8224)):
+        check(T, N, K, format, BF, seed=T)
