@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kThreads = 192;  // warps 0-3: epilogue; 4: copies; 5: MMA
 constexpr int kTmaWarp = 4, kMmaWarp = 5;
-constexpr int kMaxRaw = 32768;  // elements of x that every CTA quantises for itself
+constexpr int kMaxRaw = 32768, kMaxRawRows = 2;  // elements and rows of x that every CTA quantises for itself
 
 template <int FMT, int BN_, bool HELD>
 struct Cfg {
@@ -59,11 +59,13 @@ struct Control {
 constexpr int kRoom = 227 * 1024 - 1024 - (int)sizeof(Control);  // for the ring and the held rows
 
 // Quantises all of x for the CTA's chunks c0 .. c1 - 1, as fp4_quantize does, with the four
-// epilogue warps.
+// epilogue warps: all on one row, two on each of two, one on each of more.
 template <int FMT, int TYPE>
 __device__ void hold_raw(const LinearArgs& a, Control& ctl, uint8_t* held, int part, int x_bytes, int c0, int c1) {
   constexpr bool NV = FMT == MOE_FMT_NVFP4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int share = a.t == 1 ? 4 : a.t == 2 ? 2 : 1, mine = warp % share;  // warps of a row, and which of them
+  const int t0 = warp / share, step = 4 / share, first = (mine * 32 + lane) * 8, width = share * 256;
   auto load = [&](int t, int col, float(&v)[8]) {
     Raw<TYPE> raw;
     if (col < a.cols) raw.load(a.raw.data, t * a.raw.stride + col);
@@ -71,28 +73,32 @@ __device__ void hold_raw(const LinearArgs& a, Control& ctl, uint8_t* held, int p
     raw.floats(v);
   };
   if (NV) {
-    for (int t = 0; t < a.t; ++t) {
+    for (int t = t0; t < a.t; t += step) {
       uint32_t top = 0;
 #pragma unroll 4
-      for (int col = threadIdx.x * 8; col < a.cols; col += 128 * 8) {
+      for (int col = first; col < a.cols; col += width) {
         float v[8];
         load(t, col, v);
         const float b = max_abs(max_abs(v[0], v[1], v[2]), max_abs(v[3], v[4], v[5]), max_abs(v[6], v[7], 0.f));
         top = max(top, __float_as_uint(b));
       }
       top = __reduce_max_sync(0xffffffffu, top);
-      if (lane == 0) ctl.row_top[warp][t] = top;
+      if (lane == 0) ctl.row_top[mine][t] = top;
     }
     named_sync(1, 128);
   }
-  for (int t = 0; t < a.t; ++t) {
+  const int end = min(c1 * kChunk, (a.cols + 63) / 64 * 64);  // whole words of NVFP4's scales
+  for (int t = t0; t < a.t; t += step) {
     RowScale scale;
-    if (NV) scale = row_scale(max(max(ctl.row_top[0][t], ctl.row_top[1][t]), max(ctl.row_top[2][t], ctl.row_top[3][t])));
-    if (threadIdx.x == 0) ctl.row_scale[t] = scale.value();
-    const int end = min(c1 * kChunk, (a.cols + 63) / 64 * 64);  // whole words of NVFP4's scales
-#pragma unroll 2
-    for (int first = c0 * kChunk; first < end; first += 128 * 8) {
-      const int col = first + threadIdx.x * 8;
+    if (NV) {
+      uint32_t top = ctl.row_top[0][t];
+      for (int k = 1; k < share; ++k) top = max(top, ctl.row_top[k][t]);
+      scale = row_scale(top);
+    }
+    if (mine == 0 && lane == 0) ctl.row_scale[t] = scale.value();
+#pragma unroll 4
+    for (int from = c0 * kChunk; from < end; from += width) {
+      const int col = from + first;
       float v[8];
       load(t, col, v);
       uint32_t top = block_top<NV>(v), word;
@@ -356,13 +362,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   if (warp == kMmaWarp) tmem_dealloc(tmem, tmem_columns);
 }
 
-// Bytes of held rows that still leave a ring of six slots or more.
-template <int FMT>
-bool can_hold(int chunks) {
-  using C = Cfg<FMT, 16, true>;
-  return C::slots_of(kRoom - chunks * C::X_PART) >= 6;
-}
-
 template <int FMT, int BN, bool HELD>
 int launch(LinearArgs& a, const fp4_matrix* x, const fp4_matrix& w, int split, int sms, cudaStream_t st) {
   using C = Cfg<FMT, BN, HELD>;
@@ -405,25 +404,35 @@ int launch(LinearArgs& a, const fp4_matrix* x, const fp4_matrix& w, int split, i
 
 // Over how many CTAs a tile's columns are split: as many as still give each tile a
 // cluster of its own at the same time.
-int split_of(int tiles, int chunks, int sms) {
+int split_of(const LinearArgs& a, int rows, int sms) {
+  const long long tiles = (long long)((a.n + 127) / 128) * ((a.t + rows - 1) / rows);
+  const int chunks = (a.cols + kChunk - 1) / kChunk;
   int split = 1;
-  while (split < 8 && 2 * split <= chunks && (long long)tiles * 2 * split <= sms) split *= 2;
+  while (split < 8 && 2 * split <= chunks && tiles * 2 * split <= sms) split *= 2;
   return split;
+}
+// Whether the rows of x stay in shared memory: up to 16, if they leave a ring of six slots.
+template <int FMT>
+bool holds(const LinearArgs& a, int sms) {
+  using C = Cfg<FMT, 16, true>;
+  if (a.t > 16) return false;
+  const int chunks = (a.cols + kChunk - 1) / kChunk, split = split_of(a, 16, sms);
+  return C::slots_of(kRoom - (chunks + split - 1) / split * C::X_PART) >= 6;
+}
+bool holds(const LinearArgs& a, int format, int sms) {
+  return format == MOE_FMT_NVFP4 ? holds<MOE_FMT_NVFP4>(a, sms) : holds<MOE_FMT_MXFP4>(a, sms);
 }
 
 // x NULL: a.raw, which is held.
 template <int FMT>
 int launch(LinearArgs& a, const fp4_matrix* x, const fp4_matrix& w, int sms, cudaStream_t st) {
-  const int n_tiles = (a.n + 127) / 128, chunks = (a.cols + kChunk - 1) / kChunk;
-  if (a.t <= 16) {
-    const int split = split_of(n_tiles, chunks, sms);
-    return can_hold<FMT>((chunks + split - 1) / split) ? launch<FMT, 16, true>(a, x, w, split, sms, st)
-                                                       : launch<FMT, 16, false>(a, x, w, split, sms, st);
-  }
-  if (a.t <= 32) return launch<FMT, 32, false>(a, x, w, split_of(n_tiles, chunks, sms), sms, st);
-  if (a.t <= 64) return launch<FMT, 64, false>(a, x, w, split_of(n_tiles, chunks, sms), sms, st);
+  if (holds<FMT>(a, sms)) return launch<FMT, 16, true>(a, x, w, split_of(a, 16, sms), sms, st);
+  if (!x) return MOE_ERR_UNSUPPORTED;  // (no call gets here)
+  if (a.t <= 16) return launch<FMT, 16, false>(a, x, w, split_of(a, 16, sms), sms, st);
+  if (a.t <= 32) return launch<FMT, 32, false>(a, x, w, split_of(a, 32, sms), sms, st);
+  if (a.t <= 64) return launch<FMT, 64, false>(a, x, w, split_of(a, 64, sms), sms, st);
   if (a.t > 256) return launch_wide(a, *x, w, sms, st);
-  return launch<FMT, 128, false>(a, x, w, split_of(n_tiles * ((a.t + 127) / 128), chunks, sms), sms, st);
+  return launch<FMT, 128, false>(a, x, w, split_of(a, 128, sms), sms, st);
 }
 
 // Where fp4_linear_rows keeps its quantised rows.
@@ -502,7 +511,7 @@ int fp4_linear_rows(const void* x, long long x_stride, int x_type, int rows, con
   const int sms = moe::device_info().sms;
   if (sms <= 0) return MOE_ERR_CUDA;
   LinearArgs a = arguments(*w, bias, out, rows, dev_status);
-  if (rows <= 16 && rows * w->cols <= kMaxRaw) {
+  if (rows <= kMaxRawRows && rows * w->cols <= kMaxRaw && holds(a, w->format, sms)) {
     a.raw = in;
     if (rows == 1) a.raw.stride = 0;
     return launch(a, nullptr, *w, sms, (cudaStream_t)stream);

@@ -256,6 +256,22 @@ def test_few_elements_are_quantised_by_the_product(T, K, format):
 
 
 @pytest.mark.parametrize("format", [NV, MX])
+@pytest.mark.parametrize("T,N,K", [(1, 8192, 16384), (1, 9000, 32768), (2, 19300, 8192), (1, 6000, 32768), (16, 10000, 16384)])
+def test_few_rows_that_shared_memory_does_not_hold(T, N, K, format):
+    """Long rows over many tiles: a CTA's part of them is more than it may keep beside its ring."""
+    g = torch.Generator(device="cuda").manual_seed(K)
+    w = fp4.fp4_quantize(torch.randn(N, K, generator=g, device="cuda").to(BF), format)
+    x = torch.randn(T, K, generator=g, device="cuda").to(BF)
+    m = fp4.fp4_quantize(x, format)
+    got = fp4.fp4_linear(m, w, dtype=F32)
+    assert torch.equal(fp4.fp4_linear_rows(x, w, dtype=F32).view(torch.int32), got.view(torch.int32))
+    # (the plain product in 64 bits of what is held)
+    a, b = (fp4.fp4_dequantize(t, F32).double() for t in (m, w))
+    off = (got.double() - a @ b.T).abs()
+    assert (off <= (a.abs() @ b.abs().T) * (K + 3) * 2.0 ** -23).all()
+
+
+@pytest.mark.parametrize("format", [NV, MX])
 def test_many_tiles_of_few_rows(format):
     """More tiles than SMs: each CTA makes several, from one ring and two places of sums."""
     for T, N, K in ((1, 30000, 288), (16, 50257, 64), (17, 40000, 96), (64, 25000, 1056), (100, 20500, 320), (9, 20000, 8224)):
