@@ -125,7 +125,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = split > 1 ? (int)cluster_rank() : 0;
+  // (the rank in the cluster, by an expression that the compiler knows to be the same for the
+  // warp: with a loop whose bounds it did not, what the MMA warp issues took four times as long)
+  const int rank = blockIdx.x % split;
   const int t_tiles = (a.t + BN - 1) / BN, all = (a.n + 127) / 128 * t_tiles;
   const int first = blockIdx.x / split, step = gridDim.x / split;
   const int chunks = (a.cols + kChunk - 1) / kChunk;

@@ -162,12 +162,6 @@ def _matrix(m, name, index, shape, format=None):
                    f"on cuda:{index}, got {m!r}")
 
 
-def _short(dtype):
-    if dtype not in _SHORT:
-        raise MoeError(f"dtype must be torch.bfloat16 or torch.float16, got {dtype}")
-    return dtype
-
-
 # ---------------------------------------------------------------------------
 # Matrices
 # ---------------------------------------------------------------------------
@@ -266,9 +260,8 @@ def fp4_dequantize(m: Fp4Matrix, dtype=torch.bfloat16, out=None, stream=None):
     """The values of m's elements, [rows, cols] of dtype (or out's type)."""
     index = _of(m, "m")
     on = _on(stream, index)
-    if out is None:
-        out = _result(m.shape, dtype, m.device, stream)
-    rc = (_LIB or load()).fp4_dequantize(m.at, *_rows(out, "out", index, m.shape), on)
+    out, to = _result(m.shape, dtype, m.device, stream) if out is None else (out, _rows(out, "out", index, m.shape))
+    rc = (_LIB or load()).fp4_dequantize(m.at, *to, on)
     if rc:
         _check(rc, "fp4_dequantize")
     return out
@@ -283,12 +276,9 @@ def _targets(shape, t, dtype, format, out, matrix, index, stream, names):
     to, at = _NOTHING, None
     if out is None:
         if dtype is not None:
-            if stream is None:
-                out = _empty(shape, dtype=_short(dtype), device=t.device)
-            else:
-                with _elsewhere(stream):
-                    out = _empty(shape, dtype=_short(dtype), device=t.device)
-            to = out.data_ptr(), shape[1], _SHORT[dtype]
+            if dtype not in _SHORT:
+                raise MoeError(f"dtype must be torch.bfloat16 or torch.float16, got {dtype}")
+            out, to = _result(shape, dtype, t.device, stream)
     else:
         to = _rows(out, names[0], index, shape, _SHORT)
     if matrix is None and format is not None:
@@ -344,9 +334,7 @@ def fp4_block_norm(r, y=None, post_weight=None, gate=None, scale: float = 1.0, w
         if r_out is r:
             to, to_stride = a[:2]
         elif r_out is None:
-            with _elsewhere(stream):
-                r_out = _empty(shape, dtype=r.dtype, device=r.device)
-            to, to_stride = r_out.data_ptr(), cols
+            r_out, (to, to_stride, _) = _result(shape, r.dtype, r.device, stream)
         else:
             to, to_stride, kind = _rows(r_out, "r_out", index, shape)
             if kind != a[2]:
@@ -379,12 +367,16 @@ def _gate(gate, y, index, shape):
 
 
 def _result(shape, dtype, device, stream):
-    if dtype not in _TYPES:
+    """A new output with its address, stride and type."""
+    kind = _TYPES.get(dtype)
+    if kind is None:
         raise MoeError(f"dtype must be one of {', '.join(map(str, _TYPES))}, got {dtype}")
     if stream is None:
-        return _empty(shape, dtype=dtype, device=device)
-    with _elsewhere(stream):
-        return _empty(shape, dtype=dtype, device=device)
+        out = _empty(shape, dtype=dtype, device=device)
+    else:
+        with torch.cuda.stream(stream):
+            out = _empty(shape, dtype=dtype, device=device)
+    return out, (out.data_ptr(), shape[1], kind)
 
 
 def fp4_linear(x: Fp4Matrix, w: Fp4Matrix, bias=None, dtype=torch.bfloat16, out=None, dev_status=None, stream=None):
@@ -396,11 +388,9 @@ def fp4_linear(x: Fp4Matrix, w: Fp4Matrix, bias=None, dtype=torch.bfloat16, out=
     if x.cols != w.cols or x.format != w.format:
         raise MoeError(f"x and w must have the same columns and format, got {x!r} and {w!r}")
     shape = (x.rows, w.rows)
-    if out is None:
-        out = _result(shape, dtype, w.device, stream)
+    out, to = _result(shape, dtype, w.device, stream) if out is None else (out, _rows(out, "out", index, shape))
     rc = (_LIB or load()).fp4_linear(
-        x.at, w.at, None if bias is None else _array(bias, "bias", (w.rows,), _f32, index),
-        *_rows(out, "out", index, shape),
+        x.at, w.at, None if bias is None else _array(bias, "bias", (w.rows,), _f32, index), *to,
         None if dev_status is None else _array(dev_status, "dev_status", (1,), _i32, index), on)
     if rc:
         _check(rc, "fp4_linear")
@@ -429,8 +419,7 @@ def fp4_linear_rows(x, w: Fp4Matrix, bias=None, dtype=torch.bfloat16, out=None, 
     if cols != w.cols:
         raise MoeError(f"x must be [tokens, {w.cols}], got {list(x.shape)}")
     shape = (T, w.rows)
-    if out is None:
-        out = _result(shape, dtype, w.device, stream)
+    out, to = _result(shape, dtype, w.device, stream) if out is None else (out, _rows(out, "out", index, shape))
     if workspace is None:
         with _elsewhere(stream):
             workspace = fp4_linear_rows_workspace(w, T)
@@ -440,7 +429,7 @@ def fp4_linear_rows(x, w: Fp4Matrix, bias=None, dtype=torch.bfloat16, out=None, 
         raise MoeError("workspace must be a tensor with a shape") from None
     rc = (_LIB or load()).fp4_linear_rows(
         at, stride, kind, T, w.at, None if bias is None else _array(bias, "bias", (w.rows,), _f32, index),
-        *_rows(out, "out", index, shape), _array(workspace, "workspace", (size,), _u8, index), size,
+        *to, _array(workspace, "workspace", (size,), _u8, index), size,
         None if dev_status is None else _array(dev_status, "dev_status", (1,), _i32, index), on)
     if rc:
         _check(rc, "fp4_linear_rows")
