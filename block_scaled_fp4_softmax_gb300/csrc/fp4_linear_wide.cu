@@ -27,7 +27,7 @@ struct Cfg {
   static constexpr int X_BYTES = 128 * 128, W_BYTES = BN / 2 * 128, S_BYTES = COPIES * 512;
   static constexpr int SLOT = X_BYTES + W_BYTES + (1 + W_TILES) * S_BYTES;
   static constexpr int STAGE = kEpilogueWarps * 32 * 64;        // 64 bytes of 32 rows for each epilogue warp
-  static constexpr int ROOM = (227 * 1024 - 1024 - STAGE - 2560) / SLOT;
+  static constexpr int ROOM = (227 * 1024 - 1024 - STAGE - 256) / SLOT;
   static constexpr int SLOTS = ROOM < 8 ? ROOM : 8;
   static constexpr int SX_COLS = COPIES * 4, SW_COLS = SX_COLS * W_TILES;
   // TMEM holds the scales of as many chunks as the ring: where a slot's copies have
@@ -46,13 +46,12 @@ struct Control {
   uint32_t tmem;
   int abort;
   int loaded;  // chunks whose copies the CTA has issued, at its end
-  float2 column[256];  // w's row scale and the bias, of a tile's columns
 };
 template <class C>
 constexpr size_t smem_bytes() {
   return 1024 + (size_t)C::SLOTS * C::SLOT + C::STAGE + sizeof(Control);
 }
-static_assert(sizeof(Control) <= 2560, "Cfg::ROOM");
+static_assert(sizeof(Control) <= 256, "Cfg::ROOM");
 
 // Which tile of the grid of tiles comes i-th: blocks of 8 tiles of rows, so that the
 // tiles that run at a time share both operands in L2.
@@ -139,6 +138,8 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
     attn::prefetch_map(&args.w_scales_map);
     attn::prefetch_map(&args.x_scales_map);
   }
+  __syncthreads();
+  cluster_sync();  // the barriers of both CTAs are set up
   // (as in fp4_linear.cu: TMEM is taken between the kernel before and the one behind)
   moe::pdl_wait();
   if (warp == kMmaWarp) {
@@ -149,7 +150,6 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
   }
   fence_before_sync();
   __syncthreads();
-  cluster_sync();  // the barriers of both CTAs are set up
   fence_after_sync();
   moe::pdl_launch_dependents();
   const uint32_t tmem = ctl.tmem;
@@ -252,21 +252,34 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
     uint8_t* stage = ring + (size_t)C::SLOTS * C::SLOT + warp * (32 * 64);
     const int item = element_bytes(a.y_type);
     const long long step = a.y_stride * item;
-    const float2* column = ctl.column + first;
+    // Factors of a tile: of the lane's row, and of columns `lane` and `lane + 32` of the warp's,
+    // which the others get by shuffles.  Those of the next tile are fetched while this
+    // one's sums are awaited.
+    struct Factors {
+      float row, scale[2], add[2];
+    };
+    auto factors = [&](int at) {
+      Factors f = {1.f, {1.f, 1.f}, {0.f, 0.f}};
+      if (at >= all) return f;
+      const Tile tile(at, t_tiles, n_tiles, BN);
+      const int t = tile.t0 + 128 * rank + (warp & 3) * 32 + lane;
+      if (a.x_row && t < a.t) f.row = __ldg(a.x_row + t);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int n = tile.n0 + first + 32 * k + lane;
+        if (a.w_row && n < a.n) f.scale[k] = __ldg(a.w_row + n);
+        if (a.bias && n < a.n) f.add[k] = __ldg(a.bias + n);
+      }
+      return f;
+    };
     bool alive = true;
     int done = 0;
-    for (int at = pair; at < all; at += pairs, ++done) {
+    Factors next = factors(pair);
+    for (int at = pair; at < all && first < BN; at += pairs, ++done) {
       const Tile tile(at, t_tiles, n_tiles, BN);
       const int t0 = tile.t0 + 128 * rank + (warp & 3) * 32, n0 = tile.n0 + first;
-      named_sync(1, 32 * kEpilogueWarps);  // the tile before has been written
-      if (threadIdx.x < BN) {
-        const int n = tile.n0 + threadIdx.x;
-        ctl.column[threadIdx.x] = make_float2(a.w_row && n < a.n ? __ldg(a.w_row + n) : 1.f,
-                                              a.bias && n < a.n ? __ldg(a.bias + n) : 0.f);
-      }
-      float row = a.x_row && t0 + lane < a.t ? __ldg(a.x_row + t0 + lane) : 1.f;
-      named_sync(1, 32 * kEpilogueWarps);
-      if (first >= BN) continue;
+      Factors f = next;
+      next = factors(at + pairs);
       alive = alive && __all_sync(0xffffffffu, cluster_wait(&ctl.sums_full, done & 1, a.wait_cycles, abort_flag, a.st));
       fence_after_sync();
       float v[C::SHARE];
@@ -277,23 +290,25 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
       fence_before_sync();
       __syncwarp();
       if (lane == 0 && alive) arrive_relaxed_at(&ctl.sums_empty, 0);
-      if (!alive) row = kNaN;
+      if (!alive) f.row = kNaN;
       const int rows = min(32, a.t - t0), left = a.n - n0;
       uint8_t* y = static_cast<uint8_t*>(a.y) + (t0 * a.y_stride + n0) * item;
       if (rows <= 0) continue;
+      auto scaled = [&](int i) {  // column i of the lane's row
+        const float c = __shfl_sync(0xffffffffu, f.scale[i >> 5], i & 31);
+        const float b = a.bias ? __shfl_sync(0xffffffffu, f.add[i >> 5], i & 31) : 0.f;
+        return fmaf(v[i] * f.row, c, b);
+      };
       if (a.y_type != FP4_FP32) {
 #pragma unroll
         for (int i = 0; i < C::SHARE; i += 32) {
           if (i >= left) break;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            float f[8];
+            float q[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float2 c = column[i + 8 * k + e];
-              f[e] = fmaf(v[i + 8 * k + e] * row, c.x, c.y);
-            }
-            *staged(stage, lane, k) = a.y_type == FP4_BF16 ? attn::pack8<attn::Brain>(f) : attn::pack8<attn::Half>(f);
+            for (int e = 0; e < 8; ++e) q[e] = scaled(i + 8 * k + e);
+            *staged(stage, lane, k) = a.y_type == FP4_BF16 ? attn::pack8<attn::Brain>(q) : attn::pack8<attn::Half>(q);
           }
           write_staged(stage, lane, args.vector, y + 2 * i, step, 2, rows, left - i);
         }
@@ -303,13 +318,10 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
           if (i >= left) break;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            float f[4];
+            float q[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 c = column[i + 4 * k + e];
-              f[e] = fmaf(v[i + 4 * k + e] * row, c.x, c.y);
-            }
-            *staged(stage, lane, k) = *reinterpret_cast<const uint4*>(f);
+            for (int e = 0; e < 4; ++e) q[e] = scaled(i + 4 * k + e);
+            *staged(stage, lane, k) = *reinterpret_cast<const uint4*>(q);
           }
           write_staged(stage, lane, args.vector, y + 4 * i, step, 4, rows, left - i);
         }
