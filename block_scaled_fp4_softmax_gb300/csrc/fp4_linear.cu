@@ -433,8 +433,11 @@ int launch(LinearArgs& a, const fp4_matrix* x, const fp4_matrix& w, int sms, cud
   if (a.t <= 16) return launch<FMT, 16, false>(a, x, w, split_of(a, 16, sms), sms, st);
   if (a.t <= 32) return launch<FMT, 32, false>(a, x, w, split_of(a, 32, sms), sms, st);
   if (a.t <= 64) return launch<FMT, 64, false>(a, x, w, split_of(a, 64, sms), sms, st);
-  if (a.t > 256) return launch_wide(a, *x, w, sms, st);
-  return launch<FMT, 128, false>(a, x, w, split_of(a, 128, sms), sms, st);
+  // More rows: pairs of CTAs, unless there are so few tiles that each can have four CTAs or
+  // more (504 x 4096 x 1024: 9.8 us against 11.9 of the pairs; with two to a tile the pairs are as
+  // fast, 1024 x 4096 x 1024 12.4 and 11.9, and with one faster, 160 x 2560 x 8192 17.5 and 10.3).
+  const int split = split_of(a, 128, sms);
+  return split >= 4 ? launch<FMT, 128, false>(a, x, w, split, sms, st) : launch_wide(a, *x, w, sms, st);
 }
 
 // Where fp4_linear_rows keeps its quantised rows.
