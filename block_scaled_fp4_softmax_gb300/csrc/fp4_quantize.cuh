@@ -124,17 +124,17 @@ __device__ __forceinline__ uint32_t quantize8(const float (&v)[8], uint32_t top,
     const float s = moe::e4m3x2_to_f32x2(scale).x;
     // 1 / s of a number of four bits: one step of Newton's method rounds it correctly
     const float y0 = reciprocal(s), y = fmaf(fmaf(-s, y0, 1.f), y0, y0);
-    // with the signs as they are (r = s q + (-x), q - r / s), a zero keeps its own
-    const float2 inv = make_float2(y * down, y * down), minus = make_float2(-inv.x, -inv.x);
-    const float2 s2 = make_float2(s * up, s * up), none = make_float2(-0.f, -0.f);
+    // Of the negated quotients, so that the residual is x - s q without a negation of x and a
+    // zero keeps its sign; the codes' signs are turned round at the end.
+    const float2 minus = make_float2(-y * down, -y * down), s2 = make_float2(s * up, s * up);
+    const float2 none = make_float2(-0.f, -0.f);
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-      const float2 x = make_float2(v[i], v[i + 1]), q0 = moe::ffma2(x, inv, none);
-      const float2 r = moe::ffma2(q0, s2, make_float2(-x.x, -x.y));
-      const float2 z = moe::ffma2(r, minus, q0);
+      const float2 x = make_float2(v[i], v[i + 1]), q0 = moe::ffma2(x, minus, none);
+      const float2 z = moe::ffma2(moe::ffma2(q0, s2, x), minus, q0);
       q[i] = z.x, q[i + 1] = z.y;
     }
-    if (scale != 0u) word = to_e2m1x8(q);
+    if (scale != 0u) word = to_e2m1x8(q) ^ 0x88888888u;
   } else {
     // 6 = 1.5 * 2^2
     const bool bad = top >= 0x7F800000u;
