@@ -101,15 +101,15 @@ __device__ void hold_raw(const LinearArgs& a, Control& ctl, uint8_t* held, int p
       const int col = from + first;
       float v[8];
       load(t, col, v);
-      uint32_t top = block_top<NV>(v), word;
+      uint32_t top = block_top<NV>(v), word[1];
       if (NV && scale.tiny) scale_first(scale, v, top);
-      const uint32_t four = quantize8<NV>(v, top, scale, lane, col < a.cols, word);
+      const uint32_t four = quantize<NV>(v, top, scale, lane, col < a.cols, word);
       if (col >= c1 * kChunk) continue;
       uint8_t* at = held + (size_t)(col / kChunk - c0) * part;
       const int b = col % kChunk / 2;  // byte of the row's 128
-      *reinterpret_cast<uint32_t*>(at + t * 128 + (((b >> 4) ^ (t & 7)) << 4) + (b & 15)) = word;
-      if ((lane & (kScaleLanes<NV> - 1)) == 0)
-        *reinterpret_cast<uint32_t*>(at + x_bytes + col % kChunk / (8 * kScaleLanes<NV>) * 512 + t * 16) = four;
+      *reinterpret_cast<uint32_t*>(at + t * 128 + (((b >> 4) ^ (t & 7)) << 4) + (b & 15)) = word[0];
+      if ((lane & (kScaleLanes<NV, 8> - 1)) == 0)
+        *reinterpret_cast<uint32_t*>(at + x_bytes + col % kChunk / (8 * kScaleLanes<NV, 8>) * 512 + t * 16) = four;
     }
   }
   fence_proxy_async();

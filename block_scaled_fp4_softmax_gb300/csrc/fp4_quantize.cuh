@@ -1,6 +1,6 @@
-// Quantisation of 8 elements of a row by a thread, whose neighbours have the elements beside
-// them: blocks of 16 or 32 columns are 2 or 4 neighbouring lanes, four scales (one
-// word of the tiled layout) are 8 or 16.  The whole warp takes part.
+// Quantisation of W = 8 or 16 elements of a row by a thread, whose neighbours have the
+// elements beside them: a block of 16 or 32 columns is 1, 2 or 4 neighbouring lanes, four
+// scales (one word of the tiled layout) are four times as many.  The whole warp takes part.
 #pragma once
 
 #include "fp4.cuh"
@@ -69,17 +69,21 @@ __device__ __forceinline__ float max_abs(float a, float b, float c) {
   return d;
 }
 
-template <bool NV>
-constexpr int kScaleLanes = NV ? 8 : 16;  // lanes whose blocks' scales share a word
+template <bool NV, int W>
+constexpr int kBlockLanes = (NV ? 16 : 32) / W;  // lanes that have a block
+template <bool NV, int W>
+constexpr int kScaleLanes = 4 * kBlockLanes<NV, W>;  // ... whose blocks' scales share a word
 
 // The largest magnitude of the block as a bit pattern: in that order infinities and
 // NaN are above all numbers.
-template <bool NV>
-__device__ __forceinline__ uint32_t block_top(const float (&v)[8]) {
-  const float a = max_abs(v[0], v[1], v[2]), b = max_abs(v[3], v[4], v[5]);
-  uint32_t t = __float_as_uint(max_abs(max_abs(v[6], v[7], a), b, 0.f));
-  t = max(t, __shfl_xor_sync(0xffffffffu, t, 1));
-  if (!NV) t = max(t, __shfl_xor_sync(0xffffffffu, t, 2));
+template <bool NV, int W>
+__device__ __forceinline__ uint32_t block_top(const float (&v)[W]) {
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < W; i += 2) a = max_abs(a, v[i], v[i + 1]);
+  uint32_t t = __float_as_uint(a);
+#pragma unroll
+  for (int k = 1; k < kBlockLanes<NV, W>; k *= 2) t = max(t, __shfl_xor_sync(0xffffffffu, t, k));
   return t;
 }
 
@@ -99,21 +103,21 @@ __device__ __forceinline__ RowScale row_scale(uint32_t top) {
   s.tiny = e < -110;
   return s;
 }
-__device__ __forceinline__ void scale_first(const RowScale& s, float (&v)[8], uint32_t& top) {
+template <int W>
+__device__ __forceinline__ void scale_first(const RowScale& s, float (&v)[W], uint32_t& top) {
   top = __float_as_uint(__uint_as_float(top) * s.down);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] *= s.down;
+  for (int i = 0; i < W; ++i) v[i] *= s.down;
 }
 
-// Codes of the 8 elements (`word`), and the scales of this lane's block and its neighbours':
+// Codes of the elements (`words`), and the scales of this lane's block and its neighbours':
 // the word is the one of the first of kScaleLanes lanes.  `in`: the elements exist.  A row that
 // is tiny has been scaled before.
-template <bool NV>
-__device__ __forceinline__ uint32_t quantize8(const float (&v)[8], uint32_t top, const RowScale& row, int lane, bool in,
-                                              uint32_t& word) {
-  uint32_t scale;
-  float q[8];
-  word = 0;
+template <bool NV, int W>
+__device__ __forceinline__ uint32_t quantize(const float (&v)[W], uint32_t top, const RowScale& row, int lane, bool in,
+                                             uint32_t (&words)[W / 8]) {
+  uint32_t scale, keep, turn = 0;  // masks of the codes: all or nothing, and their signs
+  float q[W];
   if (NV) {
     // Quotients by Markstein's theorem: from a correctly rounded reciprocal and a
     // quotient within an ulp, one residual gives the correctly rounded quotient (ties
@@ -129,23 +133,29 @@ __device__ __forceinline__ uint32_t quantize8(const float (&v)[8], uint32_t top,
     const float2 minus = make_float2(-y * down, -y * down), s2 = make_float2(s * up, s * up);
     const float2 none = make_float2(-0.f, -0.f);
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
+    for (int i = 0; i < W; i += 2) {
       const float2 x = make_float2(v[i], v[i + 1]), q0 = moe::ffma2(x, minus, none);
       const float2 z = moe::ffma2(moe::ffma2(q0, s2, x), minus, q0);
       q[i] = z.x, q[i + 1] = z.y;
     }
-    if (scale != 0u) word = to_e2m1x8(q) ^ 0x88888888u;
+    turn = 0x88888888u;
+    keep = scale != 0u ? 0xFFFFFFFFu : 0u;
   } else {
     // 6 = 1.5 * 2^2
     const bool bad = top >= 0x7F800000u;
     scale = bad ? 255u : (uint32_t)max(0, (int)(top >> 23) - 2 + ((top & 0x7FFFFFu) > 0x400000u));
     const float mult = power_field(254 - (int)min(scale, 253u));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = v[i] * mult;
-    if (!bad) word = to_e2m1x8(q);
+    for (int i = 0; i < W; ++i) q[i] = v[i] * mult;
+    keep = bad ? 0u : 0xFFFFFFFFu;
+  }
+#pragma unroll
+  for (int i = 0; i < W / 8; ++i) {
+    const float(&part)[8] = *reinterpret_cast<const float(*)[8]>(q + 8 * i);
+    words[i] = (to_e2m1x8(part) ^ turn) & keep;
   }
   if (!in) scale = 0;
-  constexpr int kStep = NV ? 2 : 4;
+  constexpr int kStep = kBlockLanes<NV, W>;
   uint32_t four = scale << (8 * ((lane / kStep) & 3));
   four |= __shfl_xor_sync(0xffffffffu, four, kStep);
   four |= __shfl_xor_sync(0xffffffffu, four, 2 * kStep);

@@ -43,16 +43,18 @@ __device__ __forceinline__ void store8(void* base, long long at, int type, const
 
 // Where a thread stands: blockDim.x threads (a multiple of 32) to a row, blockDim.y
 // rows to a block.
-struct Place {
+template <int W>
+struct PlaceOf {
   int t, threads, row, cols;
   bool live;
-  __device__ Place(int rows, int cols_) : t(threadIdx.x), threads(blockDim.x), cols(cols_) {
+  __device__ PlaceOf(int rows, int cols_) : t(threadIdx.x), threads(blockDim.x), cols(cols_) {
     row = blockIdx.x * blockDim.y + threadIdx.y;
     live = row < rows;
   }
-  __device__ __forceinline__ int col(int j) const { return (j * threads + t) * 8; }
+  __device__ __forceinline__ int col(int j) const { return (j * threads + t) * W; }
   __device__ __forceinline__ bool in(int j) const { return live && col(j) < cols; }
 };
+using Place = PlaceOf<8>;
 
 // Reduction over a row's threads, in a fixed order; every thread gets the result.
 // `slots` is used once in a kernel.  All threads of the block call it.
@@ -82,8 +84,8 @@ __device__ __forceinline__ float row_sum(float v, Slots& slots) {
 // zeros past the row's end.
 // ---------------------------------------------------------------------------
 
-template <int NB, bool NV>
-__device__ __forceinline__ void to_fp4(const fp4_matrix& m, const Place& p, float (&v)[NB][8], Slots& slots) {
+template <int NB, bool NV, int W>
+__device__ __forceinline__ void to_fp4(const fp4_matrix& m, const PlaceOf<W>& p, float (&v)[NB][W], Slots& slots) {
   uint32_t top[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j) top[j] = block_top<NV>(v[j]);
@@ -104,14 +106,16 @@ __device__ __forceinline__ void to_fp4(const fp4_matrix& m, const Place& p, floa
   const int tiles = scale_tiles(m.cols, NV ? MOE_FMT_NVFP4 : MOE_FMT_MXFP4);
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
-    uint32_t word;
+    uint32_t words[W / 8];
     const bool in = p.in(j);
-    const uint32_t four = quantize8<NV>(v[j], top[j], scale, p.t & 31, in, word);
+    const uint32_t four = quantize<NV>(v[j], top[j], scale, p.t & 31, in, words);
     if (in) {
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(m.codes) + ((size_t)p.row * m.cols + p.col(j)) / 2) = word;
-      if ((p.t & (kScaleLanes<NV> - 1)) == 0)
+      uint8_t* to = static_cast<uint8_t*>(m.codes) + ((size_t)p.row * m.cols + p.col(j)) / 2;
+      if constexpr (W == 16) *reinterpret_cast<uint2*>(to) = make_uint2(words[0], words[1]);
+      else *reinterpret_cast<uint32_t*>(to) = words[0];
+      if ((p.t & (kScaleLanes<NV, W> - 1)) == 0)
         *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(m.scales) +
-                                     scale_word(p.row, p.col(j) / (8 * kScaleLanes<NV>), tiles)) = four;
+                                     scale_word(p.row, p.col(j) / (W * kScaleLanes<NV, W>), tiles)) = four;
     }
   }
 }
@@ -125,21 +129,26 @@ struct QuantizeArgs {
   fp4_matrix m;
 };
 
+// (16 elements a unit: what is done for a block is done by one thread or two)
 template <int NB, int TYPE, bool NV>
-__global__ void __launch_bounds__(NB <= 2 ? 256 : 512) quantize_kernel(const __grid_constant__ QuantizeArgs a) {
+__global__ void __launch_bounds__(512) quantize_kernel(const __grid_constant__ QuantizeArgs a) {
   __shared__ Slots slots;
-  const Place p(a.m.rows, a.m.cols);
+  const PlaceOf<16> p(a.m.rows, a.m.cols);
   moe::pdl_wait();
   moe::pdl_launch_dependents();
-  Raw<TYPE> raw[NB];
+  Raw<TYPE> raw[NB][2];
 #pragma unroll
-  for (int j = 0; j < NB; ++j) {
-    if (p.in(j)) raw[j].load(a.x.data, p.row * a.x.stride + p.col(j));
-    else raw[j].zero();
-  }
-  float v[NB][8];
+  for (int j = 0; j < NB; ++j)
 #pragma unroll
-  for (int j = 0; j < NB; ++j) raw[j].floats(v[j]);
+    for (int k = 0; k < 2; ++k) {
+      if (p.in(j)) raw[j][k].load(a.x.data, p.row * a.x.stride + p.col(j) + 8 * k);
+      else raw[j][k].zero();
+    }
+  float v[NB][16];
+#pragma unroll
+  for (int j = 0; j < NB; ++j)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) raw[j][k].floats(*reinterpret_cast<float(*)[8]>(&v[j][8 * k]));
   to_fp4<NB, NV>(a.m, p, v, slots);
 }
 
@@ -355,9 +364,9 @@ __global__ void __launch_bounds__(256) tile_scales_kernel(const uint8_t* __restr
 struct Shape {
   int nb;
   dim3 grid, block;
-  void set(int rows, int cols, int units) {
+  void set(int rows, int cols, int units, int width = 8) {
     nb = units;
-    const int threads = (cols + 8 * nb * 32 - 1) / (8 * nb * 32) * 32;
+    const int threads = (cols + width * nb * 32 - 1) / (width * nb * 32) * 32;
     const int per = threads >= 256 ? 1 : threads == 32 ? 8 : 256 / threads;
     block = dim3(threads, per);
     grid = dim3((rows + per - 1) / per);
@@ -375,6 +384,17 @@ int by_units(const LightShape& s, F f) {
          : s.nb == 2 ? f(std::integral_constant<int, 2>())
          : s.nb == 4 ? f(std::integral_constant<int, 4>())
                      : f(std::integral_constant<int, 8>());
+}
+// ... and of the quantiser, in units of 16.
+struct QuantizeShape : Shape {
+  QuantizeShape(int rows, int cols) {
+    set(rows, cols, cols > 16384 ? 4 : cols > 8192 || (rows >= 1024 && cols >= 1024) ? 2 : 1, 16);
+  }
+};
+template <class F>
+int by_units(const QuantizeShape& s, F f) {
+  return s.nb == 1 ? f(std::integral_constant<int, 1>()) : s.nb == 2 ? f(std::integral_constant<int, 2>())
+                                                                   : f(std::integral_constant<int, 4>());
 }
 // Of the norm's, whose threads hold four operands of each unit.
 struct HeavyShape : Shape {
@@ -426,7 +446,7 @@ int fp4_quantize(const void* x, long long x_stride, int x_type, const fp4_matrix
   if (const int rc = fp4::check_rows(a.x, out->rows, out->cols, true)) return rc;
   if (out->rows == 0) return MOE_OK;
   one_row(a.x, out->rows);
-  const LightShape s(out->rows, out->cols);
+  const QuantizeShape s(out->rows, out->cols);
   return by_units(s, [&](auto nb) {
     return by_type(x_type, [&](auto type) {
       return moe::launch_pdl(out->format == MOE_FMT_NVFP4 ? quantize_kernel<nb, type, true> : quantize_kernel<nb, type, false>,
