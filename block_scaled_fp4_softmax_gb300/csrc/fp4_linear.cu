@@ -13,8 +13,16 @@
 // made (two places in TMEM).  Where there are fewer tiles than SMs, a tile's columns are split
 // over a cluster of CTAs, whose sums meet in distributed shared memory in a fixed order.
 //
-// Up to 16 rows of x stay in shared memory for all tiles (HELD), if they fit.  Of a few
-// elements in all, each CTA quantises them itself, which saves a launch.
+// Up to 16 rows of x stay in shared memory for all tiles (HELD), if they fit.  One or two rows of
+// up to 32768 elements in all are quantised by each CTA itself, which saves a launch (2 us on the host)
+// and 0.5 to 1 us of the GPU; with four rows it would cost 0.5 to 1.6.
+//
+// What bounds it: the weights' bytes, 0.5625 of an element, from HBM; below some 20 MB of them the
+// chain of launch, loads, products and the exchange (3.7 us with next to no weights, 5.2 with a
+// cluster).  Measured, NVFP4, matrices of x, copy bandwidth 6.68 TB/s:
+//   7 x 2560 x 200000    50 us, 5.8 TB/s        7 x 2560 x 50257     17 us, 4.2 TB/s (393 tiles: three
+//   16 x 2560 x 8192     7.8 us                 rounds of 152 SMs, the last with 89 of them)
+//   504 x 4096 x 1024 (MXFP4, four CTAs a tile)   9.8 us
 #include <math.h>
 
 #include "fp4_mma.cuh"

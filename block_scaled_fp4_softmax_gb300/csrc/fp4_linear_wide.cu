@@ -9,6 +9,18 @@
 //
 // Barriers: full (the copies of both CTAs, at the first), empty and sums_full (commits, to
 // both CTAs), sums_empty (the epilogue warps of both CTAs, at the first).
+//
+// What bounds it: the copies into shared memory.  A chunk of a tile of 256 x 256 is 38 KB for each SM and 512
+// cycles of MMAs; with the copies it takes 626 (61 bytes a cycle and SM, 14.7 TB/s from L2 in all), with
+// the copies announced but not made 512.  Copies of scales to TMEM and the issue hide beside the MMAs.
+// Narrower tiles have more bytes an MMA and pay where they fill the rounds of tiles better.
+// The MMA is the one of 64 columns a step, half of what the card's FP4 peak is quoted with 96.
+// Measured (library GEMM in BF16 1.96 PFLOP/s):
+//   16384 x 8192 x 8192   NVFP4   315 to 339 us, 6.5 to 7.0 PFLOP/s (the card's clocks differ)
+//   4096 x 8192 x 8192    NVFP4    85 us, 6.5 PFLOP/s        MXFP4   83 us, 6.6 PFLOP/s
+//   2451 x 4096 x 5760    MXFP4    29 us, 4.0 PFLOP/s (4 rounds of 300 tiles of 192 columns)
+//   256 x 2560 x 8192     NVFP4    10 us
+// A launch costs 7 to 8 us beside its chunks: set-up, first copies, the last tile's epilogue.
 #include "fp4_mma.cuh"
 
 using namespace moe::tc;

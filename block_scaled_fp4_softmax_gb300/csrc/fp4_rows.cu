@@ -1,14 +1,24 @@
 // What stands between FP4 products: quantisation, SwiGLU and the norms around a
 // residual sum, row by row, and the way back to 16 or 32 bits.
 //
-// A row belongs to `threads` consecutive threads; a thread holds NB units of 8
-// columns, unit u = j * threads + t, so every load and store of a warp is
-// contiguous.  A block of 16 or 32 columns is 2 or 4 neighbouring lanes, four scales
-// (one 32-bit word of the tiled layout) are 8 or 16.  The row stays in registers between its
-// reductions: each element is read once and written once.
+// A row belongs to `threads` consecutive threads; a thread holds NB units of W columns, unit
+// u = j * threads + t.  A block of 16 or 32 columns is 1, 2 or 4 neighbouring lanes, four
+// scales (one 32-bit word of the tiled layout) are four times as many.  The row stays in registers between
+// its reductions: each element is read once and written once.
 //
-// What bounds these: HBM (they move 3 to 14 bytes for some 20 instructions an
-// element), and for few rows the launch and the row's two or three reductions.
+// Units are of 8 columns, so that the loads and stores of a warp are contiguous.  The quantiser takes
+// 16: then one lane works out a block's scale instead of two (or two instead of four), and the loads of 32
+// bytes a lane meet in L1 (69 us became 56 in the first case below).  SwiGLU and the norm hold two to
+// four operands of a unit and gain nothing by that (97 us for 96, 70 for 65 with NVFP4 below).
+//
+// What bounds these: HBM, or for 16-bit rows into FP4 the issue slots beside it; for few rows
+// the launch and the row's reductions.  Measured, copy bandwidth 6.68 TB/s, bytes as they have to be moved:
+//   NVFP4 of 16384 x 8192 in BF16              56 us, 6.1 TB/s     of 50257 x 2560 in FP32   84 us, 7.0 TB/s
+//   MXFP4 of 19608 x 4096 in FP16              30 us, 6.7 TB/s     back to BF16              32 us, 6.4 TB/s
+//   SwiGLU of 19608 x 5760 in BF16, to BF16    96 us, 7.1 TB/s     to NVFP4                  97 us, 5.3 TB/s
+//   norms of 19608 x 4096 in BF16 round a block in FP32, a gate for each element   168 us, 6.7 TB/s
+//   19608 x 2560 in BF16, one norm, to BF16    62 us, 6.5 TB/s     to NVFP4                  66 us, 5.0 TB/s
+//   one row of 2560: 1.4 us quantised, 2.1 through SwiGLU, 4.1 through both norms
 #include <math.h>
 
 #include <type_traits>
