@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         }
       }
     }
-    cluster_sync();  // the others have read this CTA's part
+    cluster_sync_relaxed();  // the others have read this CTA's part
   }
   fence_before_sync();
   __syncthreads();

@@ -56,8 +56,8 @@ struct Control {
   uint64_t full[8], empty[8];
   uint64_t sums_full, sums_empty, drain;
   uint32_t tmem;
-  int abort;
-  int loaded;  // chunks whose copies the CTA has issued, at its end
+  int abort, peer_abort;  // a wait has run out, in this CTA or in the other one
+  int loaded;             // chunks whose copies the CTA has issued, at its end
 };
 template <class C>
 constexpr size_t smem_bytes() {
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
     mbar_init(&ctl.sums_full, 1 + a.extra);
     mbar_init(&ctl.sums_empty, 2 * 4 * (BN / C::SHARE));
     mbar_init(&ctl.drain, 1);
-    ctl.abort = 0;
+    ctl.abort = ctl.peer_abort = 0;
     mbar_fence_init();
     attn::prefetch_map(&a.w_map);
     attn::prefetch_map(&a.x_map);
@@ -193,6 +193,9 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
         }
       }
       ctl.loaded = i;
+      // the commits that free the last slots have arrived: none is under way at the CTA's end
+      for (int k = max(0, i - C::SLOTS); k < i && alive; ++k)
+        alive = cluster_wait(&ctl.empty[k % C::SLOTS], (k / C::SLOTS) & 1, a.wait_cycles, abort_flag, a.st);
     }
     __syncwarp();
   } else if (warp == kMmaWarp && rank == 1) {
@@ -248,6 +251,9 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
         if (++slot == C::SLOTS) slot = 0, round ^= 1;
       }
     }
+    // ... nor an arrival of the other CTA's epilogue
+    if (alive && done > 0) cluster_wait(&ctl.sums_empty, (done - 1) & 1, a.wait_cycles, abort_flag, a.st);
+    __syncwarp();
     // TMEM and the ring go back only when every MMA has completed
     if (leader) {
       asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&ctl.drain))
@@ -305,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
       if (!alive) f.row = kNaN;
       const int rows = min(32, a.t - t0), left = a.n - n0;
       uint8_t* y = static_cast<uint8_t*>(a.y) + (t0 * a.y_stride + n0) * item;
-      if (rows <= 0) continue;
+      if (rows <= 0 || left <= 0) continue;
       auto scaled = [&](int i) {  // column i of the lane's row
         const float c = __shfl_sync(0xffffffffu, f.scale[i >> 5], i & 31);
         const float b = a.bias ? __shfl_sync(0xffffffffu, f.add[i >> 5], i & 31) : 0.f;
@@ -340,22 +346,35 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
       }
     }
   }
+  // No CTA's shared memory or TMEM is in use by the other any more: all copies have landed, all
+  // MMAs have completed and all arrivals have come, unless a wait has run out in one of the two.  That
+  // one says so to the other before it arrives.
   __syncthreads();
-  cluster_sync();  // every MMA has completed; the copies have, unless a wait has run out
-  if (rank == 0 && threadIdx.x == 0) {
-    // Then one CTA may have stopped a few copies before the other: what the barriers still
-    // expect of it is struck off, what they do not expect is added.
-    const int mine = ctl.loaded, other = (int)peer_word(smem_u32(&ctl.loaded), 1);
-    for (int k = max(0, max(mine, other) - C::SLOTS); k < max(mine, other); ++k) {
-      uint64_t* bar = &ctl.full[k % C::SLOTS];
-      if (k >= other)
-        asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(C::SLOT)
-                     : "memory");
-      if (k >= mine) mbar_arrive_expect_tx(bar, C::SLOT);
-      attn::bounded_wait(bar, (k / C::SLOTS) & 1, attn::kDrainCycles, nullptr, a.st);
-    }
+  const bool gave_up = *abort_flag;
+  if (gave_up) {
+    if (threadIdx.x == 0) set_peer_word(smem_u32(&ctl.peer_abort), rank ^ 1, 1);
+    cluster_sync();
+  } else {
+    cluster_sync_relaxed();
   }
-  cluster_sync();  // no CTA's shared memory or TMEM is in use by the other any more
+  if (gave_up || *(volatile int*)&ctl.peer_abort) {
+    cluster_sync();
+    if (rank == 0 && threadIdx.x == 0) {
+      // One CTA may have stopped a few copies before the other: what the barriers still expect
+      // of it is struck off, what they do not expect is added.
+      const int mine = ctl.loaded, other = (int)peer_word(smem_u32(&ctl.loaded), 1);
+      for (int k = max(0, max(mine, other) - C::SLOTS); k < max(mine, other); ++k) {
+        uint64_t* bar = &ctl.full[k % C::SLOTS];
+        if (k >= other)
+          asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(C::SLOT)
+                       : "memory");
+        if (k >= mine) mbar_arrive_expect_tx(bar, C::SLOT);
+        attn::bounded_wait(bar, (k / C::SLOTS) & 1, attn::kDrainCycles, nullptr, a.st);
+      }
+    }
+    __syncthreads();
+    cluster_sync();
+  }
   if (warp == kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM) : "memory");
 }

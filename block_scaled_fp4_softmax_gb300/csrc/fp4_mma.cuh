@@ -100,6 +100,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same for the order of execution alone: what was written before need not be seen by the
+// others (a release waits for every store that is under way, some 1300 cycles behind an epilogue).
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
 // What CTA `rank` of the cluster has at an address of this one's shared memory.
 __device__ __forceinline__ uint32_t peer_address(uint32_t saddr, int rank) {
   uint32_t at;
@@ -147,6 +152,9 @@ __device__ __forceinline__ bool cluster_wait(uint64_t* bar, uint32_t parity, lon
   return true;
 }
 
+__device__ __forceinline__ void set_peer_word(uint32_t saddr, int rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_address(saddr, rank)), "r"(v) : "memory");
+}
 // (volatile alone: behind the barriers of the cluster, but several at a time)
 __device__ __forceinline__ float4 peer_float4(uint32_t saddr, int rank) {
   float4 v;
