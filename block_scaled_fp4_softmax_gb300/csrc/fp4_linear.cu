@@ -20,9 +20,9 @@
 // What bounds it: the weights' bytes, 0.5625 of an element, from HBM; below some 20 MB of them the
 // chain of launch, loads, products and the exchange (3.7 us with next to no weights, 5.2 with a
 // cluster).  Measured, NVFP4, matrices of x, copy bandwidth 6.68 TB/s:
-//   7 x 2560 x 200000    50 us, 5.8 TB/s        7 x 2560 x 50257     17 us, 4.2 TB/s (393 tiles: three
-//   16 x 2560 x 8192     7.8 us                 rounds of 152 SMs, the last with 89 of them)
-//   504 x 4096 x 1024 (MXFP4, four CTAs a tile)   9.8 us
+//   7 x 2560 x 200000    51 us, 5.7 TB/s        7 x 2560 x 50257     17 us, 4.2 TB/s (393 tiles: three
+//   16 x 2560 x 8192     7.7 us                 rounds of 152 SMs, the last with 89 of them)
+//   504 x 4096 x 1024 (MXFP4, four CTAs a tile)   9.3 us
 #include <math.h>
 
 #include "fp4_mma.cuh"
@@ -442,8 +442,9 @@ int launch(LinearArgs& a, const fp4_matrix* x, const fp4_matrix& w, int sms, cud
   if (a.t <= 32) return launch<FMT, 32, false>(a, x, w, split_of(a, 32, sms), sms, st);
   if (a.t <= 64) return launch<FMT, 64, false>(a, x, w, split_of(a, 64, sms), sms, st);
   // More rows: pairs of CTAs, unless there are so few tiles that each can have four CTAs or
-  // more (504 x 4096 x 1024: 9.8 us against 11.9 of the pairs; with two to a tile the pairs are as
-  // fast, 1024 x 4096 x 1024 12.4 and 11.9, and with one faster, 160 x 2560 x 8192 17.5 and 10.3).
+  // more (504 x 4096 x 1024: 9.3 us against 10.8 of the pairs, 128 x 16384 x 1024 11.7 and 24.7; with two to a
+  // tile the pairs are faster, 1024 x 4096 x 1024 11.9 and 10.8, 96 x 2560 x 8192 10.4 and 9.7, and
+  // more so with one, 160 x 2560 x 8192 17.5 and 9.3).
   const int split = split_of(a, 128, sms);
   return split >= 4 ? launch<FMT, 128, false>(a, x, w, split, sms, st) : launch_wide(a, *x, w, sms, st);
 }

@@ -18,9 +18,9 @@
 // Measured (library GEMM in BF16 1.96 PFLOP/s):
 //   16384 x 8192 x 8192   NVFP4   315 to 339 us, 6.5 to 7.0 PFLOP/s (the card's clocks differ)
 //   4096 x 8192 x 8192    NVFP4    85 us, 6.5 PFLOP/s        MXFP4   83 us, 6.6 PFLOP/s
-//   2451 x 4096 x 5760    MXFP4    29 us, 4.0 PFLOP/s (4 rounds of 300 tiles of 192 columns)
-//   256 x 2560 x 8192     NVFP4    10 us
-// A launch costs 7 to 8 us beside its chunks: set-up, first copies, the last tile's epilogue.
+//   2451 x 4096 x 5760    MXFP4    27 us, 4.2 PFLOP/s (4 rounds of 300 tiles of 192 columns)
+//   256 x 2560 x 8192     NVFP4    9.3 us
+// A launch costs 6 to 7 us beside its chunks: set-up, first copies, the last tile's epilogue.
 #include "fp4_mma.cuh"
 
 using namespace moe::tc;
@@ -409,16 +409,20 @@ int launch(LinearArgs& a, const fp4_matrix& x, const fp4_matrix& w, int sms, cud
 }
 
 // The width of a tile that gives the least time: rounds of tiles over the pairs, each of
-// its chunks (2 cycles a column of y, or the 400 that issuing takes) and some 2500 cycles
-// between tiles.
+// its chunks (626, 580 and 500 cycles, which the copies take) and some 2500 cycles between
+// tiles.  With 256, 192 and 128 columns a tile, in us:
+//   512 x 9728 x 2560 17.5 17.1 15.5 (one round of each)    504 x 4096 x 5120 11.7 11.1 14.5
+//   4096 x 4096 x 5120 36.8 39.2 47.9 (5, 6, 9 rounds)      2451 x 2880 x 4096 20.9 19.1 23.8
+//   1024 x 4096 x 4096 12.0 16.6 14.9 (1, 2, 2 rounds)      8192 x 2560 x 7680 62.3 69.9 88.7
 template <int FMT>
 int by_width(LinearArgs& a, const fp4_matrix& x, const fp4_matrix& w, int sms, cudaStream_t st) {
-  const int widths[3] = {256, 192, 128};
+  const int widths[3] = {256, 192, 128}, cycles[3] = {626, 580, 500};
   long long best = 1ll << 62;
   int width = 0;
-  for (int b : widths) {
+  for (int i = 0; i < 3; ++i) {
+    const int b = widths[i];
     const long long tiles = (long long)((a.t + 255) / 256) * ((a.n + b - 1) / b), rounds = (tiles + sms / 2 - 1) / (sms / 2);
-    const long long cost = rounds * ((a.cols + kChunk - 1) / kChunk * (2 * b > 400 ? 2 * b : 400) + 2500);
+    const long long cost = rounds * ((a.cols + kChunk - 1) / kChunk * cycles[i] + 2500);
     if (cost < best) best = cost, width = b;
   }
   return width == 256 ? launch<FMT, 256>(a, x, w, sms, st) : width == 192 ? launch<FMT, 192>(a, x, w, sms, st)
