@@ -18,11 +18,11 @@
 // and 0.5 to 1 us of the GPU; with four rows it would cost 0.5 to 1.6.
 //
 // What bounds it: the weights' bytes, 0.5625 of an element, from HBM; below some 20 MB of them the
-// chain of launch, loads, products and the exchange (3.7 us with next to no weights, 5.2 with a
+// chain of launch, loads, products and the exchange (4.1 us with next to no weights, 5.2 with a
 // cluster).  Measured, NVFP4, matrices of x, copy bandwidth 6.68 TB/s:
 //   7 x 2560 x 200000    51 us, 5.7 TB/s        7 x 2560 x 50257     17 us, 4.2 TB/s (393 tiles: three
-//   16 x 2560 x 8192     7.7 us                 rounds of 152 SMs, the last with 89 of them)
-//   504 x 4096 x 1024 (MXFP4, four CTAs a tile)   9.3 us
+//   16 x 2560 x 8192     6.8 us                 rounds of 152 SMs, the last with 89 of them)
+//   504 x 4096 x 1024 (MXFP4, four CTAs a tile)   8.8 us
 #include <math.h>
 
 #include "fp4_mma.cuh"
@@ -61,64 +61,60 @@ struct Control {
   uint64_t full[10], empty[10], sums_full[2], sums_empty[2], x_full, drain;
   uint32_t tmem;
   int abort;
-  uint32_t row_top[4][16];
-  float row_scale[16];
+  uint32_t row_top[4][kMaxRawRows];
+  // factors of the CTA's rows of x, and with a cluster of its tile's columns of y
+  alignas(16) float x_row[128];
+  alignas(16) float w_row[128], bias[128];
 };
 constexpr int kRoom = 227 * 1024 - 1024 - (int)sizeof(Control);  // for the ring and the held rows
 
 // Quantises all of x for the CTA's chunks c0 .. c1 - 1, as fp4_quantize does, with the four
-// epilogue warps: all on one row, two on each of two, one on each of more.
+// epilogue warps: all on one row, two on each of two.
 template <int FMT, int TYPE>
 __device__ void hold_raw(const LinearArgs& a, Control& ctl, uint8_t* held, int part, int x_bytes, int c0, int c1) {
   constexpr bool NV = FMT == MOE_FMT_NVFP4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int share = a.t == 1 ? 4 : a.t == 2 ? 2 : 1, mine = warp % share;  // warps of a row, and which of them
-  const int t0 = warp / share, step = 4 / share, first = (mine * 32 + lane) * 8, width = share * 256;
-  auto load = [&](int t, int col, float(&v)[8]) {
+  static_assert(kMaxRawRows == 2, "the warps' shares");
+  const int share = a.t == 1 ? 4 : 2, mine = warp % share, t = warp / share;  // warps of a row, which of them, the row
+  const int first = (mine * 32 + lane) * 8, width = share * 256;
+  auto load = [&](int col, float(&v)[8]) {
     Raw<TYPE> raw;
     if (col < a.cols) raw.load(a.raw.data, t * a.raw.stride + col);
     else raw.zero();
     raw.floats(v);
   };
+  RowScale scale;
   if (NV) {
-    for (int t = t0; t < a.t; t += step) {
-      uint32_t top = 0;
+    uint32_t top = 0;
 #pragma unroll 4
-      for (int col = first; col < a.cols; col += width) {
-        float v[8];
-        load(t, col, v);
-        const float b = max_abs(max_abs(v[0], v[1], v[2]), max_abs(v[3], v[4], v[5]), max_abs(v[6], v[7], 0.f));
-        top = max(top, __float_as_uint(b));
-      }
-      top = __reduce_max_sync(0xffffffffu, top);
-      if (lane == 0) ctl.row_top[mine][t] = top;
-    }
-    named_sync(1, 128);
-  }
-  const int end = min(c1 * kChunk, (a.cols + 63) / 64 * 64);  // whole words of NVFP4's scales
-  for (int t = t0; t < a.t; t += step) {
-    RowScale scale;
-    if (NV) {
-      uint32_t top = ctl.row_top[0][t];
-      for (int k = 1; k < share; ++k) top = max(top, ctl.row_top[k][t]);
-      scale = row_scale(top);
-    }
-    if (mine == 0 && lane == 0) ctl.row_scale[t] = scale.value();
-#pragma unroll 4
-    for (int from = c0 * kChunk; from < end; from += width) {
-      const int col = from + first;
+    for (int col = first; col < a.cols; col += width) {
       float v[8];
-      load(t, col, v);
-      uint32_t top = block_top<NV>(v), word[1];
-      if (NV && scale.tiny) scale_first(scale, v, top);
-      const uint32_t four = quantize<NV>(v, top, scale, lane, col < a.cols, word);
-      if (col >= c1 * kChunk) continue;
-      uint8_t* at = held + (size_t)(col / kChunk - c0) * part;
-      const int b = col % kChunk / 2;  // byte of the row's 128
-      *reinterpret_cast<uint32_t*>(at + t * 128 + (((b >> 4) ^ (t & 7)) << 4) + (b & 15)) = word[0];
-      if ((lane & (kScaleLanes<NV, 8> - 1)) == 0)
-        *reinterpret_cast<uint32_t*>(at + x_bytes + col % kChunk / (8 * kScaleLanes<NV, 8>) * 512 + t * 16) = four;
+      load(col, v);
+      const float b = max_abs(max_abs(v[0], v[1], v[2]), max_abs(v[3], v[4], v[5]), max_abs(v[6], v[7], 0.f));
+      top = max(top, __float_as_uint(b));
     }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) ctl.row_top[mine][t] = top;
+    named_sync(1, 128);
+    for (int k = 0; k < share; ++k) top = max(top, ctl.row_top[k][t]);
+    scale = row_scale(top);
+  }
+  if (mine == 0 && lane == 0) ctl.x_row[t] = scale.value();
+  const int end = min(c1 * kChunk, (a.cols + 63) / 64 * 64);  // whole words of NVFP4's scales
+#pragma unroll 4
+  for (int from = c0 * kChunk; from < end; from += width) {
+    const int col = from + first;
+    float v[8];
+    load(col, v);
+    uint32_t top = block_top<NV>(v), word[1];
+    if (NV && scale.tiny) scale_first(scale, v, top);
+    const uint32_t four = quantize<NV>(v, top, scale, lane, col < a.cols, word);
+    if (col >= c1 * kChunk) continue;
+    uint8_t* at = held + (size_t)(col / kChunk - c0) * part;
+    const int b = col % kChunk / 2;  // byte of the row's 128
+    *reinterpret_cast<uint32_t*>(at + t * 128 + (((b >> 4) ^ (t & 7)) << 4) + (b & 15)) = word[0];
+    if ((lane & (kScaleLanes<NV, 8> - 1)) == 0)
+      *reinterpret_cast<uint32_t*>(at + x_bytes + col % kChunk / (8 * kScaleLanes<NV, 8>) * 512 + t * 16) = four;
   }
   fence_proxy_async();
   named_sync(1, 128);
@@ -268,6 +264,19 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       else hold_raw<FMT, FP4_FP32>(a, ctl, held, C::X_PART, C::X_BYTES, c0, c1);
       if (threadIdx.x == 0) mbar_arrive(&ctl.x_full);
     }
+    // The factors are fetched while the sums are awaited: one load for each row of x behind them
+    // took 40 ns a row, and the columns' behind a cluster's exchange a trip to HBM.  (All of
+    // the CTA's tiles have the same rows of x: more than one tile of them goes to clusters only.)
+    if (!a.raw.data && threadIdx.x < BN) {
+      const int t = t_of(first) + threadIdx.x;
+      ctl.x_row[threadIdx.x] = a.x_row && t < a.t ? __ldg(a.x_row + t) : 1.f;
+    }
+    if (split > 1) {
+      const int n = n_of(first) + threadIdx.x;
+      ctl.w_row[threadIdx.x] = a.w_row && n < a.n ? __ldg(a.w_row + n) : 1.f;
+      ctl.bias[threadIdx.x] = a.bias && n < a.n ? __ldg(a.bias + n) : 0.f;
+    }
+    named_sync(1, 128);
     bool alive = true;
     int done = 0;
     for (int tile = first; tile < all; tile += step, ++done) {
@@ -293,11 +302,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
           __syncwarp();
           if (lane == 0 && alive) mbar_arrive(&ctl.sums_empty[place]);
         }
+        float row[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(row + 4 * i) = *reinterpret_cast<const float4*>(ctl.x_row + j + 4 * i);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           if (j + i >= rows || n >= a.n) break;
-          const float row = HELD && a.raw.data ? ctl.row_scale[j + i] : a.x_row ? __ldg(a.x_row + t0 + j + i) : 1.f;
-          store_one(y + (j + i) * next, 0, a.y_type, fmaf(__uint_as_float(r[i]) * row, scale, add));
+          store_one(y + (j + i) * next, 0, a.y_type, fmaf(__uint_as_float(r[i]) * row[i], scale, add));
         }
       }
     }
@@ -338,15 +349,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
       for (int u = 0; u < U; ++u) {
         const int at = q + u * kThreads, j = at >> 5, n = n0 + (at & 31) * 4;
         if (at >= q1) break;
-        const float row = HELD && a.raw.data ? ctl.row_scale[j] : a.x_row ? __ldg(a.x_row + t0 + j) : 1.f;
-        const float f[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-        uint32_t out[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float scale = a.w_row && n + e < a.n ? __ldg(a.w_row + n + e) : 1.f;
-          const float add = a.bias && n + e < a.n ? __ldg(a.bias + n + e) : 0.f;
-          out[e] = __float_as_uint(fmaf(f[e] * row, scale, add));
-        }
+        const float row = ctl.x_row[j];
+        const float4 scale = *reinterpret_cast<const float4*>(ctl.w_row + (at & 31) * 4);
+        const float4 add = *reinterpret_cast<const float4*>(ctl.bias + (at & 31) * 4);
+        const uint32_t out[4] = {__float_as_uint(fmaf(v[u].x * row, scale.x, add.x)),
+                                 __float_as_uint(fmaf(v[u].y * row, scale.y, add.y)),
+                                 __float_as_uint(fmaf(v[u].z * row, scale.z, add.z)),
+                                 __float_as_uint(fmaf(v[u].w * row, scale.w, add.w))};
         uint8_t* y = static_cast<uint8_t*>(a.y) + ((t0 + j) * a.y_stride + n) * item;
         if (((uintptr_t)y & (4 * item - 1)) == 0 && n + 4 <= a.n) {
           if (item == 4) {
@@ -442,7 +451,7 @@ int launch(LinearArgs& a, const fp4_matrix* x, const fp4_matrix& w, int sms, cud
   if (a.t <= 32) return launch<FMT, 32, false>(a, x, w, split_of(a, 32, sms), sms, st);
   if (a.t <= 64) return launch<FMT, 64, false>(a, x, w, split_of(a, 64, sms), sms, st);
   // More rows: pairs of CTAs, unless there are so few tiles that each can have four CTAs or
-  // more (504 x 4096 x 1024: 9.3 us against 10.8 of the pairs, 128 x 16384 x 1024 11.7 and 24.7; with two to a
+  // more (504 x 4096 x 1024: 8.8 us against 10.8 of the pairs, 128 x 16384 x 1024 11.7 and 24.7; with two to a
   // tile the pairs are faster, 1024 x 4096 x 1024 11.9 and 10.8, 96 x 2560 x 8192 10.4 and 9.7, and
   // more so with one, 160 x 2560 x 8192 17.5 and 9.3).
   const int split = split_of(a, 128, sms);
