@@ -381,81 +381,136 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   if (warp == kMmaWarp) tmem_dealloc(tmem, tmem_columns);
 }
 
-template <int FMT, int BN, bool HELD>
-int launch(LinearArgs& a, const fp4_matrix* x, const fp4_matrix& w, int split, int sms, cudaStream_t st) {
-  using C = Cfg<FMT, BN, HELD>;
+constexpr size_t kHalf = 113 * 1024;  // of an SM's shared memory: two CTAs find room
+
+// How many clusters of 2, 4 or 8 CTAs with so much shared memory run at the same time: a
+// GPC's SMs need not be a multiple of four (of 152 SMs, with one CTA to each, 36
+// clusters of 4 and 15 of 8; 512 x 2048 x 512 with 16 clusters of 8 took 14.9 us, not 7.3).  Looked up
+// once per device, for a kernel of its own: the others' grants of shared memory differ.
+__global__ void __launch_bounds__(kThreads, 1) nothing_kernel() {}
+int clusters_at_once(int split, bool half) {
+  static std::atomic<int> known[moe::kMaxDevices][2][3];
   static moe::SmemGrant grant;
+  const int d = moe::current_device();
+  if (d < 0) return 0;
+  std::atomic<int>& entry = known[d][half][split >> 2];
+  int n = entry.load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  if (!moe::grant_smem(nothing_kernel, 2 * kHalf, grant)) return 0;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = split, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(split);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = half ? kHalf : 2 * kHalf;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, nothing_kernel, &cfg) != cudaSuccess) return 0;
+  entry.store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// What a launch takes.
+template <int FMT, int BN, bool HELD>
+struct Plan {
+  using C = Cfg<FMT, BN, HELD>;
+  int split, clusters, slots, columns;
+  size_t smem;
+
+  // Over how many CTAs a tile's columns are split: as many as still give each tile a
+  // cluster of its own at the same time.  With up to 16 rows of x the exchange takes as long as three
+  // chunks, and that many have to go elsewhere (one CTA against two, 1 x 8192 columns of y:
+  // 3 chunks 4.2 and 5.2 us, 6 chunks 5.7 and 5.7, 10 chunks 8.1 and 6.7); with more the cluster shares
+  // the rows' epilogue too (32 rows: 2 chunks 4.7 and 4.7, 6 chunks 6.7 and 5.7).
+  Plan(const LinearArgs& a, int sms) {
+    const int chunks = chunks_of(a);
+    const long long tiles = tiles_of(a);
+    set(a, 1, sms);
+    for (int k = 2; k <= 8 && 2 * split <= chunks && tiles * k <= sms; k *= 2) {
+      Plan next = *this;
+      next.set(a, k, sms);
+      if (tiles > clusters_at_once(k, next.smem <= kHalf)) break;
+      *this = next;
+    }
+    if (BN <= 16 && chunks - (chunks + split - 1) / split < 3) set(a, 1, sms);
+  }
+  static int chunks_of(const LinearArgs& a) { return (a.cols + kChunk - 1) / kChunk; }
+  static long long tiles_of(const LinearArgs& a) { return (long long)((a.n + 127) / 128) * ((a.t + BN - 1) / BN); }
+
+ private:
+  void set(const LinearArgs& a, int split_, int sms) {
+    split = split_;
+    const int most = (chunks_of(a) + split - 1) / split;  // chunks of a CTA
+    const long long tiles = tiles_of(a);
+    clusters = (int)(tiles < sms / split ? tiles : sms / split);
+    const int held = HELD ? most * C::X_PART : 0;
+    slots = held < kRoom ? C::slots_of(kRoom - held) : 0;
+    // no more than a CTA's tiles have chunks, but room for the sums that a cluster exchanges
+    const long long work = (tiles + clusters - 1) / clusters * most;
+    const int least = split > 1 ? (BN * 512 + C::SLOT - 1) / C::SLOT : 1;
+    if (slots > work) slots = (int)(work < least ? least : work);
+    // Two CTAs on an SM, of clusters in two streams, must not wait for each other's TMEM: as
+    // many as shared memory lets in have to find theirs.  So half of TMEM goes with half of
+    // the shared memory or more, and all of it with more than half.
+    smem = 1024 + (size_t)slots * C::SLOT + held + sizeof(Control);
+    columns = smem <= kHalf && C::S_COL + slots * 2 * C::S_COLS <= 256 ? 256 : 512;
+    if (smem <= kHalf) smem = columns == 256 ? kHalf : kHalf + 1024;
+  }
+};
+
+template <int FMT, int BN, bool HELD>
+int launch(LinearArgs& a, const fp4_matrix* x, const fp4_matrix& w, const Plan<FMT, BN, HELD>& p, cudaStream_t st) {
+  static moe::SmemGrant grant;
+  if (p.tiles_of(a) > 0x3FFFFFFF) return MOE_ERR_UNSUPPORTED;
   if (const int rc = codes_map(w, 128, &a.w_map)) return rc;
   if (x)
     if (const int rc = codes_map(*x, BN, &a.x_map)) return rc;
-  const int chunks = (a.cols + kChunk - 1) / kChunk, most = (chunks + split - 1) / split;  // of a CTA
-  const long long tiles = (long long)((a.n + 127) / 128) * ((a.t + BN - 1) / BN);
-  if (tiles > 0x3FFFFFFF) return MOE_ERR_UNSUPPORTED;
-  const int clusters = (int)(tiles < sms / split ? tiles : sms / split);
-  const size_t held = HELD ? (size_t)most * C::X_PART : 0;
-  int slots = C::slots_of(kRoom - (int)held);
-  // no more than a CTA's tiles have chunks, but room for the sums that a cluster exchanges
-  const long long work = (tiles + clusters - 1) / clusters * most;
-  const int least = split > 1 ? (BN * 512 + C::SLOT - 1) / C::SLOT : 1;
-  if (slots > work) slots = (int)(work < least ? least : work);
-  // Two CTAs on an SM, of clusters in two streams, must not wait for each other's TMEM: as
-  // many as shared memory lets in have to find theirs.  So half of TMEM goes with half of
-  // the shared memory or more, and all of it with more than half.
-  size_t smem = 1024 + (size_t)slots * C::SLOT + held + sizeof(Control);
-  const size_t half = 113 * 1024;
-  const int columns = smem <= half && C::S_COL + slots * 2 * C::S_COLS <= 256 ? 256 : 512;
-  if (smem <= half) smem = columns == 256 ? half : half + 1024;
-  if (!moe::grant_smem(linear_kernel<FMT, BN, HELD>, smem, grant)) return MOE_ERR_CUDA;
+  if (!moe::grant_smem(linear_kernel<FMT, BN, HELD>, p.smem, grant)) return MOE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(clusters * split));
+  cfg.gridDim = dim3((unsigned)(p.clusters * p.split));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = p.smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = split, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+  attr[1].val.clusterDim.x = p.split, attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = split > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, linear_kernel<FMT, BN, HELD>, a, split, slots, columns) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  cfg.numAttrs = p.split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, linear_kernel<FMT, BN, HELD>, a, p.split, p.slots, p.columns) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
 }
 
-// Over how many CTAs a tile's columns are split: as many as still give each tile a
-// cluster of its own at the same time.
-int split_of(const LinearArgs& a, int rows, int sms) {
-  const long long tiles = (long long)((a.n + 127) / 128) * ((a.t + rows - 1) / rows);
-  const int chunks = (a.cols + kChunk - 1) / kChunk;
-  int split = 1;
-  while (split < 8 && 2 * split <= chunks && tiles * 2 * split <= sms) split *= 2;
-  return split;
-}
 // Whether the rows of x stay in shared memory: up to 16, if they leave a ring of six slots.
 template <int FMT>
-bool holds(const LinearArgs& a, int sms) {
+bool holds(const LinearArgs& a, const Plan<FMT, 16, true>& p) {
   using C = Cfg<FMT, 16, true>;
-  if (a.t > 16) return false;
-  const int chunks = (a.cols + kChunk - 1) / kChunk, split = split_of(a, 16, sms);
-  return C::slots_of(kRoom - (chunks + split - 1) / split * C::X_PART) >= 6;
+  return a.t <= 16 && C::slots_of(kRoom - (p.chunks_of(a) + p.split - 1) / p.split * C::X_PART) >= 6;
 }
 bool holds(const LinearArgs& a, int format, int sms) {
-  return format == MOE_FMT_NVFP4 ? holds<MOE_FMT_NVFP4>(a, sms) : holds<MOE_FMT_MXFP4>(a, sms);
+  return format == MOE_FMT_NVFP4 ? holds<MOE_FMT_NVFP4>(a, {a, sms}) : holds<MOE_FMT_MXFP4>(a, {a, sms});
 }
 
 // x NULL: a.raw, which is held.
 template <int FMT>
 int launch(LinearArgs& a, const fp4_matrix* x, const fp4_matrix& w, int sms, cudaStream_t st) {
-  if (holds<FMT>(a, sms)) return launch<FMT, 16, true>(a, x, w, split_of(a, 16, sms), sms, st);
+  if (a.t <= 16) {
+    const Plan<FMT, 16, true> p(a, sms);
+    if (holds<FMT>(a, p)) return launch(a, x, w, p, st);
+  }
   if (!x) return MOE_ERR_UNSUPPORTED;  // (no call gets here)
-  if (a.t <= 16) return launch<FMT, 16, false>(a, x, w, split_of(a, 16, sms), sms, st);
-  if (a.t <= 32) return launch<FMT, 32, false>(a, x, w, split_of(a, 32, sms), sms, st);
-  if (a.t <= 64) return launch<FMT, 64, false>(a, x, w, split_of(a, 64, sms), sms, st);
-  // More rows: pairs of CTAs, unless there are so few tiles that each can have four CTAs or
-  // more (504 x 4096 x 1024: 8.8 us against 10.8 of the pairs, 128 x 16384 x 1024 11.7 and 24.7; with two to a
-  // tile the pairs are faster, 1024 x 4096 x 1024 11.9 and 10.8, 96 x 2560 x 8192 10.4 and 9.7, and
-  // more so with one, 160 x 2560 x 8192 17.5 and 9.3).
-  const int split = split_of(a, 128, sms);
-  return split >= 4 ? launch<FMT, 128, false>(a, x, w, split, sms, st) : launch_wide(a, *x, w, sms, st);
+  if (a.t <= 16) return launch<FMT, 16, false>(a, x, w, {a, sms}, st);
+  if (a.t <= 32) return launch<FMT, 32, false>(a, x, w, {a, sms}, st);
+  if (a.t <= 64) return launch<FMT, 64, false>(a, x, w, {a, sms}, st);
+  // More rows: pairs of CTAs, unless there are so few tiles that each can have four CTAs or more, and
+  // columns enough to share (504 x 8192 x 1024: 10.8 us against 13.9 of the pairs, 512 x 2048 x 512 7.3
+  // and 7.7, 504 x 1024 x 1024 7.2 and 6.7; with two to a tile the pairs are faster, 1024 x 4096
+  // x 1024 11.9 and 10.8, 96 x 2560 x 8192 10.4 and 9.7, and more so with one, 160 x 2560 x 8192 17.5 and 9.3).
+  const Plan<FMT, 128, false> p(a, sms);
+  return p.split >= 4 && a.cols > 7 * kChunk ? launch(a, x, w, p, st) : launch_wide(a, *x, w, sms, st);
 }
 
 // Where fp4_linear_rows keeps its quantised rows.
