@@ -169,15 +169,27 @@ def _matrix(m, name, index, shape, format=None):
 class Fp4Matrix:
     """A matrix in FP4: the C description plus the tensors it points into, which
     it keeps alive.  ``codes`` [rows, cols / 2] uint8, ``scales`` uint8 in the
-    layout that the products read, ``row_scale`` [rows] float32 or None."""
+    layout that products read, ``row_scale`` [rows] float32 or None: the description
+    holds their addresses, so they are written into, never replaced."""
 
     def __init__(self, codes, scales, row_scale, rows, cols, format):
-        self.codes, self.scales, self.row_scale = codes, scales, row_scale
+        _check_shape(rows, cols, format)
+        index = codes.get_device()
+        at = (_array(codes, "codes", (rows, cols // 2), _u8, index),
+              _array(scales, "scales", (_scale_bytes(rows, cols, format),), _u8, index),
+              None if row_scale is None else _array(row_scale, "row_scale", (rows,), _f32, index))
+        self._parts = codes, scales, row_scale
         self.rows, self.cols, self.format, self.shape = rows, cols, format, (rows, cols)
-        self.device, self.index = codes.device, codes.get_device()
-        self.struct = _MatrixStruct(codes.data_ptr(), scales.data_ptr(),
-                                    None if row_scale is None else row_scale.data_ptr(), rows, cols, format)
+        self.device, self.index = codes.device, index
+        self.struct = _MatrixStruct(*at, rows, cols, format)
         self.at = ctypes.addressof(self.struct)
+
+    codes = property(lambda self: self._parts[0])
+    scales = property(lambda self: self._parts[1])
+    row_scale = property(lambda self: self._parts[2])
+
+    def __reduce__(self):  # a copy, or a saved one, has a description of its own tensors
+        return Fp4Matrix, (*self._parts, self.rows, self.cols, self.format)
 
     def __repr__(self):
         return f"Fp4Matrix({self.rows} x {self.cols}, {'NVFP4' if self.format == NVFP4 else 'MXFP4'}, {self.device})"
@@ -188,6 +200,12 @@ def fp4_scale_bytes(rows: int, cols: int, format: int) -> int:
     if not (0 <= rows < 1 << 31 and 0 <= cols < 1 << 31):
         return 0
     return int(load().fp4_scale_bytes(rows, cols, format))
+
+
+def _scale_bytes(rows, cols, format):
+    """fp4_scale_bytes of a shape that has been checked, without a call."""
+    span = 4 * _BLOCK[format]
+    return (rows + 127) // 128 * ((cols + span - 1) // span) * 512
 
 
 def _check_shape(rows, cols, format):
@@ -202,7 +220,7 @@ def fp4_empty(rows: int, cols: int, format: int = NVFP4, device=None, stream=Non
     device = torch.device("cuda", _current()) if device is None else torch.device(device)
     with _elsewhere(stream):
         codes = _empty((rows, cols // 2), dtype=_u8, device=device)
-        scales = _empty(fp4_scale_bytes(rows, cols, format), dtype=_u8, device=device)
+        scales = _empty(_scale_bytes(rows, cols, format), dtype=_u8, device=device)
         row_scale = _empty(rows, dtype=_f32, device=device) if format == NVFP4 else None
     return Fp4Matrix(codes, scales, row_scale, rows, cols, format)
 
@@ -215,7 +233,7 @@ def fp4_tile_scales(scales, cols: int, format: int, tiled=None, stream=None):
     rows = scales.shape[0] if scales.dim() == 2 else -1
     _check_shape(rows, cols, format)
     at = _array(scales, "scales", (rows, cols // _BLOCK[format]), _u8, index)
-    size = fp4_scale_bytes(rows, cols, format)
+    size = _scale_bytes(rows, cols, format)
     if tiled is None:
         with _elsewhere(stream):
             tiled = _empty(size, dtype=_u8, device=scales.device)

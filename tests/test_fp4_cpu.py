@@ -1,6 +1,8 @@
 """What include/fp4.h promises and the host can show: names, sizes, the oracle's readings, refusals."""
+import copy
 import ctypes
 import os
+import pickle
 import re
 import subprocess
 import types
@@ -54,7 +56,7 @@ def test_scale_bytes(lib):
     for rows, cols, format, want in ((1, 32, NV, 512), (1, 64, NV, 512), (1, 96, NV, 1024), (128, 96, NV, 1024),
                                      (129, 96, NV, 2048), (1, 128, MX, 512), (1, 160, MX, 1024), (0, 64, NV, 0),
                                      (1 << 24, 32768, NV, (1 << 17) * 512 * 512)):
-        assert fp4.fp4_scale_bytes(rows, cols, format) == want
+        assert fp4.fp4_scale_bytes(rows, cols, format) == fp4._scale_bytes(rows, cols, format) == want
         if rows and rows < 1000:
             assert want == O.tile(np.zeros((rows, cols // O.BLOCK[format]), np.uint8)).size
     for rows, cols, format in ((-1, 64, NV), (1, 48, NV), (1, 0, NV), (1, 32800, NV), ((1 << 24) + 1, 64, NV), (1, 64, 2),
@@ -294,7 +296,8 @@ def on(t, index=0):
 
 
 def held(rows=4, cols=64, format=NV, index=0):
-    return fp4.Fp4Matrix(on(torch.zeros(rows, cols // 2, dtype=torch.uint8), index), on(torch.zeros(512, dtype=torch.uint8), index),
+    scales = torch.zeros(fp4._scale_bytes(rows, cols, format), dtype=torch.uint8)
+    return fp4.Fp4Matrix(on(torch.zeros(rows, cols // 2, dtype=torch.uint8), index), on(scales, index),
                          on(torch.ones(rows), index), rows, cols, format)
 
 
@@ -396,3 +399,30 @@ def test_shapes_of_matrices_are_refused(here):
         fp4.fp4_matrix(on(torch.zeros(4, 32)), on(torch.zeros(4, 4, dtype=torch.uint8)))
     with pytest.raises(fp4.MoeError, match="rows must be"):
         fp4.fp4_linear_rows_workspace(held(), 1 << 25)
+
+
+def test_a_matrix_is_made_of_its_parts_alone(lib):
+    """Parts that do not fit the shape would be read past their ends; a part that is replaced later
+    would leave its address behind."""
+    codes, scales, row = torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8), torch.ones(4)
+    for parts, wrong in (((codes[:3], scales, row), "codes"), ((codes, scales[:511], row), "scales"),
+                         ((codes, scales, row[:3]), "row_scale"), ((codes.float(), scales, row), "codes"),
+                         ((codes, scales.view(4, 128), row), "scales"), ((codes, scales, row.double()), "row_scale")):
+        with pytest.raises(fp4.MoeError, match=f"{wrong} must be"):
+            fp4.Fp4Matrix(*parts, 4, 64, NV)
+    with pytest.raises(fp4.MoeError, match="no FP4 matrix"):
+        fp4.Fp4Matrix(codes, scales, row, 4, 48, NV)
+    m = fp4.Fp4Matrix(codes, scales, row, 4, 64, NV)
+    for name in ("codes", "scales", "row_scale"):
+        with pytest.raises(AttributeError):
+            setattr(m, name, getattr(m, name))
+
+
+def test_copies_describe_their_own_tensors(lib):
+    codes = torch.arange(4 * 32, dtype=torch.uint8).view(4, 32)
+    m = fp4.Fp4Matrix(codes, torch.full((512,), 56, dtype=torch.uint8), None, 4, 64, NV)
+    for other in (copy.deepcopy(m), pickle.loads(pickle.dumps(m))):
+        assert other.struct.codes == other.codes.data_ptr() != codes.data_ptr() and other.struct.scales == other.scales.data_ptr()
+        assert other.struct.row_scale is None and other.row_scale is None and other.at == ctypes.addressof(other.struct)
+        assert torch.equal(other.codes, codes) and other.shape == (4, 64) and other.format == NV
+    assert copy.copy(m).struct.codes == codes.data_ptr()
