@@ -103,12 +103,18 @@ __device__ __forceinline__ void write_staged(uint8_t* stage, int lane, bool vect
       if (r < rows) *reinterpret_cast<uint4*>(to + r * step + 16 * c) = *staged(stage, r, c);
     }
   } else {  // the edge of y, or rows that do not lie on 16 bytes: 32 or 16 elements a row
+    // (eight rows at a time: 504 x 2560 x 50257 43 us, one after the other 45)
     const int per = 64 / item, first = lane / per, c = lane % per;
-    for (int r = first; r < rows; r += 32 / per) {
-      const uint8_t* from = reinterpret_cast<const uint8_t*>(staged(stage, r, (c * item) >> 4)) + ((c * item) & 15);
-      if (c >= left) continue;
-      if (item == 4) *reinterpret_cast<uint32_t*>(to + r * step + 4 * c) = *reinterpret_cast<const uint32_t*>(from);
-      else *reinterpret_cast<uint16_t*>(to + r * step + 2 * c) = *reinterpret_cast<const uint16_t*>(from);
+    auto row = [&](int r) { return reinterpret_cast<const uint8_t*>(staged(stage, r, (c * item) >> 4)) + ((c * item) & 15); };
+    if (c < left && item == 4) {
+#pragma unroll 8
+      for (int k = 0; k < 16; ++k)
+        if (const int r = first + 2 * k; r < rows)
+          *reinterpret_cast<uint32_t*>(to + r * step + 4 * c) = *reinterpret_cast<const uint32_t*>(row(r));
+    } else if (c < left) {
+#pragma unroll 8
+      for (int r = 0; r < 32; ++r)
+        if (r < rows) *reinterpret_cast<uint16_t*>(to + r * step + 2 * c) = *reinterpret_cast<const uint16_t*>(row(r));
     }
   }
   __syncwarp();
