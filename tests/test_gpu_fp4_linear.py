@@ -150,11 +150,11 @@ def test_repeats_bit_for_bit(T):
         assert torch.equal(fp4.fp4_linear(x, w, dtype=F32).view(torch.int32), want.view(torch.int32))
 
 
-@pytest.mark.parametrize("T", [1, 40, 100, 700])
-def test_streams_side_by_side_and_a_graph(T):
+@pytest.mark.parametrize("T,K", [(1, 1024), (40, 1024), (100, 1024), (100, 2080), (700, 1024)])
+def test_streams_side_by_side_and_a_graph(T, K):
     """Calls that overlap share nothing but their inputs."""
-    x = torch.randn(T, 1024, device="cuda").to(BF)
-    w = fp4.fp4_quantize(torch.randn(3000, 1024, device="cuda"))
+    x = torch.randn(T, K, device="cuda").to(BF)
+    w = fp4.fp4_quantize(torch.randn(3000, K, device="cuda"))
     want = fp4.fp4_linear_rows(x, w)
     streams = [torch.cuda.Stream() for _ in range(3)]
     outs = []
@@ -167,15 +167,15 @@ def test_streams_side_by_side_and_a_graph(T):
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         a = fp4.fp4_linear_rows(x, w)
-        b = fp4.fp4_linear_rows(a[:, :1024], w)
-    want_b = fp4.fp4_linear_rows(want[:, :1024], w)
+        b = fp4.fp4_linear_rows(a[:, :K], w)
+    want_b = fp4.fp4_linear_rows(want[:, :K], w)
     for _ in range(3):
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(a, want) and torch.equal(b, want_b)
 
 
-@pytest.mark.parametrize("T,K", [(1, 2560), (8, 256), (40, 4096), (200, 1024), (900, 1024)])
+@pytest.mark.parametrize("T,K", [(1, 2560), (8, 256), (40, 4096), (200, 1024), (200, 4096), (900, 1024)])
 def test_a_wait_that_runs_out(T, K):
     """The barrier of the sums expects an arrival that never comes: NaN, the flag, and
     the next call is right."""
@@ -276,3 +276,12 @@ def test_many_tiles_of_few_rows(format):
     """More tiles than SMs: each CTA makes several, from one ring and two places of sums."""
     for T, N, K in ((1, 30000, 288), (16, 50257, 64), (17, 40000, 96), (64, 25000, 1056), (100, 20500, 320), (9, 20000, 8224)):
         check(T, N, K, format, BF, seed=T)
+
+
+@pytest.mark.parametrize("format", [NV, MX])
+@pytest.mark.parametrize("T,N,K", [(16, 1920, 4096), (16, 2048, 4096), (60, 2048, 8192), (512, 512, 2080), (16, 4608, 8192),
+                                   (16, 4736, 8192), (4, 4736, 4096), (9, 9728, 2592), (5, 300, 1280), (16, 300, 1024)])
+def test_numbers_of_clusters(T, N, K, format):
+    """As many tiles as there are clusters of 8, 4 or 2 that run at once, and one more; columns too few to share."""
+    check(T, N, K, format, F32)
+    check(T, N, K, format, BF, bias=True)
