@@ -75,7 +75,8 @@ int fp4_quantize(const void* x, long long x_stride, int x_type, const fp4_matrix
  * nothing in what fp4_quantize made, but for magnitudes below 2^-126). */
 int fp4_dequantize(const fp4_matrix* m, void* out, long long out_stride, int out_type, void* stream);
 
-/* a = gate / (1 + exp(-gate)) * up, in FP32, for rows x cols elements.
+/* a = gate / (1 + exp(-gate)) * up, in FP32, for rows x cols elements; the quotient is
+ * -0 where exp(-gate) is 2^128 or more (gates below -88.72).
  * out (BF16 or FP16) gets a rounded, m gets a quantised as by fp4_quantize;
  * either may be NULL, not both.  gate and up are of one type. */
 int fp4_swiglu(const void* gate, long long gate_stride, const void* up, long long up_stride, int type, int rows,

@@ -186,6 +186,26 @@ def test_swiglu_extremes():
     assert torch.isnan(a[0, 3]) and torch.isinf(a[0, 9]) and torch.isnan(m.row_scale).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, FP, F32])
+def test_swiglu_of_gates_whose_exponential_is_near_the_largest_number(dtype):
+    """1 + exp(-g) above 2^126: its reciprocal is below the normal numbers, the product with the gate is not."""
+    gate = -{BF: torch.arange(73, 89, 0.5), FP: torch.arange(80.75, 88.75, 0.0625), F32: torch.linspace(80, 88.7, 2048)}[dtype]
+    gate = gate.to(dtype)[None]
+    assert gate.min() >= -88.7 and (gate < -87.5).sum() >= 2
+    for size in (1.0, -3.0, 300.0) + ((1e30,) if dtype != FP else ()):
+        up = torch.full_like(gate, size)
+        want = O.swiglu(f64(gate), f64(up))
+        # exp(-g) within 2 + |1.173 g| ulp (of 2^-23 at most), which 1 + exp(-g) takes over; its
+        # rounding and two products, half an ulp each; the reciprocal 1 ulp, and where it is
+        # subnormal (2^-128 at least, steps of 2^-149) half a step: 2^-22, 2 ulp
+        rel = (2 + 1.173 * np.abs(f64(gate)) + 1.5 + 1 + 2) * 2.0 ** -23
+        a, m = fp4.fp4_swiglu(gate.cuda(), up.cuda(), format=NV)
+        assert (np.abs(f64(a) - want) <= rounded(want, BF, np.abs(want) * rel)).all()
+        _, m = fp4.fp4_swiglu(gate.cuda(), up.cuda(), dtype=None, format=MX)
+        # (a row's scale of NVFP4 is 2^-126 at least: the smaller products above are below its codes)
+        check_fp4(m, want, rel.max())
+
+
 # ---------------------------------------------------------------------------
 # Norms around a residual sum
 # ---------------------------------------------------------------------------
