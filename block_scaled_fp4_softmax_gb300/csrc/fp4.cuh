@@ -4,6 +4,7 @@
 
 #include "common.cuh"
 #include "fp4.h"
+#include "fp4_span.h"
 
 namespace fp4 {
 
@@ -64,5 +65,17 @@ inline int check_rows(const Rows& x, int rows, int cols, bool wide) {
   if (rows > 1 && x.stride % (16 / element_bytes(x.type)) != 0) return MOE_ERR_ALIGNMENT;
   return MOE_OK;
 }
+
+// Where operands lie.  `elements`: rows that their kernel reads and writes element by element.
+inline Span span_of(const Rows& x, int rows, int cols, bool elements) {
+  Span s = rows_span(x.data, rows, cols, x.stride, element_bytes(x.type));
+  if (!elements) s.item = 0;
+  return s;
+}
+inline Span codes_span(const fp4_matrix& m) { return piece(m.codes, (long long)m.rows * m.cols / 2); }
+inline Span scales_span(const fp4_matrix& m) {
+  return piece(m.scales, (long long)((m.rows + 127) / 128) * scale_tiles(m.cols, m.format) * 512);
+}
+inline Span row_scale_span(const fp4_matrix& m) { return piece(m.row_scale, (long long)m.rows * 4); }
 
 }  // namespace fp4

@@ -560,6 +560,10 @@ int fp4_linear(const fp4_matrix* x, const fp4_matrix* w, const float* bias, void
   if (const int rc = check_output(out, x->rows, w->rows)) return rc;
   if ((uintptr_t)bias & 3u) return MOE_ERR_ALIGNMENT;
   if (x->rows == 0 || w->rows == 0) return MOE_OK;
+  const Span outs[] = {span_of(out, x->rows, w->rows, false), piece(dev_status, 4)};
+  const Span ins[] = {codes_span(*x), scales_span(*x), row_scale_span(*x),
+                      codes_span(*w), scales_span(*w), row_scale_span(*w), piece(bias, 4ll * w->rows)};
+  if (!apart(outs, ins)) return MOE_ERR_INVALID_ARG;
   const int sms = moe::device_info().sms;
   if (sms <= 0) return MOE_ERR_CUDA;
   LinearArgs a = arguments(*w, bias, out, x->rows, dev_status);
@@ -586,6 +590,10 @@ int fp4_linear_rows(const void* x, long long x_stride, int x_type, int rows, con
   if (!moe::aligned16(workspace)) return MOE_ERR_ALIGNMENT;
   const Layout l = layout(rows, w->cols, w->format);
   if (ws_bytes < l.bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const Span outs[] = {span_of(out, rows, w->rows, false), piece(workspace, (long long)l.bytes), piece(dev_status, 4)};
+  const Span ins[] = {span_of(in, rows, w->cols, false), codes_span(*w), scales_span(*w), row_scale_span(*w),
+                      piece(bias, 4ll * w->rows)};
+  if (!apart(outs, ins)) return MOE_ERR_INVALID_ARG;
   const int sms = moe::device_info().sms;
   if (sms <= 0) return MOE_ERR_CUDA;
   LinearArgs a = arguments(*w, bias, out, rows, dev_status);

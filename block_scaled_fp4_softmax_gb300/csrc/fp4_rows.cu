@@ -453,6 +453,9 @@ int fp4_tile_scales(const uint8_t* scales, int rows, int cols, int format, uint8
   if (!scales || !tiled) return MOE_ERR_INVALID_ARG;
   if (!moe::aligned16(tiled)) return MOE_ERR_ALIGNMENT;
   const int tiles = fp4::scale_tiles(cols, format);
+  const fp4::Span outs[] = {fp4::piece(tiled, (long long)fp4_scale_bytes(rows, cols, format))};
+  const fp4::Span ins[] = {fp4::piece(scales, (long long)rows * (cols / fp4::block_of(format)))};
+  if (!fp4::apart(outs, ins)) return MOE_ERR_INVALID_ARG;
   const long long blocks = ((long long)rows * tiles + 255) / 256;
   return moe::launch_pdl(tile_scales_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0,
                          (cudaStream_t)stream, scales, rows, cols / fp4::block_of(format), tiles, tiled);
@@ -465,6 +468,9 @@ int fp4_quantize(const void* x, long long x_stride, int x_type, const fp4_matrix
   if (const int rc = fp4::check_rows(a.x, out->rows, out->cols, true)) return rc;
   if (out->rows == 0) return MOE_OK;
   one_row(a.x, out->rows);
+  const fp4::Span outs[] = {fp4::codes_span(*out), fp4::scales_span(*out), fp4::row_scale_span(*out)};
+  const fp4::Span ins[] = {fp4::span_of(a.x, out->rows, out->cols, false)};
+  if (!fp4::apart(outs, ins)) return MOE_ERR_INVALID_ARG;
   const QuantizeShape s(out->rows, out->cols);
   return by_units(s, [&](auto nb) {
     return by_type(x_type, [&](auto type) {
@@ -480,6 +486,9 @@ int fp4_dequantize(const fp4_matrix* m, void* out, long long out_stride, int out
   if (const int rc = fp4::check_rows(a.out, m->rows, m->cols, true)) return rc;
   if (m->rows == 0) return MOE_OK;
   one_row(a.out, m->rows);
+  const fp4::Span outs[] = {fp4::span_of(a.out, m->rows, m->cols, false)};
+  const fp4::Span ins[] = {fp4::codes_span(*m), fp4::scales_span(*m), fp4::row_scale_span(*m)};
+  if (!fp4::apart(outs, ins)) return MOE_ERR_INVALID_ARG;
   const LightShape s(m->rows, m->cols);
   return by_units(s, [&](auto nb) {
     return by_type(out_type, [&](auto type) {
@@ -504,6 +513,9 @@ int fp4_swiglu(const void* gate, long long gate_stride, const void* up, long lon
     if (const int rc = fp4::check_target(m, rows, cols)) return rc;
   if (rows == 0) return MOE_OK;
   one_row(a.gate, rows), one_row(a.up, rows), one_row(a.out, rows);
+  const fp4::Span outs[] = {fp4::span_of(a.out, rows, cols, true), fp4::codes_span(a.m), fp4::scales_span(a.m), fp4::row_scale_span(a.m)};
+  const fp4::Span ins[] = {fp4::span_of(a.gate, rows, cols, true), fp4::span_of(a.up, rows, cols, true)};
+  if (!fp4::apart(outs, ins)) return MOE_ERR_INVALID_ARG;
   const LightShape s(rows, cols);
   return by_units(s, [&](auto nb) {
     return by_type(type, [&](auto t) {
@@ -545,6 +557,13 @@ int fp4_block_norm(const void* r, long long r_stride, int r_type, const void* y,
     if (const int rc = fp4::check_target(m, rows, cols)) return rc;
   if (rows == 0) return MOE_OK;
   for (fp4::Rows* x : {&a.r, &a.y, &a.gate, &a.r_out, &a.h}) one_row(*x, rows);
+  const fp4::Span outs[] = {fp4::span_of(a.r_out, rows, cols, true), fp4::span_of(a.h, rows, cols, true), fp4::codes_span(a.m),
+                            fp4::scales_span(a.m), fp4::row_scale_span(a.m)};
+  const fp4::Span ins[] = {fp4::span_of(a.r, rows, cols, true), fp4::span_of(a.y, rows, cols, true),
+                           gate_cols == cols ? fp4::span_of(a.gate, gate_stride == 0 ? 1 : rows, cols, true)
+                                             : fp4::span_of(a.gate, rows, 1, false),
+                           fp4::piece(post_weight, 4ll * cols), fp4::piece(weight, 4ll * cols)};
+  if (!fp4::apart(outs, ins)) return MOE_ERR_INVALID_ARG;
   const HeavyShape s(rows, cols);
   return by_units(s, [&](auto nb) {
     return by_type(r_type, [&](auto rt) {

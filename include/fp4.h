@@ -16,7 +16,10 @@
  *                     next block, into 16 bits and / or an FP4 matrix
  *   fp4_tile_scales   row-major block scales -> the layout that products read
  *
- * No output may overlap an input or another output, except where it is said.
+ * No output may share bytes with an input, another output or a workspace
+ * (MOE_ERR_INVALID_ARG); views of one buffer whose rows lie between one another's do not.  Only
+ * the 16- and 32-bit outputs of fp4_swiglu and fp4_block_norm may lie where an input with
+ * elements of the same size does, from the same address on and with the same stride.
  */
 #ifndef FP4_GB300_H
 #define FP4_GB300_H
@@ -89,8 +92,9 @@ int fp4_swiglu(const void* gate, long long gate_stride, const void* up, long lon
  * 1: an element for each row, at any stride.  gate is of y's type.  weight NULL: 1.  Weights
  * are FP32 [cols], 16-B aligned.
  * r_out, of r's type, gets r' rounded (NULL: it is not kept; it may be r itself,
- * with r's stride).  h (BF16 or FP16) and m (FP4) get h, either may be NULL, not
- * both; they are made from r' before it is rounded. */
+ * with r's stride, or y or a gate for each element, as said above).  h (BF16 or
+ * FP16) and m (FP4) get h, either may be NULL, not both; they are made from r'
+ * before it is rounded. */
 int fp4_block_norm(const void* r, long long r_stride, int r_type, const void* y, long long y_stride, int y_type,
                    const float* post_weight, const void* gate, long long gate_stride, int gate_cols, double scale,
                    const float* weight, double eps, int rows, int cols, void* r_out, long long r_out_stride, void* h,

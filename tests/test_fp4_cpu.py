@@ -256,6 +256,98 @@ def test_no_rows_need_nothing(lib):
     assert lib.fp4_tile_scales(None, 0, 64, NV, None, None) == OK
 
 
+# (3 x 64 BF16 rows are 384 bytes, FP32 768; a 3 x 64 NVFP4 matrix 96 + 512 + 12)
+X_AT, Y_AT, CODES, SCALES, FACTORS = 1 << 20, 1 << 21, 1 << 22, 1 << 23, 1 << 24
+
+
+def placed(codes=CODES, scales=SCALES, factors=FACTORS, **shape):
+    return matrix(codes, scales, factors, **shape)
+
+
+def test_rows_between_one_another_are_apart(tmp_path):
+    """csrc/fp4_span.h against sets of bytes by tests/fp4_span_check.cu."""
+    exe = tmp_path / "fp4_span_check"
+    cmd = [build._nvcc(), "-std=c++17", "-O2", "-gencode", "arch=compute_103a,code=sm_103a", "-I", build.CSRC, "-o", str(exe),
+           os.path.join(ROOT, "tests", "fp4_span_check.cu")]
+    r = subprocess.run(cmd, capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0, r.stderr[-2000:]
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0 and ", 0 failed" in r.stdout, r.stdout[-3000:]
+
+
+def test_outputs_over_inputs_are_refused_by_the_quantiser(lib):
+    for at in (X_AT, X_AT + 16, X_AT + 368, X_AT - 80):
+        assert lib.fp4_quantize(X_AT, 64, 0, placed(codes=at), None) == INVALID
+        assert lib.fp4_dequantize(placed(codes=at), X_AT, 64, 0, None) == INVALID
+    for at in (X_AT, X_AT + 368, X_AT - 496):
+        assert lib.fp4_quantize(X_AT, 64, 0, placed(scales=at), None) == INVALID
+        assert lib.fp4_dequantize(placed(scales=at), X_AT, 64, 0, None) == INVALID
+    for at in (X_AT, X_AT + 380, X_AT - 8):
+        assert lib.fp4_quantize(X_AT, 64, 0, placed(factors=at), None) == INVALID
+        assert lib.fp4_dequantize(placed(factors=at), X_AT, 64, 0, None) == INVALID
+    # a row behind two others that lie 256 bytes apart
+    assert lib.fp4_quantize(X_AT, 128, 0, placed(codes=X_AT + 2 * 256 + 112), None) == INVALID
+    for parts in (dict(scales=CODES + 80), dict(factors=CODES + 92), dict(factors=SCALES + 508)):
+        assert lib.fp4_quantize(X_AT, 64, 0, placed(**parts), None) == INVALID
+    for at in (X_AT, X_AT - 496):
+        assert lib.fp4_tile_scales(X_AT, 3, 64, NV, at, None) == INVALID
+
+
+def test_outputs_over_inputs_are_refused_by_swiglu(lib):
+    def call(out=(None, 0, 0), m=None, up=(Y_AT, 64), kind=0):
+        return lib.fp4_swiglu(X_AT, 64, *up, kind, 3, 64, *out, m, None)
+
+    for at in (X_AT + 16, X_AT - 128, X_AT + 128, X_AT + 256, Y_AT + 128, Y_AT - 256):  # shifted by some elements or rows
+        assert call(out=(at, 64, 0)) == INVALID
+    assert call(out=(X_AT, 72, 0)) == INVALID  # another stride
+    assert call(out=(X_AT, 64, 0), kind=2) == INVALID and call(out=(X_AT, 128, 0), kind=2) == INVALID  # other elements
+    for m in (placed(codes=X_AT), placed(scales=Y_AT), placed(factors=X_AT + 4)):
+        assert call(m=m) == INVALID
+    for m in (placed(codes=Y_AT), placed(scales=Y_AT), placed(factors=Y_AT)):
+        assert call(out=(Y_AT, 64, 0), up=(X_AT, 64), m=m) == INVALID  # two outputs
+
+
+def test_outputs_over_inputs_are_refused_by_the_norm(lib):
+    R, H, G, W, V = 1 << 25, 1 << 26, 1 << 27, 1 << 28, 1 << 29
+
+    def call(to=(None, 0), h=(H, 64, 0), m=None, r=(R, 64, 0), y=(Y_AT, 64, 0), gate=(G, 64, 64)):
+        return lib.fp4_block_norm(*r, *y, V, *gate, 1.0, W, 1e-6, 3, 64, *to, *h, m, None)
+
+    for at in (R + 128, R - 128, R + 256, R - 256, R + 16, Y_AT + 128, G + 128, G - 256, W, V, W + 240, V - 368, H, H + 128):
+        assert call(to=(at, 64)) == INVALID, at
+    for at in (R + 128, Y_AT - 128, G + 16, W, V):
+        assert call(h=(at, 64, 0)) == INVALID, at
+    assert call(to=(R, 72)) == INVALID and call(to=(Y_AT, 72)) == INVALID
+    assert call(to=(Y_AT, 64), y=(Y_AT, 64, 2), gate=(None, 0, 0)) == INVALID  # other elements
+    assert call(to=(G, 64), gate=(G, 0, 64)) == INVALID      # one row of gates for all rows
+    assert call(to=(G, 64), gate=(G + 32, 64, 1)) == INVALID  # a gate for each row
+    assert call(h=(G, 64, 0), gate=(G + 256, 0, 1)) == INVALID
+    for parts in (dict(codes=R), dict(scales=Y_AT + 128), dict(factors=G + 380), dict(codes=W), dict(scales=V), dict(factors=H)):
+        assert call(m=placed(**parts)) == INVALID, parts
+
+
+def test_outputs_over_inputs_are_refused_by_products(lib):
+    X, B, S, WS = 1 << 25, 1 << 26, 1 << 27, 1 << 28
+    x, w = matrix(X, X + 4096, X + 8192), placed()
+
+    def call(y, bias=B, status=S):
+        return lib.fp4_linear(x, w, bias, y, 3, 2, status, None)
+
+    for at in (X, X + 92, X - 32, X + 4096, X + 4096 + 508, X + 8192, X + 8200, CODES, SCALES - 4, FACTORS + 8, B, B + 8, B - 32, S, S - 32):
+        assert call(at) == INVALID, at
+    assert call(Y_AT, status=X + 4) == INVALID and call(Y_AT, status=B) == INVALID
+    size = lib.fp4_linear_rows_workspace(w, 3)
+
+    def rows(y=Y_AT, ws=WS, bias=B, x=X, status=S):
+        return lib.fp4_linear_rows(x, 64, 0, 3, w, bias, y, 3, 2, ws, size, status, None)
+
+    for at in (X, X + 380, X - 32, CODES, SCALES + 508, FACTORS, B, WS, WS + 96, S):
+        assert rows(y=at) == INVALID, at
+    for at in (X, X - 16, CODES, SCALES, FACTORS, B, Y_AT, Y_AT - 16):
+        assert rows(ws=at) == INVALID, at
+    assert rows(status=WS + 8) == INVALID
+
+
 # ---------------------------------------------------------------------------
 # Refusals of the binding: tensors that claim a device
 # ---------------------------------------------------------------------------

@@ -343,6 +343,64 @@ def test_streams_and_a_graph():
         assert torch.equal(a, b) and torch.equal(a, c)
 
 
+@pytest.mark.parametrize("rows,cols", [(1, 64), (1, 8224), (5, 640), (2100, 1056), (3, 16416)])
+def test_outputs_in_the_place_of_inputs(rows, cols):
+    """The same bits, whichever input of the same element size an output of SwiGLU or the norm replaces."""
+    def fresh():
+        return [rows_of(rows, cols, BF, s, 32) for s in (1, 2, 3)]
+
+    gate, up, _ = fresh()
+    want, m = fp4.fp4_swiglu(gate, up, format=NV)
+    want_half, _ = fp4.fp4_swiglu(gate, up, dtype=FP)
+    for at in (0, 1):
+        ops = fresh()
+        got, again = fp4.fp4_swiglu(ops[0], ops[1], format=NV, out=ops[at])
+        assert got is ops[at] and torch.equal(got, want) and torch.equal(again.codes, m.codes)
+        ops = fresh()
+        got, _ = fp4.fp4_swiglu(ops[0], ops[1], out=ops[at].view(FP))
+        assert torch.equal(got, want_half)
+    ones = torch.ones(cols, device="cuda")
+    args = dict(post_weight=ones, weight=ones, scale=0.5)
+    r, y, g = fresh()
+    want_r, want_h, m = fp4.fp4_block_norm(r, y, gate=g, format=MX, **args)
+    twice_r, twice_h, _ = fp4.fp4_block_norm(r, r, gate=g, **args)
+    for at in range(3):
+        for to in range(3):
+            ops = fresh()
+            if at != to:
+                got_r, got_h, again = fp4.fp4_block_norm(ops[0], ops[1], gate=ops[2], format=MX, r_out=ops[at], out=ops[to], **args)
+            else:
+                got_r, got_h, again = fp4.fp4_block_norm(ops[0], ops[1], gate=ops[2], format=MX, r_out=ops[at], **args)
+            assert torch.equal(got_r, want_r) and torch.equal(got_h, want_h) and torch.equal(again.codes, m.codes)
+    ops = fresh()
+    got_r, got_h, _ = fp4.fp4_block_norm(ops[0], ops[0], gate=ops[2], r_out=ops[0], **args)
+    assert torch.equal(got_r, twice_r) and torch.equal(got_h, twice_h)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 70, 300])
+def test_operands_side_by_side_in_one_buffer(rows):
+    """gate | up | out, r | y | r_out | h, x | y of a product: rows between one another's."""
+    cols = 320
+    buf = rows_of(rows, 4 * cols, BF, 4)
+    parts = [buf[:, i * cols:(i + 1) * cols] for i in range(4)]
+    apart = [p.clone() for p in parts]
+    want, _ = fp4.fp4_swiglu(apart[0], apart[1])
+    want_r, want_h, _ = fp4.fp4_block_norm(apart[0], apart[1])
+    w = fp4.fp4_quantize(torch.randn(cols, cols, device="cuda"))
+    want_y = fp4.fp4_linear_rows(apart[0], w)
+    got, _ = fp4.fp4_swiglu(parts[0], parts[1], out=parts[2])
+    assert torch.equal(got, want)
+    got_r, got_h, _ = fp4.fp4_block_norm(parts[0], parts[1], r_out=parts[2], out=parts[3])
+    assert torch.equal(got_r, want_r) and torch.equal(got_h, want_h)
+    assert torch.equal(fp4.fp4_linear_rows(parts[0], w, out=parts[3]), want_y)
+    assert torch.equal(parts[0], apart[0]) and torch.equal(parts[1], apart[1])
+    for call in (lambda: fp4.fp4_swiglu(parts[0], parts[1], out=buf[:, 32:32 + cols]),
+                 lambda: fp4.fp4_linear_rows(parts[0], w, out=parts[0]),
+                 lambda: fp4.fp4_block_norm(parts[0], parts[1], r_out=parts[2], out=buf[:, 3 * cols - 32:4 * cols - 32])):
+        with pytest.raises(fp4.MoeError, match="failed: status 1"):
+            call()
+
+
 def test_record_parts_are_matrices():
     """gate | up codes and scales of an expert record are the parts of one matrix."""
     H, I = 256, 128
