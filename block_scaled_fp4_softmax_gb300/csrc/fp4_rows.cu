@@ -338,10 +338,11 @@ __global__ void __launch_bounds__(NB <= 2 ? 256 : 512) dequantize_kernel(const _
   for (int j = 0; j < NB; ++j) {
     if (!p.in(j)) continue;
     // code * block scale is exact: at most 2 + 4 significant bits, of NVFP4 within FP16
-    // too; a power of two times the row's scale is
+    // too; of MXFP4 within FP32, with its subnormals, up to a scale of 2^125
     uint32_t s2 = 0;
     if (NV) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"((uint16_t)(b[j] | b[j] << 8)));
-    const float factor = NV ? row : moe::ue8m0_to_f32(b[j]) * row;
+    const float scale = NV ? 1.f : moe::ue8m0_to_f32(min(b[j], 252u));
+    const float2 scales2 = make_float2(scale, scale), row2 = make_float2(row, row), none = make_float2(-0.f, -0.f);
     float f[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -350,8 +351,15 @@ __global__ void __launch_bounds__(NB <= 2 ? 256 : 512) dequantize_kernel(const _
         const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&s2));
         h = *reinterpret_cast<const uint32_t*>(&v);
       }
-      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      f[2 * i] = v.x * factor, f[2 * i + 1] = v.y * factor;
+      float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      if (!NV) v = moe::ffma2(v, scales2, none);
+      v = moe::ffma2(v, row2, none);
+      f[2 * i] = v.x, f[2 * i + 1] = v.y;
+    }
+    if (!NV && b[j] > 252u) {  // what is left of the scale: 6 * 2^126 overflows, times the row's factor it need not
+      const float left = b[j] == 255u ? __uint_as_float(0x7FC00000u) : b[j] == 254u ? 4.f : 2.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] *= left;
     }
     store8(a.out.data, p.row * a.out.stride + p.col(j), TYPE, f);
   }

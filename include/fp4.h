@@ -74,8 +74,9 @@ int fp4_tile_scales(const uint8_t* scales, int rows, int cols, int format, uint8
  * fp4_pack_expert, but for the row's power of two. */
 int fp4_quantize(const void* x, long long x_stride, int x_type, const fp4_matrix* out, void* stream);
 
-/* The values of m's elements, rounded once to out's type (in BF16 that changes
- * nothing in what fp4_quantize made, but for magnitudes below 2^-126). */
+/* The values of m's elements: code * block scale, exactly, times the row scale in FP32, rounded
+ * to out's type (in BF16 that changes nothing in what fp4_quantize made, but for magnitudes
+ * below 2^-126). */
 int fp4_dequantize(const fp4_matrix* m, void* out, long long out_stride, int out_type, void* stream);
 
 /* a = gate / (1 + exp(-gate)) * up, in FP32, for rows x cols elements; the quotient is

@@ -133,6 +133,32 @@ def test_values_of_quantised_rows_are_exact_in_bf16(format):
     assert np.array_equal(f64(out[:, :512]), held(m)) and (out[:, 512:] == 7).all()
 
 
+@pytest.mark.parametrize("format", [NV, MX])
+def test_values_of_extreme_scales_and_factors(format):
+    """Every code under the smallest and the largest scales, in rows whose factors bring them back among
+    the numbers or carry them out of them: a zero stays zero, and nothing between overflows."""
+    block = O.BLOCK[format]
+    bytes_ = [0, 1, 8, 56, 0x7E, 17, 119, 2] if format == NV else [0, 1, 2, 127, 252, 253, 254, 64]
+    factors = [1.0, 2.0, 4.0, 0.75, 1e38, 3e38, -2.0 ** 100, 2.0 ** -100, 1.3 * 2.0 ** -126, 2.0 ** -140, 3 * 2.0 ** -149]
+    factors = np.array(factors, dtype=np.float32)
+    codes = np.tile(np.arange(block, dtype=np.uint8) % 16, (len(factors), len(bytes_)))
+    scales = np.tile(np.array(bytes_, dtype=np.uint8), (len(factors), 1))
+    m = fp4.fp4_matrix(torch.from_numpy(O.pack(codes)).cuda(), torch.from_numpy(scales).cuda(), torch.from_numpy(factors).cuda(), format)
+    want = O.values(codes, scales, factors, format)
+    for dtype in (F32, BF, FP):
+        got = f64(fp4.fp4_dequantize(m, dtype))
+        # the least that rounds to infinity: half a step past the largest number
+        top = {F32: 2.0 ** 128 * (1 - 2.0 ** -25), BF: 2.0 ** 128 * (1 - 2.0 ** -9), FP: 65520.0}[dtype]
+        # code * scale is exact, the row's factor one rounding in FP32 (a subnormal result: half of 2^-149)
+        slack = np.abs(want) * 2.0 ** -24 + 2.0 ** -150
+        near = 0 if dtype == F32 else slack  # (in FP32 there is that rounding alone, and `want` is exact)
+        over, under = np.abs(want) - near >= top, np.abs(want) + near < top
+        assert (over | under).all()
+        assert (got[over] == np.copysign(np.inf, want[over])).all()
+        assert (np.abs(got - want)[under] <= rounded(want, dtype, slack)[under]).all()
+        assert (got[want == 0] == 0).all()
+
+
 def test_nothing_is_written_behind_the_rows():
     x = rows_of(37, 288, BF, 11)
     big = [torch.full((200, 144), 0xA5, dtype=torch.uint8, device="cuda"),
