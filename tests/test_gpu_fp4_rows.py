@@ -42,6 +42,16 @@ def test_quantize(cols, dtype, format):
 
 
 @pytest.mark.parametrize("format", [NV, MX])
+@pytest.mark.parametrize("dtype", [BF, FP, F32])
+@pytest.mark.parametrize("cols", [16416, 24576, 32736, 32768])
+def test_quantize_the_longest_rows(cols, dtype, format):
+    for rows, pad in ((1, 0), (5, 32)):
+        x = rows_of(rows, cols, dtype, cols + rows, pad)
+        x[rows - 1, cols - 5] *= 30
+        same(fp4.fp4_quantize(x, format), x)
+
+
+@pytest.mark.parametrize("format", [NV, MX])
 def test_quantize_many_rows(format):
     x = rows_of(700, 160, BF, 1)
     same(fp4.fp4_quantize(x, format), x)
