@@ -285,3 +285,67 @@ def test_numbers_of_clusters(T, N, K, format):
     """As many tiles as there are clusters of 8, 4 or 2 that run at once, and one more; columns too few to share."""
     check(T, N, K, format, F32)
     check(T, N, K, format, BF, bias=True)
+
+
+# ---------------------------------------------------------------------------
+# Sums that FP32 holds: nothing may be missing, and every rounding is known
+# ---------------------------------------------------------------------------
+
+def whole(rows, cols, format, seed, scales):
+    """Any codes, a 6 in each block, block scales among `scales`: a matrix, its values in 64 bits."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    block = O.BLOCK[format]
+    codes = torch.randint(0, 16, (rows, cols), generator=g, device="cuda", dtype=torch.uint8)
+    codes[:, ::block] = codes[:, ::block] & 8 | 7
+    at = torch.randint(0, len(scales), (rows, cols // block), generator=g, device="cuda")
+    bytes_ = torch.tensor([0x38 + 8 * s if format == NV else 127 + s for s in scales], dtype=torch.uint8, device="cuda")[at]
+    m = fp4.fp4_matrix(codes[:, ::2] | codes[:, 1::2] << 4, bytes_, torch.ones(rows, device="cuda"), format)
+    v = torch.tensor(O.E2M1, device="cuda")[codes.int()]
+    return m, (v.unflatten(1, (-1, block)) * torch.tensor([2.0 ** s for s in scales], dtype=torch.float64, device="cuda")[at][..., None]).flatten(1)
+
+
+@pytest.mark.parametrize("format", [NV, MX])
+@pytest.mark.parametrize("T,N,K", [
+    (1, 300, 32768), (2, 300, 16384), (3, 140, 16416), (16, 1000, 32768), (16, 1000, 4128), (9, 20000, 4128), (16, 700, 32736),  # x held
+    (5, 9000, 32768), (16, 20000, 16416),                                                                     # x too long for that
+    (20, 500, 16416), (64, 500, 32768), (50, 20000, 2592), (100, 300, 32768), (300, 40, 32736), (500, 700, 16416),  # 32 to 128 rows a tile
+    (200, 700, 1056), (512, 9728, 2592), (2451, 2880, 4128), (2000, 4096, 16416),                             # pairs of CTAs
+])
+def test_sums_that_fp32_holds_exactly(T, N, K, format):
+    """Multiples of 1 / 4 below 2^22: no order of additions rounds, so a block that is lost, taken twice or
+    scaled by its neighbour's scale shows in every element; results are the nearest of their type."""
+    x, xv = whole(T, K, format, T + N + K, (0,))
+    w, wv = whole(N, K, format, T + N + K + 1, (0, 1))
+    bias = torch.randint(-4000, 4000, (N,), device="cuda").float() / 4
+    assert float((xv.abs() @ wv.abs().T).max()) + 1000 < 2.0 ** 22
+    want = xv @ wv.T
+    assert torch.equal(fp4.fp4_linear(x, w, dtype=F32).double(), want)
+    want += bias.double()
+    assert torch.equal(fp4.fp4_linear(x, w, bias=bias, dtype=F32).double(), want)
+    # values of one 6 a block at least are their own quantisation
+    rows = xv.to(F32)
+    assert torch.equal(fp4.fp4_linear_rows(rows, w, bias=bias, dtype=F32).double(), want)
+    # with powers of two as factors of rows and columns: some FP16 results overflow, to an infinity of their sign
+    x.row_scale[::2], w.row_scale[1::2] = 64, 8
+    want = (want - bias.double()) * x.row_scale.double()[:, None] * w.row_scale.double() + bias.double()
+    for dtype in (BF, FP):
+        got = fp4.fp4_linear(x, w, bias=bias, dtype=dtype)
+        assert torch.equal(got, want.to(dtype))
+    assert torch.isinf(got).any() and torch.isfinite(got).any()
+
+
+@pytest.mark.parametrize("format", [NV, MX])
+@pytest.mark.parametrize("T,N,K", [(1, 300, 640), (5, 200, 640), (33, 200, 1056), (150, 333, 640), (700, 1500, 512)])
+def test_fp16_results_within_their_range(T, N, K, format):
+    """Any scales and factors, sized so that no result passes 40000."""
+    x, xc, xs, xr = random_matrix(T, K, format, 3 * T, 0.5)
+    w, wc, ws, wr = random_matrix(N, K, format, 3 * T + 1, 0.5)
+    xv, wv = O.values(xc, xs, None, format), O.values(wc, ws, None, format)
+    wide = np.abs(xv @ wv.T * wr).max(1)
+    xr = (40000 / wide * np.random.default_rng(T).uniform(0.2, 1, T)).astype(np.float32)
+    x.row_scale.copy_(torch.from_numpy(xr))
+    b = torch.randn(N, device="cuda")
+    y = fp4.fp4_linear(x, w, bias=b, dtype=FP)
+    want = xv @ wv.T * xr[:, None].astype(np.float64) * wr.astype(np.float64) + f64(b)
+    assert np.abs(want).max() < 45000
+    assert (np.abs(f64(y) - want) <= rounded(want, FP, slack(xv, wv, xr, wr, f64(b), want))).all()
