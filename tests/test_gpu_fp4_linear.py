@@ -349,3 +349,49 @@ def test_fp16_results_within_their_range(T, N, K, format):
     want = xv @ wv.T * xr[:, None].astype(np.float64) * wr.astype(np.float64) + f64(b)
     assert np.abs(want).max() < 45000
     assert (np.abs(f64(y) - want) <= rounded(want, FP, slack(xv, wv, xr, wr, f64(b), want))).all()
+
+
+# ---------------------------------------------------------------------------
+# What was written just before
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("format", [NV, MX])
+@pytest.mark.parametrize("T", [1, 2, 3, 9, 16, 17, 40, 64, 90, 300])
+def test_weights_written_by_the_call_before(T, format):
+    """fp4_linear_rows reads w ahead of its quantisation of x: behind a call that has just written
+    w, its scales alone, or x, never before it has."""
+    N, K = 8192, 2560
+    g = torch.Generator(device="cuda").manual_seed(T)
+    sources = [torch.randn(N, K, generator=g, device="cuda") * 0.02 for _ in range(3)]
+    inputs = [torch.randn(T, K, generator=g, device="cuda").to(BF) for _ in range(3)]
+    made = [fp4.fp4_quantize(s, format) for s in sources]
+    plain = [torch.from_numpy(O.untile(m.scales.cpu().numpy(), N, K // O.BLOCK[format]).copy()).cuda() for m in made]
+    w, ws, x = fp4.fp4_empty(N, K, format), fp4.fp4_linear_rows_workspace(made[0], T), torch.empty(T, K, device="cuda", dtype=BF)
+    want = [[fp4.fp4_linear(fp4.fp4_quantize(i, format), m) for m in made] for i in inputs]
+    mixed = [fp4.Fp4Matrix(made[0].codes, m.scales, made[0].row_scale, N, K, format) for m in made]
+    want_mixed = [fp4.fp4_linear(fp4.fp4_quantize(inputs[0], format), m) for m in mixed]
+    fixed = fp4.Fp4Matrix(made[0].codes, torch.zeros_like(made[0].scales), made[0].row_scale, N, K, format)
+    torch.cuda.synchronize()
+
+    def steps(outs):
+        for i in range(6):
+            fp4.fp4_quantize(sources[i % 3], format, out=w)
+            x.copy_(inputs[i % 2])
+            outs.append((fp4.fp4_linear_rows(x, w, workspace=ws), want[i % 2][i % 3]))
+            fp4.fp4_quantize(sources[(i + 1) % 3], format, out=w)
+            outs.append((fp4.fp4_linear_rows(x, w, workspace=ws), want[i % 2][(i + 1) % 3]))
+            outs.append((fp4.fp4_linear(fp4.fp4_quantize(x, format), w), want[i % 2][(i + 1) % 3]))
+            fp4.fp4_tile_scales(plain[i % 3], K, format, tiled=fixed.scales)
+            outs.append((fp4.fp4_linear_rows(inputs[0], fixed, workspace=ws), want_mixed[i % 3]))
+
+    outs = []
+    steps(outs)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in outs)
+    graph, outs = torch.cuda.CUDAGraph(), []
+    with torch.cuda.graph(graph):
+        steps(outs)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in outs)
