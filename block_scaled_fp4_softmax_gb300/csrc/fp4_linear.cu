@@ -385,7 +385,7 @@ constexpr size_t kHalf = 113 * 1024;  // of an SM's shared memory: two CTAs find
 
 // How many clusters of 2, 4 or 8 CTAs with so much shared memory run at the same time: a
 // GPC's SMs need not be a multiple of four (of 152 SMs, with one CTA to each, 36
-// clusters of 4 and 15 of 8; 512 x 2048 x 512 with 16 clusters of 8 took 14.9 us, not 7.3).  Looked up
+// clusters of 4 and 15 of 8; 512 x 2048 x 512 with 16 clusters of 8 took 13.9 us, not 7.3).  Looked up
 // once per device, for a kernel of its own: the others' grants of shared memory differ.
 __global__ void __launch_bounds__(kThreads, 1) nothing_kernel() {}
 int clusters_at_once(int split, bool half) {

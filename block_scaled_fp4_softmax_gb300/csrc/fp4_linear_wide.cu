@@ -4,17 +4,17 @@
 // Each CTA of a pair holds its 128 rows of x and half of the tile's rows of w, so
 // that w's codes come to an SM once for 256 rows; the first of the two issues the MMAs of
 // both.  A persistent pair walks over tiles; its ring of chunks (fp4_linear.cu) runs
-// on from tile to tile, and the 8 epilogue warps take the sums from TMEM into
-// registers at once, so that the next tile's products start while they write.
+// on from tile to tile, and the epilogue warps (16, 12 or 8 for 256, 192 or 128 columns) take the
+// sums from TMEM into registers at once, so that the next tile's products start while they write.
 //
 // Barriers: full (the copies of both CTAs, at the first), empty and sums_full (commits, to
 // both CTAs), sums_empty (the epilogue warps of both CTAs, at the first).
 //
-// What bounds it: the copies into shared memory.  A chunk of a tile of 256 x 256 is 38 KB for each SM and 512
-// cycles of MMAs; with the copies it takes 626 (61 bytes a cycle and SM, 14.7 TB/s from L2 in all), with
-// the copies announced but not made 512.  Copies of scales to TMEM and the issue hide beside the MMAs.
+// What bounds it: the copies into shared memory.  A chunk of a tile of 256 x 256 in NVFP4 is 38 KB for each SM and
+// 512 cycles of MMAs; with the copies it takes 626 (62 bytes a cycle and SM), with the copies announced
+// but not made 512.  MXFP4's 35 KB take 610 (59).  Copies of scales to TMEM and the issue hide beside the MMAs.
 // Narrower tiles have more bytes an MMA and pay where they fill the rounds of tiles better.
-// The MMA is the one of 64 columns a step, half of what the card's FP4 peak is quoted with 96.
+// The MMA is the one of 64 columns a step, two thirds of the one of 96 that the card's FP4 peak is quoted with.
 // Measured (library GEMM in BF16 1.96 PFLOP/s):
 //   16384 x 8192 x 8192   NVFP4   315 to 339 us, 6.5 to 7.0 PFLOP/s (the card's clocks differ)
 //   4096 x 8192 x 8192    NVFP4    85 us, 6.5 PFLOP/s        MXFP4   83 us, 6.6 PFLOP/s
@@ -415,7 +415,8 @@ int launch(LinearArgs& a, const fp4_matrix& x, const fp4_matrix& w, int sms, cud
 }
 
 // The width of a tile that gives the least time: rounds of tiles over the pairs, each of
-// its chunks (626, 580 and 500 cycles, which the copies take) and some 2500 cycles between
+// its chunks (NVFP4's 626, 580 and 500 cycles, which the copies take; MXFP4's are 610, 558 and 494, and the
+// widths that come out below were its best ones too) and some 2500 cycles between
 // tiles.  With 256, 192 and 128 columns a tile, in us:
 //   512 x 9728 x 2560 17.5 17.1 15.5 (one round of each)    504 x 4096 x 5120 11.7 11.1 14.5
 //   4096 x 4096 x 5120 36.8 39.2 47.9 (5, 6, 9 rounds)      2451 x 2880 x 4096 20.9 19.1 23.8

@@ -4,7 +4,10 @@
 // A row belongs to `threads` consecutive threads; a thread holds NB units of W columns, unit
 // u = j * threads + t.  A block of 16 or 32 columns is 1, 2 or 4 neighbouring lanes, four
 // scales (one 32-bit word of the tiled layout) are four times as many.  The row stays in registers between
-// its reductions: each element is read once and written once.
+// its reductions: each element is read once and written once.  (Above 8192 columns the norm has
+// 64 registers a thread for four operands of 32 columns and keeps some of them in local memory: up to 252 bytes a
+// thread with a residual and a block in FP32, 8 to 40 with 16-bit residuals.  Nothing else spills but
+// SwiGLU of FP32 above 16384 columns, 64 bytes.)
 //
 // Units are of 8 columns, so that the loads and stores of a warp are contiguous.  The quantiser takes
 // 16: then one lane works out a block's scale instead of two (or two instead of four), and the loads of 32
@@ -17,7 +20,9 @@
 //   MXFP4 of 19608 x 4096 in FP16              30 us, 6.7 TB/s     back to BF16              32 us, 6.4 TB/s
 //   SwiGLU of 19608 x 5760 in BF16, to BF16    95 us, 7.1 TB/s     to NVFP4                  92 us, 5.6 TB/s
 //   norms of 19608 x 4096 in BF16 round a block in FP32, a gate for each element   168 us, 6.7 TB/s
+//   the same in FP32 throughout: 4096 x 8192   96 us, 6.3 TB/s     2048 x 16384             133 us, 4.5 TB/s
 //   19608 x 2560 in BF16, one norm, to BF16    62 us, 6.5 TB/s     to NVFP4                  66 us, 5.0 TB/s
+//   scales of 50257 x 2560 in NVFP4, laid out  13 us, 1.2 TB/s     of 65536 x 8192           54 us, 1.3 TB/s
 //   one row of 2560: 1.4 us quantised, 2.1 through SwiGLU, 4.1 through both norms
 #include <math.h>
 
@@ -365,7 +370,8 @@ __global__ void __launch_bounds__(NB <= 2 ? 256 : 512) dequantize_kernel(const _
   }
 }
 
-// A thread to the four scales of a row's tile.
+// A thread to the four scales of a row's tile.  What bounds it: words that are scattered by 16 bytes and
+// four loads of a byte for each (1.3 TB/s); once for a weight matrix.
 __global__ void __launch_bounds__(256) tile_scales_kernel(const uint8_t* __restrict__ in, int rows, int blocks,
                                                           int tiles, uint8_t* __restrict__ out) {
   moe::pdl_wait();

@@ -39,7 +39,7 @@ enum { FP4_BF16 = 0, FP4_FP16 = 1, FP4_FP32 = 2 };
  * codes [rows x cols / 2]: e2m1, two to a byte, the even column in the low
  *   nibble (the packing of an expert record), 16-B aligned.
  * scales, fp4_scale_bytes() of them, 16-B aligned: one byte for each block of
- *   16 columns (E4M3, MOE_FMT_NVFP4) or 32 (UE8M0, MOE_FMT_MXFP4), in tiles of
+ *   16 columns (E4M3, not negative, MOE_FMT_NVFP4) or 32 (UE8M0, MOE_FMT_MXFP4), in tiles of
  *   128 rows x 4 blocks.  With kt = ceil(blocks of a row / 4), block b of row r
  *   is byte ((r / 128) * kt + b / 4) * 512 + (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4.
  *   Blocks of a last tile past cols hold 0; rows past `rows` hold anything.
