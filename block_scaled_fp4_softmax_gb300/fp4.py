@@ -311,7 +311,8 @@ def _targets(shape, t, dtype, format, out, matrix, index, stream, names):
 def fp4_swiglu(gate, up, dtype=torch.bfloat16, format: int | None = None, out=None, matrix: Fp4Matrix | None = None,
                stream=None):
     """SiLU(gate) * up, [rows, cols] each.  Returns (out of dtype or None, FP4
-    matrix of format or None): dtype = None and format = None leave theirs away."""
+    matrix of format or None): dtype = None and format = None leave theirs away.
+    out may be gate or up, where its elements are as wide."""
     index = _index(gate, "gate")
     on = _on(stream, index)
     g, g_stride, kind = _rows(gate, "gate", index)
@@ -333,7 +334,8 @@ def fp4_block_norm(r, y=None, post_weight=None, gate=None, scale: float = 1.0, w
     """r_out = r + scale * gate * norm(y; post_weight) and its norm(r_out; weight).
 
     r, y [rows, cols]; weights [cols] float32; gate [cols], [rows, cols] or [rows,
-    1] of y's type.  r_out may be r.  Returns (r_out, norm of dtype or None, norm
+    1] of y's type.  r_out and out may be r, y or a [rows, cols] gate, where their
+    elements are as wide.  Returns (r_out, norm of dtype or None, norm
     as an FP4 matrix of format or None); without y, r itself is r_out."""
     index = _index(r, "r")
     on = _on(stream, index)
