@@ -167,13 +167,13 @@ __global__ void __launch_bounds__(512) quantize_kernel(const __grid_constant__ Q
   to_fp4<NB, NV>(a.m, p, v, slots);
 }
 
-// g / (1 + exp(-g)) as (g / 4) / ((1 + exp(-g)) / 4): for g between -88.7 and -87.3 the sum is above 2^126 and
-// its reciprocal below the normal numbers, while the quotient is not (g = -88: -5e-37).  Past them exp(-g) is
-// above 2^128, and the quotient -0.  (The reciprocal that keeps subnormal results: 116 us for 92 into NVFP4.)
+// g / (1 + exp(-g)), the reciprocal from a quarter of the sum: for g between -88.7 and -87.3 the sum is above
+// 2^126 and its reciprocal subnormal, to 2^-22 at worst, while the quotient is not (g = -88: -5e-37).  Past them
+// exp(-g) is above 2^128, and the quotient -0.  (rcp.approx without .ftz: 116 us for 92 into NVFP4.)
 __device__ __forceinline__ float silu(float g) {
   float e;  // exp(-g) / 4, the exponential of 2 within 2 ulp; below 2^-126 it is 0
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(g, -1.44269504f, -2.f)));
-  return 0.25f * g * reciprocal(0.25f + e);
+  return g * (0.25f * reciprocal(0.25f + e));
 }
 
 struct SwigluArgs {

@@ -242,6 +242,17 @@ def test_swiglu_of_gates_whose_exponential_is_near_the_largest_number(dtype):
         check_fp4(m, want, rel.max())
 
 
+def test_swiglu_of_subnormal_gates():
+    """g / 2 of the smallest numbers, times a large factor: g itself is not rounded on the way."""
+    steps = torch.cat([torch.arange(64), -torch.arange(64), 3 * 2 ** torch.arange(22), -(2 ** torch.arange(1, 11)) - 1])
+    gate = (steps.double() * 2.0 ** -149).float()[None]
+    up = torch.full_like(gate, 2.0 ** 127)
+    a, _ = fp4.fp4_swiglu(gate.cuda(), up.cuda())
+    # exp(-g) = 1: the quotient is g / 2, off by half a step of 2^-149 and no more
+    want = f64(gate) / 2 * 2.0 ** 127
+    assert (np.abs(f64(a) - want) <= rounded(want, BF, 2.0 ** -150 * 2.0 ** 127 + np.abs(want) * 2.0 ** -22)).all()
+
+
 # ---------------------------------------------------------------------------
 # Norms around a residual sum
 # ---------------------------------------------------------------------------
